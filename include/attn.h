@@ -356,6 +356,52 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
                                                  int num_splits, void* stream);
 
 /*
+ * Strides of a [B, H, N, d] tensor in elements; the d elements of a row are
+ * adjacent.
+ */
+typedef struct {
+  long long batch, head, token;
+} attn_strides;
+
+/*
+ * Rotary positions of queries and keys, in one launch.
+ *
+ * No counterpart on the pages but the KV-compression post's remark that
+ * cached keys are held rotated (shreyansh26.github.io, learned compaction:
+ * keys are un-rotated before they are compressed). For the row of token n of
+ * request b at position p = positions[b * position_batch_stride + n], pair i
+ * of the first rot_dim elements is turned by the angle p * inv_freq[i]:
+ *     y_a = magnitude * (x_a cos - x_b sin)
+ *     y_b = magnitude * (x_b cos + x_a sin)
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) when `interleaved` is 1;
+ * elements rot_dim .. d-1 are copied. inverse = 1 turns by the negative
+ * angle: with the forward's magnitude this is the gradient of the call
+ * (dx from dy), with its reciprocal the un-rotation of cached keys.
+ *
+ * q [B,Hq,N,d] and k [B,Hkv,N,d] in `dt`, at any non-negative strides (NULL:
+ * contiguous; a view of a fused projection [B,N,Hq+2Hkv,d] is one example);
+ * q_out, k_out likewise, their rows must not overlap. Hkv = 0 turns q alone
+ * (k, k_out ignored). q_out == q and k_out == k with equal strides turn in
+ * place; otherwise outputs must not overlap inputs. d even and <= 512,
+ * rot_dim even, 2 <= rot_dim <= d. positions int32 in DEVICE memory, any
+ * value, negative included; position_batch_stride 0 shares one row among all
+ * requests. inv_freq float64 [rot_dim/2] in DEVICE memory, where any scaling
+ * for long contexts is already contained; the angle is reduced modulo one
+ * turn in 64-bit fixed point, so far positions lose nothing. A frequency
+ * that is not finite gives NaN in its pairs.
+ * Rows at multiples of 16 bytes with d and rot_dim multiples of 16 (bf16) or
+ * 8 (float32) move in 16-byte pieces; everything else element by element.
+ * Pointers need their element's alignment only. B*N at most 2^31 - 256.
+ */
+ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, void* q_out,
+                               const attn_strides* q_out_strides, const void* k,
+                               const attn_strides* k_strides, void* k_out,
+                               const attn_strides* k_out_strides, const int* positions,
+                               long long position_batch_stride, const double* inv_freq, int B,
+                               int Hq, int Hkv, int N, int d, int rot_dim, int interleaved,
+                               float magnitude, int inverse, attn_dtype dt, void* stream);
+
+/*
  * Self-test of the bounded device wait (no counterpart on the pages).
  *
  * Launches one warp on `stream` that waits, with the same bounded wait the

@@ -12,6 +12,7 @@ from ._binding import (  # noqa: F401
     ATTN_OK,
     AttnError,
     AttnMask,
+    AttnStrides,
     attn_bwd,
     attn_bwd_masked,
     attn_bwd_workspace_size,
@@ -24,6 +25,7 @@ from ._binding import (  # noqa: F401
     attn_fwd,
     attn_fwd_masked,
     attn_merge_partials,
+    attn_rope,
     attn_status_string,
     attn_sync_status,
     backward,
@@ -33,5 +35,7 @@ from ._binding import (  # noqa: F401
     forward,
     lib,
     make_mask,
+    rope,
+    rope_frequencies,
 )
 from ._build import LIB_PATH, build  # noqa: F401

@@ -8,7 +8,9 @@ fallback of any kind.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -43,6 +45,13 @@ class AttnMask(ctypes.Structure):
                 ("n_global", ctypes.c_int), ("row_kv_start", ctypes.c_void_p),
                 ("row_kv_end", ctypes.c_void_p)]
 
+
+class AttnStrides(ctypes.Structure):
+    """The C ``attn_strides``: element strides of a [B, H, N, d] tensor."""
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
+                ("token", ctypes.c_longlong)]
+
+
 _SIGNATURES = {
     "attn_fwd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 6 +
                  [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
@@ -71,6 +80,9 @@ _SIGNATURES = {
                             [ctypes.c_void_p]),
     "attn_decode_splitkv_noalloc": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 5 +
                                     [ctypes.c_float, ctypes.c_int, ctypes.c_void_p]),
+    "attn_rope": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_longlong, ctypes.c_void_p] +
+                  [ctypes.c_int] * 7 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
 }
@@ -121,6 +133,32 @@ def _device_contig(*ts):
             raise ValueError("tensors must be on the GPU (device pointers)")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _device_of(t: torch.Tensor, *others):
+    """Context in which t's device is the current one; the other tensors
+    (None: absent) must be on it too."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU (device pointers)")
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one device")
+    return _CURRENT if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _strides(t: torch.Tensor):
+    """attn_strides of a [B, H, N, d] or [B, H, d] tensor whose last
+    dimension is contiguous; None (the C default) for a contiguous tensor."""
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return ctypes.byref(AttnStrides(st[0], st[1], st[2] if len(st) == 4 else 0))
 
 
 def _check(status: int, what: str):
@@ -275,6 +313,49 @@ def attn_merge_partials(o_part, m_part, l_part, o, lse, stream=None):
     _check(st, "attn_merge_partials")
 
 
+def attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved: bool = False,
+              magnitude: float = 1.0, inverse: bool = False, stream=None):
+    """attn_rope on torch tensors: q, q_out [B,Hq,N,d] (or [B,Hq,d]: one
+    token), k, k_out [B,Hkv,N,d] or None, last dimension contiguous, other
+    strides free; positions int32 [B,N] (or [N], [1,N]: shared; [B] with one
+    token); inv_freq float64 [rot_dim / 2]."""
+    shape = q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [B, Hq, N, d] or [B, Hq, d]")
+    B, Hq, d = shape[0], shape[1], shape[-1]
+    N = shape[2] if len(shape) == 4 else 1
+    Hkv = 0
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        Hkv = k.shape[1]
+        if k.shape != (B, Hkv, *shape[2:]) or k_out.shape != k.shape:
+            raise ValueError("k and k_out must be like q but for the number of heads")
+        if k.dtype != q.dtype or k_out.dtype != q.dtype:
+            raise TypeError("q, k and their outputs must have one dtype")
+    if q_out.shape != shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must be like q")
+    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float64:
+        raise TypeError("positions must be int32 and inv_freq float64")
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not positions.is_contiguous():
+        raise ValueError("positions and inv_freq must be contiguous")
+    if positions.numel() == B * N:
+        pos_stride = N
+    elif positions.numel() == N:
+        pos_stride = 0
+    else:
+        raise ValueError("positions must be [B, N], or [N] for all requests")
+    with _device_of(q, k, q_out, k_out, positions, inv_freq):
+        st = lib().attn_rope(
+            q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
+            None if k is None else k.data_ptr(), None if k is None else _strides(k),
+            None if k is None else k_out.data_ptr(), None if k is None else _strides(k_out),
+            positions.data_ptr(), pos_stride, inv_freq.data_ptr(), B, Hq, Hkv, N, d,
+            2 * inv_freq.shape[0], int(interleaved), magnitude, int(inverse), _dt(q),
+            _stream(stream))
+    _check(st, "attn_rope")
+
+
 def attn_status_string(status: int) -> str:
     return lib().attn_status_string(status).decode()
 
@@ -365,3 +446,54 @@ def decode_sparse(q, k_cache, v_cache, indices, counts, num_splits: int,
     attn_decode_sparse(q, k_cache, v_cache, indices, counts, o, lse, scale, num_splits, workspace,
                        stream)
     return o, lse
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_length: int = 0, low: float = 1.0,
+                     high: float = 32.0, device=None):
+    """Rotary frequencies (radians per position) of the rot_dim / 2 pairs,
+    float64, for ``rope``: base^(-2i / rot_dim), scaled for a context
+    ``factor`` times as long as the trained one by
+
+    "linear"  every frequency divided by ``factor``;
+    "base"    the base raised to base * factor^(rot_dim / (rot_dim - 2)), which
+              divides the lowest frequency by ``factor`` and keeps the highest;
+    "ramp"    pairs that make more than ``high`` turns over ``original_length``
+              positions kept, those with fewer than ``low`` divided by
+              ``factor``, linearly in between.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not (factor > 0 and base > 0):
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError('"base" needs at least two pairs')
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        if original_length <= 0 or not high > low:
+            raise ValueError('"ramp" needs original_length > 0 and low < high')
+        keep = ((original_length * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}: none, linear, base or ramp")
+    return f.to(device) if device is not None else f
+
+
+def rope(q, k, positions, inv_freq, interleaved: bool = False, magnitude: float = 1.0,
+         inverse: bool = False, stream=None, out=None):
+    """Rotated q and k (k may be None), contiguous, or written to
+    ``out`` = (q_out, k_out), which may be (q, k) themselves. ``inverse``
+    turns back: the gradient of the call when given dy and the same
+    magnitude. See attn_rope for shapes, rope_frequencies for inv_freq."""
+    if out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    else:
+        q_out, k_out = out
+    attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved, magnitude, inverse, stream)
+    return q_out, k_out

@@ -1,0 +1,95 @@
+// C ABI entry points around the KV cache (rotary positions): argument
+// validation and dispatch. Declarations and their documentation:
+// include/attn.h.
+
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "launchers.h"
+
+using namespace attn;
+
+namespace {
+
+inline attn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+inline bool aligned_to(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+attn_strides strides_or_contiguous(const attn_strides* s, int H, int N, int d) {
+  if (s != nullptr) return *s;
+  return attn_strides{1LL * H * N * d, 1LL * N * d, d};
+}
+
+// Whether the rows of a [B, H, N, d] tensor are apart: each dimension (by
+// growing stride) steps over all that the ones before it cover.
+bool rows_apart(const attn_strides& s, int B, int H, int N, int d) {
+  struct Dim {
+    long long stride;
+    int n;
+  } dims[3] = {{s.batch, B}, {s.head, H}, {s.token, N}};
+  std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  long long covered = d;
+  for (const Dim& x : dims) {
+    if (x.n == 1) continue;
+    if (x.stride < covered) return false;
+    covered += x.stride * (x.n - 1);
+  }
+  return true;
+}
+
+bool non_negative(const attn_strides& s) { return s.batch >= 0 && s.head >= 0 && s.token >= 0; }
+
+bool same_rows(const attn_strides& a, const attn_strides& b, int B, int H, int N) {
+  return (B == 1 || a.batch == b.batch) && (H == 1 || a.head == b.head) &&
+         (N == 1 || a.token == b.token);
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_rope(const void* q, const attn_strides* q_strides, void* q_out,
+                      const attn_strides* q_out_strides, const void* k,
+                      const attn_strides* k_strides, void* k_out,
+                      const attn_strides* k_out_strides, const int* positions,
+                      long long position_batch_stride, const double* inv_freq, int B, int Hq,
+                      int Hkv, int N, int d, int rot_dim, int interleaved, float magnitude,
+                      int inverse, attn_dtype dt, void* stream) {
+  if (B <= 0 || Hq <= 0 || Hkv < 0 || N <= 0 || d <= 0) return ATTN_ERR_INVALID_ARG;
+  if (!q || !q_out || !positions || !inv_freq) return ATTN_ERR_INVALID_ARG;
+  if (Hkv > 0 && (!k || !k_out)) return ATTN_ERR_INVALID_ARG;
+  if (dt != ATTN_F32 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim < 2 || rot_dim > d || rot_dim % 2 != 0) return ATTN_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(magnitude) || position_batch_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (d % 2 != 0 || d > 512) return ATTN_ERR_UNSUPPORTED;
+  // tokens and heads are numbered in 32 bits; grid y carries at least 4 heads a block
+  if (1LL * B * N > (1LL << 31) - 256 || 1LL * Hq + Hkv > 4 * 65535LL) return ATTN_ERR_UNSUPPORTED;
+  const uintptr_t esize = dt == ATTN_BF16 ? 2 : 4;
+  if (!aligned_to(q, esize) || !aligned_to(q_out, esize) || !aligned_to(positions, 4) ||
+      !aligned_to(inv_freq, 8))
+    return ATTN_ERR_MISALIGNED;
+  if (Hkv > 0 && (!aligned_to(k, esize) || !aligned_to(k_out, esize))) return ATTN_ERR_MISALIGNED;
+  RopeArgs a{q, q_out, k, k_out,
+             strides_or_contiguous(q_strides, Hq, N, d),
+             strides_or_contiguous(q_out_strides, Hq, N, d),
+             strides_or_contiguous(k_strides, Hkv, N, d),
+             strides_or_contiguous(k_out_strides, Hkv, N, d),
+             positions, position_batch_stride, inv_freq, B, Hq, Hkv, N, d, rot_dim, interleaved,
+             magnitude, inverse, dt, static_cast<cudaStream_t>(stream)};
+  if (!non_negative(a.qs) || !rows_apart(a.qos, B, Hq, N, d) ||
+      (q == q_out && !same_rows(a.qs, a.qos, B, Hq, N)))
+    return ATTN_ERR_INVALID_ARG;
+  if (Hkv > 0 && (!non_negative(a.ks) || !rows_apart(a.kos, B, Hkv, N, d) ||
+                  (k == k_out && !same_rows(a.ks, a.kos, B, Hkv, N))))
+    return ATTN_ERR_INVALID_ARG;
+  return from_cuda(launch_rope(a));
+}
+
+}  // extern "C"

@@ -104,6 +104,22 @@ struct MergeArgs {
   int Hq = 1, len = 0, max_len = 0, chunk = 0;
 };
 
+struct RopeArgs {
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  attn_strides qs, qos, ks, kos;
+  const int* positions;
+  long long pos_stride;
+  const double* inv_freq;
+  int B, Hq, Hkv, N, d, rot, interleaved;
+  float magnitude;
+  int inverse;
+  attn_dtype dt;
+  cudaStream_t stream;
+};
+
 // Streaming multiprocessors of the current device (cached per device); 0 if
 // it cannot be read.
 inline int device_sm_count() {
@@ -207,6 +223,7 @@ cudaError_t launch_bwd_dq(const BwdArgs& a);
 cudaError_t launch_bwd_convert(const BwdArgs& a);
 cudaError_t launch_decode_split(const DecodeArgs& a);
 cudaError_t launch_merge(const MergeArgs& a);
+cudaError_t launch_rope(const RopeArgs& a);
 
 // Per-translation-unit device error words (read and cleared).
 uint32_t take_error_fwd_tc();

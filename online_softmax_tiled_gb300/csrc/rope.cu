@@ -1,0 +1,218 @@
+// Rotary positions: y = m · R(p·w) x on pairs of each head's first rot_dim
+// elements, the rest of the head copied, for queries and keys in one launch.
+//
+// Mathematics. Pair i of a head at position p is turned by the angle p·w_i:
+//   y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin),
+// (a, b) = (i, i + rot_dim/2) or (2i, 2i + 1). R is orthogonal, so the
+// gradient of y = m R x is dx = m Rᵀ dy: the same kernel with sin negated.
+//
+// Angles. p·w loses all of its meaning in float32 at far positions (at
+// p = 10^6 and w = 1 an ulp is 1/16 rad), and float64 multiplies are scarce
+// on this chip. The angle is kept as a 64-bit fraction of a full turn
+// instead: t = 2^64 · frac(w / 2π) once per pair from w's bits and 64 bits of
+// 2/π, then p·t modulo 2^64, where whole turns fall off by themselves. The
+// error is at most |p|·1.5·2^-64 turns (below 2^-32 for every 32-bit p);
+// the remainder, a signed 64-bit integer, is rounded once to float32 and
+// goes to sincospi.
+//
+// Work. Memory bound: 8 bytes per rotated bf16 pair against a few FMAs; the
+// sincos of a (token, pair) costs tens of instructions, so a thread computes
+// the cos and sin of its pairs once and applies them to a run of heads.
+// A thread owns V pairs, 16 bytes of each half (or 32 consecutive bytes when
+// interleaved): the 8 threads of a 128-wide bf16 head read its two halves as
+// whole 128-byte lines. Shapes, strides or addresses that are not multiples
+// of 16 bytes take the same kernel with V = 1.
+
+#include "common.cuh"
+#include "launchers.h"
+
+namespace attn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// 2^64 · frac(w / 2π): w = M · 2^(e - 63) with M in [2^63, 2^64), and
+// C = floor(2^64 · 2/π), so w / 2π · 2^64 = (M·C / 2^64) · 2^(e - 1).
+ATTN_DEVINL uint64_t turns_of(double w) {
+  constexpr uint64_t kTwoOverPi = 0xA2F9836E4E441529ull;
+  const uint64_t bits = uint64_t(__double_as_longlong(w));
+  const int ef = int((bits >> 52) & 0x7ff);
+  if (ef == 0) return 0;                              // zero (and below 2^-1022)
+  const uint64_t hi = __umul64hi((bits << 11) | (1ull << 63), kTwoOverPi);
+  const int sh = 1024 - ef;                           // 1 - e
+  const uint64_t t = sh >= 64 || sh <= -64 ? 0 : sh >= 0 ? hi >> sh : hi << -sh;
+  return (bits >> 63) ? 0 - t : t;
+}
+
+// V elements of type T as raw 32-bit words (V = 1: one element).
+template <typename T, int V> struct Pack;
+template <> struct Pack<__nv_bfloat16, 8> {
+  static ATTN_DEVINL void load(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16lo(ws[i]);
+      x[2 * i + 1] = bf16hi(ws[i]);
+    }
+  }
+  static ATTN_DEVINL void store(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+};
+template <> struct Pack<float, 4> {
+  static ATTN_DEVINL void load(const float* p, float (&x)[4]) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+  }
+  static ATTN_DEVINL void store(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+template <typename T> struct Pack<T, 1> {
+  static ATTN_DEVINL void load(const T* p, float (&x)[1]) { x[0] = to_f32(*p); }
+  static ATTN_DEVINL void store(T* p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+};
+
+// One tensor of the call: heads [0, H) of x, written to y.
+template <typename T> struct RopeTensor {
+  const T* x;
+  T* y;
+  attn_strides xs, ys;
+};
+
+// Grid: x over groups of tokens (b·N + n), y over groups of `hpt` heads of
+// the Hq + Hkv heads. A thread owns one chunk of V pairs (or, past the
+// rotated part, 2V elements to copy) of one token, in all heads of the group.
+// U heads are in flight at a time, so 2U independent 16-byte loads.
+template <typename T, int V, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ positions,
+            long long pos_stride, const double* __restrict__ inv_freq, int tokens, int N, int Hq,
+            int H, int d, int rot, int hpt, float magnitude, int inverse) {
+  constexpr int U = 4;
+  pdl_launch_dependents();
+  const int per_row = d / (2 * V);                     // chunks of a row
+  const int chunk = threadIdx.x % per_row;
+  const int token = blockIdx.x * (kThreads / per_row) + threadIdx.x / per_row;
+  if (threadIdx.x >= kThreads / per_row * per_row || token >= tokens) return;
+  const int b = token / N, n = token % N;
+  const bool turned = chunk < rot / (2 * V);
+  // element offsets of the chunk's two V-element pieces
+  const int off0 = kInterleaved || !turned ? chunk * 2 * V : chunk * V;
+  const int off1 = kInterleaved || !turned ? off0 + V : off0 + rot / 2;
+
+  pdl_wait_primary();
+  float cs[V], sn[V];
+  if (turned) {
+    const long long p = positions[b * pos_stride + n];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const double w = inv_freq[chunk * V + i];
+      const long long t = (long long)(uint64_t(p) * turns_of(w));
+      float s, c;
+      sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);   // angle 2π t / 2^64
+      // a frequency that is not finite gives NaN, not a wrong angle
+      const float m = isfinite(w) ? magnitude : __int_as_float(0x7fffffff);
+      cs[i] = c * m;
+      sn[i] = inverse ? -s * m : s * m;
+    }
+  }
+  const int h1 = min(H, (int(blockIdx.y) + 1) * hpt);
+  for (int h0 = int(blockIdx.y) * hpt; h0 < h1; h0 += U) {
+    float a[U][V], c[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u;
+      if (h < h1) {
+        const RopeTensor<T>& t = h < Hq ? tq : tk;
+        const T* px = t.x + b * t.xs.batch + (h < Hq ? h : h - Hq) * t.xs.head + n * t.xs.token;
+        Pack<T, V>::load(px + off0, a[u]);
+        Pack<T, V>::load(px + off1, c[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u;
+      if (h < h1) {
+        if (turned) {
+          float e[2 * V];                              // the 2V elements in memory order
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            // interleaved: pair i is (e[2i], e[2i + 1]) of the 2V elements
+            const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : V + i;
+            const float xa = ia < V ? a[u][ia % V] : c[u][ia % V];
+            const float xb = ib < V ? a[u][ib % V] : c[u][ib % V];
+            e[ia] = fmaf(xa, cs[i], -xb * sn[i]);
+            e[ib] = fmaf(xb, cs[i], xa * sn[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            a[u][i] = e[i];
+            c[u][i] = e[V + i];
+          }
+        }
+        const RopeTensor<T>& t = h < Hq ? tq : tk;
+        T* py = t.y + b * t.ys.batch + (h < Hq ? h : h - Hq) * t.ys.head + n * t.ys.token;
+        Pack<T, V>::store(py + off0, a[u]);
+        Pack<T, V>::store(py + off1, c[u]);
+      }
+    }
+  }
+}
+
+template <typename T, int V, bool kInterleaved>
+cudaError_t launch_t(const RopeArgs& a) {
+  const int per_row = a.d / (2 * V);
+  const int tpb = kThreads / per_row;                  // tokens per block
+  const int tokens = a.B * a.N, H = a.Hq + a.Hkv;
+  const long long blocks = (1LL * tokens + tpb - 1) / tpb;
+  // Heads per thread: as many as leave two full loads of the device's
+  // threads (8 blocks of 256 per SM), at least the 4 that are in flight.
+  const long long slots = 16LL * (device_sm_count() > 0 ? device_sm_count() : 1);
+  int hpt = 4;
+  while (hpt < H && blocks * ((H + 2 * hpt - 1) / (2 * hpt)) >= slots) hpt *= 2;
+  const RopeTensor<T> tq{static_cast<const T*>(a.q), static_cast<T*>(a.q_out), a.qs, a.qos};
+  const RopeTensor<T> tk{static_cast<const T*>(a.k), static_cast<T*>(a.k_out), a.ks, a.kos};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks), unsigned((H + hpt - 1) / hpt));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_kernel<T, V, kInterleaved>, tq, tk, a.positions,
+                            a.pos_stride, a.inv_freq, tokens, a.N, a.Hq, H, a.d, a.rot, hpt,
+                            a.magnitude, a.inverse);
+}
+
+// Whether every row of a tensor starts at a multiple of 16 bytes (strides of
+// dimensions of extent one do not matter).
+bool rows16(const void* p, const attn_strides& s, int B, int H, int N, int esize) {
+  auto bad = [&](long long st, int n) { return n > 1 && (st * esize) % 16 != 0; };
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && !bad(s.batch, B) && !bad(s.head, H) &&
+         !bad(s.token, N);
+}
+
+template <typename T, int V>
+cudaError_t launch_v(const RopeArgs& a) {
+  const bool wide = a.d % (2 * V) == 0 && a.rot % (2 * V) == 0 &&
+                    rows16(a.q, a.qs, a.B, a.Hq, a.N, sizeof(T)) &&
+                    rows16(a.q_out, a.qos, a.B, a.Hq, a.N, sizeof(T)) &&
+                    (a.Hkv == 0 || (rows16(a.k, a.ks, a.B, a.Hkv, a.N, sizeof(T)) &&
+                                    rows16(a.k_out, a.kos, a.B, a.Hkv, a.N, sizeof(T))));
+  if (wide) return a.interleaved ? launch_t<T, V, true>(a) : launch_t<T, V, false>(a);
+  return a.interleaved ? launch_t<T, 1, true>(a) : launch_t<T, 1, false>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a) {
+  return a.dt == ATTN_BF16 ? launch_v<__nv_bfloat16, 8>(a) : launch_v<float, 4>(a);
+}
+
+}  // namespace attn

@@ -37,3 +37,10 @@ from .attention import (  # noqa: F401
     decode_splitkv,
     default_scale,
 )
+from .cache import (  # noqa: F401
+    decode_shared,
+    evict,
+    key_weights,
+    rope,
+    rope_angles,
+)
