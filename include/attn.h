@@ -402,6 +402,46 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
                                float magnitude, int inverse, attn_dtype dt, void* stream);
 
 /*
+ * Eviction from a KV cache by score.
+ *
+ * KV-compression post (shreyansh26.github.io), eviction policies: the first
+ * tokens (attention sinks), a recent window and the keys with the highest
+ * accumulated attention weight stay, chosen per KV head; the rest leave. For
+ * request b with n = seq_lens[b] keys and every KV head: all keys are kept if
+ * n <= n_keep; otherwise the first n_sink, the last n_recent, and of the
+ * others the n_keep - n_sink - n_recent with the highest scores, ties to the
+ * lowest index; a NaN score ranks as -inf. The kept rows of K and V go, in
+ * their order, to the front of k_out and v_out. Keys keep whatever position
+ * they were rotated by.
+ *
+ * k, v: a contiguous cache [B,Hkv,L,d] (block_table NULL; num_pages,
+ * page_size, max_pages_per_seq ignored; seq_lens NULL: every length L) or
+ * pages [num_pages,Hkv,page_size,d] reached through block_table
+ * [B,max_pages_per_seq] as for attn_decode_paged (seq_lens given; L ignored).
+ * scores float32 [B,Hkv,score_len], of which the first n of a row count.
+ * k_out, v_out [B,Hkv,out_len,d], out_len >= n_keep: with `arange(B)` as
+ * block table these are pages of out_len keys, so attn_decode_paged reads
+ * them with new_lens. scores_out float32 [B,Hkv,out_len] receives the kept
+ * scores (may be NULL). kept int32 [B,Hkv,n_keep] receives the kept indices,
+ * -1 past the new length. new_lens int32 [B] = min(n, n_keep). Rows of k_out,
+ * v_out and scores_out past the new length are left as they were. Outputs
+ * must not overlap inputs (checked for k, v, scores and seq_lens).
+ * n_sink, n_recent >= 0, n_sink + n_recent <= n_keep, n_keep >= 1; d 64 or
+ * 128; `dt` the caches' type. B * Hkv at most 65535.
+ * Device-side checks: a length outside [0, min(score_len, capacity)] counts
+ * as 0; a row behind a page index outside [0, num_pages) is not moved (its
+ * place in k_out and v_out stays as it was); attn_sync_status() reports
+ * ATTN_ERR_DEVICE_INDEX for both.
+ */
+ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float* scores,
+                                      const int* seq_lens, const int* block_table, void* k_out,
+                                      void* v_out, float* scores_out, int* kept, int* new_lens,
+                                      int B, int Hkv, int L, int num_pages, int page_size,
+                                      int max_pages_per_seq, int score_len, int d, int n_keep,
+                                      int n_sink, int n_recent, int out_len, attn_dtype dt,
+                                      void* stream);
+
+/*
  * Self-test of the bounded device wait (no counterpart on the pages).
  *
  * Launches one warp on `stream` that waits, with the same bounded wait the

@@ -17,6 +17,7 @@ from ._binding import (  # noqa: F401
     attn_bwd_masked,
     attn_bwd_workspace_size,
     attn_selftest_bounded_wait,
+    attn_cache_evict,
     attn_decode_paged,
     attn_decode_sparse,
     attn_decode_splitkv,
@@ -32,6 +33,7 @@ from ._binding import (  # noqa: F401
     decode,
     decode_paged,
     decode_sparse,
+    evict,
     forward,
     lib,
     make_mask,

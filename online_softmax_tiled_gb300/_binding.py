@@ -83,6 +83,8 @@ _SIGNATURES = {
     "attn_rope": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_longlong, ctypes.c_void_p] +
                   [ctypes.c_int] * 7 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_void_p]),
+    "attn_cache_evict": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_int] * 13 +
+                         [ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
 }
@@ -356,6 +358,48 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved: bool = False
     _check(st, "attn_rope")
 
 
+def _int32(*ts):
+    for t in ts:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise TypeError("index tensors must be contiguous int32")
+
+
+def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink: int = 0,
+                     n_recent: int = 0, seq_lens=None, block_table=None, stream=None):
+    """k, v [B,Hkv,L,d] (or pages [num_pages,Hkv,page_size,d] behind
+    block_table [B,max_pages], with seq_lens [B]); scores [B,Hkv,score_len]
+    float32; k_out, v_out [B,Hkv,out_len,d]; scores_out [B,Hkv,out_len] or
+    None; kept [B,Hkv,n_keep] and new_lens [B] int32."""
+    _device_contig(k, v, scores, k_out, v_out, scores_out)
+    _int32(kept, new_lens, seq_lens, block_table)
+    B, Hkv, n_keep = kept.shape
+    d, out_len = k.shape[3], k_out.shape[2]
+    if v.shape != k.shape or k.shape[1] != Hkv or scores.shape[:2] != (B, Hkv) or \
+            k_out.shape != (B, Hkv, out_len, d) or v_out.shape != k_out.shape or \
+            new_lens.shape != (B,) or \
+            (scores_out is not None and scores_out.shape != (B, Hkv, out_len)) or \
+            (seq_lens is not None and seq_lens.shape != (B,)) or \
+            (block_table is not None and block_table.shape[0] != B) or \
+            (block_table is None and k.shape[0] != B):
+        raise ValueError("shapes do not go together (see attn_cache_evict)")
+    if not (v.dtype == k_out.dtype == v_out.dtype == k.dtype):
+        raise TypeError("k, v and their outputs must have one dtype")
+    if scores.dtype != torch.float32 or \
+            (scores_out is not None and scores_out.dtype != torch.float32):
+        raise TypeError("scores must be float32")
+    paged = block_table is not None
+    with _device_of(k, v, scores, k_out, v_out, scores_out, kept, new_lens, seq_lens, block_table):
+        st = lib().attn_cache_evict(
+            k.data_ptr(), v.data_ptr(), scores.data_ptr(),
+            None if seq_lens is None else seq_lens.data_ptr(),
+            block_table.data_ptr() if paged else None, k_out.data_ptr(), v_out.data_ptr(),
+            None if scores_out is None else scores_out.data_ptr(), kept.data_ptr(),
+            new_lens.data_ptr(), B, Hkv, k.shape[2], k.shape[0], k.shape[2],
+            block_table.shape[1] if paged else 0, scores.shape[2], d, n_keep, n_sink, n_recent,
+            out_len, _dt(k), _stream(stream))
+    _check(st, "attn_cache_evict")
+
+
 def attn_status_string(status: int) -> str:
     return lib().attn_status_string(status).decode()
 
@@ -497,3 +541,25 @@ def rope(q, k, positions, inv_freq, interleaved: bool = False, magnitude: float 
         q_out, k_out = out
     attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved, magnitude, inverse, stream)
     return q_out, k_out
+
+
+def evict(k, v, scores, n_keep: int, n_sink: int = 0, n_recent: int = 0, seq_lens=None,
+          block_table=None, stream=None, out=None):
+    """Keep n_keep keys per request and KV head by score: k_out, v_out
+    [B,Hkv,n_keep,d], scores_out [B,Hkv,n_keep], kept indices [B,Hkv,n_keep]
+    and new_lens [B] (or ``out``, those five tensors, of which k_out, v_out and
+    scores_out may be longer than n_keep). Rows past a new length are left as
+    they were; allocated here they are zero. With block_table =
+    arange(B)[:, None] the outputs are a paged cache for decode_paged."""
+    B, Hkv = scores.shape[:2]
+    if out is None:
+        out = (k.new_zeros((B, Hkv, n_keep, k.shape[3])), k.new_zeros((B, Hkv, n_keep, k.shape[3])),
+               scores.new_zeros((B, Hkv, n_keep)),
+               torch.empty((B, Hkv, n_keep), dtype=torch.int32, device=k.device),
+               torch.empty((B,), dtype=torch.int32, device=k.device))
+    k_out, v_out, scores_out, kept, new_lens = out
+    if kept.shape[2] != n_keep:
+        raise ValueError("the kept indices must be [B, Hkv, n_keep]")
+    attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink, n_recent,
+                     seq_lens, block_table, stream)
+    return out

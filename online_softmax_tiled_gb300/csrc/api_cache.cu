@@ -1,5 +1,5 @@
-// C ABI entry points around the KV cache (rotary positions): argument
-// validation and dispatch. Declarations and their documentation:
+// C ABI entry points around the KV cache (rotary positions, eviction):
+// argument validation and dispatch. Declarations and their documentation:
 // include/attn.h.
 
 #include <stdint.h>
@@ -49,6 +49,11 @@ bool same_rows(const attn_strides& a, const attn_strides& b, int B, int H, int N
          (N == 1 || a.token == b.token);
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+
 }  // namespace
 
 extern "C" {
@@ -90,6 +95,60 @@ attn_status attn_rope(const void* q, const attn_strides* q_strides, void* q_out,
                   (k == k_out && !same_rows(a.ks, a.kos, B, Hkv, N))))
     return ATTN_ERR_INVALID_ARG;
   return from_cuda(launch_rope(a));
+}
+
+attn_status attn_cache_evict(const void* k, const void* v, const float* scores,
+                             const int* seq_lens, const int* block_table, void* k_out,
+                             void* v_out, float* scores_out, int* kept, int* new_lens, int B,
+                             int Hkv, int L, int num_pages, int page_size, int max_pages_per_seq,
+                             int score_len, int d, int n_keep, int n_sink, int n_recent,
+                             int out_len, attn_dtype dt, void* stream) {
+  if (B <= 0 || Hkv <= 0 || score_len <= 0 || d <= 0) return ATTN_ERR_INVALID_ARG;
+  if (!k || !v || !scores || !k_out || !v_out || !kept || !new_lens) return ATTN_ERR_INVALID_ARG;
+  if (n_keep < 1 || n_sink < 0 || n_recent < 0 || 1LL * n_sink + n_recent > n_keep ||
+      out_len < n_keep)
+    return ATTN_ERR_INVALID_ARG;
+  if (dt != ATTN_F32 && dt != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  long long cap = L;
+  if (block_table != nullptr) {
+    if (num_pages <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || !seq_lens)
+      return ATTN_ERR_INVALID_ARG;
+    cap = 1LL * max_pages_per_seq * page_size;
+  } else if (L <= 0 || (seq_lens == nullptr && score_len < L)) {
+    return ATTN_ERR_INVALID_ARG;
+  }
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  // key positions are 32-bit inside the kernels, (request, head) rows a grid's y
+  if (cap > (1LL << 30) || score_len > (1 << 30) || out_len > (1 << 30) ||
+      1LL * B * Hkv > 65535)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(k_out, 16) ||
+      !aligned_to(v_out, 16) || !aligned_to(scores, 4) || !aligned_to(scores_out, 4) ||
+      !aligned_to(seq_lens, 4) || !aligned_to(block_table, 4) || !aligned_to(kept, 4) ||
+      !aligned_to(new_lens, 4))
+    return ATTN_ERR_MISALIGNED;
+  const size_t row = size_t(d) * (dt == ATTN_BF16 ? 2 : 4), heads = size_t(B) * Hkv;
+  const size_t n_in = row * (block_table ? size_t(num_pages) * Hkv * page_size : heads * L);
+  struct {
+    const void* p;
+    size_t n;
+  } const in[] = {{k, n_in}, {v, n_in}, {scores, heads * score_len * 4},
+                  {seq_lens, size_t(B) * 4},
+                  {block_table, size_t(B) * max_pages_per_seq * 4}},
+    out[] = {{k_out, heads * out_len * row}, {v_out, heads * out_len * row},
+             {scores_out, heads * out_len * 4}, {kept, heads * n_keep * 4},
+             {new_lens, size_t(B) * 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (const auto& x : in)
+      if (overlap(x.p, x.n, out[i].p, out[i].n)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j].p, out[j].n, out[i].p, out[i].n)) return ATTN_ERR_INVALID_ARG;
+  }
+  EvictArgs a{k, v, scores, k_out, v_out, scores_out, kept, new_lens, seq_lens, block_table,
+              num_pages, page_size, max_pages_per_seq, B, Hkv, L, d, score_len,
+              int(cap < score_len ? cap : score_len), n_keep, n_sink, n_recent, out_len, dt,
+              static_cast<cudaStream_t>(stream)};
+  return from_cuda(launch_evict(a));
 }
 
 }  // extern "C"

@@ -120,6 +120,25 @@ struct RopeArgs {
   cudaStream_t stream;
 };
 
+struct EvictArgs {
+  const void* k;
+  const void* v;
+  const float* scores;
+  void* k_out;
+  void* v_out;
+  float* scores_out;
+  int* kept;
+  int* new_lens;
+  const int* seq_lens;
+  // block_table != nullptr: k, v are pages [num_pages, Hkv, page_size, d];
+  // otherwise a contiguous cache [B, Hkv, L, d]
+  const int* block_table;
+  int num_pages, page_size, max_pages;
+  int B, Hkv, L, d, score_len, len_cap, n_keep, n_sink, n_recent, cap_out;
+  attn_dtype dt;
+  cudaStream_t stream;
+};
+
 // Streaming multiprocessors of the current device (cached per device); 0 if
 // it cannot be read.
 inline int device_sm_count() {
@@ -224,6 +243,7 @@ cudaError_t launch_bwd_convert(const BwdArgs& a);
 cudaError_t launch_decode_split(const DecodeArgs& a);
 cudaError_t launch_merge(const MergeArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);
+cudaError_t launch_evict(const EvictArgs& a);
 
 // Per-translation-unit device error words (read and cleared).
 uint32_t take_error_fwd_tc();
@@ -231,5 +251,6 @@ uint32_t take_error_fwd_tc64();
 uint32_t take_error_bwd_tc();
 uint32_t take_error_bwd_dq();
 uint32_t take_error_decode();
+uint32_t take_error_evict();
 
 }  // namespace attn
