@@ -356,6 +356,56 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
                                                  int num_splits, void* stream);
 
 /*
+ * Decode of a batch whose requests share long prefixes.
+ *
+ * ML notes (haolingpu.github.io), KV-cache Q&A: requests with a common prefix
+ * share its cache blocks; the split-K notes' exact (o, m, l) merge joins what
+ * was computed apart. Request b attends over the keys of its prefix, then
+ * its own: requests prefix_start[p] <= b < prefix_start[p + 1] share prefix p,
+ * of prefix_lens[p] keys; requests outside [prefix_start[0],
+ * prefix_start[n_prefix]) have own keys only. The prefix's keys are read
+ * once for all requests that share them, as a matrix product over all their
+ * query rows; the own keys run as in attn_decode_paged.
+ *
+ * q [B,Hq,d] bf16. Prefix keys: k_prefix/v_prefix [num_prefix_pages,Hkv,
+ * prefix_page_size,d] bf16 behind prefix_table [n_prefix,max_prefix_pages]
+ * int32 and prefix_lens [n_prefix] int32; with max_prefix_pages > 1,
+ * prefix_page_size must be a multiple of 8 (a prefix held contiguously is one
+ * page of any size). Own keys: k_pages/v_pages [num_pages,Hkv,page_size,d]
+ * behind block_table [B,max_pages_per_seq] and seq_lens [B] (0 allowed), as
+ * for attn_decode_paged; both pools may be the same. prefix_start [n_prefix+1]
+ * int32, not decreasing. All tables and lengths in DEVICE memory. o [B,Hq,d]
+ * bf16; lse [B,Hq] float32 (may be NULL). A request without any key gets
+ * O = 0, LSE = -inf. d 64 or 128; Hq/Hkv in {1, 2, 4, 8}.
+ * num_prefix_splits, num_splits: most splits of a prefix's keys and of a
+ * request's own; 0 takes the library's choice for these sizes. The
+ * probabilities of prefix keys are rounded to bf16 for the P·V product, as in
+ * attn_fwd; all softmax state is float32.
+ * Device-side checks: a length outside [0, capacity] counts as 0, a split
+ * with a page index out of range gets no keys, a group with a start outside
+ * [0, B] or below its predecessor is empty; attn_sync_status() reports
+ * ATTN_ERR_DEVICE_INDEX. (Groups that overlap because a start decreases
+ * leave the results of their requests undefined; nothing outside the
+ * buffers is touched.)
+ * workspace: at least attn_decode_shared_workspace_size() bytes for the same
+ * sizes and splits on the current device, 256-byte aligned.
+ */
+ATTN_API size_t attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int n_prefix,
+                                                  int prefix_page_size, int max_prefix_pages,
+                                                  int page_size, int max_pages_per_seq,
+                                                  int num_prefix_splits, int num_splits);
+ATTN_API attn_status attn_decode_shared(const void* q, const void* k_prefix, const void* v_prefix,
+                                        const int* prefix_table, const int* prefix_lens,
+                                        const int* prefix_start, const void* k_pages,
+                                        const void* v_pages, const int* block_table,
+                                        const int* seq_lens, void* o, float* lse, int B, int Hq,
+                                        int Hkv, int d, int n_prefix, int num_prefix_pages,
+                                        int prefix_page_size, int max_prefix_pages, int num_pages,
+                                        int page_size, int max_pages_per_seq, float scale,
+                                        int num_prefix_splits, int num_splits, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
+/*
  * Strides of a [B, H, N, d] tensor in elements; the d elements of a row are
  * adjacent.
  */

@@ -19,6 +19,8 @@ from ._binding import (  # noqa: F401
     attn_selftest_bounded_wait,
     attn_cache_evict,
     attn_decode_paged,
+    attn_decode_shared,
+    attn_decode_shared_workspace_size,
     attn_decode_sparse,
     attn_decode_splitkv,
     attn_decode_splitkv_noalloc,
@@ -32,6 +34,7 @@ from ._binding import (  # noqa: F401
     backward,
     decode,
     decode_paged,
+    decode_shared,
     decode_sparse,
     evict,
     forward,

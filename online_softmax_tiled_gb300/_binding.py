@@ -85,6 +85,10 @@ _SIGNATURES = {
                                         ctypes.c_void_p]),
     "attn_cache_evict": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_int] * 13 +
                          [ctypes.c_void_p]),
+    "attn_decode_shared_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 11),
+    "attn_decode_shared": (ctypes.c_int, [ctypes.c_void_p] * 12 + [ctypes.c_int] * 11 +
+                           [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_size_t, ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
 }
@@ -364,6 +368,60 @@ def _int32(*ts):
             raise TypeError("index tensors must be contiguous int32")
 
 
+def _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table, num_prefix_splits,
+                      num_splits) -> int:
+    B, Hq, d = q.shape
+    return lib().attn_decode_shared_workspace_size(
+        B, Hq, k_pages.shape[1], d, prefix_table.shape[0], k_prefix.shape[2],
+        prefix_table.shape[1], k_pages.shape[2], block_table.shape[1], num_prefix_splits,
+        num_splits)
+
+
+def attn_decode_shared_workspace_size(q, k_prefix, prefix_table, k_pages, block_table,
+                                      num_prefix_splits: int = 0, num_splits: int = 0) -> int:
+    """Workspace bytes of attn_decode_shared for these tensors."""
+    with _device_of(q):
+        return _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table,
+                                 num_prefix_splits, num_splits)
+
+
+def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
+                       v_pages, block_table, seq_lens, o, lse, scale: float,
+                       num_prefix_splits: int, num_splits: int, workspace, stream=None):
+    """q [B,Hq,d] bf16; k_prefix, v_prefix [num_prefix_pages,Hkv,prefix_page,d]
+    bf16 behind prefix_table [n_prefix,max_prefix_pages], prefix_lens
+    [n_prefix] and prefix_start [n_prefix+1] int32; own pages, block_table and
+    seq_lens as for attn_decode_paged; o like q; lse [B,Hq] float32 or None."""
+    _device_contig(q, k_prefix, v_prefix, k_pages, v_pages, o, lse, workspace)
+    _int32(prefix_table, prefix_lens, prefix_start, block_table, seq_lens)
+    B, Hq, d = q.shape
+    n_prefix, max_prefix_pages = prefix_table.shape
+    num_prefix_pages, Hkv, prefix_page = k_prefix.shape[:3]
+    num_pages, page = k_pages.shape[0], k_pages.shape[2]
+    if v_prefix.shape != k_prefix.shape or v_pages.shape != k_pages.shape or \
+            k_prefix.shape[3] != d or k_pages.shape[1] != Hkv or k_pages.shape[3] != d or \
+            prefix_lens.shape != (n_prefix,) or prefix_start.shape != (n_prefix + 1,) or \
+            block_table.shape[0] != B or seq_lens.shape != (B,) or o.shape != q.shape or \
+            (lse is not None and lse.shape != (B, Hq)):
+        raise ValueError("shapes do not go together (see attn_decode_shared)")
+    for t in (q, k_prefix, v_prefix, k_pages, v_pages, o):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("q, o and the pages must be bfloat16")
+    if lse is not None and lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    with _device_of(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
+                    v_pages, block_table, seq_lens, o, lse, workspace):
+        st = lib().attn_decode_shared(
+            q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), prefix_table.data_ptr(),
+            prefix_lens.data_ptr(), prefix_start.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), B, Hq, Hkv, d, n_prefix, num_prefix_pages,
+            prefix_page, max_prefix_pages, num_pages, page, block_table.shape[1], scale,
+            num_prefix_splits, num_splits, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "attn_decode_shared")
+
+
 def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink: int = 0,
                      n_recent: int = 0, seq_lens=None, block_table=None, stream=None):
     """k, v [B,Hkv,L,d] (or pages [num_pages,Hkv,page_size,d] behind
@@ -563,3 +621,25 @@ def evict(k, v, scores, n_keep: int, n_sink: int = 0, n_recent: int = 0, seq_len
     attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink, n_recent,
                      seq_lens, block_table, stream)
     return out
+
+
+def decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages, v_pages,
+                  block_table, seq_lens, num_prefix_splits: int = 0, num_splits: int = 0,
+                  scale: float | None = None, stream=None, workspace=None):
+    """Decode of requests that share prefixes: O [B,Hq,d] bf16, LSE [B,Hq]
+    float32 over each request's prefix keys and its own. Requests
+    prefix_start[p] .. prefix_start[p+1]-1 share prefix p. Splits of 0 are
+    chosen by the library."""
+    B, Hq, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    if workspace is None:
+        with _device_of(q):
+            n = _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table,
+                                  num_prefix_splits, num_splits)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
+                       v_pages, block_table, seq_lens, o, lse, scale, num_prefix_splits,
+                       num_splits, workspace, stream)
+    return o, lse

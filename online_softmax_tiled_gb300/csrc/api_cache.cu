@@ -1,5 +1,5 @@
-// C ABI entry points around the KV cache (rotary positions, eviction):
-// argument validation and dispatch. Declarations and their documentation:
+// C ABI entry points around the KV cache (decode behind shared
+// prefixes, rotary positions, eviction): argument validation and dispatch. Declarations and their documentation:
 // include/attn.h.
 
 #include <stdint.h>
@@ -54,6 +54,40 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a != nullptr && b != nullptr && x < y + nb && y < x + na;
 }
 
+// float32 partials (o, m, l) of `splits` splits per query row
+struct PartialLayout {
+  size_t m_part, l_part, total;
+};
+PartialLayout partial_layout(long long rows, int d, long long splits) {
+  PartialLayout l;
+  const size_t n = size_t(rows) * size_t(splits);
+  l.m_part = align256(n * d * sizeof(float));
+  l.l_part = l.m_part + align256(n * sizeof(float));
+  l.total = l.l_part + align256(n * sizeof(float));
+  return l;
+}
+
+bool shared_sizes_ok(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_page_size,
+                     int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
+                     int splits) {
+  return B > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && d > 0 && n_prefix > 0 &&
+         prefix_page_size > 0 && max_prefix_pages > 0 && page_size > 0 && max_pages > 0 &&
+         prefix_splits >= 0 && splits >= 0;
+}
+
+// key positions are 32-bit in the kernels; splits, requests and KV heads are
+// grid dimensions
+bool shared_sizes_supported(int B, int Hq, int Hkv, int d, int prefix_page_size,
+                            int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
+                            int splits) {
+  const int G = Hq / Hkv;
+  return (d == 64 || d == 128) && (G == 1 || G == 2 || G == 4 || G == 8) && B <= 65535 &&
+         1LL * Hkv * G <= 65535 && prefix_splits <= 65535 && splits <= 65535 &&
+         1LL * prefix_page_size * max_prefix_pages <= (1LL << 30) &&
+         1LL * page_size * max_pages <= (1LL << 30) &&
+         (max_prefix_pages == 1 || prefix_page_size % 8 == 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,6 +129,81 @@ attn_status attn_rope(const void* q, const attn_strides* q_strides, void* q_out,
                   (k == k_out && !same_rows(a.ks, a.kos, B, Hkv, N))))
     return ATTN_ERR_INVALID_ARG;
   return from_cuda(launch_rope(a));
+}
+
+size_t attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int n_prefix,
+                                         int prefix_page_size, int max_prefix_pages,
+                                         int page_size, int max_pages_per_seq,
+                                         int num_prefix_splits, int num_splits) {
+  if (!shared_sizes_ok(B, Hq, Hkv, d, n_prefix, prefix_page_size, max_prefix_pages, page_size,
+                       max_pages_per_seq, num_prefix_splits, num_splits) ||
+      !shared_sizes_supported(B, Hq, Hkv, d, prefix_page_size, max_prefix_pages, page_size,
+                              max_pages_per_seq, num_prefix_splits, num_splits))
+    return 0;
+  const SharedPlan pl = shared_plan(B, Hq, Hkv, n_prefix, prefix_page_size, max_prefix_pages,
+                                    page_size, max_pages_per_seq, num_prefix_splits, num_splits);
+  return partial_layout(1LL * B * Hq, d, 1LL * pl.prefix_splits + pl.own_splits).total;
+}
+
+attn_status attn_decode_shared(const void* q, const void* k_prefix, const void* v_prefix,
+                               const int* prefix_table, const int* prefix_lens,
+                               const int* prefix_start, const void* k_pages, const void* v_pages,
+                               const int* block_table, const int* seq_lens, void* o, float* lse,
+                               int B, int Hq, int Hkv, int d, int n_prefix, int num_prefix_pages,
+                               int prefix_page_size, int max_prefix_pages, int num_pages,
+                               int page_size, int max_pages_per_seq, float scale,
+                               int num_prefix_splits, int num_splits, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  if (!shared_sizes_ok(B, Hq, Hkv, d, n_prefix, prefix_page_size, max_prefix_pages, page_size,
+                       max_pages_per_seq, num_prefix_splits, num_splits) ||
+      num_prefix_pages <= 0 || num_pages <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!q || !k_prefix || !v_prefix || !prefix_table || !prefix_lens || !prefix_start ||
+      !k_pages || !v_pages || !block_table || !seq_lens || !o)
+    return ATTN_ERR_INVALID_ARG;
+  // (the prefix's kernel takes row maxima before scaling)
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (!shared_sizes_supported(B, Hq, Hkv, d, prefix_page_size, max_prefix_pages, page_size,
+                              max_pages_per_seq, num_prefix_splits, num_splits))
+    return ATTN_ERR_UNSUPPORTED;
+  // rows of the pools: page coordinates of the copies are 32-bit
+  if (1LL * num_prefix_pages * Hkv > (1LL << 31) - 1 ||
+      1LL * num_pages * Hkv * page_size > (1LL << 40))
+    return ATTN_ERR_UNSUPPORTED;
+  const void* wide[] = {q, k_prefix, v_prefix, k_pages, v_pages, o};
+  for (const void* x : wide)
+    if (!aligned_to(x, 16)) return ATTN_ERR_MISALIGNED;
+  const void* narrow[] = {prefix_table, prefix_lens, prefix_start, block_table, seq_lens, lse};
+  for (const void* x : narrow)
+    if (!aligned_to(x, 4)) return ATTN_ERR_MISALIGNED;
+  const SharedPlan pl = shared_plan(B, Hq, Hkv, n_prefix, prefix_page_size, max_prefix_pages,
+                                    page_size, max_pages_per_seq, num_prefix_splits, num_splits);
+  // work items are numbered in 32 bits, as are the partial rows
+  if (1LL * B * Hq * (1LL * pl.prefix_splits + pl.own_splits) > (1LL << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  const PartialLayout lay = partial_layout(1LL * B * Hq, d, 1LL * pl.prefix_splits + pl.own_splits);
+  if (!workspace || ws_bytes < lay.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned_to(workspace, 256)) return ATTN_ERR_MISALIGNED;
+  char* ws = static_cast<char*>(workspace);
+  SharedArgs a{};
+  a.own = DecodeArgs{q, k_pages, v_pages, o, lse, B, Hq, Hkv, 0, d, scale, pl.own_splits,
+                     reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + lay.m_part),
+                     reinterpret_cast<float*>(ws + lay.l_part), static_cast<cudaStream_t>(stream)};
+  a.own.block_table = block_table;
+  a.own.seq_lens = seq_lens;
+  a.own.num_pages = num_pages;
+  a.own.page_size = page_size;
+  a.own.max_pages = max_pages_per_seq;
+  a.k_prefix = k_prefix;
+  a.v_prefix = v_prefix;
+  a.prefix_table = prefix_table;
+  a.prefix_lens = prefix_lens;
+  a.prefix_start = prefix_start;
+  a.n_prefix = n_prefix;
+  a.num_prefix_pages = num_prefix_pages;
+  a.prefix_page_size = prefix_page_size;
+  a.max_prefix_pages = max_prefix_pages;
+  return from_cuda(launch_decode_shared(a, pl));
 }
 
 attn_status attn_cache_evict(const void* k, const void* v, const float* scores,

@@ -165,6 +165,11 @@ struct PagedKV {
   const int* seq_lens;
   int num_pages, page_size, max_pages;
   int rows;   // 1: sparse index list into the per-request cache
+  // Launched behind a kernel of the same call that waited for everything
+  // before it and writes nothing this kernel reads (the shared prefix's
+  // part): this grid does not wait for it at its start. Its last CTA waits
+  // before it leaves, so that the grid's completion implies the partner's.
+  int after_partner;
 };
 
 // Where a chunk's keys come from: a contiguous cache, pages of a paged
@@ -224,8 +229,11 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   }
   // Launched as a programmatic dependent: every global access of this grid
   // (q, the KV cache, the partials a previous merge may still be reading)
-  // comes after the preceding grid has completed.
-  pdl_wait_primary();
+  // comes after the preceding grid has completed (or, behind a partner, after
+  // the one before that).
+  if (!pg.after_partner) pdl_wait_primary();
+  const bool wait_at_end = pg.after_partner && blockIdx.x == gridDim.x - 1 &&
+                           blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
 
   // This CTA's keys [key_begin, key_end): chunk s of its request.
   const int max_len = kPaged ? pg.max_pages * pg.page_size : L;
@@ -277,11 +285,15 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
       m_part[row * S + s] = -INFINITY;
       l_part[row * S + s] = 0.f;
     }
+    if (wait_at_end) pdl_wait_primary();
     return;
   }
   const int nkeys = key_end - key_begin;
   // past the request's end: the merge never reads this chunk
-  if (nkeys <= 0) return;
+  if (nkeys <= 0) {
+    if (wait_at_end) pdl_wait_primary();
+    return;
+  }
   const int nstages = (nkeys + kStageKeys - 1) / kStageKeys;
 
   // Element offset of key t of (b, g) in the K and V arrays.
@@ -515,7 +527,10 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
         }
       }
   }
-  if (!ok) return;
+  if (!ok) {
+    if (wait_at_end) pdl_wait_primary();
+    return;
+  }
 
   // Cross-group merge: exact rescale onto the common max, first the four
   // groups of each warp, then the four warps.
@@ -524,6 +539,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   warp_combine_write<D, G>(acc, m_ref, l_run, comb, warp, lane);
   __syncthreads();
   final_combine<D, G>(comb, tid, kThreads, size_t(b) * Hq + gy * G, S, s, o_part, m_part, l_part);
+  if (wait_at_end) pdl_wait_primary();
 }
 
 // One warp per output row; lane owns float4 column groups lane, lane+32, ...
@@ -618,7 +634,7 @@ cudaError_t launch_split_t(const DecodeArgs& a, int rgroups) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const PagedKV pg{a.block_table, a.seq_lens, a.num_pages, a.page_size, a.max_pages,
-                   a.sparse ? 1 : 0};
+                   a.sparse ? 1 : 0, a.after_partner ? 1 : 0};
   // listed rows: the caches as [B·Hkv·L rows][d] for row gathers
   CUtensorMap mk{}, mv{};
   if (kSource == kListedRows) {
@@ -630,7 +646,9 @@ cudaError_t launch_split_t(const DecodeArgs& a, int rgroups) {
                             static_cast<const __nv_bfloat16*>(a.q),
                             static_cast<const __nv_bfloat16*>(a.k),
                             static_cast<const __nv_bfloat16*>(a.v), a.o_part, a.m_part, a.l_part,
-                            a.Hq * a.T, a.Hkv, a.L, a.num_splits, decode_chunk(a), a.scale, pg,
+                            a.Hq * a.T, a.Hkv, a.L,
+                            a.part_stride > 0 ? a.part_stride : a.num_splits, decode_chunk(a),
+                            a.scale, pg,
                             rgroups, mk, mv);
 }
 

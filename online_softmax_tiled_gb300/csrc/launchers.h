@@ -85,6 +85,30 @@ struct DecodeArgs {
   // num_pages = L. T query tokens per request: q, o [B, Hq, T, d].
   bool sparse = false;
   int T = 1;
+  // Partials per row in o_part, m_part, l_part where that is more than
+  // num_splits (0: num_splits), and whether the preceding kernel of the
+  // stream belongs to the same call and need not be waited for.
+  int part_stride = 0;
+  bool after_partner = false;
+};
+
+// Decode behind shared prefixes. own: the call's q, outputs, partials and the
+// requests' own paged keys; partials of a row are the prefix's splits, then
+// the own ones.
+struct SharedArgs {
+  DecodeArgs own;
+  const void* k_prefix;
+  const void* v_prefix;
+  const int* prefix_table;
+  const int* prefix_lens;
+  const int* prefix_start;
+  int n_prefix, num_prefix_pages, prefix_page_size, max_prefix_pages;
+};
+struct SharedPlan {
+  bool pair;               // 256 query rows per CTA (else 128)
+  int units;               // most runs of query rows
+  int prefix_splits, prefix_chunk, own_splits;
+  int box_rows;            // rows of one copy of prefix keys
 };
 
 struct MergeArgs {
@@ -242,6 +266,10 @@ cudaError_t launch_bwd_dq(const BwdArgs& a);
 cudaError_t launch_bwd_convert(const BwdArgs& a);
 cudaError_t launch_decode_split(const DecodeArgs& a);
 cudaError_t launch_merge(const MergeArgs& a);
+SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_size,
+                       int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
+                       int own_splits);
+cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& plan);
 cudaError_t launch_rope(const RopeArgs& a);
 cudaError_t launch_evict(const EvictArgs& a);
 
@@ -252,5 +280,6 @@ uint32_t take_error_bwd_tc();
 uint32_t take_error_bwd_dq();
 uint32_t take_error_decode();
 uint32_t take_error_evict();
+uint32_t take_error_decode_shared();
 
 }  // namespace attn
