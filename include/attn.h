@@ -452,6 +452,51 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
                                float magnitude, int inverse, attn_dtype dt, void* stream);
 
 /*
+ * Attention weight that each cached key received.
+ *
+ * KV-compression post (shreyansh26.github.io), eviction by attention weight:
+ * a key's weight is its probability summed over the query heads of its KV
+ * head (the SnapKV code's grouped heads) and over the observing queries: the
+ * tokens of an observation window at a prompt's end, or every decode step,
+ * added up. With the rows' LSE from the forward or the decode call,
+ *     out[b,g,j] = decay * prev[b,g,j]
+ *                  + sum over heads h of group g, tokens i < T, of
+ *                    exp(scale * q[b,h,i] . k[b,g,j] - lse[b,h,i])
+ * for the n = seq_lens[b] keys of request b. The T queries are the last T of
+ * the n positions: with causal = 1 key j is seen by token i iff
+ * j <= n - T + i, with causal = 0 by all. A row with lse = -inf gives
+ * nothing. prev == NULL: no first term (decay ignored); prev == out adds in
+ * place; any other overlap of the two is refused. out[b,g,j] for j >= n is
+ * left as it was.
+ *
+ * q [B,Hq,T,d] bf16, lse [B,Hq,T] float32 (T = 1: decode's q and lse); k a
+ * contiguous cache [B,Hkv,L,d] bf16 (block_table NULL; seq_lens NULL: every
+ * length L) or pages [num_pages,Hkv,page_size,d] behind block_table
+ * [B,max_pages_per_seq] (seq_lens given; L ignored; page_size a multiple of
+ * 8 unless max_pages_per_seq is 1); prev, out float32 [B,Hkv,out_len].
+ * d 64 or 128; any Hq that is a multiple of Hkv; any T. scale and decay
+ * finite. Products of bf16 values are exact in the float32 accumulation,
+ * weights and sums are float32, added in a fixed order.
+ * B * Hkv at most 65535, B * Hkv * ceil(capacity / 128) and T * Hq / Hkv at
+ * most 2^30.
+ * Device-side checks: a length outside [0, min(out_len, capacity)] counts as
+ * 0; keys behind a page index outside [0, num_pages) receive nothing;
+ * attn_sync_status() reports ATTN_ERR_DEVICE_INDEX for both.
+ * workspace: at least attn_key_weights_workspace_size() bytes for the same
+ * sizes on the current device, 256-byte aligned; 0 bytes (workspace may be
+ * NULL) while T * Hq / Hkv <= 256. `capacity`: L, or max_pages_per_seq *
+ * page_size.
+ */
+ATTN_API size_t attn_key_weights_workspace_size(int B, int Hq, int Hkv, int T, int capacity,
+                                                int out_len);
+ATTN_API attn_status attn_key_weights(const void* q, const void* k, const float* lse,
+                                      const float* prev, float* out, const int* seq_lens,
+                                      const int* block_table, int B, int Hq, int Hkv, int T, int L,
+                                      int num_pages, int page_size, int max_pages_per_seq,
+                                      int out_len, int d, float scale, float decay, int causal,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Eviction from a KV cache by score.
  *
  * KV-compression post (shreyansh26.github.io), eviction policies: the first

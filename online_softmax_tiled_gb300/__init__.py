@@ -27,6 +27,8 @@ from ._binding import (  # noqa: F401
     attn_decode_workspace_size,
     attn_fwd,
     attn_fwd_masked,
+    attn_key_weights,
+    attn_key_weights_workspace_size,
     attn_merge_partials,
     attn_rope,
     attn_status_string,
@@ -38,6 +40,7 @@ from ._binding import (  # noqa: F401
     decode_sparse,
     evict,
     forward,
+    key_weights,
     lib,
     make_mask,
     rope,

@@ -89,6 +89,10 @@ _SIGNATURES = {
     "attn_decode_shared": (ctypes.c_int, [ctypes.c_void_p] * 12 + [ctypes.c_int] * 11 +
                            [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                             ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_key_weights_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "attn_key_weights": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 10 +
+                         [ctypes.c_float, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
+                          ctypes.c_size_t, ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
 }
@@ -422,6 +426,47 @@ def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_
     _check(st, "attn_decode_shared")
 
 
+def attn_key_weights_workspace_size(B, Hq, Hkv, T, capacity, out_len) -> int:
+    """Workspace bytes of attn_key_weights on the current device (0 while
+    T * Hq / Hkv <= 256)."""
+    return int(lib().attn_key_weights_workspace_size(B, Hq, Hkv, T, capacity, out_len))
+
+
+def attn_key_weights(q, k, lse, prev, out, scale: float, decay: float = 1.0, causal: bool = True,
+                     seq_lens=None, block_table=None, workspace=None, stream=None):
+    """q [B,Hq,T,d] bf16 (or [B,Hq,d]: one token), lse [B,Hq,T] (or [B,Hq])
+    float32; k [B,Hkv,L,d] bf16 (or pages [num_pages,Hkv,page_size,d] behind
+    block_table [B,max_pages], with seq_lens [B]); prev (None: absent; may be
+    out) and out [B,Hkv,out_len] float32."""
+    _device_contig(q, k, lse, prev, out, workspace)
+    _int32(seq_lens, block_table)
+    shape = q.shape
+    B, Hq, d = shape[0], shape[1], shape[-1]
+    T = shape[2] if len(shape) == 4 else 1
+    Hkv, L, out_len = k.shape[1], k.shape[2], out.shape[2]
+    paged = block_table is not None
+    if len(shape) not in (3, 4) or lse.shape != shape[:-1] or k.shape[3] != d or \
+            out.shape[:2] != (B, Hkv) or (prev is not None and prev.shape != out.shape) or \
+            (seq_lens is not None and seq_lens.shape != (B,)) or \
+            (block_table.shape[0] if paged else k.shape[0]) != B:
+        raise ValueError("shapes do not go together (see attn_key_weights)")
+    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
+        raise TypeError("q and k must be bfloat16")
+    for t in (lse, prev, out):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("lse, prev and out must be float32")
+    with _device_of(q, k, lse, prev, out, seq_lens, block_table, workspace):
+        st = lib().attn_key_weights(
+            q.data_ptr(), k.data_ptr(), lse.data_ptr(), None if prev is None else prev.data_ptr(),
+            out.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
+            block_table.data_ptr() if paged else None, B, Hq, Hkv, T, L, k.shape[0], L,
+            block_table.shape[1] if paged else 0, out_len, d, scale, decay, int(causal),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream(stream))
+    _check(st, "attn_key_weights")
+
+
 def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink: int = 0,
                      n_recent: int = 0, seq_lens=None, block_table=None, stream=None):
     """k, v [B,Hkv,L,d] (or pages [num_pages,Hkv,page_size,d] behind
@@ -643,3 +688,27 @@ def decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start
                        v_pages, block_table, seq_lens, o, lse, scale, num_prefix_splits,
                        num_splits, workspace, stream)
     return o, lse
+
+
+def key_weights(q, k, lse, prev=None, decay: float = 1.0, causal: bool = True,
+                scale: float | None = None, seq_lens=None, block_table=None, out=None,
+                stream=None, workspace=None):
+    """Attention weight each cached key received from the last T tokens, in
+    float32 [B,Hkv,L] (paged: [B,Hkv,max_pages * page_size]), plus decay *
+    prev. ``out`` may be ``prev``; keys past a request's length are left as
+    they were (allocated here, they are zero)."""
+    d = q.shape[-1]
+    B, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    cap = k.shape[2] if block_table is None else block_table.shape[1] * k.shape[2]
+    if out is None:
+        make = torch.empty if seq_lens is None else torch.zeros
+        out = make((B, Hkv, cap), dtype=torch.float32, device=k.device)
+    T = q.shape[2] if q.dim() == 4 else 1
+    if workspace is None and T * Hq > 256 * Hkv:
+        with _device_of(q):
+            n = attn_key_weights_workspace_size(B, Hq, Hkv, T, cap, out.shape[2])
+        workspace = torch.empty(n, dtype=torch.uint8, device=k.device) if n else None
+    attn_key_weights(q, k, lse, prev, out, scale, decay, causal, seq_lens, block_table, workspace,
+                     stream)
+    return out

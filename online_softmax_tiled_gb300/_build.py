@@ -24,7 +24,8 @@ LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_gb300.so")
 
 SOURCES = ["api.cu", "fwd_simt.cu", "fwd_tc.cu", "fwd_tc64.cu", "bwd_aux.cu", "bwd_simt.cu", "bwd_tc.cu",
-           "bwd_dq.cu", "decode.cu", "decode_shared.cu", "api_cache.cu", "rope.cu", "evict.cu"]
+           "bwd_dq.cu", "decode.cu", "decode_shared.cu", "api_cache.cu", "rope.cu",
+           "key_weights.cu", "evict.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -376,7 +376,7 @@ attn_status attn_sync_status(void* stream) {
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
   const uint32_t w = take_error_fwd_tc() | take_error_fwd_tc64() | take_error_bwd_tc() |
                      take_error_bwd_dq() | take_error_decode() | take_error_evict() |
-                     take_error_decode_shared();
+                     take_error_decode_shared() | take_error_key_weights();
   if (w == 0xffffffffu) return ATTN_ERR_CUDA;
   if (w & kErrTimeout) return ATTN_ERR_DEVICE_TIMEOUT;
   if (w & kErrBadIndex) return ATTN_ERR_DEVICE_INDEX;

@@ -1,5 +1,5 @@
 // C ABI entry points around the KV cache (decode behind shared
-// prefixes, rotary positions, eviction): argument validation and dispatch. Declarations and their documentation:
+// prefixes, rotary positions, key weights, eviction): argument validation and dispatch. Declarations and their documentation:
 // include/attn.h.
 
 #include <stdint.h>
@@ -86,6 +86,14 @@ bool shared_sizes_supported(int B, int Hq, int Hkv, int d, int prefix_page_size,
          1LL * prefix_page_size * max_prefix_pages <= (1LL << 30) &&
          1LL * page_size * max_pages <= (1LL << 30) &&
          (max_prefix_pages == 1 || prefix_page_size % 8 == 0);
+}
+
+bool key_weights_sizes_ok(int B, int Hq, int Hkv, int T, long long cap, int out_len) {
+  return B > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && T > 0 && cap > 0 && out_len > 0;
+}
+bool key_weights_sizes_supported(int B, int Hq, int Hkv, int T, long long cap, int out_len) {
+  return 1LL * B * Hkv <= 65535 && 1LL * (Hq / Hkv) * T <= (1LL << 30) && cap <= (1LL << 30) &&
+         out_len <= (1 << 30) && 1LL * B * Hkv * ((cap + 127) / 128) <= (1LL << 30);
 }
 
 }  // namespace
@@ -204,6 +212,53 @@ attn_status attn_decode_shared(const void* q, const void* k_prefix, const void* 
   a.prefix_page_size = prefix_page_size;
   a.max_prefix_pages = max_prefix_pages;
   return from_cuda(launch_decode_shared(a, pl));
+}
+
+size_t attn_key_weights_workspace_size(int B, int Hq, int Hkv, int T, int capacity, int out_len) {
+  if (!key_weights_sizes_ok(B, Hq, Hkv, T, capacity, out_len) ||
+      !key_weights_sizes_supported(B, Hq, Hkv, T, capacity, out_len))
+    return 0;
+  const int S = key_weights_splits(B, Hkv, Hq / Hkv * T, std::min(capacity, out_len));
+  return S == 1 ? 0 : align256(size_t(S) * B * Hkv * out_len * sizeof(float));
+}
+
+attn_status attn_key_weights(const void* q, const void* k, const float* lse, const float* prev,
+                             float* out, const int* seq_lens, const int* block_table, int B,
+                             int Hq, int Hkv, int T, int L, int num_pages, int page_size,
+                             int max_pages_per_seq, int out_len, int d, float scale, float decay,
+                             int causal, void* workspace, size_t ws_bytes, void* stream) {
+  if (!q || !k || !lse || !out) return ATTN_ERR_INVALID_ARG;
+  if (block_table != nullptr &&
+      (num_pages <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || !seq_lens))
+    return ATTN_ERR_INVALID_ARG;
+  const long long cap = block_table != nullptr ? 1LL * max_pages_per_seq * page_size : L;
+  if (!key_weights_sizes_ok(B, Hq, Hkv, T, cap, out_len)) return ATTN_ERR_INVALID_ARG;
+  if (seq_lens == nullptr && out_len < L) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || (prev != nullptr && !std::isfinite(decay)))
+    return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!key_weights_sizes_supported(B, Hq, Hkv, T, cap, out_len)) return ATTN_ERR_UNSUPPORTED;
+  if (block_table != nullptr && max_pages_per_seq > 1 && page_size % 8 != 0)
+    return ATTN_ERR_UNSUPPORTED;
+  // rows of the pool: page coordinates of the copies are 32-bit
+  if (block_table != nullptr && 1LL * num_pages * Hkv > (1LL << 31) - 1)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(lse, 4) || !aligned_to(prev, 4) ||
+      !aligned_to(out, 4) || !aligned_to(seq_lens, 4) || !aligned_to(block_table, 4))
+    return ATTN_ERR_MISALIGNED;
+  const size_t n_out = size_t(B) * Hkv * out_len * 4;
+  if (prev != out && overlap(prev, n_out, out, n_out)) return ATTN_ERR_INVALID_ARG;
+  const int len_cap = int(std::min<long long>(cap, out_len));
+  const int S = key_weights_splits(B, Hkv, Hq / Hkv * T, len_cap);
+  if (S > 1) {
+    if (!workspace || ws_bytes < align256(S * n_out)) return ATTN_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return ATTN_ERR_MISALIGNED;
+  }
+  KeyWeightsArgs a{q, k, lse, prev, out, static_cast<float*>(workspace), seq_lens, block_table,
+                   B, Hq, Hkv, T, L, num_pages, page_size, max_pages_per_seq, len_cap, out_len, d,
+                   causal, S, scale, decay, static_cast<cudaStream_t>(stream)};
+  return from_cuda(launch_key_weights(a));
 }
 
 attn_status attn_cache_evict(const void* k, const void* v, const float* scores,

@@ -144,6 +144,20 @@ struct RopeArgs {
   cudaStream_t stream;
 };
 
+struct KeyWeightsArgs {
+  const void* q;
+  const void* k;
+  const float* lse;
+  const float* prev;
+  float* out;
+  float* part;             // splits > 1: partial sums [splits][B, Hkv, out_len]
+  const int* seq_lens;
+  const int* block_table;  // nullptr: contiguous cache [B, Hkv, L, d]
+  int B, Hq, Hkv, T, L, num_pages, page_size, max_pages, len_cap, out_len, d, causal, splits;
+  float scale, decay;
+  cudaStream_t stream;
+};
+
 struct EvictArgs {
   const void* k;
   const void* v;
@@ -270,6 +284,10 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_siz
                        int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
                        int own_splits);
 cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& plan);
+// Splits of the R = (Hq / Hkv)·T query rows per KV head that
+// launch_key_weights uses for a capacity of `cap` keys.
+int key_weights_splits(int B, int Hkv, int R, int cap);
+cudaError_t launch_key_weights(const KeyWeightsArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);
 cudaError_t launch_evict(const EvictArgs& a);
 
@@ -280,6 +298,7 @@ uint32_t take_error_bwd_tc();
 uint32_t take_error_bwd_dq();
 uint32_t take_error_decode();
 uint32_t take_error_evict();
+uint32_t take_error_key_weights();
 uint32_t take_error_decode_shared();
 
 }  // namespace attn
