@@ -1,0 +1,114 @@
+"""The cache operators together, as a serving loop uses them: prompts behind a
+shared prefix are rotated and cached, decode steps read prefix and own keys
+and add up the weight each own key received, the caches are cut to the keys
+that received most, and decoding goes on over what is left. Every step is
+checked against the float64 oracle fed with the tensors that step read.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from workloads import random_like_shape, to_f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _close(got, ref, tol=1e-2):
+    err, mx = np.max(np.abs(to_f64(got) - ref)), np.max(np.abs(ref))
+    assert err <= tol * mx, (err, mx)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 8, 2), (64, 4, 4)])
+def test_serving_loop(ost, d, Hq, Hkv):
+    B, P, N, steps, cap, keep = 6, 300, 90, 5, 128, 40
+    scale, w = d ** -0.5, ost.rope_frequencies(d, device=DEV)
+    bf = torch.bfloat16
+
+    def rotated_ref(x, pos):
+        return oracle.rope(to_f64(x), pos.cpu().numpy(), w.cpu().numpy())
+
+    # the shared prefix: rotated once, one page of P keys
+    kp0 = random_like_shape((1, Hkv, P, d), bf, 1).to(DEV)
+    vp = random_like_shape((1, Hkv, P, d), bf, 2).to(DEV)
+    ppos = torch.arange(P, dtype=torch.int32, device=DEV)[None]
+    kp, _ = ost.rope(kp0, None, ppos, w)
+    _close(kp, rotated_ref(kp0, ppos), 2 ** -8 * 1.01)
+
+    # each request's own prompt, at the positions behind the prefix, into caches of `cap` keys
+    k = torch.zeros(B, Hkv, cap, d, dtype=bf, device=DEV)
+    v = torch.zeros(B, Hkv, cap, d, dtype=bf, device=DEV)
+    qkv = random_like_shape((B, N, Hq + 2 * Hkv, d), bf, 3).to(DEV)
+    pos = (P + torch.arange(N, dtype=torch.int32, device=DEV)).expand(B, N).contiguous()
+    q0, k0 = qkv[:, :, :Hq].transpose(1, 2), qkv[:, :, Hq:Hq + Hkv].transpose(1, 2)
+    q = torch.empty(B, Hq, N, d, dtype=bf, device=DEV)
+    ost.rope(q0, k0, pos, w, out=(q, k[:, :, :N]))
+    v[:, :, :N] = qkv[:, :, Hq + Hkv:].transpose(1, 2)
+    _close(k[:, :, :N], rotated_ref(k0, pos), 2 ** -8 * 1.01)
+    assert torch.all(k[:, :, N:] == 0)
+
+    # weights of the prompt's last 16 tokens over the own keys
+    _, lse = ost.forward(q, k[:, :, :N].contiguous(), v[:, :, :N].contiguous(), causal=True)
+    lens = torch.full((B,), N, dtype=torch.int32, device=DEV)
+    score = torch.zeros(B, Hkv, cap, device=DEV)
+    qw, lw = q[:, :, -16:].contiguous(), lse[:, :, -16:].contiguous()
+    ost.key_weights(qw, k, lw, out=score, seq_lens=lens)
+    ref = np.stack([oracle.key_weights(to_f64(qw[b]), to_f64(k[b, :, :N]), to_f64(lw[b]), scale)
+                    for b in range(B)])
+    _close(score[:, :, :N], ref, 1e-3)
+
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    ptable = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    plen = torch.tensor([P], dtype=torch.int32, device=DEV)
+    pstart = torch.tensor([0, B], dtype=torch.int32, device=DEV)
+
+    def step(k, v, score, lens, cap, seed, at):
+        """One token: rotate, append, decode, accumulate; returns the score reference."""
+        x = random_like_shape((B, Hq + 2 * Hkv, d), bf, seed).to(DEV)
+        p = torch.full((B,), at, dtype=torch.int32, device=DEV)
+        qt, kt = ost.rope(x[:, :Hq], x[:, Hq:Hq + Hkv], p, w)
+        rows = torch.arange(B, device=DEV)
+        k[rows, :, lens.long()] = kt
+        v[rows, :, lens.long()] = x[:, Hq + Hkv:]
+        lens += 1
+        o, lse = ost.decode_shared(qt, kp, vp, ptable, plen, pstart, k, v, table, lens)
+        pages = [to_f64(t) for t in (kp, vp)], [to_f64(t) for t in (k, v)]
+        o_ref, lse_ref = oracle.decode_shared(
+            to_f64(qt), *pages[0], np.zeros((1, 1), int), np.array([P]), np.array([0, B]),
+            *pages[1], np.arange(B)[:, None], lens.cpu().numpy(), scale)
+        _close(o, o_ref)
+        assert np.max(np.abs(to_f64(lse) - lse_ref)) <= 1e-3
+        before = to_f64(score)
+        ost.key_weights(qt, k, lse, prev=score, out=score, seq_lens=lens, block_table=table)
+        for b in range(B):
+            n = int(lens[b])
+            ref = before[b, :, :n] + oracle.key_weights(
+                to_f64(qt[b, :, None]), pages[1][0][b, :, :n], to_f64(lse[b, :, None]), scale)
+            assert np.max(np.abs(to_f64(score[b, :, :n]) - ref)) <= 1e-3 * np.max(ref)
+            assert np.array_equal(to_f64(score[b, :, n:]), before[b, :, n:])
+
+    for i in range(steps):
+        step(k, v, score, lens, cap, 10 + i, P + N + i)
+
+    # cut to `keep` keys in caches with room to grow, then go on
+    room = keep + steps
+    out = (torch.zeros(B, Hkv, room, d, dtype=bf, device=DEV),
+           torch.zeros(B, Hkv, room, d, dtype=bf, device=DEV),
+           torch.zeros(B, Hkv, room, device=DEV),
+           torch.empty(B, Hkv, keep, dtype=torch.int32, device=DEV),
+           torch.empty(B, dtype=torch.int32, device=DEV))
+    ost.evict(k, v, score, keep, n_sink=2, n_recent=8, seq_lens=lens, block_table=table, out=out)
+    k2, v2, score2, kept, lens2 = out
+    assert torch.all(lens2 == keep)
+    for b in range(B):
+        for h in range(Hkv):
+            at = oracle.evict(to_f64(score[b, h, :N + steps]), keep, 2, 8)
+            assert np.array_equal(kept[b, h].cpu().numpy(), at)
+            assert torch.equal(k2[b, h, :keep], k[b, h, at]) and \
+                torch.equal(v2[b, h, :keep], v[b, h, at]) and \
+                torch.equal(score2[b, h, :keep], score[b, h, at])
+    for i in range(steps):
+        step(k2, v2, score2, lens2, room, 50 + i, P + N + steps + i)
+    assert ost.attn_sync_status() == 0
