@@ -8,7 +8,6 @@ fallback of any kind.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -145,19 +144,56 @@ def _device_contig(*ts):
             raise ValueError("tensors must be contiguous")
 
 
-_CURRENT = contextlib.nullcontext()
+# The calls around the cache are short next to Python's own time, so their
+# checks avoid repeated attribute look-ups; what they check is written out at
+# each call.
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _device_of(t: torch.Tensor, *others):
-    """Context in which t's device is the current one; the other tensors
-    (None: absent) must be on it too."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU (device pointers)")
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one device")
-    return _CURRENT if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+def _pointers(dev: int, *ts):
+    """Addresses of contiguous tensors on device ``dev`` (None stays None)."""
+    out = []
+    for t in ts:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _typed(dtype, *ts):
+    for t in ts:
+        if t is not None and t.dtype is not dtype:
+            raise TypeError(f"expected {dtype}, got {t.dtype}")
+
+
+def _on_device(dev: int, fn, *args):
+    """fn(*args) with device ``dev`` current."""
+    if dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _stream_of(dev: int, stream):
+    """Handle of ``stream``, or of the current stream of device ``dev``."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating_on(stream, dev: int):
+    """Context for a call that allocates: what it allocates (workspaces above
+    all) must belong to the stream it runs on, or the allocator may hand it
+    out again while the call still runs."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
 
 
 def _strides(t: torch.Tensor):
@@ -330,63 +366,58 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved: bool = False
     strides free; positions int32 [B,N] (or [N], [1,N]: shared; [B] with one
     token); inv_freq float64 [rot_dim / 2]."""
     shape = q.shape
-    if len(shape) not in (3, 4):
-        raise ValueError("q must be [B, Hq, N, d] or [B, Hq, d]")
-    B, Hq, d = shape[0], shape[1], shape[-1]
-    N = shape[2] if len(shape) == 4 else 1
-    Hkv = 0
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out go together")
-    if k is not None:
-        Hkv = k.shape[1]
-        if k.shape != (B, Hkv, *shape[2:]) or k_out.shape != k.shape:
-            raise ValueError("k and k_out must be like q but for the number of heads")
-        if k.dtype != q.dtype or k_out.dtype != q.dtype:
-            raise TypeError("q, k and their outputs must have one dtype")
-    if q_out.shape != shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out must be like q")
-    if positions.dtype != torch.int32 or inv_freq.dtype != torch.float64:
-        raise TypeError("positions must be int32 and inv_freq float64")
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not positions.is_contiguous():
-        raise ValueError("positions and inv_freq must be contiguous")
-    if positions.numel() == B * N:
-        pos_stride = N
-    elif positions.numel() == N:
-        pos_stride = 0
+    dims = len(shape)
+    if dims == 4:
+        B, Hq, N, d = shape
+    elif dims == 3:
+        B, Hq, d = shape
+        N = 1
     else:
+        raise ValueError("q must be [B, Hq, N, d] or [B, Hq, d]")
+    dtype = q.dtype
+    dt = ATTN_BF16 if dtype is _BF16 else _dt(q)
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU (device pointers)")
+    if q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != dev:
+        raise ValueError("q_out must be like q")
+    Hkv, pk, sk, pko, sko = 0, None, None, None, None
+    if k is not None:
+        kshape = k.shape
+        Hkv = kshape[1]
+        if len(kshape) != dims or kshape[0] != B or kshape[2:] != shape[2:] or \
+                k_out is None or k_out.shape != kshape:
+            raise ValueError("k and k_out must be like q but for the number of heads")
+        if k.dtype is not dtype or k_out.dtype is not dtype:
+            raise TypeError("q, k and their outputs must have one dtype")
+        if k.get_device() != dev or k_out.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one GPU")
+        pk, sk, pko, sko = k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out)
+    elif k_out is not None:
+        raise ValueError("k and k_out go together")
+    if positions.dtype is not _I32 or inv_freq.dtype is not torch.float64:
+        raise TypeError("positions must be int32 and inv_freq float64")
+    count = positions.numel()
+    if count != B * N and count != N:
         raise ValueError("positions must be [B, N], or [N] for all requests")
-    with _device_of(q, k, q_out, k_out, positions, inv_freq):
-        st = lib().attn_rope(
-            q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out),
-            None if k is None else k.data_ptr(), None if k is None else _strides(k),
-            None if k is None else k_out.data_ptr(), None if k is None else _strides(k_out),
-            positions.data_ptr(), pos_stride, inv_freq.data_ptr(), B, Hq, Hkv, N, d,
-            2 * inv_freq.shape[0], int(interleaved), magnitude, int(inverse), _dt(q),
-            _stream(stream))
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    pp, pw = _pointers(dev, positions, inv_freq)
+    st = _on_device(dev, lib().attn_rope, q.data_ptr(), _strides(q), q_out.data_ptr(),
+                    _strides(q_out), pk, sk, pko, sko, pp, N if count == B * N else 0, pw, B, Hq,
+                    Hkv, N, d, 2 * inv_freq.shape[0], interleaved, magnitude, inverse, dt,
+                    _stream_of(dev, stream))
     _check(st, "attn_rope")
-
-
-def _int32(*ts):
-    for t in ts:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-            raise TypeError("index tensors must be contiguous int32")
-
-
-def _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table, num_prefix_splits,
-                      num_splits) -> int:
-    B, Hq, d = q.shape
-    return lib().attn_decode_shared_workspace_size(
-        B, Hq, k_pages.shape[1], d, prefix_table.shape[0], k_prefix.shape[2],
-        prefix_table.shape[1], k_pages.shape[2], block_table.shape[1], num_prefix_splits,
-        num_splits)
 
 
 def attn_decode_shared_workspace_size(q, k_prefix, prefix_table, k_pages, block_table,
                                       num_prefix_splits: int = 0, num_splits: int = 0) -> int:
     """Workspace bytes of attn_decode_shared for these tensors."""
-    with _device_of(q):
-        return _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table,
-                                 num_prefix_splits, num_splits)
+    B, Hq, d = q.shape
+    return _on_device(q.get_device(), lib().attn_decode_shared_workspace_size, B, Hq,
+                      k_pages.shape[1], d, prefix_table.shape[0], k_prefix.shape[2],
+                      prefix_table.shape[1], k_pages.shape[2], block_table.shape[1],
+                      num_prefix_splits, num_splits)
 
 
 def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
@@ -396,33 +427,29 @@ def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_
     bf16 behind prefix_table [n_prefix,max_prefix_pages], prefix_lens
     [n_prefix] and prefix_start [n_prefix+1] int32; own pages, block_table and
     seq_lens as for attn_decode_paged; o like q; lse [B,Hq] float32 or None."""
-    _device_contig(q, k_prefix, v_prefix, k_pages, v_pages, o, lse, workspace)
-    _int32(prefix_table, prefix_lens, prefix_start, block_table, seq_lens)
+    dev = q.get_device()
+    ptrs = _pointers(dev, q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
+                     v_pages, block_table, seq_lens, o, lse, workspace)
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU (device pointers)")
+    _typed(_BF16, q, k_prefix, v_prefix, k_pages, v_pages, o)
+    _typed(_I32, prefix_table, prefix_lens, prefix_start, block_table, seq_lens)
     B, Hq, d = q.shape
     n_prefix, max_prefix_pages = prefix_table.shape
-    num_prefix_pages, Hkv, prefix_page = k_prefix.shape[:3]
-    num_pages, page = k_pages.shape[0], k_pages.shape[2]
-    if v_prefix.shape != k_prefix.shape or v_pages.shape != k_pages.shape or \
-            k_prefix.shape[3] != d or k_pages.shape[1] != Hkv or k_pages.shape[3] != d or \
+    pshape, shape = k_prefix.shape, k_pages.shape
+    num_prefix_pages, Hkv, prefix_page, dp = pshape
+    num_pages, hk, page, dk = shape
+    tables, max_pages = block_table.shape
+    if v_prefix.shape != pshape or v_pages.shape != shape or dp != d or dk != d or hk != Hkv or \
             prefix_lens.shape != (n_prefix,) or prefix_start.shape != (n_prefix + 1,) or \
-            block_table.shape[0] != B or seq_lens.shape != (B,) or o.shape != q.shape or \
-            (lse is not None and lse.shape != (B, Hq)):
+            tables != B or seq_lens.shape != (B,) or o.shape != (B, Hq, d):
         raise ValueError("shapes do not go together (see attn_decode_shared)")
-    for t in (q, k_prefix, v_prefix, k_pages, v_pages, o):
-        if t.dtype != torch.bfloat16:
-            raise TypeError("q, o and the pages must be bfloat16")
-    if lse is not None and lse.dtype != torch.float32:
-        raise TypeError("lse must be float32")
-    with _device_of(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
-                    v_pages, block_table, seq_lens, o, lse, workspace):
-        st = lib().attn_decode_shared(
-            q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), prefix_table.data_ptr(),
-            prefix_lens.data_ptr(), prefix_start.data_ptr(), k_pages.data_ptr(),
-            v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-            None if lse is None else lse.data_ptr(), B, Hq, Hkv, d, n_prefix, num_prefix_pages,
-            prefix_page, max_prefix_pages, num_pages, page, block_table.shape[1], scale,
-            num_prefix_splits, num_splits, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(stream))
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, Hq)):
+        raise TypeError("lse must be float32 [B, Hq]")
+    st = _on_device(dev, lib().attn_decode_shared, *ptrs[:12], B, Hq, Hkv, d, n_prefix,
+                    num_prefix_pages, prefix_page, max_prefix_pages, num_pages, page, max_pages,
+                    scale, num_prefix_splits, num_splits, ptrs[12],
+                    workspace.numel() * workspace.element_size(), _stream_of(dev, stream))
     _check(st, "attn_decode_shared")
 
 
@@ -438,32 +465,33 @@ def attn_key_weights(q, k, lse, prev, out, scale: float, decay: float = 1.0, cau
     float32; k [B,Hkv,L,d] bf16 (or pages [num_pages,Hkv,page_size,d] behind
     block_table [B,max_pages], with seq_lens [B]); prev (None: absent; may be
     out) and out [B,Hkv,out_len] float32."""
-    _device_contig(q, k, lse, prev, out, workspace)
-    _int32(seq_lens, block_table)
+    dev = q.get_device()
+    pq, pk, pl, pp, po, pn, pt, pws = _pointers(dev, q, k, lse, prev, out, seq_lens, block_table,
+                                                workspace)
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU (device pointers)")
+    _typed(_BF16, q, k)
+    _typed(_F32, lse, prev, out)
+    _typed(_I32, seq_lens, block_table)
     shape = q.shape
-    B, Hq, d = shape[0], shape[1], shape[-1]
-    T = shape[2] if len(shape) == 4 else 1
-    Hkv, L, out_len = k.shape[1], k.shape[2], out.shape[2]
-    paged = block_table is not None
-    if len(shape) not in (3, 4) or lse.shape != shape[:-1] or k.shape[3] != d or \
-            out.shape[:2] != (B, Hkv) or (prev is not None and prev.shape != out.shape) or \
-            (seq_lens is not None and seq_lens.shape != (B,)) or \
-            (block_table.shape[0] if paged else k.shape[0]) != B:
+    if len(shape) == 4:
+        B, Hq, T, d = shape
+    elif len(shape) == 3:
+        B, Hq, d = shape
+        T = 1
+    else:
+        raise ValueError("q must be [B, Hq, T, d] or [B, Hq, d]")
+    n0, Hkv, L, dk = k.shape
+    ob, oh, out_len = out.shape
+    tables, max_pages = (n0, 0) if block_table is None else block_table.shape
+    if lse.shape != shape[:-1] or dk != d or ob != B or oh != Hkv or tables != B or \
+            (prev is not None and prev.shape != out.shape) or \
+            (seq_lens is not None and seq_lens.shape != (B,)):
         raise ValueError("shapes do not go together (see attn_key_weights)")
-    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
-        raise TypeError("q and k must be bfloat16")
-    for t in (lse, prev, out):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError("lse, prev and out must be float32")
-    with _device_of(q, k, lse, prev, out, seq_lens, block_table, workspace):
-        st = lib().attn_key_weights(
-            q.data_ptr(), k.data_ptr(), lse.data_ptr(), None if prev is None else prev.data_ptr(),
-            out.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
-            block_table.data_ptr() if paged else None, B, Hq, Hkv, T, L, k.shape[0], L,
-            block_table.shape[1] if paged else 0, out_len, d, scale, decay, int(causal),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(stream))
+    st = _on_device(dev, lib().attn_key_weights, pq, pk, pl, pp, po, pn, pt, B, Hq, Hkv, T, L, n0,
+                    L, max_pages, out_len, d, scale, decay, causal, pws,
+                    0 if workspace is None else workspace.numel() * workspace.element_size(),
+                    _stream_of(dev, stream))
     _check(st, "attn_key_weights")
 
 
@@ -473,33 +501,30 @@ def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_s
     block_table [B,max_pages], with seq_lens [B]); scores [B,Hkv,score_len]
     float32; k_out, v_out [B,Hkv,out_len,d]; scores_out [B,Hkv,out_len] or
     None; kept [B,Hkv,n_keep] and new_lens [B] int32."""
-    _device_contig(k, v, scores, k_out, v_out, scores_out)
-    _int32(kept, new_lens, seq_lens, block_table)
+    dev = k.get_device()
+    pk, pv, ps, pl, pt, pko, pvo, pso, pkept, pnew = _pointers(
+        dev, k, v, scores, seq_lens, block_table, k_out, v_out, scores_out, kept, new_lens)
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU (device pointers)")
+    dtype = k.dtype
+    _typed(dtype, v, k_out, v_out)
+    _typed(_F32, scores, scores_out)
+    _typed(_I32, seq_lens, block_table, kept, new_lens)
+    shape = k.shape
+    n0, hk, L, d = shape
     B, Hkv, n_keep = kept.shape
-    d, out_len = k.shape[3], k_out.shape[2]
-    if v.shape != k.shape or k.shape[1] != Hkv or scores.shape[:2] != (B, Hkv) or \
-            k_out.shape != (B, Hkv, out_len, d) or v_out.shape != k_out.shape or \
-            new_lens.shape != (B,) or \
-            (scores_out is not None and scores_out.shape != (B, Hkv, out_len)) or \
-            (seq_lens is not None and seq_lens.shape != (B,)) or \
-            (block_table is not None and block_table.shape[0] != B) or \
-            (block_table is None and k.shape[0] != B):
+    sb, sh, score_len = scores.shape
+    oshape = k_out.shape
+    out_len = oshape[2]
+    tables, max_pages = (n0, 0) if block_table is None else block_table.shape
+    if v.shape != shape or hk != Hkv or sb != B or sh != Hkv or oshape != (B, Hkv, out_len, d) or \
+            v_out.shape != oshape or tables != B or new_lens.shape != (B,) or \
+            (scores_out is not None and scores_out.shape != oshape[:3]) or \
+            (seq_lens is not None and seq_lens.shape != (B,)):
         raise ValueError("shapes do not go together (see attn_cache_evict)")
-    if not (v.dtype == k_out.dtype == v_out.dtype == k.dtype):
-        raise TypeError("k, v and their outputs must have one dtype")
-    if scores.dtype != torch.float32 or \
-            (scores_out is not None and scores_out.dtype != torch.float32):
-        raise TypeError("scores must be float32")
-    paged = block_table is not None
-    with _device_of(k, v, scores, k_out, v_out, scores_out, kept, new_lens, seq_lens, block_table):
-        st = lib().attn_cache_evict(
-            k.data_ptr(), v.data_ptr(), scores.data_ptr(),
-            None if seq_lens is None else seq_lens.data_ptr(),
-            block_table.data_ptr() if paged else None, k_out.data_ptr(), v_out.data_ptr(),
-            None if scores_out is None else scores_out.data_ptr(), kept.data_ptr(),
-            new_lens.data_ptr(), B, Hkv, k.shape[2], k.shape[0], k.shape[2],
-            block_table.shape[1] if paged else 0, scores.shape[2], d, n_keep, n_sink, n_recent,
-            out_len, _dt(k), _stream(stream))
+    st = _on_device(dev, lib().attn_cache_evict, pk, pv, ps, pl, pt, pko, pvo, pso, pkept, pnew, B,
+                    Hkv, L, n0, L, max_pages, score_len, d, n_keep, n_sink, n_recent, out_len,
+                    ATTN_BF16 if dtype is _BF16 else _dt(k), _stream_of(dev, stream))
     _check(st, "attn_cache_evict")
 
 
@@ -637,9 +662,12 @@ def rope(q, k, positions, inv_freq, interleaved: bool = False, magnitude: float 
     ``out`` = (q_out, k_out), which may be (q, k) themselves. ``inverse``
     turns back: the gradient of the call when given dy and the same
     magnitude. See attn_rope for shapes, rope_frequencies for inv_freq."""
+    if stream is not None and out is None:
+        with _allocating_on(stream, q.get_device()):
+            return rope(q, k, positions, inv_freq, interleaved, magnitude, inverse)
     if out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         q_out, k_out = out
     attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved, magnitude, inverse, stream)
@@ -654,12 +682,15 @@ def evict(k, v, scores, n_keep: int, n_sink: int = 0, n_recent: int = 0, seq_len
     scores_out may be longer than n_keep). Rows past a new length are left as
     they were; allocated here they are zero. With block_table =
     arange(B)[:, None] the outputs are a paged cache for decode_paged."""
-    B, Hkv = scores.shape[:2]
     if out is None:
+        if stream is not None:
+            with _allocating_on(stream, k.get_device()):
+                return evict(k, v, scores, n_keep, n_sink, n_recent, seq_lens, block_table)
+        B, Hkv = scores.shape[:2]
         out = (k.new_zeros((B, Hkv, n_keep, k.shape[3])), k.new_zeros((B, Hkv, n_keep, k.shape[3])),
                scores.new_zeros((B, Hkv, n_keep)),
-               torch.empty((B, Hkv, n_keep), dtype=torch.int32, device=k.device),
-               torch.empty((B,), dtype=torch.int32, device=k.device))
+               torch.empty((B, Hkv, n_keep), dtype=_I32, device=k.device),
+               torch.empty((B,), dtype=_I32, device=k.device))
     k_out, v_out, scores_out, kept, new_lens = out
     if kept.shape[2] != n_keep:
         raise ValueError("the kept indices must be [B, Hkv, n_keep]")
@@ -675,18 +706,21 @@ def decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start
     float32 over each request's prefix keys and its own. Requests
     prefix_start[p] .. prefix_start[p+1]-1 share prefix p. Splits of 0 are
     chosen by the library."""
+    if stream is not None:
+        with _allocating_on(stream, q.get_device()):
+            return decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start,
+                                 k_pages, v_pages, block_table, seq_lens, num_prefix_splits,
+                                 num_splits, scale, None, workspace)
     B, Hq, d = q.shape
-    scale = d ** -0.5 if scale is None else scale
     if workspace is None:
-        with _device_of(q):
-            n = _shared_workspace(q, k_prefix, prefix_table, k_pages, block_table,
-                                  num_prefix_splits, num_splits)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        n = attn_decode_shared_workspace_size(q, k_prefix, prefix_table, k_pages, block_table,
+                                              num_prefix_splits, num_splits)
+        workspace = q.new_empty(n, dtype=torch.uint8)
     o = torch.empty_like(q)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    lse = q.new_empty((B, Hq), dtype=_F32)
     attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
-                       v_pages, block_table, seq_lens, o, lse, scale, num_prefix_splits,
-                       num_splits, workspace, stream)
+                       v_pages, block_table, seq_lens, o, lse, d ** -0.5 if scale is None else scale,
+                       num_prefix_splits, num_splits, workspace)
     return o, lse
 
 
@@ -697,18 +731,22 @@ def key_weights(q, k, lse, prev=None, decay: float = 1.0, causal: bool = True,
     float32 [B,Hkv,L] (paged: [B,Hkv,max_pages * page_size]), plus decay *
     prev. ``out`` may be ``prev``; keys past a request's length are left as
     they were (allocated here, they are zero)."""
-    d = q.shape[-1]
-    B, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    scale = d ** -0.5 if scale is None else scale
-    cap = k.shape[2] if block_table is None else block_table.shape[1] * k.shape[2]
+    if stream is not None:
+        with _allocating_on(stream, q.get_device()):
+            return key_weights(q, k, lse, prev, decay, causal, scale, seq_lens, block_table, out,
+                               None, workspace)
+    shape = q.shape
+    B, Hq, d, T = shape[0], shape[1], shape[-1], shape[2] if len(shape) == 4 else 1
+    Hkv, cap = k.shape[1:3]
+    if block_table is not None:
+        cap *= block_table.shape[1]
     if out is None:
         make = torch.empty if seq_lens is None else torch.zeros
-        out = make((B, Hkv, cap), dtype=torch.float32, device=k.device)
-    T = q.shape[2] if q.dim() == 4 else 1
+        out = make((B, Hkv, cap), dtype=_F32, device=k.device)
     if workspace is None and T * Hq > 256 * Hkv:
-        with _device_of(q):
-            n = attn_key_weights_workspace_size(B, Hq, Hkv, T, cap, out.shape[2])
-        workspace = torch.empty(n, dtype=torch.uint8, device=k.device) if n else None
-    attn_key_weights(q, k, lse, prev, out, scale, decay, causal, seq_lens, block_table, workspace,
-                     stream)
+        n = _on_device(q.get_device(), attn_key_weights_workspace_size, B, Hq, Hkv, T, cap,
+                       out.shape[2])
+        workspace = k.new_empty(n, dtype=torch.uint8) if n else None
+    attn_key_weights(q, k, lse, prev, out, d ** -0.5 if scale is None else scale, decay, causal,
+                     seq_lens, block_table, workspace)
     return out
