@@ -12,8 +12,8 @@
 // instead: t = 2^64 · frac(w / 2π) once per pair from w's bits and 64 bits of
 // 2/π, then p·t modulo 2^64, where whole turns fall off by themselves. The
 // error is at most |p|·1.5·2^-64 turns (below 2^-32 for every 32-bit p);
-// the remainder, a signed 64-bit integer, is rounded once to float32 and
-// goes to sincospi.
+// the remainder is rounded to 32 bits, then to float32, and goes to
+// sincospi.
 //
 // Work. Memory bound: 8 bytes per rotated bf16 pair against a few FMAs; the
 // sincos of a (token, pair) costs tens of instructions, so a thread computes
@@ -30,7 +30,9 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads per block: a row has at most d / (2V) = 256 chunks with V = 1, 64
+// otherwise.
+template <int V> constexpr int kThreadsOf = V == 1 ? 256 : 128;
 
 // 2^64 · frac(w / 2π): w = M · 2^(e - 63) with M in [2^63, 2^64), and
 // C = floor(2^64 · 2/π), so w / 2π · 2^64 = (M·C / 2^64) · 2^(e - 1).
@@ -45,35 +47,36 @@ ATTN_DEVINL uint64_t turns_of(double w) {
   return (bits >> 63) ? 0 - t : t;
 }
 
-// V elements of type T as raw 32-bit words (V = 1: one element).
+// V adjacent elements as they are in memory (V = 1: one element).
 template <typename T, int V> struct Pack;
 template <> struct Pack<__nv_bfloat16, 8> {
-  static ATTN_DEVINL void load(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  using Raw = uint4;
+  static ATTN_DEVINL void open(const Raw& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16lo(ws[i]);
-      x[2 * i + 1] = bf16hi(ws[i]);
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
     }
   }
-  static ATTN_DEVINL void store(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  static ATTN_DEVINL Raw close(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
   }
 };
 template <> struct Pack<float, 4> {
-  static ATTN_DEVINL void load(const float* p, float (&x)[4]) {
-    const float4 w = *reinterpret_cast<const float4*>(p);
-    x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+  using Raw = float4;
+  static ATTN_DEVINL void open(const Raw& r, float (&x)[4]) {
+    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
   }
-  static ATTN_DEVINL void store(float* p, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  static ATTN_DEVINL Raw close(const float (&x)[4]) {
+    return make_float4(x[0], x[1], x[2], x[3]);
   }
 };
 template <typename T> struct Pack<T, 1> {
-  static ATTN_DEVINL void load(const T* p, float (&x)[1]) { x[0] = to_f32(*p); }
-  static ATTN_DEVINL void store(T* p, const float (&x)[1]) { *p = from_f32<T>(x[0]); }
+  using Raw = T;
+  static ATTN_DEVINL void open(const Raw& r, float (&x)[1]) { x[0] = to_f32(r); }
+  static ATTN_DEVINL Raw close(const float (&x)[1]) { return from_f32<T>(x[0]); }
 };
 
 // One tensor of the call: heads [0, H) of x, written to y.
@@ -86,13 +89,17 @@ template <typename T> struct RopeTensor {
 // Grid: x over groups of tokens (b·N + n), y over groups of `hpt` heads of
 // the Hq + Hkv heads. A thread owns one chunk of V pairs (or, past the
 // rotated part, 2V elements to copy) of one token, in all heads of the group.
-// U heads are in flight at a time, so 2U independent 16-byte loads.
+// U heads are in flight at a time, held as they came from memory: 2U
+// independent 16-byte loads, the first of them issued before the angles are
+// worked out.
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreadsOf<V>)
 rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ positions,
             long long pos_stride, const double* __restrict__ inv_freq, int tokens, int N, int Hq,
             int H, int d, int rot, int hpt, float magnitude, int inverse) {
-  constexpr int U = 4;
+  using P = Pack<T, V>;
+  using Raw = typename P::Raw;
+  constexpr int U = 4, kThreads = kThreadsOf<V>;
   pdl_launch_dependents();
   const int per_row = d / (2 * V);                     // chunks of a row
   const int chunk = threadIdx.x % per_row;
@@ -103,75 +110,85 @@ rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ position
   // element offsets of the chunk's two V-element pieces
   const int off0 = kInterleaved || !turned ? chunk * 2 * V : chunk * V;
   const int off1 = kInterleaved || !turned ? off0 + V : off0 + rot / 2;
+  const T* xq = tq.x + b * tq.xs.batch + n * tq.xs.token;
+  const T* xk = tk.x + b * tk.xs.batch + n * tk.xs.token;
+  T* yq = tq.y + b * tq.ys.batch + n * tq.ys.token;
+  T* yk = tk.y + b * tk.ys.batch + n * tk.ys.token;
+  const int h0 = int(blockIdx.y) * hpt, h1 = min(H, h0 + hpt);
 
   pdl_wait_primary();
+  Raw a[U], c[U];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u < h1) {
+        const T* px = h + u < Hq ? xq + (h + u) * tq.xs.head : xk + (h + u - Hq) * tk.xs.head;
+        a[u] = *reinterpret_cast<const Raw*>(px + off0);
+        c[u] = *reinterpret_cast<const Raw*>(px + off1);
+      }
+  };
+  load(h0);
   float cs[V], sn[V];
   if (turned) {
     const long long p = positions[b * pos_stride + n];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const double w = inv_freq[chunk * V + i];
-      const long long t = (long long)(uint64_t(p) * turns_of(w));
-      float s, c;
-      sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);   // angle 2π t / 2^64
+      // the angle as a fraction of a turn: its top 32 bits, rounded, are off
+      // by 2^-33 turns at most, and rounded to float32 once more
+      const uint64_t t = uint64_t(p) * turns_of(w) + 0x80000000ull;
+      float s, co;
+      sincospif(float(int(uint32_t(t >> 32))) * 0x1p-31f, &s, &co);
       // a frequency that is not finite gives NaN, not a wrong angle
       const float m = isfinite(w) ? magnitude : __int_as_float(0x7fffffff);
-      cs[i] = c * m;
+      cs[i] = co * m;
       sn[i] = inverse ? -s * m : s * m;
     }
   }
-  const int h1 = min(H, (int(blockIdx.y) + 1) * hpt);
-  for (int h0 = int(blockIdx.y) * hpt; h0 < h1; h0 += U) {
-    float a[U][V], c[U][V];
+  for (int h = h0; h < h1; h += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u;
-      if (h < h1) {
-        const RopeTensor<T>& t = h < Hq ? tq : tk;
-        const T* px = t.x + b * t.xs.batch + (h < Hq ? h : h - Hq) * t.xs.head + n * t.xs.token;
-        Pack<T, V>::load(px + off0, a[u]);
-        Pack<T, V>::load(px + off1, c[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u;
-      if (h < h1) {
+      if (h + u < h1) {
         if (turned) {
-          float e[2 * V];                              // the 2V elements in memory order
+          float x[V], z[V], e[2 * V];                  // e: the 2V results in memory order
+          P::open(a[u], x);
+          P::open(c[u], z);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            // interleaved: pair i is (e[2i], e[2i + 1]) of the 2V elements
+            // interleaved: pair i is elements 2i, 2i + 1 of the 2V
             const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : V + i;
-            const float xa = ia < V ? a[u][ia % V] : c[u][ia % V];
-            const float xb = ib < V ? a[u][ib % V] : c[u][ib % V];
+            const float xa = ia < V ? x[ia % V] : z[ia % V];
+            const float xb = ib < V ? x[ib % V] : z[ib % V];
             e[ia] = fmaf(xa, cs[i], -xb * sn[i]);
             e[ib] = fmaf(xb, cs[i], xa * sn[i]);
           }
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            a[u][i] = e[i];
-            c[u][i] = e[V + i];
+            x[i] = e[i];
+            z[i] = e[V + i];
           }
+          a[u] = P::close(x);
+          c[u] = P::close(z);
         }
-        const RopeTensor<T>& t = h < Hq ? tq : tk;
-        T* py = t.y + b * t.ys.batch + (h < Hq ? h : h - Hq) * t.ys.head + n * t.ys.token;
-        Pack<T, V>::store(py + off0, a[u]);
-        Pack<T, V>::store(py + off1, c[u]);
+        T* py = h + u < Hq ? yq + (h + u) * tq.ys.head : yk + (h + u - Hq) * tk.ys.head;
+        *reinterpret_cast<Raw*>(py + off0) = a[u];
+        *reinterpret_cast<Raw*>(py + off1) = c[u];
       }
     }
+    if (h + U < h1) load(h + U);
   }
 }
 
 template <typename T, int V, bool kInterleaved>
 cudaError_t launch_t(const RopeArgs& a) {
+  constexpr int kThreads = kThreadsOf<V>;
   const int per_row = a.d / (2 * V);
   const int tpb = kThreads / per_row;                  // tokens per block
   const int tokens = a.B * a.N, H = a.Hq + a.Hkv;
   const long long blocks = (1LL * tokens + tpb - 1) / tpb;
-  // Heads per thread: as many as leave two full loads of the device's
-  // threads (8 blocks of 256 per SM), at least the 4 that are in flight.
-  const long long slots = 16LL * (device_sm_count() > 0 ? device_sm_count() : 1);
+  // Heads per thread: as many as leave eight blocks per SM (which its
+  // registers admit), at least the 4 that are in flight.
+  const long long slots = 8LL * (device_sm_count() > 0 ? device_sm_count() : 1);
   int hpt = 4;
   while (hpt < H && blocks * ((H + 2 * hpt - 1) / (2 * hpt)) >= slots) hpt *= 2;
   const RopeTensor<T> tq{static_cast<const T*>(a.q), static_cast<T*>(a.q_out), a.qs, a.qos};
