@@ -12,8 +12,9 @@
 //
 // A row of scores is short (4 bytes a key against 4·d·2 of K and V) but its
 // passes depend on each other, so a row is spread over a cluster of up to
-// eight CTAs whose counts are summed through distributed shared memory; the
-// scores are read four times, from L2 after the first pass.
+// eight CTAs whose counts are summed through distributed shared memory. Up to
+// 131072 scores a row stay in registers through all passes; longer rows are
+// read again for each (three digits, the count of what is kept, the writing).
 //
 // Moving the rows is bound by memory: every kept row is read once and
 // written once. A thread moves 16-byte pieces, four rows of K and V in
@@ -35,13 +36,27 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kTile = kSelWarps * 128;    // scores per block-wide compaction step
+constexpr int kMaxCluster = 8;
+constexpr int kLoads = 16;                // scores a thread has in flight
+constexpr int kHeld = 32;                 // most scores a thread keeps in registers
 
-// Ascending integers for ascending scores; NaN ranks as -inf, -0 as +0.
+// Ascending integers for ascending scores; NaN ranks as -inf, -0 as +0. Every
+// score's key lies between those of -inf and +inf, strictly inside (kAbsent,
+// kAlways), in the first and last 11-bit digit even.
+constexpr uint32_t kAbsent = 0u, kAlways = 0xffffffffu;
 ATTN_DEVINL uint32_t score_key(float s) {
   if (s != s) s = -INFINITY;
   const uint32_t u = __float_as_uint(s + 0.f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
+}
+
+// The score of a key, where the key tells it (not of held ones, nor where NaN
+// or -0 may be meant).
+ATTN_DEVINL bool key_has_score(uint32_t key) {
+  return key != kAlways && key != 0x007fffffu && key != 0x80000000u;
+}
+ATTN_DEVINL float score_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
 ATTN_DEVINL int length_of(const int* seq_lens, int b, int cap, bool& bad) {
@@ -51,16 +66,15 @@ ATTN_DEVINL int length_of(const int* seq_lens, int b, int cap, bool& bad) {
   return bad ? 0 : n;
 }
 
-struct SelectSmem {
-  int hist[kBins];         // this CTA's digit counts (read by the cluster)
-  int total[kBins];        // the cluster's
-  int part[2 * kSelWarps + 2];
-  int slice[2];            // kept-for-sure and equal-to-threshold scores of this CTA's slice
+struct __align__(16) SelectSmem {
+  int hist[3][kBins];      // this CTA's digit counts, one table per pass (read by the cluster)
+  int part[kSelWarps];
+  int sure[kSelWarps], equal[kSelWarps];   // per warp's segment (read by the cluster)
   int found[2];            // digit, and how many scores rank above it
 };
 
 // One cluster per (request, KV head) row; CTA r of C owns the r-th slice of
-// the row's scores.
+// the row's scores, warp w the w-th segment of the slice.
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ seq_lens,
                     float* __restrict__ scores_out, int* __restrict__ kept,
@@ -72,6 +86,8 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
   const int C = int(cluster.num_blocks()), r = int(cluster.block_rank());
   const int row = blockIdx.x / C, b = row / Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<int4*>(sm.hist)[i] = make_int4(0, 0, 0, 0);
   pdl_wait_primary();
 
   bool bad = false;
@@ -83,57 +99,96 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
   for (int i = m + r * kSelThreads + tid; i < n_keep; i += C * kSelThreads) idx[i] = -1;
 
   const float* s = scores + size_t(row) * score_len;
-  // slices of whole warps' reads, the last ones possibly empty
-  const int per = ((n + C - 1) / C + 31) & ~31;
-  const int lo = min(n, r * per), hi = min(n, lo + per);
+  // segments of whole warp reads, the last ones possibly short or empty
+  const int seg = ((n + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31;
+  const int lo = min(n, (r * kSelWarps + warp) * seg), hi = min(n, lo + seg);
   const int mid0 = n_sink, mid1 = n - n_recent;      // the keys that are ranked
-  int need = n_keep - n_sink - n_recent;             // how many of them are kept
-  uint32_t prefix = 0;                               // threshold digits found so far
+  const bool all = n <= n_keep;                      // (the same for the whole cluster)
+  const bool held = seg <= 32 * kHeld;
+  // Key of score j of this warp's segment (which is not empty): held sinks and
+  // recents rank above everything, lanes past the segment below. The load is
+  // not behind a branch, so that a thread's loads are in flight together.
+  auto key_at = [&](int j) {
+    const uint32_t key = score_key(s[min(j, hi - 1)]);
+    return j >= hi ? kAbsent : j < mid0 || j >= mid1 ? kAlways : key;
+  };
+  // The segment in groups of kLoads warp reads; those that fit stay in
+  // registers. f(keys of the group, index of the lane's first one).
+  uint32_t keys[kHeld];
+  auto read = [&](uint32_t* key, int j) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) key[u] = key_at(j + u * 32);
+  };
+  if (held)
+#pragma unroll
+    for (int g = 0; g < kHeld; g += kLoads)
+      if (lo + g * 32 < hi) read(keys + g, lo + g * 32 + lane);
+  auto visit = [&](auto&& f) {
+    if (held) {
+#pragma unroll
+      for (int g = 0; g < kHeld; g += kLoads)
+        if (lo + g * 32 < hi) f(keys + g, lo + g * 32 + lane);
+    } else {
+      for (int j = lo; j < hi; j += 32 * kLoads) {
+        uint32_t key[kLoads];
+        read(key, j + lane);
+        f(key, j + lane);
+      }
+    }
+  };
 
-  // (the same for every thread of the cluster)
-  const bool all = n <= n_keep;
-  if (!all && need > 0) {
-    int shift = 21, bits = 11;
-    uint32_t fixed = 0;                              // mask of the digits found so far
+  int need = all ? 0 : n_keep - n_sink - n_recent;   // how many ranked keys stay
+  // Threshold: keys above it stay, and `need` of those equal to it.
+  uint32_t bar = all ? kAbsent : need == 0 ? kAlways - 1 : 0;
+  if (need > 0) {
+    __syncthreads();                                 // the tables are zero
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
-      __syncthreads();
-      const int j0 = max(lo, mid0), j1 = min(hi, mid1);
-      for (int base = j0; base < j1; base += 4 * kSelThreads) {
-        uint32_t key[4];
-        bool in[4];
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digits = pass == 2 ? 1023 : 2047;
+      int* hist = sm.hist[pass];
+      const int above_bits = shift + (pass == 2 ? 10 : 11);
+      // (in the first pass every lane counts: absent and held ones land in
+      // the first and last bin, which no score reaches and the walk ignores)
+      visit([&](const uint32_t* key, int) {
+        uint32_t low = key[0], high = key[0];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = base + u * kSelThreads + tid;
-          in[u] = j < j1;
-          key[u] = in[u] ? score_key(s[j]) : 0;
+        for (int u = 1; u < kLoads; ++u) {
+          low = min(low, key[u]);
+          high = max(high, key[u]);
+        }
+        // Scores that were never looked at are all zero: a group that agrees
+        // adds once, where every lane would queue for the same counter.
+        if (__all_sync(0xffffffffu, low == high) &&
+            __reduce_min_sync(0xffffffffu, low) == __reduce_max_sync(0xffffffffu, low)) {
+          if (lane == 0 && (pass == 0 || low >> above_bits == bar >> above_bits))
+            atomicAdd(&hist[(low >> shift) & digits], 32 * kLoads);
+          return;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool live = in[u] && (key[u] & fixed) == prefix;
-          const int digit = live ? int((key[u] >> shift) & ((1u << bits) - 1)) : -1;
-          // scores that were never looked at are all zero: one add for a
-          // warp that agrees
-          int same;
-          __match_all_sync(0xffffffffu, digit, &same);
-          if (same) {
-            if (lane == 0 && live) atomicAdd(&sm.hist[digit], 32);
-          } else if (live) {
-            atomicAdd(&sm.hist[digit], 1);
-          }
-        }
-      }
+        for (int u = 0; u < kLoads; ++u)
+          if (pass == 0 || key[u] >> above_bits == bar >> above_bits)
+            atomicAdd(&hist[(key[u] >> shift) & digits], 1);
+      });
       cluster.sync();
-      for (int i = tid; i < kBins; i += kSelThreads) {
-        int t = 0;
-        for (int c = 0; c < C; ++c) t += cluster.map_shared_rank(&sm, c)->hist[i];
-        sm.total[i] = t;
-      }
-      __syncthreads();
-      // Thread t owns bins 4t .. 4t + 3; `above` = counts of all higher bins.
-      int mine[4], sum = 0;
+      // Thread t owns bins 4t .. 4t + 3 of the cluster's sum (the CTAs'
+      // counts as independent 16-byte reads).
+      int4 part[kMaxCluster];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sum += mine[u] = sm.total[4 * tid + u];
+      for (int c = 0; c < kMaxCluster; ++c)
+        part[c] = c < C ? reinterpret_cast<const int4*>(
+                              cluster.map_shared_rank(&sm, c)->hist[pass])[tid]
+                        : make_int4(0, 0, 0, 0);
+      int mine[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        mine[0] += part[c].x;
+        mine[1] += part[c].y;
+        mine[2] += part[c].z;
+        mine[3] += part[c].w;
+      }
+      if (pass == 0 && tid == kBins / 4 - 1) mine[3] = 0;   // the held keys
+      const int sum = mine[0] + mine[1] + mine[2] + mine[3];
       int suf = sum;                                 // suffix sums over the warp's lanes
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -142,8 +197,9 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
       }
       if (lane == 0) sm.part[warp] = suf;
       __syncthreads();
-      int above = suf - sum;
-      for (int w = warp + 1; w < kSelWarps; ++w) above += sm.part[w];
+      int above = suf - sum;                         // scores in higher bins
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) above += w > warp ? sm.part[w] : 0;
 #pragma unroll
       for (int u = 3; u >= 0; --u) {
         if (above < need && above + mine[u] >= need) {
@@ -153,93 +209,54 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
         above += mine[u];
       }
       __syncthreads();
-      prefix |= uint32_t(sm.found[0]) << shift;
-      fixed |= ((1u << bits) - 1) << shift;
+      bar |= uint32_t(sm.found[0]) << shift;
       need -= sm.found[1];
-      bits = pass == 0 ? 11 : 10;
-      shift = pass == 0 ? 10 : 0;
-      // every CTA has read this CTA's counts before they are zeroed
-      cluster.sync();
     }
   }
 
-  // What becomes of key j: kept for sure, or equal to the threshold.
-  auto classify = [&](int j, float& score, bool& sure, bool& equal) {
-    const bool in = j < hi;
-    score = in ? s[j] : 0.f;
-    const bool held = j < mid0 || j >= mid1;
-    const uint32_t key = score_key(score);
-    sure = in && (all || held || (need > 0 && key > prefix));
-    equal = in && !all && !held && need > 0 && key == prefix;
-  };
-  // (with no ranked key to keep, need is 0 and only held keys stay)
-  if (tid < 2) sm.slice[tid] = 0;
-  __syncthreads();
-  {
-    int cs = 0, ce = 0;
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      float score;
-      bool sure, equal;
-      classify(j, score, sure, equal);
-      cs += sure;
-      ce += equal;
+  // Keys of this segment that stay for sure, and that equal the threshold.
+  int n_sure = 0, n_equal = 0;
+  visit([&](const uint32_t* key, int) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      n_sure += key[u] > bar;
+      n_equal += key[u] == bar;
     }
-    cs = __reduce_add_sync(0xffffffffu, cs);
-    ce = __reduce_add_sync(0xffffffffu, ce);
-    if (lane == 0) {
-      atomicAdd(&sm.slice[0], cs);
-      atomicAdd(&sm.slice[1], ce);
-    }
+  });
+  n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+  n_equal = __reduce_add_sync(0xffffffffu, n_equal);
+  if (lane == 0) {
+    sm.sure[warp] = n_sure;
+    sm.equal[warp] = n_equal;
   }
   cluster.sync();
-  int n_sure = 0, n_equal = 0;                       // in the slices before this one
-  for (int c = 0; c < r; ++c) {
-    n_sure += cluster.map_shared_rank(&sm, c)->slice[0];
-    n_equal += cluster.map_shared_rank(&sm, c)->slice[1];
+  // How many before this segment: in the warps of the CTAs before this one,
+  // then the warps before this one.
+  int s0 = 0, e0 = 0;
+  for (int i = lane; i < r * kSelWarps + warp; i += 32) {
+    const SelectSmem* o = cluster.map_shared_rank(&sm, i / kSelWarps);
+    s0 += o->sure[i % kSelWarps];
+    e0 += o->equal[i % kSelWarps];
   }
+  s0 = __reduce_add_sync(0xffffffffu, s0);
+  e0 = __reduce_add_sync(0xffffffffu, e0);
   float* so = scores_out == nullptr ? nullptr : scores_out + size_t(row) * cap_out;
-  for (int base = lo; base < hi; base += kTile) {
-    float score[4];
-    bool sure[4], equal[4];
-    int rs[4], re[4], ws = 0, we = 0;                // ranks within the warp's 128 scores
-    const uint32_t below = (1u << lane) - 1;
+  const uint32_t below = (1u << lane) - 1;
+  visit([&](const uint32_t* key, int j0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      classify(base + warp * 128 + u * 32 + lane, score[u], sure[u], equal[u]);
-      const uint32_t bs = __ballot_sync(0xffffffffu, sure[u]);
-      const uint32_t be = __ballot_sync(0xffffffffu, equal[u]);
-      rs[u] = ws + __popc(bs & below);
-      re[u] = we + __popc(be & below);
-      ws += __popc(bs);
-      we += __popc(be);
-    }
-    if (lane == 0) {
-      sm.part[warp] = ws;
-      sm.part[kSelWarps + warp] = we;
-    }
-    __syncthreads();
-    int s0 = n_sure, e0 = n_equal, ts = 0, te = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) {
-        s0 += sm.part[w];
-        e0 += sm.part[kSelWarps + w];
+    for (int u = 0; u < kLoads; ++u) {
+      const uint32_t bs = __ballot_sync(0xffffffffu, key[u] > bar);
+      const uint32_t be = __ballot_sync(0xffffffffu, key[u] == bar);
+      const int eq_before = e0 + __popc(be & below);
+      if (key[u] > bar || (key[u] == bar && eq_before < need)) {
+        const int at = s0 + __popc(bs & below) + min(eq_before, need), j = j0 + u * 32;
+        idx[at] = j;
+        if (so != nullptr) so[at] = key_has_score(key[u]) ? score_of(key[u]) : s[j];
       }
-      ts += sm.part[w];
-      te += sm.part[kSelWarps + w];
+      s0 += __popc(bs);
+      e0 += __popc(be);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int eq_before = e0 + re[u];
-      if (sure[u] || (equal[u] && eq_before < need)) {
-        const int at = s0 + rs[u] + min(eq_before, need);
-        idx[at] = base + warp * 128 + u * 32 + lane;
-        if (so != nullptr) so[at] = score[u];
-      }
-    }
-    n_sure += ts;
-    n_equal += te;
-    __syncthreads();
-  }
+  });
   // no CTA leaves while another may still read its counts
   cluster.sync();
 }
@@ -326,12 +343,15 @@ cudaError_t launch_gather(const EvictArgs& a) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a) {
-  // CTAs per row: more while all rows' CTAs stay within two per SM and each
-  // keeps 2048 scores (one per thread and load).
+  // CTAs per row: as many as hold the row's scores in registers, and more
+  // while all rows' CTAs stay within one per SM and keep 2048 scores.
   const int rows = a.B * a.Hkv;
-  const long long slots = 2LL * (device_sm_count() > 0 ? device_sm_count() : 1);
+  const long long slots = device_sm_count() > 0 ? device_sm_count() : 1;
   int C = 1;
-  while (C < 8 && 2LL * C * rows <= slots && a.len_cap / (2 * C) >= 2048) C *= 2;
+  while (C < kMaxCluster &&
+         (a.len_cap > C * kSelThreads * kHeld ||
+          (2LL * C * rows <= slots && a.len_cap / (2 * C) >= 2048)))
+    C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(rows * C));
   cfg.blockDim = dim3(kSelThreads);
