@@ -218,8 +218,7 @@ size_t attn_key_weights_workspace_size(int B, int Hq, int Hkv, int T, int capaci
   if (!key_weights_sizes_ok(B, Hq, Hkv, T, capacity, out_len) ||
       !key_weights_sizes_supported(B, Hq, Hkv, T, capacity, out_len))
     return 0;
-  const int S = key_weights_splits(B, Hkv, Hq / Hkv * T, std::min(capacity, out_len));
-  return S == 1 ? 0 : align256(size_t(S) * B * Hkv * out_len * sizeof(float));
+  return align256(size_t(key_weights_slots(Hq / Hkv * T, T)) * B * Hkv * out_len * sizeof(float));
 }
 
 attn_status attn_key_weights(const void* q, const void* k, const float* lse, const float* prev,
@@ -250,14 +249,13 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
   const size_t n_out = size_t(B) * Hkv * out_len * 4;
   if (prev != out && overlap(prev, n_out, out, n_out)) return ATTN_ERR_INVALID_ARG;
   const int len_cap = int(std::min<long long>(cap, out_len));
-  const int S = key_weights_splits(B, Hkv, Hq / Hkv * T, len_cap);
-  if (S > 1) {
-    if (!workspace || ws_bytes < align256(S * n_out)) return ATTN_ERR_WORKSPACE;
+  if (const size_t slots = key_weights_slots(Hq / Hkv * T, T)) {
+    if (!workspace || ws_bytes < align256(slots * n_out)) return ATTN_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return ATTN_ERR_MISALIGNED;
   }
   KeyWeightsArgs a{q, k, lse, prev, out, static_cast<float*>(workspace), seq_lens, block_table,
                    B, Hq, Hkv, T, L, num_pages, page_size, max_pages_per_seq, len_cap, out_len, d,
-                   causal, S, scale, decay, static_cast<cudaStream_t>(stream)};
+                   causal, scale, decay, static_cast<cudaStream_t>(stream)};
   return from_cuda(launch_key_weights(a));
 }
 

@@ -7,23 +7,24 @@
 //
 // GB300 mapping. The product is taken transposed, Sᵀ = K Qᵀ: keys are the
 // accumulator's rows (TMEM lanes), so that the thread of a key sums its
-// weights over the columns in registers and no sum crosses threads. A
-// warpgroup owns 128 keys. Per (key, row) the tensor core spends 2·d flops
-// (1/32 cycle of an SM at d = 128) and the special-function unit one
-// exponential (1/16 cycle): with many rows the exponentials bound it, with
-// few the reading of K.
+// weights over the columns in registers and no sum crosses threads. Per (key,
+// row) the tensor core spends 2·d flops and the special-function unit one
+// exponential (1/32 cycle of an SM each at d = 128): with many rows these two
+// bound it, with few the reading of K. Four warpgroups take the sums: with
+// two, each warp's chain of loads, exponentials and adds left the units idle
+// three quarters of the time.
 //
 //  * At most 256 rows (decode steps, observation windows): the rows of a
-//    (request, KV head) stay in shared memory and the keys stream past them.
-//    One persistent CTA per SM takes an equal share of all key tiles of the
-//    batch; tiles alternate between two warpgroups, so one's exponentials
-//    overlap the other's product.
+//    (request, KV head) stay in shared memory and the keys stream past them
+//    in tiles of 128. One persistent CTA per SM takes an equal share of all
+//    key tiles of the batch. Up to 64 rows each warpgroup has its own tile;
+//    with more, two warpgroups share a tile, half of the columns each.
 //  * More rows (every token of a prompt as an observer): 256 keys of a
-//    (request, KV head) stay in shared memory, 128 per warpgroup, and the
-//    rows stream past them in chunks of 128; chunks that see none of the
-//    keys are skipped. Few keys are spread over more CTAs by cutting the
-//    rows; the partial sums are then added in a fixed order by a second
-//    kernel.
+//    (request, KV head) stay in shared memory and the rows stream past them
+//    in chunks of 128, chunks that see none of the keys left out. A
+//    persistent CTA takes an equal share of all (256 keys, 128 rows) steps;
+//    where a block of keys falls to several CTAs, their partial sums are
+//    added in a fixed order by a second kernel.
 //
 // Sums are float32; every wait is bounded, as in the other kernels.
 
@@ -42,13 +43,14 @@ ATTN_DEFINE_ERROR_WORD(take_error_key_weights)
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kThreads = 384;     // TMA, MMA, row data, idle warp; two warpgroups of keys
+constexpr int kThreads = 640;     // TMA, MMA, row data, idle warp; four warpgroups
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KwArgs {
   const float* lse;        // [B, Hkv, R]
   const float* prev;
-  float* out;              // [B, Hkv, out_len], or partial sums [S][B, Hkv, out_len]
+  float* out;              // [B, Hkv, out_len]
+  float* part;             // partial sums [slots][B, Hkv, out_len] (streaming rows)
   const int* seq_lens;
   const int* block_table;
   int B, Hkv, R, T, cap, out_len, num_pages, page_size, max_pages, box_rows;
@@ -64,77 +66,88 @@ ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
   return wrong ? 0 : n;
 }
 
-// The copies of one key tile (all lanes of a converged warp): one per (box,
-// atom); boxes past the request's keys or behind a bad page index are left
-// out, their lanes' sums are not used.
-template <int D>
-ATTN_DEVINL void load_key_tile(const KwArgs& a, uint8_t* dst, const CUtensorMap* map, int b, int g,
-                               int key0, int n, uint64_t* bar, int lane) {
-  constexpr int kAtoms = D / 64;
-  const int boxes = min(kTileKeys / a.box_rows, (n - key0 + a.box_rows - 1) / a.box_rows);
-  int row = 0, outer = 0;
-  bool good = lane < boxes;
-  if (good) {
+// Where the copies of a key tile come from: lane i < boxes has the tile's i-th
+// box; boxes past the request's keys or behind a bad page index are left out
+// (their lanes' sums are not used).
+struct KeyBox {
+  int row, outer;
+  bool good;
+};
+ATTN_DEVINL KeyBox find_key_box(const KwArgs& a, int b, int g, int key0, int n, int lane) {
+  KeyBox x{0, 0, lane < min(kTileKeys / a.box_rows, (n - key0 + a.box_rows - 1) / a.box_rows)};
+  if (x.good) {
     const int key = key0 + lane * a.box_rows;
     if (a.block_table == nullptr) {
-      row = key;
-      outer = b * a.Hkv + g;
+      x.row = key;
+      x.outer = b * a.Hkv + g;
     } else {
       const int pi = key / a.page_size;
+      x.row = key - pi * a.page_size;
       const int page = a.block_table[size_t(b) * a.max_pages + pi];
-      good = page >= 0 && page < a.num_pages;
-      if (!good) attn_flag_error(kErrBadIndex);
-      row = key - pi * a.page_size;
-      outer = page * a.Hkv + g;
+      x.good = page >= 0 && page < a.num_pages;
+      x.outer = page * a.Hkv + g;
     }
   }
-  const uint32_t live = __ballot_sync(0xffffffffu, good);
+  return x;
+}
+// The copies (all lanes of a converged warp): one per (box, atom).
+template <int D>
+ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
+                               const CUtensorMap* map, uint64_t* bar, int lane) {
+  constexpr int kAtoms = D / 64;
+  const uint32_t live = __ballot_sync(0xffffffffu, x.good);
   if (lane == 0)
     mbar_arrive_expect_tx(bar, uint32_t(__popc(live)) * a.box_rows * 128 * kAtoms);
   __syncwarp();
-  if (good)
+  if (x.good)
 #pragma unroll
     for (int at = 0; at < kAtoms; ++at)
-      tc::tma_load_3d(dst + at * (kTileKeys * 128) + lane * a.box_rows * 128, map, 64 * at, row,
-                      outer, bar);
+      tc::tma_load_3d(dst + at * (kTileKeys * 128) + lane * a.box_rows * 128, map, 64 * at, x.row,
+                      x.outer, bar);
 }
 
 // Whether the page of this thread's key may be read (its lane is in use).
 ATTN_DEVINL bool page_good(const KwArgs& a, int b, int j) {
   if (a.block_table == nullptr) return true;
   const int page = a.block_table[size_t(b) * a.max_pages + j / a.page_size];
-  return page >= 0 && page < a.num_pages;
+  const bool good = page >= 0 && page < a.num_pages;
+  if (!good) attn_flag_error(kErrBadIndex);
+  return good;
 }
 
-// What a chunk of query rows needs besides Q: the log-sum-exp in log2 units
-// (+inf where the row counts for nothing: past R, or a row that saw no key)
-// and the row's token (INT_MIN past R).
+// What a column needs besides Q: minus its log-sum-exp in log2 units (-inf
+// where the row counts for nothing: no such row, or one that saw no key) and
+// its token (INT_MIN where there is no row).
 struct RowData {
-  float lse2;
+  float neg_lse2;
   int token;
 };
-ATTN_DEVINL RowData row_data(const KwArgs& a, int head, int r) {
-  if (r >= a.R) return RowData{INFINITY, INT_MIN};
+ATTN_DEVINL RowData row_data(const KwArgs& a, int head, int r, bool in) {
+  if (!in) return RowData{-INFINITY, INT_MIN};
   const float l = a.lse[size_t(head) * a.R + r];
-  return RowData{l == -INFINITY ? INFINITY : l * kLog2e, r % a.T};
+  return RowData{l == -INFINITY ? -INFINITY : -l * kLog2e, r % a.T};
 }
 
-// Σ exp2(s·c - lse2) over NC accumulator columns, the row data read from
+ATTN_DEVINL float exp2_unit(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Adds exp2(s·c - lse2) over 16 accumulator columns, the row data read from
 // shared memory (the same address for all lanes). Masked form: a column
 // counts if its token is at least `first` (the first token that sees the key).
-template <int NC, bool kMask>
-ATTN_DEVINL void add_columns(const uint32_t (&s)[NC], const float* lse2, const int* token, float c,
-                             int first, f2 (&sum)[2]) {
+template <bool kMask>
+ATTN_DEVINL void add_columns(const uint32_t (&s)[16], const float* neg_lse2, const int* token,
+                             float c, int first, f2 (&sum)[4]) {
   const f2 c2{c, c};
 #pragma unroll
-  for (int e = 0; e < NC; e += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(lse2 + e);
-    f2 x = fma2(f2{__uint_as_float(s[e]), __uint_as_float(s[e + 1])}, c2, f2{-l.x, -l.y});
-    f2 y = fma2(f2{__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])}, c2, f2{-l.z, -l.w});
-    x.x = fast_exp2(x.x);
-    x.y = fast_exp2(x.y);
-    y.x = fast_exp2(y.x);
-    y.y = fast_exp2(y.y);
+  for (int e = 0; e < 16; e += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(neg_lse2 + e);
+    f2 x = fma2(f2{__uint_as_float(s[e]), __uint_as_float(s[e + 1])}, c2, f2{l.x, l.y});
+    f2 y = fma2(f2{__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])}, c2, f2{l.z, l.w});
+    x = f2{exp2_unit(x.x), exp2_unit(x.y)};
+    y = f2{exp2_unit(y.x), exp2_unit(y.y)};
     if (kMask) {
       const int4 t = *reinterpret_cast<const int4*>(token + e);
       x.x = t.x >= first ? x.x : 0.f;
@@ -142,43 +155,36 @@ ATTN_DEVINL void add_columns(const uint32_t (&s)[NC], const float* lse2, const i
       y.x = t.z >= first ? y.x : 0.f;
       y.y = t.w >= first ? y.y : 0.f;
     }
-    sum[0] = add2(sum[0], x);
-    sum[1] = add2(sum[1], y);
+    sum[(e / 2) & 3] = add2(sum[(e / 2) & 3], x);
+    sum[(e / 2 + 1) & 3] = add2(sum[(e / 2 + 1) & 3], y);
   }
 }
 
-// Columns [0, N) of an accumulator (N a multiple of 16), 32 at a time, the
-// next ones on their way from tensor memory while the last are summed.
-// masked: every column is tested; otherwise only those past `full`.
-ATTN_DEVINL float sum_columns(uint32_t addr, int N, int full, bool masked, const float* lse2,
-                              const int* token, float c, int first) {
-  f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-  uint32_t even[32], odd[32];
-  const int n32 = N / 32;
-  auto add = [&](const uint32_t(&s)[32], int i) {
-    if (masked || 32 * i + 32 > full)
-      add_columns<32, true>(s, lse2 + 32 * i, token + 32 * i, c, first, sum);
+// Columns [n0, n1) of an accumulator (multiples of 16), the next 16 on their
+// way from tensor memory while the last are summed. masked: every column is
+// tested; otherwise only those past `full`.
+ATTN_DEVINL float sum_columns(uint32_t addr, int n0, int n1, int full, bool masked,
+                              const float* neg_lse2, const int* token, float c, int first) {
+  f2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+  uint32_t even[16], odd[16];
+  auto add = [&](const uint32_t(&s)[16], int i) {
+    if (masked || i + 16 > full)
+      add_columns<true>(s, neg_lse2 + i, token + i, c, first, sum);
     else
-      add_columns<32, false>(s, lse2 + 32 * i, token + 32 * i, c, first, sum);
+      add_columns<false>(s, neg_lse2 + i, token + i, c, first, sum);
   };
-  if (n32 > 0) tc::tmem_ld32(addr, even);
-  for (int i = 0; i < n32; i += 2) {
+  if (n0 < n1) tc::tmem_ld16(addr + n0, even);
+  for (int i = n0; i < n1; i += 32) {
     tc::tmem_ld_wait();
-    if (i + 1 < n32) tc::tmem_ld32(addr + 32 * (i + 1), odd);
+    if (i + 16 < n1) tc::tmem_ld16(addr + i + 16, odd);
     add(even, i);
-    if (i + 1 < n32) {
+    if (i + 16 < n1) {
       tc::tmem_ld_wait();
-      if (i + 2 < n32) tc::tmem_ld32(addr + 32 * (i + 2), even);
-      add(odd, i + 1);
+      if (i + 32 < n1) tc::tmem_ld16(addr + i + 32, even);
+      add(odd, i + 16);
     }
   }
-  if (N % 32 != 0) {
-    uint32_t rest[16];
-    tc::tmem_ld16(addr + 32 * n32, rest);
-    tc::tmem_ld_wait();
-    add_columns<16, true>(rest, lse2 + 32 * n32, token + 32 * n32, c, first, sum);
-  }
-  const f2 t = add2(sum[0], sum[1]);
+  const f2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
   return t.x + t.y;
 }
 
@@ -199,12 +205,14 @@ struct KeysCfg {
   static constexpr int kStages = 4 * (128 / D);
   static constexpr int kKOff = kQBufs * kQBytes;
   static constexpr int kDynSmem = kKOff + kStages * kTileBytes + 1024;
-  static constexpr uint32_t kTmemCols = 2 * NMAX;    // one accumulator per warpgroup
+  // warpgroups per tile (half of the columns each), tiles in flight
+  static constexpr int kShare = NMAX <= 64 ? 1 : 2, kAccs = 4 / kShare;
+  static constexpr uint32_t kTmemCols = kAccs * NMAX;
 };
 
 struct KeysBars {
-  uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[2], acc_empty[2];
-  uint64_t row_full[2], row_empty[2], mma_drain;
+  uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[4], acc_empty[4];
+  uint64_t row_full[2], row_empty[2], half_full[2][2], mma_drain;
   uint32_t tmem_base;
   int abort;
   int warp_sum[kThreads / 32 + 1];
@@ -246,6 +254,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
   __shared__ KeysBars bars;
   __shared__ __align__(16) float row_lse[2][NMAX];
   __shared__ __align__(16) int row_token[2][NMAX];
+  __shared__ float half_sum[2][2][C::kShare == 2 ? kTileKeys : 1];   // [accumulator][turn]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -253,10 +262,14 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
-      mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], kTileKeys);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 2 * kTileKeys);
+      mbar_init(&bars.row_empty[i], 4 * kTileKeys);
+      mbar_init(&bars.half_full[i][0], kTileKeys);
+      mbar_init(&bars.half_full[i][1], kTileKeys);
+    }
+    for (int i = 0; i < C::kAccs; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], C::kShare * kTileKeys);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
@@ -323,9 +336,16 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
+    // (the boxes of a tile are looked up one tile ahead of its copies)
     bool ok = true, fresh = true;
     int heads = 0, i = 0;
+    KeyBox box{0, 0, false};
+    if (count > 0) box = find_key_box(a, w.b, w.g, w.tile * kTileKeys, w.n, lane);
     for (; i < count && ok; ++i) {
+      const int head = w.b * a.Hkv + w.g;
+      const bool turn = w.next(a);
+      KeyBox next{0, 0, false};
+      if (i + 1 < count) next = find_key_box(a, w.b, w.g, w.tile * kTileKeys, w.n, lane);
       if (fresh) {
         const int qb = heads % C::kQBufs;
         if (heads >= C::kQBufs)
@@ -335,7 +355,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
           mbar_arrive_expect_tx(&bars.q_full[qb], uint32_t(N) * D * 2);
           for (int at = 0; at < C::kAtoms; ++at)
             tc::tma_load_3d(smem + qb * C::kQBytes + at * (NMAX * 128), &map_q, 64 * at, 0,
-                            w.b * a.Hkv + w.g, &bars.q_full[qb]);
+                            head, &bars.q_full[qb]);
         }
         __syncwarp();
         ++heads;
@@ -344,9 +364,10 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       if (i >= C::kStages)
         ok = mbar_wait_warp(&bars.k_empty[st], (i / C::kStages - 1) & 1, abort_flag);
       if (!ok) break;
-      load_key_tile<D>(a, smem + C::kKOff + st * C::kTileBytes, &map_k, w.b, w.g,
-                       w.tile * kTileKeys, w.n, &bars.k_full[st], lane);
-      fresh = w.next(a);
+      load_key_tile<D>(a, box, smem + C::kKOff + st * C::kTileBytes, &map_k, &bars.k_full[st],
+                       lane);
+      box = next;
+      fresh = turn;
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
@@ -368,9 +389,10 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         ok = mbar_wait_warp(&bars.q_full[heads % C::kQBufs], (heads / C::kQBufs) & 1, abort_flag);
         ++heads;
       }
-      const int st = i % C::kStages, t = i & 1;
+      const int st = i % C::kStages, t = i % C::kAccs;
       if (ok) ok = mbar_wait_warp(&bars.k_full[st], (i / C::kStages) & 1, abort_flag);
-      if (ok && i >= 2) ok = mbar_wait_warp(&bars.acc_empty[t], ((i >> 1) - 1) & 1, abort_flag);
+      if (ok && i >= C::kAccs)
+        ok = mbar_wait_warp(&bars.acc_empty[t], (i / C::kAccs - 1) & 1, abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t qa = q_base + ((heads - 1) % C::kQBufs) * C::kQBytes;
@@ -405,8 +427,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         if (heads >= 2) ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
         for (int r = lane; r < N; r += 32) {
-          const RowData x = row_data(a, w.b * a.Hkv + w.g, r);
-          row_lse[rb][r] = x.lse2;
+          const RowData x = row_data(a, w.b * a.Hkv + w.g, r, r < a.R);
+          row_lse[rb][r] = x.neg_lse2;
           row_token[rb][r] = x.token;
         }
         mbar_arrive(&bars.row_full[rb]);
@@ -420,9 +442,14 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ warpgroups of keys
-    const int t = (warp - 4) / 4, quarter = warp % 4;
+    // Tile i is summed by the warpgroups of accumulator i mod kAccs; of two
+    // that share it, the second hands its half of the sum to the first.
+    const int wg = (warp - 4) / 4, quarter = warp % 4;
+    const int t = wg / C::kShare, half = wg % C::kShare;
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
     const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + t * NMAX;
+    const int mid = C::kShare == 1 ? N : (N / 2 + 15) / 16 * 16;
+    const int n0 = half == 0 ? 0 : mid, n1 = half == 0 ? mid : N;
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -432,23 +459,35 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         if (!ok) break;
         ++heads;
       }
-      if ((i & 1) == t) {
-        const int j = w.tile * kTileKeys + r;
+      if (i % C::kAccs == t) {
+        const int use = i / C::kAccs, j = w.tile * kTileKeys + r;
         const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
-        const bool live = j < w.n;
+        const bool mine = half == 0 && j < w.n;
         // on their way while the product runs
-        const float prev = live && a.prev != nullptr ? a.prev[at] : 0.f;
-        const bool good = live && page_good(a, w.b, j);
-        ok = mbar_wait_warp(&bars.acc_full[t], (i >> 1) & 1, abort_flag);
+        const float prev = mine && a.prev != nullptr ? a.prev[at] : 0.f;
+        const bool good = mine && page_good(a, w.b, j);
+        ok = mbar_wait_warp(&bars.acc_full[t], use & 1, abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
         // the tile needs its columns tested if the first token misses its last key
         const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0;
-        const float sum = sum_columns(addr, N, a.R, masked, row_lse[(heads - 1) & 1],
-                                      row_token[(heads - 1) & 1], a.c, first_token(a, w.n, j));
+        float sum = sum_columns(addr, n0, n1, a.R, masked, row_lse[(heads - 1) & 1],
+                                row_token[(heads - 1) & 1], a.c, first_token(a, w.n, j));
         tc::fence_before_sync();
         mbar_arrive(&bars.acc_empty[t]);
-        if (live) {
+        if (C::kShare == 2) {
+          // (a slot is free again two uses later: the product of the next use
+          // waited for both warpgroups' arrivals above, after this read)
+          if (half == 1) {
+            half_sum[t][use & 1][r] = sum;
+            mbar_arrive(&bars.half_full[t][use & 1]);
+          } else {
+            ok = mbar_wait_warp(&bars.half_full[t][use & 1], (use >> 1) & 1, abort_flag);
+            if (!ok) break;
+            sum += half_sum[t][use & 1][r];
+          }
+        }
+        if (mine) {
           const float kept = a.prev != nullptr ? a.decay * prev : 0.f;
           a.out[at] = good ? kept + sum : kept;
         }
@@ -471,7 +510,49 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
 
 // ---------------------------------------------------------------- many rows: rows stream
 
-constexpr int kChunk = 128;        // query rows per step
+constexpr int kChunk = 128;             // query rows per step
+constexpr int kBlock = 2 * kTileKeys;   // keys per step
+
+// The R rows of a KV head as strips of `length` rows, cut into chunks of 128
+// (the last one of a strip may be short). With T >= 128 tokens a strip is a
+// query head, and under a causal mask a block of keys needs the chunks from
+// its first token's on; with fewer tokens all rows are one strip (the mask
+// then hides nothing but inside the last blocks). A step is one chunk against
+// one block of keys; a CTA takes `least` steps at least.
+struct RowSteps {
+  int strips, length, chunks, skip, least;
+};
+RowSteps row_steps(int R, int T, int causal) {
+  RowSteps s;
+  s.strips = T >= kChunk ? R / T : 1;
+  s.length = T >= kChunk ? T : R;
+  s.chunks = (s.length + kChunk - 1) / kChunk;
+  s.skip = T >= kChunk && causal;
+  // about two steps pay for a CTA's start; at most 32 partial sums a key
+  const long long all = 1LL * s.strips * s.chunks;
+  s.least = int(std::max(4LL, (all + 29) / 30));
+  return s;
+}
+__host__ __device__ inline int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
+
+// The first chunk of a strip that sees block k of a request of n keys, and
+// the steps of the block.
+ATTN_DEVINL int first_chunk(const KwArgs& a, const RowSteps& rs, int n, int k) {
+  return rs.skip ? first_token(a, n, k * kBlock) / kChunk : 0;
+}
+ATTN_DEVINL int steps_of(const KwArgs& a, const RowSteps& rs, int n, int k) {
+  return rs.strips * (rs.chunks - first_chunk(a, rs, n, k));
+}
+ATTN_DEVINL long long steps_of_head(const KwArgs& a, const RowSteps& rs, int n) {
+  long long s = 0;
+  for (int k = 0; k < blocks_of(n); ++k) s += steps_of(a, rs, n, k);
+  return s;
+}
+// Steps per CTA: an equal share, `least` at least.
+ATTN_DEVINL long long steps_per_cta(const RowSteps& rs, long long total, int grid) {
+  const long long share = (total + grid - 1) / grid;
+  return share > rs.least ? share : rs.least;
+}
 
 template <int D>
 struct RowsCfg {
@@ -480,22 +561,57 @@ struct RowsCfg {
   static constexpr int kStages = 4;
   static constexpr int kQOff = 2 * kTileBytes;       // two key tiles first
   static constexpr int kDynSmem = kQOff + kStages * kTileBytes + 1024;
-  static constexpr uint32_t kTmemCols = 512;         // two accumulators per warpgroup
+  static constexpr uint32_t kTmemCols = 512;         // [tile][turn] accumulators of kChunk columns
 };
 
 struct RowsBars {
-  uint64_t k_full, q_full[4], q_empty[4], acc_full[2][2], acc_empty[2][2];
+  uint64_t k_full, k_empty, q_full[4], q_empty[4], acc_full[2][2], acc_empty[2][2];
   uint64_t row_full[4], row_empty[4], mma_drain;
   uint32_t tmem_base;
   int abort;
+  long long warp_sum[kThreads / 32];
+  long long begin, end, each;        // this CTA's steps; the share of a CTA
+  int start[3];                      // request, head, block where they begin
+  int offset;                        // steps of that block before them
 };
 
-// Grid: key blocks of 256, the first ones (which the most rows see) of all
-// heads first; y splits the chunks of rows.
+// The pieces of a CTA's share: runs of steps of one (request, head, block).
+struct PieceWalk {
+  int b, g, k, n, blocks;
+  int step0, steps;                  // the piece, in steps of the block
+  int all;                           // the block's steps
+  long long left;
+  ATTN_DEVINL void open(const KwArgs& a) {
+    bool bad = false;
+    n = request_len(a, b, bad);
+    blocks = blocks_of(n);
+  }
+  ATTN_DEVINL void cut(const KwArgs& a, const RowSteps& rs, int from) {
+    all = steps_of(a, rs, n, k);
+    step0 = from;
+    steps = int(min((long long)(all - from), left));
+  }
+  ATTN_DEVINL void next(const KwArgs& a, const RowSteps& rs) {
+    left -= steps;
+    if (left <= 0) return;
+    if (++k >= blocks) {
+      k = 0;
+      if (++g >= a.Hkv) {
+        g = 0;
+        do {
+          ++b;
+          open(a);
+        } while (blocks == 0);
+      }
+    }
+    cut(a, rs, 0);
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
-                    const __grid_constant__ CUtensorMap map_k, KwArgs a) {
+                    const __grid_constant__ CUtensorMap map_k, KwArgs a, RowSteps rs) {
   using C = RowsCfg<D>;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -504,19 +620,18 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   __shared__ RowsBars bars;
   __shared__ __align__(16) float row_lse[C::kStages][kChunk];
   __shared__ __align__(16) int row_token[C::kStages][kChunk];
+  __shared__ float other_sum[2][kTileKeys];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int heads = a.B * a.Hkv;
-  const int head = blockIdx.x % heads, b = head / a.Hkv, g = head % a.Hkv;
-  const int key0 = int(blockIdx.x / heads) * 2 * kTileKeys;
 
   if (tid == 0) {
     bars.abort = 0;
     mbar_init(&bars.k_full, 2);
+    mbar_init(&bars.k_empty, 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 2 * kTileKeys);
+      mbar_init(&bars.row_empty[i], 4 * kTileKeys);
     }
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
@@ -532,65 +647,121 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     tc::tmem_alloc(&bars.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
   }
+  pdl_wait_primary();
+  // This CTA's share of all steps: thread t counts a run of requests, a scan
+  // over the threads gives where each run begins.
+  {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
+    long long mine = 0;
+    bool bad = false;
+    for (int b = r0; b < r1; ++b) mine += steps_of_head(a, rs, request_len(a, b, bad)) * a.Hkv;
+    if (bad && blockIdx.x == 0) attn_flag_error(kErrBadIndex);
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    if (lane == 31) bars.warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = upto - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += bars.warp_sum[w];
+      total += bars.warp_sum[w];
+    }
+    const long long each = steps_per_cta(rs, total, gridDim.x);
+    const long long begin = min(total, each * blockIdx.x), end = min(total, begin + each);
+    if (tid == 0) {
+      bars.begin = begin;
+      bars.end = end;
+      bars.each = each;
+    }
+    if (begin < end && before <= begin && begin < before + mine) {
+      long long at = before;
+      for (int b = r0; b < r1; ++b) {
+        const int n = request_len(a, b, bad);
+        const long long head = steps_of_head(a, rs, n);
+        if (begin < at + head * a.Hkv) {
+          const int g = int((begin - at) / head);
+          long long rest = (begin - at) % head;
+          int k = 0;
+          for (; rest >= steps_of(a, rs, n, k); ++k) rest -= steps_of(a, rs, n, k);
+          bars.start[0] = b;
+          bars.start[1] = g;
+          bars.start[2] = k;
+          bars.offset = int(rest);
+          break;
+        }
+        at += head * a.Hkv;
+      }
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  pdl_wait_primary();
   const uint32_t tmem = bars.tmem_base;
   volatile int* abort_flag = &bars.abort;
-
-  bool bad = false;
-  const int n = request_len(a, b, bad);
-  if (bad && tid == 0 && key0 == 0 && g == 0 && blockIdx.y == 0) attn_flag_error(kErrBadIndex);
-  // this CTA's chunks of rows; those whose latest token does not see a
-  // tile's first key are skipped by every role alike
-  const int chunks = (a.R + kChunk - 1) / kChunk;
-  const int c0 = int(1LL * chunks * blockIdx.y / gridDim.y);
-  const int c1 = int(1LL * chunks * (blockIdx.y + 1) / gridDim.y);
-  auto last_token = [&](int c) {
-    const int r0 = c * kChunk, r1 = min(a.R, r0 + kChunk) - 1;
-    return r1 / a.T > r0 / a.T ? a.T - 1 : r1 % a.T;
+  PieceWalk w{bars.start[0], bars.start[1], bars.start[2], 0, 0, 0, 0, 0, bars.end - bars.begin};
+  if (w.left > 0) {
+    w.open(a);
+    w.cut(a, rs, bars.offset);
+  }
+  // step s of a block: chunk (first + s mod per) of strip s / per
+  struct Step {
+    int strip, chunk;
   };
-  auto first_of_chunk = [&](int c) {
-    const int r0 = c * kChunk, r1 = min(a.R, r0 + kChunk) - 1;
-    return r1 / a.T > r0 / a.T ? 0 : r0 % a.T;
+  auto step_at = [&](int s) {
+    const int c0 = first_chunk(a, rs, w.n, w.k), per = rs.chunks - c0;
+    return Step{s / per, c0 + s % per};
   };
-  const int tiles = key0 >= n ? 0 : key0 + kTileKeys < n ? 2 : 1;
-  const int from[2] = {first_token(a, n, key0), first_token(a, n, key0 + kTileKeys)};
-  auto sees = [&](int c, int t) { return t < tiles && last_token(c) >= from[t]; };
+  // whether tile t of the block has keys, and whether a chunk's last token
+  // sees its first one
+  auto sees = [&](const Step& s, int t) {
+    const int key = w.k * kBlock + t * kTileKeys;
+    if (key >= w.n) return false;
+    if (!rs.skip) return true;
+    return min(rs.length, s.chunk * kChunk + kChunk) > first_token(a, w.n, key);
+  };
 
-  if (tiles == 0) {
-    // nothing to do (the partial sums of keys past the end are never read)
-  } else if (warp == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
-    for (int t = 0; t < 2; ++t) {
-      if (t < tiles)
-        load_key_tile<D>(a, smem + t * C::kTileBytes, &map_k, b, g, key0 + t * kTileKeys, n,
-                         &bars.k_full, lane);
-      else if (lane == 0)
-        mbar_arrive(&bars.k_full);
-    }
     bool ok = true;
-    int i = 0;
-    for (int c = c0; c < c1 && ok; ++c) {
-      if (!sees(c, 0)) continue;
-      const int st = i % C::kStages;
-      if (i >= C::kStages)
-        ok = mbar_wait_warp(&bars.q_empty[st], (i / C::kStages - 1) & 1, abort_flag);
+    int i = 0, pieces = 0;
+    for (; w.left > 0 && ok; w.next(a, rs)) {
+      if (pieces > 0) ok = mbar_wait_warp(&bars.k_empty, (pieces - 1) & 1, abort_flag);
       if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars.q_full[st], C::kTileBytes);
-        for (int at = 0; at < C::kAtoms; ++at)
-          tc::tma_load_3d(smem + C::kQOff + st * C::kTileBytes + at * (kChunk * 128), &map_q,
-                          64 * at, c * kChunk, head, &bars.q_full[st]);
+      for (int t = 0; t < 2; ++t) {
+        const int key = w.k * kBlock + t * kTileKeys;
+        if (key < w.n)
+          load_key_tile<D>(a, find_key_box(a, w.b, w.g, key, w.n, lane), smem + t * C::kTileBytes,
+                           &map_k, &bars.k_full, lane);
+        else if (lane == 0)
+          mbar_arrive(&bars.k_full);
       }
-      __syncwarp();
-      ++i;
+      ++pieces;
+      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
+        const int st = i % C::kStages;
+        if (i >= C::kStages)
+          ok = mbar_wait_warp(&bars.q_empty[st], (i / C::kStages - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          const Step x = step_at(s);
+          mbar_arrive_expect_tx(&bars.q_full[st], C::kTileBytes);
+          for (int at = 0; at < C::kAtoms; ++at)
+            tc::tma_load_3d(smem + C::kQOff + st * C::kTileBytes + at * (kChunk * 128), &map_q,
+                            64 * at, x.chunk * kChunk,
+                            (w.b * a.Hkv + w.g) * rs.strips + x.strip, &bars.q_full[st]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
-      mbar_wait_warp(&bars.k_full, 0, nullptr);
+      // the loads in flight land before the CTA exits
+      if (pieces > 0) mbar_wait_warp(&bars.k_full, (pieces - 1) & 1, nullptr);
       for (int j = max(0, i - C::kStages); j < i; ++j)
         mbar_wait_warp(&bars.q_full[j % C::kStages], (j / C::kStages) & 1, nullptr);
     }
@@ -598,33 +769,37 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     // ------------------------------------------------------------ MMA issuer (the whole warp)
     constexpr uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, kChunk, false, false);
     const uint32_t k_base = smem_u32(smem), q_base = smem_u32(smem + C::kQOff);
-    bool ok = mbar_wait_warp(&bars.k_full, 0, abort_flag);
-    int i = 0, used[2] = {0, 0};
-    for (int c = c0; c < c1 && ok; ++c) {
-      if (!sees(c, 0)) continue;
-      const int st = i % C::kStages;
-      ok = mbar_wait_warp(&bars.q_full[st], (i / C::kStages) & 1, abort_flag);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (!sees(c, t)) continue;
-        const int ab = used[t] & 1;
-        if (used[t] >= 2)
-          ok = mbar_wait_warp(&bars.acc_empty[t][ab], ((used[t] >> 1) - 1) & 1, abort_flag);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t ka = k_base + t * C::kTileBytes, qa = q_base + st * C::kTileBytes;
+    bool ok = true;
+    int i = 0, pieces = 0, used[2] = {0, 0};
+    for (; w.left > 0 && ok; w.next(a, rs)) {
+      ok = mbar_wait_warp(&bars.k_full, pieces & 1, abort_flag);
+      ++pieces;
+      for (int s = w.step0; s < w.step0 + w.steps && ok; ++s, ++i) {
+        const int st = i % C::kStages;
+        const Step x = step_at(s);
+        ok = mbar_wait_warp(&bars.q_full[st], (i / C::kStages) & 1, abort_flag);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (!sees(x, t)) continue;
+          const int ab = used[t] & 1;
+          if (used[t] >= 2)
+            ok = mbar_wait_warp(&bars.acc_empty[t][ab], ((used[t] >> 1) - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t ka = k_base + t * C::kTileBytes, qa = q_base + st * C::kTileBytes;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32;
-          tc::mma_ss_warp(tmem + (2 * t + ab) * kChunk,
-                          tc::smem_desc(ka + off, 16, 1024, tc::kLayoutSW128),
-                          tc::smem_desc(qa + off, 16, 1024, tc::kLayoutSW128), idesc, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32;
+            tc::mma_ss_warp(tmem + (2 * t + ab) * kChunk,
+                            tc::smem_desc(ka + off, 16, 1024, tc::kLayoutSW128),
+                            tc::smem_desc(qa + off, 16, 1024, tc::kLayoutSW128), idesc, kk > 0);
+          }
+          tc::mma_commit_warp(&bars.acc_full[t][ab]);
+          ++used[t];
         }
-        tc::mma_commit_warp(&bars.acc_full[t][ab]);
-        ++used[t];
+        if (!ok) break;
+        tc::mma_commit_warp(&bars.q_empty[st]);
       }
-      if (!ok) break;
-      tc::mma_commit_warp(&bars.q_empty[st]);
-      ++i;
+      if (ok) tc::mma_commit_warp(&bars.k_empty);
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
@@ -637,70 +812,90 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     // ------------------------------------------------------------ row data, chunks ahead
     bool ok = true;
     int i = 0;
-    for (int c = c0; c < c1 && ok; ++c) {
-      if (!sees(c, 0)) continue;
-      const int st = i % C::kStages;
-      if (i >= C::kStages)
-        ok = mbar_wait_warp(&bars.row_empty[st], (i / C::kStages - 1) & 1, abort_flag);
-      if (!ok) break;
+    for (; w.left > 0 && ok; w.next(a, rs))
+      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
+        const int st = i % C::kStages;
+        const Step x = step_at(s);
+        if (i >= C::kStages)
+          ok = mbar_wait_warp(&bars.row_empty[st], (i / C::kStages - 1) & 1, abort_flag);
+        if (!ok) break;
 #pragma unroll
-      for (int u = 0; u < kChunk / 32; ++u) {
-        const RowData x = row_data(a, head, c * kChunk + u * 32 + lane);
-        row_lse[st][u * 32 + lane] = x.lse2;
-        row_token[st][u * 32 + lane] = x.token;
+        for (int u = 0; u < kChunk / 32; ++u) {
+          const int r = x.chunk * kChunk + u * 32 + lane;  // row of the strip
+          const RowData d = row_data(a, w.b * a.Hkv + w.g, x.strip * rs.length + r, r < rs.length);
+          row_lse[st][u * 32 + lane] = d.neg_lse2;
+          row_token[st][u * 32 + lane] = d.token;
+        }
+        mbar_arrive(&bars.row_full[st]);
       }
-      mbar_arrive(&bars.row_full[st]);
-      ++i;
-    }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ warpgroups of keys
-    const int t = (warp - 4) / 4, quarter = warp % 4;
-    const int j = key0 + t * kTileKeys + quarter * 32 + lane;
-    const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + 2 * t * kChunk;
-    const bool live = j < n;
-    const size_t at = size_t(head) * a.out_len + j;
-    const float prev = live && a.prev != nullptr ? a.prev[at] : 0.f;
-    const bool good = live && page_good(a, b, j);
-    const int first = first_token(a, n, j);
-    const int all_from = first_token(a, n, key0 + t * kTileKeys + kTileKeys - 1);
-    float sum = 0.f;
+    // Warpgroup (tile t, turn) sums every other step of its tile; the two of
+    // a tile are added at the end of a piece.
+    const int wg = (warp - 4) / 4, quarter = warp % 4, t = wg >> 1, turn = wg & 1;
+    const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
+    const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + (2 * t + turn) * kChunk;
+    long long at_step = bars.begin;
     bool ok = true;
     int i = 0, used = 0;
-    for (int c = c0; c < c1 && ok; ++c) {
-      if (!sees(c, 0)) continue;
-      const int st = i % C::kStages;
-      // (waited for by a warpgroup that skips the chunk too: its arrival below
-      // must count for this round of the stage)
-      ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
-      if (!ok) break;
-      if (sees(c, t)) {
-        ok = mbar_wait_warp(&bars.acc_full[t][used & 1], (used >> 1) & 1, abort_flag);
+    for (; w.left > 0; w.next(a, rs)) {
+      const int key0 = w.k * kBlock + t * kTileKeys, j = key0 + r;
+      const bool mine = turn == 0 && j < w.n;
+      const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
+      const float prev = mine && a.prev != nullptr ? a.prev[at] : 0.f;
+      const bool good = mine && page_good(a, w.b, j);
+      const int first = first_token(a, w.n, j);
+      const int all_from = first_token(a, w.n, key0 + kTileKeys - 1);
+      float sum = 0.f;
+      for (int s = w.step0; s < w.step0 + w.steps && ok; ++s, ++i) {
+        const int st = i % C::kStages;
+        const Step x = step_at(s);
+        // (waited for by a warpgroup that skips the chunk too: its arrival
+        // below must count for this round of the stage)
+        ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
         if (!ok) break;
-        tc::fence_after_sync();
-        const bool masked = first_of_chunk(c) < all_from;
-        sum += sum_columns(addr + (used & 1) * kChunk, kChunk, a.R - c * kChunk, masked,
-                           row_lse[st], row_token[st], a.c, first);
-        tc::fence_before_sync();
-        mbar_arrive(&bars.acc_empty[t][used & 1]);
-        ++used;
+        if (sees(x, t)) {
+          if ((used & 1) == turn) {
+            ok = mbar_wait_warp(&bars.acc_full[t][turn], (used >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc::fence_after_sync();
+            // tested column by column if the chunk's first token misses a key
+            const bool masked = (rs.skip ? x.chunk * kChunk : 0) < all_from;
+            sum += sum_columns(addr, 0, kChunk, rs.length - x.chunk * kChunk, masked, row_lse[st],
+                               row_token[st], a.c, first);
+            tc::fence_before_sync();
+            mbar_arrive(&bars.acc_empty[t][turn]);
+          }
+          ++used;
+        }
+        mbar_arrive(&bars.row_empty[st]);
       }
-      mbar_arrive(&bars.row_empty[st]);
-      ++i;
+      // (after a failed wait both warpgroups of the tile still walk all pieces,
+      // so that they meet here equally often)
+      if (turn == 1) other_sum[t][r] = sum;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + t), "r"(2 * kTileKeys) : "memory");
+      if (mine && ok) {
+        sum += other_sum[t][r];
+        if (w.steps == w.all) {                          // the whole block is this CTA's
+          const float kept = a.prev != nullptr ? a.decay * prev : 0.f;
+          a.out[at] = good ? kept + sum : kept;
+        } else {
+          // the CTA's place among those of the block
+          const long long block0 = at_step - w.step0;
+          const int slot = int(blockIdx.x - block0 / bars.each);
+          a.part[size_t(slot) * a.B * a.Hkv * a.out_len + at] = good ? sum : 0.f;
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + t), "r"(2 * kTileKeys) : "memory");
+      at_step += w.steps;
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
-    } else if (live) {
-      if (gridDim.y == 1) {
-        const float kept = a.prev != nullptr ? a.decay * prev : 0.f;
-        a.out[at] = good ? kept + sum : kept;
-      } else {
-        a.out[size_t(blockIdx.y) * heads * a.out_len + at] = good ? sum : 0.f;
-      }
     }
   }
 
@@ -712,18 +907,50 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   }
 }
 
-// out = decay · prev + the S partial sums, in order.
-__global__ void __launch_bounds__(256)
-weights_join_kernel(KwArgs a, const float* __restrict__ part, int S) {
+// out = decay · prev + the partial sums of a block that fell to several CTAs,
+// in the order of the CTAs. Grid: x blocks of 256 keys, y (request, KV head).
+__global__ void __launch_bounds__(kBlock)
+weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
+  __shared__ long long sums[2][kBlock / 32];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int head = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+  const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv, k = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
-  if (j >= request_len(a, head / a.Hkv, bad)) return;
-  const size_t at = size_t(head) * a.out_len + j, step = size_t(gridDim.y) * a.out_len;
+  // steps of all requests, and of those before this one
+  long long total = 0, before = 0;
+  for (int i = tid; i < a.B; i += kBlock) {
+    const long long s = steps_of_head(a, rs, request_len(a, i, bad)) * a.Hkv;
+    total += s;
+    if (i < b) before += s;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, off);
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+  }
+  if (lane == 0) {
+    sums[0][tid >> 5] = total;
+    sums[1][tid >> 5] = before;
+  }
+  __syncthreads();
+  total = before = 0;
+  for (int w = 0; w < kBlock / 32; ++w) {
+    total += sums[0][w];
+    before += sums[1][w];
+  }
+  const int n = request_len(a, b, bad), j = k * kBlock + tid;
+  if (j >= n) return;
+  long long first = before + g * steps_of_head(a, rs, n);
+  for (int i = 0; i < k; ++i) first += steps_of(a, rs, n, i);
+  const long long each = steps_per_cta(rs, total, grid);
+  const long long last = first + steps_of(a, rs, n, k) - 1;
+  const int slots = int(last / each - first / each) + 1;
+  if (slots == 1) return;                                // written where it was summed
+  const size_t at = size_t(blockIdx.y) * a.out_len + j, step = size_t(gridDim.y) * a.out_len;
   float sum = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < S; ++s) sum += part[s * step + at];
+  for (int s = 0; s < slots; ++s) sum += a.part[s * step + at];
   a.out[at] = a.prev != nullptr ? fmaf(a.decay, a.prev[at], sum) : sum;
 }
 
@@ -765,34 +992,29 @@ cudaError_t launch_d(const KeyWeightsArgs& w, KwArgs a) {
     return cudaErrorInvalidValue;
   if (a.R <= 64) return launch_keys<D, 64>(mk, w, a);
   if (a.R <= 256) return launch_keys<D, 256>(mk, w, a);
-  if (!make_map_bf16_3d(&mq, w.q, D, a.R, uint64_t(a.B) * a.Hkv, kChunk))
+  const RowSteps rs = row_steps(a.R, a.T, a.causal);
+  if (!make_map_bf16_3d(&mq, w.q, D, rs.length, uint64_t(a.B) * a.Hkv * rs.strips, kChunk))
     return cudaErrorInvalidValue;
-  const int blocks = (a.cap + 2 * kTileKeys - 1) / (2 * kTileKeys);
-  const int S = w.splits;
-  KwArgs pa = a;
-  if (S > 1) pa.out = w.part;
-  cudaError_t e = launch(weights_rows_kernel<D>, dim3(unsigned(blocks) * a.B * a.Hkv, S), kThreads,
-                         RowsCfg<D>::kDynSmem, w.stream, mq, mk, pa);
-  if (e != cudaSuccess || S == 1) return e;
-  return launch(weights_join_kernel, dim3((a.cap + 255) / 256, a.B * a.Hkv), 256, 0, w.stream, a,
-                static_cast<const float*>(w.part), S);
+  const long long most = 1LL * a.B * a.Hkv * blocks_of(a.cap) * rs.strips * rs.chunks;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 1;
+  const int grid = int(std::min<long long>(sms, (most + rs.least - 1) / rs.least));
+  cudaError_t e = launch(weights_rows_kernel<D>, dim3(grid), kThreads, RowsCfg<D>::kDynSmem,
+                         w.stream, mq, mk, a, rs);
+  if (e != cudaSuccess) return e;
+  return launch(weights_join_kernel, dim3(blocks_of(a.cap), a.B * a.Hkv), 2 * kTileKeys, 0,
+                w.stream, a, rs, grid);
 }
 
 }  // namespace
 
-// Splits of the query rows: none while they stay in shared memory; else as
-// many as give four CTAs per SM (their work differs under the causal mask),
-// of eight chunks at least.
-int key_weights_splits(int B, int Hkv, int R, int cap) {
-  if (R <= 256) return 1;
-  const long long sms = device_sm_count() > 0 ? device_sm_count() : 152;
-  const long long ctas = 1LL * B * Hkv * ((cap + 2 * kTileKeys - 1) / (2 * kTileKeys));
-  const long long most = std::max(1, (R + kChunk - 1) / kChunk / 8);
-  return int(std::min<long long>(std::min<long long>(most, 64), (4 * sms + ctas - 1) / ctas));
+int key_weights_slots(int R, int T) {
+  if (R <= 256) return 0;
+  const RowSteps rs = row_steps(R, T, 0);
+  return (rs.strips * rs.chunks - 1) / rs.least + 2;
 }
 
 cudaError_t launch_key_weights(const KeyWeightsArgs& w) {
-  KwArgs a{w.lse, w.prev, w.out, w.seq_lens, w.block_table, w.B, w.Hkv, w.Hq / w.Hkv * w.T, w.T,
+  KwArgs a{w.lse, w.prev, w.out, w.part, w.seq_lens, w.block_table, w.B, w.Hkv, w.Hq / w.Hkv * w.T, w.T,
            w.len_cap, w.out_len, w.num_pages, w.page_size, w.max_pages, kTileKeys, w.causal,
            w.scale * kLog2e, w.decay};
   // copies of a key tile: whole tiles of a contiguous cache or a single

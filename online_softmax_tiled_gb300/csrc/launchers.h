@@ -150,10 +150,10 @@ struct KeyWeightsArgs {
   const float* lse;
   const float* prev;
   float* out;
-  float* part;             // splits > 1: partial sums [splits][B, Hkv, out_len]
+  float* part;             // partial sums [key_weights_slots(R, T)][B, Hkv, out_len]
   const int* seq_lens;
   const int* block_table;  // nullptr: contiguous cache [B, Hkv, L, d]
-  int B, Hq, Hkv, T, L, num_pages, page_size, max_pages, len_cap, out_len, d, causal, splits;
+  int B, Hq, Hkv, T, L, num_pages, page_size, max_pages, len_cap, out_len, d, causal;
   float scale, decay;
   cudaStream_t stream;
 };
@@ -284,9 +284,9 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_siz
                        int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
                        int own_splits);
 cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& plan);
-// Splits of the R = (Hq / Hkv)·T query rows per KV head that
-// launch_key_weights uses for a capacity of `cap` keys.
-int key_weights_splits(int B, int Hkv, int R, int cap);
+// Most partial sums per key that launch_key_weights leaves with R = (Hq /
+// Hkv)·T query rows per KV head (0: none).
+int key_weights_slots(int R, int T);
 cudaError_t launch_key_weights(const KeyWeightsArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);
 cudaError_t launch_evict(const EvictArgs& a);
