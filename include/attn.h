@@ -464,8 +464,8 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
  *                    exp(scale * q[b,h,i] . k[b,g,j] - lse[b,h,i])
  * for the n = seq_lens[b] keys of request b. The T queries are the last T of
  * the n positions: with causal = 1 key j is seen by token i iff
- * j <= n - T + i, with causal = 0 by all. A row with lse = -inf gives
- * nothing. prev == NULL: no first term (decay ignored); prev == out adds in
+ * j <= n - T + i, with causal = 0 by all. A row with an infinite lse
+ * gives nothing. prev == NULL: no first term (decay ignored); prev == out adds in
  * place; any other overlap of the two is refused. out[b,g,j] for j >= n is
  * left as it was.
  *
@@ -474,8 +474,8 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
  * length L) or pages [num_pages,Hkv,page_size,d] behind block_table
  * [B,max_pages_per_seq] (seq_lens given; L ignored; page_size a multiple of
  * 8 unless max_pages_per_seq is 1); prev, out float32 [B,Hkv,out_len].
- * d 64 or 128; any Hq that is a multiple of Hkv; any T. scale and decay
- * finite. Products of bf16 values are exact in the float32 accumulation,
+ * d 64 or 128; any Hq that is a multiple of Hkv; any T. scale finite and at
+ * least 1e-30, decay finite. Products of bf16 values are exact in the float32 accumulation,
  * weights and sums are float32, added in a fixed order.
  * B * Hkv at most 65535, B * Hkv * ceil(capacity / 128) and T * Hq / Hkv at
  * most 2^30.

@@ -233,7 +233,8 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
   const long long cap = block_table != nullptr ? 1LL * max_pages_per_seq * page_size : L;
   if (!key_weights_sizes_ok(B, Hq, Hkv, T, cap, out_len)) return ATTN_ERR_INVALID_ARG;
   if (seq_lens == nullptr && out_len < L) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || (prev != nullptr && !std::isfinite(decay)))
+  // (1 / scale times a log-sum-exp must stay in range)
+  if (!(scale >= 1e-30f) || !std::isfinite(scale) || (prev != nullptr && !std::isfinite(decay)))
     return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;

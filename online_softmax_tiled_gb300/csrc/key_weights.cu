@@ -10,21 +10,25 @@
 // weights over the columns in registers and no sum crosses threads. Per (key,
 // row) the tensor core spends 2·d flops and the special-function unit one
 // exponential (1/32 cycle of an SM each at d = 128): with many rows these two
-// bound it, with few the reading of K. Four warpgroups take the sums: with
-// two, each warp's chain of loads, exponentials and adds left the units idle
-// three quarters of the time.
+// bound it, with few the reading of K. A warpgroup reads 128 accumulator
+// columns into registers at once and gives the accumulator back before it
+// computes, so that products and exponentials overlap. The rows' -lse/scale
+// enters the accumulator as one more K = 16 step of the product (a tile of
+// ones times three bf16 parts that make up the float32), because a per-column
+// read of it from shared memory competes with the product's operands: both
+// take about 100 bytes a cycle.
 //
 //  * At most 256 rows (decode steps, observation windows): the rows of a
 //    (request, KV head) stay in shared memory and the keys stream past them
 //    in tiles of 128. One persistent CTA per SM takes an equal share of all
-//    key tiles of the batch. Up to 64 rows each warpgroup has its own tile;
-//    with more, two warpgroups share a tile, half of the columns each.
+//    key tiles of the batch. Up to 128 rows the two warpgroups take
+//    alternate tiles; with more, half of the columns of every tile.
 //  * More rows (every token of a prompt as an observer): 256 keys of a
-//    (request, KV head) stay in shared memory and the rows stream past them
-//    in chunks of 128, chunks that see none of the keys left out. A
-//    persistent CTA takes an equal share of all (256 keys, 128 rows) steps;
-//    where a block of keys falls to several CTAs, their partial sums are
-//    added in a fixed order by a second kernel.
+//    (request, KV head) stay in shared memory, 128 per warpgroup, and the
+//    rows stream past them in chunks of 128, chunks that see none of the
+//    keys left out. A persistent CTA takes an equal share of all (256 keys,
+//    128 rows) steps; where a block of keys falls to several CTAs, their
+//    partial sums are added in a fixed order by a second kernel.
 //
 // Sums are float32; every wait is bounded, as in the other kernels.
 
@@ -43,7 +47,7 @@ ATTN_DEFINE_ERROR_WORD(take_error_key_weights)
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kThreads = 640;     // TMA, MMA, row data, idle warp; four warpgroups
+constexpr int kThreads = 384;     // TMA, MMA, row data, idle warp; two warpgroups of keys
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KwArgs {
@@ -55,7 +59,7 @@ struct KwArgs {
   const int* block_table;
   int B, Hkv, R, T, cap, out_len, num_pages, page_size, max_pages, box_rows;
   int causal;
-  float c, decay;          // scale · log2 e
+  float c, inv_scale, decay;   // scale · log2 e, 1 / scale
 };
 
 ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
@@ -106,26 +110,59 @@ ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
                       x.outer, bar);
 }
 
-// Whether the page of this thread's key may be read (its lane is in use).
-ATTN_DEVINL bool page_good(const KwArgs& a, int b, int j) {
-  if (a.block_table == nullptr) return true;
-  const int page = a.block_table[size_t(b) * a.max_pages + j / a.page_size];
-  const bool good = page >= 0 && page < a.num_pages;
-  if (!good) attn_flag_error(kErrBadIndex);
-  return good;
+// What a row needs besides Q: -lse/scale as three bf16 parts whose sum is the
+// float32 value (far below any score where the row counts for nothing: no
+// such row, or an infinite lse, as of a row that saw no key), and its token
+// (INT_MIN where there is no row).
+//
+// The parts are the row's first three columns of a K = 16 operand tile: core
+// matrices of 8 rows x 16 bytes, two along K, groups of 8 rows every 256
+// bytes; the other columns stay zero.
+constexpr int kPartsRow = 32;                 // bytes of a row in the operand tile
+constexpr float kFarBelow = -3.0e38f;
+ATTN_DEVINL void put_row(const KwArgs& a, int head, int r, bool in, uint8_t* parts, int n,
+                         int* token) {
+  float v = kFarBelow;
+  if (in) {
+    const float l = a.lse[size_t(head) * a.R + r];
+    v = -l * a.inv_scale;
+    if (fabsf(l) == INFINITY) v = kFarBelow;
+    if (v > -kFarBelow) v = -kFarBelow;
+    if (v < kFarBelow) v = kFarBelow;
+  }
+  token[n] = in ? r % a.T : INT_MIN;
+  const float p0 = __bfloat162float(__float2bfloat16_rn(v));
+  const float p1 = __bfloat162float(__float2bfloat16_rn(v - p0));
+  *reinterpret_cast<uint4*>(parts + (n >> 3) * 256 + (n & 7) * 16) =
+      make_uint4(pack_bf16x2(p0, p1), pack_bf16x2(v - p0 - p1, 0.f), 0u, 0u);
+}
+// Ones for the other operand (128 rows x 16), zeros for `bytes` of parts.
+ATTN_DEVINL void fill_parts(uint8_t* ones, uint8_t* parts, int bytes, int tid) {
+  for (int i = tid; i < kTileKeys * kPartsRow / 16; i += kThreads)
+    reinterpret_cast<uint4*>(ones)[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u,
+                                                   0x3F803F80u);
+  for (int i = tid; i < bytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(parts)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
 }
 
-// What a column needs besides Q: minus its log-sum-exp in log2 units (-inf
-// where the row counts for nothing: no such row, or one that saw no key) and
-// its token (INT_MIN where there is no row).
-struct RowData {
-  float neg_lse2;
-  int token;
-};
-ATTN_DEVINL RowData row_data(const KwArgs& a, int head, int r, bool in) {
-  if (!in) return RowData{-INFINITY, INT_MIN};
-  const float l = a.lse[size_t(head) * a.R + r];
-  return RowData{l == -INFINITY ? -INFINITY : -l * kLog2e, r % a.T};
+// Sᵀ - lse/scale for one key tile against n query rows, all lanes of the
+// issuing warp: D/16 steps over K and Q (128-byte swizzle, `pitch` rows per
+// 64-column atom of Q), then the parts.
+template <int D>
+ATTN_DEVINL void issue_product(uint32_t acc, uint32_t ka, uint32_t qa, int pitch, uint32_t ones,
+                               uint32_t parts, int n) {
+  const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, n, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    tc::mma_ss_warp(acc,
+                    tc::smem_desc(ka + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32, 16, 1024,
+                                  tc::kLayoutSW128),
+                    tc::smem_desc(qa + (kk / 4) * (pitch * 128) + (kk % 4) * 32, 16, 1024,
+                                  tc::kLayoutSW128),
+                    idesc, kk > 0);
+  tc::mma_ss_warp(acc, tc::smem_desc(ones, 128, 256, tc::kLayoutNone),
+                  tc::smem_desc(parts, 128, 256, tc::kLayoutNone), idesc, 1u);
 }
 
 ATTN_DEVINL float exp2_unit(float x) {
@@ -134,18 +171,16 @@ ATTN_DEVINL float exp2_unit(float x) {
   return y;
 }
 
-// Adds exp2(s·c - lse2) over 16 accumulator columns, the row data read from
-// shared memory (the same address for all lanes). Masked form: a column
-// counts if its token is at least `first` (the first token that sees the key).
+// Adds exp2(c·s) over 16 columns. Masked form: a column counts if its token
+// is at least `first` (the first token that sees the key).
 template <bool kMask>
-ATTN_DEVINL void add_columns(const uint32_t (&s)[16], const float* neg_lse2, const int* token,
-                             float c, int first, f2 (&sum)[4]) {
+ATTN_DEVINL void add_columns(const uint32_t* s, const int* token, float c, int first,
+                             f2 (&sum)[4]) {
   const f2 c2{c, c};
 #pragma unroll
   for (int e = 0; e < 16; e += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(neg_lse2 + e);
-    f2 x = fma2(f2{__uint_as_float(s[e]), __uint_as_float(s[e + 1])}, c2, f2{l.x, l.y});
-    f2 y = fma2(f2{__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])}, c2, f2{l.z, l.w});
+    f2 x = mul2(f2{__uint_as_float(s[e]), __uint_as_float(s[e + 1])}, c2);
+    f2 y = mul2(f2{__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])}, c2);
     x = f2{exp2_unit(x.x), exp2_unit(x.y)};
     y = f2{exp2_unit(y.x), exp2_unit(y.y)};
     if (kMask) {
@@ -160,32 +195,67 @@ ATTN_DEVINL void add_columns(const uint32_t (&s)[16], const float* neg_lse2, con
   }
 }
 
-// Columns [n0, n1) of an accumulator (multiples of 16), the next 16 on their
-// way from tensor memory while the last are summed. masked: every column is
-// tested; otherwise only those past `full`.
-ATTN_DEVINL float sum_columns(uint32_t addr, int n0, int n1, int full, bool masked,
-                              const float* neg_lse2, const int* token, float c, int first) {
+// The sum over n columns (a multiple of 16, at most 128) of an accumulator,
+// which is given back (an arrival on `empty`) as soon as it is in registers.
+// masked: every column is tested; otherwise only those past `full`.
+ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const int* token,
+                              float c, int first, uint64_t* empty) {
+  uint32_t s[128];
+  if (n == 128) {
+#pragma unroll
+    for (int i = 0; i < 128; i += 32)
+      tc::tmem_ld32(addr + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 128; i += 16)
+      if (i < n) tc::tmem_ld16(addr + i, *reinterpret_cast<uint32_t(*)[16]>(&s[i]));
+  }
+  tc::tmem_ld_wait();
+  tc::fence_before_sync();
+  mbar_arrive(empty);
   f2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-  uint32_t even[16], odd[16];
-  auto add = [&](const uint32_t(&s)[16], int i) {
-    if (masked || i + 16 > full)
-      add_columns<true>(s, neg_lse2 + i, token + i, c, first, sum);
-    else
-      add_columns<false>(s, neg_lse2 + i, token + i, c, first, sum);
-  };
-  if (n0 < n1) tc::tmem_ld16(addr + n0, even);
-  for (int i = n0; i < n1; i += 32) {
-    tc::tmem_ld_wait();
-    if (i + 16 < n1) tc::tmem_ld16(addr + i + 16, odd);
-    add(even, i);
-    if (i + 16 < n1) {
-      tc::tmem_ld_wait();
-      if (i + 32 < n1) tc::tmem_ld16(addr + i + 32, even);
-      add(odd, i + 16);
-    }
+  if (!masked && n == 128 && full >= 128) {
+#pragma unroll
+    for (int i = 0; i < 128; i += 16) add_columns<false>(s + i, token + i, c, first, sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 128; i += 16)
+      if (i < n) {
+        if (masked || i + 16 > full)
+          add_columns<true>(s + i, token + i, c, first, sum);
+        else
+          add_columns<false>(s + i, token + i, c, first, sum);
+      }
   }
   const f2 t = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
   return t.x + t.y;
+}
+
+// What the thread of a key reads for its output, on its way before the sum.
+struct KeyOut {
+  size_t at;
+  float prev;
+  int page;                    // of a paged cache; checked when the sum is written
+  bool live;
+};
+ATTN_DEVINL KeyOut find_key_out(const KwArgs& a, int b, int g, int j, int n) {
+  KeyOut o{(size_t(b) * a.Hkv + g) * a.out_len + j, 0.f, 0, j < n};
+  if (o.live) {
+    if (a.prev != nullptr) o.prev = a.prev[o.at];
+    if (a.block_table != nullptr)
+      o.page = a.block_table[size_t(b) * a.max_pages + j / a.page_size];
+  }
+  return o;
+}
+ATTN_DEVINL bool page_good(const KwArgs& a, const KeyOut& o) {
+  const bool good = a.block_table == nullptr || (o.page >= 0 && o.page < a.num_pages);
+  if (!good) attn_flag_error(kErrBadIndex);
+  return good;
+}
+ATTN_DEVINL void write_key(const KwArgs& a, const KeyOut& o, float sum) {
+  if (!o.live) return;
+  const float kept = a.prev != nullptr ? a.decay * o.prev : 0.f;
+  a.out[o.at] = page_good(a, o) ? kept + sum : kept;
 }
 
 // The first token that sees key j (any token without a causal mask, but
@@ -200,19 +270,23 @@ template <int D, int NMAX>
 struct KeysCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTileKeys * D * 2;
-  static constexpr int kQBufs = NMAX <= 64 ? 2 : 1;
+  // warpgroups that share a tile (128 columns each), or else alternate
+  static constexpr int kShare = NMAX / 128;
+  static constexpr int kQBufs = kShare == 1 ? 2 : 1;
   static constexpr int kQBytes = NMAX * D * 2;
   static constexpr int kStages = 4 * (128 / D);
   static constexpr int kKOff = kQBufs * kQBytes;
-  static constexpr int kDynSmem = kKOff + kStages * kTileBytes + 1024;
-  // warpgroups per tile (half of the columns each), tiles in flight
-  static constexpr int kShare = NMAX <= 64 ? 1 : 2, kAccs = 4 / kShare;
-  static constexpr uint32_t kTmemCols = kAccs * NMAX;
+  static constexpr int kOnesOff = kKOff + kStages * kTileBytes;
+  static constexpr int kPartsOff = kOnesOff + kTileKeys * kPartsRow;   // of two heads
+  static constexpr int kPartsBytes = NMAX * kPartsRow;
+  static constexpr int kDynSmem = kPartsOff + 2 * kPartsBytes + 1024;
+  // accumulators: two of 128 columns per warpgroup, or two of 256 for both
+  static constexpr uint32_t kTmemCols = 512;
 };
 
 struct KeysBars {
   uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[4], acc_empty[4];
-  uint64_t row_full[2], row_empty[2], half_full[2][2], mma_drain;
+  uint64_t row_full[2], row_empty[2], half_full[3], mma_drain;
   uint32_t tmem_base;
   int abort;
   int warp_sum[kThreads / 32 + 1];
@@ -252,9 +326,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   __shared__ KeysBars bars;
-  __shared__ __align__(16) float row_lse[2][NMAX];
   __shared__ __align__(16) int row_token[2][NMAX];
-  __shared__ float half_sum[2][2][C::kShare == 2 ? kTileKeys : 1];   // [accumulator][turn]
+  __shared__ float half_sum[3][C::kShare == 2 ? kTileKeys : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -263,14 +336,13 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 4 * kTileKeys);
-      mbar_init(&bars.half_full[i][0], kTileKeys);
-      mbar_init(&bars.half_full[i][1], kTileKeys);
+      mbar_init(&bars.row_empty[i], 2 * kTileKeys + 1);   // the warpgroups and the products
     }
-    for (int i = 0; i < C::kAccs; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], C::kShare * kTileKeys);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.half_full[i], kTileKeys);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
       mbar_init(&bars.k_empty[i], 1);
@@ -284,6 +356,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     tc::tmem_alloc(&bars.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
   }
+  fill_parts(smem + C::kOnesOff, smem + C::kPartsOff, 2 * C::kPartsBytes, tid);
   pdl_wait_primary();
   // This CTA's share of the batch's key tiles: thread t counts a run of
   // requests, a scan over the threads gives where each run begins.
@@ -337,6 +410,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
     // (the boxes of a tile are looked up one tile ahead of its copies)
+    regs_dec<80>();
     bool ok = true, fresh = true;
     int heads = 0, i = 0;
     KeyBox box{0, 0, false};
@@ -380,35 +454,35 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
-    const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, N, false, false);
+    regs_dec<80>();
     const uint32_t q_base = smem_u32(smem), k_base = smem_u32(smem + C::kKOff);
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
       if (fresh) {
         ok = mbar_wait_warp(&bars.q_full[heads % C::kQBufs], (heads / C::kQBufs) & 1, abort_flag);
+        if (ok) ok = mbar_wait_warp(&bars.row_full[heads & 1], (heads >> 1) & 1, abort_flag);
         ++heads;
       }
-      const int st = i % C::kStages, t = i % C::kAccs;
+      const int st = i % C::kStages;
       if (ok) ok = mbar_wait_warp(&bars.k_full[st], (i / C::kStages) & 1, abort_flag);
-      if (ok && i >= C::kAccs)
-        ok = mbar_wait_warp(&bars.acc_empty[t], (i / C::kAccs - 1) & 1, abort_flag);
+      const int use = C::kShare == 1 ? i >> 1 : i;
+      const int acc = C::kShare == 1 ? 2 * (i & 1) + (use & 1) : use & 1;
+      if (ok && use >= 2)
+        ok = mbar_wait_warp(&bars.acc_empty[acc], ((use >> 1) - 1) & 1, abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t qa = q_base + ((heads - 1) % C::kQBufs) * C::kQBytes;
-      const uint32_t ka = k_base + st * C::kTileBytes;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc::mma_ss_warp(tmem + t * NMAX,
-                        tc::smem_desc(ka + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32, 16, 1024,
-                                      tc::kLayoutSW128),
-                        tc::smem_desc(qa + (kk / 4) * (NMAX * 128) + (kk % 4) * 32, 16, 1024,
-                                      tc::kLayoutSW128),
-                        idesc, kk > 0);
-      tc::mma_commit_warp(&bars.acc_full[t]);
+      issue_product<D>(tmem + acc * NMAX, k_base + st * C::kTileBytes,
+                       q_base + ((heads - 1) % C::kQBufs) * C::kQBytes, NMAX,
+                       smem_u32(smem + C::kOnesOff),
+                       smem_u32(smem + C::kPartsOff + ((heads - 1) & 1) * C::kPartsBytes), N);
+      tc::mma_commit_warp(&bars.acc_full[acc]);
       tc::mma_commit_warp(&bars.k_empty[st]);
       fresh = w.next(a);
-      if (fresh) tc::mma_commit_warp(&bars.q_empty[(heads - 1) % C::kQBufs]);
+      if (fresh) {
+        tc::mma_commit_warp(&bars.q_empty[(heads - 1) % C::kQBufs]);
+        tc::mma_commit_warp(&bars.row_empty[(heads - 1) & 1]);
+      }
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
@@ -419,6 +493,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_wait_warp(&bars.mma_drain, 0, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------------ row data, one head ahead
+    regs_dec<80>();
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -426,11 +501,10 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         const int rb = heads & 1;
         if (heads >= 2) ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
-        for (int r = lane; r < N; r += 32) {
-          const RowData x = row_data(a, w.b * a.Hkv + w.g, r, r < a.R);
-          row_lse[rb][r] = x.neg_lse2;
-          row_token[rb][r] = x.token;
-        }
+        for (int r = lane; r < N; r += 32)
+          put_row(a, w.b * a.Hkv + w.g, r, r < a.R, smem + C::kPartsOff + rb * C::kPartsBytes, r,
+                  row_token[rb]);
+        fence_proxy_async_smem();
         mbar_arrive(&bars.row_full[rb]);
         ++heads;
       }
@@ -440,16 +514,32 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    regs_dec<80>();
+  } else {
     // ------------------------------------------------------------ warpgroups of keys
-    // Tile i is summed by the warpgroups of accumulator i mod kAccs; of two
-    // that share it, the second hands its half of the sum to the first.
-    const int wg = (warp - 4) / 4, quarter = warp % 4;
-    const int t = wg / C::kShare, half = wg % C::kShare;
+    // 128 x 80 + 256 x 208 registers <= 384 x 168 at launch
+    regs_inc<208>();
+    // Alternate tiles, or half of the columns of each: then the second
+    // warpgroup hands its sum to the first.
+    const int t = (warp - 4) / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
-    const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + t * NMAX;
-    const int mid = C::kShare == 1 ? N : (N / 2 + 15) / 16 * 16;
-    const int n0 = half == 0 ? 0 : mid, n1 = half == 0 ? mid : N;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const int col0 = C::kShare == 1 ? 0 : 128 * t, cols = min(N - col0, 128);
+    const bool writes = C::kShare == 1 || t == 0;
+    constexpr int kEvery = C::kShare == 1 ? 2 : 1;       // this warpgroup's tiles
+    // what the next of its tiles needs for its output, fetched a tile early
+    TileWalk ahead = w;
+    int ahead_at = 0;
+    auto fetch = [&](int i) {
+      KeyOut o{0, 0.f, 0, false};
+      if (writes && i < count) {
+        for (; ahead_at < i; ++ahead_at) ahead.next(a);
+        o = find_key_out(a, ahead.b, ahead.g, ahead.tile * kTileKeys + r, ahead.n);
+      }
+      return o;
+    };
+    KeyOut out = fetch(C::kShare == 1 ? t : 0);
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -459,38 +549,32 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         if (!ok) break;
         ++heads;
       }
-      if (i % C::kAccs == t) {
-        const int use = i / C::kAccs, j = w.tile * kTileKeys + r;
-        const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
-        const bool mine = half == 0 && j < w.n;
-        // on their way while the product runs
-        const float prev = mine && a.prev != nullptr ? a.prev[at] : 0.f;
-        const bool good = mine && page_good(a, w.b, j);
-        ok = mbar_wait_warp(&bars.acc_full[t], use & 1, abort_flag);
+      if (C::kShare == 2 || (i & 1) == t) {
+        const int use = C::kShare == 1 ? i >> 1 : i;
+        const int acc = C::kShare == 1 ? 2 * t + (use & 1) : use & 1;
+        const KeyOut next = fetch(i + kEvery);
+        ok = mbar_wait_warp(&bars.acc_full[acc], (use >> 1) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
         // the tile needs its columns tested if the first token misses its last key
         const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0;
-        float sum = sum_columns(addr, n0, n1, a.R, masked, row_lse[(heads - 1) & 1],
-                                row_token[(heads - 1) & 1], a.c, first_token(a, w.n, j));
-        tc::fence_before_sync();
-        mbar_arrive(&bars.acc_empty[t]);
+        float sum = sum_columns(lanes + acc * NMAX + col0, cols, a.R - col0, masked,
+                                row_token[(heads - 1) & 1] + col0, a.c,
+                                first_token(a, w.n, w.tile * kTileKeys + r), &bars.acc_empty[acc]);
         if (C::kShare == 2) {
-          // (a slot is free again two uses later: the product of the next use
-          // waited for both warpgroups' arrivals above, after this read)
-          if (half == 1) {
-            half_sum[t][use & 1][r] = sum;
-            mbar_arrive(&bars.half_full[t][use & 1]);
+          // Three slots: the second warpgroup is at most two tiles ahead (an
+          // accumulator is filled again once both have read it).
+          if (t == 1) {
+            half_sum[i % 3][r] = sum;
+            mbar_arrive(&bars.half_full[i % 3]);
           } else {
-            ok = mbar_wait_warp(&bars.half_full[t][use & 1], (use >> 1) & 1, abort_flag);
+            ok = mbar_wait_warp(&bars.half_full[i % 3], (i / 3) & 1, abort_flag);
             if (!ok) break;
-            sum += half_sum[t][use & 1][r];
+            sum += half_sum[i % 3][r];
           }
         }
-        if (mine) {
-          const float kept = a.prev != nullptr ? a.decay * prev : 0.f;
-          a.out[at] = good ? kept + sum : kept;
-        }
+        if (writes) write_key(a, out, sum);
+        out = next;
       }
       fresh = w.next(a);
     }
@@ -560,7 +644,10 @@ struct RowsCfg {
   static constexpr int kTileBytes = kTileKeys * D * 2;
   static constexpr int kStages = 4;
   static constexpr int kQOff = 2 * kTileBytes;       // two key tiles first
-  static constexpr int kDynSmem = kQOff + kStages * kTileBytes + 1024;
+  static constexpr int kOnesOff = kQOff + kStages * kTileBytes;
+  static constexpr int kPartsOff = kOnesOff + kTileKeys * kPartsRow;   // of a stage's rows
+  static constexpr int kPartsBytes = kChunk * kPartsRow;
+  static constexpr int kDynSmem = kPartsOff + kStages * kPartsBytes + 1024;
   static constexpr uint32_t kTmemCols = 512;         // [tile][turn] accumulators of kChunk columns
 };
 
@@ -618,9 +705,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   __shared__ RowsBars bars;
-  __shared__ __align__(16) float row_lse[C::kStages][kChunk];
   __shared__ __align__(16) int row_token[C::kStages][kChunk];
-  __shared__ float other_sum[2][kTileKeys];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -631,7 +716,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 4 * kTileKeys);
+      mbar_init(&bars.row_empty[i], 2 * kTileKeys + 1);   // the warpgroups and the products
     }
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
@@ -647,6 +732,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     tc::tmem_alloc(&bars.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
   }
+  fill_parts(smem + C::kOnesOff, smem + C::kPartsOff, C::kStages * C::kPartsBytes, tid);
   pdl_wait_primary();
   // This CTA's share of all steps: thread t counts a run of requests, a scan
   // over the threads gives where each run begins.
@@ -726,6 +812,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
+    regs_dec<80>();
     bool ok = true;
     int i = 0, pieces = 0;
     for (; w.left > 0 && ok; w.next(a, rs)) {
@@ -767,7 +854,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, kChunk, false, false);
+    regs_dec<80>();
     const uint32_t k_base = smem_u32(smem), q_base = smem_u32(smem + C::kQOff);
     bool ok = true;
     int i = 0, pieces = 0, used[2] = {0, 0};
@@ -778,6 +865,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         const int st = i % C::kStages;
         const Step x = step_at(s);
         ok = mbar_wait_warp(&bars.q_full[st], (i / C::kStages) & 1, abort_flag);
+        if (ok) ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
         for (int t = 0; t < 2 && ok; ++t) {
           if (!sees(x, t)) continue;
           const int ab = used[t] & 1;
@@ -785,19 +873,15 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
             ok = mbar_wait_warp(&bars.acc_empty[t][ab], ((used[t] >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t ka = k_base + t * C::kTileBytes, qa = q_base + st * C::kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32;
-            tc::mma_ss_warp(tmem + (2 * t + ab) * kChunk,
-                            tc::smem_desc(ka + off, 16, 1024, tc::kLayoutSW128),
-                            tc::smem_desc(qa + off, 16, 1024, tc::kLayoutSW128), idesc, kk > 0);
-          }
+          issue_product<D>(tmem + (2 * t + ab) * kChunk, k_base + t * C::kTileBytes,
+                           q_base + st * C::kTileBytes, kChunk, smem_u32(smem + C::kOnesOff),
+                           smem_u32(smem + C::kPartsOff + st * C::kPartsBytes), kChunk);
           tc::mma_commit_warp(&bars.acc_full[t][ab]);
           ++used[t];
         }
         if (!ok) break;
         tc::mma_commit_warp(&bars.q_empty[st]);
+        tc::mma_commit_warp(&bars.row_empty[st]);
       }
       if (ok) tc::mma_commit_warp(&bars.k_empty);
     }
@@ -810,6 +894,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_wait_warp(&bars.mma_drain, 0, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------------ row data, chunks ahead
+    regs_dec<80>();
     bool ok = true;
     int i = 0;
     for (; w.left > 0 && ok; w.next(a, rs))
@@ -822,36 +907,35 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int u = 0; u < kChunk / 32; ++u) {
           const int r = x.chunk * kChunk + u * 32 + lane;  // row of the strip
-          const RowData d = row_data(a, w.b * a.Hkv + w.g, x.strip * rs.length + r, r < rs.length);
-          row_lse[st][u * 32 + lane] = d.neg_lse2;
-          row_token[st][u * 32 + lane] = d.token;
+          put_row(a, w.b * a.Hkv + w.g, x.strip * rs.length + r, r < rs.length,
+                  smem + C::kPartsOff + st * C::kPartsBytes, u * 32 + lane, row_token[st]);
         }
+        fence_proxy_async_smem();
         mbar_arrive(&bars.row_full[st]);
       }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    regs_dec<80>();
+  } else {
     // ------------------------------------------------------------ warpgroups of keys
-    // Warpgroup (tile t, turn) sums every other step of its tile; the two of
-    // a tile are added at the end of a piece.
-    const int wg = (warp - 4) / 4, quarter = warp % 4, t = wg >> 1, turn = wg & 1;
+    // 128 x 80 + 256 x 208 registers <= 384 x 168 at launch
+    regs_inc<208>();
+    const int t = (warp - 4) / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
-    const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + (2 * t + turn) * kChunk;
+    const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + 2 * t * kChunk;
     long long at_step = bars.begin;
     bool ok = true;
     int i = 0, used = 0;
-    for (; w.left > 0; w.next(a, rs)) {
+    for (; w.left > 0 && ok; w.next(a, rs)) {
       const int key0 = w.k * kBlock + t * kTileKeys, j = key0 + r;
-      const bool mine = turn == 0 && j < w.n;
-      const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
-      const float prev = mine && a.prev != nullptr ? a.prev[at] : 0.f;
-      const bool good = mine && page_good(a, w.b, j);
+      const KeyOut out = find_key_out(a, w.b, w.g, j, w.n);
       const int first = first_token(a, w.n, j);
       const int all_from = first_token(a, w.n, key0 + kTileKeys - 1);
       float sum = 0.f;
-      for (int s = w.step0; s < w.step0 + w.steps && ok; ++s, ++i) {
+      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
         const int st = i % C::kStages;
         const Step x = step_at(s);
         // (waited for by a warpgroup that skips the chunk too: its arrival
@@ -859,38 +943,26 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
         if (!ok) break;
         if (sees(x, t)) {
-          if ((used & 1) == turn) {
-            ok = mbar_wait_warp(&bars.acc_full[t][turn], (used >> 1) & 1, abort_flag);
-            if (!ok) break;
-            tc::fence_after_sync();
-            // tested column by column if the chunk's first token misses a key
-            const bool masked = (rs.skip ? x.chunk * kChunk : 0) < all_from;
-            sum += sum_columns(addr, 0, kChunk, rs.length - x.chunk * kChunk, masked, row_lse[st],
-                               row_token[st], a.c, first);
-            tc::fence_before_sync();
-            mbar_arrive(&bars.acc_empty[t][turn]);
-          }
+          const int turn = used & 1;
+          ok = mbar_wait_warp(&bars.acc_full[t][turn], (used >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc::fence_after_sync();
+          // tested column by column if the chunk's first token misses a key
+          const bool masked = (rs.skip ? x.chunk * kChunk : 0) < all_from;
+          sum += sum_columns(addr + turn * kChunk, kChunk, rs.length - x.chunk * kChunk, masked,
+                             row_token[st], a.c, first, &bars.acc_empty[t][turn]);
           ++used;
         }
         mbar_arrive(&bars.row_empty[st]);
       }
-      // (after a failed wait both warpgroups of the tile still walk all pieces,
-      // so that they meet here equally often)
-      if (turn == 1) other_sum[t][r] = sum;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + t), "r"(2 * kTileKeys) : "memory");
-      if (mine && ok) {
-        sum += other_sum[t][r];
-        if (w.steps == w.all) {                          // the whole block is this CTA's
-          const float kept = a.prev != nullptr ? a.decay * prev : 0.f;
-          a.out[at] = good ? kept + sum : kept;
-        } else {
-          // the CTA's place among those of the block
-          const long long block0 = at_step - w.step0;
-          const int slot = int(blockIdx.x - block0 / bars.each);
-          a.part[size_t(slot) * a.B * a.Hkv * a.out_len + at] = good ? sum : 0.f;
-        }
+      if (!ok) break;
+      if (w.steps == w.all) {                            // the whole block is this CTA's
+        write_key(a, out, sum);
+      } else if (out.live) {
+        // the CTA's place among those of the block
+        const int slot = int(blockIdx.x - (at_step - w.step0) / bars.each);
+        a.part[size_t(slot) * a.B * a.Hkv * a.out_len + out.at] = page_good(a, out) ? sum : 0.f;
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + t), "r"(2 * kTileKeys) : "memory");
       at_step += w.steps;
     }
     if (!ok) {
@@ -990,7 +1062,7 @@ cudaError_t launch_d(const KeyWeightsArgs& w, KwArgs a) {
   if (!make_map_bf16_3d(&mk, w.k, D, paged ? w.page_size : w.L,
                         uint64_t(paged ? w.num_pages : w.B) * w.Hkv, a.box_rows))
     return cudaErrorInvalidValue;
-  if (a.R <= 64) return launch_keys<D, 64>(mk, w, a);
+  if (a.R <= 128) return launch_keys<D, 128>(mk, w, a);
   if (a.R <= 256) return launch_keys<D, 256>(mk, w, a);
   const RowSteps rs = row_steps(a.R, a.T, a.causal);
   if (!make_map_bf16_3d(&mq, w.q, D, rs.length, uint64_t(a.B) * a.Hkv * rs.strips, kChunk))
@@ -1016,7 +1088,7 @@ int key_weights_slots(int R, int T) {
 cudaError_t launch_key_weights(const KeyWeightsArgs& w) {
   KwArgs a{w.lse, w.prev, w.out, w.part, w.seq_lens, w.block_table, w.B, w.Hkv, w.Hq / w.Hkv * w.T, w.T,
            w.len_cap, w.out_len, w.num_pages, w.page_size, w.max_pages, kTileKeys, w.causal,
-           w.scale * kLog2e, w.decay};
+           w.scale * kLog2e, 1.f / w.scale, w.decay};
   // copies of a key tile: whole tiles of a contiguous cache or a single
   // page, else the largest power of two that divides the page size
   if (w.block_table != nullptr && w.max_pages > 1)
