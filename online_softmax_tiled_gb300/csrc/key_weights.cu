@@ -20,9 +20,8 @@
 //
 //  * At most 256 rows (decode steps, observation windows): the rows of a
 //    (request, KV head) stay in shared memory and the keys stream past them
-//    in tiles of 128. One persistent CTA per SM takes an equal share of all
-//    key tiles of the batch. Up to 128 rows the two warpgroups take
-//    alternate tiles; with more, half of the columns of every tile.
+//    in tiles of 128, which the two warpgroups take in turn. One persistent
+//    CTA per SM takes an equal share of all key tiles of the batch.
 //  * More rows (every token of a prompt as an observer): 256 keys of a
 //    (request, KV head) stay in shared memory, 128 per warpgroup, and the
 //    rows stream past them in chunks of 128, chunks that see none of the
@@ -71,15 +70,15 @@ ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
 }
 
 // Where the copies of a key tile come from: lane i < boxes has the tile's i-th
-// box; boxes past the request's keys or behind a bad page index are left out
-// (their lanes' sums are not used).
+// box. The page index is only looked at when the copies are issued, one tile
+// later, so that reading it holds nothing up.
 struct KeyBox {
-  int row, outer;
-  bool good;
+  int row, outer, page;        // page: of a paged cache, outer then the KV head
+  bool in;
 };
 ATTN_DEVINL KeyBox find_key_box(const KwArgs& a, int b, int g, int key0, int n, int lane) {
-  KeyBox x{0, 0, lane < min(kTileKeys / a.box_rows, (n - key0 + a.box_rows - 1) / a.box_rows)};
-  if (x.good) {
+  KeyBox x{0, 0, 0, lane < min(kTileKeys / a.box_rows, (n - key0 + a.box_rows - 1) / a.box_rows)};
+  if (x.in) {
     const int key = key0 + lane * a.box_rows;
     if (a.block_table == nullptr) {
       x.row = key;
@@ -87,27 +86,29 @@ ATTN_DEVINL KeyBox find_key_box(const KwArgs& a, int b, int g, int key0, int n, 
     } else {
       const int pi = key / a.page_size;
       x.row = key - pi * a.page_size;
-      const int page = a.block_table[size_t(b) * a.max_pages + pi];
-      x.good = page >= 0 && page < a.num_pages;
-      x.outer = page * a.Hkv + g;
+      x.outer = g;
+      x.page = a.block_table[size_t(b) * a.max_pages + pi];
     }
   }
   return x;
 }
-// The copies (all lanes of a converged warp): one per (box, atom).
+// The copies (all lanes of a converged warp): one per (box, atom); boxes past
+// the request's keys or behind a bad page index are left out (their lanes'
+// sums are not used).
 template <int D>
 ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
                                const CUtensorMap* map, uint64_t* bar, int lane) {
   constexpr int kAtoms = D / 64;
-  const uint32_t live = __ballot_sync(0xffffffffu, x.good);
+  const bool good = x.in && x.page >= 0 && (a.block_table == nullptr || x.page < a.num_pages);
+  const uint32_t live = __ballot_sync(0xffffffffu, good);
   if (lane == 0)
     mbar_arrive_expect_tx(bar, uint32_t(__popc(live)) * a.box_rows * 128 * kAtoms);
   __syncwarp();
-  if (x.good)
+  if (good)
 #pragma unroll
     for (int at = 0; at < kAtoms; ++at)
       tc::tma_load_3d(dst + at * (kTileKeys * 128) + lane * a.box_rows * 128, map, 64 * at, x.row,
-                      x.outer, bar);
+                      x.page * a.Hkv + x.outer, bar);
 }
 
 // What a row needs besides Q: -lse/scale as three bf16 parts whose sum is the
@@ -120,21 +121,31 @@ ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
 // bytes; the other columns stay zero.
 constexpr int kPartsRow = 32;                 // bytes of a row in the operand tile
 constexpr float kFarBelow = -3.0e38f;
-ATTN_DEVINL void put_row(const KwArgs& a, int head, int r, bool in, uint8_t* parts, int n,
-                         int* token) {
-  float v = kFarBelow;
-  if (in) {
-    const float l = a.lse[size_t(head) * a.R + r];
-    v = -l * a.inv_scale;
-    if (fabsf(l) == INFINITY) v = kFarBelow;
+// Rows n = lane, lane + 32, ... < 32·kRows of the tile are rows first + n of a
+// strip of `length` that begins at row `base` of the head (the reads of all
+// rows in flight together).
+template <int kRows>
+ATTN_DEVINL void put_rows(const KwArgs& a, int head, int base, int first, int length, int count,
+                          uint8_t* parts, int* token, int lane) {
+  float l[kRows];
+  const float* lse = a.lse + size_t(head) * a.R + base;
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) l[u] = lse[min(first + u * 32 + lane, length - 1)];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int n = u * 32 + lane;
+    if (n >= count) break;
+    const bool in = first + n < length;
+    float v = -l[u] * a.inv_scale;
+    if (!in || fabsf(l[u]) == INFINITY || v < kFarBelow) v = kFarBelow;
     if (v > -kFarBelow) v = -kFarBelow;
-    if (v < kFarBelow) v = kFarBelow;
+    token[n] = in ? (base + first + n) % a.T : INT_MIN;
+    const float p0 = __bfloat162float(__float2bfloat16_rn(v));
+    const float p1 = __bfloat162float(__float2bfloat16_rn(v - p0));
+    *reinterpret_cast<uint4*>(parts + (n >> 3) * 256 + (n & 7) * 16) =
+        make_uint4(pack_bf16x2(p0, p1), pack_bf16x2(v - p0 - p1, 0.f), 0u, 0u);
   }
-  token[n] = in ? r % a.T : INT_MIN;
-  const float p0 = __bfloat162float(__float2bfloat16_rn(v));
-  const float p1 = __bfloat162float(__float2bfloat16_rn(v - p0));
-  *reinterpret_cast<uint4*>(parts + (n >> 3) * 256 + (n & 7) * 16) =
-      make_uint4(pack_bf16x2(p0, p1), pack_bf16x2(v - p0 - p1, 0.f), 0u, 0u);
+  fence_proxy_async_smem();
 }
 // Ones for the other operand (128 rows x 16), zeros for `bytes` of parts.
 ATTN_DEVINL void fill_parts(uint8_t* ones, uint8_t* parts, int bytes, int tid) {
@@ -196,7 +207,8 @@ ATTN_DEVINL void add_columns(const uint32_t* s, const int* token, float c, int f
 }
 
 // The sum over n columns (a multiple of 16, at most 128) of an accumulator,
-// which is given back (an arrival on `empty`) as soon as it is in registers.
+// which is given back (an arrival on `empty`, if any) as soon as it is in
+// registers.
 // masked: every column is tested; otherwise only those past `full`.
 ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const int* token,
                               float c, int first, uint64_t* empty) {
@@ -211,8 +223,10 @@ ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const
       if (i < n) tc::tmem_ld16(addr + i, *reinterpret_cast<uint32_t(*)[16]>(&s[i]));
   }
   tc::tmem_ld_wait();
-  tc::fence_before_sync();
-  mbar_arrive(empty);
+  if (empty != nullptr) {
+    tc::fence_before_sync();
+    mbar_arrive(empty);
+  }
   f2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
   if (!masked && n == 128 && full >= 128) {
 #pragma unroll
@@ -233,15 +247,13 @@ ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const
 
 // What the thread of a key reads for its output, on its way before the sum.
 struct KeyOut {
-  size_t at;
   float prev;
   int page;                    // of a paged cache; checked when the sum is written
-  bool live;
 };
 ATTN_DEVINL KeyOut find_key_out(const KwArgs& a, int b, int g, int j, int n) {
-  KeyOut o{(size_t(b) * a.Hkv + g) * a.out_len + j, 0.f, 0, j < n};
-  if (o.live) {
-    if (a.prev != nullptr) o.prev = a.prev[o.at];
+  KeyOut o{0.f, 0};
+  if (j < n) {
+    if (a.prev != nullptr) o.prev = a.prev[(size_t(b) * a.Hkv + g) * a.out_len + j];
     if (a.block_table != nullptr)
       o.page = a.block_table[size_t(b) * a.max_pages + j / a.page_size];
   }
@@ -252,10 +264,9 @@ ATTN_DEVINL bool page_good(const KwArgs& a, const KeyOut& o) {
   if (!good) attn_flag_error(kErrBadIndex);
   return good;
 }
-ATTN_DEVINL void write_key(const KwArgs& a, const KeyOut& o, float sum) {
-  if (!o.live) return;
+ATTN_DEVINL void write_key(const KwArgs& a, size_t at, const KeyOut& o, float sum) {
   const float kept = a.prev != nullptr ? a.decay * o.prev : 0.f;
-  a.out[o.at] = page_good(a, o) ? kept + sum : kept;
+  a.out[at] = page_good(a, o) ? kept + sum : kept;
 }
 
 // The first token that sees key j (any token without a causal mask, but
@@ -270,9 +281,9 @@ template <int D, int NMAX>
 struct KeysCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTileKeys * D * 2;
-  // warpgroups that share a tile (128 columns each), or else alternate
-  static constexpr int kShare = NMAX / 128;
-  static constexpr int kQBufs = kShare == 1 ? 2 : 1;
+  static constexpr int kQBufs = NMAX <= 128 ? 2 : 1;
+  // accumulators per warpgroup
+  static constexpr int kTurns = 256 / NMAX;
   static constexpr int kQBytes = NMAX * D * 2;
   static constexpr int kStages = 4 * (128 / D);
   static constexpr int kKOff = kQBufs * kQBytes;
@@ -280,13 +291,12 @@ struct KeysCfg {
   static constexpr int kPartsOff = kOnesOff + kTileKeys * kPartsRow;   // of two heads
   static constexpr int kPartsBytes = NMAX * kPartsRow;
   static constexpr int kDynSmem = kPartsOff + 2 * kPartsBytes + 1024;
-  // accumulators: two of 128 columns per warpgroup, or two of 256 for both
-  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kTmemCols = 512;   // [warpgroup][turn] accumulators
 };
 
 struct KeysBars {
   uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[4], acc_empty[4];
-  uint64_t row_full[2], row_empty[2], half_full[3], mma_drain;
+  uint64_t row_full[2], row_empty[2], mma_drain;
   uint32_t tmem_base;
   int abort;
   int warp_sum[kThreads / 32 + 1];
@@ -327,7 +337,6 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
                                              ~uintptr_t(1023));
   __shared__ KeysBars bars;
   __shared__ __align__(16) int row_token[2][NMAX];
-  __shared__ float half_sum[3][C::kShare == 2 ? kTileKeys : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -340,9 +349,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], C::kShare * kTileKeys);
+      mbar_init(&bars.acc_empty[i], kTileKeys);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(&bars.half_full[i], kTileKeys);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
       mbar_init(&bars.k_empty[i], 1);
@@ -413,12 +421,12 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     regs_dec<80>();
     bool ok = true, fresh = true;
     int heads = 0, i = 0;
-    KeyBox box{0, 0, false};
+    KeyBox box{0, 0, 0, false};
     if (count > 0) box = find_key_box(a, w.b, w.g, w.tile * kTileKeys, w.n, lane);
     for (; i < count && ok; ++i) {
       const int head = w.b * a.Hkv + w.g;
       const bool turn = w.next(a);
-      KeyBox next{0, 0, false};
+      KeyBox next{0, 0, 0, false};
       if (i + 1 < count) next = find_key_box(a, w.b, w.g, w.tile * kTileKeys, w.n, lane);
       if (fresh) {
         const int qb = heads % C::kQBufs;
@@ -466,10 +474,9 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       const int st = i % C::kStages;
       if (ok) ok = mbar_wait_warp(&bars.k_full[st], (i / C::kStages) & 1, abort_flag);
-      const int use = C::kShare == 1 ? i >> 1 : i;
-      const int acc = C::kShare == 1 ? 2 * (i & 1) + (use & 1) : use & 1;
-      if (ok && use >= 2)
-        ok = mbar_wait_warp(&bars.acc_empty[acc], ((use >> 1) - 1) & 1, abort_flag);
+      const int use = i >> 1, acc = C::kTurns * (i & 1) + use % C::kTurns;
+      if (ok && use >= C::kTurns)
+        ok = mbar_wait_warp(&bars.acc_empty[acc], (use / C::kTurns - 1) & 1, abort_flag);
       if (!ok) break;
       tc::fence_after_sync();
       issue_product<D>(tmem + acc * NMAX, k_base + st * C::kTileBytes,
@@ -501,10 +508,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         const int rb = heads & 1;
         if (heads >= 2) ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
-        for (int r = lane; r < N; r += 32)
-          put_row(a, w.b * a.Hkv + w.g, r, r < a.R, smem + C::kPartsOff + rb * C::kPartsBytes, r,
-                  row_token[rb]);
-        fence_proxy_async_smem();
+        put_rows<NMAX / 32>(a, w.b * a.Hkv + w.g, 0, 0, a.R, N,
+                            smem + C::kPartsOff + rb * C::kPartsBytes, row_token[rb], lane);
         mbar_arrive(&bars.row_full[rb]);
         ++heads;
       }
@@ -520,26 +525,22 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     // ------------------------------------------------------------ warpgroups of keys
     // 128 x 80 + 256 x 208 registers <= 384 x 168 at launch
     regs_inc<208>();
-    // Alternate tiles, or half of the columns of each: then the second
-    // warpgroup hands its sum to the first.
-    const int t = (warp - 4) / 4, quarter = warp % 4;
+    const int t = (warp - 4) / 4, quarter = warp % 4;    // takes tiles t, t + 2, ...
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    const int col0 = C::kShare == 1 ? 0 : 128 * t, cols = min(N - col0, 128);
-    const bool writes = C::kShare == 1 || t == 0;
-    constexpr int kEvery = C::kShare == 1 ? 2 : 1;       // this warpgroup's tiles
-    // what the next of its tiles needs for its output, fetched a tile early
+    // what its next tile needs for the output, fetched a tile early
     TileWalk ahead = w;
     int ahead_at = 0;
+    const bool fetches = a.prev != nullptr || a.block_table != nullptr;
     auto fetch = [&](int i) {
-      KeyOut o{0, 0.f, 0, false};
-      if (writes && i < count) {
+      KeyOut o{0.f, 0};
+      if (fetches && i < count) {
         for (; ahead_at < i; ++ahead_at) ahead.next(a);
         o = find_key_out(a, ahead.b, ahead.g, ahead.tile * kTileKeys + r, ahead.n);
       }
       return o;
     };
-    KeyOut out = fetch(C::kShare == 1 ? t : 0);
+    KeyOut out = fetch(t);
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -549,31 +550,23 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         if (!ok) break;
         ++heads;
       }
-      if (C::kShare == 2 || (i & 1) == t) {
-        const int use = C::kShare == 1 ? i >> 1 : i;
-        const int acc = C::kShare == 1 ? 2 * t + (use & 1) : use & 1;
-        const KeyOut next = fetch(i + kEvery);
-        ok = mbar_wait_warp(&bars.acc_full[acc], (use >> 1) & 1, abort_flag);
+      if ((i & 1) == t) {
+        const int use = i >> 1, acc = C::kTurns * t + use % C::kTurns;
+        const KeyOut next = fetch(i + 2);
+        ok = mbar_wait_warp(&bars.acc_full[acc], (use / C::kTurns) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
+        const int j = w.tile * kTileKeys + r, first = first_token(a, w.n, j);
         // the tile needs its columns tested if the first token misses its last key
         const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0;
-        float sum = sum_columns(lanes + acc * NMAX + col0, cols, a.R - col0, masked,
-                                row_token[(heads - 1) & 1] + col0, a.c,
-                                first_token(a, w.n, w.tile * kTileKeys + r), &bars.acc_empty[acc]);
-        if (C::kShare == 2) {
-          // Three slots: the second warpgroup is at most two tiles ahead (an
-          // accumulator is filled again once both have read it).
-          if (t == 1) {
-            half_sum[i % 3][r] = sum;
-            mbar_arrive(&bars.half_full[i % 3]);
-          } else {
-            ok = mbar_wait_warp(&bars.half_full[i % 3], (i / 3) & 1, abort_flag);
-            if (!ok) break;
-            sum += half_sum[i % 3][r];
-          }
-        }
-        if (writes) write_key(a, out, sum);
+        const int* token = row_token[(heads - 1) & 1];
+        float sum = 0.f;
+#pragma unroll 1
+        for (int col = 0; col < N; col += 128)
+          sum += sum_columns(lanes + acc * NMAX + col, min(N - col, 128), a.R - col, masked,
+                             token + col, a.c, first,
+                             col + 128 < N ? nullptr : &bars.acc_empty[acc]);
+        if (j < w.n) write_key(a, (size_t(w.b) * a.Hkv + w.g) * a.out_len + j, out, sum);
         out = next;
       }
       fresh = w.next(a);
@@ -904,13 +897,9 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         if (i >= C::kStages)
           ok = mbar_wait_warp(&bars.row_empty[st], (i / C::kStages - 1) & 1, abort_flag);
         if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < kChunk / 32; ++u) {
-          const int r = x.chunk * kChunk + u * 32 + lane;  // row of the strip
-          put_row(a, w.b * a.Hkv + w.g, x.strip * rs.length + r, r < rs.length,
-                  smem + C::kPartsOff + st * C::kPartsBytes, u * 32 + lane, row_token[st]);
-        }
-        fence_proxy_async_smem();
+        put_rows<kChunk / 32>(a, w.b * a.Hkv + w.g, x.strip * rs.length, x.chunk * kChunk,
+                              rs.length, kChunk, smem + C::kPartsOff + st * C::kPartsBytes,
+                              row_token[st], lane);
         mbar_arrive(&bars.row_full[st]);
       }
     if (!ok) {
@@ -956,12 +945,14 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         mbar_arrive(&bars.row_empty[st]);
       }
       if (!ok) break;
-      if (w.steps == w.all) {                            // the whole block is this CTA's
-        write_key(a, out, sum);
-      } else if (out.live) {
+      const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
+      if (j >= w.n) {
+      } else if (w.steps == w.all) {                     // the whole block is this CTA's
+        write_key(a, at, out, sum);
+      } else {
         // the CTA's place among those of the block
         const int slot = int(blockIdx.x - (at_step - w.step0) / bars.each);
-        a.part[size_t(slot) * a.B * a.Hkv * a.out_len + out.at] = page_good(a, out) ? sum : 0.f;
+        a.part[size_t(slot) * a.B * a.Hkv * a.out_len + at] = page_good(a, out) ? sum : 0.f;
       }
       at_step += w.steps;
     }
