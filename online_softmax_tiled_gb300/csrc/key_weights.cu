@@ -57,7 +57,7 @@ struct KwArgs {
   const int* seq_lens;
   const int* block_table;
   int B, Hkv, R, T, cap, out_len, num_pages, page_size, max_pages, box_rows;
-  int causal;
+  int causal, joined;      // joined: key tiles by make_map_joined's copies
   float c, inv_scale, decay;   // scale · log2 e, 1 / scale
 };
 
@@ -92,9 +92,32 @@ ATTN_DEVINL KeyBox find_key_box(const KwArgs& a, int b, int g, int key0, int n, 
   }
   return x;
 }
-// The copies (all lanes of a converged warp): one per (box, atom); boxes past
-// the request's keys or behind a bad page index are left out (their lanes'
-// sums are not used).
+// A key tile in shared memory is made of 1024-byte pieces, 8 keys x 64
+// elements (128-byte swizzle). Contiguous caches and single pages: one copy of
+// 128 keys per 64-column half, the halves one after the other. Pages: one
+// copy per page piece that takes both halves (a copy costs its issue, and
+// 16-key pages need eight a tile either way), the halves of 8 keys next to
+// each other.
+struct KeySteps {
+  uint32_t group, half;        // bytes from 8 keys to the next, from half to half
+};
+template <int D> ATTN_DEVINL KeySteps key_steps(const KwArgs& a) {
+  return a.joined ? KeySteps{1024 * (D / 64), 1024} : KeySteps{1024, kTileKeys * 128};
+}
+
+ATTN_DEVINL void tma_load_5d(void* smem_dst, const CUtensorMap* map, int c3, int c4,
+                             uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4),
+        "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The copies of a tile (all lanes of a converged warp); boxes past the
+// request's keys or behind a bad page index are left out (their lanes' sums
+// are not used).
 template <int D>
 ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
                                const CUtensorMap* map, uint64_t* bar, int lane) {
@@ -104,11 +127,33 @@ ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
   if (lane == 0)
     mbar_arrive_expect_tx(bar, uint32_t(__popc(live)) * a.box_rows * 128 * kAtoms);
   __syncwarp();
-  if (good)
+  const int outer = x.page * a.Hkv + x.outer;
+  if (good) {
+    if (a.joined) {
+      tma_load_5d(dst + lane * a.box_rows * 128 * kAtoms, map, x.row / 8, outer, bar);
+    } else {
 #pragma unroll
-    for (int at = 0; at < kAtoms; ++at)
-      tc::tma_load_3d(dst + at * (kTileKeys * 128) + lane * a.box_rows * 128, map, 64 * at, x.row,
-                      x.page * a.Hkv + x.outer, bar);
+      for (int at = 0; at < kAtoms; ++at)
+        tc::tma_load_3d(dst + at * (kTileKeys * 128) + lane * a.box_rows * 128, map, 64 * at,
+                        x.row, outer, bar);
+    }
+  }
+}
+
+// The map of joined copies: K as [outer][row / 8][half][row % 8][64], boxes of
+// box_rows rows.
+bool make_map_joined(CUtensorMap* m, const void* base, int d, int rows, uint64_t outer,
+                     int box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t row = cuuint64_t(d) * 2;
+  const cuuint64_t dims[5] = {64, 8, cuuint64_t(d / 64), cuuint64_t(rows / 8), outer};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, rows * row};
+  const cuuint32_t box[5] = {64, 8, cuuint32_t(d / 64), cuuint32_t(box_rows / 8), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What a row needs besides Q: -lse/scale as three bf16 parts whose sum is the
@@ -157,23 +202,22 @@ ATTN_DEVINL void fill_parts(uint8_t* ones, uint8_t* parts, int bytes, int tid) {
   fence_proxy_async_smem();
 }
 
-// Sᵀ - lse/scale for one key tile against n query rows, all lanes of the
-// issuing warp: D/16 steps over K and Q (128-byte swizzle, `pitch` rows per
-// 64-column atom of Q), then the parts.
+// Sᵀ - lse/scale for one key tile against query rows, all lanes of the
+// issuing warp: D/16 steps over K and Q (128-byte swizzle; the second half of
+// K lies k_half, that of Q q_half descriptor units of 16 bytes on), then the
+// parts. The descriptors are the caller's, so that a step costs two additions.
 template <int D>
-ATTN_DEVINL void issue_product(uint32_t acc, uint32_t ka, uint32_t qa, int pitch, uint32_t ones,
-                               uint32_t parts, int n) {
-  const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, n, false, false);
+ATTN_DEVINL void issue_product(uint32_t acc, uint64_t k_desc, uint32_t k_half, uint64_t q_desc,
+                               uint32_t q_half, uint64_t ones_desc, uint64_t parts_desc,
+                               uint32_t idesc) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    tc::mma_ss_warp(acc,
-                    tc::smem_desc(ka + (kk / 4) * (kTileKeys * 128) + (kk % 4) * 32, 16, 1024,
-                                  tc::kLayoutSW128),
-                    tc::smem_desc(qa + (kk / 4) * (pitch * 128) + (kk % 4) * 32, 16, 1024,
-                                  tc::kLayoutSW128),
-                    idesc, kk > 0);
-  tc::mma_ss_warp(acc, tc::smem_desc(ones, 128, 256, tc::kLayoutNone),
-                  tc::smem_desc(parts, 128, 256, tc::kLayoutNone), idesc, 1u);
+    tc::mma_ss_warp(acc, k_desc + (kk / 4) * k_half + (kk % 4) * 2,
+                    q_desc + (kk / 4) * q_half + (kk % 4) * 2, idesc, kk > 0);
+  tc::mma_ss_warp(acc, ones_desc, parts_desc, idesc, 1u);
+}
+ATTN_DEVINL uint64_t parts_desc_of(uint32_t addr) {
+  return tc::smem_desc(addr, 128, 256, tc::kLayoutNone);
 }
 
 ATTN_DEVINL float exp2_unit(float x) {
@@ -245,7 +289,7 @@ ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const
   return t.x + t.y;
 }
 
-// What the thread of a key reads for its output, on its way before the sum.
+// What the thread of a key reads for its output, on its way during the sum.
 struct KeyOut {
   float prev;
   int page;                    // of a paged cache; checked when the sum is written
@@ -282,8 +326,6 @@ struct KeysCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTileKeys * D * 2;
   static constexpr int kQBufs = NMAX <= 128 ? 2 : 1;
-  // accumulators per warpgroup
-  static constexpr int kTurns = 256 / NMAX;
   static constexpr int kQBytes = NMAX * D * 2;
   static constexpr int kStages = 4 * (128 / D);
   static constexpr int kKOff = kQBufs * kQBytes;
@@ -291,11 +333,14 @@ struct KeysCfg {
   static constexpr int kPartsOff = kOnesOff + kTileKeys * kPartsRow;   // of two heads
   static constexpr int kPartsBytes = NMAX * kPartsRow;
   static constexpr int kDynSmem = kPartsOff + 2 * kPartsBytes + 1024;
-  static constexpr uint32_t kTmemCols = 512;   // [warpgroup][turn] accumulators
+  // accumulators per warpgroup, of NMAX columns (a product of 256 columns
+  // reads 96 bytes of shared memory a cycle, one of 128 columns 128: the limit)
+  static constexpr int kTurns = 256 / NMAX;
+  static constexpr uint32_t kTmemCols = 512;
 };
 
 struct KeysBars {
-  uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[4], acc_empty[4];
+  uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], acc_full[2][2], acc_empty[2][2];
   uint64_t row_full[2], row_empty[2], mma_drain;
   uint32_t tmem_base;
   int abort;
@@ -348,8 +393,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&bars.row_empty[i], 2 * kTileKeys + 1);   // the warpgroups and the products
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], kTileKeys);
+      mbar_init(&bars.acc_full[i >> 1][i & 1], 1);
+      mbar_init(&bars.acc_empty[i >> 1][i & 1], kTileKeys);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
@@ -463,27 +508,39 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
     regs_dec<80>();
-    const uint32_t q_base = smem_u32(smem), k_base = smem_u32(smem + C::kKOff);
+    const KeySteps step = key_steps<D>(a);
+    const uint64_t q0 = tc::smem_desc(smem_u32(smem), 16, 1024, tc::kLayoutSW128);
+    const uint64_t k0 = tc::smem_desc(smem_u32(smem + C::kKOff), 16, step.group, tc::kLayoutSW128);
+    const uint64_t ones = parts_desc_of(smem_u32(smem + C::kOnesOff));
+    const uint64_t parts0 = parts_desc_of(smem_u32(smem + C::kPartsOff));
+    const uint32_t k_half = step.half / 16, q_half = NMAX * 128 / 16;
+    const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, N, false, false);
     bool ok = true, fresh = true;
     int heads = 0;
+    uint64_t q_desc = q0, parts = parts0;
     for (int i = 0; i < count && ok; ++i) {
       if (fresh) {
         ok = mbar_wait_warp(&bars.q_full[heads % C::kQBufs], (heads / C::kQBufs) & 1, abort_flag);
         if (ok) ok = mbar_wait_warp(&bars.row_full[heads & 1], (heads >> 1) & 1, abort_flag);
+        q_desc = q0 + (heads % C::kQBufs) * (C::kQBytes / 16);
+        parts = parts0 + (heads & 1) * (C::kPartsBytes / 16);
         ++heads;
       }
       const int st = i % C::kStages;
-      if (ok) ok = mbar_wait_warp(&bars.k_full[st], (i / C::kStages) & 1, abort_flag);
-      const int use = i >> 1, acc = C::kTurns * (i & 1) + use % C::kTurns;
-      if (ok && use >= C::kTurns)
-        ok = mbar_wait_warp(&bars.acc_empty[acc], (use / C::kTurns - 1) & 1, abort_flag);
+      const int t = i & 1, use = i >> 1, turn = use % C::kTurns;
+      if (ok) {
+        uint64_t* full = &bars.k_full[st];
+        const uint32_t k_phase = (i / C::kStages) & 1;
+        ok = use >= C::kTurns
+                 ? mbar_wait2_warp(full, k_phase, &bars.acc_empty[t][turn],
+                                   (use / C::kTurns - 1) & 1, abort_flag)
+                 : mbar_wait_warp(full, k_phase, abort_flag);
+      }
       if (!ok) break;
       tc::fence_after_sync();
-      issue_product<D>(tmem + acc * NMAX, k_base + st * C::kTileBytes,
-                       q_base + ((heads - 1) % C::kQBufs) * C::kQBytes, NMAX,
-                       smem_u32(smem + C::kOnesOff),
-                       smem_u32(smem + C::kPartsOff + ((heads - 1) & 1) * C::kPartsBytes), N);
-      tc::mma_commit_warp(&bars.acc_full[acc]);
+      issue_product<D>(tmem + (C::kTurns * t + turn) * NMAX, k0 + st * (C::kTileBytes / 16), k_half,
+                       q_desc, q_half, ones, parts, idesc);
+      tc::mma_commit_warp(&bars.acc_full[t][turn]);
       tc::mma_commit_warp(&bars.k_empty[st]);
       fresh = w.next(a);
       if (fresh) {
@@ -528,19 +585,6 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     const int t = (warp - 4) / 4, quarter = warp % 4;    // takes tiles t, t + 2, ...
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    // what its next tile needs for the output, fetched a tile early
-    TileWalk ahead = w;
-    int ahead_at = 0;
-    const bool fetches = a.prev != nullptr || a.block_table != nullptr;
-    auto fetch = [&](int i) {
-      KeyOut o{0.f, 0};
-      if (fetches && i < count) {
-        for (; ahead_at < i; ++ahead_at) ahead.next(a);
-        o = find_key_out(a, ahead.b, ahead.g, ahead.tile * kTileKeys + r, ahead.n);
-      }
-      return o;
-    };
-    KeyOut out = fetch(t);
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -551,23 +595,22 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         ++heads;
       }
       if ((i & 1) == t) {
-        const int use = i >> 1, acc = C::kTurns * t + use % C::kTurns;
-        const KeyOut next = fetch(i + 2);
-        ok = mbar_wait_warp(&bars.acc_full[acc], (use / C::kTurns) & 1, abort_flag);
+        const int use = i >> 1, turn = use % C::kTurns;
+        const int j = w.tile * kTileKeys + r, first = first_token(a, w.n, j);
+        const KeyOut out = find_key_out(a, w.b, w.g, j, w.n);
+        ok = mbar_wait_warp(&bars.acc_full[t][turn], (use / C::kTurns) & 1, abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
-        const int j = w.tile * kTileKeys + r, first = first_token(a, w.n, j);
         // the tile needs its columns tested if the first token misses its last key
         const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0;
         const int* token = row_token[(heads - 1) & 1];
         float sum = 0.f;
 #pragma unroll 1
         for (int col = 0; col < N; col += 128)
-          sum += sum_columns(lanes + acc * NMAX + col, min(N - col, 128), a.R - col, masked,
-                             token + col, a.c, first,
-                             col + 128 < N ? nullptr : &bars.acc_empty[acc]);
+          sum += sum_columns(lanes + (C::kTurns * t + turn) * NMAX + col, min(N - col, 128),
+                             a.R - col, masked, token + col, a.c, first,
+                             col + 128 < N ? nullptr : &bars.acc_empty[t][turn]);
         if (j < w.n) write_key(a, (size_t(w.b) * a.Hkv + w.g) * a.out_len + j, out, sum);
-        out = next;
       }
       fresh = w.next(a);
     }
@@ -848,7 +891,12 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
     regs_dec<80>();
-    const uint32_t k_base = smem_u32(smem), q_base = smem_u32(smem + C::kQOff);
+    const KeySteps step = key_steps<D>(a);
+    const uint64_t k0 = tc::smem_desc(smem_u32(smem), 16, step.group, tc::kLayoutSW128);
+    const uint64_t q0 = tc::smem_desc(smem_u32(smem + C::kQOff), 16, 1024, tc::kLayoutSW128);
+    const uint64_t ones = parts_desc_of(smem_u32(smem + C::kOnesOff));
+    const uint64_t parts0 = parts_desc_of(smem_u32(smem + C::kPartsOff));
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, kChunk, false, false);
     bool ok = true;
     int i = 0, pieces = 0, used[2] = {0, 0};
     for (; w.left > 0 && ok; w.next(a, rs)) {
@@ -857,8 +905,8 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
       for (int s = w.step0; s < w.step0 + w.steps && ok; ++s, ++i) {
         const int st = i % C::kStages;
         const Step x = step_at(s);
-        ok = mbar_wait_warp(&bars.q_full[st], (i / C::kStages) & 1, abort_flag);
-        if (ok) ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
+        ok = mbar_wait2_warp(&bars.q_full[st], (i / C::kStages) & 1, &bars.row_full[st],
+                             (i / C::kStages) & 1, abort_flag);
         for (int t = 0; t < 2 && ok; ++t) {
           if (!sees(x, t)) continue;
           const int ab = used[t] & 1;
@@ -866,9 +914,9 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
             ok = mbar_wait_warp(&bars.acc_empty[t][ab], ((used[t] >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           tc::fence_after_sync();
-          issue_product<D>(tmem + (2 * t + ab) * kChunk, k_base + t * C::kTileBytes,
-                           q_base + st * C::kTileBytes, kChunk, smem_u32(smem + C::kOnesOff),
-                           smem_u32(smem + C::kPartsOff + st * C::kPartsBytes), kChunk);
+          issue_product<D>(tmem + (2 * t + ab) * kChunk, k0 + t * (C::kTileBytes / 16),
+                           step.half / 16, q0 + st * (C::kTileBytes / 16), kChunk * 128 / 16, ones,
+                           parts0 + st * (C::kPartsBytes / 16), idesc);
           tc::mma_commit_warp(&bars.acc_full[t][ab]);
           ++used[t];
         }
@@ -1050,8 +1098,9 @@ template <int D>
 cudaError_t launch_d(const KeyWeightsArgs& w, KwArgs a) {
   CUtensorMap mk, mq;
   const bool paged = w.block_table != nullptr;
-  if (!make_map_bf16_3d(&mk, w.k, D, paged ? w.page_size : w.L,
-                        uint64_t(paged ? w.num_pages : w.B) * w.Hkv, a.box_rows))
+  const uint64_t outer = uint64_t(paged ? w.num_pages : w.B) * w.Hkv;
+  if (!(a.joined ? make_map_joined(&mk, w.k, D, w.page_size, outer, a.box_rows)
+                 : make_map_bf16_3d(&mk, w.k, D, paged ? w.page_size : w.L, outer, a.box_rows)))
     return cudaErrorInvalidValue;
   if (a.R <= 128) return launch_keys<D, 128>(mk, w, a);
   if (a.R <= 256) return launch_keys<D, 256>(mk, w, a);
@@ -1079,7 +1128,7 @@ int key_weights_slots(int R, int T) {
 cudaError_t launch_key_weights(const KeyWeightsArgs& w) {
   KwArgs a{w.lse, w.prev, w.out, w.part, w.seq_lens, w.block_table, w.B, w.Hkv, w.Hq / w.Hkv * w.T, w.T,
            w.len_cap, w.out_len, w.num_pages, w.page_size, w.max_pages, kTileKeys, w.causal,
-           w.scale * kLog2e, 1.f / w.scale, w.decay};
+           w.block_table != nullptr && w.max_pages > 1, w.scale * kLog2e, 1.f / w.scale, w.decay};
   // copies of a key tile: whole tiles of a contiguous cache or a single
   // page, else the largest power of two that divides the page size
   if (w.block_table != nullptr && w.max_pages > 1)
