@@ -46,7 +46,7 @@ ATTN_DEFINE_ERROR_WORD(take_error_key_weights)
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kThreads = 384;     // TMA, MMA, row data, idle warp; two warpgroups of keys
+constexpr int kThreads = 352;     // TMA, MMA and row-data warps; two groups of four for the keys
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KwArgs {
@@ -463,7 +463,6 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
     // (the boxes of a tile are looked up one tile ahead of its copies)
-    regs_dec<80>();
     bool ok = true, fresh = true;
     int heads = 0, i = 0;
     KeyBox box{0, 0, 0, false};
@@ -507,7 +506,6 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
-    regs_dec<80>();
     const KeySteps step = key_steps<D>(a);
     const uint64_t q0 = tc::smem_desc(smem_u32(smem), 16, 1024, tc::kLayoutSW128);
     const uint64_t k0 = tc::smem_desc(smem_u32(smem + C::kKOff), 16, step.group, tc::kLayoutSW128);
@@ -557,7 +555,6 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_wait_warp(&bars.mma_drain, 0, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------------ row data, one head ahead
-    regs_dec<80>();
     bool ok = true, fresh = true;
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
@@ -576,13 +573,9 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
     }
-  } else if (warp == 3) {
-    regs_dec<80>();
   } else {
     // ------------------------------------------------------------ warpgroups of keys
-    // 128 x 80 + 256 x 208 registers <= 384 x 168 at launch
-    regs_inc<208>();
-    const int t = (warp - 4) / 4, quarter = warp % 4;    // takes tiles t, t + 2, ...
+    const int t = (warp - 3) / 4, quarter = warp % 4;    // takes tiles t, t + 2, ...
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
     bool ok = true, fresh = true;
@@ -848,7 +841,6 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
-    regs_dec<80>();
     bool ok = true;
     int i = 0, pieces = 0;
     for (; w.left > 0 && ok; w.next(a, rs)) {
@@ -890,7 +882,6 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the whole warp)
-    regs_dec<80>();
     const KeySteps step = key_steps<D>(a);
     const uint64_t k0 = tc::smem_desc(smem_u32(smem), 16, step.group, tc::kLayoutSW128);
     const uint64_t q0 = tc::smem_desc(smem_u32(smem + C::kQOff), 16, 1024, tc::kLayoutSW128);
@@ -935,7 +926,6 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_wait_warp(&bars.mma_drain, 0, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------------ row data, chunks ahead
-    regs_dec<80>();
     bool ok = true;
     int i = 0;
     for (; w.left > 0 && ok; w.next(a, rs))
@@ -954,13 +944,9 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
     }
-  } else if (warp == 3) {
-    regs_dec<80>();
   } else {
     // ------------------------------------------------------------ warpgroups of keys
-    // 128 x 80 + 256 x 208 registers <= 384 x 168 at launch
-    regs_inc<208>();
-    const int t = (warp - 4) / 4, quarter = warp % 4;
+    const int t = (warp - 3) / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;                   // key of the tile (TMEM lane)
     const uint32_t addr = tmem + (uint32_t(quarter * 32) << 16) + 2 * t * kChunk;
     long long at_step = bars.begin;
