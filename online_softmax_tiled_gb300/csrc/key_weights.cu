@@ -251,11 +251,11 @@ ATTN_DEVINL void add_columns(const uint32_t* s, const int* token, float c, int f
 }
 
 // The sum over n columns (a multiple of 16, at most 128) of an accumulator,
-// which is given back (an arrival on `empty`, if any) as soon as it is in
-// registers.
+// which is given back (an arrival per warp on `empty`, if any) as soon as it
+// is in registers.
 // masked: every column is tested; otherwise only those past `full`.
 ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const int* token,
-                              float c, int first, uint64_t* empty) {
+                              float c, int first, uint64_t* empty, int lane) {
   uint32_t s[128];
   if (n == 128) {
 #pragma unroll
@@ -269,7 +269,8 @@ ATTN_DEVINL float sum_columns(uint32_t addr, int n, int full, bool masked, const
   tc::tmem_ld_wait();
   if (empty != nullptr) {
     tc::fence_before_sync();
-    mbar_arrive(empty);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty);
   }
   f2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
   if (!masked && n == 128 && full >= 128) {
@@ -390,11 +391,11 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 2 * kTileKeys + 1);   // the warpgroups and the products
+      mbar_init(&bars.row_empty[i], 8 + 1);   // the key warps and the products
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.acc_full[i >> 1][i & 1], 1);
-      mbar_init(&bars.acc_empty[i >> 1][i & 1], kTileKeys);
+      mbar_init(&bars.acc_empty[i >> 1][i & 1], 4);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
@@ -582,7 +583,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     int heads = 0;
     for (int i = 0; i < count && ok; ++i) {
       if (fresh) {
-        if (heads > 0) mbar_arrive(&bars.row_empty[(heads - 1) & 1]);
+        __syncwarp();
+        if (heads > 0 && lane == 0) mbar_arrive(&bars.row_empty[(heads - 1) & 1]);
         ok = mbar_wait_warp(&bars.row_full[heads & 1], (heads >> 1) & 1, abort_flag);
         if (!ok) break;
         ++heads;
@@ -602,7 +604,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         for (int col = 0; col < N; col += 128)
           sum += sum_columns(lanes + (C::kTurns * t + turn) * NMAX + col, min(N - col, 128),
                              a.R - col, masked, token + col, a.c, first,
-                             col + 128 < N ? nullptr : &bars.acc_empty[t][turn]);
+                             col + 128 < N ? nullptr : &bars.acc_empty[t][turn], lane);
         if (j < w.n) write_key(a, (size_t(w.b) * a.Hkv + w.g) * a.out_len + j, out, sum);
       }
       fresh = w.next(a);
@@ -745,12 +747,12 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.row_full[i], 32);
-      mbar_init(&bars.row_empty[i], 2 * kTileKeys + 1);   // the warpgroups and the products
+      mbar_init(&bars.row_empty[i], 8 + 1);   // the key warps and the products
     }
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.acc_full[t][i], 1);
-        mbar_init(&bars.acc_empty[t][i], kTileKeys);
+        mbar_init(&bars.acc_empty[t][i], 4);
       }
     mbar_init(&bars.mma_drain, 1);
     fence_barrier_init();
@@ -822,13 +824,20 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     w.open(a);
     w.cut(a, rs, bars.offset);
   }
-  // step s of a block: chunk (first + s mod per) of strip s / per
+  // Step s of a block is chunk (first + s mod per) of strip s / per; and the
+  // step after one.
   struct Step {
     int strip, chunk;
   };
   auto step_at = [&](int s) {
     const int c0 = first_chunk(a, rs, w.n, w.k), per = rs.chunks - c0;
     return Step{s / per, c0 + s % per};
+  };
+  auto advance = [&](Step& s) {
+    if (++s.chunk == rs.chunks) {
+      s.chunk = first_chunk(a, rs, w.n, w.k);
+      ++s.strip;
+    }
   };
   // whether tile t of the block has keys, and whether a chunk's last token
   // sees its first one
@@ -855,13 +864,13 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
           mbar_arrive(&bars.k_full);
       }
       ++pieces;
-      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
+      Step x = step_at(w.step0);
+      for (int s = 0; s < w.steps; ++s, ++i, advance(x)) {
         const int st = i % C::kStages;
         if (i >= C::kStages)
           ok = mbar_wait_warp(&bars.q_empty[st], (i / C::kStages - 1) & 1, abort_flag);
         if (!ok) break;
         if (lane == 0) {
-          const Step x = step_at(s);
           mbar_arrive_expect_tx(&bars.q_full[st], C::kTileBytes);
           for (int at = 0; at < C::kAtoms; ++at)
             tc::tma_load_3d(smem + C::kQOff + st * C::kTileBytes + at * (kChunk * 128), &map_q,
@@ -893,9 +902,9 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     for (; w.left > 0 && ok; w.next(a, rs)) {
       ok = mbar_wait_warp(&bars.k_full, pieces & 1, abort_flag);
       ++pieces;
-      for (int s = w.step0; s < w.step0 + w.steps && ok; ++s, ++i) {
+      Step x = step_at(w.step0);
+      for (int s = 0; s < w.steps && ok; ++s, ++i, advance(x)) {
         const int st = i % C::kStages;
-        const Step x = step_at(s);
         ok = mbar_wait2_warp(&bars.q_full[st], (i / C::kStages) & 1, &bars.row_full[st],
                              (i / C::kStages) & 1, abort_flag);
         for (int t = 0; t < 2 && ok; ++t) {
@@ -928,10 +937,10 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
     // ------------------------------------------------------------ row data, chunks ahead
     bool ok = true;
     int i = 0;
-    for (; w.left > 0 && ok; w.next(a, rs))
-      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
+    for (; w.left > 0 && ok; w.next(a, rs)) {
+      Step x = step_at(w.step0);
+      for (int s = 0; s < w.steps; ++s, ++i, advance(x)) {
         const int st = i % C::kStages;
-        const Step x = step_at(s);
         if (i >= C::kStages)
           ok = mbar_wait_warp(&bars.row_empty[st], (i / C::kStages - 1) & 1, abort_flag);
         if (!ok) break;
@@ -940,6 +949,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
                               row_token[st], lane);
         mbar_arrive(&bars.row_full[st]);
       }
+    }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
       bars.abort = 1;
@@ -958,13 +968,9 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
       const int first = first_token(a, w.n, j);
       const int all_from = first_token(a, w.n, key0 + kTileKeys - 1);
       float sum = 0.f;
-      for (int s = w.step0; s < w.step0 + w.steps; ++s, ++i) {
+      Step x = step_at(w.step0);
+      for (int s = 0; s < w.steps; ++s, ++i, advance(x)) {
         const int st = i % C::kStages;
-        const Step x = step_at(s);
-        // (waited for by a warpgroup that skips the chunk too: its arrival
-        // below must count for this round of the stage)
-        ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
-        if (!ok) break;
         if (sees(x, t)) {
           const int turn = used & 1;
           ok = mbar_wait_warp(&bars.acc_full[t][turn], (used >> 1) & 1, abort_flag);
@@ -973,10 +979,16 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
           // tested column by column if the chunk's first token misses a key
           const bool masked = (rs.skip ? x.chunk * kChunk : 0) < all_from;
           sum += sum_columns(addr + turn * kChunk, kChunk, rs.length - x.chunk * kChunk, masked,
-                             row_token[st], a.c, first, &bars.acc_empty[t][turn]);
+                             row_token[st], a.c, first, &bars.acc_empty[t][turn], lane);
           ++used;
+        } else {
+          // (waited for all the same, so that the arrival below counts for
+          // this round of the stage; above, the product has waited for it)
+          ok = mbar_wait_warp(&bars.row_full[st], (i / C::kStages) & 1, abort_flag);
+          if (!ok) break;
         }
-        mbar_arrive(&bars.row_empty[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.row_empty[st]);
       }
       if (!ok) break;
       const size_t at = (size_t(w.b) * a.Hkv + w.g) * a.out_len + j;
