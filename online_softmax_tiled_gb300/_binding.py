@@ -9,12 +9,13 @@ fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 
 import torch
 
-from ._build import LIB_PATH
+from ._build import CALLS_PATH, LIB_PATH
 
 ATTN_OK = 0
 ATTN_F32 = 0
@@ -144,67 +145,40 @@ def _device_contig(*ts):
             raise ValueError("tensors must be contiguous")
 
 
-# The calls around the cache are short next to Python's own time, so their
-# checks avoid repeated attribute look-ups; what they check is written out at
-# each call.
-
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CALLS = None
 
 
-def _pointers(dev: int, *ts):
-    """Addresses of contiguous tensors on device ``dev`` (None stays None)."""
-    out = []
-    for t in ts:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one GPU")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        out.append(t.data_ptr())
-    return out
+def _calls():
+    """The Python calls of the cache operators (csrc/py_cache.cpp), which check
+    their tensors and launch on the tensors' device."""
+    global _CALLS
+    if _CALLS is None:
+        lib()                       # built, and loaded before what links against it
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} missing: run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        spec = importlib.util.spec_from_file_location("_cache_calls", CALLS_PATH)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        calls.set_error(AttnError)
+        _CALLS = calls
+    return _CALLS
 
 
-def _typed(dtype, *ts):
-    for t in ts:
-        if t is not None and t.dtype is not dtype:
-            raise TypeError(f"expected {dtype}, got {t.dtype}")
-
-
-def _on_device(dev: int, fn, *args):
-    """fn(*args) with device ``dev`` current."""
-    if dev == torch.cuda.current_device():
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
-
-
-def _stream_of(dev: int, stream):
-    """Handle of ``stream``, or of the current stream of device ``dev``."""
+def _handle(stream):
+    """Handle of a stream; None: the current stream of the call's device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _allocating_on(stream, dev: int):
+def _allocating_on(stream, t: torch.Tensor):
     """Context for a call that allocates: what it allocates (workspaces above
     all) must belong to the stream it runs on, or the allocator may hand it
     out again while the call still runs."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     return torch.cuda.stream(stream)
-
-
-def _strides(t: torch.Tensor):
-    """attn_strides of a [B, H, N, d] or [B, H, d] tensor whose last
-    dimension is contiguous; None (the C default) for a contiguous tensor."""
-    if t.is_contiguous():
-        return None
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1:
-        raise ValueError("the last dimension must be contiguous")
-    return ctypes.byref(AttnStrides(st[0], st[1], st[2] if len(st) == 4 else 0))
 
 
 def _check(status: int, what: str):
@@ -365,59 +339,19 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved: bool = False
     token), k, k_out [B,Hkv,N,d] or None, last dimension contiguous, other
     strides free; positions int32 [B,N] (or [N], [1,N]: shared; [B] with one
     token); inv_freq float64 [rot_dim / 2]."""
-    shape = q.shape
-    dims = len(shape)
-    if dims == 4:
-        B, Hq, N, d = shape
-    elif dims == 3:
-        B, Hq, d = shape
-        N = 1
-    else:
-        raise ValueError("q must be [B, Hq, N, d] or [B, Hq, d]")
-    dtype = q.dtype
-    dt = ATTN_BF16 if dtype is _BF16 else _dt(q)
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on the GPU (device pointers)")
-    if q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != dev:
-        raise ValueError("q_out must be like q")
-    Hkv, pk, sk, pko, sko = 0, None, None, None, None
-    if k is not None:
-        kshape = k.shape
-        Hkv = kshape[1]
-        if len(kshape) != dims or kshape[0] != B or kshape[2:] != shape[2:] or \
-                k_out is None or k_out.shape != kshape:
-            raise ValueError("k and k_out must be like q but for the number of heads")
-        if k.dtype is not dtype or k_out.dtype is not dtype:
-            raise TypeError("q, k and their outputs must have one dtype")
-        if k.get_device() != dev or k_out.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one GPU")
-        pk, sk, pko, sko = k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out)
-    elif k_out is not None:
-        raise ValueError("k and k_out go together")
-    if positions.dtype is not _I32 or inv_freq.dtype is not torch.float64:
-        raise TypeError("positions must be int32 and inv_freq float64")
-    count = positions.numel()
-    if count != B * N and count != N:
-        raise ValueError("positions must be [B, N], or [N] for all requests")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot_dim / 2]")
-    pp, pw = _pointers(dev, positions, inv_freq)
-    st = _on_device(dev, lib().attn_rope, q.data_ptr(), _strides(q), q_out.data_ptr(),
-                    _strides(q_out), pk, sk, pko, sko, pp, N if count == B * N else 0, pw, B, Hq,
-                    Hkv, N, d, 2 * inv_freq.shape[0], interleaved, magnitude, inverse, dt,
-                    _stream_of(dev, stream))
-    _check(st, "attn_rope")
+    _calls().rope(q, k, positions, inv_freq, interleaved, magnitude, inverse, q_out, k_out,
+                  _handle(stream))
 
 
 def attn_decode_shared_workspace_size(q, k_prefix, prefix_table, k_pages, block_table,
                                       num_prefix_splits: int = 0, num_splits: int = 0) -> int:
     """Workspace bytes of attn_decode_shared for these tensors."""
     B, Hq, d = q.shape
-    return _on_device(q.get_device(), lib().attn_decode_shared_workspace_size, B, Hq,
-                      k_pages.shape[1], d, prefix_table.shape[0], k_prefix.shape[2],
-                      prefix_table.shape[1], k_pages.shape[2], block_table.shape[1],
-                      num_prefix_splits, num_splits)
+    with torch.cuda.device(q.device):
+        return lib().attn_decode_shared_workspace_size(
+            B, Hq, k_pages.shape[1], d, prefix_table.shape[0], k_prefix.shape[2],
+            prefix_table.shape[1], k_pages.shape[2], block_table.shape[1], num_prefix_splits,
+            num_splits)
 
 
 def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
@@ -427,30 +361,9 @@ def attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_
     bf16 behind prefix_table [n_prefix,max_prefix_pages], prefix_lens
     [n_prefix] and prefix_start [n_prefix+1] int32; own pages, block_table and
     seq_lens as for attn_decode_paged; o like q; lse [B,Hq] float32 or None."""
-    dev = q.get_device()
-    ptrs = _pointers(dev, q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
-                     v_pages, block_table, seq_lens, o, lse, workspace)
-    if dev < 0:
-        raise ValueError("tensors must be on the GPU (device pointers)")
-    _typed(_BF16, q, k_prefix, v_prefix, k_pages, v_pages, o)
-    _typed(_I32, prefix_table, prefix_lens, prefix_start, block_table, seq_lens)
-    B, Hq, d = q.shape
-    n_prefix, max_prefix_pages = prefix_table.shape
-    pshape, shape = k_prefix.shape, k_pages.shape
-    num_prefix_pages, Hkv, prefix_page, dp = pshape
-    num_pages, hk, page, dk = shape
-    tables, max_pages = block_table.shape
-    if v_prefix.shape != pshape or v_pages.shape != shape or dp != d or dk != d or hk != Hkv or \
-            prefix_lens.shape != (n_prefix,) or prefix_start.shape != (n_prefix + 1,) or \
-            tables != B or seq_lens.shape != (B,) or o.shape != (B, Hq, d):
-        raise ValueError("shapes do not go together (see attn_decode_shared)")
-    if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, Hq)):
-        raise TypeError("lse must be float32 [B, Hq]")
-    st = _on_device(dev, lib().attn_decode_shared, *ptrs[:12], B, Hq, Hkv, d, n_prefix,
-                    num_prefix_pages, prefix_page, max_prefix_pages, num_pages, page, max_pages,
-                    scale, num_prefix_splits, num_splits, ptrs[12],
-                    workspace.numel() * workspace.element_size(), _stream_of(dev, stream))
-    _check(st, "attn_decode_shared")
+    _calls().decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
+                           v_pages, block_table, seq_lens, o, lse, scale, num_prefix_splits,
+                           num_splits, workspace, False, _handle(stream))
 
 
 def attn_key_weights_workspace_size(B, Hq, Hkv, T, capacity, out_len) -> int:
@@ -465,34 +378,8 @@ def attn_key_weights(q, k, lse, prev, out, scale: float, decay: float = 1.0, cau
     float32; k [B,Hkv,L,d] bf16 (or pages [num_pages,Hkv,page_size,d] behind
     block_table [B,max_pages], with seq_lens [B]); prev (None: absent; may be
     out) and out [B,Hkv,out_len] float32."""
-    dev = q.get_device()
-    pq, pk, pl, pp, po, pn, pt, pws = _pointers(dev, q, k, lse, prev, out, seq_lens, block_table,
-                                                workspace)
-    if dev < 0:
-        raise ValueError("tensors must be on the GPU (device pointers)")
-    _typed(_BF16, q, k)
-    _typed(_F32, lse, prev, out)
-    _typed(_I32, seq_lens, block_table)
-    shape = q.shape
-    if len(shape) == 4:
-        B, Hq, T, d = shape
-    elif len(shape) == 3:
-        B, Hq, d = shape
-        T = 1
-    else:
-        raise ValueError("q must be [B, Hq, T, d] or [B, Hq, d]")
-    n0, Hkv, L, dk = k.shape
-    ob, oh, out_len = out.shape
-    tables, max_pages = (n0, 0) if block_table is None else block_table.shape
-    if lse.shape != shape[:-1] or dk != d or ob != B or oh != Hkv or tables != B or \
-            (prev is not None and prev.shape != out.shape) or \
-            (seq_lens is not None and seq_lens.shape != (B,)):
-        raise ValueError("shapes do not go together (see attn_key_weights)")
-    st = _on_device(dev, lib().attn_key_weights, pq, pk, pl, pp, po, pn, pt, B, Hq, Hkv, T, L, n0,
-                    L, max_pages, out_len, d, scale, decay, causal, pws,
-                    0 if workspace is None else workspace.numel() * workspace.element_size(),
-                    _stream_of(dev, stream))
-    _check(st, "attn_key_weights")
+    _calls().key_weights(q, k, lse, prev, out, scale, decay, causal, seq_lens, block_table,
+                         workspace, False, _handle(stream))
 
 
 def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink: int = 0,
@@ -501,31 +388,8 @@ def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_s
     block_table [B,max_pages], with seq_lens [B]); scores [B,Hkv,score_len]
     float32; k_out, v_out [B,Hkv,out_len,d]; scores_out [B,Hkv,out_len] or
     None; kept [B,Hkv,n_keep] and new_lens [B] int32."""
-    dev = k.get_device()
-    pk, pv, ps, pl, pt, pko, pvo, pso, pkept, pnew = _pointers(
-        dev, k, v, scores, seq_lens, block_table, k_out, v_out, scores_out, kept, new_lens)
-    if dev < 0:
-        raise ValueError("tensors must be on the GPU (device pointers)")
-    dtype = k.dtype
-    _typed(dtype, v, k_out, v_out)
-    _typed(_F32, scores, scores_out)
-    _typed(_I32, seq_lens, block_table, kept, new_lens)
-    shape = k.shape
-    n0, hk, L, d = shape
-    B, Hkv, n_keep = kept.shape
-    sb, sh, score_len = scores.shape
-    oshape = k_out.shape
-    out_len = oshape[2]
-    tables, max_pages = (n0, 0) if block_table is None else block_table.shape
-    if v.shape != shape or hk != Hkv or sb != B or sh != Hkv or oshape != (B, Hkv, out_len, d) or \
-            v_out.shape != oshape or tables != B or new_lens.shape != (B,) or \
-            (scores_out is not None and scores_out.shape != oshape[:3]) or \
-            (seq_lens is not None and seq_lens.shape != (B,)):
-        raise ValueError("shapes do not go together (see attn_cache_evict)")
-    st = _on_device(dev, lib().attn_cache_evict, pk, pv, ps, pl, pt, pko, pvo, pso, pkept, pnew, B,
-                    Hkv, L, n0, L, max_pages, score_len, d, n_keep, n_sink, n_recent, out_len,
-                    ATTN_BF16 if dtype is _BF16 else _dt(k), _stream_of(dev, stream))
-    _check(st, "attn_cache_evict")
+    _calls().evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_sink, n_recent,
+                   seq_lens, block_table, _handle(stream))
 
 
 def attn_status_string(status: int) -> str:
@@ -662,16 +526,15 @@ def rope(q, k, positions, inv_freq, interleaved: bool = False, magnitude: float 
     ``out`` = (q_out, k_out), which may be (q, k) themselves. ``inverse``
     turns back: the gradient of the call when given dy and the same
     magnitude. See attn_rope for shapes, rope_frequencies for inv_freq."""
-    if stream is not None and out is None:
-        with _allocating_on(stream, q.get_device()):
+    if out is not None:
+        _calls().rope(q, k, positions, inv_freq, interleaved, magnitude, inverse, *out,
+                      _handle(stream))
+        return out
+    if stream is not None:
+        with _allocating_on(stream, q):
             return rope(q, k, positions, inv_freq, interleaved, magnitude, inverse)
-    if out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-    else:
-        q_out, k_out = out
-    attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved, magnitude, inverse, stream)
-    return q_out, k_out
+    return _calls().rope(q, k, positions, inv_freq, interleaved, magnitude, inverse, None, None,
+                         None)
 
 
 def evict(k, v, scores, n_keep: int, n_sink: int = 0, n_recent: int = 0, seq_lens=None,
@@ -684,13 +547,13 @@ def evict(k, v, scores, n_keep: int, n_sink: int = 0, n_recent: int = 0, seq_len
     arange(B)[:, None] the outputs are a paged cache for decode_paged."""
     if out is None:
         if stream is not None:
-            with _allocating_on(stream, k.get_device()):
+            with _allocating_on(stream, k):
                 return evict(k, v, scores, n_keep, n_sink, n_recent, seq_lens, block_table)
         B, Hkv = scores.shape[:2]
         out = (k.new_zeros((B, Hkv, n_keep, k.shape[3])), k.new_zeros((B, Hkv, n_keep, k.shape[3])),
                scores.new_zeros((B, Hkv, n_keep)),
-               torch.empty((B, Hkv, n_keep), dtype=_I32, device=k.device),
-               torch.empty((B,), dtype=_I32, device=k.device))
+               torch.empty((B, Hkv, n_keep), dtype=torch.int32, device=k.device),
+               torch.empty((B,), dtype=torch.int32, device=k.device))
     k_out, v_out, scores_out, kept, new_lens = out
     if kept.shape[2] != n_keep:
         raise ValueError("the kept indices must be [B, Hkv, n_keep]")
@@ -707,21 +570,14 @@ def decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start
     prefix_start[p] .. prefix_start[p+1]-1 share prefix p. Splits of 0 are
     chosen by the library."""
     if stream is not None:
-        with _allocating_on(stream, q.get_device()):
+        with _allocating_on(stream, q):
             return decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start,
                                  k_pages, v_pages, block_table, seq_lens, num_prefix_splits,
                                  num_splits, scale, None, workspace)
-    B, Hq, d = q.shape
-    if workspace is None:
-        n = attn_decode_shared_workspace_size(q, k_prefix, prefix_table, k_pages, block_table,
-                                              num_prefix_splits, num_splits)
-        workspace = q.new_empty(n, dtype=torch.uint8)
-    o = torch.empty_like(q)
-    lse = q.new_empty((B, Hq), dtype=_F32)
-    attn_decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start, k_pages,
-                       v_pages, block_table, seq_lens, o, lse, d ** -0.5 if scale is None else scale,
-                       num_prefix_splits, num_splits, workspace)
-    return o, lse
+    return _calls().decode_shared(q, k_prefix, v_prefix, prefix_table, prefix_lens, prefix_start,
+                                  k_pages, v_pages, block_table, seq_lens, None, None,
+                                  q.shape[-1] ** -0.5 if scale is None else scale,
+                                  num_prefix_splits, num_splits, workspace, True, None)
 
 
 def key_weights(q, k, lse, prev=None, decay: float = 1.0, causal: bool = True,
@@ -732,21 +588,9 @@ def key_weights(q, k, lse, prev=None, decay: float = 1.0, causal: bool = True,
     prev. ``out`` may be ``prev``; keys past a request's length are left as
     they were (allocated here, they are zero)."""
     if stream is not None:
-        with _allocating_on(stream, q.get_device()):
+        with _allocating_on(stream, q):
             return key_weights(q, k, lse, prev, decay, causal, scale, seq_lens, block_table, out,
                                None, workspace)
-    shape = q.shape
-    B, Hq, d, T = shape[0], shape[1], shape[-1], shape[2] if len(shape) == 4 else 1
-    Hkv, cap = k.shape[1:3]
-    if block_table is not None:
-        cap *= block_table.shape[1]
-    if out is None:
-        make = torch.empty if seq_lens is None else torch.zeros
-        out = make((B, Hkv, cap), dtype=_F32, device=k.device)
-    if workspace is None and T * Hq > 256 * Hkv:
-        n = _on_device(q.get_device(), attn_key_weights_workspace_size, B, Hq, Hkv, T, cap,
-                       out.shape[2])
-        workspace = k.new_empty(n, dtype=torch.uint8) if n else None
-    attn_key_weights(q, k, lse, prev, out, d ** -0.5 if scale is None else scale, decay, causal,
-                     seq_lens, block_table, workspace)
-    return out
+    return _calls().key_weights(q, k, lse, prev, out,
+                                q.shape[-1] ** -0.5 if scale is None else scale, decay, causal,
+                                seq_lens, block_table, workspace, True, None)

@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library ``_lib/libattn_gb300.so`` for sm_103a.
+"""Build the in-tree CUDA library ``_lib/libattn_gb300.so`` for sm_103a, and the
+Python calls of the cache operators, ``_lib/_cache_calls.so``, on top of it.
 
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel into
 ``<repo>/_build/`` and linked into one shared library with a C ABI
@@ -13,6 +14,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 BUILD_DIR = os.path.join(REPO_DIR, "_build")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_gb300.so")
+CALLS_PATH = os.path.join(LIB_DIR, "_cache_calls.so")
 
 SOURCES = ["api.cu", "fwd_simt.cu", "fwd_tc.cu", "fwd_tc64.cu", "bwd_aux.cu", "bwd_simt.cu", "bwd_tc.cu",
            "bwd_dq.cu", "decode.cu", "decode_shared.cu", "api_cache.cu", "rope.cu",
@@ -54,10 +57,31 @@ def _run(cmd):
     return res.stdout + res.stderr
 
 
+def _calls_commands(obj: str, out: str):
+    """The host compiler's commands (compile, link) for the Python calls,
+    against the installed torch and this Python."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    libs = os.path.join(root, "lib")
+    cxx = shutil.which("g++") or "g++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+                "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-isystem", sysconfig.get_paths()["include"],
+                "-isystem", os.path.join(cuda, "include"),
+                "-c", os.path.join(CSRC, "py_cache.cpp"), "-o", obj]
+    link = [cxx, "-shared", obj, "-o", out, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+            "-lc10", "-lc10_cuda", "-L" + LIB_DIR, "-l:" + os.path.basename(LIB_PATH),
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link the library if needed; return its path."""
-    if (not force and os.path.exists(LIB_PATH)
-            and os.path.getmtime(LIB_PATH) >= _inputs_mtime()):
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _inputs_mtime()
+                         for p in (LIB_PATH, CALLS_PATH)):
         return LIB_PATH
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -69,8 +93,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         out = _run([nvcc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
         return obj, out
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    tmp_calls = CALLS_PATH + ".tmp"
+    calls_compile, calls_link = _calls_commands(os.path.join(BUILD_DIR, "py_cache.o"), tmp_calls)
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(_run, calls_compile)
         results = list(ex.map(compile_one, SOURCES))
+        calls.result()
     if verbose or ptxas_info:
         for (_, out), src in zip(results, SOURCES):
             if out.strip():
@@ -78,6 +106,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB_PATH + ".tmp"
     _run([nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *[o for o, _ in results]])
     os.replace(tmp, LIB_PATH)
+    _run(calls_link)
+    os.replace(tmp_calls, CALLS_PATH)
     return LIB_PATH
 
 
