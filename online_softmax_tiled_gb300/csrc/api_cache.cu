@@ -148,7 +148,7 @@ size_t attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int n_pr
       !shared_sizes_supported(B, Hq, Hkv, d, prefix_page_size, max_prefix_pages, page_size,
                               max_pages_per_seq, num_prefix_splits, num_splits))
     return 0;
-  const SharedPlan pl = shared_plan(B, Hq, Hkv, n_prefix, prefix_page_size, max_prefix_pages,
+  const SharedPlan pl = shared_plan(B, Hq, Hkv, d, n_prefix, prefix_page_size, max_prefix_pages,
                                     page_size, max_pages_per_seq, num_prefix_splits, num_splits);
   return partial_layout(1LL * B * Hq, d, 1LL * pl.prefix_splits + pl.own_splits).total;
 }
@@ -184,7 +184,7 @@ attn_status attn_decode_shared(const void* q, const void* k_prefix, const void* 
   const void* narrow[] = {prefix_table, prefix_lens, prefix_start, block_table, seq_lens, lse};
   for (const void* x : narrow)
     if (!aligned_to(x, 4)) return ATTN_ERR_MISALIGNED;
-  const SharedPlan pl = shared_plan(B, Hq, Hkv, n_prefix, prefix_page_size, max_prefix_pages,
+  const SharedPlan pl = shared_plan(B, Hq, Hkv, d, n_prefix, prefix_page_size, max_prefix_pages,
                                     page_size, max_pages_per_seq, num_prefix_splits, num_splits);
   // work items are numbered in 32 bits, as are the partial rows
   if (1LL * B * Hq * (1LL * pl.prefix_splits + pl.own_splits) > (1LL << 30))

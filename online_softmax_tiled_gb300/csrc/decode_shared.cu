@@ -36,6 +36,7 @@
 // prefix leaves idle; the merge waits for both.
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "launchers.h"
@@ -708,7 +709,7 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
 
 // How a call is cut, from its sizes alone (group sizes and lengths are only
 // known on the device).
-SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_size,
+SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_page_size,
                        int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
                        int own_splits) {
   SharedPlan pl;
@@ -720,15 +721,32 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_siz
   pl.units = int(std::min<long long>((rows + per - 1) / per + n_prefix - 1, B));
   const long long cap = 1LL * prefix_page_size * max_prefix_pages;
   const long long tiles = (cap + kBN - 1) / kBN;
+  const long long own_cap = 1LL * page_size * max_pages;
+  if (own_splits <= 0) {
+    // One round of the split kernel's three CTAs per SM, or chunks of 512
+    // keys (16 at most) where there are more, but 128 keys at least.
+    const long long want = (3 * sms + 1LL * B * Hkv - 1) / (1LL * B * Hkv);
+    const long long chunks = std::min(16LL, (own_cap + 511) / 512);
+    own_splits = int(std::max(1LL, std::min(std::max(want, chunks), (own_cap + 127) / 128)));
+  }
   if (prefix_splits <= 0) {
-    // Splits that take the fewest rounds of key tiles with one CTA per SM,
-    // each CTA paying about two tiles for its start and its partial rows.
-    const long long ctas = Hkv * std::max<long long>(n_prefix, (rows + per - 1) / per);
-    long long best = -1;
+    // Both parts run at once, so a call takes as long as a prefix CTA, or as
+    // the work of both spread over all SMs, then as the merge of the splits.
+    // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
+    // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
+    // its partial rows; own keys, half their capacity, at 3 TB/s; 0.5 + 0.6
+    // per MB of partials for every split to merge.
+    const double tile = (pl.pair ? 2.3 : 1.2) * d / 128, tiles_all = double(tiles);
+    const double ctas = double(Hkv) * std::max<long long>(n_prefix, (rows + per - 1) / per);
+    const double own = 1.0 * B * Hkv * own_cap / 2 * d * 4 / 3e6;
+    const double merge = 0.5 + 0.6e-6 * B * Hq * d * 4;
+    double best = 0;
     prefix_splits = 1;
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
-      const long long cost = ((ctas * s + sms - 1) / sms) * ((tiles + s - 1) / s + 2);
-      if (best < 0 || cost < best) {
+      const double cta = (double((tiles + s - 1) / s) + 4) * tile * std::ceil(ctas * s / sms);
+      const double all = ctas * (tiles_all + 4 * s) * tile / sms + own;
+      const double cost = std::max(cta, all) + s * merge;
+      if (s == 1 || cost < best) {
         best = cost;
         prefix_splits = s;
       }
@@ -737,13 +755,6 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_siz
   const long long per_split = (tiles + prefix_splits - 1) / prefix_splits;
   pl.prefix_chunk = int(per_split * kBN);
   pl.prefix_splits = int((tiles + per_split - 1) / per_split);
-  if (own_splits <= 0) {
-    // four rounds of the split kernel's three CTAs per SM, chunks of 128
-    // keys at least
-    const long long own_cap = 1LL * page_size * max_pages;
-    const long long want = (12 * sms + 1LL * B * Hkv - 1) / (1LL * B * Hkv);
-    own_splits = int(std::max<long long>(1, std::min<long long>(want, (own_cap + 127) / 128)));
-  }
   pl.own_splits = own_splits;
   // copies of a key tile: whole tiles of a single page, else the largest
   // power of two that divides the page size

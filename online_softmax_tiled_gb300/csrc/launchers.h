@@ -280,7 +280,7 @@ cudaError_t launch_bwd_dq(const BwdArgs& a);
 cudaError_t launch_bwd_convert(const BwdArgs& a);
 cudaError_t launch_decode_split(const DecodeArgs& a);
 cudaError_t launch_merge(const MergeArgs& a);
-SharedPlan shared_plan(int B, int Hq, int Hkv, int n_prefix, int prefix_page_size,
+SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_page_size,
                        int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
                        int own_splits);
 cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& plan);
