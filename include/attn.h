@@ -378,7 +378,8 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
  * bf16; lse [B,Hq] float32 (may be NULL). A request without any key gets
  * O = 0, LSE = -inf. d 64 or 128; Hq/Hkv in {1, 2, 4, 8}.
  * num_prefix_splits, num_splits: most splits of a prefix's keys and of a
- * request's own; 0 takes the library's choice for these sizes. The
+ * request's own; 0 takes the library's choice, made from the sizes alone (a
+ * table much wider than the lengths it serves is no harm). The
  * probabilities of prefix keys are rounded to bf16 for the P·V product, as in
  * attn_fwd; all softmax state is float32.
  * Device-side checks: a length outside [0, capacity] counts as 0, a split
@@ -465,9 +466,9 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
  * for the n = seq_lens[b] keys of request b. The T queries are the last T of
  * the n positions: with causal = 1 key j is seen by token i iff
  * j <= n - T + i, with causal = 0 by all. A row with an infinite lse
- * gives nothing. prev == NULL: no first term (decay ignored); prev == out adds in
- * place; any other overlap of the two is refused. out[b,g,j] for j >= n is
- * left as it was.
+ * gives nothing, whatever its q holds. prev == NULL: no first term (decay
+ * ignored); prev == out adds in place; any other overlap of the two is
+ * refused. out[b,g,j] for j >= n is left as it was.
  *
  * q [B,Hq,T,d] bf16, lse [B,Hq,T] float32 (T = 1: decode's q and lse); k a
  * contiguous cache [B,Hkv,L,d] bf16 (block_table NULL; seq_lens NULL: every
@@ -557,8 +558,8 @@ ATTN_API const char* attn_status_string(attn_status s);
 /*
  * Synchronise `stream`, then report (and clear) the library's device error
  * word: ATTN_ERR_DEVICE_TIMEOUT if a bounded device wait ran out since the
- * last check, else ATTN_ERR_DEVICE_INDEX if a paged decode met an
- * out-of-range length or page index; ATTN_ERR_CUDA if the stream reports a
+ * last check, else ATTN_ERR_DEVICE_INDEX if a call that reads lengths or
+ * page indices from device memory met one out of range; ATTN_ERR_CUDA if the stream reports a
  * CUDA error; else ATTN_OK.
  */
 ATTN_API attn_status attn_sync_status(void* stream);

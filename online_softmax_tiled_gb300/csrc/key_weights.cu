@@ -159,7 +159,9 @@ bool make_map_joined(CUtensorMap* m, const void* base, int d, int rows, uint64_t
 // What a row needs besides Q: -lse/scale as three bf16 parts whose sum is the
 // float32 value (far below any score where the row counts for nothing: no
 // such row, or an infinite lse, as of a row that saw no key), and its token
-// (INT_MIN where there is no row).
+// (INT_MIN where the row counts for nothing: a Q that is not finite would
+// still reach the sum). Returns whether a row of the strip has an infinite
+// lse: then every column is to be tested.
 //
 // The parts are the row's first three columns of a K = 16 operand tile: core
 // matrices of 8 rows x 16 bytes, two along K, groups of 8 rows every 256
@@ -170,27 +172,30 @@ constexpr float kFarBelow = -3.0e38f;
 // strip of `length` that begins at row `base` of the head (the reads of all
 // rows in flight together).
 template <int kRows>
-ATTN_DEVINL void put_rows(const KwArgs& a, int head, int base, int first, int length, int count,
+ATTN_DEVINL bool put_rows(const KwArgs& a, int head, int base, int first, int length, int count,
                           uint8_t* parts, int* token, int lane) {
   float l[kRows];
   const float* lse = a.lse + size_t(head) * a.R + base;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) l[u] = lse[min(first + u * 32 + lane, length - 1)];
+  bool dead = false;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int n = u * 32 + lane;
     if (n >= count) break;
-    const bool in = first + n < length;
+    const bool in = first + n < length, none = fabsf(l[u]) == INFINITY;
+    dead |= in && none;
     float v = -l[u] * a.inv_scale;
-    if (!in || fabsf(l[u]) == INFINITY || v < kFarBelow) v = kFarBelow;
+    if (!in || none || v < kFarBelow) v = kFarBelow;
     if (v > -kFarBelow) v = -kFarBelow;
-    token[n] = in ? (base + first + n) % a.T : INT_MIN;
+    token[n] = in && !none ? (base + first + n) % a.T : INT_MIN;
     const float p0 = __bfloat162float(__float2bfloat16_rn(v));
     const float p1 = __bfloat162float(__float2bfloat16_rn(v - p0));
     *reinterpret_cast<uint4*>(parts + (n >> 3) * 256 + (n & 7) * 16) =
         make_uint4(pack_bf16x2(p0, p1), pack_bf16x2(v - p0 - p1, 0.f), 0u, 0u);
   }
   fence_proxy_async_smem();
+  return __any_sync(0xffffffffu, dead);
 }
 // Ones for the other operand (128 rows x 16), zeros for `bytes` of parts.
 ATTN_DEVINL void fill_parts(uint8_t* ones, uint8_t* parts, int bytes, int tid) {
@@ -383,6 +388,7 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
                                              ~uintptr_t(1023));
   __shared__ KeysBars bars;
   __shared__ __align__(16) int row_token[2][NMAX];
+  __shared__ int row_dead[2];          // some row has an infinite lse
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -563,8 +569,10 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         const int rb = heads & 1;
         if (heads >= 2) ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
-        put_rows<NMAX / 32>(a, w.b * a.Hkv + w.g, 0, 0, a.R, N,
-                            smem + C::kPartsOff + rb * C::kPartsBytes, row_token[rb], lane);
+        const bool dead = put_rows<NMAX / 32>(a, w.b * a.Hkv + w.g, 0, 0, a.R, N,
+                                              smem + C::kPartsOff + rb * C::kPartsBytes,
+                                              row_token[rb], lane);
+        if (lane == 0) row_dead[rb] = dead;
         mbar_arrive(&bars.row_full[rb]);
         ++heads;
       }
@@ -597,7 +605,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
         if (!ok) break;
         tc::fence_after_sync();
         // the tile needs its columns tested if the first token misses its last key
-        const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0;
+        const bool masked = first_token(a, w.n, w.tile * kTileKeys + kTileKeys - 1) > 0 ||
+                            row_dead[(heads - 1) & 1];
         const int* token = row_token[(heads - 1) & 1];
         float sum = 0.f;
 #pragma unroll 1
@@ -737,6 +746,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
                                              ~uintptr_t(1023));
   __shared__ RowsBars bars;
   __shared__ __align__(16) int row_token[C::kStages][kChunk];
+  __shared__ int row_dead[C::kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -944,9 +954,10 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         if (i >= C::kStages)
           ok = mbar_wait_warp(&bars.row_empty[st], (i / C::kStages - 1) & 1, abort_flag);
         if (!ok) break;
-        put_rows<kChunk / 32>(a, w.b * a.Hkv + w.g, x.strip * rs.length, x.chunk * kChunk,
-                              rs.length, kChunk, smem + C::kPartsOff + st * C::kPartsBytes,
-                              row_token[st], lane);
+        const bool dead = put_rows<kChunk / 32>(
+            a, w.b * a.Hkv + w.g, x.strip * rs.length, x.chunk * kChunk, rs.length, kChunk,
+            smem + C::kPartsOff + st * C::kPartsBytes, row_token[st], lane);
+        if (lane == 0) row_dead[st] = dead;
         mbar_arrive(&bars.row_full[st]);
       }
     }
@@ -977,7 +988,8 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!ok) break;
           tc::fence_after_sync();
           // tested column by column if the chunk's first token misses a key
-          const bool masked = (rs.skip ? x.chunk * kChunk : 0) < all_from;
+          const bool masked =
+              (rs.skip ? x.chunk * kChunk : 0) < all_from || row_dead[st];
           sum += sum_columns(addr + turn * kChunk, kChunk, rs.length - x.chunk * kChunk, masked,
                              row_token[st], a.c, first, &bars.acc_empty[t][turn], lane);
           ++used;

@@ -211,6 +211,28 @@ def test_in_place_scale_and_dead_rows(ost):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,L,causal", [(1, 300, True), (60, 200, True), (60, 200, False),
+                                        (300, 300, True), (300, 700, False)])
+def test_dead_rows_may_hold_anything(ost, T, L, causal):
+    """Queries of rows with an infinite normaliser (padding) may be NaN or
+    infinite; the others' weights are what they were."""
+    q = random_like_shape((2, 4, T, 64), torch.bfloat16, 5).to(DEV)
+    k = random_like_shape((2, 2, L, 64), torch.bfloat16, 6).to(DEV)
+    lse = torch.full((2, 4, T), 5.0, device=DEV)
+    lse[0, 1, ::3] = -float("inf")
+    lse[0, 0, -1] = float("inf")
+    lse[1, 3] = -float("inf")
+    want = ost.key_weights(q, k, lse, causal=causal)
+    q[0, 1, ::3] = float("nan")
+    q[0, 0, -1] = 3e38
+    q[1, 3] = float("inf")
+    got = ost.key_weights(q, k, lse, causal=causal)
+    torch.cuda.synchronize()
+    assert ost.attn_sync_status() == 0
+    assert torch.equal(got, want) and bool(torch.isfinite(got).all())
+
+
+@pytest.mark.gpu
 def test_with_the_librarys_own_lse(ost):
     """Decode and prefill LSE in, probabilities out: each head and token
     gives one in all."""
