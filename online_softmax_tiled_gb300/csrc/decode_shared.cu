@@ -723,10 +723,12 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
   const long long tiles = (cap + kBN - 1) / kBN;
   const long long own_cap = 1LL * page_size * max_pages;
   if (own_splits <= 0) {
-    // One round of the split kernel's three CTAs per SM, or chunks of 512
-    // keys (16 at most) where there are more, but 128 keys at least.
+    // One round of the split kernel's three CTAs per SM, or a split per 512
+    // keys of capacity, four at most, where that is more, but 128 keys a split
+    // at least (64 requests of up to 1024 keys: 60, 55, 57, 65 us with 1, 2,
+    // 4, 8 splits; 128 of up to 8192: 481, 410, 361, 362).
     const long long want = (3 * sms + 1LL * B * Hkv - 1) / (1LL * B * Hkv);
-    const long long chunks = std::min(16LL, (own_cap + 511) / 512);
+    const long long chunks = std::min(4LL, (own_cap + 511) / 512);
     own_splits = int(std::max(1LL, std::min(std::max(want, chunks), (own_cap + 127) / 128)));
   }
   if (prefix_splits <= 0) {
@@ -734,11 +736,13 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
     // the work of both spread over all SMs, then as the merge of the splits.
     // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
     // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
-    // its partial rows; own keys, half their capacity, at 3 TB/s; 0.5 + 0.6
-    // per MB of partials for every split to merge.
+    // its partial rows; own keys, half their capacity but 512 at most (the
+    // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
+    // partials for every split to merge. (64 requests behind 8192 keys: 80, 55,
+    // 59, 69 us with 2, 4, 8, 19 splits, 19 filling the device.)
     const double tile = (pl.pair ? 2.3 : 1.2) * d / 128, tiles_all = double(tiles);
     const double ctas = double(Hkv) * std::max<long long>(n_prefix, (rows + per - 1) / per);
-    const double own = 1.0 * B * Hkv * own_cap / 2 * d * 4 / 3e6;
+    const double own = 1.0 * B * Hkv * std::min(own_cap / 2, 512LL) * d * 4 / 3e6;
     const double merge = 0.5 + 0.6e-6 * B * Hq * d * 4;
     double best = 0;
     prefix_splits = 1;

@@ -12,8 +12,9 @@ TEST INFRASTRUCTURE ONLY (see the package docstring). Sources:
 
 Readings where the pages are silent: a pair is turned by p·w (counter-
 clockwise in the (a, b) plane); ties between scores go to the lowest index; a
-NaN score ranks as -inf. Every function is pinned by
-``tests/test_oracle_cache.py``.
+NaN score ranks as -inf. Every function is pinned on the CPU by the tests of
+its operator: ``tests/test_rope.py``, ``tests/test_decode_shared.py``,
+``tests/test_key_weights.py`` and ``tests/test_evict.py``.
 """
 
 from __future__ import annotations
