@@ -6,7 +6,9 @@
 // want = n_keep - n_sink - n_recent, found exactly by a radix descent over
 // the scores mapped to ordered 32-bit integers (11, 11 and 10 bits): each
 // pass counts the digits of the scores that share the prefix found so far
-// and walks the counts from the top. Scores above the threshold are kept,
+// and walks the counts from the top; the last passes fall away where all
+// scores of the digit found stay, as where no other score shares 22 bits with
+// the threshold. Scores above the threshold are kept,
 // those equal to it as long as places remain, lowest index first: the
 // result does not depend on the order of the counting atomics.
 //
@@ -19,6 +21,13 @@
 // Moving the rows is bound by memory: every kept row is read once and
 // written once. A thread moves 16-byte pieces, four rows of K and V in
 // flight.
+//
+// Measured: 64 rows of 32768 scores, 4096 kept of d = 128 in bf16, 16-key
+// pages: 59.6 us, of which the moving of the rows takes 40 (268 MB read and
+// written, 6.6 TB/s) and the selection the rest: 4 to load the scores, 2 a
+// pass, a barrier of the cluster between each, 3 to write the indices; none of
+// it near a limit, all of it latency. With two CTAs a row; four or eight were
+// slower (they share SMs). 6 rows of 1000, 128 kept: 10.2 us.
 
 #include <cooperative_groups.h>
 
@@ -70,7 +79,7 @@ struct __align__(16) SelectSmem {
   int hist[3][kBins];      // this CTA's digit counts, one table per pass (read by the cluster)
   int part[kSelWarps];
   int sure[kSelWarps], equal[kSelWarps];   // per warp's segment (read by the cluster)
-  int found[2];            // digit, and how many scores rank above it
+  int found[3];            // digit, how many scores rank above it, how many have it
 };
 
 // One cluster per (request, KV head) row; CTA r of C owns the r-th slice of
@@ -106,23 +115,28 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
   const bool all = n <= n_keep;                      // (the same for the whole cluster)
   const bool held = seg <= 32 * kHeld;
   // Key of score j of this warp's segment (which is not empty): held sinks and
-  // recents rank above everything, lanes past the segment below. The load is
-  // not behind a branch, so that a thread's loads are in flight together.
-  auto key_at = [&](int j) {
-    const uint32_t key = score_key(s[min(j, hi - 1)]);
-    return j >= hi ? kAbsent : j < mid0 || j >= mid1 ? kAlways : key;
+  // recents rank above everything, lanes past the segment below. (Its load is
+  // made for every lane, none behind a branch, so that a thread's loads are in
+  // flight together.)
+  auto key_of = [&](float score, int j) {
+    return j >= hi ? kAbsent : j < mid0 || j >= mid1 ? kAlways : score_key(score);
   };
   // The segment in groups of kLoads warp reads; those that fit stay in
   // registers. f(keys of the group, index of the lane's first one).
   uint32_t keys[kHeld];
   auto read = [&](uint32_t* key, int j) {
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) key[u] = key_at(j + u * 32);
-  };
-  if (held)
+    for (int u = 0; u < kLoads; ++u) key[u] = __float_as_uint(s[min(j + u * 32, hi - 1)]);
 #pragma unroll
-    for (int g = 0; g < kHeld; g += kLoads)
-      if (lo + g * 32 < hi) read(keys + g, lo + g * 32 + lane);
+    for (int u = 0; u < kLoads; ++u) key[u] = key_of(__uint_as_float(key[u]), j + u * 32);
+  };
+  if (held && lo < hi) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) keys[u] = __float_as_uint(s[min(lo + u * 32 + lane, hi - 1)]);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      keys[u] = key_of(__uint_as_float(keys[u]), lo + u * 32 + lane);
+  }
   auto visit = [&](auto&& f) {
     if (held) {
 #pragma unroll
@@ -205,12 +219,18 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
         if (above < need && above + mine[u] >= need) {
           sm.found[0] = 4 * tid + u;
           sm.found[1] = above;
+          sm.found[2] = mine[u];
         }
         above += mine[u];
       }
       __syncthreads();
       bar |= uint32_t(sm.found[0]) << shift;
       need -= sm.found[1];
+      if (need == sm.found[2]) {                     // all of the digit's scores stay
+        bar -= 1;                                    // (no score has a zero first digit)
+        need = 0;
+        break;
+      }
     }
   }
 
@@ -242,21 +262,34 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
   e0 = __reduce_add_sync(0xffffffffu, e0);
   float* so = scores_out == nullptr ? nullptr : scores_out + size_t(row) * cap_out;
   const uint32_t below = (1u << lane) - 1;
-  visit([&](const uint32_t* key, int j0) {
+  auto keep = [&](uint32_t key, int at, int j) {
+    idx[at] = j;
+    if (so != nullptr) so[at] = key_has_score(key) ? score_of(key) : s[j];
+  };
+  if (need == 0) {
+    // (nearly always: no tie is cut; counting bits is what this loop costs)
+    visit([&](const uint32_t* key, int j0) {
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const uint32_t bs = __ballot_sync(0xffffffffu, key[u] > bar);
-      const uint32_t be = __ballot_sync(0xffffffffu, key[u] == bar);
-      const int eq_before = e0 + __popc(be & below);
-      if (key[u] > bar || (key[u] == bar && eq_before < need)) {
-        const int at = s0 + __popc(bs & below) + min(eq_before, need), j = j0 + u * 32;
-        idx[at] = j;
-        if (so != nullptr) so[at] = key_has_score(key[u]) ? score_of(key[u]) : s[j];
+      for (int u = 0; u < kLoads; ++u) {
+        const uint32_t bs = __ballot_sync(0xffffffffu, key[u] > bar);
+        if (key[u] > bar) keep(key[u], s0 + __popc(bs & below), j0 + u * 32);
+        s0 += __popc(bs);
       }
-      s0 += __popc(bs);
-      e0 += __popc(be);
-    }
-  });
+    });
+  } else {
+    visit([&](const uint32_t* key, int j0) {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const uint32_t bs = __ballot_sync(0xffffffffu, key[u] > bar);
+        const uint32_t be = __ballot_sync(0xffffffffu, key[u] == bar);
+        const int eq_before = e0 + __popc(be & below);
+        if (key[u] > bar || (key[u] == bar && eq_before < need))
+          keep(key[u], s0 + __popc(bs & below) + min(eq_before, need), j0 + u * 32);
+        s0 += __popc(bs);
+        e0 += __popc(be);
+      }
+    });
+  }
   // no CTA leaves while another may still read its counts
   cluster.sync();
 }
