@@ -271,6 +271,37 @@ def test_bad_tables_are_flagged_not_read(ost):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 200])
+def test_offsets_past_32_bits(ost, page):
+    """Pages past 2^32 bytes (2^31 elements) of their pool give what the same
+    pages at its front give; 200 keys: one page a table row."""
+    Hkv, d = 8, 128
+    total = (1 << 32) // (Hkv * page * d * 2) + 64
+    k = torch.zeros(total, Hkv, page, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    g = torch.Generator().manual_seed(3)
+    for x in (k, v):
+        x[:16] = torch.randn(16, Hkv, page, d, generator=g).to(torch.bfloat16).to(DEV)
+        x[-16:] = x[:16]
+    q = torch.randn(3, 32, d, generator=g).to(torch.bfloat16).to(DEV)
+    n = 1 if page == 200 else 4
+    table = torch.arange(16, dtype=torch.int32, device=DEV)
+    lens = torch.tensor([page * n - 3, 0, 17], dtype=torch.int32, device=DEV)
+    plen = torch.tensor([page * n - 5], dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+
+    def run(at):
+        t = table + at
+        return ost.decode_shared(q, k, v, t[12:12 + n].view(1, n).contiguous(), plen, start, k, v,
+                                 t[:3 * n].view(3, n).contiguous(), lens)
+    near, far = run(0), run(total - 16)
+    torch.cuda.synchronize()
+    assert ost.attn_sync_status() == 0
+    assert torch.equal(near[0], far[0]) and torch.equal(near[1], far[1])
+    assert bool((near[0] != 0).any())
+
+
+@pytest.mark.gpu
 def test_streams_graphs_and_calls_at_once(ost):
     """Two calls at once on two streams (their own workspaces), a captured
     and replayed call, and many calls back to back on one workspace."""

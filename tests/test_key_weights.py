@@ -248,6 +248,34 @@ def test_with_the_librarys_own_lse(ost):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 130])
+def test_offsets_past_32_bits(ost, T):
+    """Pages, and heads of a contiguous cache, past 2^32 bytes (2^31 elements)
+    give what the same keys at the front give."""
+    Hkv, page, d, lens = 2, 16, 128, [61, 30]
+    total = (1 << 32) // (Hkv * page * d * 2) + 64
+    k = torch.zeros(total, Hkv, page, d, dtype=torch.bfloat16, device=DEV)
+    k[:8] = random_like_shape((8, Hkv, page, d), torch.bfloat16, 1).to(DEV)
+    k[-8:] = k[:8]
+    q = random_like_shape((2, 4, T, d), torch.bfloat16, 2).to(DEV)
+    lse = torch.full((2, 4, T), 4.0, device=DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    table = torch.arange(8, dtype=torch.int32, device=DEV).view(2, 4)
+    near, far = (ost.key_weights(q, k, lse, causal=False, seq_lens=sl, block_table=table + at)
+                 for at in (0, total - 8))
+    L = total * page // 64 * 64                      # [1, 2, L, d], past 2^32 bytes too
+    flat = k.view(-1)[:Hkv * L * d].view(1, Hkv, L, d)
+    flat[0, 1, -1000:] = random_like_shape((1000, d), torch.bfloat16, 3).to(DEV)
+    w = ost.key_weights(q[:1], flat, lse[:1], causal=False)
+    torch.cuda.synchronize()
+    assert ost.attn_sync_status() == 0
+    assert torch.equal(near, far) and bool((near != 0).any())
+    same = ost.key_weights(q[:1, 2:], flat[:, 1:, -1000:].contiguous(), lse[:1, 2:], causal=False)
+    # (2 T terms, added in another order where their rows are split over CTAs)
+    assert torch.allclose(w[:, 1:, -1000:], same, rtol=4 * T * 2.0 ** -24, atol=0)
+
+
+@pytest.mark.gpu
 def test_bad_lengths_and_pages_are_flagged_not_read(ost):
     k = random_like_shape((9, 1, 16, 64), torch.bfloat16, 1).to(DEV)
     q = random_like_shape((3, 2, 1, 64), torch.bfloat16, 2).to(DEV)

@@ -291,6 +291,22 @@ def test_gradient_through_attention(ost):
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits(ost):
+    """Rows past 2^32 bytes (2^31 elements) turn like the same rows alone."""
+    N, Hq, Hkv, d = 460000, 32, 5, 128
+    x = torch.zeros(1, N, Hq + Hkv, d, dtype=torch.bfloat16, device=DEV)
+    x[0, -64:] = random_like_shape((64, Hq + Hkv, d), torch.bfloat16, 1).to(DEV)
+    q, k = (y.transpose(1, 2) for y in (x[:, :, :Hq], x[:, :, Hq:]))
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    f = ost.rope_frequencies(d, device=DEV)
+    want = ost.rope(q[:, :, -64:], k[:, :, -64:], pos[-64:].contiguous(), f)
+    got = ost.rope(q, k, pos, f, out=(q, k))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][:, :, -64:], want[0]) and torch.equal(got[1][:, :, -64:], want[1])
+    assert not bool(x[0, :-64].any())
+
+
+@pytest.mark.gpu
 def test_stream_graph_and_binding_refusals(ost):
     w = _freq(64).to(DEV)
     x = random_like_shape((2, 4, 9, 64), torch.bfloat16, 12).to(DEV)
