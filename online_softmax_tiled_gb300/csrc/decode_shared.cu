@@ -30,11 +30,12 @@
 // unused rows may hold anything, and 0 · NaN is NaN).
 //
 // Measured (32 heads on 8, d = 128): 64 requests behind 8192 keys, 0 to 1024
-// of their own each, 16-key pages: 53 us, 168 MB of K and V, of which the own
+// of their own each, 16-key pages: 49 us, 168 MB of K and V, of which the own
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 96 to 107 us, 438 MB. Four requests behind 500 keys: 14 us, three launches.
+// 96 to 105 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
+// a CUDA graph, three launches.
 // Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
 // and 76, 128 rows 41 and 37.
 //
@@ -92,7 +93,7 @@ struct Bars {
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort;
-  int unit[3];               // prefix, first request, requests of this CTA's rows
+  int unit[4];               // prefix, first request, requests of this CTA's rows; keys
 };
 
 struct PrefixArgs {
@@ -179,11 +180,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   pdl_wait_primary();
   // This CTA's run of rows: warp 0 counts the runs of the prefixes in order.
   if (warp == 0) {
-    int seen = 0, p_of = -1, first_of = 0, n_of = 0;
+    int seen = 0, p_of = -1, first_of = 0, n_of = 0, len_of = 0;
     bool bad = false;
     for (int p0 = 0; p0 < a.n_prefix && p_of < 0; p0 += 32) {
-      int first = 0, last = 0;
-      if (p0 + lane < a.n_prefix) bad |= !group_of(a.prefix_start, p0 + lane, a.B, first, last);
+      int first = 0, last = 0, len = 0;
+      if (p0 + lane < a.n_prefix) {
+        len = a.prefix_lens[p0 + lane];
+        bad |= !group_of(a.prefix_start, p0 + lane, a.B, first, last);
+      }
       const int units = (last - first + per_unit - 1) / per_unit;
       int upto = units;
 #pragma unroll
@@ -198,6 +202,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         p_of = p0 + src;
         first_of = __shfl_sync(0xffffffffu, first + u * per_unit, src);
         n_of = min(per_unit, __shfl_sync(0xffffffffu, last, src) - first_of);
+        len_of = __shfl_sync(0xffffffffu, len, src);
       }
       seen += __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -206,6 +211,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       bars.unit[0] = p_of;
       bars.unit[1] = first_of;
       bars.unit[2] = n_of;
+      bars.unit[3] = len_of;
     }
   }
   tc::fence_before_sync();
@@ -223,7 +229,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   const int* table = nullptr;
   bool bad = false;
   if (p >= 0) {
-    const int len = a.prefix_lens[p];
+    const int len = bars.unit[3];
     if ((len < 0 || len > cap) && tid == 0) attn_flag_error(kErrBadIndex);
     const int n = checked_len(len, cap);
     key0 = min(n, int(blockIdx.x) * a.chunk);
@@ -590,7 +596,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 
 // One warp per output row: the prefix's partials [0, np) and the request's
 // own [s_own, s_own + no), each weighted by exp(m_t - m), fetched eight at a
-// time with independent loads.
+// time with independent loads. Latency is what it costs: everything that can
+// be known before the partials is, and m, l and o come in one round trip.
 struct SharedMergeArgs {
   const float* o_part;
   const float* m_part;
@@ -605,10 +612,10 @@ struct SharedMergeArgs {
 
 __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
   constexpr int kBatch = 8;
-  pdl_wait_primary();
-  pdl_launch_dependents();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= a.rows) return;
+  // (Lengths and starts may be read at once: the prefix kernel has waited for
+  // all that precedes the call before this grid could start.)
   const int b = row / a.Hq;
   int np = 0;
   for (int p0 = 0; p0 < a.n_prefix; p0 += 32) {
@@ -622,51 +629,58 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
     }
   }
   const int no = (checked_len(a.seq_lens[b], a.own_cap) + a.own_chunk - 1) / a.own_chunk;
-  const int nv = np + no;
+  const int nv = np + no, d4 = a.d / 4;                // (d4 is 16 or 32: a column per lane)
   auto slot = [&](int t) { return t < np ? t : t - np + a.s_own; };
   const float* mr = a.m_part + size_t(row) * a.stride;
   const float* lr = a.l_part + size_t(row) * a.stride;
-  float mx = -INFINITY;
-  for (int t = lane; t < nv; t += 32) mx = fmaxf(mx, mr[slot(t)]);
+  const float4* prow = reinterpret_cast<const float4*>(a.o_part + size_t(row) * a.stride * a.d);
+  // (a partial without mass may hold anything)
+  auto fetch = [&](float4 (&x)[kBatch], int t0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      x[u] = t0 + u < nv && lane < d4 ? prow[size_t(slot(t0 + u)) * d4 + lane]
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  // m and l of partials `lane`, and the first batch of o, in one round trip
+  const float m0 = lane < nv ? mr[slot(lane)] : -INFINITY;
+  const float l0 = lane < nv ? lr[slot(lane)] : 0.f;
+  float4 x[kBatch];
+  fetch(x, 0);
+  float mx = m0;
+  for (int t = lane + 32; t < nv; t += 32) mx = fmaxf(mx, mr[slot(t)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float l = 0.f;
-  if (mx != -INFINITY)
-    for (int t = lane; t < nv; t += 32) {
-      const float mt = mr[slot(t)];
-      if (mt != -INFINITY) l = fmaf(expf(mt - mx), lr[slot(t)], l);
-    }
+  const bool empty = mx == -INFINITY;
+  auto weight = [&](float m) { return m == -INFINITY ? 0.f : expf(m - mx); };
+  const float w0 = weight(m0);
+  float l = w0 != 0.f ? w0 * l0 : 0.f;
+  for (int t = lane + 32; t < nv; t += 32) {
+    const float w = weight(mr[slot(t)]);
+    if (w != 0.f) l = fmaf(w, lr[slot(t)], l);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  const bool empty = mx == -INFINITY;
-  const float inv = empty ? 0.f : 1.f / l;
-  const float4* prow = reinterpret_cast<const float4*>(a.o_part + size_t(row) * a.stride * a.d);
-  const int d4 = a.d / 4;
-  for (int c4 = lane; c4 < d4; c4 += 32) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!empty)
-      for (int t0 = 0; t0 < nv; t0 += kBatch) {
-        float4 x[kBatch];
-        float w[kBatch];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t0 = 0; t0 < nv; t0 += kBatch) {
+    if (t0 > 0) fetch(x, t0);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int t = t0 + u;
-          const float mt = t < nv ? mr[slot(t)] : -INFINITY;
-          w[u] = mt == -INFINITY ? 0.f : expf(mt - mx);
-          x[u] = w[u] != 0.f ? prow[size_t(slot(t)) * d4 + c4] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          acc.x = fmaf(w[u], x[u].x, acc.x);
-          acc.y = fmaf(w[u], x[u].y, acc.y);
-          acc.z = fmaf(w[u], x[u].z, acc.z);
-          acc.w = fmaf(w[u], x[u].w, acc.w);
-        }
-      }
-    uint2 w2 = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                          pack_bf16x2(acc.z * inv, acc.w * inv));
-    reinterpret_cast<uint2*>(a.o + size_t(row) * a.d)[c4] = w2;
+    for (int u = 0; u < kBatch; ++u) {
+      const int t = t0 + u;
+      const float ws = __shfl_sync(0xffffffffu, w0, t & 31);
+      const float w = t < 32 ? ws : t < nv ? weight(mr[slot(t)]) : 0.f;
+      if (w == 0.f) continue;
+      acc.x = fmaf(w, x[u].x, acc.x);
+      acc.y = fmaf(w, x[u].y, acc.y);
+      acc.z = fmaf(w, x[u].z, acc.z);
+      acc.w = fmaf(w, x[u].w, acc.w);
+    }
   }
+  const float inv = empty ? 0.f : 1.f / l;
+  if (lane < d4)
+    reinterpret_cast<uint2*>(a.o + size_t(row) * a.d)[lane] = make_uint2(
+        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (a.lse != nullptr && lane == 0) a.lse[row] = empty ? -INFINITY : mx + logf(l);
 }
 
