@@ -23,11 +23,12 @@
 // flight.
 //
 // Measured: 64 rows of 32768 scores, 4096 kept of d = 128 in bf16, 16-key
-// pages: 59.6 us, of which the moving of the rows takes 40 (268 MB read and
+// pages: 59.3 us, of which the moving of the rows takes 40 (268 MB read and
 // written, 6.6 TB/s) and the selection the rest: 4 to load the scores, 2 a
 // pass, a barrier of the cluster between each, 3 to write the indices; none of
 // it near a limit, all of it latency. With two CTAs a row; four or eight were
-// slower (they share SMs). 6 rows of 1000, 128 kept: 10.2 us.
+// slower (they share SMs). 6 rows of 1000, 128 kept: 8.8 us, 8.1
+// in a CUDA graph.
 
 #include <cooperative_groups.h>
 
@@ -90,14 +91,24 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
                     int* __restrict__ new_lens, int Hkv, int score_len, int cap, int cap_out,
                     int n_keep, int n_sink, int n_recent) {
   __shared__ SelectSmem sm;
-  pdl_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), r = int(cluster.block_rank());
   const int row = blockIdx.x / C, b = row / Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
     reinterpret_cast<int4*>(sm.hist)[i] = make_int4(0, 0, 0, 0);
+  // (the gathering kernel's start may rely on this wait: it reads the lengths
+  // before it waits for this kernel)
   pdl_wait_primary();
+  pdl_launch_dependents();
+  // A barrier over the row's CTAs; a cluster's takes 600 to 1000 cycles, a
+  // single CTA's own a few dozen.
+  auto row_sync = [&] {
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
 
   bool bad = false;
   const int n = length_of(seq_lens, b, cap, bad);
@@ -184,7 +195,7 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
           if (pass == 0 || key[u] >> above_bits == bar >> above_bits)
             atomicAdd(&hist[(key[u] >> shift) & digits], 1);
       });
-      cluster.sync();
+      row_sync();
       // Thread t owns bins 4t .. 4t + 3 of the cluster's sum (the CTAs'
       // counts as independent 16-byte reads).
       int4 part[kMaxCluster];
@@ -249,7 +260,7 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
     sm.sure[warp] = n_sure;
     sm.equal[warp] = n_equal;
   }
-  cluster.sync();
+  row_sync();
   // How many before this segment: in the warps of the CTAs before this one,
   // then the warps before this one.
   int s0 = 0, e0 = 0;
@@ -291,7 +302,7 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
     });
   }
   // no CTA leaves while another may still read its counts
-  cluster.sync();
+  if (C > 1) cluster.sync();
 }
 
 struct GatherArgs {
@@ -311,11 +322,11 @@ struct GatherArgs {
 template <int kPieces>
 __global__ void __launch_bounds__(256) evict_gather_kernel(GatherArgs a) {
   constexpr int U = 4, kRows = 256 / kPieces;
-  pdl_launch_dependents();
-  pdl_wait_primary();
   const int row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
   bool bad = false;
   const int m = min(length_of(a.seq_lens, b, a.len_cap, bad), a.n_keep);
+  pdl_wait_primary();
+  pdl_launch_dependents();
   const int piece = threadIdx.x % kPieces;
   const int i0 = blockIdx.x * kRows * U + threadIdx.x / kPieces;
   const int* idx = a.kept + size_t(row) * a.n_keep;
