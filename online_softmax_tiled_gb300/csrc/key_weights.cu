@@ -33,13 +33,13 @@
 //    keys left out. A persistent CTA takes an equal share of all (256 keys,
 //    128 rows) steps; where a block of keys falls to several CTAs, their
 //    partial sums are added in a fixed order by a second kernel. Measured:
-//    4096 tokens and keys, causal, 16 heads on 4: 45.5 us, 755 TFLOP/s of the
+//    4096 tokens and keys, causal, 16 heads on 4: 42 us, 818 TFLOP/s of the
 //    visible half, exponentials at 0.4 of the special-function unit's rate and
 //    the tensor core as busy.
 //
 // Both forms at 256 rows (2 x 8 heads of 16384 keys): 22.5 us with the rows
 // kept, 37 with the keys kept. Past 256 rows the kept rows and a ring of K do
-// not fit in shared memory: 272 rows take 46 us.
+// not fit in shared memory: 260 rows take 45 us, 512 take 49.
 //
 // Sums are float32; every wait is bounded, as in the other kernels.
 
@@ -81,6 +81,10 @@ ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
   return wrong ? 0 : n;
 }
 
+// (a 64-bit division takes several hundred cycles)
+ATTN_DEVINL long long quotient(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : uint32_t(x) / uint32_t(y);
+}
 // Where the copies of a key tile come from: lane i < boxes has the tile's i-th
 // box. The page index is only looked at when the copies are issued, one tile
 // later, so that reading it holds nothing up.
@@ -453,8 +457,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
       if (w < warp) before += bars.warp_sum[w];
       total += bars.warp_sum[w];
     }
-    const int first = int(1LL * total * blockIdx.x / gridDim.x);
-    const int last = int(1LL * total * (blockIdx.x + 1) / gridDim.x);
+    const int first = int(quotient(1LL * total * blockIdx.x, gridDim.x));
+    const int last = int(quotient(1LL * total * (blockIdx.x + 1), gridDim.x));
     if (tid == 0) bars.count = last - first;
     if (first < last && before <= first && first < before + mine) {
       int at = before;
@@ -670,7 +674,8 @@ RowSteps row_steps(int R, int T, bool per_head) {
 }
 // A strip per head leaves out half the steps of its last T keys, but pays for
 // every head's short last chunk: T = 4096 tokens and keys take half the steps,
-// 192 tokens of four heads over 2 x 16384 keys 8 instead of 6 (108 us against 65).
+// 192 tokens of four heads over 2 x 16384 keys 8 instead of 6 (108 us against
+// 65 when both were measured).
 RowSteps row_steps_for(int R, int T, int causal, int cap) {
   const RowSteps head = row_steps(R, T, true), one = row_steps(R, T, false);
   const double hidden = 0.5 * std::min(T, cap) / cap;
@@ -686,14 +691,24 @@ ATTN_DEVINL int first_chunk(const KwArgs& a, const RowSteps& rs, int n, int k) {
 ATTN_DEVINL int steps_of(const KwArgs& a, const RowSteps& rs, int n, int k) {
   return rs.strips * (rs.chunks - first_chunk(a, rs, n, k));
 }
+// The steps of a head's first k blocks. Block i leaves out max(0, 2 i - c)
+// chunks of a strip, c = ceil((n - T) / 128): an arithmetic series from the
+// first i with 2 i > c on.
+ATTN_DEVINL long long steps_before(const KwArgs& a, const RowSteps& rs, int n, int k) {
+  long long s = 1LL * k * rs.chunks;
+  if (rs.skip) {
+    const int m = n - a.T, c = m >= 0 ? (m + kChunk - 1) / kChunk : -(-m / kChunk);
+    const int from = c >= 0 ? c / 2 + 1 : 0;
+    if (k > from) s -= 1LL * (k - from) * (k - 1 + from - c);
+  }
+  return s * rs.strips;
+}
 ATTN_DEVINL long long steps_of_head(const KwArgs& a, const RowSteps& rs, int n) {
-  long long s = 0;
-  for (int k = 0; k < blocks_of(n); ++k) s += steps_of(a, rs, n, k);
-  return s;
+  return steps_before(a, rs, n, blocks_of(n));
 }
 // Steps per CTA: an equal share, `least` at least.
 ATTN_DEVINL long long steps_per_cta(const RowSteps& rs, long long total, int grid) {
-  const long long share = (total + grid - 1) / grid;
+  const long long share = quotient(total + grid - 1, grid);
   return share > rs.least ? share : rs.least;
 }
 
@@ -759,7 +774,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k, KwArgs a, RowSteps rs) {
   using C = RowsCfg<D>;
-  pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -794,6 +808,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   fill_parts(smem + C::kOnesOff, smem + C::kPartsOff, C::kStages * C::kPartsBytes, tid);
   pdl_wait_primary();
+  pdl_launch_dependents();
   // This CTA's share of all steps: thread t counts a run of requests, a scan
   // over the threads gives where each run begins.
   {
@@ -829,14 +844,20 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         const int n = request_len(a, b, bad);
         const long long head = steps_of_head(a, rs, n);
         if (begin < at + head * a.Hkv) {
-          const int g = int((begin - at) / head);
-          long long rest = (begin - at) % head;
-          int k = 0;
-          for (; rest >= steps_of(a, rs, n, k); ++k) rest -= steps_of(a, rs, n, k);
+          const int g = int(quotient(begin - at, head));
+          const long long rest = begin - at - g * head;
+          int k = 0, over = blocks_of(n);                // the last block that begins at or before
+          while (over - k > 1) {
+            const int mid = (k + over) / 2;
+            if (steps_before(a, rs, n, mid) <= rest)
+              k = mid;
+            else
+              over = mid;
+          }
           bars.start[0] = b;
           bars.start[1] = g;
           bars.start[2] = k;
-          bars.offset = int(rest);
+          bars.offset = int(rest - steps_before(a, rs, n, k));
           break;
         }
         at += head * a.Hkv;
@@ -1028,7 +1049,7 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         write_key(a, at, out, sum);
       } else {
         // the CTA's place among those of the block
-        const int slot = int(blockIdx.x - (at_step - w.step0) / bars.each);
+        const int slot = int(blockIdx.x) - int(quotient(at_step - w.step0, bars.each));
         a.part[size_t(slot) * a.B * a.Hkv * a.out_len + at] = page_good(a, out) ? sum : 0.f;
       }
       at_step += w.steps;
@@ -1052,8 +1073,6 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
 __global__ void __launch_bounds__(kBlock)
 weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
   __shared__ long long sums[2][kBlock / 32];
-  pdl_wait_primary();
-  pdl_launch_dependents();
   const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv, k = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
@@ -1080,13 +1099,15 @@ weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
     before += sums[1][w];
   }
   const int n = request_len(a, b, bad), j = k * kBlock + tid;
-  if (j >= n) return;
-  long long first = before + g * steps_of_head(a, rs, n);
-  for (int i = 0; i < k; ++i) first += steps_of(a, rs, n, i);
+  const long long first = before + g * steps_of_head(a, rs, n) + steps_before(a, rs, n, k);
   const long long each = steps_per_cta(rs, total, grid);
   const long long last = first + steps_of(a, rs, n, k) - 1;
-  const int slots = int(last / each - first / each) + 1;
-  if (slots == 1) return;                                // written where it was summed
+  const int slots = int(quotient(last, each) - quotient(first, each)) + 1;
+  // (Lengths may be read before: the kernel that made the sums lets this one
+  // start only once all that precedes the call is complete.)
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (j >= n || slots == 1) return;                      // (one: written where it was summed)
   const size_t at = size_t(blockIdx.y) * a.out_len + j, step = size_t(gridDim.y) * a.out_len;
   float sum = 0.f;
 #pragma unroll 4
