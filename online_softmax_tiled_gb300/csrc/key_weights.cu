@@ -23,7 +23,7 @@
 //    in tiles of 128, which the two warpgroups take in turn. One persistent
 //    CTA per SM takes an equal share of all key tiles of the batch. Measured:
 //    one token of 64 requests (4 rows a KV head, 8 KV heads, 2048 to 4096 keys
-//    of 128 in 16-key pages) 76 us, 5.4 TB/s, bound by reading K; 64 tokens
+//    of 128 in 16-key pages) 72 us, 5.8 TB/s, bound by reading K; 64 tokens
 //    over 2 x 16384 keys (256 rows) 22.5 us, 764 TFLOP/s, where a warpgroup
 //    takes 2 x 1400 cycles to load and sum a tile's 256 columns and then waits
 //    for its next product, 1500 to 1900 cycles from issue to use.
@@ -85,6 +85,7 @@ ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
 ATTN_DEVINL long long quotient(long long x, long long y) {
   return (x | y) >> 32 ? x / y : uint32_t(x) / uint32_t(y);
 }
+
 // Where the copies of a key tile come from: lane i < boxes has the tile's i-th
 // box. The page index is only looked at when the copies are issued, one tile
 // later, so that reading it holds nothing up.
@@ -93,7 +94,8 @@ struct KeyBox {
   bool in;
 };
 ATTN_DEVINL KeyBox find_key_box(const KwArgs& a, int b, int g, int key0, int n, int lane) {
-  KeyBox x{0, 0, 0, lane < min(kTileKeys / a.box_rows, (n - key0 + a.box_rows - 1) / a.box_rows)};
+  const int shift = 31 - __clz(a.box_rows);            // box_rows is a power of two
+  KeyBox x{0, 0, 0, lane < min(kTileKeys, n - key0 + a.box_rows - 1) >> shift};
   if (x.in) {
     const int key = key0 + lane * a.box_rows;
     if (a.block_table == nullptr) {
@@ -901,21 +903,27 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (the whole warp)
     bool ok = true;
-    int i = 0, pieces = 0;
+    int i = 0, pieces = 0;                               // chunks and blocks asked for
     for (; w.left > 0 && ok; w.next(a, rs)) {
-      if (pieces > 0) ok = mbar_wait_warp(&bars.k_empty, (pieces - 1) & 1, abort_flag);
-      if (!ok) break;
-      for (int t = 0; t < 2; ++t) {
-        const int key = w.k * kBlock + t * kTileKeys;
-        if (key < w.n)
-          load_key_tile<D>(a, find_key_box(a, w.b, w.g, key, w.n, lane), smem + t * C::kTileBytes,
-                           &map_k, &bars.k_full, lane);
-        else if (lane == 0)
-          mbar_arrive(&bars.k_full);
-      }
-      ++pieces;
+      KeyBox box[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        box[t] = find_key_box(a, w.b, w.g, w.k * kBlock + t * kTileKeys, w.n, lane);
       Step x = step_at(w.step0);
-      for (int s = 0; s < w.steps; ++s, ++i, advance(x)) {
+      for (int s = 0; s < w.steps && ok; ++s, ++i, advance(x)) {
+        // The keys of the block before leave when its last products are done:
+        // meanwhile the first chunks of this one are on their way.
+        if (s == min(w.steps, C::kStages - 1) - 1) {
+          if (pieces > 0) ok = mbar_wait_warp(&bars.k_empty, (pieces - 1) & 1, abort_flag);
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (w.k * kBlock + t * kTileKeys < w.n)
+              load_key_tile<D>(a, box[t], smem + t * C::kTileBytes, &map_k, &bars.k_full, lane);
+            else if (lane == 0)
+              mbar_arrive(&bars.k_full);
+          ++pieces;
+        }
         const int st = i % C::kStages;
         if (i >= C::kStages)
           ok = mbar_wait_warp(&bars.q_empty[st], (i / C::kStages - 1) & 1, abort_flag);
@@ -929,7 +937,6 @@ weights_rows_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         __syncwarp();
       }
-      if (!ok) break;
     }
     if (!ok) {
       if (lane == 0) attn_flag_error(kErrTimeout);
