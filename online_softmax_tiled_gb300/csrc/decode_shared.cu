@@ -24,20 +24,23 @@
 //   otherwise: both hold the same 128 rows and take alternate key tiles, so
 //     one's softmax overlaps the other's products and a third stage of K and
 //     V is loading; they are merged at the end through shared memory.
-// Key tiles come from pages by one TMA copy per page piece: 128 rows, or the
-// largest power of two that divides the page size. Value rows past the
+// Key tiles come from pages by one TMA copy per page piece (128 rows, or the
+// largest power of two that divides the page size) that takes whole rows: a
+// copy costs about 100 cycles to issue, and 16-key pages need eight a tile as
+// it is. Value rows past the
 // prefix's end are zeroed in shared memory before the product (a page's
 // unused rows may hold anything, and 0 · NaN is NaN).
 //
 // Measured (32 heads on 8, d = 128): 64 requests behind 8192 keys, 0 to 1024
-// of their own each, 16-key pages: 49 us, 168 MB of K and V, of which the own
+// of their own each, 16-key pages: 49 to 52 us, 168 MB of K and V, of which the own
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 96 to 105 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
+// 93 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
 // a CUDA graph, three launches.
 // Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
-// and 76, 128 rows 41 and 37.
+// and 76, 128 rows 41 and 37 (with copies of half rows, 4 us more at 16-key
+// pages).
 //
 // Order. The three kernels of a call are launched as programmatic
 // dependents. The prefix kernel lets the split kernel start once what
@@ -104,6 +107,7 @@ struct PrefixArgs {
   float* m_part;
   float* l_part;
   int B, Hq, Hkv, G, n_prefix, num_pages, page_size, max_pages, box_rows, chunk, stride;
+  int joined;                // copies that take both 64-column halves of a row
   float scale;
 };
 
@@ -248,6 +252,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   bad = __syncthreads_or(bad);
   const int nj = bad ? 0 : (n_keys + kBN - 1) / kBN;      // key tiles
   const int rows = n_req * a.G;                            // valid query rows
+  // A key tile in shared memory: bytes from 8 keys to the next, and from one
+  // 64-column half to the other.
+  const uint32_t group = a.joined ? 1024 * C::kAtoms : 1024;
+  const uint32_t half = a.joined ? 1024 : kBN * 128;
   // tiles of warpgroup t: all (kPair; none without rows), or every other one
   const int n_t[2] = {kPair ? (rows > 0 ? nj : 0) : (nj + 1) / 2,
                       kPair ? (rows > kBM ? nj : 0) : nj / 2};
@@ -273,19 +281,24 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                             b0 + t * (kBM / a.G), &bars.q_full);
       }
       const int boxes = kBN / a.box_rows;
-      // one copy per (box, atom); boxes past the chunk's keys are not read
+      // one copy per box, or per (box, half); boxes past the chunk's keys are not read
       auto load = [&](uint8_t* dst, const CUtensorMap* map, int j, uint64_t* bar) {
         const int here = min(boxes, (n_keys - j * kBN + a.box_rows - 1) / a.box_rows);
         if (lane == 0)
           mbar_arrive_expect_tx(bar, uint32_t(here) * a.box_rows * 128 * C::kAtoms);
         __syncwarp();
-        for (int i = lane; i < here * C::kAtoms; i += 32) {
-          const int box = i / C::kAtoms, at = i % C::kAtoms;
+        const int copies = a.joined ? 1 : C::kAtoms;       // of a box
+        for (int i = lane; i < here * copies; i += 32) {
+          const int box = i / copies, at = i % copies;
           const int key = key0 + j * kBN + box * a.box_rows;
           const int pi = key / a.page_size;
           const int page = pi - page0 < kPagesCached ? pages[pi - page0] : table[pi];
-          tc::tma_load_3d(dst + at * (kBN * 128) + box * a.box_rows * 128, map, 64 * at,
-                          key - pi * a.page_size, page * a.Hkv + g, bar);
+          if (a.joined)
+            tc::tma_load_5d(dst + box * a.box_rows * 128 * C::kAtoms, map, 0, 0, 0,
+                            (key - pi * a.page_size) / 8, page * a.Hkv + g, bar);
+          else
+            tc::tma_load_3d(dst + at * (kBN * 128) + box * a.box_rows * 128, map, 64 * at,
+                            key - pi * a.page_size, page * a.Hkv + g, bar);
         }
       };
       int issued_k = 0, issued_v = 0;
@@ -327,10 +340,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const uint32_t ka = k_base + (j % C::kStages) * C::kTileBytes;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kBM * 128) + (kk % 4) * 32;
           tc::mma_ss_warp(tmem + C::kColS + t * kBN,
-                          tc::smem_desc(qa + off, 16, 1024, tc::kLayoutSW128),
-                          tc::smem_desc(ka + off, 16, 1024, tc::kLayoutSW128), idesc_s, kk > 0);
+                          tc::smem_desc(qa + (kk / 4) * (kBM * 128) + (kk % 4) * 32, 16, 1024,
+                                        tc::kLayoutSW128),
+                          tc::smem_desc(ka + (kk / 4) * half + (kk % 4) * 32, 16, group,
+                                        tc::kLayoutSW128),
+                          idesc_s, kk > 0);
         }
         tc::mma_commit_warp(&bars.s_full[t]);
       };
@@ -339,7 +354,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           tc::mma_ts_warp(tmem + C::kColO + t * D, tmem + C::kColS + t * kBN + kk * 8,
-                          tc::smem_desc(va + kk * 2048, kBN * 128, 1024, tc::kLayoutSW128),
+                          tc::smem_desc(va + kk * 2 * group, half, group, tc::kLayoutSW128),
                           idesc_o, (!first || kk > 0) ? 1u : 0u);
         tc::mma_commit_warp(&bars.o_done[t]);
       };
@@ -497,12 +512,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ok = mbar_wait_warp(&bars.v_full[j % C::kStages], (j / C::kStages) & 1, abort_flag);
         if (!ok) break;
         if (r >= valid) {
-          uint8_t* vt = smem + C::kVOff + (j % C::kStages) * C::kTileBytes + r * 128;
+          uint8_t* vt = smem + C::kVOff + (j % C::kStages) * C::kTileBytes + (r / 8) * group +
+                        r % 8 * 128;
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(vt + at * (kBN * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(vt + at * half + e * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
@@ -704,9 +720,14 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
   const int G = a.own.Hq / a.own.Hkv;
   const uint64_t outer = uint64_t(a.num_prefix_pages) * a.own.Hkv;
   CUtensorMap mq, mk, mv;
-  if (!make_map_q(&mq, a.own.q, a.own.B, a.own.Hq, D, G) ||
-      !make_map_bf16_3d(&mk, a.k_prefix, D, a.prefix_page_size, outer, pl.box_rows) ||
-      !make_map_bf16_3d(&mv, a.v_prefix, D, a.prefix_page_size, outer, pl.box_rows))
+  // (pages have a multiple of 8 rows where a table row has more than one)
+  const bool joined = a.max_prefix_pages > 1;
+  auto map = [&](CUtensorMap* m, const void* base) {
+    return joined ? make_map_bf16_joined(m, base, D, a.prefix_page_size, outer, pl.box_rows)
+                  : make_map_bf16_3d(m, base, D, a.prefix_page_size, outer, pl.box_rows);
+  };
+  if (!make_map_q(&mq, a.own.q, a.own.B, a.own.Hq, D, G) || !map(&mk, a.k_prefix) ||
+      !map(&mv, a.v_prefix))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D, kPair>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynSmem);
@@ -714,7 +735,7 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
   const PrefixArgs pa{a.prefix_table, a.prefix_lens, a.prefix_start, a.own.o_part, a.own.m_part,
                       a.own.l_part, a.own.B, a.own.Hq, a.own.Hkv, G, a.n_prefix,
                       a.num_prefix_pages, a.prefix_page_size, a.max_prefix_pages, pl.box_rows,
-                      pl.prefix_chunk, pl.prefix_splits + pl.own_splits, a.own.scale};
+                      pl.prefix_chunk, pl.prefix_splits + pl.own_splits, joined, a.own.scale};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.prefix_splits, a.own.Hkv, pl.units);
   cfg.blockDim = dim3(kThreads);
@@ -746,13 +767,13 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
   const long long tiles = (cap + kBN - 1) / kBN;
   const long long own_cap = 1LL * page_size * max_pages;
   if (own_splits <= 0) {
-    // One round of the split kernel's three CTAs per SM, or a split per 512
-    // keys of capacity, four at most, where that is more, but 128 keys a split
-    // at least (64 requests of up to 1024 keys: 60, 55, 57, 65 us with 1, 2,
-    // 4, 8 splits; 128 of up to 8192: 481, 410, 361, 362).
+    // A split per 512 keys of capacity, as many as make one round of the split
+    // kernel's three CTAs per SM, or four where that is more (64 requests of up
+    // to 1024 keys: 57, 52, 52, 58 us with 1, 2, 4, 8 splits; 128 of up to
+    // 8192: 481, 410, 361, 362; 16 of up to 400, 64 heads: 21.4 and 25.8 with
+    // 1 and 4).
     const long long want = (3 * sms + 1LL * B * Hkv - 1) / (1LL * B * Hkv);
-    const long long chunks = std::min(4LL, (own_cap + 511) / 512);
-    own_splits = int(std::max(1LL, std::min(std::max(want, chunks), (own_cap + 127) / 128)));
+    own_splits = int(std::min((own_cap + 511) / 512, std::max(4LL, want)));
   }
   if (prefix_splits <= 0) {
     // Both parts run at once, so a call takes as long as a prefix CTA, or as
@@ -761,8 +782,8 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
     // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
     // its partial rows; own keys, half their capacity but 512 at most (the
     // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
-    // partials for every split to merge. (64 requests behind 8192 keys: 80, 55,
-    // 59, 69 us with 2, 4, 8, 19 splits, 19 filling the device.)
+    // partials for every split to merge. (64 requests behind 8192 keys: 71, 52,
+    // 56 us with 2, 4, 8 splits, 69 with 19, which fill the device.)
     const double tile = (pl.pair ? 2.3 : 1.2) * d / 128, tiles_all = double(tiles);
     const double ctas = double(Hkv) * std::max<long long>(n_prefix, (rows + per - 1) / per);
     const double own = 1.0 * B * Hkv * std::min(own_cap / 2, 512LL) * d * 4 / 3e6;

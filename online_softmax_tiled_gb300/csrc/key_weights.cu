@@ -69,7 +69,7 @@ struct KwArgs {
   const int* seq_lens;
   const int* block_table;
   int B, Hkv, R, T, cap, out_len, num_pages, page_size, max_pages, box_rows;
-  int causal, joined;      // joined: key tiles by make_map_joined's copies
+  int causal, joined;      // joined: key tiles by make_map_bf16_joined's copies
   float c, inv_scale, decay;   // scale · log2 e, 1 / scale
 };
 
@@ -123,16 +123,6 @@ template <int D> ATTN_DEVINL KeySteps key_steps(const KwArgs& a) {
   return a.joined ? KeySteps{1024 * (D / 64), 1024} : KeySteps{1024, kTileKeys * 128};
 }
 
-ATTN_DEVINL void tma_load_5d(void* smem_dst, const CUtensorMap* map, int c3, int c4,
-                             uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
-      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4),
-        "r"(smem_u32(bar))
-      : "memory");
-}
-
 // The copies of a tile (all lanes of a converged warp); boxes past the
 // request's keys or behind a bad page index are left out (their lanes' sums
 // are not used).
@@ -148,7 +138,7 @@ ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
   const int outer = x.page * a.Hkv + x.outer;
   if (good) {
     if (a.joined) {
-      tma_load_5d(dst + lane * a.box_rows * 128 * kAtoms, map, x.row / 8, outer, bar);
+      tc::tma_load_5d(dst + lane * a.box_rows * 128 * kAtoms, map, 0, 0, 0, x.row / 8, outer, bar);
     } else {
 #pragma unroll
       for (int at = 0; at < kAtoms; ++at)
@@ -156,22 +146,6 @@ ATTN_DEVINL void load_key_tile(const KwArgs& a, const KeyBox& x, uint8_t* dst,
                         x.row, outer, bar);
     }
   }
-}
-
-// The map of joined copies: K as [outer][row / 8][half][row % 8][64], boxes of
-// box_rows rows.
-bool make_map_joined(CUtensorMap* m, const void* base, int d, int rows, uint64_t outer,
-                     int box_rows) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  const cuuint64_t row = cuuint64_t(d) * 2;
-  const cuuint64_t dims[5] = {64, 8, cuuint64_t(d / 64), cuuint64_t(rows / 8), outer};
-  const cuuint64_t strides[4] = {row, 128, 8 * row, rows * row};
-  const cuuint32_t box[5] = {64, 8, cuuint32_t(d / 64), cuuint32_t(box_rows / 8), 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What a row needs besides Q: -lse/scale as three bf16 parts whose sum is the
@@ -1156,7 +1130,7 @@ cudaError_t launch_d(const KeyWeightsArgs& w, KwArgs a) {
   CUtensorMap mk, mq;
   const bool paged = w.block_table != nullptr;
   const uint64_t outer = uint64_t(paged ? w.num_pages : w.B) * w.Hkv;
-  if (!(a.joined ? make_map_joined(&mk, w.k, D, w.page_size, outer, a.box_rows)
+  if (!(a.joined ? make_map_bf16_joined(&mk, w.k, D, w.page_size, outer, a.box_rows)
                  : make_map_bf16_3d(&mk, w.k, D, paged ? w.page_size : w.L, outer, a.box_rows)))
     return cudaErrorInvalidValue;
   // Up to 128 rows there is room for those of the next (request, head) too:

@@ -63,6 +63,24 @@ inline bool make_map_f32_3d(CUtensorMap* m, const void* base, uint64_t cols, uin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map over a bf16 tensor [outer][rows][cols] (cols 64 or 128, contiguous,
+// rows a multiple of 8) for copies that take whole rows: viewed as
+// [outer][row / 8][64-column half][row % 8][64], boxes of box_rows rows (a
+// multiple of 8), 128-byte swizzle. A box lands as 1024-byte pieces of 8 rows
+// x 64 columns, the halves of 8 rows next to each other.
+inline bool make_map_bf16_joined(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                                 uint64_t outer, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[5] = {64, 8, cols / 64, rows / 8, outer};
+  const cuuint64_t strides[4] = {cols * 2, 128, cols * 16, rows * cols * 2};
+  const cuuint32_t box[5] = {64, 8, cuuint32_t(cols / 64), box_rows / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Map over a bf16 tensor viewed as [rows][cols] (cols contiguous) for
 // row gathers (tile::gather4): box = (cols, 1), no swizzle, so four gathered
 // rows land as a plain row-major block. cols * 2 bytes must be a multiple of
