@@ -32,11 +32,11 @@
 // unused rows may hold anything, and 0 · NaN is NaN).
 //
 // Measured (32 heads on 8, d = 128): 64 requests behind 8192 keys, 0 to 1024
-// of their own each, 16-key pages: 49 to 52 us, 168 MB of K and V, of which the own
+// of their own each, 16-key pages: 49 to 51 us, 168 MB of K and V, of which the own
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 93 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
+// 92 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
 // a CUDA graph, three launches.
 // Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
 // and 76, 128 rows 41 and 37 (with copies of half rows, 4 us more at 16-key
@@ -280,25 +280,31 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tc::tma_load_3d(smem + t * C::kTileBytes + at * (kBM * 128), &map_q, 64 * at, g * a.G,
                             b0 + t * (kBM / a.G), &bars.q_full);
       }
-      const int boxes = kBN / a.box_rows;
-      // one copy per box, or per (box, half); boxes past the chunk's keys are not read
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, int j, uint64_t* bar) {
-        const int here = min(boxes, (n_keys - j * kBN + a.box_rows - 1) / a.box_rows);
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar, uint32_t(here) * a.box_rows * 128 * C::kAtoms);
+      // Lane i < here issues the copies of the tile's i-th box, for K and V
+      // alike; boxes past the chunk's keys are not read. (A single page comes
+      // as one box, in halves.)
+      const int shift = 31 - __clz(a.box_rows);            // box_rows is a power of two
+      int here = 0, row = 0, outer = 0;
+      auto look_up = [&](int j) {
+        const int at = j * kBN + lane * a.box_rows;
+        here = min(kBN, n_keys - j * kBN + a.box_rows - 1) >> shift;
+        if (lane < here) {
+          const int pi = (key0 + at) / a.page_size;
+          row = key0 + at - pi * a.page_size;
+          outer = (pi - page0 < kPagesCached ? pages[pi - page0] : table[pi]) * a.Hkv + g;
+        }
+      };
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(here) * a.box_rows * 128 * C::kAtoms);
         __syncwarp();
-        const int copies = a.joined ? 1 : C::kAtoms;       // of a box
-        for (int i = lane; i < here * copies; i += 32) {
-          const int box = i / copies, at = i % copies;
-          const int key = key0 + j * kBN + box * a.box_rows;
-          const int pi = key / a.page_size;
-          const int page = pi - page0 < kPagesCached ? pages[pi - page0] : table[pi];
+        if (lane < here) {
           if (a.joined)
-            tc::tma_load_5d(dst + box * a.box_rows * 128 * C::kAtoms, map, 0, 0, 0,
-                            (key - pi * a.page_size) / 8, page * a.Hkv + g, bar);
+            tc::tma_load_5d(dst + lane * a.box_rows * 128 * C::kAtoms, map, 0, 0, 0, row / 8, outer,
+                            bar);
           else
-            tc::tma_load_3d(dst + at * (kBN * 128) + box * a.box_rows * 128, map, 64 * at,
-                            key - pi * a.page_size, page * a.Hkv + g, bar);
+#pragma unroll
+            for (int at = 0; at < C::kAtoms; ++at)
+              tc::tma_load_3d(dst + at * (kBN * 128), map, 64 * at, row, outer, bar);
         }
       };
       int issued_k = 0, issued_v = 0;
@@ -306,13 +312,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       for (int j = 0; j < nj; ++j) {
         const int st = j % C::kStages;
         const uint32_t ph = (j / C::kStages) & 1;
+        look_up(j);
         if (j >= C::kStages) ok = mbar_wait_warp(&bars.k_empty[st], ph ^ 1, abort_flag);
         if (!ok) break;
-        load(smem + C::kKOff + st * C::kTileBytes, &map_k, j, &bars.k_full[st]);
+        load(smem + C::kKOff + st * C::kTileBytes, &map_k, &bars.k_full[st]);
         ++issued_k;
         if (j >= C::kStages) ok = mbar_wait_warp(&bars.v_empty[st], ph ^ 1, abort_flag);
         if (!ok) break;
-        load(smem + C::kVOff + st * C::kTileBytes, &map_v, j, &bars.v_full[st]);
+        load(smem + C::kVOff + st * C::kTileBytes, &map_v, &bars.v_full[st]);
         ++issued_v;
       }
       if (!ok) {
