@@ -73,7 +73,8 @@ def _calls_commands(obj: str, out: str):
                 "-isystem", os.path.join(cuda, "include"),
                 "-c", os.path.join(CSRC, "py_cache.cpp"), "-o", obj]
     link = [cxx, "-shared", obj, "-o", out, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-ltorch",
-            "-lc10", "-lc10_cuda", "-L" + LIB_DIR, "-l:" + os.path.basename(LIB_PATH),
+            "-ltorch_cuda", "-lc10", "-lc10_cuda",
+            "-L" + LIB_DIR, "-l:" + os.path.basename(LIB_PATH),
             "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
     return compile_, link
 

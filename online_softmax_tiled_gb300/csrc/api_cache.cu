@@ -1,6 +1,6 @@
-// C ABI entry points around the KV cache (decode behind shared
-// prefixes, rotary positions, key weights, eviction): argument validation and dispatch. Declarations and their documentation:
-// include/attn.h.
+// C ABI entry points around the KV cache (decode behind shared prefixes,
+// rotary positions, key weights, eviction): argument validation and dispatch.
+// Declarations and their documentation: include/attn.h.
 
 #include <stdint.h>
 

@@ -36,8 +36,7 @@
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 92 us, 438 MB. Four requests behind 500 keys: 14 us from Python, 11.8 in
-// a CUDA graph, three launches.
+// 92 us, 438 MB. Four requests behind 500 keys: 11.8 us, three launches.
 // Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
 // and 76, 128 rows 41 and 37 (with copies of half rows, 4 us more at 16-key
 // pages).
@@ -821,7 +820,8 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
 
 cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& pl) {
   const bool d64 = a.own.d == 64;
-  cudaError_t e = pl.pair ? (d64 ? launch_prefix_t<64, true>(a, pl) : launch_prefix_t<128, true>(a, pl))
+  cudaError_t e = pl.pair ? (d64 ? launch_prefix_t<64, true>(a, pl)
+                                 : launch_prefix_t<128, true>(a, pl))
                           : (d64 ? launch_prefix_t<64, false>(a, pl)
                                  : launch_prefix_t<128, false>(a, pl));
   if (e != cudaSuccess) return e;

@@ -559,7 +559,8 @@ weights_keys_kernel(const __grid_constant__ CUtensorMap map_q,
     for (int i = 0; i < count && ok; ++i) {
       if (fresh) {
         const int rb = heads & 1;
-        if (heads >= 2) ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
+        if (heads >= 2)
+          ok = mbar_wait_warp(&bars.row_empty[rb], ((heads >> 1) - 1) & 1, abort_flag);
         if (!ok) break;
         const bool dead = put_rows<NMAX / 32>(a, w.b * a.Hkv + w.g, 0, 0, a.R, N,
                                               smem + C::kPartsOff + rb * C::kPartsBytes,
@@ -1164,9 +1165,10 @@ int key_weights_slots(int R, int T) {
 }
 
 cudaError_t launch_key_weights(const KeyWeightsArgs& w) {
-  KwArgs a{w.lse, w.prev, w.out, w.part, w.seq_lens, w.block_table, w.B, w.Hkv, w.Hq / w.Hkv * w.T, w.T,
-           w.len_cap, w.out_len, w.num_pages, w.page_size, w.max_pages, kTileKeys, w.causal,
-           w.block_table != nullptr && w.max_pages > 1, w.scale * kLog2e, 1.f / w.scale, w.decay};
+  KwArgs a{w.lse, w.prev, w.out, w.part, w.seq_lens, w.block_table, w.B, w.Hkv,
+           w.Hq / w.Hkv * w.T, w.T, w.len_cap, w.out_len, w.num_pages, w.page_size, w.max_pages,
+           kTileKeys, w.causal, w.block_table != nullptr && w.max_pages > 1, w.scale * kLog2e,
+           1.f / w.scale, w.decay};
   // copies of a key tile: whole tiles of a contiguous cache or a single
   // page, else the largest power of two that divides the page size, both
   // 64-column halves in one copy (issuing a copy takes about 100 cycles: 99.7

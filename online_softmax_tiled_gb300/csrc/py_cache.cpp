@@ -10,9 +10,9 @@
 
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -112,6 +112,13 @@ struct Device {
   }
 };
 
+// A new contiguous tensor on the current device (straight from the allocator's
+// factory: the way through the dispatcher takes about as long again).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType dtype, const Device& dev) {
+  return at::Tensor(at::detail::empty_cuda(
+      sizes, dtype, c10::Device(c10::kCUDA, c10::DeviceIndex(dev.index)), std::nullopt));
+}
+
 attn_dtype dtype_of(const at::Tensor& t) {
   if (t.scalar_type() == at::kBFloat16) return ATTN_BF16;
   if (t.scalar_type() == at::kFloat) return ATTN_F32;
@@ -189,8 +196,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse_value("k and k_out go together");
     }
     if (!q_out) {
-      q_out = at::empty_like(q, at::MemoryFormat::Contiguous);
-      if (k && !k_out) k_out = at::empty_like(*k, at::MemoryFormat::Contiguous);
+      q_out = fresh(q.sizes(), q.scalar_type(), dev);
+      if (k && !k_out) k_out = fresh(k->sizes(), q.scalar_type(), dev);
     }
     if (k.has_value() != k_out.has_value()) refuse_value("k and k_out go together");
     for (const auto& p : {std::make_pair(&q, &q_out), std::make_pair(k ? &*k : nullptr, &k_out)}) {
@@ -250,27 +257,34 @@ PyObject* py_decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev.index)};
     const float scale = real(a[12]);
     const int sp = small_int(a[13]), so = small_int(a[14]);
+    c10::DataPtr own_ws;
+    size_t own_bytes = 0;
     if (truth(a[16])) {
-      o = at::empty_like(q);
-      lse = at::empty({B, Hq}, q.options().dtype(at::kFloat));
-      if (!ws)
-        ws = at::empty({int64_t(attn_decode_shared_workspace_size(
-                           B, Hq, Hkv, d, n_prefix, size(kp, 2), size(pt, 1), size(kk, 2),
-                           size(bt, 1), sp, so))},
-                       q.options().dtype(at::kByte));
+      o = fresh(q.sizes(), at::kBFloat16, dev);
+      lse = fresh({B, Hq}, at::kFloat, dev);
+      if (!ws) {
+        // (freed when the call returns, to be handed out again on its stream)
+        own_bytes = attn_decode_shared_workspace_size(B, Hq, Hkv, d, n_prefix, size(kp, 2),
+                                                      size(pt, 1), size(kk, 2), size(bt, 1), sp,
+                                                      so);
+        own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(own_bytes);
+      }
     }
-    if (!o || !ws) refuse_value("o and workspace are needed");
+    if (!o || (!ws && !truth(a[16]))) refuse_value("o and workspace are needed");
     if (!same_shape(*o, q) || (lse && (lse->dim() != 2 || lse->size(0) != B || lse->size(1) != Hq)))
       refuse_value("shapes do not go together (see attn_decode_shared)");
-    dev.on(*ws);
-    if (!ws->is_contiguous()) refuse_value("tensors must be contiguous");
+    if (ws) {
+      dev.on(*ws);
+      if (!ws->is_contiguous()) refuse_value("tensors must be contiguous");
+    }
     auto ints = [](const void* p) { return static_cast<const int*>(p); };
     check(attn_decode_shared(in[0], in[1], in[2], ints(in[3]), ints(in[4]), ints(in[5]), in[6],
                              in[7], ints(in[8]), ints(in[9]), dev.data(*o, at::kBFloat16),
                              static_cast<float*>(dev.data(lse, at::kFloat)), B, Hq, Hkv, d,
                              n_prefix, size(kp, 0), size(kp, 2), size(pt, 1), size(kk, 0),
-                             size(kk, 2), size(bt, 1), scale, sp, so, ws->data_ptr(),
-                             size_t(ws->nbytes()), dev.stream(a[17])),
+                             size(kk, 2), size(bt, 1), scale, sp, so,
+                             ws ? ws->data_ptr() : own_ws.get(),
+                             ws ? size_t(ws->nbytes()) : own_bytes, dev.stream(a[17])),
           "attn_decode_shared");
     return pair(*o, lse);
   });
@@ -298,8 +312,8 @@ PyObject* py_key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev.index)};
     const int64_t cap = bt ? int64_t(max_pages) * L : L;
     if (!out && allocate) {
-      const auto opts = k.options().dtype(at::kFloat);
-      out = sl ? at::zeros({B, Hkv, cap}, opts) : at::empty({B, Hkv, cap}, opts);
+      out = sl ? at::zeros({B, Hkv, cap}, k.options().dtype(at::kFloat))
+               : fresh({B, Hkv, cap}, at::kFloat, dev);
     }
     if (!out) refuse_value("out is needed");
     if (out->dim() != 3 || out->size(0) != B || out->size(1) != Hkv || k.size(3) != d ||
@@ -309,7 +323,7 @@ PyObject* py_key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int out_len = size(*out, 2);
     if (!ws && allocate && Hkv > 0 && int64_t(T) * Hq > 256LL * Hkv && cap < (1LL << 31)) {
       const size_t need = attn_key_weights_workspace_size(B, Hq, Hkv, T, int(cap), out_len);
-      if (need > 0) ws = at::empty({int64_t(need)}, k.options().dtype(at::kByte));
+      if (need > 0) ws = fresh({int64_t(need)}, at::kByte, dev);
     }
     if (ws) {
       dev.on(*ws);

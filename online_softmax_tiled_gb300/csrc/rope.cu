@@ -27,8 +27,7 @@
 // 52.5 us (6.4 TB/s, 0.94 of a plain copy; 86 us where the views start one
 // element off and take V = 1). 2 x 4096 tokens of 20 heads, half of each
 // turned, interleaved, as a gradient: 16.8 us (5.0 TB/s). One token of 64
-// requests: 6.4 us back to back, which is what launching a kernel from Python
-// costs.
+// requests: 4.7 us back to back from Python, 3.1 in a CUDA graph.
 
 #include "common.cuh"
 #include "launchers.h"
