@@ -38,8 +38,8 @@
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
 // 92 us, 438 MB. Four requests behind 500 keys: 11.8 us, three launches.
 // Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
-// and 76, 128 rows 41 and 37 (with copies of half rows, 4 us more at 16-key
-// pages).
+// and 76, 128 rows 41 and 37; over three prefixes of 128 rows on average 111
+// and 102.
 //
 // Order. The three kernels of a call are launched as programmatic
 // dependents. The prefix kernel lets the split kernel start once what
