@@ -206,8 +206,10 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!same_shape(*p.first, **p.second) || (*p.second)->scalar_type() != q.scalar_type())
         refuse_value("outputs must be like q and k");
     }
-    const int64_t count = pos.numel();
-    if (count != int64_t(B) * N && count != N)
+    // [B, N], or [N] or [1, N] for all requests; of one token also [B]
+    const int64_t rows = pos.dim() == 2 ? pos.size(0) : pos.dim() == 1 && N == 1 ? pos.size(0) : 1;
+    const int64_t cols = pos.dim() == 2 || (pos.dim() == 1 && N > 1) ? pos.size(-1) : 1;
+    if (pos.dim() < 1 || pos.dim() > 2 || cols != N || (rows != B && rows != 1))
       refuse_value("positions must be [B, N], or [N] for all requests");
     if (freq.dim() != 1) refuse_value("inv_freq must be [rot_dim / 2]");
     const void* pp = dev.data(pos, at::kInt);
@@ -220,7 +222,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check(attn_rope(q.data_ptr(), &qs, q_out->data_ptr(), &qos, k ? k->data_ptr() : nullptr,
                     k ? &ks : nullptr, k ? k_out->data_ptr() : nullptr, k ? &kos : nullptr,
-                    static_cast<const int*>(pp), count == int64_t(B) * N ? N : 0,
+                    static_cast<const int*>(pp), rows == B ? N : 0,
                     static_cast<const double*>(pw), B, Hq, Hkv, N, d, 2 * size(freq, 0),
                     truth(a[4]), real(a[5]), truth(a[6]), dt, dev.stream(a[9])),
           "attn_rope");

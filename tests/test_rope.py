@@ -332,3 +332,22 @@ def test_stream_graph_and_binding_refusals(ost):
         args = {"q": x, "k": None, "positions": pos, "inv_freq": w, **bad}
         with pytest.raises((ValueError, TypeError)):
             ost.rope(**args)
+
+
+@pytest.mark.gpu
+def test_position_shapes(ost):
+    """[B, N], [N] or [1, N]; for one token also [B] or [1]. Other shapes of
+    the same size are refused, not read in another order."""
+    w = _freq(64).to(DEV)
+    x = random_like_shape((3, 2, 5, 64), torch.bfloat16, 13).to(DEV)
+    pos = torch.arange(2, 7, dtype=torch.int32, device=DEV)
+    want = ost.rope(x, None, pos.expand(3, 5).contiguous(), w)[0]
+    assert torch.equal(ost.rope(x, None, pos, w)[0], want)
+    assert torch.equal(ost.rope(x, None, pos[None], w)[0], want)
+    one = ost.rope(x[:, :, 0], None, pos[:1], w)[0]
+    assert torch.equal(ost.rope(x[:, :, 0], None, pos[:1].expand(3).contiguous(), w)[0], one)
+    all_of = torch.arange(15, dtype=torch.int32, device=DEV)
+    for bad in (all_of, all_of.view(5, 3), all_of.view(3, 5, 1), all_of[:3], all_of[:5].view(5, 1),
+                all_of[0]):
+        with pytest.raises(ValueError):
+            ost.rope(x, None, bad, w)
