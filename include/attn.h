@@ -380,8 +380,8 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
  * num_prefix_splits, num_splits: most splits of a prefix's keys and of a
  * request's own; 0 takes the library's choice, made from the sizes alone (a
  * table much wider than the lengths it serves is no harm). The
- * probabilities of prefix keys are rounded to bf16 for the P·V product, as in
- * attn_fwd; all softmax state is float32.
+ * probabilities of prefix keys enter the P·V product as two bf16 parts each
+ * (2^-16 of a probability is lost at most); all softmax state is float32.
  * Device-side checks: a length outside [0, capacity] counts as 0, a split
  * with a page index out of range gets no keys, a group with a start outside
  * [0, B] or below its predecessor is empty; attn_sync_status() reports

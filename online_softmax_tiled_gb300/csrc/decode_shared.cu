@@ -32,14 +32,16 @@
 // unused rows may hold anything, and 0 · NaN is NaN).
 //
 // Measured (32 heads on 8, d = 128): 64 requests behind 8192 keys, 0 to 1024
-// of their own each, 16-key pages: 49 to 51 us, 168 MB of K and V, of which the own
+// of their own each, 16-key pages: 52 us, 168 MB of K and V, of which the own
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 92 us, 438 MB. Four requests behind 500 keys: 11.8 us, three launches.
-// Pairs against single runs at 8192 keys: 256 rows 52 and 55 us, 512 rows 59
-// and 76, 128 rows 41 and 37; over three prefixes of 128 rows on average 111
-// and 102.
+// 113 us, 438 MB. Four requests behind 500 keys: 12.2 us, three launches.
+// (With P̃ as one bf16 part: 49, 92 and 11.8.) A key tile takes 1.15 us, 2.2
+// where it feeds 256 rows.
+// Pairs against single runs at 8192 keys: 256 rows 53 and 55 us, 512 rows 91
+// and 93, 128 rows 41 and 34; over three prefixes of 128 rows on average 127
+// and 117.
 //
 // Order. The three kernels of a call are launched as programmatic
 // dependents. The prefix kernel lets the split kernel start once what
@@ -357,11 +359,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       };
       auto issue_pv = [&](int t, int j, bool first) {
         const uint32_t va = v_base + (j % C::kStages) * C::kTileBytes;
+        // (P̃'s rounded values lie in the first 64 columns, the rests behind)
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          tc::mma_ts_warp(tmem + C::kColO + t * D, tmem + C::kColS + t * kBN + kk * 8,
-                          tc::smem_desc(va + kk * 2 * group, half, group, tc::kLayoutSW128),
-                          idesc_o, (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            tc::mma_ts_warp(tmem + C::kColO + t * D,
+                            tmem + C::kColS + t * kBN + part * (kBN / 2) + kk * 8,
+                            tc::smem_desc(va + kk * 2 * group, half, group, tc::kLayoutSW128),
+                            idesc_o, (!first || part + kk > 0) ? 1u : 0u);
         tc::mma_commit_warp(&bars.o_done[t]);
       };
       auto k_ready = [&](int j) {
@@ -484,17 +490,20 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const f2 cc2{c, c}, nm2{neg_m, neg_m};
       f2 rs2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+      for (int part = 0; part < 4; ++part) {
+        uint32_t pk[16], rest[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          f2 x = fma2(f2{s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]}, cc2, nm2);
+        for (int e = 0; e < 16; ++e) {
+          f2 x = fma2(f2{s[part * 32 + 2 * e], s[part * 32 + 2 * e + 1]}, cc2, nm2);
           x.x = fast_exp2(x.x);
           x.y = fast_exp2(x.y);
           rs2[e & 3] = add2(rs2[e & 3], x);
           pk[e] = pack_bf16x2(x.x, x.y);
+          x = fma2(f2{bf16lo(pk[e]), bf16hi(pk[e])}, f2{-1.f, -1.f}, x);   // exact
+          rest[e] = pack_bf16x2(x.x, x.y);
         }
-        tmem_st32(s_addr + half * 32, pk);
+        tc::tmem_st16(s_addr + part * 16, pk);
+        tc::tmem_st16(s_addr + kBN / 2 + part * 16, rest);
       }
       const f2 rsa = add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3]));
       l_run = fmaf(alpha, l_run, rsa.x + rsa.y);
@@ -783,13 +792,16 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
   }
   if (prefix_splits <= 0) {
     // Both parts run at once, so a call takes as long as a prefix CTA, or as
-    // the work of both spread over all SMs, then as the merge of the splits.
+    // the work of both spread over all SMs, then as the merge of the splits;
+    // where the two meet, shorter CTAs pack better (0.15 of a CTA's time).
     // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
     // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
     // its partial rows; own keys, half their capacity but 512 at most (the
     // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
-    // partials for every split to merge. (64 requests behind 8192 keys: 71, 52,
-    // 56 us with 2, 4, 8 splits, 69 with 19, which fill the device.)
+    // partials for every split to merge. (64 requests behind 8192 keys: 87, 65,
+    // 53, 57, 61 us with 2, 3, 4, 5, 8 splits, 69 with 19, which fill the
+    // device; 128 of them 103, 92, 93 with 2, 3, 4; 96 behind three prefixes up
+    // to 32768: 147, 117, 117, 124 with 3, 4, 5, 6.)
     const double tile = (pl.pair ? 2.3 : 1.2) * d / 128, tiles_all = double(tiles);
     const double ctas = double(Hkv) * std::max<long long>(n_prefix, (rows + per - 1) / per);
     const double own = 1.0 * B * Hkv * std::min(own_cap / 2, 512LL) * d * 4 / 3e6;
@@ -799,7 +811,7 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
       const double cta = (double((tiles + s - 1) / s) + 4) * tile * std::ceil(ctas * s / sms);
       const double all = ctas * (tiles_all + 4 * s) * tile / sms + own;
-      const double cost = std::max(cta, all) + s * merge;
+      const double cost = std::max(cta, all) + 0.15 * cta + s * merge;
       if (s == 1 || cost < best) {
         best = cost;
         prefix_splits = s;

@@ -349,3 +349,38 @@ def test_binding_refusals(ost):
     with pytest.raises(ost.AttnError):
         ost.decode_shared(*(x[n] for n in ORDER), workspace=torch.empty(256, device=DEV,
                                                                         dtype=torch.uint8))
+
+
+def _exact_scores(x, seed):
+    """The case with scores that float32 holds exactly: queries are the first
+    unit vector, keys differ in their first element only, between -3 and 0."""
+    g = torch.Generator().manual_seed(seed)
+    x["q"].zero_()
+    x["q"][..., 0] = 1
+    for n in ("k_prefix", "k_pages"):
+        k0 = -3 * torch.rand(x[n].shape[:-1], generator=g)
+        x[n] = torch.zeros_like(x[n])
+        x[n][..., 0] = k0.to(DEV)
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,d,plen", [(4, 8, 2, 64, 40), (6, 8, 1, 128, 300),
+                                             (70, 16, 4, 128, 129), (40, 32, 4, 64, 77)])
+@pytest.mark.parametrize("sp", [0, 1])
+def test_prefix_probabilities_keep_more_than_bf16(ost, B, Hq, Hkv, d, plen, sp):
+    """As accurate as the paged decode of the same keys. Scores s are exact
+    here, so beside the output's own rounding (half a step, 2^-8 of the value)
+    a probability is off by two bf16 parts' 2^-16, by the scaling to log2
+    units (three roundings of a number below 4.5, 2^-22 of the probability
+    each) and by the exponential and the division by the sum (2^-21 together),
+    and a sum of 300 float32 terms, rounded or cut, by 300 · 2^-23: below
+    2^-14 in all."""
+    x = _exact_scores(_case(B, Hq, Hkv, d, [0, B], [plen], 8, [i % 3 for i in range(B)], 16,
+                            seed=plen), plen)
+    o, _ = ost.decode_shared(*(x[n] for n in ORDER), sp, 0, 1.0)
+    torch.cuda.synchronize()
+    o_ref, spread = _ref(x, 1.0)[0], _ref(x, 1.0, True)[0]
+    err = np.abs(to_f64(o) - o_ref)
+    assert np.all(err <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -14 * spread), \
+        (err - 2.0 ** -8 * np.abs(o_ref)).max()
