@@ -169,6 +169,10 @@ struct PagedKV {
   // before it and writes nothing this kernel reads (the shared prefix's
   // part): this grid does not wait for it at its start. Its last CTA waits
   // before it leaves, so that the grid's completion implies the partner's.
+  // The partner lets this grid start only once what precedes the call is
+  // complete and in L2; a grid that has not waited itself is not promised
+  // that its SM's L1 holds nothing older, so everything read here comes from
+  // L2 (keys and values through the bulk copies, the rest by __ldcg).
   int after_partner;
 };
 
@@ -244,7 +248,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   if (kPaged) {
     // The length and every table entry the chunk can touch, as independent
     // loads; entries are checked once the length says which ones are used.
-    Lb = pg.seq_lens[b];
+    Lb = __ldcg(pg.seq_lens + b);
     const int nominal = s * chunk;
     p_first = nominal / pg.page_size;
     const int p_cap = min(pg.max_pages, (min(max_len, nominal + chunk) + pg.page_size - 1) /
@@ -253,7 +257,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int p = p_first + tid + i * kThreads;
-      ent[i] = p < p_cap ? table_row[p] : 0;
+      ent[i] = p < p_cap ? __ldcg(table_row + p) : 0;
     }
     if (Lb < 0 || Lb > max_len) {
       if (s == 0 && g == 0 && tid == 0) attn_flag_error(kErrBadIndex);
@@ -269,7 +273,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
     // chunks of more than 4 x kThreads pages (pages far smaller than the
     // chunk): the rest checked straight from the table
     for (int p = p_first + 4 * kThreads + tid; p < p_used; p += kThreads) {
-      const int e = table_row[p];
+      const int e = __ldcg(table_row + p);
       bad |= e < 0 || e >= pg.num_pages;
     }
   }
@@ -303,7 +307,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   const size_t page_elems = sparse ? size_t(D) : size_t(Hkv) * pg.page_size * D;
   auto page_of = [&](int t) {
     const int i = t / pg.page_size - p_first;
-    return i < kChunkPagesCached ? chunk_pages[i] : table_row[t / pg.page_size];
+    return i < kChunkPagesCached ? chunk_pages[i] : __ldcg(table_row + t / pg.page_size);
   };
   // Paged bulk copies: with pages of a multiple of 16 keys a 32-key stage
   // touches at most two pages, and the source offsets of the first
@@ -407,7 +411,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
     const __nv_bfloat16* qh = q + (size_t(b) * Hq + gy * G + h) * D;
 #pragma unroll
     for (int vv = 0; vv < NV; ++vv) {
-      const uint4 w = *reinterpret_cast<const uint4*>(qh + 64 * vv + 8 * sub);
+      const uint4 w = __ldcg(reinterpret_cast<const uint4*>(qh + 64 * vv + 8 * sub));
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) qf[h][vv * 4 + e] = f2{bf16lo(ws[e]) * qs, bf16hi(ws[e]) * qs};

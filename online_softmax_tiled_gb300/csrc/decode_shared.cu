@@ -131,8 +131,8 @@ ATTN_DEVINL void tmem_st32(uint32_t ta, const uint32_t (&r)[32]) {
 // Requests [first, last) of prefix p; an entry outside [0, B] or one below
 // its predecessor leaves the group empty.
 ATTN_DEVINL bool group_of(const int* start, int p, int B, int& first, int& last) {
-  first = start[p];
-  last = start[p + 1];
+  first = __ldcg(start + p);
+  last = __ldcg(start + p + 1);
   const bool good = first >= 0 && last >= first && last <= B;
   if (!good) first = last = 0;
   return good;
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
   constexpr int kBatch = 8;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= a.rows) return;
-  // (Lengths and starts may be read at once: the prefix kernel has waited for
-  // all that precedes the call before this grid could start.)
+  // (Lengths and starts may be read at once, from L2: the prefix kernel has
+  // waited for all that precedes the call before this grid could start.)
   const int b = row / a.Hq;
   int np = 0;
   for (int p0 = 0; p0 < a.n_prefix; p0 += 32) {
@@ -654,12 +654,12 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
     if (p0 + lane < a.n_prefix) group_of(a.prefix_start, p0 + lane, a.B, first, last);
     const uint32_t hit = __ballot_sync(0xffffffffu, first <= b && b < last);
     if (hit) {
-      const int n = checked_len(a.prefix_lens[p0 + __ffs(hit) - 1], a.prefix_cap);
+      const int n = checked_len(__ldcg(a.prefix_lens + p0 + __ffs(hit) - 1), a.prefix_cap);
       np = (n + a.prefix_chunk - 1) / a.prefix_chunk;
       break;
     }
   }
-  const int no = (checked_len(a.seq_lens[b], a.own_cap) + a.own_chunk - 1) / a.own_chunk;
+  const int no = (checked_len(__ldcg(a.seq_lens + b), a.own_cap) + a.own_chunk - 1) / a.own_chunk;
   const int nv = np + no, d4 = a.d / 4;                // (d4 is 16 or 32: a column per lane)
   auto slot = [&](int t) { return t < np ? t : t - np + a.s_own; };
   const float* mr = a.m_part + size_t(row) * a.stride;

@@ -71,7 +71,7 @@ ATTN_DEVINL float score_of(uint32_t key) {
 
 ATTN_DEVINL int length_of(const int* seq_lens, int b, int cap, bool& bad) {
   if (seq_lens == nullptr) return cap;
-  const int n = seq_lens[b];
+  const int n = __ldcg(seq_lens + b);
   bad = n < 0 || n > cap;
   return bad ? 0 : n;
 }
@@ -97,8 +97,8 @@ evict_select_kernel(const float* __restrict__ scores, const int* __restrict__ se
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
     reinterpret_cast<int4*>(sm.hist)[i] = make_int4(0, 0, 0, 0);
-  // (the gathering kernel's start may rely on this wait: it reads the lengths
-  // before it waits for this kernel)
+  // (the gathering kernel's start may rely on this wait: it reads the lengths,
+  // from L2, before it waits for this kernel)
   pdl_wait_primary();
   pdl_launch_dependents();
   // A barrier over the row's CTAs; a cluster's takes 600 to 1000 cycles, a

@@ -75,7 +75,7 @@ struct KwArgs {
 
 ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
   if (a.seq_lens == nullptr) return a.cap;
-  const int n = a.seq_lens[b];
+  const int n = __ldcg(a.seq_lens + b);
   const bool wrong = n < 0 || n > a.cap;
   bad |= wrong;
   return wrong ? 0 : n;
@@ -1085,7 +1085,7 @@ weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
   const long long each = steps_per_cta(rs, total, grid);
   const long long last = first + steps_of(a, rs, n, k) - 1;
   const int slots = int(quotient(last, each) - quotient(first, each)) + 1;
-  // (Lengths may be read before: the kernel that made the sums lets this one
+  // (Lengths may be read before, from L2: the kernel that made the sums lets this one
   // start only once all that precedes the call is complete.)
   pdl_wait_primary();
   pdl_launch_dependents();

@@ -112,3 +112,59 @@ def test_serving_loop(ost, d, Hq, Hkv):
     for i in range(steps):
         step(k2, v2, score2, lens2, room, 50 + i, P + N + steps + i)
     assert ost.attn_sync_status() == 0
+
+
+def test_library_calls_alone_hand_over_queries_and_lengths(ost):
+    """Queries, lengths and caches that one call rewrites in place and the next
+    reads, with no other kernel of any kind between them: the same results as
+    with the device idle between calls."""
+    B, Hq, Hkv, d, L, P, T, keep = 12, 8, 2, 128, 200, 900, 80, 48
+    bf, steps = torch.bfloat16, 8
+    w = ost.rope_frequencies(d, device=DEV)
+    q0 = random_like_shape((B, Hq, d), bf, 1).to(DEV)
+    pos = [torch.full((B, 1), 1000 * i, dtype=torch.int32, device=DEV) for i in range(steps)]
+    lens = [torch.tensor([(37 * i + 11 * b) % 60 for b in range(B)], dtype=torch.int32, device=DEV)
+            for i in range(steps)]
+    k, v = (random_like_shape((B, Hkv, L, d), bf, s).to(DEV) for s in (2, 3))
+    kp, vp = (random_like_shape((1, Hkv, P, d), bf, s).to(DEV) for s in (4, 5))
+    scores = [random_like_shape((B, Hkv, L), torch.float32, 6 + i).to(DEV) for i in range(steps)]
+    qt = random_like_shape((B, Hq, T, d), bf, 30).to(DEV)
+    lt = torch.full((B, Hq, T), 7.0, device=DEV)
+    prefix = [torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+              torch.tensor([P], dtype=torch.int32, device=DEV),
+              torch.tensor([0, B], dtype=torch.int32, device=DEV)]
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    n1 = ost.attn_decode_shared_workspace_size(q0, kp, prefix[0], k[:, :, :keep], table)
+    n2 = ost.attn_key_weights_workspace_size(B, Hq, Hkv, T, keep, keep)
+    assert n2 > 0                                   # more rows than are kept: sums are joined
+    ws1, ws2 = (torch.empty(n, dtype=torch.uint8, device=DEV) for n in (n1, n2))
+
+    def run(idle):
+        z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device=DEV)  # noqa: E731
+        q, ko, vo = z(B, Hq, d, t=bf), z(B, Hkv, keep, d, t=bf), z(B, Hkv, keep, d, t=bf)
+        so, kept, new = z(B, Hkv, keep), z(B, Hkv, keep, t=torch.int32), z(B, t=torch.int32)
+        outs = [(z(B, Hq, d, t=bf), z(B, Hq), z(B, Hkv, keep), z(B, Hkv, 20, d, t=bf),
+                 z(B, Hkv, 20, d, t=bf), z(B, Hkv, 20, t=torch.int32), z(B, t=torch.int32))
+                for _ in range(steps)]
+        torch.cuda.synchronize()
+        after = torch.cuda.synchronize if idle else (lambda: None)
+        for i, (o, lse, sums, k2, v2, kept2, new2) in enumerate(outs):
+            ost.attn_cache_evict(k, v, scores[i], ko, vo, so, kept, new, 2, 3, seq_lens=lens[i])
+            after()
+            ost.attn_rope(q0, None, q, None, pos[i], w)
+            after()
+            ost.attn_decode_shared(q, kp, vp, *prefix, ko, vo, table, new, o, lse, d ** -0.5, 0, 0,
+                                   ws1)
+            after()
+            ost.attn_key_weights(qt, ko, lt, None, sums, d ** -0.5, seq_lens=new, workspace=ws2)
+            after()
+            ost.attn_cache_evict(ko, vo, sums, k2, v2, None, kept2, new2, 1, 1, seq_lens=new)
+            after()
+            ost.attn_rope(q0, None, q, None, pos[-1 - i], w)
+            after()
+        torch.cuda.synchronize()
+        return outs
+    want = run(True)
+    for _ in range(5):
+        for a, b in zip(want, run(False)):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
