@@ -438,8 +438,9 @@ typedef struct {
  * value, negative included; position_batch_stride 0 shares one row among all
  * requests. inv_freq float64 [rot_dim/2] in DEVICE memory, where any scaling
  * for long contexts is already contained; the angle is reduced modulo one
- * turn in 64-bit fixed point, so far positions lose nothing. A frequency
- * that is not finite gives NaN in its pairs.
+ * turn in 64-bit fixed point: below 2^64 radians a position it is off by less
+ * than 2^-32 turns at every position before it is rounded to float32. A
+ * frequency that is not finite, or of 2^64 and more, gives NaN in its pairs.
  * Rows at multiples of 16 bytes with d and rot_dim multiples of 16 (bf16) or
  * 8 (float32) move in 16-byte pieces; everything else element by element.
  * Pointers need their element's alignment only. B*N at most 2^31 - 256.

@@ -351,3 +351,27 @@ def test_position_shapes(ost):
                 all_of[0]):
         with pytest.raises(ValueError):
             ost.rope(x, None, bad, w)
+
+
+@pytest.mark.gpu
+def test_far_positions_of_large_frequencies(ost):
+    """The bound of the module docstring up to 2^64 radians a position (the
+    fixed-point angle is off by 2^-32 turns at most, 2^-28 radians, well
+    inside it); from there on NaN, not a wrong angle."""
+    pos = torch.tensor([[2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 0, 1, -1, 3, 10 ** 9]],
+                       dtype=torch.int32)
+    w = torch.tensor([1e6, -1e10, 1e4, 8.1, 1e15, 2.0 ** 63, 1.8e19, math.nextafter(2.0 ** 64, 0),
+                      2.0 ** 64, -1e20, 2.0 ** 65, 1e300, -2.0 ** 40, 1.2345e12, 4.4e18, 100.0],
+                     dtype=torch.float64)
+    for dt, inter in ((torch.float32, False), (torch.bfloat16, True)):
+        x = random_like_shape((1, 2, 8, 32), dt, 3).to(DEV)
+        y, _ = ost.rope(x, None, pos.to(DEV), w.to(DEV), inter)
+        pairs = y.view(1, 2, 8, 16, 2) if inter else y.view(1, 2, 8, 2, 16).transpose(3, 4)
+        bad = w.abs() >= 2.0 ** 64
+        assert bad.sum() == 4 and bool(pairs[..., bad, :].isnan().all())
+        good = torch.where(bad, torch.tensor(0.0, dtype=torch.float64), w)
+        xz = x.clone()
+        (xz.view(1, 2, 8, 16, 2) if inter else xz.view(1, 2, 8, 2, 16).transpose(3, 4)
+         )[..., bad, :] = 0
+        pairs[..., bad, :] = 0                       # (a frequency of zero leaves zeros)
+        _check(y, xz, pos, good, inter, 1.0, False)
