@@ -433,7 +433,9 @@ typedef struct {
  * contiguous; a view of a fused projection [B,N,Hq+2Hkv,d] is one example);
  * q_out, k_out likewise, their rows must not overlap. Hkv = 0 turns q alone
  * (k, k_out ignored). q_out == q and k_out == k with equal strides turn in
- * place; otherwise outputs must not overlap inputs. d even and <= 512,
+ * place; any other row of an output that shares a byte with an input or with
+ * the other output is refused (rows between each other's, as of views of one
+ * buffer, are fine). d even and <= 512,
  * rot_dim even, 2 <= rot_dim <= d. positions int32 in DEVICE memory, any
  * value, negative included; position_batch_stride 0 shares one row among all
  * requests. inv_freq float64 [rot_dim/2] in DEVICE memory, where any scaling

@@ -49,6 +49,84 @@ bool same_rows(const attn_strides& a, const attn_strides& b, int B, int H, int N
          (N == 1 || a.token == b.token);
 }
 
+// Rows of `len` bytes at base + i·stride0 + j·stride1 + k·stride2 (bytes;
+// strides >= 0).
+struct RowSet {
+  const void* base;
+  long long len;
+  long long stride[3];
+  int n[3];
+  __int128 first() const { return __int128(reinterpret_cast<uintptr_t>(base)); }
+  __int128 last() const {      // of its bytes
+    __int128 at = first() + len - 1;
+    for (int i = 0; i < 3; ++i) at += __int128(stride[i]) * (n[i] - 1);
+    return at;
+  }
+};
+RowSet row_set(const void* p, const attn_strides& s, int B, int H, int N, int d, long long esize) {
+  return {p, d * esize, {s.batch * esize, s.head * esize, s.token * esize}, {B, H, N}};
+}
+
+// Whether a byte belongs to rows of both sets. With the strides of both as
+// one list, the row starts lie a.base - b.base + Σ stride·x apart, each x in a
+// range of its own (equal strides joined), and two rows meet where that is in
+// [-(a.len - 1), b.len - 1]. The x are tried from the largest stride down,
+// those only from which the smaller strides can still reach: one or two each
+// for sets that lie apart or inside each other's gaps. Sets that would take
+// long to tell count as meeting.
+struct RowsMeet {
+  using Wide = __int128;
+  Wide stride[6], lo[6], hi[6], rest_lo[7], rest_hi[7];
+  Wide from, to;               // distances at which rows meet
+  int dims = 0, left = 4096;   // distances still to be tried
+
+  void add(long long s, long long first, long long last) {
+    if (s == 0 || first == last) return;
+    int i = 0;
+    while (i < dims && stride[i] > s) ++i;
+    if (i < dims && stride[i] == s) {
+      lo[i] += first;
+      hi[i] += last;
+      return;
+    }
+    for (int k = dims++; k > i; --k) {
+      stride[k] = stride[k - 1];
+      lo[k] = lo[k - 1];
+      hi[k] = hi[k - 1];
+    }
+    stride[i] = s;
+    lo[i] = first;
+    hi[i] = last;
+  }
+  static Wide floor_div(Wide x, Wide y) { return x / y - (x % y < 0); }
+  bool search(int k, Wide at) {
+    if (--left < 0) return true;
+    if (k == dims) return at >= from && at <= to;
+    const Wide s = stride[k];
+    const Wide x0 = std::max(lo[k], -floor_div(at + rest_hi[k + 1] - from, s));
+    const Wide x1 = std::min(hi[k], floor_div(to - at - rest_lo[k + 1], s));
+    for (Wide x = x0; x <= x1; ++x)
+      if (search(k + 1, at + s * x)) return true;
+    return false;
+  }
+  static bool test(const RowSet& a, const RowSet& b) {
+    if (a.first() > b.last() || b.first() > a.last()) return false;
+    RowsMeet m;
+    for (int i = 0; i < 3; ++i) {
+      m.add(a.stride[i], 0, a.n[i] - 1);
+      m.add(b.stride[i], -(b.n[i] - 1LL), 0);
+    }
+    m.rest_lo[m.dims] = m.rest_hi[m.dims] = 0;
+    for (int k = m.dims - 1; k >= 0; --k) {
+      m.rest_lo[k] = m.rest_lo[k + 1] + m.stride[k] * m.lo[k];
+      m.rest_hi[k] = m.rest_hi[k + 1] + m.stride[k] * m.hi[k];
+    }
+    m.from = -(a.len - 1);
+    m.to = b.len - 1;
+    return m.search(0, a.first() - b.first());
+  }
+};
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a != nullptr && b != nullptr && x < y + nb && y < x + na;
@@ -136,6 +214,20 @@ attn_status attn_rope(const void* q, const attn_strides* q_strides, void* q_out,
   if (Hkv > 0 && (!non_negative(a.ks) || !rows_apart(a.kos, B, Hkv, N, d) ||
                   (k == k_out && !same_rows(a.ks, a.kos, B, Hkv, N))))
     return ATTN_ERR_INVALID_ARG;
+  // blocks run in any order: but for a tensor turned in place, nothing that is
+  // written may be read by the call or written twice
+  const long long e = static_cast<long long>(esize);
+  const RowSet in[] = {row_set(q, a.qs, B, Hq, N, d, e), row_set(k, a.ks, B, Hkv, N, d, e),
+                       {positions, 4, {position_batch_stride * 4, 4, 0}, {B, N, 1}},
+                       {inv_freq, rot_dim / 2 * 8LL, {0, 0, 0}, {1, 1, 1}}},
+               out[] = {row_set(q_out, a.qos, B, Hq, N, d, e),
+                        row_set(k_out, a.kos, B, Hkv, N, d, e)};
+  for (int i = 0; i < (Hkv > 0 ? 2 : 1); ++i)
+    for (int j = 0; j < 4; ++j)
+      if ((j != 1 || Hkv > 0) && !(i == j && in[j].base == out[i].base) &&
+          RowsMeet::test(in[j], out[i]))
+        return ATTN_ERR_INVALID_ARG;
+  if (Hkv > 0 && RowsMeet::test(out[0], out[1])) return ATTN_ERR_INVALID_ARG;
   return from_cuda(launch_rope(a));
 }
 

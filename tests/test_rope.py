@@ -375,3 +375,75 @@ def test_far_positions_of_large_frequencies(ost):
          )[..., bad, :] = 0
         pairs[..., bad, :] = 0                       # (a frequency of zero leaves zeros)
         _check(y, xz, pos, good, inter, 1.0, False)
+
+
+def _rows_of(base, strides, B, H, N, d):
+    """Bytes of the float32 rows of a [B, H, N, d] tensor."""
+    return {base + 4 * (b * strides[0] + h * strides[1] + n * strides[2]) + i
+            for b in range(B) for h in range(H) for n in range(N) for i in range(4 * d)}
+
+
+def test_outputs_on_top_of_inputs_or_each_other_are_refused(lib):
+    """Exactly the calls whose outputs share a byte with an input (but for one
+    turned in place) or with each other, among 3000 random layouts in one small
+    range of addresses, and some by hand."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: nothing may launch")
+    rng = np.random.default_rng(5)
+    seen = [0, 0]
+    for _ in range(3000):
+        B, Hq, Hkv, N, d = (int(x) for x in rng.integers([1, 1, 1, 1, 1], [3, 4, 3, 4, 3]))
+        d *= 2
+
+        def layout(H):
+            if rng.random() < 0.5:                  # heads of a fused projection
+                per = H + int(rng.integers(0, 4))
+                return [N * per * d, d, per * d]
+            gap = int(rng.integers(0, 3)) * d
+            return [H * (N * d + gap), N * d + gap, d]
+        at = [P + 4 * int(rng.integers(0, 60)) for _ in range(4)]
+        st = [layout(H) for H in (Hq, Hq, Hkv, Hkv)]
+        for i in (0, 2):                            # in place
+            if rng.random() < 0.5:
+                at[i + 1], st[i + 1] = at[i], st[i]
+        rows = [_rows_of(a, s, B, H, N, d) for a, s, H in zip(at, st, (Hq, Hq, Hkv, Hkv))]
+        meet = bool(rows[1] & rows[3]) or bool(rows[1] & rows[2]) or bool(rows[3] & rows[0])
+        for i in (0, 2):
+            # (strides of extents of one do not matter)
+            same = at[i] == at[i + 1] and rows[i] == rows[i + 1]
+            meet |= not same and bool(rows[i] & rows[i + 1])
+        got = _call(lib, q=at[0], qs=st[0], qo=at[1], qos=st[1], k=at[2], ks=st[2], ko=at[3],
+                    kos=st[3], pos=1 << 30, w=1 << 31, pstride=N, B=B, Hq=Hq, Hkv=Hkv, N=N, d=d,
+                    rot=d, dt=0)
+        assert (got == INVALID) == meet, (B, Hq, Hkv, N, d, at, st)
+        seen[meet] += 1
+    assert min(seen) > 300
+    far = 1 << 30
+    size = 2 * 4 * 4 * 64 * 2                       # bytes of q
+    free = dict(qo=far, k=2 * far, ko=3 * far, pos=4 * far, w=5 * far)
+    assert _call(lib, **free) != INVALID
+    for bad in (dict(qo=P + 128), dict(qo=P + size - 16), dict(ko=far), dict(ko=P), dict(qo=2 * far),
+                dict(qo=2 * far, ko=P), dict(pos=far + size - 4), dict(w=3 * far + 8),
+                dict(pos=far - 4)):
+        assert _call(lib, **{**free, **bad}) == INVALID, bad
+    assert _call(lib, **{**free, "qo": P, "ko": 2 * far}) != INVALID
+
+
+@pytest.mark.gpu
+def test_binding_refuses_swapped_and_shifted_outputs(ost):
+    w, pos = _freq(64).to(DEV), torch.arange(9, dtype=torch.int32, device=DEV)
+    buf = random_like_shape((3, 2, 4, 10, 64), torch.float32, 14).to(DEV)
+    q, k = buf[0, :, :, :9], buf[1, :, :, :9]
+    before = buf.clone()
+    for out in ((k, q), (buf[0, :, :, 1:], buf[2, :, :, :9]), (buf[2, :, :, :9], buf[2, :, :, 1:]),
+                (buf[2, :, :, :9], buf[2, :, :, :9]), (k, buf[2, :, :, :9])):
+        with pytest.raises(ost.AttnError):
+            ost.rope(q, k, pos, w, out=out)
+    with pytest.raises(ost.AttnError):
+        ost.rope(q, q, pos, w, out=(q, k))          # turned in place and read as k
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before)
+    want = ost.rope(q, k, pos, w)
+    ost.rope(q, k, pos, w, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(buf[2], before[2]) and torch.equal(buf[:2, :, :, 9], before[:2, :, :, 9])
