@@ -470,8 +470,8 @@ ATTN_API attn_status attn_rope(const void* q, const attn_strides* q_strides, voi
  * the n positions: with causal = 1 key j is seen by token i iff
  * j <= n - T + i, with causal = 0 by all. A row with an infinite lse
  * gives nothing, whatever its q holds. prev == NULL: no first term (decay
- * ignored); prev == out adds in place; any other overlap of the two is
- * refused. out[b,g,j] for j >= n is left as it was.
+ * ignored); prev == out adds in place; any other overlap of out with an
+ * input is refused. out[b,g,j] for j >= n is left as it was.
  *
  * q [B,Hq,T,d] bf16, lse [B,Hq,T] float32 (T = 1: decode's q and lse); k a
  * contiguous cache [B,Hkv,L,d] bf16 (block_table NULL; seq_lens NULL: every

@@ -341,6 +341,13 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
     return ATTN_ERR_MISALIGNED;
   const size_t n_out = size_t(B) * Hkv * out_len * 4;
   if (prev != out && overlap(prev, n_out, out, n_out)) return ATTN_ERR_INVALID_ARG;
+  const size_t rows = size_t(B) * Hq * T, keys = block_table != nullptr
+                                                     ? size_t(num_pages) * Hkv * page_size
+                                                     : size_t(B) * Hkv * L;
+  if (overlap(q, rows * d * 2, out, n_out) || overlap(k, keys * d * 2, out, n_out) ||
+      overlap(lse, rows * 4, out, n_out) || overlap(seq_lens, size_t(B) * 4, out, n_out) ||
+      overlap(block_table, size_t(B) * max_pages_per_seq * 4, out, n_out))
+    return ATTN_ERR_INVALID_ARG;
   const int len_cap = int(std::min<long long>(cap, out_len));
   if (const size_t slots = key_weights_slots(Hq / Hkv * T, T)) {
     if (!workspace || ws_bytes < align256(slots * n_out)) return ATTN_ERR_WORKSPACE;

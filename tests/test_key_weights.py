@@ -335,3 +335,22 @@ def test_binding_refusals(ost):
             ost.key_weights(**{**dict(q=q, k=k, lse=lse, out=out), **bad})
     with pytest.raises(ost.AttnError):
         ost.key_weights(q, k, lse, scale=float("nan"))
+
+
+@pytest.mark.parametrize("kwargs", [
+    dict(out=P), dict(out=P - 2 * 2 * 100 * 4 + 4), dict(out=P + 2 * 4 * 3 * 64 * 2 - 4),   # q
+    dict(out=2 * P + 2 * 2 * 100 * 64 * 2 - 4), dict(out=3 * P), dict(out=6 * P + 4),
+    {**PAGED, "out": 2 * P + 9 * 2 * 16 * 64 * 2 - 4}, {**PAGED, "out": 7 * P + 2 * 4 * 4 - 4},
+])
+def test_outputs_on_top_of_inputs_are_refused(lib, kwargs):
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: nothing may launch")
+    assert _call(lib, **kwargs) == INVALID
+
+
+def test_outputs_next_to_inputs_are_not_refused(lib):
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: nothing may launch")
+    for kwargs in (dict(), dict(out=P - 2 * 2 * 100 * 4), dict(out=P + 2 * 4 * 3 * 64 * 2),
+                   dict(out=2 * P + 2 * 2 * 100 * 64 * 2), dict(out=4 * P), PAGED):
+        assert _call(lib, **kwargs) != INVALID
