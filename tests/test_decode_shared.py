@@ -384,3 +384,16 @@ def test_prefix_probabilities_keep_more_than_bf16(ost, B, Hq, Hkv, d, plen, sp):
     err = np.abs(to_f64(o) - o_ref)
     assert np.all(err <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -14 * spread), \
         (err - 2.0 ** -8 * np.abs(o_ref)).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,d,start,plens,ppage,lens,page", [
+    (5, 32, 4, 128, [0, 2, 5], [300, 150], 16, [7, 0, 33, 64, 5], 16),
+    (40, 16, 2, 128, [0, 40], [700], 64, [i % 50 for i in range(40)], 16),   # 320 rows: two runs
+])
+@pytest.mark.parametrize("sp,so", [(0, 0), (3, 2)])
+def test_eight_query_heads_of_128(ost, B, Hq, Hkv, d, start, plens, ppage, lens, page, sp, so):
+    x = _case(B, Hq, Hkv, d, start, plens, ppage, lens, page, seed=B)
+    o, lse = ost.decode_shared(*(x[n] for n in ORDER), sp, so)
+    torch.cuda.synchronize()
+    _check(o, lse, x, d ** -0.5)

@@ -247,3 +247,39 @@ def test_stream_graph_and_binding_refusals(ost):
             ost.evict(**args)
     with pytest.raises(ost.AttnError):
         ost.evict(k, v, s, 40, 30, 11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["rand", "ties", "zeros", "signed", "odd"])
+def test_rows_that_do_not_stay_in_registers(ost, kind):
+    """More than 131072 scores a row are read again for every pass: ties that
+    are cut, NaN and infinities, held keys and ragged last segments, beside a
+    request short enough to be held."""
+    _check(ost, 3, 1, 140001, 64, 4001, 3, 70, 0, [139990, 131500, 5000], kind, seed=7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["rand", "ties"])
+def test_four_ctas_a_row(ost, kind):
+    """32 rows of more than 8192 scores: two CTAs a row would leave SMs idle."""
+    _check(ost, 4, 8, 9001, 64, 300, 2, 17, 0, [9001, 8999, 4097, 301], kind, seed=11)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits_in_a_stable_order(ost):
+    """As test_offsets_past_32_bits, whose scores tie now and then: here with
+    seeded scores and the ties' lower index first."""
+    B, Hkv, L, d, keep = 1, 18, 1 << 20, 128, 300
+    k = torch.empty(B, Hkv, L, d, dtype=torch.bfloat16, device=DEV)
+    k.view(torch.int16).view(-1, d)[:] = torch.arange(Hkv * L, device=DEV)[:, None] % 32749
+    v = k.flip(2)
+    g = torch.Generator().manual_seed(17)
+    s = (torch.rand(Hkv, L, generator=g) * 4096).floor().to(DEV)[None]     # 256 keys a score
+    ko, vo, so, kept, new = ost.evict(k, v, s, keep)
+    for h in range(Hkv):
+        order = torch.sort(s[0, h], descending=True, stable=True).indices
+        at = torch.sort(order[:keep]).values
+        assert torch.equal(kept[0, h].long(), at)
+        assert torch.equal(ko[0, h].view(torch.int16), k[0, h, at].view(torch.int16))
+        assert torch.equal(vo[0, h].view(torch.int16), v[0, h, at].view(torch.int16))
+        assert torch.equal(so[0, h], s[0, h, at])

@@ -354,3 +354,14 @@ def test_outputs_next_to_inputs_are_not_refused(lib):
     for kwargs in (dict(), dict(out=P - 2 * 2 * 100 * 4), dict(out=P + 2 * 4 * 3 * 64 * 2),
                    dict(out=2 * P + 2 * 2 * 100 * 64 * 2), dict(out=4 * P), PAGED):
         assert _call(lib, **kwargs) != INVALID
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_requests_than_threads(ost, causal):
+    """Requests are counted by the threads of a CTA, several each past 352 (and
+    past 256 where partial sums are joined); lengths of zero among them."""
+    lens = [0 if i % 7 == 0 else 1 + (i * 53) % 300 for i in range(800)]
+    _check(ost, 800, 2, 1, 1, 300, 64, 0, lens, causal, seed=21)
+    lens = [0 if i % 5 == 0 else 300 if i == 399 else 1 + (i * 29) % 40 for i in range(400)]
+    _check(ost, 400, 1, 1, 260, 300, 64, 0, lens, causal, 0.5, seed=22)
