@@ -378,8 +378,11 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
  * bf16; lse [B,Hq] float32 (may be NULL). A request without any key gets
  * O = 0, LSE = -inf. d 64 or 128; Hq/Hkv in {1, 2, 4, 8}.
  * num_prefix_splits, num_splits: most splits of a prefix's keys and of a
- * request's own; 0 takes the library's choice, made from the sizes alone (a
- * table much wider than the lengths it serves is no harm). The
+ * request's own; 0 takes the library's choice. A prefix is cut by its own
+ * length, on the device, so columns of prefix_table that no prefix uses cost
+ * next to nothing; own keys are cut by what block_table can hold, as in
+ * attn_decode_paged, so a table much wider than the lengths it serves leaves
+ * a request fewer of its splits. The
  * probabilities of prefix keys enter the P·V product as two bf16 parts each
  * (2^-16 of a probability is lost at most); all softmax state is float32.
  * Device-side checks: a length outside [0, capacity] counts as 0, a split

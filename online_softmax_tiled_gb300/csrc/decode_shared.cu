@@ -32,16 +32,17 @@
 // unused rows may hold anything, and 0 · NaN is NaN).
 //
 // Measured (32 heads on 8, d = 128): 64 requests behind 8192 keys, 0 to 1024
-// of their own each, 16-key pages: 52 us, 168 MB of K and V, of which the own
+// of their own each, 16-key pages: 53 us, 168 MB of K and V, of which the own
 // keys' 134 MB alone take 40 (short pieces of keys: a CTA's start-up, not the
 // bandwidth, bounds them) and the prefix's tiles 43 on 32 SMs beside them.
 // 96 requests behind three documents of 16384 to 32768 keys, 64-key pages:
-// 113 us, 438 MB. Four requests behind 500 keys: 12.2 us, three launches.
+// 113 us, 438 MB. Four requests behind 500 keys: 12.7 us, three launches.
 // (With P̃ as one bf16 part: 49, 92 and 11.8.) A key tile takes 1.15 us, 2.2
 // where it feeds 256 rows.
 // Pairs against single runs at 8192 keys: 256 rows 53 and 55 us, 512 rows 91
 // and 93, 128 rows 41 and 34; over three prefixes of 128 rows on average 127
-// and 117.
+// and 117. The same calls with a prefix_table 16 times as wide take 58, 119 and
+// 13 (cut by what the table holds: 162, 317 and 15).
 //
 // Order. The three kernels of a call are launched as programmatic
 // dependents. The prefix kernel lets the split kernel start once what
@@ -97,7 +98,7 @@ struct Bars {
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort;
-  int unit[4];               // prefix, first request, requests of this CTA's rows; keys
+  int unit[5];               // prefix, first request, requests of this CTA's rows; keys, chunk
 };
 
 struct PrefixArgs {
@@ -107,7 +108,8 @@ struct PrefixArgs {
   float* o_part;
   float* m_part;
   float* l_part;
-  int B, Hq, Hkv, G, n_prefix, num_pages, page_size, max_pages, box_rows, chunk, stride;
+  int B, Hq, Hkv, G, n_prefix, num_pages, page_size, max_pages, box_rows, most, stride;
+  SplitCost cost;
   int joined;                // copies that take both 64-column halves of a row
   float scale;
 };
@@ -136,6 +138,45 @@ ATTN_DEVINL bool group_of(const int* start, int p, int B, int& first, int& last)
   const bool good = first >= 0 && last >= first && last <= B;
   if (!good) first = last = 0;
   return good;
+}
+
+// (rounded operation by operation: two kernels must choose the same splits)
+__host__ __device__ inline float split_cost(const SplitCost& c, int tiles, int s) {
+#ifdef __CUDA_ARCH__
+  auto mul = [](float x, float y) { return __fmul_rn(x, y); };
+  auto add = [](float x, float y) { return __fadd_rn(x, y); };
+#else
+  auto mul = [](float x, float y) { return x * y; };
+  auto add = [](float x, float y) { return x + y; };
+#endif
+  // (divisions take longer than all the rest; 1e-4 is above the product's
+  // rounding and below what a part of a wave counts)
+  const float waves = fmaxf(1.f, ceilf(add(mul(c.filled, float(s)), -1e-4f)));
+  const float cta = mul(mul(float((unsigned(tiles) + s - 1) / unsigned(s) + 4), waves), c.tile);
+  const float all = add(mul(float(tiles + 4 * s), c.work), c.own);
+  return add(add(fmaxf(cta, all), mul(0.15f, cta)), mul(float(s), c.merge));
+}
+constexpr int kMostSplits = 64;      // that are chosen
+
+// Keys per split of a prefix of n keys (a whole warp): the cheapest of at most
+// `most` splits for the prefix's own length, not for what its table could hold.
+ATTN_DEVINL int chunk_of(const SplitCost& c, int n, int most, int lane) {
+  const int tiles = (n + kBN - 1) / kBN;
+  int s = most;
+  if (!c.fixed) {
+    uint32_t best = 0xffffffffu;
+    for (int s0 = 1; s0 <= most; s0 += 32) {
+      const uint32_t cost =
+          s0 + lane <= most ? __float_as_uint(split_cost(c, tiles, s0 + lane)) : 0xffffffffu;
+      const uint32_t low = __reduce_min_sync(0xffffffffu, cost);
+      const uint32_t who = __ballot_sync(0xffffffffu, cost == low);
+      if (low < best) {
+        best = low;
+        s = s0 + __ffs(who) - 1;
+      }
+    }
+  }
+  return max(1, (tiles + s - 1) / s) * kBN;
 }
 
 ATTN_DEVINL int checked_len(int n, int cap) { return n < 0 || n > cap ? 0 : n; }
@@ -212,11 +253,16 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       seen += __shfl_sync(0xffffffffu, upto, 31);
     }
     if (bad) attn_flag_error(kErrBadIndex);
+    const int cap = a.max_pages * a.page_size;
+    if ((len_of < 0 || len_of > cap) && lane == 0) attn_flag_error(kErrBadIndex);
+    len_of = checked_len(len_of, cap);
+    const int chunk = chunk_of(a.cost, len_of, a.most, lane);
     if (lane == 0) {
       bars.unit[0] = p_of;
       bars.unit[1] = first_of;
       bars.unit[2] = n_of;
       bars.unit[3] = len_of;
+      bars.unit[4] = chunk;
     }
   }
   tc::fence_before_sync();
@@ -229,16 +275,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   const int p = bars.unit[0], b0 = bars.unit[1], n_req = bars.unit[2];
 
   // This CTA's keys, and their pages checked (all before any is read).
-  const int cap = a.max_pages * a.page_size;
   int n_keys = 0, key0 = 0;
   const int* table = nullptr;
   bool bad = false;
   if (p >= 0) {
-    const int len = bars.unit[3];
-    if ((len < 0 || len > cap) && tid == 0) attn_flag_error(kErrBadIndex);
-    const int n = checked_len(len, cap);
-    key0 = min(n, int(blockIdx.x) * a.chunk);
-    n_keys = min(n - key0, a.chunk);
+    const int n = bars.unit[3], chunk = bars.unit[4];
+    key0 = int(min((long long)n, 1LL * blockIdx.x * chunk));
+    n_keys = min(n - key0, chunk);
     table = a.prefix_table + size_t(p) * a.max_pages;
   }
   const int page0 = key0 / a.page_size;
@@ -638,7 +681,8 @@ struct SharedMergeArgs {
   const int* prefix_lens;
   const int* prefix_start;
   const int* seq_lens;
-  int rows, Hq, d, B, n_prefix, prefix_cap, prefix_chunk, own_cap, own_chunk, s_own, stride;
+  int rows, Hq, d, B, n_prefix, prefix_cap, own_cap, own_chunk, s_own, stride;
+  SplitCost cost;
 };
 
 __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
@@ -655,7 +699,8 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(SharedMergeArgs a) {
     const uint32_t hit = __ballot_sync(0xffffffffu, first <= b && b < last);
     if (hit) {
       const int n = checked_len(__ldcg(a.prefix_lens + p0 + __ffs(hit) - 1), a.prefix_cap);
-      np = (n + a.prefix_chunk - 1) / a.prefix_chunk;
+      const int chunk = chunk_of(a.cost, n, a.s_own, lane);
+      np = (n + chunk - 1) / chunk;
       break;
     }
   }
@@ -750,7 +795,7 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
   const PrefixArgs pa{a.prefix_table, a.prefix_lens, a.prefix_start, a.own.o_part, a.own.m_part,
                       a.own.l_part, a.own.B, a.own.Hq, a.own.Hkv, G, a.n_prefix,
                       a.num_prefix_pages, a.prefix_page_size, a.max_prefix_pages, pl.box_rows,
-                      pl.prefix_chunk, pl.prefix_splits + pl.own_splits, joined, a.own.scale};
+                      pl.prefix_splits, pl.prefix_splits + pl.own_splits, pl.cost, joined, a.own.scale};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.prefix_splits, a.own.Hkv, pl.units);
   cfg.blockDim = dim3(kThreads);
@@ -766,8 +811,8 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
 
 }  // namespace
 
-// How a call is cut, from its sizes alone (group sizes and lengths are only
-// known on the device).
+// How a call is cut, as far as its sizes tell (group sizes and lengths are
+// only known on the device).
 SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_page_size,
                        int max_prefix_pages, int page_size, int max_pages, int prefix_splits,
                        int own_splits) {
@@ -790,36 +835,34 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
     const long long want = (3 * sms + 1LL * B * Hkv - 1) / (1LL * B * Hkv);
     own_splits = int(std::min((own_cap + 511) / 512, std::max(4LL, want)));
   }
+  // Both parts run at once, so a call takes as long as a prefix CTA, or as
+  // the work of both spread over all SMs, then as the merge of the splits;
+  // where the two meet, shorter CTAs pack better (0.15 of a CTA's time).
+  // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
+  // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
+  // its partial rows; own keys, half their capacity but 512 at most (the
+  // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
+  // partials for every split to merge. (64 requests behind 8192 keys: 87, 65,
+  // 53, 57, 61 us with 2, 3, 4, 5, 8 splits, 69 with 19, which fill the
+  // device; 128 of them 103, 92, 93 with 2, 3, 4; 96 behind three prefixes up
+  // to 32768: 147, 117, 117, 124 with 3, 4, 5, 6.) Here for what the table can
+  // hold, which bounds the splits of all prefixes; each prefix's own are chosen
+  // by the same costs from its length, on the device.
+  pl.cost.tile = float((pl.pair ? 2.3 : 1.2) * d / 128);
+  pl.cost.filled =
+      float(1.0 * Hkv * std::max<long long>(n_prefix, (rows + per - 1) / per) / double(sms));
+  pl.cost.work = pl.cost.tile * pl.cost.filled;
+  pl.cost.own = float(1.0 * B * Hkv * std::min(own_cap / 2, 512LL) * d * 4 / 3e6);
+  pl.cost.merge = float(0.5 + 0.6e-6 * B * Hq * d * 4);
+  pl.cost.fixed = prefix_splits > 0;
   if (prefix_splits <= 0) {
-    // Both parts run at once, so a call takes as long as a prefix CTA, or as
-    // the work of both spread over all SMs, then as the merge of the splits;
-    // where the two meet, shorter CTAs pack better (0.15 of a CTA's time).
-    // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
-    // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
-    // its partial rows; own keys, half their capacity but 512 at most (the
-    // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
-    // partials for every split to merge. (64 requests behind 8192 keys: 87, 65,
-    // 53, 57, 61 us with 2, 3, 4, 5, 8 splits, 69 with 19, which fill the
-    // device; 128 of them 103, 92, 93 with 2, 3, 4; 96 behind three prefixes up
-    // to 32768: 147, 117, 117, 124 with 3, 4, 5, 6.)
-    const double tile = (pl.pair ? 2.3 : 1.2) * d / 128, tiles_all = double(tiles);
-    const double ctas = double(Hkv) * std::max<long long>(n_prefix, (rows + per - 1) / per);
-    const double own = 1.0 * B * Hkv * std::min(own_cap / 2, 512LL) * d * 4 / 3e6;
-    const double merge = 0.5 + 0.6e-6 * B * Hq * d * 4;
-    double best = 0;
     prefix_splits = 1;
-    for (int s = 1; s <= 64 && s <= tiles; ++s) {
-      const double cta = (double((tiles + s - 1) / s) + 4) * tile * std::ceil(ctas * s / sms);
-      const double all = ctas * (tiles_all + 4 * s) * tile / sms + own;
-      const double cost = std::max(cta, all) + 0.15 * cta + s * merge;
-      if (s == 1 || cost < best) {
-        best = cost;
+    for (int s = 2; s <= kMostSplits && s <= tiles; ++s)
+      if (split_cost(pl.cost, int(tiles), s) < split_cost(pl.cost, int(tiles), prefix_splits))
         prefix_splits = s;
-      }
-    }
   }
+  // (as many as the longest prefix would use)
   const long long per_split = (tiles + prefix_splits - 1) / prefix_splits;
-  pl.prefix_chunk = int(per_split * kBN);
   pl.prefix_splits = int((tiles + per_split - 1) / per_split);
   pl.own_splits = own_splits;
   // copies of a key tile: whole tiles of a single page, else the largest
@@ -851,8 +894,8 @@ cudaError_t launch_decode_shared(const SharedArgs& a, const SharedPlan& pl) {
                           static_cast<__nv_bfloat16*>(a.own.o), a.own.lse, a.prefix_lens,
                           a.prefix_start, a.own.seq_lens, a.own.B * a.own.Hq, a.own.Hq, a.own.d,
                           a.own.B, a.n_prefix, a.max_prefix_pages * a.prefix_page_size,
-                          pl.prefix_chunk, a.own.max_pages * a.own.page_size, decode_chunk(own),
-                          pl.prefix_splits, own.part_stride};
+                          a.own.max_pages * a.own.page_size, decode_chunk(own), pl.prefix_splits,
+                          own.part_stride, pl.cost};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((m.rows + 7) / 8));
   cfg.blockDim = dim3(256);

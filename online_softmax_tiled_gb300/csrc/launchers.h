@@ -104,10 +104,20 @@ struct SharedArgs {
   const int* prefix_start;
   int n_prefix, num_prefix_pages, prefix_page_size, max_prefix_pages;
 };
+// Time of a call behind a prefix of `tiles` key tiles cut into s splits, in
+// microseconds (see shared_plan, which makes it).
+struct SplitCost {
+  float tile;              // a key tile in a CTA
+  float work;              // a key tile in all CTAs of a split, over the device
+  float own, merge;        // the own keys; merging a split
+  float filled;            // CTAs of a split per SM
+  int fixed;               // every prefix takes all splits (no choice left)
+};
 struct SharedPlan {
   bool pair;               // 256 query rows per CTA (else 128)
   int units;               // most runs of query rows
-  int prefix_splits, prefix_chunk, own_splits;
+  int prefix_splits, own_splits;   // most splits (the partials' stride)
+  SplitCost cost;
   int box_rows;            // rows of one copy of prefix keys
 };
 

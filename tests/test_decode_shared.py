@@ -397,3 +397,22 @@ def test_eight_query_heads_of_128(ost, B, Hq, Hkv, d, start, plens, ppage, lens,
     o, lse = ost.decode_shared(*(x[n] for n in ORDER), sp, so)
     torch.cuda.synchronize()
     _check(o, lse, x, d ** -0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,d,plens", [(16, 8, 2, 64, [4096]), (64, 16, 4, 128, [6400]),
+                                              (40, 16, 4, 128, [8192, 1600])])
+@pytest.mark.parametrize("wider", [3, 16])
+def test_a_wider_table_changes_nothing(ost, B, Hq, Hkv, d, plens, wider):
+    """Splits follow each prefix's own length, not what its table could hold:
+    the same bits from a table with many unused columns."""
+    start = [0, B] if len(plens) == 1 else [0, B // 3, B]
+    x = _case(B, Hq, Hkv, d, start, plens, 16, [5] * B, 16, seed=B)
+    o, lse = ost.decode_shared(*(x[n] for n in ORDER))
+    torch.cuda.synchronize()
+    _check(o, lse, x, d ** -0.5)
+    pt = x["prefix_table"]
+    x["prefix_table"] = torch.cat([pt, torch.full_like(pt, -1).repeat(1, wider - 1)], 1)
+    o2, lse2 = ost.decode_shared(*(x[n] for n in ORDER))
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
