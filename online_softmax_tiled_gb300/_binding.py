@@ -15,7 +15,7 @@ import os
 
 import torch
 
-from ._build import CALLS_PATH, LIB_PATH
+from ._build import CALLS_PATH, LIB_PATH, calls_current
 
 ATTN_OK = 0
 ATTN_F32 = 0
@@ -157,6 +157,9 @@ def _calls():
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} missing: run "
                                "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        if not calls_current():
+            raise RuntimeError(f"{CALLS_PATH} was built for another Python or torch: run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` again")
         spec = importlib.util.spec_from_file_location("_cache_calls", CALLS_PATH)
         calls = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(calls)

@@ -6,7 +6,10 @@ Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel into
 (``include/attn.h``). The CUDA runtime is linked statically; the driver's
 tensor-map encoder is fetched at run time, so the library loads on machines
 without a GPU. Rebuilds happen only when a source or header is newer than the
-library.
+library. The Python calls need the host compiler and the headers of this Python
+and the installed torch; they hold for those alone, so what they were built
+against is written beside them and a change of it rebuilds them. The library
+needs none of that: it is linked even where the calls cannot be built.
 """
 
 from __future__ import annotations
@@ -25,6 +28,7 @@ BUILD_DIR = os.path.join(REPO_DIR, "_build")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_gb300.so")
 CALLS_PATH = os.path.join(LIB_DIR, "_cache_calls.so")
+STAMP_PATH = CALLS_PATH + ".stamp"
 
 SOURCES = ["api.cu", "fwd_simt.cu", "fwd_tc.cu", "fwd_tc64.cu", "bwd_aux.cu", "bwd_simt.cu", "bwd_tc.cu",
            "bwd_dq.cu", "decode.cu", "decode_shared.cu", "api_cache.cu", "rope.cu",
@@ -79,10 +83,33 @@ def _calls_commands(obj: str, out: str):
     return compile_, link
 
 
+def calls_stamp() -> str:
+    """What the Python calls hold for: this Python and the installed torch."""
+    import torch
+    return " ".join([str(sysconfig.get_config_var("SOABI")), torch.__version__,
+                     f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                     os.path.dirname(os.path.abspath(torch.__file__))])
+
+
+def calls_current() -> bool:
+    """Whether the built Python calls are for this Python and torch."""
+    if not (os.path.exists(CALLS_PATH) and os.path.exists(STAMP_PATH)):
+        return False
+    try:
+        with open(STAMP_PATH) as f:
+            return f.read() == calls_stamp()
+    except ImportError:
+        return False
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link the library if needed; return its path."""
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _inputs_mtime()
-                         for p in (LIB_PATH, CALLS_PATH)):
+    newest = _inputs_mtime()
+
+    def fresh(path):
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= newest
+    lib_fresh, calls_fresh = fresh(LIB_PATH), fresh(CALLS_PATH) and calls_current()
+    if lib_fresh and calls_fresh:
         return LIB_PATH
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -94,21 +121,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         out = _run([nvcc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
         return obj, out
 
-    tmp_calls = CALLS_PATH + ".tmp"
-    calls_compile, calls_link = _calls_commands(os.path.join(BUILD_DIR, "py_cache.o"), tmp_calls)
+    def compile_calls():
+        tmp = CALLS_PATH + ".tmp"
+        compile_, link = _calls_commands(os.path.join(BUILD_DIR, "py_cache.o"), tmp)
+        _run(compile_)
+        return link, tmp
+
     with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(_run, calls_compile)
-        results = list(ex.map(compile_one, SOURCES))
-        calls.result()
-    if verbose or ptxas_info:
-        for (_, out), src in zip(results, SOURCES):
-            if out.strip():
-                print(f"--- {src}\n{out}")
-    tmp = LIB_PATH + ".tmp"
-    _run([nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *[o for o, _ in results]])
-    os.replace(tmp, LIB_PATH)
-    _run(calls_link)
-    os.replace(tmp_calls, CALLS_PATH)
+        calls = None if calls_fresh else ex.submit(compile_calls)
+        if not lib_fresh:
+            results = list(ex.map(compile_one, SOURCES))
+            if verbose or ptxas_info:
+                for (_, out), src in zip(results, SOURCES):
+                    if out.strip():
+                        print(f"--- {src}\n{out}")
+            tmp = LIB_PATH + ".tmp"
+            _run([nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *[o for o, _ in results]])
+            os.replace(tmp, LIB_PATH)
+        if calls is not None:
+            link, tmp = calls.result()   # (an error of theirs comes behind the linked library)
+            _run(link)
+            if os.path.exists(STAMP_PATH):
+                os.remove(STAMP_PATH)
+            os.replace(tmp, CALLS_PATH)
+            with open(STAMP_PATH, "w") as f:
+                f.write(calls_stamp())
     return LIB_PATH
 
 
