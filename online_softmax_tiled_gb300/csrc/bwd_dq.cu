@@ -82,21 +82,6 @@ ATTN_DEVINL void tma_store_commit_and_wait() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-ATTN_DEVINL void named_bar_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-ATTN_DEVINL void tmem_st32(uint32_t ta, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(ta), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 // D = X Yᵀ over the head dimension into tensor memory at d_tmem: X and Y
 // are 128 x d tiles (K-major, 128-byte swizzle, 64-column atoms of 128 rows)
 // at shared addresses xa and ya. Called by every lane of the issuing warp.
@@ -413,7 +398,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       uint32_t pk[32];                             // dS_j as bf16 pairs
       ds_pairs<kGeneral>(sr, dr, c, nl, nd, masked, key0, limit, vis0, vis1, pk);
       // over the S_j columns this warpgroup has just read
-      tmem_st32(s_addr, pk);
+      tc::tmem_st32(s_addr, pk);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       mbar_arrive(&bars.p_full[j & 1]);
@@ -836,7 +821,7 @@ bwd_dq_persistent_kernel(const __grid_constant__ CUtensorMap map_q,
         uint32_t pk[32];                             // dS as bf16 pairs
         ds_pairs<false, kWin>(sr, dr, c, nl, nd, key0 + 63 > limit || (kWin && key0 < lo), key0,
                               limit, 0u, 0u, pk, lo);
-        tmem_st32(s_addr, pk);                       // over the S columns just read
+        tc::tmem_st32(s_addr, pk);                       // over the S columns just read
         tc::tmem_st_wait();
         tc::fence_before_sync();
         mbar_arrive(&bars.p_full[g & 1]);

@@ -108,6 +108,11 @@ ATTN_DEVINL void pdl_launch_dependents() {
 }
 ATTN_DEVINL void pdl_wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A barrier of `count` threads of the CTA, one of 16.
+ATTN_DEVINL void named_bar_sync(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Register re-split between warpgroups (all warps of a warpgroup execute it).
 template <int N> ATTN_DEVINL void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

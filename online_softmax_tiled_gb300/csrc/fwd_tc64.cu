@@ -107,21 +107,6 @@ ATTN_DEVINL void tma_store_wait_read() {
 }
 // every committed store has completed
 ATTN_DEVINL void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-ATTN_DEVINL void named_bar_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-ATTN_DEVINL void tmem_st32(uint32_t ta, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(ta), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 ATTN_DEVINL TileWork read_work(const TileWork* slot) {
   const volatile TileWork* v = slot;
   TileWork tw;
@@ -537,8 +522,8 @@ fwd_tc64_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!ok) break;
           tc::fence_after_sync();
         }
-        tmem_st32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        tc::tmem_st32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tc::tmem_st32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         const f2 rsa = add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3]));
         l_run = fmaf(alpha, l_run, rsa.x + rsa.y);
 
@@ -551,7 +536,7 @@ fwd_tc64_kernel(const __grid_constant__ CUtensorMap map_q,
             tc::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-            tmem_st32(o_addr + ch * 32, orr);
+            tc::tmem_st32(o_addr + ch * 32, orr);
           }
         }
         tc::tmem_st_wait();
