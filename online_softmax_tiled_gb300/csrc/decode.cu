@@ -165,21 +165,26 @@ struct PagedKV {
   const int* seq_lens;
   int num_pages, page_size, max_pages;
   int rows;   // 1: sparse index list into the per-request cache
-  // Launched behind a kernel of the same call that waited for everything
-  // before it and writes nothing this kernel reads (the shared prefix's
-  // part): this grid does not wait for it at its start. Its last CTA waits
-  // before it leaves, so that the grid's completion implies the partner's.
-  // The partner lets this grid start only once what precedes the call is
-  // complete and in L2; a grid that has not waited itself is not promised
-  // that its SM's L1 holds nothing older, so everything read here comes from
-  // L2 (keys and values through the bulk copies, the rest by __ldcg).
-  int after_partner;
 };
 
 // Where a chunk's keys come from: a contiguous cache, pages of a paged
 // cache (bulk copies by one thread), or a list of rows (tile::gather4 copies
 // of four rows each, issued by the lanes of warp 0).
-enum KeySource : int { kContiguous = 0, kPages = 1, kListedRows = 2 };
+//
+// kPagesBehind: pages, launched behind a kernel of the same call that waited
+// for everything before it and writes nothing this kernel reads (the shared
+// prefix's part). This grid does not wait for it at its start; its last CTA
+// waits before it leaves, so that the grid's completion implies the partner's.
+// The partner lets this grid start only once what precedes the call is
+// complete and in L2; a grid that has not waited itself is not promised that
+// its SM's L1 holds nothing older, so everything read here comes from L2 (keys
+// and values through the bulk copies, the rest by load_once). A form of its
+// own: as a branch of the others it cost them 1 to 2 %.
+enum KeySource : int { kContiguous = 0, kPages = 1, kListedRows = 2, kPagesBehind = 3 };
+
+template <int kSource, typename T> ATTN_DEVINL T load_once(const T* p) {
+  return kSource == kPagesBehind ? __ldcg(p) : *p;
+}
 
 // Four rows of a 2-D tensor map (box: one row of `cols` elements), given by
 // their row coordinates, into consecutive rows at smem_dst (tile::gather4).
@@ -202,6 +207,8 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
                     const __grid_constant__ CUtensorMap map_k_rows,
                     const __grid_constant__ CUtensorMap map_v_rows) {
   constexpr bool kPaged = kSource != kContiguous;   // keys reached through a table
+  constexpr bool kBehind = kSource == kPagesBehind;
+  constexpr bool kInPages = kSource == kPages || kBehind;
   constexpr int NV = D / 64;                       // 16-byte pieces per lane per row
   constexpr int kRowBytes = D * 2;
   constexpr int kStageBytes = kStageKeys * kRowBytes;
@@ -213,7 +220,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   __shared__ uint64_t full_bar[kStages];
   __shared__ int abort_flag;
   __shared__ int chunk_pages[kPaged ? kChunkPagesCached : 1];
-  constexpr int kPreStages = kSource == kPages ? 64 : 1;
+  constexpr int kPreStages = kInPages ? 64 : 1;
   __shared__ size_t stage_src[kPreStages][2];   // element offsets of a stage's one or two segments
   __shared__ int stage_rows[kPreStages][2];
 
@@ -235,8 +242,8 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   // (q, the KV cache, the partials a previous merge may still be reading)
   // comes after the preceding grid has completed (or, behind a partner, after
   // the one before that).
-  if (!pg.after_partner) pdl_wait_primary();
-  const bool wait_at_end = pg.after_partner && blockIdx.x == gridDim.x - 1 &&
+  if (!kBehind) pdl_wait_primary();
+  const bool wait_at_end = kBehind && blockIdx.x == gridDim.x - 1 &&
                            blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
 
   // This CTA's keys [key_begin, key_end): chunk s of its request.
@@ -248,7 +255,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   if (kPaged) {
     // The length and every table entry the chunk can touch, as independent
     // loads; entries are checked once the length says which ones are used.
-    Lb = __ldcg(pg.seq_lens + b);
+    Lb = load_once<kSource>(pg.seq_lens + b);
     const int nominal = s * chunk;
     p_first = nominal / pg.page_size;
     const int p_cap = min(pg.max_pages, (min(max_len, nominal + chunk) + pg.page_size - 1) /
@@ -257,7 +264,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int p = p_first + tid + i * kThreads;
-      ent[i] = p < p_cap ? __ldcg(table_row + p) : 0;
+      ent[i] = p < p_cap ? load_once<kSource>(table_row + p) : 0;
     }
     if (Lb < 0 || Lb > max_len) {
       if (s == 0 && g == 0 && tid == 0) attn_flag_error(kErrBadIndex);
@@ -273,7 +280,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
     // chunks of more than 4 x kThreads pages (pages far smaller than the
     // chunk): the rest checked straight from the table
     for (int p = p_first + 4 * kThreads + tid; p < p_used; p += kThreads) {
-      const int e = __ldcg(table_row + p);
+      const int e = load_once<kSource>(table_row + p);
       bad |= e < 0 || e >= pg.num_pages;
     }
   }
@@ -307,14 +314,15 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
   const size_t page_elems = sparse ? size_t(D) : size_t(Hkv) * pg.page_size * D;
   auto page_of = [&](int t) {
     const int i = t / pg.page_size - p_first;
-    return i < kChunkPagesCached ? chunk_pages[i] : __ldcg(table_row + t / pg.page_size);
+    return i < kChunkPagesCached ? chunk_pages[i]
+                                 : load_once<kSource>(table_row + t / pg.page_size);
   };
   // Paged bulk copies: with pages of a multiple of 16 keys a 32-key stage
   // touches at most two pages, and the source offsets of the first
   // kPreStages stages are worked out here by all threads at once, so the
   // copying thread spends a few instructions per stage (the per-stage
   // barrier waits for it) instead of dividing by the page size.
-  const bool pre = kSource == kPages && pg.page_size % 16 == 0;
+  const bool pre = kInPages && pg.page_size % 16 == 0;
   if (pre) {
     for (int st = tid; st < min(nstages, kPreStages); st += kThreads) {
       const int t0 = key_begin + st * kStageKeys;
@@ -411,7 +419,7 @@ decode_split_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
     const __nv_bfloat16* qh = q + (size_t(b) * Hq + gy * G + h) * D;
 #pragma unroll
     for (int vv = 0; vv < NV; ++vv) {
-      const uint4 w = __ldcg(reinterpret_cast<const uint4*>(qh + 64 * vv + 8 * sub));
+      const uint4 w = load_once<kSource>(reinterpret_cast<const uint4*>(qh + 64 * vv + 8 * sub));
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) qf[h][vv * 4 + e] = f2{bf16lo(ws[e]) * qs, bf16hi(ws[e]) * qs};
@@ -638,7 +646,7 @@ cudaError_t launch_split_t(const DecodeArgs& a, int rgroups) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const PagedKV pg{a.block_table, a.seq_lens, a.num_pages, a.page_size, a.max_pages,
-                   a.sparse ? 1 : 0, a.after_partner ? 1 : 0};
+                   a.sparse ? 1 : 0};
   // listed rows: the caches as [B·Hkv·L rows][d] for row gathers
   CUtensorMap mk{}, mv{};
   if (kSource == kListedRows) {
@@ -680,6 +688,8 @@ cudaError_t launch_split_d(const DecodeArgs& a) {
 cudaError_t launch_decode_split(const DecodeArgs& a) {
   if (a.block_table != nullptr && a.sparse)
     return a.d == 64 ? launch_split_d<64, kListedRows>(a) : launch_split_d<128, kListedRows>(a);
+  if (a.after_partner)
+    return a.d == 64 ? launch_split_d<64, kPagesBehind>(a) : launch_split_d<128, kPagesBehind>(a);
   if (a.block_table != nullptr)
     return a.d == 64 ? launch_split_d<64, kPages>(a) : launch_split_d<128, kPages>(a);
   return a.d == 64 ? launch_split_d<64, kContiguous>(a) : launch_split_d<128, kContiguous>(a);
