@@ -376,7 +376,8 @@ ATTN_API attn_status attn_decode_splitkv_noalloc(const void* q, const void* k_ca
  * for attn_decode_paged; both pools may be the same. prefix_start [n_prefix+1]
  * int32, not decreasing. All tables and lengths in DEVICE memory. o [B,Hq,d]
  * bf16; lse [B,Hq] float32 (may be NULL). A request without any key gets
- * O = 0, LSE = -inf. d 64 or 128; Hq/Hkv in {1, 2, 4, 8}.
+ * O = 0, LSE = -inf. d 64 or 128; Hq/Hkv in {1, 2, 4, 8}; scale positive and
+ * finite.
  * num_prefix_splits, num_splits: most splits of a prefix's keys and of a
  * request's own; 0 takes the library's choice. A prefix is cut by its own
  * length, on the device, so columns of prefix_table that no prefix uses cost
@@ -438,14 +439,14 @@ typedef struct {
  * (k, k_out ignored). q_out == q and k_out == k with equal strides turn in
  * place; any other row of an output that shares a byte with an input or with
  * the other output is refused (rows between each other's, as of views of one
- * buffer, are fine). d even and <= 512,
- * rot_dim even, 2 <= rot_dim <= d. positions int32 in DEVICE memory, any
- * value, negative included; position_batch_stride 0 shares one row among all
- * requests. inv_freq float64 [rot_dim/2] in DEVICE memory, where any scaling
- * for long contexts is already contained; the angle is reduced modulo one
- * turn in 64-bit fixed point: below 2^64 radians a position it is off by less
- * than 2^-32 turns at every position before it is rounded to float32. A
- * frequency that is not finite, or of 2^64 and more, gives NaN in its pairs.
+ * buffer, are fine). d even and <= 512, rot_dim even, 2 <= rot_dim <= d.
+ * positions int32 in DEVICE memory, any value, negative included;
+ * position_batch_stride 0 shares one row among all requests. inv_freq float64
+ * [rot_dim/2] in DEVICE memory, where any scaling for long contexts is already
+ * contained; the angle is reduced modulo one turn in 64-bit fixed point: below
+ * 2^64 radians a position it is off by less than 2^-32 turns at every position
+ * before it is rounded to float32. A frequency that is not finite, or of 2^64
+ * and more, gives NaN in its pairs.
  * Rows at multiples of 16 bytes with d and rot_dim multiples of 16 (bf16) or
  * 8 (float32) move in 16-byte pieces; everything else element by element.
  * Pointers need their element's alignment only. B*N at most 2^31 - 256.

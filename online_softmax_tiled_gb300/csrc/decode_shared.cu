@@ -779,7 +779,8 @@ cudaError_t launch_prefix_t(const SharedArgs& a, const SharedPlan& pl) {
   const PrefixArgs pa{a.prefix_table, a.prefix_lens, a.prefix_start, a.own.o_part, a.own.m_part,
                       a.own.l_part, a.own.B, a.own.Hq, a.own.Hkv, G, a.n_prefix,
                       a.num_prefix_pages, a.prefix_page_size, a.max_prefix_pages, pl.box_rows,
-                      pl.prefix_splits, pl.prefix_splits + pl.own_splits, pl.cost, joined, a.own.scale};
+                      pl.prefix_splits, pl.prefix_splits + pl.own_splits, pl.cost, joined,
+                      a.own.scale};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.prefix_splits, a.own.Hkv, pl.units);
   cfg.blockDim = dim3(kThreads);
@@ -822,17 +823,17 @@ SharedPlan shared_plan(int B, int Hq, int Hkv, int d, int n_prefix, int prefix_p
   // Both parts run at once, so a call takes as long as a prefix CTA, or as
   // the work of both spread over all SMs, then as the merge of the splits;
   // where the two meet, shorter CTAs pack better (0.15 of a CTA's time).
-  // In microseconds, as measured for d = 128 (d = 64 takes half): 1.2 for a
-  // key tile, 2.3 where it feeds 256 rows; four tiles for a CTA's start and
-  // its partial rows; own keys, half their capacity but 512 at most (the
-  // capacity says little of the lengths), at 3 TB/s; 0.5 + 0.6 per MB of
-  // partials for every split to merge. (64 requests behind 8192 keys: 87, 65,
-  // 53, 57, 61 us with 2, 3, 4, 5, 8 splits, 69 with 19, which fill the
-  // device; 128 of them 103, 92, 93 with 2, 3, 4; 96 behind three prefixes up
-  // to 32768: 147, 117, 117, 124 with 3, 4, 5, 6.) Here for what the table can
-  // hold, which bounds the splits of all prefixes; each prefix's own are chosen
-  // by the same costs from its length, on the device.
-  pl.cost.tile = float((pl.pair ? 2.3 : 1.2) * d / 128);
+  // In microseconds, as measured: 1.2 for a key tile, 2.3 where it feeds 256
+  // rows (1.8 with d = 64); four tiles for a CTA's start and its partial rows;
+  // own keys, half their capacity but 512 at most (the capacity says little of
+  // the lengths), at 3 TB/s; 0.5 + 0.6 per MB of partials for every split to
+  // merge. (64 requests behind 8192 keys: 87, 65, 53, 57, 61 us with 2, 3, 4,
+  // 5, 8 splits, 69 with 19, which fill the device; 128 of them 103, 92, 93
+  // with 2, 3, 4; 96 behind three prefixes up to 32768: 147, 117, 117, 124
+  // with 3, 4, 5, 6.) Here for what the table can hold, which bounds the splits
+  // of all prefixes; each prefix's own are chosen by the same costs from its
+  // length, on the device.
+  pl.cost.tile = pl.pair ? (d == 64 ? 1.8f : 2.3f) : 1.2f;
   pl.cost.filled =
       float(1.0 * Hkv * std::max<long long>(n_prefix, (rows + per - 1) / per) / double(sms));
   pl.cost.work = pl.cost.tile * pl.cost.filled;
