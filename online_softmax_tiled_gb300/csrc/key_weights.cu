@@ -73,9 +73,11 @@ struct KwArgs {
   float c, inv_scale, decay;   // scale · log2 e, 1 / scale
 };
 
+// (kEarly: read before the kernel has waited, so from L2)
+template <bool kEarly = false>
 ATTN_DEVINL int request_len(const KwArgs& a, int b, bool& bad) {
   if (a.seq_lens == nullptr) return a.cap;
-  const int n = __ldcg(a.seq_lens + b);
+  const int n = kEarly ? __ldcg(a.seq_lens + b) : a.seq_lens[b];
   const bool wrong = n < 0 || n > a.cap;
   bad |= wrong;
   return wrong ? 0 : n;
@@ -1061,7 +1063,7 @@ weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
   // steps of all requests, and of those before this one
   long long total = 0, before = 0;
   for (int i = tid; i < a.B; i += kBlock) {
-    const long long s = steps_of_head(a, rs, request_len(a, i, bad)) * a.Hkv;
+    const long long s = steps_of_head(a, rs, request_len<true>(a, i, bad)) * a.Hkv;
     total += s;
     if (i < b) before += s;
   }
@@ -1080,7 +1082,7 @@ weights_join_kernel(KwArgs a, RowSteps rs, int grid) {
     total += sums[0][w];
     before += sums[1][w];
   }
-  const int n = request_len(a, b, bad), j = k * kBlock + tid;
+  const int n = request_len<true>(a, b, bad), j = k * kBlock + tid;
   const long long first = before + g * steps_of_head(a, rs, n) + steps_before(a, rs, n, k);
   const long long each = steps_per_cta(rs, total, grid);
   const long long last = first + steps_of(a, rs, n, k) - 1;
