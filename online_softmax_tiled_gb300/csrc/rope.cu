@@ -25,10 +25,10 @@
 // of 16 bytes take the same kernel with V = 1.
 //
 // Measured: 2 x 8192 tokens of 40 bf16 heads of 128 out of a fused projection
-// 52.5 us (6.4 TB/s, 0.94 of a plain copy; 86 us where the views start one
+// 53.0 us (6.3 TB/s, 0.93 of a plain copy; 86 us where the views start one
 // element off and take V = 1). 2 x 4096 tokens of 20 heads, half of each
-// turned, interleaved, as a gradient: 16.8 us (5.0 TB/s). One token of 64
-// requests: 4.7 us back to back from Python, 3.1 in a CUDA graph.
+// turned, interleaved, as a gradient: 16.4 us (5.1 TB/s). One token of 64
+// requests: 4.8 us back to back from Python, 2.8 in a CUDA graph.
 
 #include "common.cuh"
 #include "launchers.h"
@@ -153,8 +153,10 @@ rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ position
       const uint64_t t = uint64_t(p) * turns_of(w) + 0x80000000ull;
       float s, co;
       sincospif(float(int(uint32_t(t >> 32))) * 0x1p-31f, &s, &co);
-      // a frequency that is not finite, or too large, gives NaN, not a wrong angle
-      const float m = fabs(w) < 0x1p64 ? magnitude : __int_as_float(0x7fffffff);
+      // a frequency that is not finite, or of 2^64 and more, gives NaN, not a
+      // wrong angle (its exponent tells; comparing float64 values is slow here)
+      const bool good = ((uint64_t(__double_as_longlong(w)) >> 52) & 0x7ff) < 1023 + 64;
+      const float m = good ? magnitude : __int_as_float(0x7fffffff);
       cs[i] = co * m;
       sn[i] = inverse ? -s * m : s * m;
     }
