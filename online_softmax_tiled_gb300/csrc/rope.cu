@@ -25,7 +25,7 @@
 // of 16 bytes take the same kernel with V = 1.
 //
 // Measured: 2 x 8192 tokens of 40 bf16 heads of 128 out of a fused projection
-// 53.0 us (6.3 TB/s, 0.93 of a plain copy; 86 us where the views start one
+// 53.0 us (6.3 TB/s, 0.93 of a plain copy; 88 us where the views start one
 // element off and take V = 1). 2 x 4096 tokens of 20 heads, half of each
 // turned, interleaved, as a gradient: 16.4 us (5.1 TB/s). One token of 64
 // requests: 4.8 us back to back from Python, 2.8 in a CUDA graph.

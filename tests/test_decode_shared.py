@@ -416,3 +416,15 @@ def test_a_wider_table_changes_nothing(ost, B, Hq, Hkv, d, plens, wider):
     o2, lse2 = ost.decode_shared(*(x[n] for n in ORDER))
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_splits_than_a_warp_has_lanes(ost, d):
+    """Splits asked for by the caller, more than are ever chosen: a row's
+    partials are merged in several rounds, at every remainder of eight."""
+    x = _case(5, 8, 2, d, [0, 2, 5], [9000, 4500], 16, [1500, 0, 33, 700, 1100], 16, seed=d)
+    for sp, so in ((70, 40), (71, 1), (1, 47), (65535, 3)):
+        o, lse = ost.decode_shared(*(x[n] for n in ORDER), sp, so)
+        torch.cuda.synchronize()
+        _check(o, lse, x, d ** -0.5)
