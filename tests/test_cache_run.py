@@ -168,3 +168,53 @@ def test_library_calls_alone_hand_over_queries_and_lengths(ost):
     for _ in range(5):
         for a, b in zip(want, run(False)):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_allocating_calls_captured_and_replayed(ost):
+    """Each call allocates its outputs and workspace inside a captured graph; two
+    graphs from one pool, replayed in turn on new inputs, give what the same
+    calls give outside."""
+    B, Hq, Hkv, d, L, P, T, keep = 6, 16, 2, 128, 300, 700, 40, 64
+    bf = torch.bfloat16
+    w = ost.rope_frequencies(d, device=DEV)
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    prefix = [torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+              torch.tensor([P], dtype=torch.int32, device=DEV),
+              torch.tensor([0, B], dtype=torch.int32, device=DEV)]
+    kp, vp = (random_like_shape((1, Hkv, P, d), bf, s).to(DEV) for s in (1, 2))
+
+    def inputs(seed):
+        x = [random_like_shape(s, bf, seed + i) for i, s in
+             enumerate([(B, Hq, d), (B, Hkv, L, d), (B, Hkv, L, d), (B, Hq, T, d)])]
+        g = torch.Generator().manual_seed(seed)
+        return [t.to(DEV) for t in x] + [
+            torch.randint(0, L + 1, (B,), generator=g).to(torch.int32).to(DEV),
+            torch.randint(0, 5000, (B,), generator=g).to(torch.int32).to(DEV),
+            torch.full((B, Hq, T), 6.0).to(DEV)]
+
+    def calls(q, k, v, qt, lens, pos, lt):
+        qr, _ = ost.rope(q, None, pos, w)
+        o, lse = ost.decode_shared(qr, kp, vp, *prefix, k, v, table, lens)
+        score = ost.key_weights(qt, k, lt, seq_lens=lens)             # joined sums
+        score = ost.key_weights(qr, k, lse, prev=score, out=score, seq_lens=lens)
+        return (qr, o, lse, score, *ost.evict(k, v, score, keep, 2, 5, seq_lens=lens))
+    x = inputs(10)
+    calls(*x)
+    torch.cuda.synchronize()
+    graphs, outs, pool = [], [], None
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            outs.append(calls(*x))
+        pool = graph.pool()
+        graphs.append(graph)
+    for seed in (20, 40, 60):
+        for a, b in zip(x, inputs(seed)):
+            a.copy_(b)
+        want = calls(*x)
+        for graph, got in zip(graphs, outs):
+            for t in got:
+                t.view(torch.uint8).fill_(0xff)        # (zeroed again by the graph itself)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, r) for p, r in zip(got, want))
