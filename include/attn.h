@@ -545,6 +545,159 @@ ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float*
                                       void* stream);
 
 /*
+ * Appending keys and values to a paged cache, with the rotation applied on the
+ * way.
+ *
+ * ML notes (haolingpu.github.io), KV-cache Q&A: a step's keys and values join
+ * the cache's pages; KV-compression post (shreyansh26.github.io): cached keys are
+ * held rotated. Request b brings m = new_lens[b] tokens (new_lens NULL: N), the
+ * last m of its n = seq_lens[b] keys: token i < m becomes row n - m + i, its key
+ * rotated as by attn_rope (bit for bit) at position positions[b *
+ * position_batch_stride + i] (positions NULL: at n - m + i), its value as it
+ * is. q is rotated at the same positions into q_out. Tokens i >= m are padding:
+ * their rows of q_out are left as they were, like all rows of the pages but those
+ * of new tokens.
+ *
+ * q [B,Hq,N,d], k and v [B,Hkv,N,d] in `dt`, at any non-negative strides (NULL:
+ * contiguous), q_out likewise; q_out == q with equal strides turns in place.
+ * Hq = 0: no queries (q, q_out ignored); Hq need not be a multiple of Hkv.
+ * k_pages, v_pages [num_pages,Hkv,page_size,d] in `dt` behind block_table
+ * [B,max_pages_per_seq] and seq_lens [B] as for attn_decode_paged (one that is
+ * given the lengths after this call reads the new keys). rot_dim even, 0 <=
+ * rot_dim <= d (0: no rotation, inv_freq ignored); inv_freq, interleaved,
+ * magnitude as for attn_rope. d 64 or 128. Entries of block_table that no new
+ * token falls into are not read. Nothing that is written may overlap what is read
+ * or written elsewhere (checked); two new tokens that block_table sends to one row
+ * leave either of them there.
+ * Rows at multiples of 16 bytes with rot_dim a multiple of 16 (interleaved: 8)
+ * move in 16-byte pieces; everything else element by element. q, q_out, k, v need
+ * their element's alignment only. B * N at most 2^31 - 256, page_size *
+ * max_pages_per_seq at most 2^30, fewer than 2^32 rows in a pool.
+ * Device-side checks: a request with seq_lens outside [0, capacity] or new_lens
+ * outside [0, min(N, n)] has no tokens; a token behind a page index outside [0,
+ * num_pages) is not stored (its q_out is written); attn_sync_status() reports
+ * ATTN_ERR_DEVICE_INDEX for both.
+ */
+ATTN_API attn_status attn_cache_append(const void* q, const attn_strides* q_strides, void* q_out,
+                                       const attn_strides* q_out_strides, const void* k,
+                                       const attn_strides* k_strides, const void* v,
+                                       const attn_strides* v_strides, void* k_pages, void* v_pages,
+                                       const int* block_table, const int* seq_lens,
+                                       const int* new_lens, const int* positions,
+                                       long long position_batch_stride, const double* inv_freq,
+                                       int B, int Hq, int Hkv, int N, int d, int rot_dim,
+                                       int interleaved, float magnitude, int num_pages,
+                                       int page_size, int max_pages_per_seq, attn_dtype dt,
+                                       void* stream);
+
+/*
+ * attn_cache_append into a cache held in 4 bits.
+ *
+ * A row of d elements is held as d/32 groups of 32 adjacent ones. A group's
+ * scale is bf16(max |x| / 6); its elements are the e2m1 codes nearest to
+ * x / scale (a sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6; ties to the even code,
+ * beyond 6 the code of 6), both from the float32 values of the rotated key or
+ * the value as it is, in IEEE divisions. An element is off by at most the scale
+ * (half the widest step between codes) while the scale is a normal number; a
+ * group whose scale underflows to 0 reads as zeros, one with an element that is
+ * not finite as NaN. The pools are
+ * k_codes, v_codes [num_pages,Hkv,page_size,d/2] bytes and k_scales, v_scales
+ * [num_pages,Hkv,page_size,d/32] bf16; byte (d/16) g + 2c + b of a row's codes
+ * holds elements 32c + 4g + 2b (low half) and 32c + 4g + 2b + 1 (g < 8, b < 2):
+ * the order in which the decode's matrix products take them. 9/16 of a byte an
+ * element. `dt` is the type of q, k, v and q_out. Otherwise as attn_cache_append.
+ */
+ATTN_API attn_status attn_cache_append4(const void* q, const attn_strides* q_strides, void* q_out,
+                                        const attn_strides* q_out_strides, const void* k,
+                                        const attn_strides* k_strides, const void* v,
+                                        const attn_strides* v_strides, void* k_codes,
+                                        void* k_scales, void* v_codes, void* v_scales,
+                                        const int* block_table, const int* seq_lens,
+                                        const int* new_lens, const int* positions,
+                                        long long position_batch_stride, const double* inv_freq,
+                                        int B, int Hq, int Hkv, int N, int d, int rot_dim,
+                                        int interleaved, float magnitude, int num_pages,
+                                        int page_size, int max_pages_per_seq, attn_dtype dt,
+                                        void* stream);
+
+/*
+ * The keys and values of a 4-bit cache (attn_cache_append4) as bf16, in the
+ * order of their positions: row j < seq_lens[b] of k_out[b, h] and v_out[b, h] is
+ * code * scale of key j, rounded once. For calls that take contiguous caches,
+ * as attn_fwd for the next chunk of a prompt, and for attn_cache_evict.
+ *
+ * k_out, v_out [B,Hkv,L,d] bf16; rows past a request's length are left as they
+ * were. B * Hkv at most 65535, otherwise the limits of attn_cache_append4.
+ * Outputs must not overlap inputs (checked).
+ * Device-side checks: a length outside [0, min(L, capacity)] counts as 0; a row
+ * behind a page index outside [0, num_pages) is left as it was;
+ * attn_sync_status() reports ATTN_ERR_DEVICE_INDEX for both.
+ */
+ATTN_API attn_status attn_cache_read4(const void* k_codes, const void* k_scales,
+                                      const void* v_codes, const void* v_scales,
+                                      const int* block_table, const int* seq_lens, void* k_out,
+                                      void* v_out, int B, int Hkv, int L, int num_pages,
+                                      int page_size, int max_pages_per_seq, int d, void* stream);
+
+/*
+ * Decode of T tokens per request over a paged cache, under a sliding window
+ * and the first tokens that stay visible.
+ *
+ * KV-compression post (shreyansh26.github.io): a streaming cache keeps the first
+ * tokens (attention sinks) and a recent window; ML notes, split-K notes: T query
+ * tokens, the exact (o, m, l) merge. The T queries are the last T of the n =
+ * seq_lens[b] positions (T = 1: a decode step; more: drafted tokens to be
+ * verified). Key j is visible to token i at position p = n - T + i iff
+ *     (j <= p and (window_left < 0 or j >= p - window_left)) or j < n_global,
+ * as under attn_mask {window_left, 0, n_global}; j < n throughout. A token
+ * without a visible key gets O = 0, LSE = -inf. What a hidden key's row holds
+ * does not matter.
+ *
+ * q, o [B,Hq,T,d] bf16, lse [B,Hq,T] float32 (may be NULL); k_pages, v_pages
+ * [num_pages,Hkv,page_size,d] bf16 behind block_table [B,max_pages_per_seq] and
+ * seq_lens [B], as for attn_decode_paged; entries of block_table whose pages hold
+ * no key that a token of the request sees are not read (pages that have left the
+ * window may have been given back). Any page_size >= 1, any Hq that is a multiple
+ * of Hkv, d 64 or 128, scale positive and finite, n_global >= 0. Keys are read
+ * once for every 8 query rows per KV head while Hq / Hkv * T <= 8, for every 16
+ * beyond. The probabilities enter the P·V product as two bf16 parts (2^-17 of one
+ * is lost at most); all softmax state is float32, and results do not depend on
+ * the order in which anything runs.
+ * Device-side checks: a length outside [0, capacity] counts as 0; keys behind a
+ * page index outside [0, num_pages) are not seen; attn_sync_status() reports
+ * ATTN_ERR_DEVICE_INDEX for both.
+ * B at most 65535, Hq / Hkv * T at most 65536, page_size * max_pages_per_seq at
+ * most 2^30, fewer than 2^32 rows in a pool, B * Hkv * ceil(Hq / Hkv * T / 8) *
+ * ceil(capacity / 64) below 2^30.
+ * workspace: at least attn_decode_window_workspace_size() bytes for the same
+ * sizes on the current device, 256-byte aligned; it depends on the device and on
+ * Hq / Hkv * T, not on the lengths.
+ */
+ATTN_API size_t attn_decode_window_workspace_size(int B, int Hq, int Hkv, int T, int d);
+ATTN_API attn_status attn_decode_window(const void* q, const void* k_pages, const void* v_pages,
+                                        const int* block_table, const int* seq_lens, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int T, int num_pages,
+                                        int page_size, int max_pages_per_seq, int d, float scale,
+                                        int window_left, int n_global, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
+/*
+ * attn_decode_window over a cache held in 4 bits (attn_cache_append4), with the
+ * same workspace. Attention over the values code * scale: the products with
+ * codes are exact, a group's scale multiplies their sum in float32 (K) or the
+ * probability (V), which then enters the product in float16 (2^-12 of it is
+ * lost). A group whose scale is not finite spoils its own elements of V, and the
+ * key that it belongs to in K, for the tokens that see it.
+ */
+ATTN_API attn_status attn_decode_cache4(const void* q, const void* k_codes, const void* k_scales,
+                                        const void* v_codes, const void* v_scales,
+                                        const int* block_table, const int* seq_lens, void* o,
+                                        float* lse, int B, int Hq, int Hkv, int T, int num_pages,
+                                        int page_size, int max_pages_per_seq, int d, float scale,
+                                        int window_left, int n_global, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
+/*
  * Self-test of the bounded device wait (no counterpart on the pages).
  *
  * Launches one warp on `stream` that waits, with the same bounded wait the

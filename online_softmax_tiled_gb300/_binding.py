@@ -93,6 +93,21 @@ _SIGNATURES = {
     "attn_key_weights": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 10 +
                          [ctypes.c_float, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
                           ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_cache_append": (ctypes.c_int, [ctypes.c_void_p] * 14 +
+                          [ctypes.c_longlong, ctypes.c_void_p] + [ctypes.c_int] * 7 +
+                          [ctypes.c_float] + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
+    "attn_cache_append4": (ctypes.c_int, [ctypes.c_void_p] * 16 +
+                           [ctypes.c_longlong, ctypes.c_void_p] + [ctypes.c_int] * 7 +
+                           [ctypes.c_float] + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
+    "attn_cache_read4": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int] * 7 +
+                         [ctypes.c_void_p]),
+    "attn_decode_window_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 5),
+    "attn_decode_window": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 8 +
+                           [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_decode_cache4": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] * 8 +
+                           [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_size_t, ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_sync_status": (ctypes.c_int, [ctypes.c_void_p]),
 }
@@ -395,6 +410,59 @@ def attn_cache_evict(k, v, scores, k_out, v_out, scores_out, kept, new_lens, n_s
                    seq_lens, block_table, _handle(stream))
 
 
+def attn_cache_append(q, k, v, k_pages, v_pages, block_table, seq_lens, q_out, inv_freq=None,
+                      positions=None, new_lens=None, interleaved: bool = False,
+                      magnitude: float = 1.0, stream=None):
+    """attn_cache_append on torch tensors: q, q_out [B,Hq,N,d] (or [B,Hq,d]: one
+    token; None: no queries), k, v [B,Hkv,N,d], last dimension contiguous, other
+    strides free; k_pages, v_pages [num_pages,Hkv,page_size,d] of k's dtype;
+    block_table [B,max_pages], seq_lens [B] (with the new tokens), new_lens [B]
+    (None: N) and positions as for attn_rope (None: a key's row) int32; inv_freq
+    float64 [rot_dim / 2] (None: no rotation)."""
+    _calls().append(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq, positions,
+                    new_lens, interleaved, magnitude, q_out, False, _handle(stream))
+
+
+def attn_cache_append4(q, k, v, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, q_out,
+                       inv_freq=None, positions=None, new_lens=None, interleaved: bool = False,
+                       magnitude: float = 1.0, stream=None):
+    """attn_cache_append into 4 bits: k_codes, v_codes uint8
+    [num_pages,Hkv,page_size,d/2], k_scales, v_scales bf16
+    [num_pages,Hkv,page_size,d/32]; otherwise as attn_cache_append."""
+    _calls().append4(q, k, v, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                     inv_freq, positions, new_lens, interleaved, magnitude, q_out, False,
+                     _handle(stream))
+
+
+def attn_cache_read4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k_out, v_out,
+                     stream=None):
+    """Rows of a 4-bit cache into k_out, v_out [B,Hkv,L,d] bf16."""
+    _calls().read4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k_out, v_out,
+                   _handle(stream))
+
+
+def attn_decode_window_workspace_size(B, Hq, Hkv, T, d) -> int:
+    """Workspace bytes of attn_decode_window and attn_decode_cache4 on the
+    current device."""
+    return int(lib().attn_decode_window_workspace_size(B, Hq, Hkv, T, d))
+
+
+def attn_decode_window(q, k_pages, v_pages, block_table, seq_lens, o, lse, scale: float,
+                       window_left: int, n_global: int, workspace, stream=None):
+    """q, o [B,Hq,T,d] bf16 (or [B,Hq,d]: one token), pages, block_table and
+    seq_lens as for attn_decode_paged, lse [B,Hq,T] (or [B,Hq]) float32 or None;
+    the T tokens are the last of seq_lens."""
+    _calls().window(q, k_pages, v_pages, block_table, seq_lens, o, lse, scale, window_left,
+                    n_global, workspace, False, _handle(stream))
+
+
+def attn_decode_cache4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, lse,
+                       scale: float, window_left: int, n_global: int, workspace, stream=None):
+    """attn_decode_window over the pools of attn_cache_append4."""
+    _calls().cache4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, lse, scale,
+                    window_left, n_global, workspace, False, _handle(stream))
+
+
 def attn_status_string(status: int) -> str:
     return lib().attn_status_string(status).decode()
 
@@ -597,3 +665,79 @@ def key_weights(q, k, lse, prev=None, decay: float = 1.0, causal: bool = True,
     return _calls().key_weights(q, k, lse, prev, out,
                                 q.shape[-1] ** -0.5 if scale is None else scale, decay, causal,
                                 seq_lens, block_table, workspace, True, None)
+
+
+def cache_append(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None, positions=None,
+                 new_lens=None, interleaved: bool = False, magnitude: float = 1.0, stream=None,
+                 out=None):
+    """Append each request's new keys (rotated) and values to its pages, where
+    they become the last of its seq_lens keys, and return the rotated q (None
+    without q), contiguous or in ``out`` (which may be q). With new_lens, tokens
+    past a request's count are padding; their rows of the result are left as they
+    were (allocated here, they are undefined). See attn_cache_append."""
+    if stream is not None and out is None and q is not None:
+        with _allocating_on(stream, k):
+            return cache_append(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq,
+                                positions, new_lens, interleaved, magnitude)
+    return _calls().append(q, k, v, k_pages, v_pages, block_table, seq_lens, inv_freq, positions,
+                           new_lens, interleaved, magnitude, out, True, _handle(stream))
+
+
+def cache_append4(q, k, v, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                  inv_freq=None, positions=None, new_lens=None, interleaved: bool = False,
+                  magnitude: float = 1.0, stream=None, out=None):
+    """cache_append into a cache held in 4 bits (attn_cache_append4)."""
+    if stream is not None and out is None and q is not None:
+        with _allocating_on(stream, k):
+            return cache_append4(q, k, v, k_codes, k_scales, v_codes, v_scales, block_table,
+                                 seq_lens, inv_freq, positions, new_lens, interleaved, magnitude)
+    return _calls().append4(q, k, v, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                            inv_freq, positions, new_lens, interleaved, magnitude, out, True,
+                            _handle(stream))
+
+
+def cache_read4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, length=None,
+                stream=None, out=None):
+    """Keys and values of a 4-bit cache as bf16 [B,Hkv,length,d] each (length
+    None: all that the table can hold), zeros past a request's keys; or into
+    ``out`` = (k_out, v_out), whose other rows are left as they were."""
+    if out is None:
+        if stream is not None:
+            with _allocating_on(stream, k_codes):
+                return cache_read4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                                   length)
+        if length is None:
+            length = block_table.shape[1] * k_codes.shape[2]
+        shape = (block_table.shape[0], k_codes.shape[1], length, 2 * k_codes.shape[3])
+        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=k_codes.device)
+                    for _ in range(2))
+    return _calls().read4(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, *out,
+                          _handle(stream))
+
+
+def decode_window(q, k_pages, v_pages, block_table, seq_lens, window_left: int = -1,
+                  n_global: int = 0, scale: float | None = None, stream=None, workspace=None):
+    """Decode of the last T tokens of each request over its pages: O like q
+    [B,Hq,T,d] (or [B,Hq,d]: one token) bf16, LSE float32. Token at position p
+    sees keys p - window_left .. p (window_left < 0: 0 .. p) and the first
+    n_global."""
+    if stream is not None:
+        with _allocating_on(stream, q):
+            return decode_window(q, k_pages, v_pages, block_table, seq_lens, window_left, n_global,
+                                 scale, None, workspace)
+    return _calls().window(q, k_pages, v_pages, block_table, seq_lens, None, None,
+                           q.shape[-1] ** -0.5 if scale is None else scale, window_left, n_global,
+                           workspace, True, None)
+
+
+def decode_cache4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                  window_left: int = -1, n_global: int = 0, scale: float | None = None,
+                  stream=None, workspace=None):
+    """decode_window over a cache held in 4 bits (cache_append4)."""
+    if stream is not None:
+        with _allocating_on(stream, q):
+            return decode_cache4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
+                                 window_left, n_global, scale, None, workspace)
+    return _calls().cache4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, None,
+                           None, q.shape[-1] ** -0.5 if scale is None else scale, window_left,
+                           n_global, workspace, True, None)

@@ -32,7 +32,7 @@ STAMP_PATH = CALLS_PATH + ".stamp"
 
 SOURCES = ["api.cu", "fwd_simt.cu", "fwd_tc.cu", "fwd_tc64.cu", "bwd_aux.cu", "bwd_simt.cu", "bwd_tc.cu",
            "bwd_dq.cu", "decode.cu", "decode_shared.cu", "api_cache.cu", "rope.cu",
-           "key_weights.cu", "evict.cu"]
+           "key_weights.cu", "evict.cu", "api_paged.cu", "cache_append.cu", "decode_window.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1,0 +1,940 @@
+// Decode of T tokens per request over a paged cache, under a sliding window
+// and the first tokens that stay visible, the cache in bf16
+// (attn_decode_window) or in 4 bits (attn_decode_cache4).
+//
+// Mathematics. Softmax attention with the online recurrence: per query row a
+// reference m, Σ p and Σ p v of p = 2^(s - m); the reference moves only when a
+// score passes it by 8, so p <= 2^8. Partial sums of one row, of warps or of
+// CTAs, are joined exactly on the larger reference.
+//
+// 4 bits. With K codes k̂ and one scale per group of 32 elements,
+// s = Σ_c scale_c (Σ_{i in c} q_i k̂_i): the sums of a group are one pair of
+// matrix products on exact float16 values (queries are scaled by a power of two
+// per row, which float16 then holds to 2^-33 of the row's largest), scaled and
+// added in float32. For V the scale differs per key, the index summed over:
+// P·scale_c is what enters the product, in float16 (2^-12 of a probability; bf16
+// would lose 2^-9) times a power of two f that follows the largest scale seen,
+// so that it stays between 2^-24 and 2^15.
+//
+// bf16. P enters P·V as two bf16 parts (2^-17 of a probability is lost at most).
+//
+// Work. Memory bound: 4·D bytes of K and V per key and KV head (4 bits: 9/8·D),
+// 4·D flops per (query row, key). A warp takes 16 keys a step. Sᵀ = K Qᵀ has the
+// keys as rows of the fragments, so that 8 query rows (the heads of a group times
+// the tokens) fill an instruction; P moves into the fragments of Oᵀ = Vᵀ Pᵀ by
+// transposes of 8 x 8 within the warp. K and V fragments of a 4-bit row are built
+// in registers straight from its bytes (fp4.cuh), at one conversion for two
+// values; the tensor instructions are those that take both operands from
+// registers, since values unpacked for the ones that read shared memory would be
+// written there at four times their size.
+//
+// Order. All visible keys of all requests and KV heads, in tiles of 16 of which
+// four make a unit, are laid end to end and cut into equal shares, one per CTA
+// (lengths are read on the device). A CTA whose share begins or ends inside a
+// (request, head) leaves a partial result there, two at most; a dependent launch
+// joins them. Each warp copies its own tiles into a ring of its own, kStages - 1
+// ahead, with no barrier of the CTA until the end of a run.
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "launchers.h"
+
+namespace attn {
+
+ATTN_DEFINE_ERROR_WORD(take_error_decode_window)
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
+
+struct WindowParams {
+  const __nv_bfloat16* q;
+  const uint8_t *k, *v;                     // pools of bf16 rows, or of codes
+  const uint8_t *k_scales, *v_scales;       // 4 bits
+  const int *table, *lens;
+  __nv_bfloat16* o;
+  float* lse;
+  float *o_part, *m_part, *l_part;          // [2 · CTAs][rows of a block][D], [...]
+  int B, Hkv, T, R, blocks;                 // R = query rows per KV head, in `blocks` blocks
+  int num_pages, page_size, max_pages, cap, left, n_global;
+  uint32_t page_mul;                        // key / page_size = umulhi(2 key, mul) >> shift
+  int page_shift, grid;
+  float scale_log2;
+};
+
+// ------------------------------------------------------------ division of work
+
+// What a request's tiles are: `global` tiles from key 0 on, then the tiles
+// from `first` to the one that holds key n - 1.
+struct Tiles {
+  int n, lo, global, first, count, units;
+  ATTN_DEVINL int at(int i) const { return i < global ? i : i - global + first; }
+};
+ATTN_DEVINL Tiles tiles_of(const WindowParams& p, int n) {
+  Tiles t;
+  t.n = unsigned(n) <= unsigned(p.cap) ? n : 0;
+  // first key of the first token's window
+  t.lo = p.left < 0 ? 0 : max(0, t.n - p.T - min(p.left, t.n));
+  const int end = (t.n + kTile - 1) / kTile;
+  t.global = min(end, (min(p.n_global, t.n) + kTile - 1) / kTile);
+  t.first = max(t.lo / kTile, t.global);
+  t.count = t.global + max(0, end - t.first);
+  t.units = (t.count + kWarps - 1) / kWarps;
+  return t;
+}
+
+// Sums over the requests: of all their units, and of those before request
+// `upto` (all threads of the block get both).
+template <int kN> struct UnitSums {
+  int total, before;
+  ATTN_DEVINL UnitSums(const WindowParams& p, int upto) {
+    __shared__ int part[2][kN / 32];
+    int a = 0, b = 0;
+    for (int r = threadIdx.x; r < p.B; r += kN) {
+      const int u = tiles_of(p, p.lens[r]).units;
+      a += u;
+      if (r < upto) b += u;
+    }
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    if (threadIdx.x % 32 == 0) {
+      part[0][threadIdx.x / 32] = a;
+      part[1][threadIdx.x / 32] = b;
+    }
+    __syncthreads();
+    total = before = 0;
+    for (int w = 0; w < kN / 32; ++w) {
+      total += part[0][w];
+      before += part[1][w];
+    }
+    __syncthreads();
+  }
+};
+
+// Share c of `ctas` equal ones of `units`: [start(c), start(c + 1)).
+ATTN_DEVINL int share_start(int c, int ctas, int units) {
+  return int((long long)c * units / ctas);
+}
+// The share that holds unit u.
+ATTN_DEVINL int share_of(int u, int ctas, int units) {
+  return int(((long long)(u + 1) * ctas - 1) / units);
+}
+
+// ------------------------------------------------------------ instructions
+
+template <bool kHalf>
+ATTN_DEVINL void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+ATTN_DEVINL uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+ATTN_DEVINL void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+ATTN_DEVINL void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+ATTN_DEVINL uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// kBytes from global to shared memory, zeros where !valid (nothing is read then).
+template <int kBytes> ATTN_DEVINL void copy_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? kBytes : 0;
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(n) : "memory");
+}
+ATTN_DEVINL void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> ATTN_DEVINL void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+ATTN_DEVINL uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+ATTN_DEVINL uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+ATTN_DEVINL uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+ATTN_DEVINL float max_over_keys(float x) {   // lanes of one t
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+ATTN_DEVINL float sum_over_keys(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+ATTN_DEVINL float pow2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// ------------------------------------------------------------ the tiles
+
+// A warp's ring: K and V rows of kTile keys a stage, then (4 bits) their scales.
+template <int D, bool k4> struct Ring {
+  static constexpr int kRow = k4 ? D / 2 : 2 * D;           // bytes of a row
+  static constexpr int kScales = k4 ? D / 16 : 0;           // and of its scales
+  static constexpr int kStage = 2 * kTile * (kRow + kScales);
+  static constexpr int kStages = k4 ? 4 : 3;
+  static constexpr int kBytes = kStages * kStage;
+  static constexpr int kPieces = kRow / 16;                 // 16-byte pieces of a row
+
+  // Where piece c of K row r starts in a stage. bf16: pieces of a row are turned
+  // by the row, so that the eight rows of an 8 x 8 load lie in different banks.
+  // 4 bits: rows as they come; a quarter warp reads two whole rows.
+  static ATTN_DEVINL int k_at(int r, int c) {
+    return r * kRow + 16 * (k4 ? c : c ^ (r & 7));
+  }
+  // V. 4 bits: a lane reads rows 2t, 2t + 1, 2t + 8 and 2t + 9, so even rows come
+  // first, then odd ones, and every second pair of them is turned by two pieces.
+  static ATTN_DEVINL int v_at(int r, int c) {
+    if (!k4) return kTile * kRow + k_at(r, c);
+    const int s = r / 2 + (r & 1) * 8;
+    return kTile * kRow + s * kRow + 16 * (D == 128 ? c ^ (s & 2) : c);
+  }
+  static ATTN_DEVINL int k_scale_at(int r) { return 2 * kTile * kRow + r * kScales; }
+  static ATTN_DEVINL int v_scale_at(int r) { return k_scale_at(r) + kTile * kScales; }
+};
+
+// CTAs per SM the registers are cut for.
+template <int NT, bool k4> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
+
+template <int D, bool k4, int NT>
+constexpr int smem_bytes() {
+  constexpr int ring = kWarps * Ring<D, k4>::kBytes;
+  constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
+  return (ring > join ? ring : join) + kWarps * 8 * NT * 8;
+}
+
+// NT blocks of 8 query rows at a time.
+template <int D, bool k4, int NT>
+__global__ void __launch_bounds__(kThreads, kResident<NT, k4>)
+window_kernel(const __grid_constant__ WindowParams p) {
+  using RingT = Ring<D, k4>;
+  constexpr int kStages = RingT::kStages, kRows = 8 * NT, kM = D / 16, kGroups = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int start_at[2];
+  pdl_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const uint32_t ring = smem_u32(smem) + warp * RingT::kBytes;
+  float* join = reinterpret_cast<float*>(smem);
+  constexpr int kJoin = kWarps * kRows * (D + 4) * 4, kRing = kWarps * RingT::kBytes;
+  float* join_ml = reinterpret_cast<float*>(smem + (kRing > kJoin ? kRing : kJoin));
+
+  pdl_wait_primary();
+  // this CTA's share, and the request it begins in
+  const int per_request = p.Hkv * p.blocks;
+  const int units = UnitSums<kThreads>(p, 0).total * per_request;
+  if (blockIdx.x == 0)
+    for (int r = threadIdx.x; r < p.B; r += kThreads)
+      if (unsigned(p.lens[r]) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
+  const int ctas = min(p.grid, units);
+  if (int(blockIdx.x) >= ctas) return;
+  const int u_begin = share_start(blockIdx.x, ctas, units),
+            u_end = share_start(blockIdx.x + 1, ctas, units);
+  int b = 0, before = 0;
+  if (warp == 0) {
+    for (int r0 = 0; r0 < p.B; r0 += 32) {
+      const int x = r0 + lane < p.B ? tiles_of(p, p.lens[r0 + lane]).units * per_request : 0;
+      int incl = x;
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u_begin);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        b = r0 + at;
+        before += __shfl_sync(0xffffffffu, incl - x, at);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      start_at[0] = b;
+      start_at[1] = before;
+    }
+  }
+  __syncthreads();
+  b = start_at[0];
+  before = start_at[1];
+
+  for (int u = u_begin; u < u_end;) {
+    Tiles tl = tiles_of(p, p.lens[b]);
+    while (u >= before + tl.units * per_request) {
+      before += tl.units * per_request;
+      tl = tiles_of(p, p.lens[++b]);
+    }
+    const int item = (u - before) / tl.units, local = (u - before) % tl.units;
+    const int h = item / p.blocks, r0 = item % p.blocks * kRows;
+    const int run = min(tl.units - local, u_end - u);
+    const bool whole = run == tl.units;
+    const int i_end = min(tl.count, kWarps * (local + run));
+    const int rows = min(kRows, p.R - r0);
+    const long long q_row0 = (1LL * b * p.Hkv + h) * p.R + r0;
+
+    // Row of the pool that holds key kTile·at(i) + lane % 16; the table entry is
+    // read a step before the copies that need it.
+    int next_page = 0;
+    auto wanted = [&](int key) { return key < tl.n && (key >= tl.lo || key < p.n_global); };
+    auto look_up = [&](int i) {
+      if (i >= i_end) return;
+      const int key = kTile * tl.at(i) + lane % kTile;
+      const uint32_t page = __umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift;
+      if (wanted(key)) next_page = p.table[1LL * b * p.max_pages + page];
+    };
+    uint32_t seen_keys[kStages];                  // of the tiles in the ring, a bit a key
+    auto issue = [&](int i, int stage) -> uint32_t {
+      uint32_t mask = 0;
+      if (i < i_end) {
+        const int key = kTile * tl.at(i) + lane % kTile;
+        const uint32_t page = __umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift;
+        const bool valid = wanted(key) && unsigned(next_page) < unsigned(p.num_pages);
+        if (!valid && wanted(key)) attn_flag_error(kErrBadIndex);
+        mask = __ballot_sync(0xffffffffu, valid) & 0xffffu;
+        // (a pool has fewer than 2^32 rows)
+        const uint32_t row = valid ? (uint32_t(next_page) * uint32_t(p.Hkv) + uint32_t(h)) *
+                                             uint32_t(p.page_size) +
+                                         (uint32_t(key) - page * uint32_t(p.page_size))
+                                   : 0u;
+        const uint32_t to = ring + stage * RingT::kStage;
+        constexpr int kPer = 32 / RingT::kPieces;           // rows a step
+#pragma unroll
+        for (int s = 0; s < kTile / kPer; ++s) {
+          const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
+          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
+          const bool ok = (mask >> r) & 1u;
+          const size_t off = size_t(from) * RingT::kRow + 16 * c;
+          copy_async<16>(to + RingT::k_at(r, c), p.k + off, ok);
+          copy_async<16>(to + RingT::v_at(r, c), p.v + off, ok);
+        }
+        if constexpr (k4) {
+          const int r = lane % kTile;
+          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
+          const uint8_t* src = (lane < kTile ? p.k_scales : p.v_scales) +
+                               size_t(from) * RingT::kScales;
+          copy_async<RingT::kScales>(
+              to + (lane < kTile ? RingT::k_scale_at(r) : RingT::v_scale_at(r)), src,
+              (mask >> r) & 1u);
+        }
+      }
+      copies_commit();
+      return mask;
+    };
+
+    int i = kWarps * local + warp;
+    look_up(i);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      seen_keys[s] = issue(i + s * kWarps, s);
+      look_up(i + (s + 1) * kWarps);
+    }
+
+    // Query rows as the fragments of Qᵀ: lane (g, t) holds row g of each block.
+    // 4 bits: k-step 2c + s is the elements 32c + 8t + 4s .. + 3; scaled by a power
+    // of two that puts the row's largest value into [2^8, 2^9).
+    uint32_t qf[kM][NT][2];
+    float to_log2[NT][2];                         // scores times this, per column
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool live = 8 * nt + g < rows;
+      const __nv_bfloat16* src = p.q + (q_row0 + 8 * nt + g) * D;
+      if constexpr (k4) {
+        uint4 raw[kGroups];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) {
+          raw[c] = live ? *reinterpret_cast<const uint4*>(src + 32 * c + 8 * t)
+                        : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(int(top >> 7) - 127, -100);
+        const float up = pow2i(8 - e);
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qf[2 * c + j / 2][nt][j % 2] = pack_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
+        }
+        const float down = fmaxf(p.scale_log2 * pow2i(e - 8), 1.17549435e-38f);
+        to_log2[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        to_log2[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kM; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            qf[j][nt][s] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * j + 8 * s + 2 * t)
+                                : 0u;
+        to_log2[nt][0] = to_log2[nt][1] = p.scale_log2;
+      }
+    }
+    // last key of each column's token
+    int last[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) last[nt][j] = tl.n - p.T + (r0 + 8 * nt + 2 * t + j) % p.T;
+
+    float o[kM][NT][4], m[NT][2], l[NT][2], f = 1.f;
+    bool fresh = true;                            // f is of no tile yet
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < kM; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[mt][nt][j] = 0.f;
+    }
+
+    for (; i < i_end; i += kStages * kWarps) {
+#pragma unroll
+      for (int stage = 0; stage < kStages; ++stage) {
+        const int it = i + stage * kWarps;
+        if (it >= i_end) break;
+        copies_wait<kStages - 2>();
+        __syncwarp();
+        // (the copies go into the stage that was used last)
+        seen_keys[(stage + kStages - 1) % kStages] =
+            issue(it + (kStages - 1) * kWarps, (stage + kStages - 1) % kStages);
+        look_up(it + kStages * kWarps);
+        const uint32_t at = ring + stage * RingT::kStage;
+        const uint32_t seen = seen_keys[stage];
+        const int key0 = kTile * tl.at(it);
+        const bool full = seen == 0xffffu &&
+                          ((key0 + kTile - 1 <= tl.n - p.T &&
+                            (p.left < 0 || key0 >= tl.n - 1 - p.left)) ||
+                           key0 + kTile <= p.n_global);
+
+        // Sᵀ: rows are keys g and g + 8, columns query rows 2t and 2t + 1
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+        float vs[2][kGroups];                     // 4 bits: scales of V, keys g and g + 8
+        if constexpr (k4) {
+          uint32_t w[2][D / 32];                  // codes of keys g, g + 8
+          float ks[2][kGroups];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = g + 8 * j;
+            uint32_t sk[D / 64], sv[D / 64];
+            if constexpr (D == 128) {
+              const uint4 x = lds128(at + RingT::k_at(r, t));
+              w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
+              const uint2 y = lds64(at + RingT::k_scale_at(r)), z = lds64(at + RingT::v_scale_at(r));
+              sk[0] = y.x; sk[1] = y.y; sv[0] = z.x; sv[1] = z.y;
+            } else {
+              const uint2 x = lds64(at + RingT::k_at(r, 0) + 8 * t);
+              w[j][0] = x.x; w[j][1] = x.y;
+              sk[0] = lds32(at + RingT::k_scale_at(r));
+              sv[0] = lds32(at + RingT::v_scale_at(r));
+            }
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c) {
+              ks[j][c] = c % 2 ? bf16hi(sk[c / 2]) : bf16lo(sk[c / 2]);
+              vs[j][c] = c % 2 ? bf16hi(sv[c / 2]) : bf16lo(sv[c / 2]);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kGroups; ++c) {
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[nt][j] = 0.f;
+#pragma unroll
+            for (int step = 0; step < 2; ++step) {
+              const uint32_t w0 = w[0][step * (D / 64) + c / 2], w1 = w[1][step * (D / 64) + c / 2];
+              uint32_t a[4];
+              if (c % 2) {
+                a[0] = e2m1x2_to_f16x2<2>(w0); a[1] = e2m1x2_to_f16x2<2>(w1);
+                a[2] = e2m1x2_to_f16x2<3>(w0); a[3] = e2m1x2_to_f16x2<3>(w1);
+              } else {
+                a[0] = e2m1x2_to_f16x2<0>(w0); a[1] = e2m1x2_to_f16x2<0>(w1);
+                a[2] = e2m1x2_to_f16x2<1>(w0); a[3] = e2m1x2_to_f16x2<1>(w1);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(x[nt], a, qf[2 * c + step][nt][0], qf[2 * c + step][nt][1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(x[nt][j], ks[j / 2][c], s[nt][j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kM; ++j) {
+            uint32_t a[4];
+            // matrices: keys 0-7, keys 8-15, then the same of the next 8 elements
+            ldmatrix4(a, at + RingT::k_at(lane % 16, 2 * j + lane / 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[j][nt][0], qf[j][nt][1]);
+          }
+        }
+
+        // scores in log2 units, hidden ones -inf
+        bool above = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[nt][j] *= to_log2[nt][j % 2];
+            if (!full) {
+              const int r = g + 8 * (j / 2), key = key0 + r, top = last[nt][j % 2];
+              const bool vis = ((seen >> r) & 1u) &&
+                               ((key <= top && (p.left < 0 || key >= top - p.left)) ||
+                                key < p.n_global);
+              if (!vis) s[nt][j] = -INFINITY;
+            }
+            above |= s[nt][j] > m[nt][j % 2] + 8.f;
+          }
+        float vmax = 0.f;
+        if constexpr (k4) {
+#pragma unroll
+          for (int c = 0; c < kGroups; ++c) vmax = max3(vmax, vs[0][c], vs[1][c]);
+          above |= vmax * f > 128.f;
+        }
+        if (__any_sync(0xffffffffu, above)) {
+          // the references move: everything so far is rescaled
+          float by_f = 1.f;
+          if constexpr (k4) {
+            // (a scale that is not finite counts for nothing: its group alone is lost)
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (vs[j][c] < INFINITY) top = max(top, __float_as_uint(fmaxf(vs[j][c], 0.f)));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const float want = pow2i(6 - max(int(top >> 23) - 127, -100));
+            if (fresh || want < f) {
+              by_f = want / f;                    // (of zeros, when fresh)
+              f = want;
+              fresh = false;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float to = fmaxf(m[nt][j], max_over_keys(fmaxf(s[nt][j], s[nt][j + 2])));
+              const float by = to == m[nt][j] ? 1.f : fast_exp2(m[nt][j] - to);
+              m[nt][j] = to;
+              l[nt][j] *= by;
+#pragma unroll
+              for (int mt = 0; mt < kM; ++mt) {
+                o[mt][nt][j] *= by * by_f;
+                o[mt][nt][j + 2] *= by * by_f;
+              }
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float ref = m[nt][j % 2];
+            s[nt][j] = fast_exp2(s[nt][j] - (ref == -INFINITY ? 0.f : ref));
+            l[nt][j % 2] += s[nt][j];
+          }
+
+        // Oᵀ += Vᵀ Pᵀ
+        if constexpr (k4) {
+          // codes of keys 2t, 2t + 1 (and + 8): bytes (D/16)·g of their rows, the
+          // low halves of a pair of keys in one byte, then the high halves
+          uint32_t lo[2][D / 64], hi[2][D / 64];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t x[D / 64], y[D / 64];
+            if constexpr (D == 128) {
+              const uint2 a = lds64(at + RingT::v_at(2 * t + 8 * j, g / 2) + 8 * (g % 2)),
+                          c = lds64(at + RingT::v_at(2 * t + 1 + 8 * j, g / 2) + 8 * (g % 2));
+              x[0] = a.x; x[1] = a.y; y[0] = c.x; y[1] = c.y;
+            } else {
+              x[0] = lds32(at + RingT::v_at(2 * t + 8 * j, g / 4) + 4 * (g % 4));
+              y[0] = lds32(at + RingT::v_at(2 * t + 1 + 8 * j, g / 4) + 4 * (g % 4));
+            }
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              lo[j][c] = (x[c] & 0x0f0f0f0fu) | ((y[c] << 4) & 0xf0f0f0f0u);
+              hi[j][c] = ((x[c] >> 4) & 0x0f0f0f0fu) | (y[c] & 0xf0f0f0f0u);
+            }
+          }
+          // a key that only some rows see may hold anything in its scale
+          const bool pick = !full && p.T > 1;
+#pragma unroll
+          for (int c = 0; c < kGroups; ++c) {
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float w = vs[j][c] * f;
+                float a = s[nt][2 * j] * w, z = s[nt][2 * j + 1] * w;
+                if (pick) {
+                  if (s[nt][2 * j] == 0.f) a = 0.f;
+                  if (s[nt][2 * j + 1] == 0.f) z = 0.f;
+                }
+                pf[nt][j] = transpose8x8(pack_f16x2(a, z));
+              }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t a[4];
+              if (c % 2) {
+                a[0] = y ? e2m1x2_to_f16x2<3>(lo[0][c / 2]) : e2m1x2_to_f16x2<2>(lo[0][c / 2]);
+                a[1] = y ? e2m1x2_to_f16x2<3>(hi[0][c / 2]) : e2m1x2_to_f16x2<2>(hi[0][c / 2]);
+                a[2] = y ? e2m1x2_to_f16x2<3>(lo[1][c / 2]) : e2m1x2_to_f16x2<2>(lo[1][c / 2]);
+                a[3] = y ? e2m1x2_to_f16x2<3>(hi[1][c / 2]) : e2m1x2_to_f16x2<2>(hi[1][c / 2]);
+              } else {
+                a[0] = y ? e2m1x2_to_f16x2<1>(lo[0][c / 2]) : e2m1x2_to_f16x2<0>(lo[0][c / 2]);
+                a[1] = y ? e2m1x2_to_f16x2<1>(hi[0][c / 2]) : e2m1x2_to_f16x2<0>(hi[0][c / 2]);
+                a[2] = y ? e2m1x2_to_f16x2<1>(lo[1][c / 2]) : e2m1x2_to_f16x2<0>(lo[1][c / 2]);
+                a[3] = y ? e2m1x2_to_f16x2<1>(hi[1][c / 2]) : e2m1x2_to_f16x2<0>(hi[1][c / 2]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<true>(o[2 * c + y][nt], a, pf[nt][0], pf[nt][1]);
+            }
+          }
+        } else {
+          uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x = pack_bf16x2(s[nt][2 * j], s[nt][2 * j + 1]);
+              const uint32_t y = pack_bf16x2(s[nt][2 * j] - bf16lo(x), s[nt][2 * j + 1] - bf16hi(x));
+              hi[nt][j] = transpose8x8(x);
+              lo[nt][j] = transpose8x8(y);
+            }
+          // Keys that only some of the tokens see may hold values that are not
+          // finite, which would reach every row through the product (0 · inf):
+          // then the tokens' rows go one token after the other, each over the
+          // keys that it sees, the others' V as zeros.
+          bool spoilt = false;
+          if (!full && p.T > 1) {
+            for (int c = lane; c < kTile * RingT::kPieces; c += 32) {
+              const uint4 x = lds128(at + kTile * RingT::kRow + 16 * c);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                spoilt |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+            }
+            spoilt = __any_sync(0xffffffffu, spoilt);
+          }
+          if (!spoilt) {
+#pragma unroll
+            for (int mt = 0; mt < kM; ++mt) {
+              uint32_t a[4];
+              // matrices: elements 0-7 and 8-15 of keys 0-7, then of keys 8-15
+              ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
+                                                  2 * mt + lane / 8 % 2));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816<false>(o[mt][nt], a, lo[nt][0], lo[nt][1]);
+                mma16816<false>(o[mt][nt], a, hi[nt][0], hi[nt][1]);
+              }
+            }
+          } else {
+            for (int tok = 0; tok < p.T; ++tok) {
+              // keys 2t, 2t + 1, 2t + 8, 2t + 9 as masks of pairs, for this token
+              const int top = tl.n - p.T + tok;
+              uint32_t keep[2] = {0u, 0u};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = 2 * t + (j & 1) + 8 * (j / 2), key = key0 + r;
+                if (((seen >> r) & 1u) && ((key <= top && (p.left < 0 || key >= top - p.left)) ||
+                                           key < p.n_global))
+                  keep[j / 2] |= j & 1 ? 0xffff0000u : 0xffffu;
+              }
+#pragma unroll
+              for (int mt = 0; mt < kM; ++mt) {
+                uint32_t a[4];
+                ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
+                                                    2 * mt + lane / 8 % 2));
+                a[0] &= keep[0];
+                a[1] &= keep[0];
+                a[2] &= keep[1];
+                a[3] &= keep[1];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  // P of this token's rows; others take no part (their sums would
+                  // be spoilt by what this token sees), so a product of their own
+                  const bool mine = (r0 + 8 * nt + g) % p.T == tok;
+                  float x[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816<false>(x, a, mine ? lo[nt][0] : 0u, mine ? lo[nt][1] : 0u);
+                  mma16816<false>(x, a, mine ? hi[nt][0] : 0u, mine ? hi[nt][1] : 0u);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if ((r0 + 8 * nt + 2 * t + j % 2) % p.T == tok) o[mt][nt][j] += x[j];
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // join the warps
+    copies_wait<0>();
+    __syncthreads();
+    const float unscale = 1.f / f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float sum = sum_over_keys(l[nt][j]);
+        if (g == 0) {
+          join_ml[2 * (warp * kRows + 8 * nt + 2 * t + j)] = m[nt][j];
+          join_ml[2 * (warp * kRows + 8 * nt + 2 * t + j) + 1] = sum;
+        }
+        float* row = join + (warp * kRows + 8 * nt + 2 * t + j) * (D + 4);
+        if constexpr (k4) {
+#pragma unroll
+          for (int c = 0; c < kGroups; ++c)
+            *reinterpret_cast<float4*>(row + 32 * c + 4 * g) =
+                make_float4(o[2 * c][nt][j] * unscale, o[2 * c][nt][j + 2] * unscale,
+                            o[2 * c + 1][nt][j] * unscale, o[2 * c + 1][nt][j + 2] * unscale);
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < kM; ++mt) {
+            row[16 * mt + g] = o[mt][nt][j];
+            row[16 * mt + 8 + g] = o[mt][nt][j + 2];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    for (int x = threadIdx.x; x < rows * (D / 8); x += kThreads) {
+      const int r = x / (D / 8), e = x % (D / 8) * 8;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join_ml[2 * (w * kRows + r)]);
+      float sum = 0.f, acc[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = join_ml[2 * (w * kRows + r)], lw = join_ml[2 * (w * kRows + r) + 1];
+        // (a NaN among the scores is in the sums, not in the references)
+        const float by = mw == -INFINITY ? (lw != lw ? 1.f : 0.f) : fast_exp2(mw - top);
+        sum += by * lw;
+        const float* row = join + (w * kRows + r) * (D + 4) + e;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = by != 0.f ? fmaf(by, row[j], acc[j]) : acc[j];
+      }
+      if (whole) {
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+        if (empty)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+        *reinterpret_cast<uint4*>(p.o + (q_row0 + r) * D + e) =
+            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                       pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        if (e == 0 && p.lse != nullptr)
+          p.lse[q_row0 + r] =
+              empty ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, 0.693147180559945f, logf(sum));
+      } else {
+        float4* to = reinterpret_cast<float4*>(p.o_part + (1LL * slot * kRows + r) * D + e);
+        to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (e == 0) {
+          p.m_part[slot * kRows + r] = top;
+          p.l_part[slot * kRows + r] = sum;
+        }
+      }
+    }
+    u += run;
+    if (u < u_end) __syncthreads();               // the ring is written again
+  }
+}
+
+// Joins the partial results of rows that more than one CTA worked on, and
+// writes those of requests without keys. Grid: x over groups of 8 of the Hkv·R
+// rows of request y.
+constexpr int kJoinWarps = 8;
+template <int D, int kRows>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+window_join_kernel(const __grid_constant__ WindowParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int b = blockIdx.y, lane = threadIdx.x % 32;
+  const UnitSums<32 * kJoinWarps> sums(p, b);
+  const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32;
+  if (row >= p.Hkv * p.R) return;
+  const int h = row / p.R, r = row % p.R;
+  const Tiles tl = tiles_of(p, p.lens[b]);
+  const long long q_row = 1LL * b * p.Hkv * p.R + row;
+  constexpr int kPer = D / 32;
+  float acc[kPer] = {}, sum = 0.f, top = -INFINITY;
+  if (tl.units > 0) {
+    const int per_request = p.Hkv * p.blocks, units = sums.total * per_request;
+    const int ctas = min(p.grid, units);
+    const int u0 = sums.before * per_request + (h * p.blocks + r / kRows) * tl.units;
+    const int c0 = share_of(u0, ctas, units), c1 = share_of(u0 + tl.units - 1, ctas, units);
+    if (c0 == c1) return;                         // its CTA has written it
+    const bool at_start = share_start(c0, ctas, units) == u0;
+    auto slot_of = [&](int c) { return (2 * c + (c == c0 && !at_start ? 1 : 0)) * kRows + r % kRows; };
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.m_part[slot_of(c)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int c = c0; c <= c1; ++c) {
+      const int s = slot_of(c);
+      const float mc = p.m_part[s], lc = p.l_part[s];
+      const float by = mc == -INFINITY ? (lc != lc ? 1.f : 0.f) : fast_exp2(mc - top);
+      const float* part = p.o_part + 1LL * s * D + kPer * lane;
+      float x[kPer];
+      if constexpr (kPer == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(part);
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(part);
+        x[0] = y.x; x[1] = y.y;
+      }
+      sum += by * lc;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] = by != 0.f ? fmaf(by, x[j], acc[j]) : acc[j];
+    }
+  }
+  const bool empty = sum == 0.f;
+  const float inv = empty ? 0.f : 1.f / sum;
+  __nv_bfloat16* to = p.o + q_row * D + kPer * lane;
+#pragma unroll
+  for (int j = 0; j < kPer; j += 2)
+    *reinterpret_cast<uint32_t*>(to + j) =
+        empty ? 0u : pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[q_row] =
+        empty ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, 0.693147180559945f, logf(sum));
+}
+
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem,
+                             const WindowParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<WindowParams*>(&p)};
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int D, bool k4, int NT>
+cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
+  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT>);
+  constexpr int smem = smem_bytes<D, k4, NT>();
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  p.blocks = (p.R + 8 * NT - 1) / (8 * NT);
+  // most units that there can be, by the table and the window
+  long long tiles = (p.cap + kTile - 1) / kTile;
+  if (p.left >= 0)
+    tiles = std::min(tiles, (1LL * p.left + p.T + kTile - 1) / kTile + 1 +
+                                (1LL * p.n_global + kTile - 1) / kTile);
+  const long long most = 1LL * p.B * p.Hkv * p.blocks * ((tiles + kWarps - 1) / kWarps);
+  p.grid = int(std::min<long long>(most, 1LL * a.sm_count * kResident<NT, k4>));
+  e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, p, a.stream);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT>),
+                          dim3(unsigned((p.Hkv * p.R + kJoinWarps - 1) / kJoinWarps),
+                               unsigned(p.B)),
+                          32 * kJoinWarps, 0, p, a.stream);
+}
+
+template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams& p) {
+  return p.R <= 8 ? launch_t<D, k4, 1>(a, p) : launch_t<D, k4, 2>(a, p);
+}
+
+}  // namespace
+
+int window_partial_rows(int R, int sm_count) {
+  // two partial results of 8 or 16 rows per CTA
+  return R <= 8 ? sm_count * kResident<1, true> * 2 * 8 : sm_count * kResident<2, true> * 2 * 16;
+}
+
+cudaError_t launch_decode_window(const WindowArgs& a) {
+  WindowParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k = static_cast<const uint8_t*>(a.k);
+  p.v = static_cast<const uint8_t*>(a.v);
+  p.k_scales = static_cast<const uint8_t*>(a.k_scales);
+  p.v_scales = static_cast<const uint8_t*>(a.v_scales);
+  p.table = a.block_table;
+  p.lens = a.seq_lens;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.o_part = a.o_part;
+  p.m_part = a.m_part;
+  p.l_part = a.l_part;
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.T = a.T;
+  p.R = a.Hq / a.Hkv * a.T;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.cap = a.max_pages * a.page_size;
+  // (clamped to the capacity, so that sums of positions stay in 32 bits)
+  p.left = a.window_left < 0 ? -1 : std::min(a.window_left, p.cap);
+  p.n_global = std::min(a.n_global, p.cap);
+  // For d = page_size and 2^s >= d, m = floor(2^(31 + s) / d) + 1 < 2^32 has
+  // key·m / 2^(31 + s) = key / d + key·x with 0 < x <= 2^-(31 + s), which is too
+  // little to reach the next whole number for key < 2^31.
+  int s = 0;
+  while ((1LL << s) < a.page_size) ++s;
+  p.page_shift = s;
+  p.page_mul = uint32_t((1ULL << (31 + s)) / unsigned(a.page_size) + 1);
+  p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
+  if (a.k_scales != nullptr)
+    return a.d == 64 ? launch_d<64, true>(a, p) : launch_d<128, true>(a, p);
+  return a.d == 64 ? launch_d<64, false>(a, p) : launch_d<128, false>(a, p);
+}
+
+}  // namespace attn

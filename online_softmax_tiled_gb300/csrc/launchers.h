@@ -187,6 +187,68 @@ struct EvictArgs {
   cudaStream_t stream;
 };
 
+struct AppendArgs {
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  attn_strides qs, qos, ks, vs;
+  void* k_pool;            // rows, or 4-bit codes with
+  void* v_pool;
+  void* k_scales;          // their scales (nullptr: rows of dtype dt)
+  void* v_scales;
+  const int* block_table;
+  const int* seq_lens;
+  const int* new_lens;     // nullptr: N
+  const int* positions;    // nullptr: a key's row
+  long long pos_stride;
+  const double* inv_freq;
+  int B, Hq, Hkv, N, d, rot, interleaved;
+  float magnitude;
+  int num_pages, page_size, max_pages;
+  attn_dtype dt;
+  cudaStream_t stream;
+};
+
+struct Read4Args {
+  const void* k_codes;
+  const void* k_scales;
+  const void* v_codes;
+  const void* v_scales;
+  const int* block_table;
+  const int* seq_lens;
+  void* k_out;
+  void* v_out;
+  int B, Hkv, L, d, num_pages, page_size, max_pages;
+  cudaStream_t stream;
+};
+
+struct WindowArgs {
+  const void* q;
+  const void* k;           // pages of bf16 rows, or of 4-bit codes with
+  const void* v;
+  const void* k_scales;    // their scales (nullptr: bf16)
+  const void* v_scales;
+  const int* block_table;
+  const int* seq_lens;
+  void* o;
+  float* lse;
+  float* o_part;           // [window_partial_rows][d], [..], [..]
+  float* m_part;
+  float* l_part;
+  int B, Hq, Hkv, T, num_pages, page_size, max_pages, d, window_left, n_global, sm_count;
+  float scale;
+  cudaStream_t stream;
+};
+
+// Whether every row of a [B, H, N, ...] tensor starts at a multiple of 16 bytes
+// (strides of dimensions of extent one do not matter).
+inline bool rows16(const void* p, const attn_strides& s, int B, int H, int N, int esize) {
+  auto bad = [&](long long st, int n) { return n > 1 && (st * esize) % 16 != 0; };
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && !bad(s.batch, B) && !bad(s.head, H) &&
+         !bad(s.token, N);
+}
+
 // Streaming multiprocessors of the current device (cached per device); 0 if
 // it cannot be read.
 inline int device_sm_count() {
@@ -300,6 +362,12 @@ int key_weights_slots(int R, int T);
 cudaError_t launch_key_weights(const KeyWeightsArgs& a);
 cudaError_t launch_rope(const RopeArgs& a);
 cudaError_t launch_evict(const EvictArgs& a);
+cudaError_t launch_cache_append(const AppendArgs& a);
+cudaError_t launch_cache_read4(const Read4Args& a);
+// Rows of partial results that launch_decode_window may leave, with R query rows
+// per KV head.
+int window_partial_rows(int R, int sm_count);
+cudaError_t launch_decode_window(const WindowArgs& a);
 
 // Per-translation-unit device error words (read and cleared).
 uint32_t take_error_fwd_tc();
@@ -310,5 +378,7 @@ uint32_t take_error_decode();
 uint32_t take_error_evict();
 uint32_t take_error_key_weights();
 uint32_t take_error_decode_shared();
+uint32_t take_error_cache_append();
+uint32_t take_error_decode_window();
 
 }  // namespace attn

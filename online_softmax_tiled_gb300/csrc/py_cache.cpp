@@ -1,6 +1,8 @@
 // Python calls of the cache operators (attn_rope, attn_decode_shared,
-// attn_key_weights, attn_cache_evict): checks of the tensors, their pointers,
-// shapes and strides, the current stream, and the C call. The operators run
+// attn_key_weights, attn_cache_evict, attn_cache_append, attn_cache_append4,
+// attn_cache_read4, attn_decode_window, attn_decode_cache4): checks of the
+// tensors, their pointers, shapes and strides, the current stream, and the C
+// call. The operators run
 // for a few microseconds; the same checks written in Python took two to five
 // times as long as the kernels of a small call.
 //
@@ -171,6 +173,17 @@ attn_strides strides_of(const at::Tensor& t) {
   return attn_strides{st[0], st[1], n == 4 ? st[2] : 0};
 }
 
+// Positions of the tokens of a [B, H, N, d] (or [B, H, d]) tensor: [B, N], or [N]
+// or [1, N] for all requests; of one token also [B]. Gives the stride between
+// requests.
+int64_t position_stride(const at::Tensor& pos, int64_t B, int64_t N) {
+  const int64_t rows = pos.dim() == 2 ? pos.size(0) : pos.dim() == 1 && N == 1 ? pos.size(0) : 1;
+  const int64_t cols = pos.dim() == 2 || (pos.dim() == 1 && N > 1) ? pos.size(-1) : 1;
+  if (pos.dim() < 1 || pos.dim() > 2 || cols != N || (rows != B && rows != 1))
+    refuse_value("positions must be [B, N], or [N] for all requests");
+  return rows == B ? N : 0;
+}
+
 // q, k, positions, inv_freq, interleaved, magnitude, inverse, q_out, k_out, stream
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject* {
@@ -206,11 +219,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!same_shape(*p.first, **p.second) || (*p.second)->scalar_type() != q.scalar_type())
         refuse_value("outputs must be like q and k");
     }
-    // [B, N], or [N] or [1, N] for all requests; of one token also [B]
-    const int64_t rows = pos.dim() == 2 ? pos.size(0) : pos.dim() == 1 && N == 1 ? pos.size(0) : 1;
-    const int64_t cols = pos.dim() == 2 || (pos.dim() == 1 && N > 1) ? pos.size(-1) : 1;
-    if (pos.dim() < 1 || pos.dim() > 2 || cols != N || (rows != B && rows != 1))
-      refuse_value("positions must be [B, N], or [N] for all requests");
+    const int64_t pos_stride = position_stride(pos, B, N);
     if (freq.dim() != 1) refuse_value("inv_freq must be [rot_dim / 2]");
     const void* pp = dev.data(pos, at::kInt);
     const void* pw = dev.data(freq, at::kDouble);
@@ -222,7 +231,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check(attn_rope(q.data_ptr(), &qs, q_out->data_ptr(), &qos, k ? k->data_ptr() : nullptr,
                     k ? &ks : nullptr, k ? k_out->data_ptr() : nullptr, k ? &kos : nullptr,
-                    static_cast<const int*>(pp), rows == B ? N : 0,
+                    static_cast<const int*>(pp), pos_stride,
                     static_cast<const double*>(pw), B, Hq, Hkv, N, d, 2 * size(freq, 0),
                     truth(a[4]), real(a[5]), truth(a[6]), dt, dev.stream(a[9])),
           "attn_rope");
@@ -380,6 +389,198 @@ PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The pools of a paged cache: [num_pages, Hkv, page_size, d] rows, or codes
+// [.., d / 2] and scales [.., d / 32].
+struct Pools {
+  at::Tensor k, v;
+  Opt ks, vs;
+  int pages, Hkv, page, d;
+  void *kp, *vp, *ksp = nullptr, *vsp = nullptr;
+  Pools(PyObject* const* a, const Device& dev, at::ScalarType rows, bool four)
+      : k(tensor(a[0], four ? "k_codes" : "k_pages")), v(tensor(a[four ? 2 : 1], "v")) {
+    if (k.dim() != 4 || !same_shape(k, v)) refuse_value("pools must be alike, [pages, Hkv, page, d]");
+    pages = size(k, 0);
+    Hkv = size(k, 1);
+    page = size(k, 2);
+    d = size(k, 3) * (four ? 2 : 1);
+    const at::ScalarType type = four ? at::kByte : rows;
+    kp = dev.data(k, type);
+    vp = dev.data(v, type);
+    if (!four) return;
+    ks = tensor(a[1], "k_scales");
+    vs = tensor(a[3], "v_scales");
+    if (ks->dim() != 4 || !same_shape(*ks, *vs) || ks->sizes().slice(0, 3) != k.sizes().slice(0, 3) ||
+        ks->size(3) * 32 != d)
+      refuse_value("scales must be [pages, Hkv, page, d / 32]");
+    ksp = dev.data(*ks, at::kBFloat16);
+    vsp = dev.data(*vs, at::kBFloat16);
+  }
+};
+
+// Block table [B, max_pages] and lengths [B] of a call's requests.
+struct Requests {
+  const int *table, *lens;
+  int max_pages;
+  Requests(const at::Tensor& t, const at::Tensor& l, int64_t B, const Device& dev) {
+    if (t.dim() != 2 || t.size(0) != B || l.dim() != 1 || l.size(0) != B)
+      refuse_value("block_table must be [B, max_pages], seq_lens [B]");
+    table = static_cast<const int*>(dev.data(t, at::kInt));
+    lens = static_cast<const int*>(dev.data(l, at::kInt));
+    max_pages = size(t, 1);
+  }
+};
+
+// q, k, v, 2 (rows) or 4 (4 bits) pools, block_table, seq_lens, inv_freq,
+// positions, new_lens, interleaved, magnitude, q_out, allocate, stream
+template <bool kFour> PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  constexpr int kPools = kFour ? 4 : 2;
+  return guarded(n, 13 + kPools, [&]() -> PyObject* {
+    const Opt q = optional_tensor(a[0], "q");
+    const at::Tensor k = tensor(a[1], "k"), v = tensor(a[2], "v");
+    PyObject* const* r = a + 3 + kPools;
+    const Opt freq = optional_tensor(r[2], "inv_freq"), pos = optional_tensor(r[3], "positions"),
+              fresh_lens = optional_tensor(r[4], "new_lens");
+    Opt q_out = optional_tensor(r[7], "q_out");
+    const Device dev(k);
+    const int64_t dims = k.dim();
+    if (dims != 3 && dims != 4) refuse_value("k must be [B, Hkv, N, d] or [B, Hkv, d]");
+    const attn_dtype dt = dtype_of(k);
+    const int B = size(k, 0), Hkv = size(k, 1), N = dims == 4 ? size(k, 2) : 1,
+              d = size(k, int(dims) - 1);
+    dev.on(v);
+    if (!same_shape(k, v) || v.scalar_type() != k.scalar_type())
+      refuse_value("k and v must be alike");
+    c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev.index)};
+    const Pools pools(a + 3, dev, k.scalar_type(), kFour);
+    if (pools.Hkv != Hkv || pools.d != d) refuse_value("pools must have the heads and d of k");
+    const Requests req(tensor(r[0], "block_table"), tensor(r[1], "seq_lens"), B, dev);
+    int Hq = 0;
+    if (q) {
+      dev.on(*q);
+      if (q->dim() != dims || q->size(0) != B || q->sizes().slice(2) != k.sizes().slice(2) ||
+          q->scalar_type() != k.scalar_type())
+        refuse_value("q must be like k but for the number of heads");
+      Hq = size(*q, 1);
+      if (!q_out && truth(r[8])) q_out = fresh(q->sizes(), q->scalar_type(), dev);
+      if (!q_out) refuse_value("q_out is needed");
+      dev.on(*q_out);
+      if (!same_shape(*q, *q_out) || q_out->scalar_type() != q->scalar_type())
+        refuse_value("q_out must be like q");
+    } else if (q_out) {
+      refuse_value("q and q_out go together");
+    }
+    if (freq && freq->dim() != 1) refuse_value("inv_freq must be [rot_dim / 2]");
+    if (fresh_lens && (fresh_lens->dim() != 1 || fresh_lens->size(0) != B))
+      refuse_value("new_lens must be [B]");
+    attn_strides qs{}, qos{};
+    if (q) {
+      qs = strides_of(*q);
+      qos = strides_of(*q_out);
+    }
+    const attn_strides ks = strides_of(k), vs = strides_of(v);
+    const int rot = freq ? 2 * size(*freq, 0) : 0;
+    auto ints = [&](const Opt& t) { return static_cast<const int*>(dev.data(t, at::kInt)); };
+    const double* fp = static_cast<const double*>(dev.data(freq, at::kDouble));
+    const int64_t stride = pos ? position_stride(*pos, B, N) : 0;
+    const void* qp = q ? q->data_ptr() : nullptr;
+    void* qop = q ? q_out->data_ptr() : nullptr;
+    if constexpr (kFour)
+      check(attn_cache_append4(qp, &qs, qop, &qos, k.data_ptr(), &ks, v.data_ptr(), &vs, pools.kp,
+                               pools.ksp, pools.vp, pools.vsp, req.table, req.lens,
+                               ints(fresh_lens), ints(pos), stride, fp, B, Hq, Hkv, N, d, rot,
+                               truth(r[5]), real(r[6]), pools.pages, pools.page, req.max_pages, dt,
+                               dev.stream(r[9])),
+            "attn_cache_append4");
+    else
+      check(attn_cache_append(qp, &qs, qop, &qos, k.data_ptr(), &ks, v.data_ptr(), &vs, pools.kp,
+                              pools.vp, req.table, req.lens, ints(fresh_lens), ints(pos), stride,
+                              fp, B, Hq, Hkv, N, d, rot, truth(r[5]), real(r[6]), pools.pages,
+                              pools.page, req.max_pages, dt, dev.stream(r[9])),
+            "attn_cache_append");
+    if (!q) Py_RETURN_NONE;
+    return THPVariable_Wrap(*q_out);
+  });
+}
+
+// 4 pools, block_table, seq_lens, k_out, v_out, stream
+PyObject* py_read4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const at::Tensor ko = tensor(a[6], "k_out"), vo = tensor(a[7], "v_out");
+    const Device dev(ko);
+    if (ko.dim() != 4 || !same_shape(ko, vo)) refuse_value("outputs must be [B, Hkv, L, d]");
+    const int B = size(ko, 0);
+    c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev.index)};
+    const Pools pools(a, dev, at::kByte, true);
+    if (ko.size(1) != pools.Hkv || ko.size(3) != pools.d)
+      refuse_value("outputs must have the heads and d of the pools");
+    const Requests req(tensor(a[4], "block_table"), tensor(a[5], "seq_lens"), B, dev);
+    check(attn_cache_read4(pools.kp, pools.ksp, pools.vp, pools.vsp, req.table, req.lens,
+                           dev.data(ko, at::kBFloat16), dev.data(vo, at::kBFloat16), B, pools.Hkv,
+                           size(ko, 2), pools.pages, pools.page, req.max_pages, pools.d,
+                           dev.stream(a[8])),
+          "attn_cache_read4");
+    return pair(ko, vo);
+  });
+}
+
+// q, 2 (bf16) or 4 (4 bits) pools, block_table, seq_lens, o, lse, scale,
+// window_left, n_global, workspace, allocate, stream
+template <bool kFour> PyObject* py_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  constexpr int kPools = kFour ? 4 : 2;
+  return guarded(n, 11 + kPools, [&]() -> PyObject* {
+    const at::Tensor q = tensor(a[0], "q");
+    PyObject* const* r = a + 1 + kPools;
+    Opt o = optional_tensor(r[2], "o"), lse = optional_tensor(r[3], "lse");
+    const Opt ws = optional_tensor(r[7], "workspace");
+    const bool allocate = truth(r[8]);
+    const Device dev(q);
+    const int64_t dims = q.dim();
+    if (dims != 3 && dims != 4) refuse_value("q must be [B, Hq, T, d] or [B, Hq, d]");
+    const int B = size(q, 0), Hq = size(q, 1), T = dims == 4 ? size(q, 2) : 1,
+              d = size(q, int(dims) - 1);
+    const void* qp = dev.data(q, at::kBFloat16);
+    c10::cuda::CUDAGuard guard{c10::DeviceIndex(dev.index)};
+    const Pools pools(a + 1, dev, at::kBFloat16, kFour);
+    if (pools.d != d) refuse_value("pools must have the d of q");
+    const Requests req(tensor(r[0], "block_table"), tensor(r[1], "seq_lens"), B, dev);
+    c10::DataPtr own_ws;
+    size_t own_bytes = 0;
+    if (allocate) {
+      o = fresh(q.sizes(), at::kBFloat16, dev);
+      lse = fresh(q.sizes().slice(0, dims - 1), at::kFloat, dev);
+      if (!ws) {
+        // (freed when the call returns, to be handed out again on its stream)
+        own_bytes = attn_decode_window_workspace_size(B, Hq, pools.Hkv, T, d);
+        own_ws = c10::cuda::CUDACachingAllocator::get()->allocate(own_bytes);
+      }
+    }
+    if (!o || (!ws && !allocate)) refuse_value("o and workspace are needed");
+    if (!same_shape(*o, q) || (lse && lse->sizes() != q.sizes().slice(0, dims - 1)))
+      refuse_value("o must be like q, lse like q without d");
+    if (ws) {
+      dev.on(*ws);
+      if (!ws->is_contiguous()) refuse_value("tensors must be contiguous");
+    }
+    void* op = dev.data(*o, at::kBFloat16);
+    float* lp = static_cast<float*>(dev.data(lse, at::kFloat));
+    void* wp = ws ? ws->data_ptr() : own_ws.get();
+    const size_t wn = ws ? size_t(ws->nbytes()) : own_bytes;
+    const float scale = real(r[4]);
+    const int left = small_int(r[5]), global = small_int(r[6]);
+    if constexpr (kFour)
+      check(attn_decode_cache4(qp, pools.kp, pools.ksp, pools.vp, pools.vsp, req.table, req.lens,
+                               op, lp, B, Hq, pools.Hkv, T, pools.pages, pools.page, req.max_pages,
+                               d, scale, left, global, wp, wn, dev.stream(r[9])),
+            "attn_decode_cache4");
+    else
+      check(attn_decode_window(qp, pools.kp, pools.vp, req.table, req.lens, op, lp, B, Hq,
+                               pools.Hkv, T, pools.pages, pools.page, req.max_pages, d, scale, left,
+                               global, wp, wn, dev.stream(r[9])),
+            "attn_decode_window");
+    return pair(*o, lse);
+  });
+}
+
 PyObject* py_set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XDECREF(g_error);
@@ -392,6 +593,11 @@ PyMethodDef g_methods[] = {FAST("rope", py_rope),
                            FAST("decode_shared", py_decode_shared),
                            FAST("key_weights", py_key_weights),
                            FAST("evict", py_evict),
+                           FAST("append", py_append<false>),
+                           FAST("append4", py_append<true>),
+                           FAST("read4", py_read4),
+                           FAST("window", py_window<false>),
+                           FAST("cache4", py_window<true>),
                            {"set_error", py_set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_cache_calls", nullptr, -1, g_methods,

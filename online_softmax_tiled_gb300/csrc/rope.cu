@@ -6,15 +6,7 @@
 // (a, b) = (i, i + rot_dim/2) or (2i, 2i + 1). R is orthogonal, so the
 // gradient of y = m R x is dx = m Rᵀ dy: the same kernel with sin negated.
 //
-// Angles. p·w loses all of its meaning in float32 at far positions (at
-// p = 10^6 and w = 1 an ulp is 1/16 rad), and float64 multiplies are scarce
-// on this chip. The angle is kept as a 64-bit fraction of a full turn
-// instead: t = 2^64 · frac(w / 2π) once per pair from w's bits and 128 bits of
-// 2/π, then p·t modulo 2^64, where whole turns fall off by themselves. For
-// |w| < 2^64 the error is at most |p|·1.5·2^-64 turns (below 2^-32 for every
-// 32-bit p); larger frequencies, of which 128 bits do not tell the fraction,
-// give NaN like those that are not finite. The remainder is rounded to 32
-// bits, then to float32, and goes to sincospi.
+// Angles: 64-bit fractions of a turn (rope_math.cuh).
 //
 // Work. Memory bound: 8 bytes per rotated bf16 pair against a few FMAs; the
 // sincos of a (token, pair) costs tens of instructions, so a thread computes
@@ -32,6 +24,7 @@
 
 #include "common.cuh"
 #include "launchers.h"
+#include "rope_math.cuh"
 
 namespace attn {
 
@@ -40,26 +33,6 @@ namespace {
 // Threads per block: a row has at most d / (2V) = 256 chunks with V = 1, 64
 // otherwise.
 template <int V> constexpr int kThreadsOf = V == 1 ? 256 : 128;
-
-// 2^64 · frac(w / 2π) for |w| < 2^64: w = M · 2^(e - 63) with M in
-// [2^63, 2^64), and C = floor(2^128 · 2/π), so w / 2π · 2^64 =
-// P · 2^(e - 65) with P = M·C / 2^64, below 2^128. P is off by less than two
-// units, one for the bits of 2/π past C and one for those cut off, and they
-// count 2^(e - 65) <= 1/4 each here.
-ATTN_DEVINL uint64_t turns_of(double w) {
-  constexpr uint64_t kHi = 0xA2F9836E4E441529ull, kLo = 0xFC2757D1F534DDC0ull;
-  const uint64_t bits = uint64_t(__double_as_longlong(w));
-  const int ef = int((bits >> 52) & 0x7ff);            // e + 1023
-  const uint64_t M = (bits << 11) | (1ull << 63);
-  const uint64_t mid = M * kHi, low = mid + __umul64hi(M, kLo);
-  const uint64_t high = __umul64hi(M, kHi) + (low < mid);
-  const int sh = max(2, 1088 - ef);                    // 65 - e
-  // (ef = 0: zero, and below 2^-1022)
-  const uint64_t t = ef == 0 || sh >= 128 ? 0
-                     : sh >= 64           ? high >> (sh - 64)
-                                          : high << (64 - sh) | low >> sh;
-  return (bits >> 63) ? 0 - t : t;
-}
 
 // V adjacent elements as they are in memory (V = 1: one element).
 template <typename T, int V> struct Pack;
@@ -147,18 +120,8 @@ rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ position
     const long long p = positions[b * pos_stride + n];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const double w = inv_freq[chunk * V + i];
-      // the angle as a fraction of a turn: its top 32 bits, rounded, are off
-      // by 2^-33 turns at most, and rounded to float32 once more
-      const uint64_t t = uint64_t(p) * turns_of(w) + 0x80000000ull;
-      float s, co;
-      sincospif(float(int(uint32_t(t >> 32))) * 0x1p-31f, &s, &co);
-      // a frequency that is not finite, or of 2^64 and more, gives NaN, not a
-      // wrong angle (its exponent tells; comparing float64 values is slow here)
-      const bool good = ((uint64_t(__double_as_longlong(w)) >> 52) & 0x7ff) < 1023 + 64;
-      const float m = good ? magnitude : __int_as_float(0x7fffffff);
-      cs[i] = co * m;
-      sn[i] = inverse ? -s * m : s * m;
+      turn_cos_sin(p, inv_freq[chunk * V + i], magnitude, cs[i], sn[i]);
+      if (inverse) sn[i] = -sn[i];
     }
   }
   for (int h = h0; h < h1; h += U) {
@@ -223,14 +186,6 @@ cudaError_t launch_t(const RopeArgs& a) {
   return cudaLaunchKernelEx(&cfg, rope_kernel<T, V, kInterleaved>, tq, tk, a.positions,
                             a.pos_stride, a.inv_freq, tokens, a.N, a.Hq, H, a.d, a.rot, hpt,
                             a.magnitude, a.inverse);
-}
-
-// Whether every row of a tensor starts at a multiple of 16 bytes (strides of
-// dimensions of extent one do not matter).
-bool rows16(const void* p, const attn_strides& s, int B, int H, int N, int esize) {
-  auto bad = [&](long long st, int n) { return n > 1 && (st * esize) % 16 != 0; };
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && !bad(s.batch, B) && !bad(s.head, H) &&
-         !bad(s.token, N);
 }
 
 template <typename T, int V>

@@ -38,9 +38,15 @@ from .attention import (  # noqa: F401
     default_scale,
 )
 from .cache import (  # noqa: F401
+    LEVELS,
     decode_shared,
+    decode_window,
     evict,
     key_weights,
+    quantise4,
     rope,
     rope_angles,
+    round_bf16,
+    unpack4,
+    values4,
 )

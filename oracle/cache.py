@@ -14,7 +14,8 @@ Readings where the pages are silent: a pair is turned by p·w (counter-
 clockwise in the (a, b) plane); ties between scores go to the lowest index; a
 NaN score ranks as -inf. Every function is pinned on the CPU by the tests of
 its operator: ``tests/test_rope.py``, ``tests/test_decode_shared.py``,
-``tests/test_key_weights.py`` and ``tests/test_evict.py``.
+``tests/test_key_weights.py``, ``tests/test_evict.py``,
+``tests/test_cache_append.py`` and ``tests/test_decode_window.py``.
 """
 
 from __future__ import annotations
@@ -134,3 +135,75 @@ def evict(scores, n_keep, n_sink=0, n_recent=0):
     best = rank[:n_keep - n_sink - n_recent]
     return np.array(sorted([*range(n_sink), *best, *range(n - n_recent, n)]), dtype=np.int64)
 
+
+LEVELS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])       # of e2m1 codes 0 .. 7
+
+
+def round_bf16(x):
+    """The bf16 value nearest to x, ties to the even one (float64 in and out;
+    normal and subnormal bf16 numbers)."""
+    x = np.asarray(x, dtype=np.float64)
+    _, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e - 8, -133))
+    return np.rint(x / step) * step
+
+
+def quantise4(x):
+    """4-bit form of rows x [..., d]: codes [..., d] (0 .. 15, bit 3 the sign) and
+    scales [..., d / 32], a group's largest magnitude over 6 as bf16; codes are
+    nearest to x / scale, ties to the even code. Finite values only."""
+    g = np.asarray(x, dtype=np.float64).reshape(*np.shape(x)[:-1], -1, 32)
+    scale = round_bf16(np.max(np.abs(g), -1) / 6)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        m = np.where(scale[..., None] == 0, 0.0, np.abs(g) / scale[..., None])
+    far = np.abs(m[..., None] - LEVELS)
+    best = far.min(-1, keepdims=True)
+    # of two equally near codes the even one
+    code = np.argmin(np.where(far == best, np.arange(8) % 2, 2), -1)
+    code = code + 8 * (np.signbit(g) & (scale[..., None] != 0))
+    return code.reshape(np.shape(x)), scale
+
+
+def values4(codes, scales):
+    """Rows [..., d] that codes [..., d] and scales [..., d / 32] stand for."""
+    v = np.where(codes >= 8, -1.0, 1.0) * LEVELS[codes % 8]
+    return v * np.repeat(scales, 32, -1)
+
+
+def unpack4(packed):
+    """Codes [..., d] of packed rows [..., d / 2]: byte (d / 16) g + 2 c + b holds
+    elements 32 c + 4 g + 2 b (low half) and the next."""
+    d = 2 * packed.shape[-1]
+    out = np.empty(packed.shape[:-1] + (d,), dtype=np.int64)
+    for g in range(8):
+        for c in range(d // 32):
+            for b in range(2):
+                byte = packed[..., d // 16 * g + 2 * c + b].astype(np.int64)
+                out[..., 32 * c + 4 * g + 2 * b] = byte % 16
+                out[..., 32 * c + 4 * g + 2 * b + 1] = byte // 16
+    return out
+
+
+def decode_window(q, k, v, scale, window_left=-1, n_global=0):
+    """One request: the T queries q [Hq, T, d] are the last of the n positions of
+    k, v [Hkv, n, d]; token i at p = n - T + i sees key j iff (j <= p and
+    (window_left < 0 or j >= p - window_left)) or j < n_global. Hidden keys take
+    no part, whatever they hold. Returns o [Hq, T, d], lse [Hq, T] and
+    the weighted mean of |v| that tolerances refer to."""
+    Hq, T, d = q.shape
+    Hkv, n, _ = k.shape
+    o, spread = np.zeros((Hq, T, d)), np.zeros((Hq, T, d))
+    lse = np.full((Hq, T), NEG_INF)
+    j = np.arange(n)
+    for i in range(T):
+        p = n - T + i
+        seen = (j <= p) & ((j >= p - window_left) if window_left >= 0 else True) | (j < n_global)
+        if not seen.any():
+            continue
+        for h in range(Hq):
+            kk, vv = k[h // (Hq // Hkv), seen], v[h // (Hq // Hkv), seen]
+            s = scale * (kk @ q[h, i])
+            w = softmax_rows(s[None])[0]
+            o[h, i], spread[h, i] = w @ vv, w @ np.abs(vv)
+            lse[h, i] = logsumexp_rows(s[None])[0]
+    return o, lse, spread
