@@ -686,8 +686,9 @@ ATTN_API attn_status attn_decode_window(const void* q, const void* k_pages, cons
  * same workspace. Attention over the values code * scale: the products with
  * codes are exact, a group's scale multiplies their sum in float32 (K) or the
  * probability (V), which then enters the product in float16 (2^-12 of it is
- * lost). A group whose scale is not finite spoils its own elements of V, and the
- * key that it belongs to in K, for the tokens that see it.
+ * lost; scales of V from 2^-60 to 2^90 of any size keep this). A group whose scale
+ * is not finite spoils its own elements of V, and the key that it belongs to in K,
+ * for the tokens that see it.
  */
 ATTN_API attn_status attn_decode_cache4(const void* q, const void* k_codes, const void* k_scales,
                                         const void* v_codes, const void* v_scales,

@@ -36,6 +36,7 @@
 // ahead, with no barrier of the CTA until the end of a run.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -85,15 +86,21 @@ ATTN_DEVINL Tiles tiles_of(const WindowParams& p, int n) {
   return t;
 }
 
-// Sums over the requests: of all their units, and of those before request
+// Work is divided by cost: every run of units of one (request, KV head, block of
+// rows) counts as kItemCost units more, for its queries, its start and its end.
+// The places of an item are its kItemCost first ones, then one per unit.
+constexpr int kItemCost = 2;
+ATTN_DEVINL int places_of(int units) { return units > 0 ? units + kItemCost : 0; }
+
+// Sums over the requests of an item's places: of all, and of those before request
 // `upto` (all threads of the block get both).
-template <int kN> struct UnitSums {
+template <int kN> struct PlaceSums {
   int total, before;
-  ATTN_DEVINL UnitSums(const WindowParams& p, int upto) {
+  ATTN_DEVINL PlaceSums(const WindowParams& p, int upto) {
     __shared__ int part[2][kN / 32];
     int a = 0, b = 0;
     for (int r = threadIdx.x; r < p.B; r += kN) {
-      const int u = tiles_of(p, p.lens[r]).units;
+      const int u = places_of(tiles_of(p, p.lens[r]).units);
       a += u;
       if (r < upto) b += u;
     }
@@ -113,13 +120,50 @@ template <int kN> struct UnitSums {
   }
 };
 
-// Share c of `ctas` equal ones of `units`: [start(c), start(c + 1)).
-ATTN_DEVINL int share_start(int c, int ctas, int units) {
-  return int((long long)c * units / ctas);
+// Share c of `ctas` equal ones of `places`: [start(c), start(c + 1)).
+ATTN_DEVINL int share_start(int c, int ctas, int places) {
+  return int((long long)c * places / ctas);
 }
-// The share that holds unit u.
-ATTN_DEVINL int share_of(int u, int ctas, int units) {
-  return int(((long long)(u + 1) * ctas - 1) / units);
+// The share that holds a place.
+ATTN_DEVINL int share_of(int place, int ctas, int places) {
+  return int(((long long)(place + 1) * ctas - 1) / places);
+}
+
+// Where a share begins, as units: the request of its first unit, the units of all
+// requests before that one, and the units before the share. Worked out by a warp.
+struct Place {
+  int b, before, unit;
+};
+ATTN_DEVINL Place find_place(const WindowParams& p, int place, int lane) {
+  const int per_request = p.Hkv * p.blocks;
+  int places = 0, units = 0;                      // of the requests so far
+  for (int r0 = 0; r0 < p.B; r0 += 32) {
+    const int u = r0 + lane < p.B ? tiles_of(p, p.lens[r0 + lane]).units : 0;
+    int incl = places_of(u) * per_request, incl_u = u * per_request;
+    const int own = incl, own_u = incl_u;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off),
+                y = __shfl_up_sync(0xffffffffu, incl_u, off);
+      if (lane >= off) {
+        incl += x;
+        incl_u += y;
+      }
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, places + incl > place);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      const int rest = place - places - __shfl_sync(0xffffffffu, incl - own, at);
+      const int per = __shfl_sync(0xffffffffu, u, at);
+      units += __shfl_sync(0xffffffffu, incl_u - own_u, at);
+      const int item = rest / places_of(per);
+      const int in = max(0, rest - item * places_of(per) - kItemCost);
+      return {r0 + at, units, units + item * per + in};
+    }
+    places += __shfl_sync(0xffffffffu, incl, 31);
+    units += __shfl_sync(0xffffffffu, incl_u, 31);
+  }
+  return {p.B, units, units};                     // the end of all
 }
 
 // ------------------------------------------------------------ instructions
@@ -136,6 +180,13 @@ ATTN_DEVINL void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, ui
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from zero.
+ATTN_DEVINL void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+               "{%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 ATTN_DEVINL uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -155,15 +206,12 @@ ATTN_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// kBytes from global to shared memory, zeros where !valid (nothing is read then).
-template <int kBytes> ATTN_DEVINL void copy_async(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? kBytes : 0;
+template <int kBytes> ATTN_DEVINL void copy_async(uint32_t dst, const void* src) {
   if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
-                 "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
 }
 ATTN_DEVINL void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> ATTN_DEVINL void copies_wait() {
@@ -185,6 +233,9 @@ ATTN_DEVINL uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
   return r;
 }
+ATTN_DEVINL void sts32(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
 ATTN_DEVINL float max_over_keys(float x) {   // lanes of one t
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -199,11 +250,13 @@ ATTN_DEVINL float pow2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23)
 
 // ------------------------------------------------------------ the tiles
 
-// A warp's ring: K and V rows of kTile keys a stage, then (4 bits) their scales.
+// A warp's ring: K and V rows of kTile keys a stage, then (4 bits) their scales,
+// then (pages that do not hold whole tiles) a word that says which keys are there.
 template <int D, bool k4> struct Ring {
   static constexpr int kRow = k4 ? D / 2 : 2 * D;           // bytes of a row
   static constexpr int kScales = k4 ? D / 16 : 0;           // and of its scales
-  static constexpr int kStage = 2 * kTile * (kRow + kScales);
+  static constexpr int kInfo = 2 * kTile * (kRow + kScales);
+  static constexpr int kStage = kInfo + 16;
   static constexpr int kStages = k4 ? 4 : 3;
   static constexpr int kBytes = kStages * kStage;
   static constexpr int kPieces = kRow / 16;                 // 16-byte pieces of a row
@@ -228,67 +281,201 @@ template <int D, bool k4> struct Ring {
 // CTAs per SM the registers are cut for.
 template <int NT, bool k4> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
 
+// Warps whose sums are handed to warp 0 at a time, each as [kM·NT][32 lanes] of
+// four floats.
+template <int NT, bool k4> constexpr int kHanded = k4 && NT == 1 ? 3 : 1;
+
 template <int D, bool k4, int NT>
 constexpr int smem_bytes() {
-  constexpr int ring = kWarps * Ring<D, k4>::kBytes;
-  constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
-  return (ring > join ? ring : join) + kWarps * 8 * NT * 8;
+  return kWarps * Ring<D, k4>::kBytes + kHanded<NT, k4> * (D / 16) * NT * 512 +
+         kWarps * 8 * NT * 8;
 }
 
-// NT blocks of 8 query rows at a time.
-template <int D, bool k4, int NT>
+// What a tile is: nothing to compute, all keys seen by all tokens, or neither.
+enum : uint32_t { kNone = 0, kFull = 1, kPart = 2 };
+
+// NT blocks of 8 query rows at a time. kRuns: pages hold whole tiles (page_size
+// a multiple of 16), so a tile's rows are adjacent: one table entry and one
+// address instead of one per row.
+template <int D, bool k4, int NT, bool kRuns>
 __global__ void __launch_bounds__(kThreads, kResident<NT, k4>)
 window_kernel(const __grid_constant__ WindowParams p) {
   using RingT = Ring<D, k4>;
   constexpr int kStages = RingT::kStages, kRows = 8 * NT, kM = D / 16, kGroups = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int start_at[2];
+  __shared__ Place share[2];
   pdl_launch_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  // (uniform, and known to be)
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
+  const int g = lane / 4, t = lane % 4;
   const uint32_t ring = smem_u32(smem) + warp * RingT::kBytes;
-  float* join = reinterpret_cast<float*>(smem);
-  constexpr int kJoin = kWarps * kRows * (D + 4) * 4, kRing = kWarps * RingT::kBytes;
-  float* join_ml = reinterpret_cast<float*>(smem + (kRing > kJoin ? kRing : kJoin));
+  float4* handed = reinterpret_cast<float4*>(smem + kWarps * RingT::kBytes);
+  float2* handed_ml = reinterpret_cast<float2*>(handed + kHanded<NT, k4> * kM * NT * 32);
 
   pdl_wait_primary();
   // this CTA's share, and the request it begins in
   const int per_request = p.Hkv * p.blocks;
-  const int units = UnitSums<kThreads>(p, 0).total * per_request;
+  const int places = PlaceSums<kThreads>(p, 0).total * per_request;
   if (blockIdx.x == 0)
     for (int r = threadIdx.x; r < p.B; r += kThreads)
       if (unsigned(p.lens[r]) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
-  const int ctas = min(p.grid, units);
+  const int ctas = min(p.grid, places);
   if (int(blockIdx.x) >= ctas) return;
-  const int u_begin = share_start(blockIdx.x, ctas, units),
-            u_end = share_start(blockIdx.x + 1, ctas, units);
-  int b = 0, before = 0;
-  if (warp == 0) {
-    for (int r0 = 0; r0 < p.B; r0 += 32) {
-      const int x = r0 + lane < p.B ? tiles_of(p, p.lens[r0 + lane]).units * per_request : 0;
-      int incl = x;
-#pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u_begin);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        b = r0 + at;
-        before += __shfl_sync(0xffffffffu, incl - x, at);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      start_at[0] = b;
-      start_at[1] = before;
-    }
+  if (warp < 2) {
+    const Place at = find_place(p, share_start(blockIdx.x + warp, ctas, places), lane);
+    if (lane == 0) share[warp] = at;
   }
   __syncthreads();
-  b = start_at[0];
-  before = start_at[1];
+  int b = share[0].b, before = share[0].before;
+  const int u_begin = share[0].unit, u_end = share[1].unit;
 
+  // The warp's tile k is its quarter of unit u_begin + k. Tiles 32 i .. 32 i + 31
+  // are worked out at once, one per lane, while those before them are computed:
+  // `ahead` is the run that follows the one in use.
+  struct Tile {
+    uint32_t row;                                 // kRuns: of the pool; else the first key
+    uint32_t what;
+    int b, h;                                     // !kRuns
+  } now{}, ahead{};
+  int ahead_page = 0, ahead_slot = 0, pb = b, pbefore = before;
+  auto look_ahead = [&](int k) {                  // of tiles k .. k + 31
+    const int u = u_begin + k + lane;
+    ahead.what = kNone;
+    ahead_page = 0;
+    if (u < u_end) {
+      Tiles tl = tiles_of(p, p.lens[pb]);
+      while (u >= pbefore + tl.units * per_request) {
+        pbefore += tl.units * per_request;
+        tl = tiles_of(p, p.lens[++pb]);
+      }
+      const int item = (u - pbefore) / tl.units;
+      const int i = kWarps * ((u - pbefore) - item * tl.units) + warp;
+      if (i < tl.count) {
+        const int key0 = kTile * tl.at(i);
+        ahead.what = (key0 + kTile - 1 <= tl.n - p.T &&
+                      (p.left < 0 || key0 >= tl.n - 1 - p.left)) ||
+                             key0 + kTile <= min(p.n_global, tl.n) ? kFull : kPart;
+        ahead.b = pb;
+        ahead.h = item / p.blocks;
+        if constexpr (kRuns) {
+          const int page = int(__umulhi(2u * uint32_t(key0), p.page_mul) >> p.page_shift);
+          ahead_slot = key0 - page * p.page_size;
+          ahead_page = p.table[1LL * pb * p.max_pages + page];
+        } else {
+          ahead.row = uint32_t(key0);
+        }
+      }
+    }
+    pb = __shfl_sync(0xffffffffu, pb, 31);
+    pbefore = __shfl_sync(0xffffffffu, pbefore, 31);
+  };
+  const int n_tiles = u_end - u_begin;
+  // !kRuns: a tile's table entries, key lane % 16's, read a tile before its copies.
+  // (Keys that no token sees are not looked up: their pages may be gone.)
+  int next_page = 0;
+  auto key_page = [&](int key) { return int(__umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift); };
+  auto wanted = [&](int rb, int key) {
+    const Tiles tl = tiles_of(p, p.lens[rb]);
+    return key < tl.n && (key >= tl.lo || key < p.n_global);
+  };
+  auto look_up = [&](int k) {
+    if (kRuns || k >= n_tiles) return;
+    if (k % 32 == 0) {
+      now = ahead;
+      look_ahead(k + 32);
+    }
+    if (__shfl_sync(0xffffffffu, now.what, k % 32) == kNone) return;
+    const int key = int(__shfl_sync(0xffffffffu, now.row, k % 32)) + lane % kTile;
+    const int rb = __shfl_sync(0xffffffffu, now.b, k % 32);
+    next_page = wanted(rb, key) ? p.table[1LL * rb * p.max_pages + key_page(key)] : -1;
+  };
+  // the lane's parts of a tile's copies
+  const uint8_t* const k_src = p.k + 16 * lane;
+  const uint8_t* const v_src = p.v + 16 * lane;
+  const uint8_t* const s_src =
+      k4 ? (lane < kTile ? p.k_scales : p.v_scales) + lane % kTile * RingT::kScales : nullptr;
+  constexpr int kPer = 32 / RingT::kPieces;       // rows a step of the copies
+  const uint32_t k_dst = ring + RingT::k_at(lane / RingT::kPieces, lane % RingT::kPieces);
+  const uint32_t v_dst = ring + RingT::v_at(lane / RingT::kPieces, lane % RingT::kPieces);
+  const uint32_t s_dst = ring + (lane < kTile ? RingT::k_scale_at(lane % kTile)
+                                              : RingT::v_scale_at(lane % kTile));
+  uint32_t whats = 0;                             // of the tiles in the ring, two bits each
+  auto issue = [&](int k, uint32_t stage) {       // stage: its offset in the ring
+    whats >>= 2;
+    if (k < n_tiles) {
+      uint32_t what;
+      if constexpr (kRuns) {
+        if (k % 32 == 0) {
+          // (a pool has fewer than 2^32 rows)
+          now = ahead;
+          const bool ok = unsigned(ahead_page) < unsigned(p.num_pages);
+          if (!ok && now.what != kNone) {
+            attn_flag_error(kErrBadIndex);
+            now.what = kNone;
+          }
+          now.row = (uint32_t(ok ? ahead_page : 0) * uint32_t(p.Hkv) + uint32_t(now.h)) *
+                        uint32_t(p.page_size) + uint32_t(ahead_slot);
+          look_ahead(k + 32);
+        }
+        const uint32_t row = __shfl_sync(0xffffffffu, now.row, k % 32);
+        what = __shfl_sync(0xffffffffu, now.what, k % 32);
+        if (what != kNone) {
+          // all 16 rows, of which the page has room for each, seen or not
+          const uint8_t* kp = k_src + size_t(row) * RingT::kRow;
+          const uint8_t* vp = v_src + size_t(row) * RingT::kRow;
+#pragma unroll
+          for (int s = 0; s < kTile / kPer; ++s) {
+            // (the swizzles repeat, or turn by a constant)
+            const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
+            const uint32_t kd = k4 ? k_dst + s * kPer * RingT::kRow : ring + RingT::k_at(r, c);
+            const uint32_t vd = k4 ? v_dst + s * kPer / 2 * RingT::kRow : ring + RingT::v_at(r, c);
+            copy_async<16>(kd + stage, kp + s * kPer * RingT::kRow);
+            copy_async<16>(vd + stage, vp + s * kPer * RingT::kRow);
+          }
+          if constexpr (k4)
+            copy_async<RingT::kScales>(s_dst + stage, s_src + size_t(row) * RingT::kScales);
+        }
+      } else {
+        what = __shfl_sync(0xffffffffu, now.what, k % 32);
+        if (what != kNone) {
+          const int key = int(__shfl_sync(0xffffffffu, now.row, k % 32)) + lane % kTile;
+          const int h = __shfl_sync(0xffffffffu, now.h, k % 32);
+          const int rb = __shfl_sync(0xffffffffu, now.b, k % 32);
+          const bool ok = unsigned(next_page) < unsigned(p.num_pages);
+          if (!ok && wanted(rb, key)) attn_flag_error(kErrBadIndex);
+          const uint32_t row = ok ? (uint32_t(next_page) * uint32_t(p.Hkv) + uint32_t(h)) *
+                                            uint32_t(p.page_size) +
+                                        uint32_t(key - key_page(key) * p.page_size)
+                                  : 0u;
+          const uint32_t there = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+#pragma unroll
+          for (int s = 0; s < kTile / kPer; ++s) {
+            const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
+            const size_t off = size_t(__shfl_sync(0xffffffffu, row, r)) * RingT::kRow + 16 * c;
+            copy_async<16>(ring + stage + RingT::k_at(r, c), p.k + off);
+            copy_async<16>(ring + stage + RingT::v_at(r, c), p.v + off);
+          }
+          if constexpr (k4)
+            copy_async<RingT::kScales>(s_dst + stage, (lane < kTile ? p.k_scales : p.v_scales) +
+                                                          size_t(row) * RingT::kScales);
+          if (there != 0xffffu) what = there != 0 ? kPart : kNone;
+          sts32(ring + stage + RingT::kInfo, there);
+        }
+      }
+      whats |= what << (2 * (kStages - 1));
+    }
+    copies_commit();
+  };
+  look_ahead(0);
+  look_up(0);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    issue(s, s * RingT::kStage);
+    look_up(s + 1);
+  }
+
+  int k = 0;
+  uint32_t stage = 0;                             // of tile k
   for (int u = u_begin; u < u_end;) {
     Tiles tl = tiles_of(p, p.lens[b]);
     while (u >= before + tl.units * per_request) {
@@ -299,66 +486,8 @@ window_kernel(const __grid_constant__ WindowParams p) {
     const int h = item / p.blocks, r0 = item % p.blocks * kRows;
     const int run = min(tl.units - local, u_end - u);
     const bool whole = run == tl.units;
-    const int i_end = min(tl.count, kWarps * (local + run));
     const int rows = min(kRows, p.R - r0);
     const long long q_row0 = (1LL * b * p.Hkv + h) * p.R + r0;
-
-    // Row of the pool that holds key kTile·at(i) + lane % 16; the table entry is
-    // read a step before the copies that need it.
-    int next_page = 0;
-    auto wanted = [&](int key) { return key < tl.n && (key >= tl.lo || key < p.n_global); };
-    auto look_up = [&](int i) {
-      if (i >= i_end) return;
-      const int key = kTile * tl.at(i) + lane % kTile;
-      const uint32_t page = __umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift;
-      if (wanted(key)) next_page = p.table[1LL * b * p.max_pages + page];
-    };
-    uint32_t seen_keys[kStages];                  // of the tiles in the ring, a bit a key
-    auto issue = [&](int i, int stage) -> uint32_t {
-      uint32_t mask = 0;
-      if (i < i_end) {
-        const int key = kTile * tl.at(i) + lane % kTile;
-        const uint32_t page = __umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift;
-        const bool valid = wanted(key) && unsigned(next_page) < unsigned(p.num_pages);
-        if (!valid && wanted(key)) attn_flag_error(kErrBadIndex);
-        mask = __ballot_sync(0xffffffffu, valid) & 0xffffu;
-        // (a pool has fewer than 2^32 rows)
-        const uint32_t row = valid ? (uint32_t(next_page) * uint32_t(p.Hkv) + uint32_t(h)) *
-                                             uint32_t(p.page_size) +
-                                         (uint32_t(key) - page * uint32_t(p.page_size))
-                                   : 0u;
-        const uint32_t to = ring + stage * RingT::kStage;
-        constexpr int kPer = 32 / RingT::kPieces;           // rows a step
-#pragma unroll
-        for (int s = 0; s < kTile / kPer; ++s) {
-          const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
-          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-          const bool ok = (mask >> r) & 1u;
-          const size_t off = size_t(from) * RingT::kRow + 16 * c;
-          copy_async<16>(to + RingT::k_at(r, c), p.k + off, ok);
-          copy_async<16>(to + RingT::v_at(r, c), p.v + off, ok);
-        }
-        if constexpr (k4) {
-          const int r = lane % kTile;
-          const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-          const uint8_t* src = (lane < kTile ? p.k_scales : p.v_scales) +
-                               size_t(from) * RingT::kScales;
-          copy_async<RingT::kScales>(
-              to + (lane < kTile ? RingT::k_scale_at(r) : RingT::v_scale_at(r)), src,
-              (mask >> r) & 1u);
-        }
-      }
-      copies_commit();
-      return mask;
-    };
-
-    int i = kWarps * local + warp;
-    look_up(i);
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      seen_keys[s] = issue(i + s * kWarps, s);
-      look_up(i + (s + 1) * kWarps);
-    }
 
     // Query rows as the fragments of Qᵀ: lane (g, t) holds row g of each block.
     // 4 bits: k-step 2c + s is the elements 32c + 8t + 4s .. + 3; scaled by a power
@@ -411,14 +540,17 @@ window_kernel(const __grid_constant__ WindowParams p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) last[nt][j] = tl.n - p.T + (r0 + 8 * nt + 2 * t + j) % p.T;
 
-    float o[kM][NT][4], m[NT][2], l[NT][2], f = 1.f;
-    bool fresh = true;                            // f is of no tile yet
+    // m: row maxima, in log2 units, as of the last time that one was passed by 8;
+    // limit: 8 above them, as raw sums. Sums are of 2^(s - m + e_f).
+    float o[kM][NT][4], m[NT][2], limit[NT][2], minus_ref[NT][2], l[NT][2], v_limit = 128.f;
+    int e_f = 0;
+    bool fresh = true;                            // e_f is of no tile yet
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        m[nt][j] = -INFINITY;
-        l[nt][j] = 0.f;
+        m[nt][j] = limit[nt][j] = -INFINITY;
+        l[nt][j] = minus_ref[nt][j] = 0.f;
       }
 #pragma unroll
       for (int mt = 0; mt < kM; ++mt)
@@ -426,183 +558,198 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int j = 0; j < 4; ++j) o[mt][nt][j] = 0.f;
     }
 
-    for (; i < i_end; i += kStages * kWarps) {
-#pragma unroll
-      for (int stage = 0; stage < kStages; ++stage) {
-        const int it = i + stage * kWarps;
-        if (it >= i_end) break;
-        copies_wait<kStages - 2>();
-        __syncwarp();
-        // (the copies go into the stage that was used last)
-        seen_keys[(stage + kStages - 1) % kStages] =
-            issue(it + (kStages - 1) * kWarps, (stage + kStages - 1) % kStages);
-        look_up(it + kStages * kWarps);
-        const uint32_t at = ring + stage * RingT::kStage;
-        const uint32_t seen = seen_keys[stage];
-        const int key0 = kTile * tl.at(it);
-        const bool full = seen == 0xffffu &&
-                          ((key0 + kTile - 1 <= tl.n - p.T &&
-                            (p.left < 0 || key0 >= tl.n - 1 - p.left)) ||
-                           key0 + kTile <= p.n_global);
+    for (int i = kWarps * local + warp; i < kWarps * (local + run); i += kWarps, ++k) {
+      copies_wait<kStages - 2>();
+      __syncwarp();
+      // (the copies go into the stage that was used last)
+      issue(k + kStages - 1, stage == 0 ? (kStages - 1) * RingT::kStage : stage - RingT::kStage);
+      look_up(k + kStages);
+      const uint32_t at = ring + stage;
+      stage = stage == (kStages - 1) * RingT::kStage ? 0 : stage + RingT::kStage;
+      const uint32_t what = whats & 3u;
+      if (what == kNone) continue;
+      const bool full = what == kFull;
 
-        // Sᵀ: rows are keys g and g + 8, columns query rows 2t and 2t + 1
-        float s[NT][4];
+      // Sᵀ: rows are keys g and g + 8, columns query rows 2t and 2t + 1
+      float s[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
-        float vs[2][kGroups];                     // 4 bits: scales of V, keys g and g + 8
-        if constexpr (k4) {
-          uint32_t w[2][D / 32];                  // codes of keys g, g + 8
-          float ks[2][kGroups];
+        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+      float vs[2][kGroups];                     // 4 bits: scales of V, keys g and g + 8
+      if constexpr (k4) {
+        uint32_t w[2][D / 32];                  // codes of keys g, g + 8
+        float ks[2][kGroups];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = g + 8 * j;
-            uint32_t sk[D / 64], sv[D / 64];
-            if constexpr (D == 128) {
-              const uint4 x = lds128(at + RingT::k_at(r, t));
-              w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
-              const uint2 y = lds64(at + RingT::k_scale_at(r)), z = lds64(at + RingT::v_scale_at(r));
-              sk[0] = y.x; sk[1] = y.y; sv[0] = z.x; sv[1] = z.y;
-            } else {
-              const uint2 x = lds64(at + RingT::k_at(r, 0) + 8 * t);
-              w[j][0] = x.x; w[j][1] = x.y;
-              sk[0] = lds32(at + RingT::k_scale_at(r));
-              sv[0] = lds32(at + RingT::v_scale_at(r));
-            }
-#pragma unroll
-            for (int c = 0; c < kGroups; ++c) {
-              ks[j][c] = c % 2 ? bf16hi(sk[c / 2]) : bf16lo(sk[c / 2]);
-              vs[j][c] = c % 2 ? bf16hi(sv[c / 2]) : bf16lo(sv[c / 2]);
-            }
+        for (int j = 0; j < 2; ++j) {
+          const int r = g + 8 * j;
+          uint32_t sk[D / 64], sv[D / 64];
+          if constexpr (D == 128) {
+            const uint4 x = lds128(at + RingT::k_at(r, t));
+            w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
+            const uint2 y = lds64(at + RingT::k_scale_at(r)), z = lds64(at + RingT::v_scale_at(r));
+            sk[0] = y.x; sk[1] = y.y; sv[0] = z.x; sv[1] = z.y;
+          } else {
+            const uint2 x = lds64(at + RingT::k_at(r, 0) + 8 * t);
+            w[j][0] = x.x; w[j][1] = x.y;
+            sk[0] = lds32(at + RingT::k_scale_at(r));
+            sv[0] = lds32(at + RingT::v_scale_at(r));
           }
 #pragma unroll
           for (int c = 0; c < kGroups; ++c) {
-            float x[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x[nt][j] = 0.f;
-#pragma unroll
-            for (int step = 0; step < 2; ++step) {
-              const uint32_t w0 = w[0][step * (D / 64) + c / 2], w1 = w[1][step * (D / 64) + c / 2];
-              uint32_t a[4];
-              if (c % 2) {
-                a[0] = e2m1x2_to_f16x2<2>(w0); a[1] = e2m1x2_to_f16x2<2>(w1);
-                a[2] = e2m1x2_to_f16x2<3>(w0); a[3] = e2m1x2_to_f16x2<3>(w1);
-              } else {
-                a[0] = e2m1x2_to_f16x2<0>(w0); a[1] = e2m1x2_to_f16x2<0>(w1);
-                a[2] = e2m1x2_to_f16x2<1>(w0); a[3] = e2m1x2_to_f16x2<1>(w1);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(x[nt], a, qf[2 * c + step][nt][0], qf[2 * c + step][nt][1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(x[nt][j], ks[j / 2][c], s[nt][j]);
+            ks[j][c] = c % 2 ? bf16hi(sk[c / 2]) : bf16lo(sk[c / 2]);
+            vs[j][c] = c % 2 ? bf16hi(sv[c / 2]) : bf16lo(sv[c / 2]);
           }
-        } else {
+        }
 #pragma unroll
-          for (int j = 0; j < kM; ++j) {
+        for (int c = 0; c < kGroups; ++c) {
+          float x[NT][4];
+#pragma unroll
+          for (int step = 0; step < 2; ++step) {
+            const uint32_t w0 = w[0][step * (D / 64) + c / 2], w1 = w[1][step * (D / 64) + c / 2];
             uint32_t a[4];
-            // matrices: keys 0-7, keys 8-15, then the same of the next 8 elements
-            ldmatrix4(a, at + RingT::k_at(lane % 16, 2 * j + lane / 16));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[j][nt][0], qf[j][nt][1]);
-          }
-        }
-
-        // scores in log2 units, hidden ones -inf
-        bool above = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[nt][j] *= to_log2[nt][j % 2];
-            if (!full) {
-              const int r = g + 8 * (j / 2), key = key0 + r, top = last[nt][j % 2];
-              const bool vis = ((seen >> r) & 1u) &&
-                               ((key <= top && (p.left < 0 || key >= top - p.left)) ||
-                                key < p.n_global);
-              if (!vis) s[nt][j] = -INFINITY;
+            if (c % 2) {
+              a[0] = e2m1x2_to_f16x2<2>(w0); a[1] = e2m1x2_to_f16x2<2>(w1);
+              a[2] = e2m1x2_to_f16x2<3>(w0); a[3] = e2m1x2_to_f16x2<3>(w1);
+            } else {
+              a[0] = e2m1x2_to_f16x2<0>(w0); a[1] = e2m1x2_to_f16x2<0>(w1);
+              a[2] = e2m1x2_to_f16x2<1>(w0); a[3] = e2m1x2_to_f16x2<1>(w1);
             }
-            above |= s[nt][j] > m[nt][j % 2] + 8.f;
-          }
-        float vmax = 0.f;
-        if constexpr (k4) {
 #pragma unroll
-          for (int c = 0; c < kGroups; ++c) vmax = max3(vmax, vs[0][c], vs[1][c]);
-          above |= vmax * f > 128.f;
-        }
-        if (__any_sync(0xffffffffu, above)) {
-          // the references move: everything so far is rescaled
-          float by_f = 1.f;
-          if constexpr (k4) {
-            // (a scale that is not finite counts for nothing: its group alone is lost)
-            uint32_t top = 0;
-#pragma unroll
-            for (int c = 0; c < kGroups; ++c)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (vs[j][c] < INFINITY) top = max(top, __float_as_uint(fmaxf(vs[j][c], 0.f)));
-            top = __reduce_max_sync(0xffffffffu, top);
-            const float want = pow2i(6 - max(int(top >> 23) - 127, -100));
-            if (fresh || want < f) {
-              by_f = want / f;                    // (of zeros, when fresh)
-              f = want;
-              fresh = false;
+            for (int nt = 0; nt < NT; ++nt) {
+              if (step == 0)
+                mma16816_first(x[nt], a, qf[2 * c][nt][0], qf[2 * c][nt][1]);
+              else
+                mma16816<true>(x[nt], a, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
             }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float to = fmaxf(m[nt][j], max_over_keys(fmaxf(s[nt][j], s[nt][j + 2])));
-              const float by = to == m[nt][j] ? 1.f : fast_exp2(m[nt][j] - to);
-              m[nt][j] = to;
-              l[nt][j] *= by;
+            for (int j = 0; j < 4; ++j)
+              s[nt][j] = c == 0 ? x[nt][j] * ks[j / 2][0] : fmaf(x[nt][j], ks[j / 2][c], s[nt][j]);
+        }
+      } else {
 #pragma unroll
-              for (int mt = 0; mt < kM; ++mt) {
-                o[mt][nt][j] *= by * by_f;
-                o[mt][nt][j + 2] *= by * by_f;
-              }
-            }
+        for (int j = 0; j < kM; ++j) {
+          uint32_t a[4];
+          // matrices: keys 0-7, keys 8-15, then the same of the next 8 elements
+          ldmatrix4(a, at + RingT::k_at(lane % 16, 2 * j + lane / 16));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[j][nt][0], qf[j][nt][1]);
+        }
+      }
+
+      uint32_t hidden[NT][2];                     // !full: bits 0 .. 15, keys a row does not see
+      if (!full) {
+        const int key0 = kTile * tl.at(i);
+        // key x of a tile counted from key0: bits below(x)
+        auto below = [](int x) { return (1u << max(0, min(kTile, x))) - 1u; };
+        const uint32_t there = (kRuns ? 0xffffu : lds32(at + RingT::kInfo)) & below(tl.n - key0);
+        const uint32_t first = below(p.n_global - key0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int top = last[nt][j];
+            const uint32_t near = below(top + 1 - key0) &
+                                  ~(p.left < 0 ? 0u : below(top - p.left - key0));
+            hidden[nt][j] = ~(there & (near | first));
+            if ((hidden[nt][j] >> g) & 1u) s[nt][j] = -INFINITY;
+            if ((hidden[nt][j] >> (g + 8)) & 1u) s[nt][j + 2] = -INFINITY;
+          }
+        if constexpr (k4) {                       // what no token sees has no say in e_f
+          const uint32_t any = there & (~below(tl.lo - key0) | first);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (!((any >> (g + 8 * j)) & 1u))
+#pragma unroll
+              for (int c = 0; c < kGroups; ++c) vs[j][c] = 0.f;
+        }
+      }
+      // whether a score passes its row's maximum so far by 8 binary orders, or a
+      // scale of V the power of two that P is taken with by 2^7
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) above |= fmaxf(s[nt][j], s[nt][j + 2]) > limit[nt][j];
+      if constexpr (k4) {
+        float vmax = 0.f;
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) vmax = max3(vmax, vs[0][c], vs[1][c]);
+        above |= vmax > v_limit;
+      }
+      if (__any_sync(0xffffffffu, above)) {
+        // the references move: everything so far is rescaled
+        int e_new = e_f;
+        if constexpr (k4) {
+          // (a scale that is not finite counts for nothing: its group alone is lost)
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (vs[j][c] < INFINITY) top = max(top, __float_as_uint(fmaxf(vs[j][c], 0.f)));
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int want = 6 - min(max(int(top >> 23) - 127, -60), 90);
+          if (fresh || want < e_f) e_new = want;
+          fresh = false;
+          v_limit = pow2i(7 - e_new);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ref = m[nt][j % 2];
-            s[nt][j] = fast_exp2(s[nt][j] - (ref == -INFINITY ? 0.f : ref));
-            l[nt][j % 2] += s[nt][j];
-          }
-
-        // Oᵀ += Vᵀ Pᵀ
-        if constexpr (k4) {
-          // codes of keys 2t, 2t + 1 (and + 8): bytes (D/16)·g of their rows, the
-          // low halves of a pair of keys in one byte, then the high halves
-          uint32_t lo[2][D / 64], hi[2][D / 64];
-#pragma unroll
           for (int j = 0; j < 2; ++j) {
-            uint32_t x[D / 64], y[D / 64];
-            if constexpr (D == 128) {
-              const uint2 a = lds64(at + RingT::v_at(2 * t + 8 * j, g / 2) + 8 * (g % 2)),
-                          c = lds64(at + RingT::v_at(2 * t + 1 + 8 * j, g / 2) + 8 * (g % 2));
-              x[0] = a.x; x[1] = a.y; y[0] = c.x; y[1] = c.y;
-            } else {
-              x[0] = lds32(at + RingT::v_at(2 * t + 8 * j, g / 4) + 4 * (g % 4));
-              y[0] = lds32(at + RingT::v_at(2 * t + 1 + 8 * j, g / 4) + 4 * (g % 4));
-            }
+            const float to = fmaxf(m[nt][j], max_over_keys(fmaxf(s[nt][j], s[nt][j + 2])) *
+                                                 to_log2[nt][j]);
+            // (nothing seen yet: sums of zeros, whatever they are scaled by)
+            const float by = to == -INFINITY ? 1.f
+                             : to == m[nt][j] && e_new == e_f
+                                 ? 1.f : fast_exp2(m[nt][j] - to + float(e_new - e_f));
+            m[nt][j] = to;
+            limit[nt][j] = to == -INFINITY ? -INFINITY : (to + 8.f) / to_log2[nt][j];
+            minus_ref[nt][j] = to == -INFINITY ? 0.f : float(e_new) - to;
+            l[nt][j] *= by;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              lo[j][c] = (x[c] & 0x0f0f0f0fu) | ((y[c] << 4) & 0xf0f0f0f0u);
-              hi[j][c] = ((x[c] >> 4) & 0x0f0f0f0fu) | (y[c] & 0xf0f0f0f0u);
+            for (int mt = 0; mt < kM; ++mt) {
+              o[mt][nt][j] *= by;
+              o[mt][nt][j + 2] *= by;
             }
           }
-          // a key that only some rows see may hold anything in its scale
-          const bool pick = !full && p.T > 1;
+        e_f = e_new;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[nt][j] = fast_exp2(fmaf(s[nt][j], to_log2[nt][j % 2], minus_ref[nt][j % 2]));
+          l[nt][j % 2] += s[nt][j];
+        }
+
+      // Oᵀ += Vᵀ Pᵀ
+      if constexpr (k4) {
+        // codes of keys 2t, 2t + 1 (and + 8): bytes (D/16)·g of their rows, the
+        // low halves of a pair of keys in one byte, then the high halves
+        uint32_t lo[2][D / 64], hi[2][D / 64];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t x[D / 64], y[D / 64];
+          if constexpr (D == 128) {
+            const uint2 a = lds64(at + RingT::v_at(2 * t + 8 * j, g / 2) + 8 * (g % 2)),
+                        c = lds64(at + RingT::v_at(2 * t + 1 + 8 * j, g / 2) + 8 * (g % 2));
+            x[0] = a.x; x[1] = a.y; y[0] = c.x; y[1] = c.y;
+          } else {
+            x[0] = lds32(at + RingT::v_at(2 * t + 8 * j, g / 4) + 4 * (g % 4));
+            y[0] = lds32(at + RingT::v_at(2 * t + 1 + 8 * j, g / 4) + 4 * (g % 4));
+          }
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            lo[j][c] = (x[c] & 0x0f0f0f0fu) | ((y[c] << 4) & 0xf0f0f0f0u);
+            hi[j][c] = ((x[c] >> 4) & 0x0f0f0f0fu) | (y[c] & 0xf0f0f0f0u);
+          }
+        }
+        auto product = [&](auto pick) {
 #pragma unroll
           for (int c = 0; c < kGroups; ++c) {
             uint32_t pf[NT][2];
@@ -610,11 +757,10 @@ window_kernel(const __grid_constant__ WindowParams p) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float w = vs[j][c] * f;
-                float a = s[nt][2 * j] * w, z = s[nt][2 * j + 1] * w;
-                if (pick) {
-                  if (s[nt][2 * j] == 0.f) a = 0.f;
-                  if (s[nt][2 * j + 1] == 0.f) z = 0.f;
+                float a = s[nt][2 * j] * vs[j][c], z = s[nt][2 * j + 1] * vs[j][c];
+                if constexpr (decltype(pick)::value) {
+                  if ((hidden[nt][0] >> (g + 8 * j)) & 1u) a = 0.f;
+                  if ((hidden[nt][1] >> (g + 8 * j)) & 1u) z = 0.f;
                 }
                 pf[nt][j] = transpose8x8(pack_f16x2(a, z));
               }
@@ -637,78 +783,84 @@ window_kernel(const __grid_constant__ WindowParams p) {
                 mma16816<true>(o[2 * c + y][nt], a, pf[nt][0], pf[nt][1]);
             }
           }
-        } else {
-          uint32_t hi[NT][2], lo[NT][2];
+        };
+        // a key that a row does not see may hold anything in its scale
+        if (full)
+          product(std::false_type{});
+        else
+          product(std::true_type{});
+      } else {
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t x = pack_bf16x2(s[nt][2 * j], s[nt][2 * j + 1]);
-              const uint32_t y = pack_bf16x2(s[nt][2 * j] - bf16lo(x), s[nt][2 * j + 1] - bf16hi(x));
-              hi[nt][j] = transpose8x8(x);
-              lo[nt][j] = transpose8x8(y);
-            }
-          // Keys that only some of the tokens see may hold values that are not
-          // finite, which would reach every row through the product (0 · inf):
-          // then the tokens' rows go one token after the other, each over the
-          // keys that it sees, the others' V as zeros.
-          bool spoilt = false;
-          if (!full && p.T > 1) {
-            for (int c = lane; c < kTile * RingT::kPieces; c += 32) {
-              const uint4 x = lds128(at + kTile * RingT::kRow + 16 * c);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                spoilt |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
-            }
-            spoilt = __any_sync(0xffffffffu, spoilt);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x = pack_bf16x2(s[nt][2 * j], s[nt][2 * j + 1]);
+            const uint32_t y = pack_bf16x2(s[nt][2 * j] - bf16lo(x), s[nt][2 * j + 1] - bf16hi(x));
+            hi[nt][j] = transpose8x8(x);
+            lo[nt][j] = transpose8x8(y);
           }
-          if (!spoilt) {
+        // Keys that a token does not see may hold values that are not finite, which
+        // would reach its rows through the product (0 · inf): then the tokens'
+        // rows go one token after the other, each over the keys that it sees,
+        // the others' V as zeros.
+        bool spoilt = false;
+        if (!full) {
+          for (int c = lane; c < kTile * RingT::kPieces; c += 32) {
+            const uint4 x = lds128(at + kTile * RingT::kRow + 16 * c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              spoilt |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+          }
+          spoilt = __any_sync(0xffffffffu, spoilt);
+        }
+        if (!spoilt) {
+#pragma unroll
+          for (int mt = 0; mt < kM; ++mt) {
+            uint32_t a[4];
+            // matrices: elements 0-7 and 8-15 of keys 0-7, then of keys 8-15
+            ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
+                                                2 * mt + lane / 8 % 2));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<false>(o[mt][nt], a, lo[nt][0], lo[nt][1]);
+              mma16816<false>(o[mt][nt], a, hi[nt][0], hi[nt][1]);
+            }
+          }
+        } else {
+          for (int tok = 0; tok < p.T; ++tok) {
+            // keys 2t, 2t + 1, 2t + 8, 2t + 9 as masks of pairs, for this token
+            const int top = tl.n - p.T + tok, key0 = kTile * tl.at(i);
+            const uint32_t there = kRuns ? 0xffffu : lds32(at + RingT::kInfo);
+            uint32_t keep[2] = {0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = 2 * t + (j & 1) + 8 * (j / 2), key = key0 + r;
+              if (((there >> r) & 1u) && key < tl.n &&
+                  ((key <= top && (p.left < 0 || key >= top - p.left)) || key < p.n_global))
+                keep[j / 2] |= j & 1 ? 0xffff0000u : 0xffffu;
+            }
 #pragma unroll
             for (int mt = 0; mt < kM; ++mt) {
               uint32_t a[4];
-              // matrices: elements 0-7 and 8-15 of keys 0-7, then of keys 8-15
               ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
                                                   2 * mt + lane / 8 % 2));
+              a[0] &= keep[0];
+              a[1] &= keep[0];
+              a[2] &= keep[1];
+              a[3] &= keep[1];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816<false>(o[mt][nt], a, lo[nt][0], lo[nt][1]);
-                mma16816<false>(o[mt][nt], a, hi[nt][0], hi[nt][1]);
-              }
-            }
-          } else {
-            for (int tok = 0; tok < p.T; ++tok) {
-              // keys 2t, 2t + 1, 2t + 8, 2t + 9 as masks of pairs, for this token
-              const int top = tl.n - p.T + tok;
-              uint32_t keep[2] = {0u, 0u};
+                // P of this token's rows; others take no part (their sums would
+                // be spoilt by what this token sees), so a product of their own
+                const bool mine = (r0 + 8 * nt + g) % p.T == tok;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<false>(x, a, mine ? lo[nt][0] : 0u, mine ? lo[nt][1] : 0u);
+                mma16816<false>(x, a, mine ? hi[nt][0] : 0u, mine ? hi[nt][1] : 0u);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int r = 2 * t + (j & 1) + 8 * (j / 2), key = key0 + r;
-                if (((seen >> r) & 1u) && ((key <= top && (p.left < 0 || key >= top - p.left)) ||
-                                           key < p.n_global))
-                  keep[j / 2] |= j & 1 ? 0xffff0000u : 0xffffu;
-              }
-#pragma unroll
-              for (int mt = 0; mt < kM; ++mt) {
-                uint32_t a[4];
-                ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
-                                                    2 * mt + lane / 8 % 2));
-                a[0] &= keep[0];
-                a[1] &= keep[0];
-                a[2] &= keep[1];
-                a[3] &= keep[1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  // P of this token's rows; others take no part (their sums would
-                  // be spoilt by what this token sees), so a product of their own
-                  const bool mine = (r0 + 8 * nt + g) % p.T == tok;
-                  float x[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma16816<false>(x, a, mine ? lo[nt][0] : 0u, mine ? lo[nt][1] : 0u);
-                  mma16816<false>(x, a, mine ? hi[nt][0] : 0u, mine ? hi[nt][1] : 0u);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if ((r0 + 8 * nt + 2 * t + j % 2) % p.T == tok) o[mt][nt][j] += x[j];
-                }
+                for (int j = 0; j < 4; ++j)
+                  if ((r0 + 8 * nt + 2 * t + j % 2) % p.T == tok) o[mt][nt][j] += x[j];
               }
             }
           }
@@ -716,133 +868,196 @@ window_kernel(const __grid_constant__ WindowParams p) {
       }
     }
 
-    // join the warps
-    copies_wait<0>();
-    __syncthreads();
-    const float unscale = 1.f / f;
+    // Join the warps into warp 0's sums. From here on m is the reference of the sums.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float sum = sum_over_keys(l[nt][j]);
-        if (g == 0) {
-          join_ml[2 * (warp * kRows + 8 * nt + 2 * t + j)] = m[nt][j];
-          join_ml[2 * (warp * kRows + 8 * nt + 2 * t + j) + 1] = sum;
-        }
-        float* row = join + (warp * kRows + 8 * nt + 2 * t + j) * (D + 4);
-        if constexpr (k4) {
+        l[nt][j] = sum_over_keys(l[nt][j]);
+        m[nt][j] -= float(e_f);                   // (-inf stays)
+        if (g == 0)
+          handed_ml[warp * kRows + 8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
+      }
+    for (int w0 = 1; w0 < kWarps; w0 += kHanded<NT, k4>) {
+      if (warp >= w0 && warp < w0 + kHanded<NT, k4>) {
+        float4* to = handed + (warp - w0) * kM * NT * 32 + lane;
 #pragma unroll
-          for (int c = 0; c < kGroups; ++c)
-            *reinterpret_cast<float4*>(row + 32 * c + 4 * g) =
-                make_float4(o[2 * c][nt][j] * unscale, o[2 * c][nt][j + 2] * unscale,
-                            o[2 * c + 1][nt][j] * unscale, o[2 * c + 1][nt][j + 2] * unscale);
-        } else {
+        for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < kM; ++mt) {
-            row[16 * mt + g] = o[mt][nt][j];
-            row[16 * mt + 8 + g] = o[mt][nt][j + 2];
+          for (int nt = 0; nt < NT; ++nt)
+            to[(mt * NT + nt) * 32] =
+                make_float4(o[mt][nt][0], o[mt][nt][1], o[mt][nt][2], o[mt][nt][3]);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = w0; w < min(kWarps, w0 + kHanded<NT, k4>); ++w) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float mine[2], theirs[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 ml = handed_ml[w * kRows + 8 * nt + 2 * t + j];
+              const float to = fmaxf(m[nt][j], ml.x);
+              // (a NaN among the scores is in the sums, not in the references)
+              mine[j] = m[nt][j] == -INFINITY ? 1.f : fast_exp2(m[nt][j] - to);
+              theirs[j] = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - to);
+              m[nt][j] = to;
+              l[nt][j] = l[nt][j] * mine[j] + ml.y * theirs[j];
+            }
+            const float4* from = handed + (w - w0) * kM * NT * 32 + lane;
+#pragma unroll
+            for (int mt = 0; mt < kM; ++mt) {
+              const float4 x = from[(mt * NT + nt) * 32];
+              o[mt][nt][0] = o[mt][nt][0] * mine[0] + x.x * theirs[0];
+              o[mt][nt][1] = o[mt][nt][1] * mine[1] + x.y * theirs[1];
+              o[mt][nt][2] = o[mt][nt][2] * mine[0] + x.z * theirs[0];
+              o[mt][nt][3] = o[mt][nt][3] * mine[1] + x.w * theirs[1];
+            }
           }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
-    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
-    for (int x = threadIdx.x; x < rows * (D / 8); x += kThreads) {
-      const int r = x / (D / 8), e = x % (D / 8) * 8;
-      float top = -INFINITY;
+    if (warp == 0) {
+      const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join_ml[2 * (w * kRows + r)]);
-      float sum = 0.f, acc[8] = {};
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = join_ml[2 * (w * kRows + r)], lw = join_ml[2 * (w * kRows + r) + 1];
-        // (a NaN among the scores is in the sums, not in the references)
-        const float by = mw == -INFINITY ? (lw != lw ? 1.f : 0.f) : fast_exp2(mw - top);
-        sum += by * lw;
-        const float* row = join + (w * kRows + r) * (D + 4) + e;
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * nt + 2 * t + j;
+          if (r >= rows) continue;
+          const bool empty = l[nt][j] == 0.f;
+          const float by = !whole ? 1.f : empty ? 0.f : 1.f / l[nt][j];
+          auto value = [&](int mt, int half) {
+            return whole && empty ? 0.f : o[mt][nt][j + 2 * half] * by;
+          };
+          __nv_bfloat16* out = p.o + (q_row0 + r) * D;
+          float* part = p.o_part + (1LL * slot * kRows + r) * D;
+          if constexpr (k4) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = by != 0.f ? fmaf(by, row[j], acc[j]) : acc[j];
-      }
-      if (whole) {
-        const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
-        if (empty)
+            for (int c = 0; c < kGroups; ++c) {
+              const float x[4] = {value(2 * c, 0), value(2 * c, 1), value(2 * c + 1, 0),
+                                  value(2 * c + 1, 1)};
+              if (whole)
+                *reinterpret_cast<uint2*>(out + 32 * c + 4 * g) =
+                    make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+              else
+                *reinterpret_cast<float4*>(part + 32 * c + 4 * g) =
+                    make_float4(x[0], x[1], x[2], x[3]);
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-        *reinterpret_cast<uint4*>(p.o + (q_row0 + r) * D + e) =
-            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                       pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-        if (e == 0 && p.lse != nullptr)
-          p.lse[q_row0 + r] =
-              empty ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, 0.693147180559945f, logf(sum));
-      } else {
-        float4* to = reinterpret_cast<float4*>(p.o_part + (1LL * slot * kRows + r) * D + e);
-        to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (e == 0) {
-          p.m_part[slot * kRows + r] = top;
-          p.l_part[slot * kRows + r] = sum;
+            for (int mt = 0; mt < kM; ++mt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int e = 16 * mt + 8 * half + g;
+                if (whole)
+                  out[e] = __float2bfloat16_rn(value(mt, half));
+                else
+                  part[e] = value(mt, half);
+              }
+          }
+          if (g == 0) {
+            if (!whole) {
+              p.m_part[slot * kRows + r] = m[nt][j];
+              p.l_part[slot * kRows + r] = l[nt][j];
+            } else if (p.lse != nullptr) {
+              p.lse[q_row0 + r] = empty ? -INFINITY
+                                        : fmaf(m[nt][j] == -INFINITY ? 0.f : m[nt][j],
+                                               0.693147180559945f, logf(l[nt][j]));
+            }
+          }
         }
-      }
     }
     u += run;
-    if (u < u_end) __syncthreads();               // the ring is written again
   }
 }
 
 // Joins the partial results of rows that more than one CTA worked on, and
-// writes those of requests without keys. Grid: x over groups of 8 of the Hkv·R
-// rows of request y.
-constexpr int kJoinWarps = 8;
-template <int D, int kRows>
+// writes those of requests without keys. kPer warps a row; grid: x over groups of
+// kJoinWarps / kPer of the Hkv·R rows of request y. Partial results are fetched
+// eight at a time.
+constexpr int kJoinWarps = 8, kFewRows = 1024;
+template <int D, int kRows, int kPer>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 window_join_kernel(const __grid_constant__ WindowParams p) {
+  constexpr int kLane = D / 32, kBatch = 8;       // elements of a lane
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int b = blockIdx.y, lane = threadIdx.x % 32;
-  const UnitSums<32 * kJoinWarps> sums(p, b);
-  const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32;
+  const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const PlaceSums<32 * kJoinWarps> sums(p, b);
+  const int row = blockIdx.x * (kJoinWarps / kPer) + warp / kPer;
   if (row >= p.Hkv * p.R) return;
   const int h = row / p.R, r = row % p.R;
   const Tiles tl = tiles_of(p, p.lens[b]);
   const long long q_row = 1LL * b * p.Hkv * p.R + row;
-  constexpr int kPer = D / 32;
-  float acc[kPer] = {}, sum = 0.f, top = -INFINITY;
+  float acc[kLane] = {}, sum = 0.f, top = -INFINITY;
   if (tl.units > 0) {
-    const int per_request = p.Hkv * p.blocks, units = sums.total * per_request;
-    const int ctas = min(p.grid, units);
-    const int u0 = sums.before * per_request + (h * p.blocks + r / kRows) * tl.units;
-    const int c0 = share_of(u0, ctas, units), c1 = share_of(u0 + tl.units - 1, ctas, units);
+    const int per_request = p.Hkv * p.blocks, places = sums.total * per_request;
+    const int ctas = min(p.grid, places);
+    const int item = sums.before * per_request +
+                     (h * p.blocks + r / kRows) * places_of(tl.units);
+    const int u0 = item + kItemCost, u1 = u0 + tl.units - 1;
+    const int c0 = share_of(u0, ctas, places), c1 = share_of(u1, ctas, places);
     if (c0 == c1) return;                         // its CTA has written it
-    const bool at_start = share_start(c0, ctas, units) == u0;
-    auto slot_of = [&](int c) { return (2 * c + (c == c0 && !at_start ? 1 : 0)) * kRows + r % kRows; };
+    // (a share that begins before the item holds a unit of another one first)
+    const bool at_start = share_start(c0, ctas, places) >= item;
+    auto slot_of = [&](int c) {
+      return (2 * c + (c == c0 && !at_start ? 1 : 0)) * kRows + r % kRows;
+    };
     for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.m_part[slot_of(c)]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    for (int c = c0; c <= c1; ++c) {
-      const int s = slot_of(c);
-      const float mc = p.m_part[s], lc = p.l_part[s];
-      const float by = mc == -INFINITY ? (lc != lc ? 1.f : 0.f) : fast_exp2(mc - top);
-      const float* part = p.o_part + 1LL * s * D + kPer * lane;
-      float x[kPer];
-      if constexpr (kPer == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(part);
-        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(part);
-        x[0] = y.x; x[1] = y.y;
-      }
-      sum += by * lc;
+    for (int first = c0 + warp % kPer; first <= c1; first += kPer * kBatch) {
+      float x[kBatch][kLane], by[kBatch], l[kBatch];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) acc[j] = by != 0.f ? fmaf(by, x[j], acc[j]) : acc[j];
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = first + i * kPer;
+        by[i] = l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) x[i][j] = 0.f;
+        if (c > c1) continue;
+        const int s = slot_of(c);
+        const float mc = p.m_part[s];
+        l[i] = p.l_part[s];
+        // (a NaN among the scores is in the sums, not in the references)
+        by[i] = mc == -INFINITY ? 1.f : fast_exp2(mc - top);
+        const float* part = p.o_part + 1LL * s * D + kLane * lane;
+        if constexpr (kLane == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(part);
+          x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(part);
+          x[i][0] = y.x; x[i][1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        sum = fmaf(by[i], l[i], sum);
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) acc[j] = fmaf(by[i], x[i][j], acc[j]);
+      }
+    }
+  }
+  if constexpr (kPer > 1) {
+    __shared__ float others[kJoinWarps][D + 1];
+#pragma unroll
+    for (int j = 0; j < kLane; ++j) others[warp][kLane * lane + j] = acc[j];
+    if (lane == 0) others[warp][D] = sum;
+    __syncthreads();
+    if (warp % kPer != 0) return;
+    for (int w = warp + 1; w < warp + kPer; ++w) {
+      sum += others[w][D];
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) acc[j] += others[w][kLane * lane + j];
     }
   }
   const bool empty = sum == 0.f;
   const float inv = empty ? 0.f : 1.f / sum;
-  __nv_bfloat16* to = p.o + q_row * D + kPer * lane;
+  __nv_bfloat16* to = p.o + q_row * D + kLane * lane;
 #pragma unroll
-  for (int j = 0; j < kPer; j += 2)
+  for (int j = 0; j < kLane; j += 2)
     *reinterpret_cast<uint32_t*>(to + j) =
         empty ? 0u : pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
@@ -866,9 +1081,9 @@ cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int sme
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-template <int D, bool k4, int NT>
+template <int D, bool k4, int NT, bool kRuns>
 cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
-  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT>);
+  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns>);
   constexpr int smem = smem_bytes<D, k4, NT>();
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -882,14 +1097,21 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   p.grid = int(std::min<long long>(most, 1LL * a.sm_count * kResident<NT, k4>));
   e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, p, a.stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT>),
-                          dim3(unsigned((p.Hkv * p.R + kJoinWarps - 1) / kJoinWarps),
-                               unsigned(p.B)),
+  // Few rows have many partial results each, over which a block's warps share.
+  const int rows = p.Hkv * p.R;
+  if (1LL * p.B * rows <= kFewRows)
+    return launch_dependent(
+        reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, kJoinWarps>),
+        dim3(unsigned(rows), unsigned(p.B)), 32 * kJoinWarps, 0, p, a.stream);
+  return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, 1>),
+                          dim3(unsigned((rows + kJoinWarps - 1) / kJoinWarps), unsigned(p.B)),
                           32 * kJoinWarps, 0, p, a.stream);
 }
 
 template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams& p) {
-  return p.R <= 8 ? launch_t<D, k4, 1>(a, p) : launch_t<D, k4, 2>(a, p);
+  if (p.page_size % kTile == 0)
+    return p.R <= 8 ? launch_t<D, k4, 1, true>(a, p) : launch_t<D, k4, 2, true>(a, p);
+  return p.R <= 8 ? launch_t<D, k4, 1, false>(a, p) : launch_t<D, k4, 2, false>(a, p);
 }
 
 }  // namespace
