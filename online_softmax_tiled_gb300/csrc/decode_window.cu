@@ -48,7 +48,10 @@ ATTN_DEFINE_ERROR_WORD(take_error_decode_window)
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+// Keys of a fragment, and runs of them in a step of a warp.
+constexpr int kKeys = 16;
+template <bool k4, int NT> constexpr int kRunsOf = k4 && NT == 1 ? 2 : 1;
 
 struct WindowParams {
   const __nv_bfloat16* q;
@@ -73,7 +76,7 @@ struct Tiles {
   int n, lo, global, first, count, units;
   ATTN_DEVINL int at(int i) const { return i < global ? i : i - global + first; }
 };
-ATTN_DEVINL Tiles tiles_of(const WindowParams& p, int n) {
+template <int kTile> ATTN_DEVINL Tiles tiles_of(const WindowParams& p, int n) {
   Tiles t;
   t.n = unsigned(n) <= unsigned(p.cap) ? n : 0;
   // first key of the first token's window
@@ -94,13 +97,13 @@ ATTN_DEVINL int places_of(int units) { return units > 0 ? units + kItemCost : 0;
 
 // Sums over the requests of an item's places: of all, and of those before request
 // `upto` (all threads of the block get both).
-template <int kN> struct PlaceSums {
+template <int kN, int kTile> struct PlaceSums {
   int total, before;
   ATTN_DEVINL PlaceSums(const WindowParams& p, int upto) {
     __shared__ int part[2][kN / 32];
     int a = 0, b = 0;
     for (int r = threadIdx.x; r < p.B; r += kN) {
-      const int u = places_of(tiles_of(p, p.lens[r]).units);
+      const int u = places_of(tiles_of<kTile>(p, p.lens[r]).units);
       a += u;
       if (r < upto) b += u;
     }
@@ -134,11 +137,12 @@ ATTN_DEVINL int share_of(int place, int ctas, int places) {
 struct Place {
   int b, before, unit;
 };
+template <int kTile>
 ATTN_DEVINL Place find_place(const WindowParams& p, int place, int lane) {
   const int per_request = p.Hkv * p.blocks;
   int places = 0, units = 0;                      // of the requests so far
   for (int r0 = 0; r0 < p.B; r0 += 32) {
-    const int u = r0 + lane < p.B ? tiles_of(p, p.lens[r0 + lane]).units : 0;
+    const int u = r0 + lane < p.B ? tiles_of<kTile>(p, p.lens[r0 + lane]).units : 0;
     int incl = places_of(u) * per_request, incl_u = u * per_request;
     const int own = incl, own_u = incl_u;
 #pragma unroll
@@ -250,14 +254,16 @@ ATTN_DEVINL float pow2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23)
 
 // ------------------------------------------------------------ the tiles
 
-// A warp's ring: K and V rows of kTile keys a stage, then (4 bits) their scales,
-// then (pages that do not hold whole tiles) a word that says which keys are there.
-template <int D, bool k4> struct Ring {
+// A warp's ring. A stage holds runs of K rows, V rows and (4 bits) scales of 16
+// keys each, then (pages that do not hold whole runs) a word that says which keys
+// are there.
+template <int D, bool k4, int kRun> struct Ring {
   static constexpr int kRow = k4 ? D / 2 : 2 * D;           // bytes of a row
   static constexpr int kScales = k4 ? D / 16 : 0;           // and of its scales
-  static constexpr int kInfo = 2 * kTile * (kRow + kScales);
+  static constexpr int kPart = 2 * kKeys * (kRow + kScales);  // bytes of a run
+  static constexpr int kInfo = kRun * kPart;
   static constexpr int kStage = kInfo + 16;
-  static constexpr int kStages = k4 ? 4 : 3;
+  static constexpr int kStages = kRun == 2 ? 2 : k4 ? 4 : 3;
   static constexpr int kBytes = kStages * kStage;
   static constexpr int kPieces = kRow / 16;                 // 16-byte pieces of a row
 
@@ -270,38 +276,49 @@ template <int D, bool k4> struct Ring {
   // V. 4 bits: a lane reads rows 2t, 2t + 1, 2t + 8 and 2t + 9, so even rows come
   // first, then odd ones, and every second pair of them is turned by two pieces.
   static ATTN_DEVINL int v_at(int r, int c) {
-    if (!k4) return kTile * kRow + k_at(r, c);
+    if (!k4) return kKeys * kRow + k_at(r, c);
     const int s = r / 2 + (r & 1) * 8;
-    return kTile * kRow + s * kRow + 16 * (D == 128 ? c ^ (s & 2) : c);
+    return kKeys * kRow + s * kRow + 16 * (D == 128 ? c ^ (s & 2) : c);
   }
-  static ATTN_DEVINL int k_scale_at(int r) { return 2 * kTile * kRow + r * kScales; }
-  static ATTN_DEVINL int v_scale_at(int r) { return k_scale_at(r) + kTile * kScales; }
+  static ATTN_DEVINL int k_scale_at(int r) { return 2 * kKeys * kRow + r * kScales; }
+  static ATTN_DEVINL int v_scale_at(int r) { return k_scale_at(r) + kKeys * kScales; }
 };
 
 // CTAs per SM the registers are cut for.
-template <int NT, bool k4> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
+template <int NT, bool k4, bool kTwice> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
 
 // Warps whose sums are handed to warp 0 at a time, each as [kM·NT][32 lanes] of
 // four floats.
 template <int NT, bool k4> constexpr int kHanded = k4 && NT == 1 ? 3 : 1;
 
-template <int D, bool k4, int NT>
+template <int D, bool k4, int NT, bool kTwice>
 constexpr int smem_bytes() {
-  return kWarps * Ring<D, k4>::kBytes + kHanded<NT, k4> * (D / 16) * NT * 512 +
+  return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes + kHanded<NT, k4> * (kTwice ? D / 32 : D / 16) * NT * 512 +
          kWarps * 8 * NT * 8;
 }
 
-// What a tile is: nothing to compute, all keys seen by all tokens, or neither.
-enum : uint32_t { kNone = 0, kFull = 1, kPart = 2 };
+// What a tile is: nothing to compute, all keys seen by all tokens, or neither;
+// kLacks << r: run r of its keys is not there.
+enum : uint32_t { kNone = 0, kFull = 1, kPart = 2, kLacks = 4 };
 
 // NT blocks of 8 query rows at a time. kRuns: pages hold whole tiles (page_size
 // a multiple of 16), so a tile's rows are adjacent: one table entry and one
-// address instead of one per row.
-template <int D, bool k4, int NT, bool kRuns>
-__global__ void __launch_bounds__(kThreads, kResident<NT, k4>)
+// address instead of one per row. kTwice (4 bits, up to 4 query rows): the
+// fragments' columns 4 .. 7 hold the rows a second time and take the odd groups of
+// 32 elements, columns 0 .. 3 the even ones, so that a lane scales half as many sums
+// and probabilities (the unscaled halves of columns come out of the products
+// too, and are not read).
+template <int D, bool k4, int NT, bool kRuns, bool kTwice>
+__global__ void __launch_bounds__(kThreads, kResident<NT, k4, kTwice>)
 window_kernel(const __grid_constant__ WindowParams p) {
-  using RingT = Ring<D, k4>;
-  constexpr int kStages = RingT::kStages, kRows = 8 * NT, kM = D / 16, kGroups = D / 32;
+  constexpr int kRun = kRunsOf<k4, NT>, kTile = kRun * kKeys;
+  using RingT = Ring<D, k4, kRun>;
+  constexpr int kStages = RingT::kStages, kRows = 8 * NT, kGroups = D / 32;
+  // blocks of 16 elements of a row's sums (kTwice: even and odd groups share theirs)
+  constexpr int kM = kTwice ? D / 32 : D / 16, kQ = D / 16;
+  // groups that a lane scales
+  constexpr int kOwn = kTwice ? kGroups / 2 : kGroups;
+  constexpr int kRowMask = kTwice ? 3 : 15;       // of a column's query row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Place share[2];
   pdl_launch_dependents();
@@ -315,14 +332,14 @@ window_kernel(const __grid_constant__ WindowParams p) {
   pdl_wait_primary();
   // this CTA's share, and the request it begins in
   const int per_request = p.Hkv * p.blocks;
-  const int places = PlaceSums<kThreads>(p, 0).total * per_request;
+  const int places = PlaceSums<kThreads, kTile>(p, 0).total * per_request;
   if (blockIdx.x == 0)
     for (int r = threadIdx.x; r < p.B; r += kThreads)
       if (unsigned(p.lens[r]) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
   const int ctas = min(p.grid, places);
   if (int(blockIdx.x) >= ctas) return;
   if (warp < 2) {
-    const Place at = find_place(p, share_start(blockIdx.x + warp, ctas, places), lane);
+    const Place at = find_place<kTile>(p, share_start(blockIdx.x + warp, ctas, places), lane);
     if (lane == 0) share[warp] = at;
   }
   __syncthreads();
@@ -333,20 +350,23 @@ window_kernel(const __grid_constant__ WindowParams p) {
   // are worked out at once, one per lane, while those before them are computed:
   // `ahead` is the run that follows the one in use.
   struct Tile {
-    uint32_t row;                                 // kRuns: of the pool; else the first key
+    uint32_t row[kRun];                           // kRuns: of the pool; else the first key
     uint32_t what;
     int b, h;                                     // !kRuns
   } now{}, ahead{};
-  int ahead_page = 0, ahead_slot = 0, pb = b, pbefore = before;
+  int ahead_page[kRun] = {}, ahead_slot[kRun] = {}, pb = b, pbefore = before;
+  auto wanted = [&](const Tiles& tl, int key) {   // by any token
+    return key < tl.n && (key >= tl.lo || key < p.n_global);
+  };
+  auto page_of = [&](int key) { return int(__umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift); };
   auto look_ahead = [&](int k) {                  // of tiles k .. k + 31
     const int u = u_begin + k + lane;
     ahead.what = kNone;
-    ahead_page = 0;
     if (u < u_end) {
-      Tiles tl = tiles_of(p, p.lens[pb]);
+      Tiles tl = tiles_of<kTile>(p, p.lens[pb]);
       while (u >= pbefore + tl.units * per_request) {
         pbefore += tl.units * per_request;
-        tl = tiles_of(p, p.lens[++pb]);
+        tl = tiles_of<kTile>(p, p.lens[++pb]);
       }
       const int item = (u - pbefore) / tl.units;
       const int i = kWarps * ((u - pbefore) - item * tl.units) + warp;
@@ -358,11 +378,18 @@ window_kernel(const __grid_constant__ WindowParams p) {
         ahead.b = pb;
         ahead.h = item / p.blocks;
         if constexpr (kRuns) {
-          const int page = int(__umulhi(2u * uint32_t(key0), p.page_mul) >> p.page_shift);
-          ahead_slot = key0 - page * p.page_size;
-          ahead_page = p.table[1LL * pb * p.max_pages + page];
+#pragma unroll
+          for (int r = 0; r < kRun; ++r) {
+            // (a run whose first key is not wanted may have none at all, and no page)
+            const int key = key0 + r * kKeys;
+            const bool any = wanted(tl, key) || wanted(tl, max(key, min(tl.lo, key + kKeys - 1)));
+            const int page = page_of(key);
+            ahead_slot[r] = key - page * p.page_size;
+            ahead_page[r] = any ? p.table[1LL * pb * p.max_pages + page] : 0;
+            if (!any) ahead.what |= kLacks << r;
+          }
         } else {
-          ahead.row = uint32_t(key0);
+          ahead.row[0] = uint32_t(key0);
         }
       }
     }
@@ -370,14 +397,9 @@ window_kernel(const __grid_constant__ WindowParams p) {
     pbefore = __shfl_sync(0xffffffffu, pbefore, 31);
   };
   const int n_tiles = u_end - u_begin;
-  // !kRuns: a tile's table entries, key lane % 16's, read a tile before its copies.
+  // !kRuns: a tile's table entries, key lane % kTile's, read a tile before its copies.
   // (Keys that no token sees are not looked up: their pages may be gone.)
   int next_page = 0;
-  auto key_page = [&](int key) { return int(__umulhi(2u * uint32_t(key), p.page_mul) >> p.page_shift); };
-  auto wanted = [&](int rb, int key) {
-    const Tiles tl = tiles_of(p, p.lens[rb]);
-    return key < tl.n && (key >= tl.lo || key < p.n_global);
-  };
   auto look_up = [&](int k) {
     if (kRuns || k >= n_tiles) return;
     if (k % 32 == 0) {
@@ -385,84 +407,106 @@ window_kernel(const __grid_constant__ WindowParams p) {
       look_ahead(k + 32);
     }
     if (__shfl_sync(0xffffffffu, now.what, k % 32) == kNone) return;
-    const int key = int(__shfl_sync(0xffffffffu, now.row, k % 32)) + lane % kTile;
+    const int key = int(__shfl_sync(0xffffffffu, now.row[0], k % 32)) + lane % kTile;
     const int rb = __shfl_sync(0xffffffffu, now.b, k % 32);
-    next_page = wanted(rb, key) ? p.table[1LL * rb * p.max_pages + key_page(key)] : -1;
+    next_page = wanted(tiles_of<kTile>(p, p.lens[rb]), key)
+                    ? p.table[1LL * rb * p.max_pages + page_of(key)] : -1;
   };
+  // kTwice: picks the low half (columns 0 .. 3) or the high half of two scales, as a float
+  const uint32_t own_half = t < 2 ? 0x1044u : 0x3244u;
+  const uint32_t low_columns = g < 4 ? 0xffffffffu : 0u;   // of a fragment of Pᵀ
   // the lane's parts of a tile's copies
   const uint8_t* const k_src = p.k + 16 * lane;
   const uint8_t* const v_src = p.v + 16 * lane;
   const uint8_t* const s_src =
-      k4 ? (lane < kTile ? p.k_scales : p.v_scales) + lane % kTile * RingT::kScales : nullptr;
+      k4 ? (lane < kKeys ? p.k_scales : p.v_scales) + lane % kKeys * RingT::kScales : nullptr;
   constexpr int kPer = 32 / RingT::kPieces;       // rows a step of the copies
   const uint32_t k_dst = ring + RingT::k_at(lane / RingT::kPieces, lane % RingT::kPieces);
   const uint32_t v_dst = ring + RingT::v_at(lane / RingT::kPieces, lane % RingT::kPieces);
-  const uint32_t s_dst = ring + (lane < kTile ? RingT::k_scale_at(lane % kTile)
-                                              : RingT::v_scale_at(lane % kTile));
-  uint32_t whats = 0;                             // of the tiles in the ring, two bits each
+  const uint32_t s_dst = ring + (lane < kKeys ? RingT::k_scale_at(lane % kKeys)
+                                              : RingT::v_scale_at(lane % kKeys));
+  uint32_t whats = 0;                             // of the tiles in the ring, four bits each
   auto issue = [&](int k, uint32_t stage) {       // stage: its offset in the ring
-    whats >>= 2;
+    whats >>= 4;
     if (k < n_tiles) {
       uint32_t what;
       if constexpr (kRuns) {
         if (k % 32 == 0) {
-          // (a pool has fewer than 2^32 rows)
           now = ahead;
-          const bool ok = unsigned(ahead_page) < unsigned(p.num_pages);
-          if (!ok && now.what != kNone) {
-            attn_flag_error(kErrBadIndex);
-            now.what = kNone;
+#pragma unroll
+          for (int r = 0; r < kRun; ++r) {
+            // (a pool has fewer than 2^32 rows)
+            const bool ok = unsigned(ahead_page[r]) < unsigned(p.num_pages);
+            if (!ok && now.what != kNone) {
+              attn_flag_error(kErrBadIndex);
+              now.what = (now.what & ~kFull) | kPart | kLacks << r;
+            }
+            now.row[r] = (uint32_t(ok ? ahead_page[r] : 0) * uint32_t(p.Hkv) + uint32_t(now.h)) *
+                             uint32_t(p.page_size) + uint32_t(ahead_slot[r]);
           }
-          now.row = (uint32_t(ok ? ahead_page : 0) * uint32_t(p.Hkv) + uint32_t(now.h)) *
-                        uint32_t(p.page_size) + uint32_t(ahead_slot);
           look_ahead(k + 32);
         }
-        const uint32_t row = __shfl_sync(0xffffffffu, now.row, k % 32);
         what = __shfl_sync(0xffffffffu, now.what, k % 32);
         if (what != kNone) {
-          // all 16 rows, of which the page has room for each, seen or not
-          const uint8_t* kp = k_src + size_t(row) * RingT::kRow;
-          const uint8_t* vp = v_src + size_t(row) * RingT::kRow;
 #pragma unroll
-          for (int s = 0; s < kTile / kPer; ++s) {
-            // (the swizzles repeat, or turn by a constant)
-            const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
-            const uint32_t kd = k4 ? k_dst + s * kPer * RingT::kRow : ring + RingT::k_at(r, c);
-            const uint32_t vd = k4 ? v_dst + s * kPer / 2 * RingT::kRow : ring + RingT::v_at(r, c);
-            copy_async<16>(kd + stage, kp + s * kPer * RingT::kRow);
-            copy_async<16>(vd + stage, vp + s * kPer * RingT::kRow);
+          for (int run = 0; run < kRun; ++run) {
+            // all 16 rows, of which the page has room for each, seen or not
+            const uint32_t row = __shfl_sync(0xffffffffu, now.row[run], k % 32);
+            const uint32_t to = stage + run * RingT::kPart;
+            const uint8_t* kp = k_src + size_t(row) * RingT::kRow;
+            const uint8_t* vp = v_src + size_t(row) * RingT::kRow;
+#pragma unroll
+            for (int s = 0; s < kKeys / kPer; ++s) {
+              // (the swizzles repeat, or turn by a constant)
+              const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
+              const uint32_t kd = k4 ? k_dst + s * kPer * RingT::kRow : ring + RingT::k_at(r, c);
+              const uint32_t vd = k4 ? v_dst + s * kPer / 2 * RingT::kRow : ring + RingT::v_at(r, c);
+              copy_async<16>(kd + to, kp + s * kPer * RingT::kRow);
+              copy_async<16>(vd + to, vp + s * kPer * RingT::kRow);
+            }
+            if constexpr (k4)
+              copy_async<RingT::kScales>(s_dst + to, s_src + size_t(row) * RingT::kScales);
           }
-          if constexpr (k4)
-            copy_async<RingT::kScales>(s_dst + stage, s_src + size_t(row) * RingT::kScales);
         }
       } else {
         what = __shfl_sync(0xffffffffu, now.what, k % 32);
         if (what != kNone) {
-          const int key = int(__shfl_sync(0xffffffffu, now.row, k % 32)) + lane % kTile;
+          const int key = int(__shfl_sync(0xffffffffu, now.row[0], k % 32)) + lane % kTile;
           const int h = __shfl_sync(0xffffffffu, now.h, k % 32);
           const int rb = __shfl_sync(0xffffffffu, now.b, k % 32);
           const bool ok = unsigned(next_page) < unsigned(p.num_pages);
-          if (!ok && wanted(rb, key)) attn_flag_error(kErrBadIndex);
+          if (!ok && wanted(tiles_of<kTile>(p, p.lens[rb]), key)) attn_flag_error(kErrBadIndex);
           const uint32_t row = ok ? (uint32_t(next_page) * uint32_t(p.Hkv) + uint32_t(h)) *
                                             uint32_t(p.page_size) +
-                                        uint32_t(key - key_page(key) * p.page_size)
+                                        uint32_t(key - page_of(key) * p.page_size)
                                   : 0u;
-          const uint32_t there = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+          constexpr uint32_t kAll = kTile == 32 ? 0xffffffffu : 0xffffu;
+          const uint32_t there = __ballot_sync(0xffffffffu, ok) & kAll;
 #pragma unroll
-          for (int s = 0; s < kTile / kPer; ++s) {
-            const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
-            const size_t off = size_t(__shfl_sync(0xffffffffu, row, r)) * RingT::kRow + 16 * c;
-            copy_async<16>(ring + stage + RingT::k_at(r, c), p.k + off);
-            copy_async<16>(ring + stage + RingT::v_at(r, c), p.v + off);
+          for (int run = 0; run < kRun; ++run) {
+            const uint32_t to = ring + stage + run * RingT::kPart;
+#pragma unroll
+            for (int s = 0; s < kKeys / kPer; ++s) {
+              const int r = s * kPer + lane / RingT::kPieces, c = lane % RingT::kPieces;
+              const size_t off =
+                  size_t(__shfl_sync(0xffffffffu, row, run * kKeys + r)) * RingT::kRow + 16 * c;
+              copy_async<16>(to + RingT::k_at(r, c), p.k + off);
+              copy_async<16>(to + RingT::v_at(r, c), p.v + off);
+            }
+            if constexpr (k4) {
+              const size_t off =
+                  size_t(__shfl_sync(0xffffffffu, row, run * kKeys + lane % kKeys)) *
+                  RingT::kScales;
+              copy_async<RingT::kScales>(
+                  s_dst + stage + run * RingT::kPart,
+                  (lane < kKeys ? p.k_scales : p.v_scales) + off);
+            }
           }
-          if constexpr (k4)
-            copy_async<RingT::kScales>(s_dst + stage, (lane < kTile ? p.k_scales : p.v_scales) +
-                                                          size_t(row) * RingT::kScales);
-          if (there != 0xffffu) what = there != 0 ? kPart : kNone;
+          if (there != kAll) what = there != 0 ? kPart : kNone;
           sts32(ring + stage + RingT::kInfo, there);
         }
       }
-      whats |= what << (2 * (kStages - 1));
+      whats |= what << (4 * (kStages - 1));
     }
     copies_commit();
   };
@@ -477,10 +521,10 @@ window_kernel(const __grid_constant__ WindowParams p) {
   int k = 0;
   uint32_t stage = 0;                             // of tile k
   for (int u = u_begin; u < u_end;) {
-    Tiles tl = tiles_of(p, p.lens[b]);
+    Tiles tl = tiles_of<kTile>(p, p.lens[b]);
     while (u >= before + tl.units * per_request) {
       before += tl.units * per_request;
-      tl = tiles_of(p, p.lens[++b]);
+      tl = tiles_of<kTile>(p, p.lens[++b]);
     }
     const int item = (u - before) / tl.units, local = (u - before) % tl.units;
     const int h = item / p.blocks, r0 = item % p.blocks * kRows;
@@ -492,12 +536,13 @@ window_kernel(const __grid_constant__ WindowParams p) {
     // Query rows as the fragments of Qᵀ: lane (g, t) holds row g of each block.
     // 4 bits: k-step 2c + s is the elements 32c + 8t + 4s .. + 3; scaled by a power
     // of two that puts the row's largest value into [2^8, 2^9).
-    uint32_t qf[kM][NT][2];
+    uint32_t qf[kQ][NT][2];
     float to_log2[NT][2];                         // scores times this, per column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool live = 8 * nt + g < rows;
-      const __nv_bfloat16* src = p.q + (q_row0 + 8 * nt + g) * D;
+      const int row = (8 * nt + g) & kRowMask;
+      const bool live = row < rows;
+      const __nv_bfloat16* src = p.q + (q_row0 + row) * D;
       if constexpr (k4) {
         uint4 raw[kGroups];
         uint32_t top = 0;
@@ -518,14 +563,15 @@ window_kernel(const __grid_constant__ WindowParams p) {
           const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            qf[2 * c + j / 2][nt][j % 2] = pack_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
+            qf[2 * c + j / 2][nt][j % 2] =
+                kTwice && c % 2 != g / 4 ? 0u : pack_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
         }
         const float down = fmaxf(p.scale_log2 * pow2i(e - 8), 1.17549435e-38f);
         to_log2[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
         to_log2[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
       } else {
 #pragma unroll
-        for (int j = 0; j < kM; ++j)
+        for (int j = 0; j < kQ; ++j)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
             qf[j][nt][s] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * j + 8 * s + 2 * t)
@@ -538,7 +584,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) last[nt][j] = tl.n - p.T + (r0 + 8 * nt + 2 * t + j) % p.T;
+      for (int j = 0; j < 2; ++j) last[nt][j] = tl.n - p.T + (r0 + ((8 * nt + 2 * t + j) & kRowMask)) % p.T;
 
     // m: row maxima, in log2 units, as of the last time that one was passed by 8;
     // limit: 8 above them, as raw sums. Sums are of 2^(s - m + e_f).
@@ -566,86 +612,114 @@ window_kernel(const __grid_constant__ WindowParams p) {
       look_up(k + kStages);
       const uint32_t at = ring + stage;
       stage = stage == (kStages - 1) * RingT::kStage ? 0 : stage + RingT::kStage;
-      const uint32_t what = whats & 3u;
+      const uint32_t what = whats & 15u;
       if (what == kNone) continue;
       const bool full = what == kFull;
 
-      // Sᵀ: rows are keys g and g + 8, columns query rows 2t and 2t + 1
-      float s[NT][4];
+      // Sᵀ: rows are keys g and g + 8 of a run, columns query rows 2t and 2t + 1
+      float s[kRun][NT][4];
+      float vs[kRun][2][kOwn];                    // 4 bits: scales of V, keys g and g + 8
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int run_ = 0; run_ < kRun; ++run_) {
+        const uint32_t from = at + run_ * RingT::kPart;
+        float (&sr)[NT][4] = s[run_];
+        if constexpr (k4) {
+          uint32_t w[2][D / 32];                  // codes of keys g, g + 8
+          float ks[2][kOwn];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
-      float vs[2][kGroups];                     // 4 bits: scales of V, keys g and g + 8
-      if constexpr (k4) {
-        uint32_t w[2][D / 32];                  // codes of keys g, g + 8
-        float ks[2][kGroups];
+          for (int j = 0; j < 2; ++j) {
+            const int r = g + 8 * j;
+            uint32_t sk[D / 64], sv[D / 64];
+            if constexpr (D == 128) {
+              const uint4 x = lds128(from + RingT::k_at(r, t));
+              w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
+              const uint2 y = lds64(from + RingT::k_scale_at(r)),
+                          z = lds64(from + RingT::v_scale_at(r));
+              sk[0] = y.x; sk[1] = y.y; sv[0] = z.x; sv[1] = z.y;
+            } else {
+              const uint2 x = lds64(from + RingT::k_at(r, 0) + 8 * t);
+              w[j][0] = x.x; w[j][1] = x.y;
+              sk[0] = lds32(from + RingT::k_scale_at(r));
+              sv[0] = lds32(from + RingT::v_scale_at(r));
+            }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = g + 8 * j;
-          uint32_t sk[D / 64], sv[D / 64];
-          if constexpr (D == 128) {
-            const uint4 x = lds128(at + RingT::k_at(r, t));
-            w[j][0] = x.x; w[j][1] = x.y; w[j][2] = x.z; w[j][3] = x.w;
-            const uint2 y = lds64(at + RingT::k_scale_at(r)), z = lds64(at + RingT::v_scale_at(r));
-            sk[0] = y.x; sk[1] = y.y; sv[0] = z.x; sv[1] = z.y;
-          } else {
-            const uint2 x = lds64(at + RingT::k_at(r, 0) + 8 * t);
-            w[j][0] = x.x; w[j][1] = x.y;
-            sk[0] = lds32(at + RingT::k_scale_at(r));
-            sv[0] = lds32(at + RingT::v_scale_at(r));
+            for (int c = 0; c < kOwn; ++c) {
+              if constexpr (kTwice) {             // the half of the pair that is this lane's
+                ks[j][c] = __uint_as_float(__byte_perm(sk[c], 0, own_half));
+                vs[run_][j][c] = __uint_as_float(__byte_perm(sv[c], 0, own_half));
+              } else {
+                ks[j][c] = c % 2 ? bf16hi(sk[c / 2]) : bf16lo(sk[c / 2]);
+                vs[run_][j][c] = c % 2 ? bf16hi(sv[c / 2]) : bf16lo(sv[c / 2]);
+              }
+            }
           }
+          float x[NT][4];                         // sums of a group (kTwice: of two)
 #pragma unroll
           for (int c = 0; c < kGroups; ++c) {
-            ks[j][c] = c % 2 ? bf16hi(sk[c / 2]) : bf16lo(sk[c / 2]);
-            vs[j][c] = c % 2 ? bf16hi(sv[c / 2]) : bf16lo(sv[c / 2]);
-          }
-        }
 #pragma unroll
-        for (int c = 0; c < kGroups; ++c) {
-          float x[NT][4];
+            for (int step = 0; step < 2; ++step) {
+              const uint32_t w0 = w[0][step * (D / 64) + c / 2],
+                             w1 = w[1][step * (D / 64) + c / 2];
+              uint32_t a[4];
+              if (c % 2) {
+                a[0] = e2m1x2_to_f16x2<2>(w0); a[1] = e2m1x2_to_f16x2<2>(w1);
+                a[2] = e2m1x2_to_f16x2<3>(w0); a[3] = e2m1x2_to_f16x2<3>(w1);
+              } else {
+                a[0] = e2m1x2_to_f16x2<0>(w0); a[1] = e2m1x2_to_f16x2<0>(w1);
+                a[2] = e2m1x2_to_f16x2<1>(w0); a[3] = e2m1x2_to_f16x2<1>(w1);
+              }
 #pragma unroll
-          for (int step = 0; step < 2; ++step) {
-            const uint32_t w0 = w[0][step * (D / 64) + c / 2], w1 = w[1][step * (D / 64) + c / 2];
-            uint32_t a[4];
-            if (c % 2) {
-              a[0] = e2m1x2_to_f16x2<2>(w0); a[1] = e2m1x2_to_f16x2<2>(w1);
-              a[2] = e2m1x2_to_f16x2<3>(w0); a[3] = e2m1x2_to_f16x2<3>(w1);
-            } else {
-              a[0] = e2m1x2_to_f16x2<0>(w0); a[1] = e2m1x2_to_f16x2<0>(w1);
-              a[2] = e2m1x2_to_f16x2<1>(w0); a[3] = e2m1x2_to_f16x2<1>(w1);
+              for (int nt = 0; nt < NT; ++nt) {
+                if (step == 0 && !(kTwice && c % 2))
+                  mma16816_first(x[nt], a, qf[2 * c][nt][0], qf[2 * c][nt][1]);
+                else
+                  mma16816<true>(x[nt], a, qf[2 * c + step][nt][0], qf[2 * c + step][nt][1]);
+              }
             }
+            if (kTwice && c % 2 == 0) continue;
+            const int o_ = kTwice ? c / 2 : c;    // of the lane's scales
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (step == 0)
-                mma16816_first(x[nt], a, qf[2 * c][nt][0], qf[2 * c][nt][1]);
-              else
-                mma16816<true>(x[nt], a, qf[2 * c + 1][nt][0], qf[2 * c + 1][nt][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sr[nt][j] = o_ == 0 ? x[nt][j] * ks[j / 2][0]
+                                    : fmaf(x[nt][j], ks[j / 2][o_], sr[nt][j]);
           }
+          if constexpr (kTwice) {                 // even and odd groups together
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sr[0][j] += __shfl_xor_sync(0xffffffffu, sr[0][j], 2);
+          }
+        } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              s[nt][j] = c == 0 ? x[nt][j] * ks[j / 2][0] : fmaf(x[nt][j], ks[j / 2][c], s[nt][j]);
-        }
-      } else {
+            for (int j = 0; j < 4; ++j) sr[nt][j] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kM; ++j) {
-          uint32_t a[4];
-          // matrices: keys 0-7, keys 8-15, then the same of the next 8 elements
-          ldmatrix4(a, at + RingT::k_at(lane % 16, 2 * j + lane / 16));
+          for (int j = 0; j < kQ; ++j) {
+            uint32_t a[4];
+            // matrices: keys 0-7, keys 8-15, then the same of the next 8 elements
+            ldmatrix4(a, from + RingT::k_at(lane % 16, 2 * j + lane / 16));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[j][nt][0], qf[j][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(sr[nt], a, qf[j][nt][0], qf[j][nt][1]);
+          }
         }
       }
 
-      uint32_t hidden[NT][2];                     // !full: bits 0 .. 15, keys a row does not see
+      uint32_t hidden[NT][2];                     // !full: a bit a key that a row does not see
       if (!full) {
         const int key0 = kTile * tl.at(i);
-        // key x of a tile counted from key0: bits below(x)
-        auto below = [](int x) { return (1u << max(0, min(kTile, x))) - 1u; };
-        const uint32_t there = (kRuns ? 0xffffu : lds32(at + RingT::kInfo)) & below(tl.n - key0);
+        // the tile's keys below key0 + x
+        auto below = [](int x) {
+          return x <= 0 ? 0u : x >= kTile ? 0xffffffffu : (1u << x) - 1u;
+        };
+        uint32_t there = below(tl.n - key0);
+        if constexpr (!kRuns) {
+          there &= lds32(at + RingT::kInfo);
+        } else {
+#pragma unroll
+          for (int r = 0; r < kRun; ++r)
+            if (what & (kLacks << r)) there &= ~(0xffffu << (16 * r));
+        }
         const uint32_t first = below(p.n_global - key0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -655,29 +729,41 @@ window_kernel(const __grid_constant__ WindowParams p) {
             const uint32_t near = below(top + 1 - key0) &
                                   ~(p.left < 0 ? 0u : below(top - p.left - key0));
             hidden[nt][j] = ~(there & (near | first));
-            if ((hidden[nt][j] >> g) & 1u) s[nt][j] = -INFINITY;
-            if ((hidden[nt][j] >> (g + 8)) & 1u) s[nt][j + 2] = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kRun; ++r) {
+              if ((hidden[nt][j] >> (16 * r + g)) & 1u) s[r][nt][j] = -INFINITY;
+              if ((hidden[nt][j] >> (16 * r + g + 8)) & 1u) s[r][nt][j + 2] = -INFINITY;
+            }
           }
         if constexpr (k4) {                       // what no token sees has no say in e_f
           const uint32_t any = there & (~below(tl.lo - key0) | first);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (!((any >> (g + 8 * j)) & 1u))
+          for (int r = 0; r < kRun; ++r)
 #pragma unroll
-              for (int c = 0; c < kGroups; ++c) vs[j][c] = 0.f;
+            for (int j = 0; j < 2; ++j)
+              if (!((any >> (16 * r + g + 8 * j)) & 1u))
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c) vs[r][j][c] = 0.f;
         }
       }
       // whether a score passes its row's maximum so far by 8 binary orders, or a
       // scale of V the power of two that P is taken with by 2^7
+      auto top_score = [&](int nt, int j) {
+        float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+        if constexpr (kRun == 2) x = max3(x, s[kRun - 1][nt][j], s[kRun - 1][nt][j + 2]);
+        return x;
+      };
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) above |= fmaxf(s[nt][j], s[nt][j + 2]) > limit[nt][j];
+        for (int j = 0; j < 2; ++j) above |= top_score(nt, j) > limit[nt][j];
       if constexpr (k4) {
         float vmax = 0.f;
 #pragma unroll
-        for (int c = 0; c < kGroups; ++c) vmax = max3(vmax, vs[0][c], vs[1][c]);
+        for (int r = 0; r < kRun; ++r)
+#pragma unroll
+          for (int c = 0; c < kOwn; ++c) vmax = max3(vmax, vs[r][0][c], vs[r][1][c]);
         above |= vmax > v_limit;
       }
       if (__any_sync(0xffffffffu, above)) {
@@ -687,10 +773,13 @@ window_kernel(const __grid_constant__ WindowParams p) {
           // (a scale that is not finite counts for nothing: its group alone is lost)
           uint32_t top = 0;
 #pragma unroll
-          for (int c = 0; c < kGroups; ++c)
+          for (int r = 0; r < kRun; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (vs[j][c] < INFINITY) top = max(top, __float_as_uint(fmaxf(vs[j][c], 0.f)));
+            for (int c = 0; c < kOwn; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (vs[r][j][c] < INFINITY)
+                  top = max(top, __float_as_uint(fmaxf(vs[r][j][c], 0.f)));
           top = __reduce_max_sync(0xffffffffu, top);
           const int want = 6 - min(max(int(top >> 23) - 127, -60), 90);
           if (fresh || want < e_f) e_new = want;
@@ -701,8 +790,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float to = fmaxf(m[nt][j], max_over_keys(fmaxf(s[nt][j], s[nt][j + 2])) *
-                                                 to_log2[nt][j]);
+            const float to = fmaxf(m[nt][j], max_over_keys(top_score(nt, j)) * to_log2[nt][j]);
             // (nothing seen yet: sums of zeros, whatever they are scaled by)
             const float by = to == -INFINITY ? 1.f
                              : to == m[nt][j] && e_new == e_f
@@ -720,67 +808,83 @@ window_kernel(const __grid_constant__ WindowParams p) {
         e_f = e_new;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int r = 0; r < kRun; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[nt][j] = fast_exp2(fmaf(s[nt][j], to_log2[nt][j % 2], minus_ref[nt][j % 2]));
-          l[nt][j % 2] += s[nt][j];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[r][nt][j] =
+                fast_exp2(fmaf(s[r][nt][j], to_log2[nt][j % 2], minus_ref[nt][j % 2]));
+            l[nt][j % 2] += s[r][nt][j];
+          }
 
       // Oᵀ += Vᵀ Pᵀ
       if constexpr (k4) {
-        // codes of keys 2t, 2t + 1 (and + 8): bytes (D/16)·g of their rows, the
-        // low halves of a pair of keys in one byte, then the high halves
-        uint32_t lo[2][D / 64], hi[2][D / 64];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t x[D / 64], y[D / 64];
-          if constexpr (D == 128) {
-            const uint2 a = lds64(at + RingT::v_at(2 * t + 8 * j, g / 2) + 8 * (g % 2)),
-                        c = lds64(at + RingT::v_at(2 * t + 1 + 8 * j, g / 2) + 8 * (g % 2));
-            x[0] = a.x; x[1] = a.y; y[0] = c.x; y[1] = c.y;
-          } else {
-            x[0] = lds32(at + RingT::v_at(2 * t + 8 * j, g / 4) + 4 * (g % 4));
-            y[0] = lds32(at + RingT::v_at(2 * t + 1 + 8 * j, g / 4) + 4 * (g % 4));
-          }
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            lo[j][c] = (x[c] & 0x0f0f0f0fu) | ((y[c] << 4) & 0xf0f0f0f0u);
-            hi[j][c] = ((x[c] >> 4) & 0x0f0f0f0fu) | (y[c] & 0xf0f0f0f0u);
-          }
-        }
         auto product = [&](auto pick) {
 #pragma unroll
-          for (int c = 0; c < kGroups; ++c) {
+          for (int r = 0; r < kRun; ++r) {
+            const uint32_t from = at + r * RingT::kPart;
+            // codes of keys 2t, 2t + 1 (and + 8): bytes (D/16)·g of their rows, the
+            // low halves of a pair of keys in one byte, then the high halves
+            uint32_t lo[2][D / 64], hi[2][D / 64];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t x[D / 64], y[D / 64];
+              if constexpr (D == 128) {
+                const uint2 a = lds64(from + RingT::v_at(2 * t + 8 * j, g / 2) + 8 * (g % 2)),
+                            c = lds64(from + RingT::v_at(2 * t + 1 + 8 * j, g / 2) + 8 * (g % 2));
+                x[0] = a.x; x[1] = a.y; y[0] = c.x; y[1] = c.y;
+              } else {
+                x[0] = lds32(from + RingT::v_at(2 * t + 8 * j, g / 4) + 4 * (g % 4));
+                y[0] = lds32(from + RingT::v_at(2 * t + 1 + 8 * j, g / 4) + 4 * (g % 4));
+              }
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                lo[j][c] = (x[c] & 0x0f0f0f0fu) | ((y[c] << 4) & 0xf0f0f0f0u);
+                hi[j][c] = ((x[c] >> 4) & 0x0f0f0f0fu) | (y[c] & 0xf0f0f0f0u);
+              }
+            }
             uint32_t pf[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < kGroups; ++c) {
+              const int o_ = kTwice ? c / 2 : c;  // of the lane's scales
+              if (!(kTwice && c % 2)) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float a = s[nt][2 * j] * vs[j][c], z = s[nt][2 * j + 1] * vs[j][c];
-                if constexpr (decltype(pick)::value) {
-                  if ((hidden[nt][0] >> (g + 8 * j)) & 1u) a = 0.f;
-                  if ((hidden[nt][1] >> (g + 8 * j)) & 1u) z = 0.f;
-                }
-                pf[nt][j] = transpose8x8(pack_f16x2(a, z));
-              }
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a[4];
-              if (c % 2) {
-                a[0] = y ? e2m1x2_to_f16x2<3>(lo[0][c / 2]) : e2m1x2_to_f16x2<2>(lo[0][c / 2]);
-                a[1] = y ? e2m1x2_to_f16x2<3>(hi[0][c / 2]) : e2m1x2_to_f16x2<2>(hi[0][c / 2]);
-                a[2] = y ? e2m1x2_to_f16x2<3>(lo[1][c / 2]) : e2m1x2_to_f16x2<2>(lo[1][c / 2]);
-                a[3] = y ? e2m1x2_to_f16x2<3>(hi[1][c / 2]) : e2m1x2_to_f16x2<2>(hi[1][c / 2]);
-              } else {
-                a[0] = y ? e2m1x2_to_f16x2<1>(lo[0][c / 2]) : e2m1x2_to_f16x2<0>(lo[0][c / 2]);
-                a[1] = y ? e2m1x2_to_f16x2<1>(hi[0][c / 2]) : e2m1x2_to_f16x2<0>(hi[0][c / 2]);
-                a[2] = y ? e2m1x2_to_f16x2<1>(lo[1][c / 2]) : e2m1x2_to_f16x2<0>(lo[1][c / 2]);
-                a[3] = y ? e2m1x2_to_f16x2<1>(hi[1][c / 2]) : e2m1x2_to_f16x2<0>(hi[1][c / 2]);
+                  for (int j = 0; j < 2; ++j) {
+                    float a = s[r][nt][2 * j] * vs[r][j][o_], z = s[r][nt][2 * j + 1] * vs[r][j][o_];
+                    if constexpr (decltype(pick)::value) {
+                      if ((hidden[nt][0] >> (16 * r + g + 8 * j)) & 1u) a = 0.f;
+                      if ((hidden[nt][1] >> (16 * r + g + 8 * j)) & 1u) z = 0.f;
+                    }
+                    pf[nt][j] = transpose8x8(pack_f16x2(a, z));
+                  }
               }
+              uint32_t b[NT][2];                  // (kTwice: of this group's columns)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(o[2 * c + y][nt], a, pf[nt][0], pf[nt][1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  b[nt][j] = !kTwice ? pf[nt][j] : pf[nt][j] & (c % 2 ? ~low_columns : low_columns);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                if (c % 2) {
+                  a[0] = y ? e2m1x2_to_f16x2<3>(lo[0][c / 2]) : e2m1x2_to_f16x2<2>(lo[0][c / 2]);
+                  a[1] = y ? e2m1x2_to_f16x2<3>(hi[0][c / 2]) : e2m1x2_to_f16x2<2>(hi[0][c / 2]);
+                  a[2] = y ? e2m1x2_to_f16x2<3>(lo[1][c / 2]) : e2m1x2_to_f16x2<2>(lo[1][c / 2]);
+                  a[3] = y ? e2m1x2_to_f16x2<3>(hi[1][c / 2]) : e2m1x2_to_f16x2<2>(hi[1][c / 2]);
+                } else {
+                  a[0] = y ? e2m1x2_to_f16x2<1>(lo[0][c / 2]) : e2m1x2_to_f16x2<0>(lo[0][c / 2]);
+                  a[1] = y ? e2m1x2_to_f16x2<1>(hi[0][c / 2]) : e2m1x2_to_f16x2<0>(hi[0][c / 2]);
+                  a[2] = y ? e2m1x2_to_f16x2<1>(lo[1][c / 2]) : e2m1x2_to_f16x2<0>(lo[1][c / 2]);
+                  a[3] = y ? e2m1x2_to_f16x2<1>(hi[1][c / 2]) : e2m1x2_to_f16x2<0>(hi[1][c / 2]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<true>(o[2 * o_ + y][nt], a, b[nt][0], b[nt][1]);
+              }
             }
           }
         };
@@ -795,10 +899,10 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t x = pack_bf16x2(s[nt][2 * j], s[nt][2 * j + 1]);
-            const uint32_t y = pack_bf16x2(s[nt][2 * j] - bf16lo(x), s[nt][2 * j + 1] - bf16hi(x));
+            const float a = s[0][nt][2 * j], z = s[0][nt][2 * j + 1];
+            const uint32_t x = pack_bf16x2(a, z);
             hi[nt][j] = transpose8x8(x);
-            lo[nt][j] = transpose8x8(y);
+            lo[nt][j] = transpose8x8(pack_bf16x2(a - bf16lo(x), z - bf16hi(x)));
           }
         // Keys that a token does not see may hold values that are not finite, which
         // would reach its rows through the product (0 · inf): then the tokens'
@@ -924,7 +1028,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int r = 8 * nt + 2 * t + j;
+          const int r = (8 * nt + 2 * t + j) & kRowMask;
           if (r >= rows) continue;
           const bool empty = l[nt][j] == 0.f;
           const float by = !whole ? 1.f : empty ? 0.f : 1.f / l[nt][j];
@@ -935,9 +1039,10 @@ window_kernel(const __grid_constant__ WindowParams p) {
           float* part = p.o_part + (1LL * slot * kRows + r) * D;
           if constexpr (k4) {
 #pragma unroll
-            for (int c = 0; c < kGroups; ++c) {
-              const float x[4] = {value(2 * c, 0), value(2 * c, 1), value(2 * c + 1, 0),
-                                  value(2 * c + 1, 1)};
+            for (int c_ = 0; c_ < kM / 2; ++c_) {
+              const int c = kTwice ? 2 * c_ + t / 2 : c_;
+              const float x[4] = {value(2 * c_, 0), value(2 * c_, 1), value(2 * c_ + 1, 0),
+                                  value(2 * c_ + 1, 1)};
               if (whole)
                 *reinterpret_cast<uint2*>(out + 32 * c + 4 * g) =
                     make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
@@ -957,7 +1062,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
                   part[e] = value(mt, half);
               }
           }
-          if (g == 0) {
+          if (g == 0 && !(kTwice && t >= 2)) {
             if (!whole) {
               p.m_part[slot * kRows + r] = m[nt][j];
               p.l_part[slot * kRows + r] = l[nt][j];
@@ -978,18 +1083,18 @@ window_kernel(const __grid_constant__ WindowParams p) {
 // kJoinWarps / kPer of the Hkv·R rows of request y. Partial results are fetched
 // eight at a time.
 constexpr int kJoinWarps = 8, kFewRows = 1024;
-template <int D, int kRows, int kPer>
+template <int D, int kRows, int kPer, int kTile>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 window_join_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kLane = D / 32, kBatch = 8;       // elements of a lane
   pdl_wait_primary();
   pdl_launch_dependents();
   const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const PlaceSums<32 * kJoinWarps> sums(p, b);
+  const PlaceSums<32 * kJoinWarps, kTile> sums(p, b);
   const int row = blockIdx.x * (kJoinWarps / kPer) + warp / kPer;
   if (row >= p.Hkv * p.R) return;
   const int h = row / p.R, r = row % p.R;
-  const Tiles tl = tiles_of(p, p.lens[b]);
+  const Tiles tl = tiles_of<kTile>(p, p.lens[b]);
   const long long q_row = 1LL * b * p.Hkv * p.R + row;
   float acc[kLane] = {}, sum = 0.f, top = -INFINITY;
   if (tl.units > 0) {
@@ -1081,10 +1186,11 @@ cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int sme
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-template <int D, bool k4, int NT, bool kRuns>
+template <int D, bool k4, int NT, bool kRuns, bool kTwice = false>
 cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
-  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns>);
-  constexpr int smem = smem_bytes<D, k4, NT>();
+  constexpr int kTile = kKeys * kRunsOf<k4, NT>;
+  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
+  constexpr int smem = smem_bytes<D, k4, NT, kTwice>();
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   p.blocks = (p.R + 8 * NT - 1) / (8 * NT);
@@ -1094,22 +1200,25 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
     tiles = std::min(tiles, (1LL * p.left + p.T + kTile - 1) / kTile + 1 +
                                 (1LL * p.n_global + kTile - 1) / kTile);
   const long long most = 1LL * p.B * p.Hkv * p.blocks * ((tiles + kWarps - 1) / kWarps);
-  p.grid = int(std::min<long long>(most, 1LL * a.sm_count * kResident<NT, k4>));
+  p.grid = int(std::min<long long>(most, 1LL * a.sm_count * kResident<NT, k4, kTwice>));
   e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, p, a.stream);
   if (e != cudaSuccess) return e;
   // Few rows have many partial results each, over which a block's warps share.
   const int rows = p.Hkv * p.R;
   if (1LL * p.B * rows <= kFewRows)
     return launch_dependent(
-        reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, kJoinWarps>),
+        reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, kJoinWarps, kTile>),
         dim3(unsigned(rows), unsigned(p.B)), 32 * kJoinWarps, 0, p, a.stream);
-  return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, 1>),
+  return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, 1, kTile>),
                           dim3(unsigned((rows + kJoinWarps - 1) / kJoinWarps), unsigned(p.B)),
                           32 * kJoinWarps, 0, p, a.stream);
 }
 
 template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams& p) {
-  if (p.page_size % kTile == 0)
+  if (k4 && p.R <= 4)
+    return p.page_size % kKeys == 0 ? launch_t<D, k4, 1, true, k4>(a, p)
+                                    : launch_t<D, k4, 1, false, k4>(a, p);
+  if (p.page_size % kKeys == 0)
     return p.R <= 8 ? launch_t<D, k4, 1, true>(a, p) : launch_t<D, k4, 2, true>(a, p);
   return p.R <= 8 ? launch_t<D, k4, 1, false>(a, p) : launch_t<D, k4, 2, false>(a, p);
 }
@@ -1118,7 +1227,7 @@ template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams
 
 int window_partial_rows(int R, int sm_count) {
   // two partial results of 8 or 16 rows per CTA
-  return R <= 8 ? sm_count * kResident<1, true> * 2 * 8 : sm_count * kResident<2, true> * 2 * 16;
+  return R <= 8 ? sm_count * kResident<1, true, true> * 2 * 8 : sm_count * kResident<2, true, false> * 2 * 16;
 }
 
 cudaError_t launch_decode_window(const WindowArgs& a) {
