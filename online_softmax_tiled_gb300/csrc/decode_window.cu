@@ -32,15 +32,22 @@
 // four make a unit, are laid end to end and cut into equal shares, one per CTA
 // (lengths are read on the device). A CTA whose share begins or ends inside a
 // (request, head) leaves a partial result there, two at most; a dependent launch
-// joins them. Each warp copies its own tiles into a ring of its own, kStages - 1
+// joins them. Calls of so few and short items that the CTAs of one cluster cover
+// each one run as clusters instead, which join through distributed shared memory:
+// one launch, and no sums over the lengths before it starts. Each warp copies its own tiles into a ring of its own, kStages - 1
 // ahead, with no barrier of the CTA until the end of a run.
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
 #include "fp4.cuh"
 #include "launchers.h"
+
+namespace cg = cooperative_groups;
 
 namespace attn {
 
@@ -65,6 +72,7 @@ struct WindowParams {
   int num_pages, page_size, max_pages, cap, left, n_global;
   uint32_t page_mul;                        // key / page_size = umulhi(2 key, mul) >> shift
   int page_shift, grid;
+  int cluster;                              // CTAs of an item, 0: shares of all items
   float scale_log2;
 };
 
@@ -97,13 +105,15 @@ ATTN_DEVINL int places_of(int units) { return units > 0 ? units + kItemCost : 0;
 
 // Sums over the requests of an item's places: of all, and of those before request
 // `upto` (all threads of the block get both).
-template <int kN, int kTile> struct PlaceSums {
+// kEarly: lengths may only come from L2.
+template <int kN, int kTile, bool kEarly> struct PlaceSums {
   int total, before;
   ATTN_DEVINL PlaceSums(const WindowParams& p, int upto) {
     __shared__ int part[2][kN / 32];
     int a = 0, b = 0;
     for (int r = threadIdx.x; r < p.B; r += kN) {
-      const int u = places_of(tiles_of<kTile>(p, p.lens[r]).units);
+      const int n = kEarly ? __ldcg(p.lens + r) : p.lens[r];
+      const int u = places_of(tiles_of<kTile>(p, n).units);
       a += u;
       if (r < upto) b += u;
     }
@@ -132,42 +142,82 @@ ATTN_DEVINL int share_of(int place, int ctas, int places) {
   return int(((long long)(place + 1) * ctas - 1) / places);
 }
 
-// Where a share begins, as units: the request of its first unit, the units of all
-// requests before that one, and the units before the share. Worked out by a warp.
-struct Place {
-  int b, before, unit;
+// A share as units: its first and the one past its last, the request of the first,
+// and the units of all requests before that one.
+struct Share {
+  int begin, end, b, before;
 };
-template <int kTile>
-ATTN_DEVINL Place find_place(const WindowParams& p, int place, int lane) {
+// The share of this CTA, worked out by its threads: each adds up a run of
+// requests, the block's running sums find the threads whose requests hold the
+// share's ends. Places are counted as units are.
+template <int kTile> ATTN_DEVINL Share find_share(const WindowParams& p, int cta) {
+  __shared__ int sums[2][kWarps];
+  __shared__ Share share;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int per_request = p.Hkv * p.blocks;
-  int places = 0, units = 0;                      // of the requests so far
-  for (int r0 = 0; r0 < p.B; r0 += 32) {
-    const int u = r0 + lane < p.B ? tiles_of<kTile>(p, p.lens[r0 + lane]).units : 0;
-    int incl = places_of(u) * per_request, incl_u = u * per_request;
-    const int own = incl, own_u = incl_u;
-#pragma unroll
-    for (int off = 1; off < 32; off *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, off),
-                y = __shfl_up_sync(0xffffffffu, incl_u, off);
-      if (lane >= off) {
-        incl += x;
-        incl_u += y;
-      }
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, places + incl > place);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      const int rest = place - places - __shfl_sync(0xffffffffu, incl - own, at);
-      const int per = __shfl_sync(0xffffffffu, u, at);
-      units += __shfl_sync(0xffffffffu, incl_u - own_u, at);
-      const int item = rest / places_of(per);
-      const int in = max(0, rest - item * places_of(per) - kItemCost);
-      return {r0 + at, units, units + item * per + in};
-    }
-    places += __shfl_sync(0xffffffffu, incl, 31);
-    units += __shfl_sync(0xffffffffu, incl_u, 31);
+  const int per = (p.B + kThreads - 1) / kThreads, r0 = min(p.B, tid * per),
+            r1 = min(p.B, r0 + per);
+  int places = 0, units = 0;                      // of the thread's requests
+  for (int r = r0; r < r1; ++r) {
+    const int n = p.lens[r], u = tiles_of<kTile>(p, n).units;
+    if (cta == 0 && unsigned(n) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
+    places += places_of(u);
+    units += u;
   }
-  return {p.B, units, units};                     // the end of all
+  places *= per_request;
+  units *= per_request;
+  int at = places, at_u = units;                  // running sums, the thread's included
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, at, off), y = __shfl_up_sync(0xffffffffu, at_u, off);
+    if (lane >= off) {
+      at += x;
+      at_u += y;
+    }
+  }
+  if (lane == 31) {
+    sums[0][warp] = at;
+    sums[1][warp] = at_u;
+  }
+  __syncthreads();
+  int all = 0, all_u = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      at += sums[0][w];
+      at_u += sums[1][w];
+    }
+    all += sums[0][w];
+    all_u += sums[1][w];
+  }
+  const int ctas = min(p.grid, all);
+  if (cta >= ctas) return {0, 0, 0, 0};
+#pragma unroll
+  for (int end = 0; end < 2; ++end) {
+    const int place = share_start(cta + end, ctas, all);
+    if (end == 1 && place == all && tid == 0) share.end = all_u;
+    if (place < at - places || place >= at) continue;
+    int from = at - places, from_u = at_u - units, r = r0, u;
+    while (true) {
+      u = tiles_of<kTile>(p, p.lens[r]).units;
+      if (place < from + places_of(u) * per_request) break;
+      from += places_of(u) * per_request;
+      from_u += u * per_request;
+      ++r;
+    }
+    const int item = (place - from) / places_of(u);
+    const int unit =
+        from_u + item * u + max(0, place - from - item * places_of(u) - kItemCost);
+    if (end == 1) {
+      share.end = unit;
+    } else {
+      share.begin = unit;
+      share.b = r;
+      share.before = from_u;
+    }
+  }
+  __syncthreads();
+  return share;
 }
 
 // ------------------------------------------------------------ instructions
@@ -287,14 +337,16 @@ template <int D, bool k4, int kRun> struct Ring {
 // CTAs per SM the registers are cut for.
 template <int NT, bool k4, bool kTwice> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
 
-// Warps whose sums are handed to warp 0 at a time, each as [kM·NT][32 lanes] of
-// four floats.
-template <int NT, bool k4> constexpr int kHanded = k4 && NT == 1 ? 3 : 1;
+// Blocks of 16 elements whose sums the warps hand one another at a time, each as
+// [32 lanes] of four floats a warp and block of 8 rows: all of them, or as many as
+// leave shared memory for two CTAs an SM.
+template <int D, bool k4, int NT, bool kTwice>
+constexpr int kAtOnce = k4 ? (kTwice ? D / 32 : D / 16) : 4 / NT;
 
 template <int D, bool k4, int NT, bool kTwice>
 constexpr int smem_bytes() {
-  return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes + kHanded<NT, k4> * (kTwice ? D / 32 : D / 16) * NT * 512 +
-         kWarps * 8 * NT * 8;
+  return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes +
+         kAtOnce<D, k4, NT, kTwice> * NT * kWarps * 512 + kWarps * 8 * NT * 8;
 }
 
 // What a tile is: nothing to compute, all keys seen by all tokens, or neither;
@@ -320,31 +372,34 @@ window_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kOwn = kTwice ? kGroups / 2 : kGroups;
   constexpr int kRowMask = kTwice ? 3 : 15;       // of a column's query row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Place share[2];
-  pdl_launch_dependents();
   // (uniform, and known to be)
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const uint32_t ring = smem_u32(smem) + warp * RingT::kBytes;
   float4* handed = reinterpret_cast<float4*>(smem + kWarps * RingT::kBytes);
-  float2* handed_ml = reinterpret_cast<float2*>(handed + kHanded<NT, k4> * kM * NT * 32);
+  constexpr int kHand = kAtOnce<D, k4, NT, kTwice>;
+  float2* handed_ml = reinterpret_cast<float2*>(handed + kHand * NT * kWarps * 32);
 
   pdl_wait_primary();
-  // this CTA's share, and the request it begins in
+  // (only now: the join reads lengths before it waits for this grid)
+  pdl_launch_dependents();
   const int per_request = p.Hkv * p.blocks;
-  const int places = PlaceSums<kThreads, kTile>(p, 0).total * per_request;
-  if (blockIdx.x == 0)
-    for (int r = threadIdx.x; r < p.B; r += kThreads)
-      if (unsigned(p.lens[r]) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
-  const int ctas = min(p.grid, places);
-  if (int(blockIdx.x) >= ctas) return;
-  if (warp < 2) {
-    const Place at = find_place<kTile>(p, share_start(blockIdx.x + warp, ctas, places), lane);
-    if (lane == 0) share[warp] = at;
+  int b = 0, before = 0, u_begin, u_end;
+  if (p.cluster > 0) {
+    const int item = int(blockIdx.x) / p.cluster, rank = int(blockIdx.x) % p.cluster;
+    b = item / per_request;
+    if (unsigned(p.lens[b]) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
+    const int units = tiles_of<kTile>(p, p.lens[b]).units, first = item % per_request * units;
+    u_begin = first + share_start(rank, p.cluster, units);
+    u_end = first + share_start(rank + 1, p.cluster, units);
+  } else {
+    const Share share = find_share<kTile>(p, int(blockIdx.x));
+    if (share.begin == share.end) return;
+    b = share.b;
+    before = share.before;
+    u_begin = share.begin;
+    u_end = share.end;
   }
-  __syncthreads();
-  int b = share[0].b, before = share[0].before;
-  const int u_begin = share[0].unit, u_end = share[1].unit;
 
   // The warp's tile k is its quarter of unit u_begin + k. Tiles 32 i .. 32 i + 31
   // are worked out at once, one per lane, while those before them are computed:
@@ -444,7 +499,6 @@ window_kernel(const __grid_constant__ WindowParams p) {
             now.row[r] = (uint32_t(ok ? ahead_page[r] : 0) * uint32_t(p.Hkv) + uint32_t(now.h)) *
                              uint32_t(p.page_size) + uint32_t(ahead_slot[r]);
           }
-          look_ahead(k + 32);
         }
         what = __shfl_sync(0xffffffffu, now.what, k % 32);
         if (what != kNone) {
@@ -468,6 +522,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
               copy_async<RingT::kScales>(s_dst + to, s_src + size_t(row) * RingT::kScales);
           }
         }
+        if (k % 32 == 0) look_ahead(k + 32);      // (behind the copies: it takes a while)
       } else {
         what = __shfl_sync(0xffffffffu, now.what, k % 32);
         if (what != kNone) {
@@ -510,26 +565,26 @@ window_kernel(const __grid_constant__ WindowParams p) {
     }
     copies_commit();
   };
-  look_ahead(0);
-  look_up(0);
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    issue(s, s * RingT::kStage);
-    look_up(s + 1);
-  }
-
   int k = 0;
   uint32_t stage = 0;                             // of tile k
-  for (int u = u_begin; u < u_end;) {
+  bool once = p.cluster > 0;                      // a cluster's CTA takes one run, if empty
+  for (int u = u_begin; u < u_end || once;) {
     Tiles tl = tiles_of<kTile>(p, p.lens[b]);
-    while (u >= before + tl.units * per_request) {
-      before += tl.units * per_request;
-      tl = tiles_of<kTile>(p, p.lens[++b]);
+    int item;
+    if (once) {
+      item = int(blockIdx.x) / p.cluster % per_request;
+      once = false;
+    } else {
+      while (u >= before + tl.units * per_request) {
+        before += tl.units * per_request;
+        tl = tiles_of<kTile>(p, p.lens[++b]);
+      }
+      item = (u - before) / tl.units;
     }
-    const int item = (u - before) / tl.units, local = (u - before) % tl.units;
+    const int local = u - before - item * tl.units;
     const int h = item / p.blocks, r0 = item % p.blocks * kRows;
     const int run = min(tl.units - local, u_end - u);
-    const bool whole = run == tl.units;
+    const bool whole = p.cluster > 0 || run == tl.units;
     const int rows = min(kRows, p.R - r0);
     const long long q_row0 = (1LL * b * p.Hkv + h) * p.R + r0;
 
@@ -537,45 +592,62 @@ window_kernel(const __grid_constant__ WindowParams p) {
     // 4 bits: k-step 2c + s is the elements 32c + 8t + 4s .. + 3; scaled by a power
     // of two that puts the row's largest value into [2^8, 2^9).
     uint32_t qf[kQ][NT][2];
-    float to_log2[NT][2];                         // scores times this, per column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = (8 * nt + g) & kRowMask;
-      const bool live = row < rows;
       const __nv_bfloat16* src = p.q + (q_row0 + row) * D;
       if constexpr (k4) {
-        uint4 raw[kGroups];
-        uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < kGroups; ++c) {
-          raw[c] = live ? *reinterpret_cast<const uint4*>(src + 32 * c + 8 * t)
-                        : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (row < rows) w = *reinterpret_cast<const uint4*>(src + 32 * c + 8 * t);
+          qf[2 * c][nt][0] = w.x; qf[2 * c][nt][1] = w.y;
+          qf[2 * c + 1][nt][0] = w.z; qf[2 * c + 1][nt][1] = w.w;
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(int(top >> 7) - 127, -100);
-        const float up = pow2i(8 - e);
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c) {
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            qf[2 * c + j / 2][nt][j % 2] =
-                kTwice && c % 2 != g / 4 ? 0u : pack_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
-        }
-        const float down = fmaxf(p.scale_log2 * pow2i(e - 8), 1.17549435e-38f);
-        to_log2[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-        to_log2[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
       } else {
 #pragma unroll
         for (int j = 0; j < kQ; ++j)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            qf[j][nt][s] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * j + 8 * s + 2 * t)
-                                : 0u;
+            qf[j][nt][s] = row < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * j + 8 * s + 2 * t)
+                                      : 0u;
+      }
+    }
+    if (u == u_begin) {                           // the ring begins
+      look_ahead(0);
+      look_up(0);
+#pragma unroll 1
+      for (int s = 0; s < kStages - 1; ++s) {
+        issue(s, s * RingT::kStage);
+        look_up(s + 1);
+      }
+    }
+    float to_log2[NT][2];                         // scores times this, per column
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if constexpr (k4) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kQ; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            top = max(top, max(qf[j][nt][s] & 0x7fffu, (qf[j][nt][s] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(int(top >> 7) - 127, -100);
+        const float up = pow2i(8 - e);
+#pragma unroll
+        for (int j = 0; j < kQ; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t w = qf[j][nt][s];
+            qf[j][nt][s] =
+                kTwice && j / 2 % 2 != g / 4 ? 0u : pack_f16x2(bf16lo(w) * up, bf16hi(w) * up);
+          }
+        const float down = fmaxf(p.scale_log2 * pow2i(e - 8), 1.17549435e-38f);
+        to_log2[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        to_log2[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      } else {
         to_log2[nt][0] = to_log2[nt][1] = p.scale_log2;
       }
     }
@@ -972,7 +1044,8 @@ window_kernel(const __grid_constant__ WindowParams p) {
       }
     }
 
-    // Join the warps into warp 0's sums. From here on m is the reference of the sums.
+    // Join the warps' sums, each warp some of the blocks of elements. From here on
+    // m is the reference of the sums.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -982,98 +1055,147 @@ window_kernel(const __grid_constant__ WindowParams p) {
         if (g == 0)
           handed_ml[warp * kRows + 8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
       }
-    for (int w0 = 1; w0 < kWarps; w0 += kHanded<NT, k4>) {
-      if (warp >= w0 && warp < w0 + kHanded<NT, k4>) {
-        float4* to = handed + (warp - w0) * kM * NT * 32 + lane;
+    constexpr int kMine = (kM * NT + kWarps - 1) / kWarps;   // blocks of a warp, at most
+    auto mine = [&](int x) { return kM * NT % kWarps == 0 || x * kWarps + warp < kM * NT; };
+    float4 sum[kMine];
+    // Of `parts` results with (m, l) at ml[part · kRows + row]: what each is
+    // scaled by, and the joined m and l.
+    auto weigh = [&](auto ml_of, int parts, int nt, int j, float (&w)[8]) {
+      float top = -INFINITY, all = 0.f;
+      const int row = 8 * nt + 2 * t + j;
 #pragma unroll
-        for (int mt = 0; mt < kM; ++mt)
+      for (int x = 0; x < 8; ++x)
+        if (x < parts) top = fmaxf(top, ml_of(x)[row].x);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            to[(mt * NT + nt) * 32] =
-                make_float4(o[mt][nt][0], o[mt][nt][1], o[mt][nt][2], o[mt][nt][3]);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        for (int w = w0; w < min(kWarps, w0 + kHanded<NT, k4>); ++w) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float mine[2], theirs[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 ml = handed_ml[w * kRows + 8 * nt + 2 * t + j];
-              const float to = fmaxf(m[nt][j], ml.x);
-              // (a NaN among the scores is in the sums, not in the references)
-              mine[j] = m[nt][j] == -INFINITY ? 1.f : fast_exp2(m[nt][j] - to);
-              theirs[j] = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - to);
-              m[nt][j] = to;
-              l[nt][j] = l[nt][j] * mine[j] + ml.y * theirs[j];
-            }
-            const float4* from = handed + (w - w0) * kM * NT * 32 + lane;
-#pragma unroll
-            for (int mt = 0; mt < kM; ++mt) {
-              const float4 x = from[(mt * NT + nt) * 32];
-              o[mt][nt][0] = o[mt][nt][0] * mine[0] + x.x * theirs[0];
-              o[mt][nt][1] = o[mt][nt][1] * mine[1] + x.y * theirs[1];
-              o[mt][nt][2] = o[mt][nt][2] * mine[0] + x.z * theirs[0];
-              o[mt][nt][3] = o[mt][nt][3] * mine[1] + x.w * theirs[1];
-            }
-          }
+      for (int x = 0; x < 8; ++x)
+        if (x < parts) {
+          const float2 ml = ml_of(x)[row];
+          // (a NaN among the scores is in the sums, not in the references)
+          w[x] = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - top);
+          all += w[x] * ml.y;
         }
+      m[nt][j] = top;
+      l[nt][j] = all;
+    };
+    auto add = [](float4& to, const float4& x, float w0, float w1) {
+      to.x += x.x * w0; to.y += x.y * w1; to.z += x.z * w0; to.w += x.w * w1;
+    };
+    float w[NT][2][8];
+#pragma unroll
+    for (int m0 = 0; m0 < kM; m0 += kHand) {
+#pragma unroll
+      for (int mt = 0; mt < kHand; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          handed[((mt * NT + nt) * kWarps + warp) * 32 + lane] = make_float4(
+              o[m0 + mt][nt][0], o[m0 + mt][nt][1], o[m0 + mt][nt][2], o[m0 + mt][nt][3]);
+      __syncthreads();
+      if (m0 == 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            weigh([&](int x) { return handed_ml + x * kRows; }, kWarps, nt, j, w[nt][j]);
+#pragma unroll
+      for (int x = 0; x < (kHand * NT + kWarps - 1) / kWarps; ++x) {
+        if (!mine(x)) continue;
+        const int at = x * kWarps + warp, nt = NT == 1 ? 0 : warp % NT;
+        float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y)
+          add(to, handed[(at * kWarps + y) * 32 + lane],
+              NT == 1 || nt == 0 ? w[0][0][y] : w[NT - 1][0][y],
+              NT == 1 || nt == 0 ? w[0][1][y] : w[NT - 1][1][y]);
+        sum[m0 * NT / kWarps + x] = to;
       }
       __syncthreads();
     }
-    if (warp == 0) {
-      const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    if (p.cluster > 1) {
+      // join the CTAs, into the first one's sums
+      cg::cluster_group cluster = cg::this_cluster();
+      const bool first = cluster.block_rank() == 0;
+#pragma unroll
+      for (int x = 0; x < kMine; ++x)
+        if (mine(x)) handed[(x * kWarps + warp) * 32 + lane] = sum[x];
+      if (warp == 0 && g == 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            handed_ml[8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
+      cluster.sync();
+      if (first) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            weigh([&](int x) { return cluster.map_shared_rank(handed_ml, x); }, p.cluster, nt, j,
+                  w[nt][j]);
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+          if (!mine(x)) continue;
+          const int nt = NT == 1 ? 0 : warp % NT;
+          float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < p.cluster)
+              add(to, cluster.map_shared_rank(handed, c)[(x * kWarps + warp) * 32 + lane],
+                  NT == 1 || nt == 0 ? w[0][0][c] : w[NT - 1][0][c],
+                  NT == 1 || nt == 0 ? w[0][1][c] : w[NT - 1][1][c]);
+          sum[x] = to;
+        }
+      }
+      cluster.sync();                             // (what is read from has to stay)
+      if (!first) return;
+    }
+    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int nt = NT == 1 ? 0 : warp % NT, r = (8 * nt + 2 * t + j) & kRowMask;
+      const float lr = NT == 1 || nt == 0 ? l[0][j] : l[NT - 1][j];
+      const float by = !whole ? 1.f : lr == 0.f ? 0.f : 1.f / lr;
+      if (r >= rows) continue;
+      __nv_bfloat16* out = p.o + (q_row0 + r) * D;
+      float* part = p.o_part + (1LL * slot * kRows + r) * D;
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        if (!mine(x)) continue;
+        const int mt = (x * kWarps + warp) / NT;
+        const float a = (j ? sum[x].y : sum[x].x) * by, z = (j ? sum[x].w : sum[x].z) * by;
+        if constexpr (k4) {
+          const int e = 32 * (kTwice ? 2 * (mt / 2) + t / 2 : mt / 2) + 4 * g + 2 * (mt % 2);
+          if (whole)
+            *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(a, z);
+          else
+            *reinterpret_cast<float2*>(part + e) = make_float2(a, z);
+        } else {
+          const int e = 16 * mt + g;
+          if (whole) {
+            out[e] = __float2bfloat16_rn(a);
+            out[e + 8] = __float2bfloat16_rn(z);
+          } else {
+            part[e] = a;
+            part[e + 8] = z;
+          }
+        }
+      }
+    }
+    if (warp == 0 && g == 0 && !(kTwice && t >= 2))
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int r = (8 * nt + 2 * t + j) & kRowMask;
           if (r >= rows) continue;
-          const bool empty = l[nt][j] == 0.f;
-          const float by = !whole ? 1.f : empty ? 0.f : 1.f / l[nt][j];
-          auto value = [&](int mt, int half) {
-            return whole && empty ? 0.f : o[mt][nt][j + 2 * half] * by;
-          };
-          __nv_bfloat16* out = p.o + (q_row0 + r) * D;
-          float* part = p.o_part + (1LL * slot * kRows + r) * D;
-          if constexpr (k4) {
-#pragma unroll
-            for (int c_ = 0; c_ < kM / 2; ++c_) {
-              const int c = kTwice ? 2 * c_ + t / 2 : c_;
-              const float x[4] = {value(2 * c_, 0), value(2 * c_, 1), value(2 * c_ + 1, 0),
-                                  value(2 * c_ + 1, 1)};
-              if (whole)
-                *reinterpret_cast<uint2*>(out + 32 * c + 4 * g) =
-                    make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-              else
-                *reinterpret_cast<float4*>(part + 32 * c + 4 * g) =
-                    make_float4(x[0], x[1], x[2], x[3]);
-            }
-          } else {
-#pragma unroll
-            for (int mt = 0; mt < kM; ++mt)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int e = 16 * mt + 8 * half + g;
-                if (whole)
-                  out[e] = __float2bfloat16_rn(value(mt, half));
-                else
-                  part[e] = value(mt, half);
-              }
-          }
-          if (g == 0 && !(kTwice && t >= 2)) {
-            if (!whole) {
-              p.m_part[slot * kRows + r] = m[nt][j];
-              p.l_part[slot * kRows + r] = l[nt][j];
-            } else if (p.lse != nullptr) {
-              p.lse[q_row0 + r] = empty ? -INFINITY
-                                        : fmaf(m[nt][j] == -INFINITY ? 0.f : m[nt][j],
-                                               0.693147180559945f, logf(l[nt][j]));
-            }
+          if (!whole) {
+            p.m_part[slot * kRows + r] = m[nt][j];
+            p.l_part[slot * kRows + r] = l[nt][j];
+          } else if (p.lse != nullptr) {
+            p.lse[q_row0 + r] = l[nt][j] == 0.f ? -INFINITY
+                                                : fmaf(m[nt][j] == -INFINITY ? 0.f : m[nt][j],
+                                                       0.693147180559945f, logf(l[nt][j]));
           }
         }
-    }
     u += run;
   }
 }
@@ -1082,19 +1204,18 @@ window_kernel(const __grid_constant__ WindowParams p) {
 // writes those of requests without keys. kPer warps a row; grid: x over groups of
 // kJoinWarps / kPer of the Hkv·R rows of request y. Partial results are fetched
 // eight at a time.
-constexpr int kJoinWarps = 8, kFewRows = 1024;
+constexpr int kJoinWarps = 8, kFewRows = 1024, kClusterUnits = 2;
 template <int D, int kRows, int kPer, int kTile>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 window_join_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kLane = D / 32, kBatch = 8;       // elements of a lane
-  pdl_wait_primary();
-  pdl_launch_dependents();
+  // The lengths are read before the wait: this grid starts when every CTA of the
+  // one before it has waited for what precedes the call.
   const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const PlaceSums<32 * kJoinWarps, kTile> sums(p, b);
+  const PlaceSums<32 * kJoinWarps, kTile, true> sums(p, b);
   const int row = blockIdx.x * (kJoinWarps / kPer) + warp / kPer;
-  if (row >= p.Hkv * p.R) return;
   const int h = row / p.R, r = row % p.R;
-  const Tiles tl = tiles_of<kTile>(p, p.lens[b]);
+  const Tiles tl = tiles_of<kTile>(p, __ldcg(p.lens + b));
   const long long q_row = 1LL * b * p.Hkv * p.R + row;
   float acc[kLane] = {}, sum = 0.f, top = -INFINITY;
   if (tl.units > 0) {
@@ -1104,12 +1225,14 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
                      (h * p.blocks + r / kRows) * places_of(tl.units);
     const int u0 = item + kItemCost, u1 = u0 + tl.units - 1;
     const int c0 = share_of(u0, ctas, places), c1 = share_of(u1, ctas, places);
-    if (c0 == c1) return;                         // its CTA has written it
     // (a share that begins before the item holds a unit of another one first)
     const bool at_start = share_start(c0, ctas, places) >= item;
     auto slot_of = [&](int c) {
       return (2 * c + (c == c0 && !at_start ? 1 : 0)) * kRows + r % kRows;
     };
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (row >= p.Hkv * p.R || c0 == c1) return;   // (one CTA alone has written its rows)
     for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.m_part[slot_of(c)]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -1144,6 +1267,10 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
         for (int j = 0; j < kLane; ++j) acc[j] = fmaf(by[i], x[i][j], acc[j]);
       }
     }
+  } else {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (row >= p.Hkv * p.R) return;
   }
   if constexpr (kPer > 1) {
     __shared__ float others[kJoinWarps][D + 1];
@@ -1170,48 +1297,78 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
         empty ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, 0.693147180559945f, logf(sum));
 }
 
-cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem,
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem, int cluster,
                              const WindowParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
   void* args[] = {const_cast<WindowParams*>(&p)};
   return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+// A kernel's shared memory is asked for once per device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <int D, bool k4, int NT, bool kRuns, bool kTwice = false>
 cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   constexpr int kTile = kKeys * kRunsOf<k4, NT>;
-  const void* kernel = reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
   constexpr int smem = smem_bytes<D, k4, NT, kTwice>();
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const void* kernel =
+      reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return e;
   p.blocks = (p.R + 8 * NT - 1) / (8 * NT);
-  // most units that there can be, by the table and the window
+  // most units that an item can have, by the table and the window
   long long tiles = (p.cap + kTile - 1) / kTile;
   if (p.left >= 0)
     tiles = std::min(tiles, (1LL * p.left + p.T + kTile - 1) / kTile + 1 +
                                 (1LL * p.n_global + kTile - 1) / kTile);
-  const long long most = 1LL * p.B * p.Hkv * p.blocks * ((tiles + kWarps - 1) / kWarps);
-  p.grid = int(std::min<long long>(most, 1LL * a.sm_count * kResident<NT, k4, kTwice>));
-  e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, p, a.stream);
+  const long long units = (tiles + kWarps - 1) / kWarps, items = 1LL * p.B * p.Hkv * p.blocks;
+  const long long slots = 1LL * a.sm_count * kResident<NT, k4, kTwice>;
+  // Clusters, where all of them run at once and a CTA has two units at most.
+  int cluster = 1;
+  while (cluster < 8 && cluster < units) cluster *= 2;
+  if (units <= kClusterUnits * cluster && items * cluster <= slots) {
+    p.cluster = cluster;
+    p.grid = int(items) * cluster;
+    return launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, cluster, p, a.stream);
+  }
+  p.grid = int(std::min(items * (units + kItemCost), slots));
+  e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, 1, p, a.stream);
   if (e != cudaSuccess) return e;
   // Few rows have many partial results each, over which a block's warps share.
   const int rows = p.Hkv * p.R;
   if (1LL * p.B * rows <= kFewRows)
     return launch_dependent(
         reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, kJoinWarps, kTile>),
-        dim3(unsigned(rows), unsigned(p.B)), 32 * kJoinWarps, 0, p, a.stream);
+        dim3(unsigned(rows), unsigned(p.B)), 32 * kJoinWarps, 0, 1, p, a.stream);
   return launch_dependent(reinterpret_cast<const void*>(window_join_kernel<D, 8 * NT, 1, kTile>),
                           dim3(unsigned((rows + kJoinWarps - 1) / kJoinWarps), unsigned(p.B)),
-                          32 * kJoinWarps, 0, p, a.stream);
+                          32 * kJoinWarps, 0, 1, p, a.stream);
 }
 
 template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams& p) {
@@ -1227,7 +1384,8 @@ template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams
 
 int window_partial_rows(int R, int sm_count) {
   // two partial results of 8 or 16 rows per CTA
-  return R <= 8 ? sm_count * kResident<1, true, true> * 2 * 8 : sm_count * kResident<2, true, false> * 2 * 16;
+  return R <= 8 ? sm_count * kResident<1, true, true> * 2 * 8
+                : sm_count * kResident<2, true, false> * 2 * 16;
 }
 
 cudaError_t launch_decode_window(const WindowArgs& a) {
