@@ -13,13 +13,15 @@
 // gets the scale NaN.
 //
 // Work. Memory bound: a token's rows are read once and written once. A thread
-// owns 8 adjacent elements of a row (16 bytes of bf16), D/8 lanes a row, through
-// a run of heads of its token: query heads, then key heads, then value heads.
-// It loads its piece and, where pairs lie rot_dim/2 apart, the piece of the
-// partners too: twice the loads of a thread that owns whole pairs (from L1, the
-// same bytes from memory), and the four lanes of a 4-bit group are neighbours
-// whatever the layout of the pairs. The rows of a warp are whole, so rows turned
-// in place are read by all their lanes before any is written (__syncwarp).
+// owns two pieces of 8 adjacent elements (16 bytes of bf16) that hold whole pairs,
+// D/16 lanes a row, through a run of heads of its token: query heads, then key
+// heads, then value heads. The block's warps take different heads of the same
+// tokens, whose angles they work out together. The pieces of a 4-bit group lie
+// with neighbouring lanes; what does not fit that (rows or pairs off multiples of
+// 16 bytes, pairs across halves of groups) goes element by element.
+
+#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -32,31 +34,21 @@ ATTN_DEFINE_ERROR_WORD(take_error_cache_append)
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 
-// 8 adjacent elements as they are in memory.
-template <typename T> struct alignas(16) Piece {
-  T x[8];
+// V adjacent elements as they are in memory, 16 bytes or 32.
+template <typename T, int V> struct alignas(16) Piece {
+  T x[V];
 };
-template <typename T, bool kWide> ATTN_DEVINL void load_piece(Piece<T>& p, const T* src) {
-  if constexpr (kWide) {
+template <typename T, int V> ATTN_DEVINL void load_piece(Piece<T, V>& p, const T* src) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(p) / 16); ++i)
-      reinterpret_cast<uint4*>(&p)[i] = reinterpret_cast<const uint4*>(src)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p.x[i] = src[i];
-  }
+  for (int i = 0; i < int(sizeof(p) / 16); ++i)
+    reinterpret_cast<uint4*>(&p)[i] = reinterpret_cast<const uint4*>(src)[i];
 }
-template <typename T, bool kWide> ATTN_DEVINL void store_piece(T* dst, const Piece<T>& p) {
-  if constexpr (kWide) {
+template <typename T, int V> ATTN_DEVINL void store_piece(T* dst, const Piece<T, V>& p) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(p) / 16); ++i)
-      reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(&p)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dst[i] = p.x[i];
-  }
+  for (int i = 0; i < int(sizeof(p) / 16); ++i)
+    reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(&p)[i];
 }
 
 template <typename T> struct AppendParams {
@@ -69,166 +61,383 @@ template <typename T> struct AppendParams {
   long long pos_stride;
   const double* inv_freq;
   int tokens, N, Hq, Hkv, num_pages, page_size, max_pages, rot, hpt;
+  unsigned blocks, groups;                  // of tokens, of heads
   float magnitude;
 };
 
-// Codes and scale of the 8 elements y of a lane, whose group's other 24 are
-// those of the lanes around it (l ^ 1, l ^ 2, l ^ 3), into a row's D/2 code bytes
-// and D/32 scales. All lanes of the warp call it; those of rows that are not
-// `live` write nothing.
-template <int D>
-ATTN_DEVINL void store_row4(const float (&y)[8], uint8_t* codes, __nv_bfloat16* scales, int l,
-                            bool live) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // (as integers, infinities and NaN are above every finite value)
-  const bool finite = top < 0x7f800000u;
-  const __nv_bfloat16 s = __float2bfloat16_rn(
-      finite ? __fdiv_rn(__uint_as_float(top), 6.f) : __uint_as_float(0x7fffffffu));
-  const float sf = __bfloat162float(s);
-  uint32_t x = 0;
-  if (finite && sf != 0.f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x |= f32_to_e2m1x2(__fdiv_rn(y[2 * i], sf), __fdiv_rn(y[2 * i + 1], sf)) << (8 * i);
+template <typename T, bool k4> constexpr int kPiece = k4 ? 8 : 16 / int(sizeof(T));
+
+// A token of a block: its request, its number among the request's new ones, and
+// its place among the request's keys, -1 where it has none.
+struct Token {
+  int b, i, key;
+};
+template <typename T>
+ATTN_DEVINL Token token_at(const AppendParams<T>& p, int token, bool report) {
+  Token t{0, 0, -1};
+  if (token < p.tokens) {
+    t.b = token / p.N;
+    t.i = token - t.b * p.N;
+    const int n = p.lens[t.b], m = p.new_lens != nullptr ? p.new_lens[t.b] : p.N;
+    if (n < 0 || n > p.max_pages * p.page_size || m < 0 || m > min(p.N, n)) {
+      if (report && t.i == 0) attn_flag_error(kErrBadIndex);
+    } else if (t.i < m) {
+      t.key = n - m + t.i;
+    }
   }
-  // The lane's low two bytes are of g = 2t, its high two of 2t + 1, of group c.
-  // Lane c of the D/32 that share t writes the c-th word of their D/8 bytes.
-  constexpr int kWords = D / 64;                       // words of one g
-  const int c = l / 4, t = l % 4, lane = threadIdx.x & 31;
-  const int src = (lane & ~(D / 8 - 1)) + 8 * (c % kWords) + t;
-  const uint32_t a = __shfl_sync(0xffffffffu, x, src), b = __shfl_sync(0xffffffffu, x, src + 4);
-  const uint32_t word = c / kWords ? __byte_perm(a, b, 0x7632) : __byte_perm(a, b, 0x5410);
-  if (!live) return;
-  *reinterpret_cast<uint32_t*>(codes + t * (D / 8) + 4 * c) = word;
-  if (t == 0) scales[c] = s;
+  return t;
+}
+// Its row of the pool for head 0, -1 where there is none.
+template <typename T>
+ATTN_DEVINL long long pool_row(const AppendParams<T>& p, const Token& t, bool report) {
+  if (t.key < 0) return -1;
+  const int page = p.table[1LL * t.b * p.max_pages + t.key / p.page_size];
+  if (unsigned(page) < unsigned(p.num_pages))
+    return 1LL * page * p.Hkv * p.page_size + t.key % p.page_size;
+  if (report) attn_flag_error(kErrBadIndex);
+  return -1;
+}
+template <typename T>
+ATTN_DEVINL float2 token_turn(const AppendParams<T>& p, const Token& t, int pair) {
+  float2 x = make_float2(1.f, 0.f);
+  if (t.key >= 0)
+    turn_cos_sin(p.positions != nullptr ? p.positions[t.b * p.pos_stride + t.i] : t.key,
+                 p.inv_freq[pair], p.magnitude, x.x, x.y);
+  return x;
 }
 
-// Grid: x over groups of tokens (b·N + i), y over runs of `hpt` of the
-// Hq + 2 Hkv heads. U heads are in flight at a time.
-template <typename T, int D, bool kWide, bool kInterleaved, bool k4>
-__global__ void __launch_bounds__(kThreads)
+// The larger magnitude, NaN if either is not a number.
+ATTN_DEVINL float larger(float a, float b) {
+  float x;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return x;
+}
+template <int V> ATTN_DEVINL float largest(const float (&y)[V]) {
+  float top = larger(y[0], y[1]);
+#pragma unroll
+  for (int i = 2; i < V; ++i) top = larger(top, y[i]);
+  return top;
+}
+// The largest of four neighbouring lanes (or of two).
+template <int kLanes> ATTN_DEVINL float largest_of_lanes(float top) {
+#pragma unroll
+  for (int off = 1; off < kLanes; off *= 2)
+    top = larger(top, __shfl_xor_sync(0xffffffffu, top, off));
+  return top;
+}
+// A group's scale from its largest magnitude.
+ATTN_DEVINL __nv_bfloat16 scale_of(float top) {
+  return __float2bfloat16_rn(top < INFINITY ? __fdiv_rn(top, 6.f) : __uint_as_float(0x7fffffffu));
+}
+// Codes of V elements (8), two a byte; zeros where the scale is 0 or not a number. The
+// quotients are correctly rounded: q = y·r with r = 1 / s rounded once, then
+// q + (y - q·s)·r (Markstein 1990: the residual of a q within an ulp is exact in an
+// FMA, and the corrected sum rounds to the quotient), for scales whose reciprocals
+// and residuals stay normal numbers; others divide.
+template <int V> ATTN_DEVINL uint32_t codes_of(const float (&y)[V], __nv_bfloat16 scale) {
+  const float s = __bfloat162float(scale);
+  float q[V];
+  if (s >= 0x1p-90f && s <= 0x1p90f) {
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float first = y[i] * r;
+      q[i] = fmaf(fmaf(-first, s, y[i]), r, first);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
+  }
+  uint32_t x = 0;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) x |= f32_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
+  return x;
+}
+
+// The codes x0, x1 of a lane's two pieces (8 elements a word, of which the low
+// half belongs to one g, the high half to the next) into a row's bytes, in which
+// the 16-bit halves of one g follow one another by group. Lane c of the row holds
+//   interleaved:   elements 16c .. 16c + 15, both of group c / 2;
+//   otherwise, of D = 64:  8 (c mod 4) .. of groups 0 and 1;
+//              of D = 128: 8 (c mod 4) .. of groups c / 4 and c / 4 + 2, or
+//                          (kNear) of groups 2 (c / 4) and 2 (c / 4) + 1.
+// Every lane stores 8 bytes. All lanes of the warp call it.
+template <int D, bool kInterleaved>
+ATTN_DEVINL void store_codes(uint32_t x0, uint32_t x1, uint8_t* row, int c, bool near, bool live) {
+  constexpr uint32_t kLow = 0x5410u, kHigh = 0x7632u;  // both words' low or high halves
+  uint32_t w0, w1;
+  int at;
+  if constexpr (D == 64 && !kInterleaved) {
+    w0 = __byte_perm(x0, x1, kLow);
+    w1 = __byte_perm(x0, x1, kHigh);
+    at = 8 * c;
+  } else if constexpr (D == 64) {
+    // (lanes c and c ^ 2 hold the groups of the same elements)
+    const bool second = c / 2;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, second ? x0 : x1, 2);
+    const uint32_t a = second ? y : x0, b = second ? x1 : y;
+    w0 = __byte_perm(a, b, kLow);
+    w1 = __byte_perm(a, b, kHigh);
+    at = 16 * (c % 2) + 8 * second;
+  } else if constexpr (!kInterleaved) {
+    // lanes c and c ^ 4 hold all four groups of the same elements; the first
+    // stores the halves of one g, the second those of the next
+    const bool second = c / 4;
+    const uint32_t y0 = __shfl_xor_sync(0xffffffffu, x0, 4),
+                   y1 = __shfl_xor_sync(0xffffffffu, x1, 4);
+    const uint32_t l0 = second ? y0 : x0, l1 = second ? y1 : x1, u0 = second ? x0 : y0,
+                   u1 = second ? x1 : y1;
+    const uint32_t pick = second ? kHigh : kLow;
+    w0 = __byte_perm(l0, near ? l1 : u0, pick);
+    w1 = __byte_perm(near ? u0 : l1, u1, pick);
+    at = 16 * (c % 4) + 8 * second;
+  } else {
+    // lane c = 2 group + p holds the words 2p and 2p + 1 of its group; it stores
+    // those halves (low: group even, high: odd) of all groups' word 2p + group / 2
+    const int group = c / 2;
+    const bool upper = group / 2, odd = group % 2;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, upper ? x0 : x1, 4);
+    const uint32_t lo = upper ? y : x0, hi = upper ? x1 : y;     // groups group % 2, + 2
+    const uint32_t own = __byte_perm(lo, hi, odd ? kHigh : kLow);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(lo, hi, odd ? kLow : kHigh), 2);
+    const uint32_t even_ = odd ? other : own, odd_ = odd ? own : other;
+    w0 = __byte_perm(even_, odd_, kLow);
+    w1 = __byte_perm(even_, odd_, kHigh);
+    at = 16 * (2 * (c % 2) + upper) + 8 * odd;
+  }
+  if (live) *reinterpret_cast<uint2*>(row + at) = make_uint2(w0, w1);
+}
+
+// Rows in 16-byte pieces. Grid: groups of tokens (b·N + i), fastest, and runs of the
+// Hq + 2 Hkv heads; with 4 bits the last heads, which take longest, first. A thread
+// takes `hpt` heads, U in flight at a time, the first while the angles are worked
+// out. kSpread: the block's warps take different heads of the same tokens and work out
+// their angles together, one or two a thread; otherwise they take different tokens,
+// every thread with its own angles.
+template <typename T, int D, bool kInterleaved, bool k4, bool kSpread>
+__global__ void __launch_bounds__(kThreads, k4 ? 5 : 6)
 append_kernel(const __grid_constant__ AppendParams<T> p) {
-  constexpr int kLanes = D / 8, U = sizeof(T) == 2 ? 4 : 2;
-  constexpr int kAngles = kInterleaved ? 4 : 8;        // of the 8 elements
+  // elements of a piece: 16 bytes of them; with 4 bits a quarter of a group
+  constexpr int V = kPiece<T, k4>, kLanes = D / (2 * V), U = V * sizeof(T) == 16 ? 4 : 2;
+  constexpr int kTokens = (kSpread ? 32 : kThreads) / kLanes, kPairs = D / 2;
+  __shared__ alignas(16) float2 turns[kSpread ? kTokens : 1][kPairs];
   pdl_launch_dependents();
-  const int l = threadIdx.x % kLanes, e0 = 8 * l;
-  const int token = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const bool in_grid = token < p.tokens;
-  const int b = in_grid ? token / p.N : 0, i = in_grid ? token % p.N : 0;
+  // (uniform, and known to be)
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
+  const int c = threadIdx.x % kLanes, mine = (kSpread ? threadIdx.x % 32 : threadIdx.x) / kLanes;
   const int H = p.Hq + 2 * p.Hkv;
-  const int h0 = int(blockIdx.y) * p.hpt, h1 = min(H, h0 + p.hpt);
-  // with rows that move in 16-byte pieces a piece is turned as a whole or not
-  const bool turned = e0 < p.rot;
+  const int group = int(blockIdx.x % p.blocks);
+  const int run_of = int(blockIdx.x / p.blocks);
+  const int hb = (k4 ? int(p.groups) - 1 - run_of : run_of) * p.hpt * (kSpread ? kWarps : 1);
+  const int h0 = hb + (kSpread ? warp * p.hpt : 0), h1 = min(H, h0 + p.hpt);
+  const int token0 = group * kTokens;
+  const bool turned = c < p.rot / (2 * V);
   const int half = p.rot / 2;
-  const int mate = kInterleaved || !turned ? 0 : e0 < half ? half : -half;
-  const T* xq = p.q + b * p.qs.batch + i * p.qs.token + e0;
-  const T* xk = p.k + b * p.ks.batch + i * p.ks.token + e0;
-  const T* xv = p.v + b * p.vs.batch + i * p.vs.token + e0;
-  T* yq = p.q_out + b * p.qos.batch + i * p.qos.token + e0;
+  // where the lane's two pieces begin
+  int off0, off1;
+  if (kInterleaved) {
+    off0 = 2 * V * c;
+    off1 = off0 + V;
+  } else if (turned) {
+    off0 = V * c;
+    off1 = off0 + half;
+  } else {
+    off0 = p.rot + V * (c - p.rot / (2 * V));
+    off1 = off0 + (D - p.rot) / 2;
+  }
 
   pdl_wait_primary();
-  Piece<T> own[U], other[U];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = h + u;
-      if (at >= h1 || !in_grid) continue;
-      const T* x = at < p.Hq           ? xq + at * p.qs.head
-                   : at < p.Hq + p.Hkv ? xk + (at - p.Hq) * p.ks.head
-                                       : xv + (at - p.Hq - p.Hkv) * p.vs.head;
-      load_piece<T, kWide>(own[u], x);
-      if (!kInterleaved && turned && at < p.Hq + p.Hkv) {
-        if constexpr (kWide) {
-          load_piece<T, true>(other[u], x + mate);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (e0 + j < p.rot) other[u].x[j] = x[e0 + j < half ? j + half : j - half];
-        }
-      }
-    }
+  const Token own = token_at(p, token0 + mine, c == 0 && hb == 0 && (!kSpread || warp == 0));
+  const bool live = own.key >= 0;
+  // Padding is not loaded, but for small calls, which do not wait for the lengths.
+  const bool fetch = kSpread || p.new_lens == nullptr ? token0 + mine < p.tokens : live;
+  // the thread's heads of each kind: [first, end)
+  const int q0 = min(h0, p.Hq), q1 = min(h1, p.Hq);
+  const int k0 = max(h0 - p.Hq, 0), k1 = min(max(h1 - p.Hq, 0), p.Hkv);
+  const int v0 = max(h0 - p.Hq - p.Hkv, 0), v1 = max(h1 - p.Hq - p.Hkv, 0);
+  auto rows = [&](const T* x, const attn_strides& s, int head) {
+    return x + own.b * s.batch + own.i * s.token + head * s.head;
   };
-  load(h0);
-
-  // the token's row of the cache
-  int row_of = -1;                                     // its position among the request's keys
-  if (in_grid) {
-    const int n = p.lens[b], m = p.new_lens != nullptr ? p.new_lens[b] : p.N;
-    if (n < 0 || n > p.max_pages * p.page_size || m < 0 || m > min(p.N, n)) {
-      if (l == 0 && h0 == 0 && i == 0) attn_flag_error(kErrBadIndex);
-    } else if (i < m) {
-      row_of = n - m + i;
-    }
-  }
-  const bool live = row_of >= 0;
-  long long row = -1;                                  // of the pool, head 0
-  if (live && h1 > p.Hq) {
-    const int page = p.table[1LL * b * p.max_pages + row_of / p.page_size];
-    if (unsigned(page) < unsigned(p.num_pages))
-      row = 1LL * page * p.Hkv * p.page_size + row_of % p.page_size;
-    else if (l == 0)
-      attn_flag_error(kErrBadIndex);
-  }
-  float cs[kAngles], sn[kAngles];
-  if (turned && live && h0 < p.Hq + p.Hkv) {
-    const long long at = p.positions != nullptr ? p.positions[b * p.pos_stride + i] : row_of;
+  Piece<T, V> x0[U], x1[U];
+  auto load = [&](const T* x, long long step, int n) {
 #pragma unroll
-    for (int j = 0; j < kAngles; ++j) {
-      const int e = kInterleaved ? e0 + 2 * j : e0 + j;
-      if (kWide || e < p.rot) {
-        turn_cos_sin(at, p.inv_freq[kInterleaved ? e / 2 : e < half ? e : e - half],
-                     p.magnitude, cs[j], sn[j]);
-        if (!kInterleaved && e < half) sn[j] = -sn[j];
+    for (int u = 0; u < U; ++u)
+      if (u < n && fetch) {
+        load_piece(x0[u], x + u * step + off0);
+        load_piece(x1[u], x + u * step + off1);
+      }
+  };
+  if (q0 < q1)
+    load(rows(p.q, p.qs, q0), p.qs.head, q1 - q0);
+  else if (k0 < k1)
+    load(rows(p.k, p.ks, k0), p.ks.head, k1 - k0);
+  else
+    load(rows(p.v, p.vs, v0), p.vs.head, v1 - v0);
+  const long long row = h1 > max(h0, p.Hq) ? pool_row(p, own, c == 0) : -1;
+  float cs[V], sn[V];
+  if (p.rot > 0 && hb < p.Hq + p.Hkv) {                // (the same for the whole block)
+    if constexpr (kSpread) {
+      for (int a = threadIdx.x; a < kTokens * kPairs; a += kThreads)
+        if (a % kPairs < half)
+          turns[a / kPairs][a % kPairs] =
+              token_turn(p, token_at(p, token0 + a / kPairs, false), a % kPairs);
+      __syncthreads();
+    }
+    if (turned) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 y = kSpread ? turns[kSpread ? mine : 0][V * c + i] : token_turn(p, own, V * c + i);
+        cs[i] = y.x;
+        sn[i] = y.y;
       }
     }
   }
-  for (int h = h0; h < h1; h += U) {
-    // every lane of a row has read what a row turned in place overwrites
-    __syncwarp();
+  // `n` heads of one kind from x on, `step` elements apart; `out`: where the first
+  // of them goes, in rows of T `out_step` apart or (4 bits) as rows of the pool. The
+  // first U are there already if `loaded`.
+  auto run = [&](auto kind, const T* x, long long step, T* out, long long out_step, int n,
+                 bool loaded) {
+    constexpr int kKind = decltype(kind)::value;       // 0: queries, 1: keys, 2: values
+    constexpr bool kFour = k4 && kKind > 0;
+    if (!loaded) load(x, step, n);
+    const bool stored = kKind == 0 ? live : row >= 0;
+    long long pool = 0;                                // 4 bits: the row of the pool
+    if constexpr (kFour) pool = row + 1LL * (kKind == 1 ? k0 : v0) * p.page_size;
+    for (int h = 0; h < n; h += U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = h + u;
-      if (at >= h1) break;
-      float y[8];
+      for (int u = 0; u < U; ++u) {
+        if (h + u >= n) break;
+        if (kKind < 2 || kFour) {                      // (a value that stays T is copied)
+          float y0[V], y1[V];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = to_f32(own[u].x[j]);
-      if (turned && at < p.Hq + p.Hkv) {
+          for (int j = 0; j < V; ++j) {
+            y0[j] = to_f32(x0[u].x[j]);
+            y1[j] = to_f32(x1[u].x[j]);
+          }
+          if (kKind < 2 && turned) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (!kWide && e0 + j >= p.rot) continue;
-          const float x = to_f32(own[u].x[j]);
-          if constexpr (kInterleaved) {
-            const float z = to_f32(own[u].x[j ^ 1]) * sn[j / 2];
-            y[j] = fmaf(x, cs[j / 2], j % 2 ? z : -z);
+            for (int i = 0; i < V; ++i) {
+              // pair i: elements 2i, 2i + 1 of both pieces, or i of either
+              float& a = !kInterleaved ? y0[i] : i < V / 2 ? y0[2 * i % V] : y1[2 * i % V];
+              float& b = !kInterleaved ? y1[i] : i < V / 2 ? y0[2 * i % V + 1] : y1[2 * i % V + 1];
+              const float xa = a, xb = b;
+              a = fmaf(xa, cs[i], -xb * sn[i]);
+              b = fmaf(xb, cs[i], xa * sn[i]);
+            }
+          }
+          if constexpr (kFour) {
+            const float top0 = largest(y0), top1 = largest(y1);
+            __nv_bfloat16 s0, s1;
+            if constexpr (kInterleaved) {
+              s0 = s1 = scale_of(largest_of_lanes<2>(larger(top0, top1)));
+            } else {
+              s0 = scale_of(largest_of_lanes<4>(top0));
+              s1 = scale_of(largest_of_lanes<4>(top1));
+            }
+            const long long to = pool + 1LL * (h + u) * p.page_size;
+            uint8_t* codes = static_cast<uint8_t*>(kKind == 1 ? p.k_pool : p.v_pool);
+            __nv_bfloat16* scales = (kKind == 1 ? p.k_scales : p.v_scales) + to * (D / 32);
+            store_codes<D, kInterleaved>(codes_of(y0, s0), codes_of(y1, s1), codes + to * (D / 2),
+                                         c, p.rot == D / 2, stored);
+            if (stored && c % (kInterleaved ? 2 : 4) == 0) {
+              scales[off0 / 32] = s0;
+              if (!kInterleaved) scales[off1 / 32] = s1;
+            }
           } else {
-            y[j] = fmaf(x, cs[j], to_f32(other[u].x[j]) * sn[j]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              x0[u].x[j] = from_f32<T>(y0[j]);
+              x1[u].x[j] = from_f32<T>(y1[j]);
+            }
           }
         }
+        if (!kFour && stored) {
+          store_piece(out + u * out_step + off0, x0[u]);
+          store_piece(out + u * out_step + off1, x1[u]);
+        }
       }
-      const bool is_q = at < p.Hq, is_k = at < p.Hq + p.Hkv;
-      const int head = is_k ? at - p.Hq : at - p.Hq - p.Hkv;
-      const long long to = row + 1LL * head * p.page_size;
-      if (k4 && !is_q) {
-        uint8_t* codes = static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool);
-        __nv_bfloat16* scales = is_k ? p.k_scales : p.v_scales;
-        store_row4<D>(y, codes + to * (D / 2), scales + to * (D / 32), l, row >= 0);
-        continue;
-      }
-      Piece<T> out;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) out.x[j] = from_f32<T>(y[j]);
-      if (is_q) {
-        if (live) store_piece<T, kWide>(yq + at * p.qos.head, out);
-      } else if (row >= 0) {
-        T* pool = static_cast<T*>(is_k ? p.k_pool : p.v_pool);
-        store_piece<T, true>(pool + to * D + e0, out);
-      }
+      x += U * step;
+      out += U * out_step;
+      if (h + U < n) load(x, step, n - h - U);
     }
-    if (h + U < h1) load(h + U);
+  };
+  if (q0 < q1)
+    run(std::integral_constant<int, 0>{}, rows(p.q, p.qs, q0), p.qs.head,
+        p.q_out + own.b * p.qos.batch + own.i * p.qos.token + q0 * p.qos.head, p.qos.head,
+        q1 - q0, true);
+  const long long head_rows = 1LL * p.page_size * D;
+  if (k0 < k1)
+    run(std::integral_constant<int, 1>{}, rows(p.k, p.ks, k0), p.ks.head,
+        static_cast<T*>(p.k_pool) + (k4 ? 0 : row * D + k0 * head_rows), head_rows, k1 - k0,
+        q0 >= q1);
+  if (v0 < v1)
+    run(std::integral_constant<int, 2>{}, rows(p.v, p.vs, v0), p.vs.head,
+        static_cast<T*>(p.v_pool) + (k4 ? 0 : row * D + v0 * head_rows), head_rows, v1 - v0,
+        q0 >= q1 && k0 >= k1);
+}
+
+// The same element by element: any alignment, any rot_dim. A thread owns 8
+// adjacent elements, D/8 lanes a row, and reads the partners of its pairs too; the
+// rows of a warp are whole, so that rows turned in place are read by all their
+// lanes before any is written.
+template <typename T, int D, bool k4>
+__global__ void __launch_bounds__(kThreads)
+append_any_kernel(const __grid_constant__ AppendParams<T> p, int interleaved) {
+  constexpr int kLanes = D / 8, kTokens = 32 / kLanes, kPairs = D / 2;
+  __shared__ float2 turns[kTokens][kPairs];
+  pdl_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % kLanes, e0 = 8 * l;
+  const int mine = lane / kLanes, token0 = int(blockIdx.x % p.blocks) * kTokens, half = p.rot / 2;
+  const int H = p.Hq + 2 * p.Hkv, hb = int(blockIdx.x / p.blocks) * p.hpt * kWarps;
+  const int h0 = hb + warp * p.hpt, h1 = min(H, h0 + p.hpt);
+  pdl_wait_primary();
+  const Token own = token_at(p, token0 + mine, l == 0 && hb == 0 && warp == 0);
+  const bool live = own.key >= 0;
+  const long long row = h1 > max(h0, p.Hq) ? pool_row(p, own, l == 0) : -1;
+  for (int a = threadIdx.x; a < kTokens * kPairs; a += kThreads)
+    if (a % kPairs < half)
+      turns[a / kPairs][a % kPairs] =
+          token_turn(p, token_at(p, token0 + a / kPairs, false), a % kPairs);
+  __syncthreads();
+  for (int at = h0; at < h1; ++at) {
+    const bool is_q = at < p.Hq, is_k = at < p.Hq + p.Hkv;
+    const int head = is_q ? at : is_k ? at - p.Hq : at - p.Hq - p.Hkv;
+    const attn_strides& s = is_q ? p.qs : is_k ? p.ks : p.vs;
+    const T* x = (is_q ? p.q : is_k ? p.k : p.v) + own.b * s.batch + own.i * s.token +
+                 head * s.head;
+    float y[8] = {};
+    if (live)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = e0 + j;
+        y[j] = to_f32(x[e]);
+        if (is_k && e < p.rot) {
+          const bool second = interleaved ? e % 2 : e >= half;
+          const int mate = interleaved ? e ^ 1 : second ? e - half : e + half;
+          const float2 t = turns[mine][interleaved ? e / 2 : second ? e - half : e];
+          const float z = to_f32(x[mate]) * t.y;
+          y[j] = fmaf(y[j], t.x, second ? z : -z);
+        }
+      }
+    __syncwarp();
+    const long long to = row + 1LL * head * p.page_size;
+    if (k4 && !is_q) {
+      const __nv_bfloat16 scale = scale_of(largest_of_lanes<4>(largest(y)));
+      const uint32_t w = codes_of(y, scale);
+      if (row >= 0) {
+        const int c = l / 4, t = l % 4;                // group, and which 8 of it
+        uint16_t* codes = reinterpret_cast<uint16_t*>(
+            static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool) + to * (D / 2));
+        codes[2 * t * (D / 32) + c] = uint16_t(w);
+        codes[(2 * t + 1) * (D / 32) + c] = uint16_t(w >> 16);
+        if (t == 0) (is_k ? p.k_scales : p.v_scales)[to * (D / 32) + c] = scale;
+      }
+    } else if (is_q ? live : row >= 0) {
+      T* out = is_q ? p.q_out + own.b * p.qos.batch + own.i * p.qos.token + head * p.qos.head
+                    : static_cast<T*>(is_k ? p.k_pool : p.v_pool) + to * D;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[e0 + j] = from_f32<T>(y[j]);
+    }
   }
 }
 
@@ -305,10 +514,10 @@ read4_kernel(const uint8_t* __restrict__ k_codes, const __nv_bfloat16* __restric
   }
 }
 
-void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid,
+void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid, int threads,
                       cudaStream_t stream) {
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -316,7 +525,7 @@ void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 g
   cfg.numAttrs = 1;
 }
 
-template <typename T, int D, bool kWide, bool kInterleaved, bool k4>
+template <typename T, int D, bool k4>
 cudaError_t launch_t(const AppendArgs& a) {
   AppendParams<T> p{};
   p.q = static_cast<const T*>(a.q);
@@ -346,35 +555,45 @@ cudaError_t launch_t(const AppendArgs& a) {
   p.max_pages = a.max_pages;
   p.rot = a.rot;
   p.magnitude = a.magnitude;
-  const int tpb = kThreads / (D / 8), H = a.Hq + 2 * a.Hkv;
-  const long long blocks = (1LL * p.tokens + tpb - 1) / tpb;
-  // Heads per thread, a power of two times the 4 that are in flight: as many as
-  // leave eight blocks per SM (as in rope.cu).
-  const long long slots = 8LL * (device_sm_count() > 0 ? device_sm_count() : 1);
-  p.hpt = 4;
-  while (p.hpt < H && blocks * ((H + 2 * p.hpt - 1) / (2 * p.hpt)) >= slots) p.hpt *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  dependent_launch(cfg, attr, dim3(unsigned(blocks), unsigned((H + p.hpt - 1) / p.hpt)), a.stream);
-  return cudaLaunchKernelEx(&cfg, append_kernel<T, D, kWide, kInterleaved, k4>, p);
-}
-
-template <typename T, int D, bool k4>
-cudaError_t launch_d(const AppendArgs& a) {
-  const bool wide = a.rot % (a.interleaved ? 8 : 16) == 0 &&
+  // Rows in 16-byte pieces where they and their pairs lie so; with 4 bits a pair's
+  // pieces have to be whole quarters of groups, too.
+  constexpr int V = kPiece<T, k4>;
+  const bool wide = a.rot % (k4 && !a.interleaved ? 64 : 2 * V) == 0 &&
                     (a.Hq == 0 || (rows16(a.q, a.qs, a.B, a.Hq, a.N, sizeof(T)) &&
                                    rows16(a.q_out, a.qos, a.B, a.Hq, a.N, sizeof(T)))) &&
                     rows16(a.k, a.ks, a.B, a.Hkv, a.N, sizeof(T)) &&
                     rows16(a.v, a.vs, a.B, a.Hkv, a.N, sizeof(T));
-  if (wide)
-    return a.interleaved ? launch_t<T, D, true, true, k4>(a) : launch_t<T, D, true, false, k4>(a);
-  return a.interleaved ? launch_t<T, D, false, true, k4>(a) : launch_t<T, D, false, false, k4>(a);
+  // Many tokens: 8 heads a thread, where that gives eight blocks an SM. Fewer: the
+  // warps spread over the heads, with as many heads each as leave four blocks an SM.
+  const int H = a.Hq + 2 * a.Hkv, sms = std::max(1, device_sm_count());
+  const int rows = 64 * V / D;                         // of a warp
+  const long long plain = (1LL * p.tokens + kWarps * rows - 1) / (kWarps * rows);
+  const bool spread = !wide || plain * ((H + 7) / 8) < 8LL * sms;
+  const int tokens = !wide ? 256 / D : spread ? rows : kWarps * rows;   // of a block
+  const long long blocks = (1LL * p.tokens + tokens - 1) / tokens;
+  p.hpt = spread ? 4 : 8;
+  if (spread)
+    while (p.hpt > 1 && blocks * ((H + kWarps * p.hpt - 1) / (kWarps * p.hpt)) < 4LL * sms)
+      p.hpt /= 2;
+  const int heads = p.hpt * (spread ? kWarps : 1);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  p.blocks = unsigned(blocks);
+  p.groups = unsigned((H + heads - 1) / heads);
+  if (blocks * p.groups > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  dependent_launch(cfg, attr, dim3(unsigned(blocks * p.groups)), kThreads, a.stream);
+  if (!wide) return cudaLaunchKernelEx(&cfg, append_any_kernel<T, D, k4>, p, a.interleaved);
+  if (spread)
+    return a.interleaved ? cudaLaunchKernelEx(&cfg, append_kernel<T, D, true, k4, true>, p)
+                         : cudaLaunchKernelEx(&cfg, append_kernel<T, D, false, k4, true>, p);
+  return a.interleaved ? cudaLaunchKernelEx(&cfg, append_kernel<T, D, true, k4, false>, p)
+                       : cudaLaunchKernelEx(&cfg, append_kernel<T, D, false, k4, false>, p);
 }
 
 template <typename T> cudaError_t launch_type(const AppendArgs& a) {
   const bool four = a.k_scales != nullptr;
-  if (a.d == 64) return four ? launch_d<T, 64, true>(a) : launch_d<T, 64, false>(a);
-  return four ? launch_d<T, 128, true>(a) : launch_d<T, 128, false>(a);
+  if (a.d == 64) return four ? launch_t<T, 64, true>(a) : launch_t<T, 64, false>(a);
+  return four ? launch_t<T, 128, true>(a) : launch_t<T, 128, false>(a);
 }
 
 }  // namespace
@@ -390,7 +609,7 @@ cudaError_t launch_cache_read4(const Read4Args& a) {
   dependent_launch(cfg, attr,
                    dim3(unsigned((a.L + kRowsPerBlock - 1) / kRowsPerBlock),
                         unsigned(a.B * a.Hkv), 2),
-                   a.stream);
+                   kThreads, a.stream);
   auto run = [&](auto* kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint8_t*>(a.k_codes),
                               static_cast<const __nv_bfloat16*>(a.k_scales),
