@@ -227,7 +227,7 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
   const int c = threadIdx.x % kLanes, mine = (kSpread ? threadIdx.x % 32 : threadIdx.x) / kLanes;
   const int H = p.Hq + 2 * p.Hkv;
   const int group = int(blockIdx.x % p.blocks);
-  const int run_of = int(blockIdx.x / p.blocks);
+  const int run_of = int(blockIdx.x / p.blocks);       // (of heads, from the first: hb)
   const int hb = (k4 ? int(p.groups) - 1 - run_of : run_of) * p.hpt * (kSpread ? kWarps : 1);
   const int h0 = hb + (kSpread ? warp * p.hpt : 0), h1 = min(H, h0 + p.hpt);
   const int token0 = group * kTokens;
@@ -293,28 +293,25 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
     }
   }
   // `n` heads of one kind from x on, `step` elements apart; `out`: where the first
-  // of them goes, in rows of T `out_step` apart or (4 bits) as rows of the pool. The
+  // of them goes, in rows of T `out_step` apart, or (4 bits) its codes and scales. The
   // first U are there already if `loaded`.
+  enum { kCopied, kTurned, kCoded };                   // (values stay T; queries, keys; 4 bits)
   auto run = [&](auto kind, const T* x, long long step, T* out, long long out_step, int n,
-                 bool loaded) {
-    constexpr int kKind = decltype(kind)::value;       // 0: queries, 1: keys, 2: values
-    constexpr bool kFour = k4 && kKind > 0;
+                 bool loaded, bool stored, bool turn, uint8_t* codes, __nv_bfloat16* scales) {
+    constexpr int kKind = decltype(kind)::value;
     if (!loaded) load(x, step, n);
-    const bool stored = kKind == 0 ? live : row >= 0;
-    long long pool = 0;                                // 4 bits: the row of the pool
-    if constexpr (kFour) pool = row + 1LL * (kKind == 1 ? k0 : v0) * p.page_size;
     for (int h = 0; h < n; h += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (h + u >= n) break;
-        if (kKind < 2 || kFour) {                      // (a value that stays T is copied)
+        if (kKind != kCopied) {
           float y0[V], y1[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             y0[j] = to_f32(x0[u].x[j]);
             y1[j] = to_f32(x1[u].x[j]);
           }
-          if (kKind < 2 && turned) {
+          if (turn) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
               // pair i: elements 2i, 2i + 1 of both pieces, or i of either
@@ -325,7 +322,7 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
               b = fmaf(xb, cs[i], xa * sn[i]);
             }
           }
-          if constexpr (kFour) {
+          if constexpr (kKind == kCoded) {
             const float top0 = largest(y0), top1 = largest(y1);
             __nv_bfloat16 s0, s1;
             if constexpr (kInterleaved) {
@@ -334,15 +331,14 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
               s0 = scale_of(largest_of_lanes<4>(top0));
               s1 = scale_of(largest_of_lanes<4>(top1));
             }
-            const long long to = pool + 1LL * (h + u) * p.page_size;
-            uint8_t* codes = static_cast<uint8_t*>(kKind == 1 ? p.k_pool : p.v_pool);
-            __nv_bfloat16* scales = (kKind == 1 ? p.k_scales : p.v_scales) + to * (D / 32);
-            store_codes<D, kInterleaved>(codes_of(y0, s0), codes_of(y1, s1), codes + to * (D / 2),
-                                         c, p.rot == D / 2, stored);
+            store_codes<D, kInterleaved>(codes_of(y0, s0), codes_of(y1, s1), codes, c,
+                                         p.rot == D / 2, stored);
             if (stored && c % (kInterleaved ? 2 : 4) == 0) {
               scales[off0 / 32] = s0;
               if (!kInterleaved) scales[off1 / 32] = s1;
             }
+            codes += p.page_size * (D / 2);
+            scales += p.page_size * (D / 32);
           } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -351,7 +347,7 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
             }
           }
         }
-        if (!kFour && stored) {
+        if (kKind != kCoded && stored) {
           store_piece(out + u * out_step + off0, x0[u]);
           store_piece(out + u * out_step + off1, x1[u]);
         }
@@ -362,18 +358,33 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
     }
   };
   if (q0 < q1)
-    run(std::integral_constant<int, 0>{}, rows(p.q, p.qs, q0), p.qs.head,
+    run(std::integral_constant<int, kTurned>{}, rows(p.q, p.qs, q0), p.qs.head,
         p.q_out + own.b * p.qos.batch + own.i * p.qos.token + q0 * p.qos.head, p.qos.head,
-        q1 - q0, true);
+        q1 - q0, true, live, turned, nullptr, nullptr);
   const long long head_rows = 1LL * p.page_size * D;
-  if (k0 < k1)
-    run(std::integral_constant<int, 1>{}, rows(p.k, p.ks, k0), p.ks.head,
-        static_cast<T*>(p.k_pool) + (k4 ? 0 : row * D + k0 * head_rows), head_rows, k1 - k0,
-        q0 >= q1);
-  if (v0 < v1)
-    run(std::integral_constant<int, 2>{}, rows(p.v, p.vs, v0), p.vs.head,
-        static_cast<T*>(p.v_pool) + (k4 ? 0 : row * D + v0 * head_rows), head_rows, v1 - v0,
-        q0 >= q1 && k0 >= k1);
+  if constexpr (k4) {
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {             // (one copy of the code for both)
+      const int first = kind ? v0 : k0, end = kind ? v1 : k1;
+      const long long to = row + 1LL * first * p.page_size;
+      if (first < end)
+        run(std::integral_constant<int, kCoded>{},
+            kind ? rows(p.v, p.vs, first) : rows(p.k, p.ks, first),
+            kind ? p.vs.head : p.ks.head, static_cast<T*>(nullptr), 0, end - first,
+            q0 >= q1 && (kind == 0 || k0 >= k1), row >= 0, turned && kind == 0,
+            static_cast<uint8_t*>(kind ? p.v_pool : p.k_pool) + to * (D / 2),
+            (kind ? p.v_scales : p.k_scales) + to * (D / 32));
+    }
+  } else {
+    if (k0 < k1)
+      run(std::integral_constant<int, kTurned>{}, rows(p.k, p.ks, k0), p.ks.head,
+          static_cast<T*>(p.k_pool) + row * D + k0 * head_rows, head_rows, k1 - k0, q0 >= q1,
+          row >= 0, turned, nullptr, nullptr);
+    if (v0 < v1)
+      run(std::integral_constant<int, kCopied>{}, rows(p.v, p.vs, v0), p.vs.head,
+          static_cast<T*>(p.v_pool) + row * D + v0 * head_rows, head_rows, v1 - v0,
+          q0 >= q1 && k0 >= k1, row >= 0, false, nullptr, nullptr);
+  }
 }
 
 // The same element by element: any alignment, any rot_dim. A thread owns 8
@@ -563,15 +574,16 @@ cudaError_t launch_t(const AppendArgs& a) {
                                    rows16(a.q_out, a.qos, a.B, a.Hq, a.N, sizeof(T)))) &&
                     rows16(a.k, a.ks, a.B, a.Hkv, a.N, sizeof(T)) &&
                     rows16(a.v, a.vs, a.B, a.Hkv, a.N, sizeof(T));
-  // Many tokens: 8 heads a thread, where that gives eight blocks an SM. Fewer: the
-  // warps spread over the heads, with as many heads each as leave four blocks an SM.
+  // Many tokens: 8 heads a thread (4 bits: 16, so that angles are worked out less
+  // often), where that gives eight blocks an SM. Fewer: the warps spread over the
+  // heads, with as many heads each as leave four blocks an SM.
   const int H = a.Hq + 2 * a.Hkv, sms = std::max(1, device_sm_count());
   const int rows = 64 * V / D;                         // of a warp
   const long long plain = (1LL * p.tokens + kWarps * rows - 1) / (kWarps * rows);
   const bool spread = !wide || plain * ((H + 7) / 8) < 8LL * sms;
   const int tokens = !wide ? 256 / D : spread ? rows : kWarps * rows;   // of a block
   const long long blocks = (1LL * p.tokens + tokens - 1) / tokens;
-  p.hpt = spread ? 4 : 8;
+  p.hpt = spread ? 4 : k4 && plain * ((H + 15) / 16) >= 8LL * sms ? 16 : 8;
   if (spread)
     while (p.hpt > 1 && blocks * ((H + kWarps * p.hpt - 1) / (kWarps * p.hpt)) < 4LL * sms)
       p.hpt /= 2;

@@ -55,7 +55,7 @@ ATTN_DEFINE_ERROR_WORD(take_error_decode_window)
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kMaxCluster = 8, kSmemPerSm = 228 * 1024;
 // Keys of a fragment, and runs of them in a step of a warp.
 constexpr int kKeys = 16;
 template <bool k4, int NT> constexpr int kRunsOf = k4 && NT == 1 ? 2 : 1;
@@ -133,13 +133,17 @@ template <int kN, int kTile, bool kEarly> struct PlaceSums {
   }
 };
 
-// Share c of `ctas` equal ones of `places`: [start(c), start(c + 1)).
+// Share c of `ctas` equal ones of `places` (below 2^31): [start(c), start(c + 1)).
 ATTN_DEVINL int share_start(int c, int ctas, int places) {
-  return int((long long)c * places / ctas);
+  const int q = places / ctas, r = places - q * ctas;
+  return c * q + c * r / ctas;                    // (ctas below 2^12)
 }
 // The share that holds a place.
 ATTN_DEVINL int share_of(int place, int ctas, int places) {
-  return int(((long long)(place + 1) * ctas - 1) / places);
+  int c = min(ctas - 1, int(float(place) / float(places) * float(ctas)));
+  while (c + 1 < ctas && share_start(c + 1, ctas, places) <= place) ++c;
+  while (c > 0 && share_start(c, ctas, places) > place) --c;
+  return c;
 }
 
 // A share as units: its first and the one past its last, the request of the first,
@@ -271,6 +275,13 @@ ATTN_DEVINL void copies_commit() { asm volatile("cp.async.commit_group;" ::: "me
 template <int kLeft> ATTN_DEVINL void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+// The barrier of a cluster's threads in two halves.
+ATTN_DEVINL void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+ATTN_DEVINL void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 ATTN_DEVINL uint4 lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -344,9 +355,16 @@ template <int D, bool k4, int NT, bool kTwice>
 constexpr int kAtOnce = k4 ? (kTwice ? D / 32 : D / 16) : 4 / NT;
 
 template <int D, bool k4, int NT, bool kTwice>
-constexpr int smem_bytes() {
-  return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes +
-         kAtOnce<D, k4, NT, kTwice> * NT * kWarps * 512 + kWarps * 8 * NT * 8;
+constexpr int handed_bytes() {                    // (m, l) too
+  return kAtOnce<D, k4, NT, kTwice> * NT * kWarps * 512 + kWarps * 8 * NT * 8;
+}
+template <int D, bool k4, int NT>
+constexpr int ring_bytes() { return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes; }
+// What the other CTAs of a cluster write into the first one's shared memory, in the
+// place of its rings.
+template <int D, int NT, bool kTwice>
+constexpr int inbox_bytes() {
+  return (kMaxCluster - 1) * ((kTwice ? D / 32 : D / 16) * NT * 512 + 8 * NT * 8);
 }
 
 // What a tile is: nothing to compute, all keys seen by all tokens, or neither;
@@ -375,8 +393,9 @@ window_kernel(const __grid_constant__ WindowParams p) {
   // (uniform, and known to be)
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
-  const uint32_t ring = smem_u32(smem) + warp * RingT::kBytes;
-  float4* handed = reinterpret_cast<float4*>(smem + kWarps * RingT::kBytes);
+  float4* handed = reinterpret_cast<float4*>(smem);
+  uint8_t* const rings = smem + handed_bytes<D, k4, NT, kTwice>();
+  const uint32_t ring = smem_u32(rings) + warp * RingT::kBytes;
   constexpr int kHand = kAtOnce<D, k4, NT, kTwice>;
   float2* handed_ml = reinterpret_cast<float2*>(handed + kHand * NT * kWarps * 32);
 
@@ -1044,6 +1063,8 @@ window_kernel(const __grid_constant__ WindowParams p) {
       }
     }
 
+    // (a cluster's CTA takes one run: its rings are done with, and may be written to)
+    if (p.cluster > 1) cluster_arrive();
     // Join the warps' sums, each warp some of the blocks of elements. From here on
     // m is the reference of the sums.
 #pragma unroll
@@ -1060,14 +1081,14 @@ window_kernel(const __grid_constant__ WindowParams p) {
     float4 sum[kMine];
     // Of `parts` results with (m, l) at ml[part · kRows + row]: what each is
     // scaled by, and the joined m and l.
-    auto weigh = [&](auto ml_of, int parts, int nt, int j, float (&w)[8]) {
+    auto weigh = [&](auto ml_of, int parts, int nt, int j, float (&w)[kMaxCluster]) {
       float top = -INFINITY, all = 0.f;
       const int row = 8 * nt + 2 * t + j;
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < kMaxCluster; ++x)
         if (x < parts) top = fmaxf(top, ml_of(x)[row].x);
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < kMaxCluster; ++x)
         if (x < parts) {
           const float2 ml = ml_of(x)[row];
           // (a NaN among the scores is in the sums, not in the references)
@@ -1080,7 +1101,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
     auto add = [](float4& to, const float4& x, float w0, float w1) {
       to.x += x.x * w0; to.y += x.y * w1; to.z += x.z * w0; to.w += x.w * w1;
     };
-    float w[NT][2][8];
+    float w[NT][2][kMaxCluster];
 #pragma unroll
     for (int m0 = 0; m0 < kM; m0 += kHand) {
 #pragma unroll
@@ -1111,42 +1132,54 @@ window_kernel(const __grid_constant__ WindowParams p) {
       __syncthreads();
     }
     if (p.cluster > 1) {
-      // join the CTAs, into the first one's sums
+      // Join the CTAs: the others write into the first one's shared memory.
       cg::cluster_group cluster = cg::this_cluster();
-      const bool first = cluster.block_rank() == 0;
+      const int rank = int(cluster.block_rank());
+      float4* inbox = reinterpret_cast<float4*>(rings);
+      float2* inbox_ml = reinterpret_cast<float2*>(inbox + (kMaxCluster - 1) * kM * NT * 32);
+      cluster_wait();
+      if (rank > 0) {
+        float4* to = cluster.map_shared_rank(inbox, 0) + (rank - 1) * kM * NT * 32 + lane;
 #pragma unroll
-      for (int x = 0; x < kMine; ++x)
-        if (mine(x)) handed[(x * kWarps + warp) * 32 + lane] = sum[x];
-      if (warp == 0 && g == 0)
+        for (int x = 0; x < kMine; ++x)
+          if (mine(x)) to[(x * kWarps + warp) * 32] = sum[x];
+        if (warp == 0 && g == 0) {
+          float2* to_ml = cluster.map_shared_rank(inbox_ml, 0) + (rank - 1) * kRows;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) to_ml[8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
+        }
+      } else if (warp == 0 && g == 0) {           // (its own, for all of its warps)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             handed_ml[8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
-      cluster.sync();
-      if (first) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            weigh([&](int x) { return cluster.map_shared_rank(handed_ml, x); }, p.cluster, nt, j,
-                  w[nt][j]);
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-          if (!mine(x)) continue;
-          const int nt = NT == 1 ? 0 : warp % NT;
-          float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < p.cluster)
-              add(to, cluster.map_shared_rank(handed, c)[(x * kWarps + warp) * 32 + lane],
-                  NT == 1 || nt == 0 ? w[0][0][c] : w[NT - 1][0][c],
-                  NT == 1 || nt == 0 ? w[0][1][c] : w[NT - 1][1][c]);
-          sum[x] = to;
-        }
       }
-      cluster.sync();                             // (what is read from has to stay)
-      if (!first) return;
+      cluster_arrive();
+      if (rank > 0) return;
+      cluster_wait();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          weigh([&](int x) { return x == 0 ? handed_ml : inbox_ml + (x - 1) * kRows; }, p.cluster,
+                nt, j, w[nt][j]);
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        if (!mine(x)) continue;
+        const int nt = NT == 1 ? 0 : warp % NT;
+        float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < p.cluster)
+            add(to, c == 0 ? sum[x]
+                           : inbox[((c - 1) * kM * NT + x * kWarps + warp) * 32 + lane],
+                NT == 1 || nt == 0 ? w[0][0][c] : w[NT - 1][0][c],
+                NT == 1 || nt == 0 ? w[0][1][c] : w[NT - 1][1][c]);
+        sum[x] = to;
+      }
     }
     const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
 #pragma unroll
@@ -1233,24 +1266,20 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
     pdl_wait_primary();
     pdl_launch_dependents();
     if (row >= p.Hkv * p.R || c0 == c1) return;   // (one CTA alone has written its rows)
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.m_part[slot_of(c)]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     for (int first = c0 + warp % kPer; first <= c1; first += kPer * kBatch) {
-      float x[kBatch][kLane], by[kBatch], l[kBatch];
+      // (one round trip to memory: nothing of a batch depends on the rest of it)
+      float x[kBatch][kLane], m[kBatch], l[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int c = first + i * kPer;
-        by[i] = l[i] = 0.f;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < kLane; ++j) x[i][j] = 0.f;
         if (c > c1) continue;
         const int s = slot_of(c);
-        const float mc = p.m_part[s];
+        m[i] = p.m_part[s];
         l[i] = p.l_part[s];
-        // (a NaN among the scores is in the sums, not in the references)
-        by[i] = mc == -INFINITY ? 1.f : fast_exp2(mc - top);
         const float* part = p.o_part + 1LL * s * D + kLane * lane;
         if constexpr (kLane == 4) {
           const float4 y = *reinterpret_cast<const float4*>(part);
@@ -1260,11 +1289,21 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
           x[i][0] = y.x; x[i][1] = y.y;
         }
       }
+      float to = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) to = fmaxf(to, m[i]);
+      // (a NaN among the scores is in the sums, not in the references)
+      const float before = top == -INFINITY ? 1.f : fast_exp2(top - to);
+      top = to;
+      sum *= before;
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) acc[j] *= before;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        sum = fmaf(by[i], l[i], sum);
+        const float by = m[i] == -INFINITY ? 1.f : fast_exp2(m[i] - to);
+        sum = fmaf(by, l[i], sum);
 #pragma unroll
-        for (int j = 0; j < kLane; ++j) acc[j] = fmaf(by[i], x[i][j], acc[j]);
+        for (int j = 0; j < kLane; ++j) acc[j] = fmaf(by, x[i][j], acc[j]);
       }
     }
   } else {
@@ -1273,16 +1312,29 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
     if (row >= p.Hkv * p.R) return;
   }
   if constexpr (kPer > 1) {
-    __shared__ float others[kJoinWarps][D + 1];
+    __shared__ float others[kJoinWarps][D + 2];
 #pragma unroll
     for (int j = 0; j < kLane; ++j) others[warp][kLane * lane + j] = acc[j];
-    if (lane == 0) others[warp][D] = sum;
+    if (lane == 0) {
+      others[warp][D] = sum;
+      others[warp][D + 1] = top;
+    }
     __syncthreads();
     if (warp % kPer != 0) return;
-    for (int w = warp + 1; w < warp + kPer; ++w) {
-      sum += others[w][D];
+    const float own = top;
 #pragma unroll
-      for (int j = 0; j < kLane; ++j) acc[j] += others[w][kLane * lane + j];
+    for (int w = 1; w < kPer; ++w) top = fmaxf(top, others[warp + w][D + 1]);
+    const float by = own == -INFINITY ? 1.f : fast_exp2(own - top);
+    sum *= by;
+#pragma unroll
+    for (int j = 0; j < kLane; ++j) acc[j] *= by;
+#pragma unroll
+    for (int w = 1; w < kPer; ++w) {
+      const float theirs = others[warp + w][D + 1];
+      const float with = theirs == -INFINITY ? 1.f : fast_exp2(theirs - top);
+      sum += with * others[warp + w][D];
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) acc[j] += with * others[warp + w][kLane * lane + j];
     }
   }
   const bool empty = sum == 0.f;
@@ -1335,11 +1387,13 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 template <int D, bool k4, int NT, bool kRuns, bool kTwice = false>
 cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   constexpr int kTile = kKeys * kRunsOf<k4, NT>;
-  constexpr int smem = smem_bytes<D, k4, NT, kTwice>();
+  constexpr int handed = handed_bytes<D, k4, NT, kTwice>(), rings = ring_bytes<D, k4, NT>(),
+                inbox = inbox_bytes<D, NT, kTwice>();
+  constexpr int smem = handed + rings, smem_cluster = handed + std::max(rings, inbox);
   const void* kernel =
       reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(kernel, smem, allowed);
+  cudaError_t e = allow_smem(kernel, smem_cluster, allowed);
   if (e != cudaSuccess) return e;
   p.blocks = (p.R + 8 * NT - 1) / (8 * NT);
   // most units that an item can have, by the table and the window
@@ -1351,11 +1405,13 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   const long long slots = 1LL * a.sm_count * kResident<NT, k4, kTwice>;
   // Clusters, where all of them run at once and a CTA has two units at most.
   int cluster = 1;
-  while (cluster < 8 && cluster < units) cluster *= 2;
-  if (units <= kClusterUnits * cluster && items * cluster <= slots) {
+  while (cluster < kMaxCluster && cluster < units) cluster *= 2;
+  constexpr int resident = std::min(kResident<NT, k4, kTwice>, kSmemPerSm / (smem_cluster + 1024));
+  if (units <= kClusterUnits * cluster && items * cluster <= 1LL * a.sm_count * resident) {
     p.cluster = cluster;
     p.grid = int(items) * cluster;
-    return launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, cluster, p, a.stream);
+    return launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem_cluster, cluster, p,
+                            a.stream);
   }
   p.grid = int(std::min(items * (units + kItemCost), slots));
   e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, 1, p, a.stream);
