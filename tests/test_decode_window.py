@@ -278,6 +278,16 @@ def test_shares_of_many_and_of_long_requests(ost, four, lens, Hq, Hkv, T, left, 
 @pytest.mark.gpu
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [32, 24])
+@pytest.mark.parametrize("Hq,T", [(6, 1), (8, 2), (6, 4), (4, 20)])   # 3, 8, 12, 40 rows a KV head
+@pytest.mark.parametrize("left", [-1, 2500])
+def test_shares_at_every_number_of_rows(ost, four, d, page, Hq, T, left):
+    _check(ost, four, [4000, 1, 900, 0, 3977], Hq, 2, T, d, page, left, 5, seed=6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
 def test_peaked_rows_and_moving_references(ost, four, d):
     """Scores that rise along the keys by far more than the reference lets pass."""
     lens, Hkv, Hq = [600], 1, 2
