@@ -71,10 +71,16 @@ struct WindowParams {
   int B, Hkv, T, R, blocks;                 // R = query rows per KV head, in `blocks` blocks
   int num_pages, page_size, max_pages, cap, left, n_global;
   uint32_t page_mul;                        // key / page_size = umulhi(2 key, mul) >> shift
-  int page_shift, grid;
+  int page_shift;
+  int teams, block_teams;                   // of warps, in all and in a block
   int cluster;                              // CTAs of an item, 0: shares of all items
   float scale_log2;
 };
+
+// The barrier of a team's threads.
+ATTN_DEVINL void team_sync(int in_block) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + in_block), "n"(kThreads) : "memory");
+}
 
 // ------------------------------------------------------------ division of work
 
@@ -133,16 +139,16 @@ template <int kN, int kTile, bool kEarly> struct PlaceSums {
   }
 };
 
-// Share c of `ctas` equal ones of `places` (below 2^31): [start(c), start(c + 1)).
-ATTN_DEVINL int share_start(int c, int ctas, int places) {
-  const int q = places / ctas, r = places - q * ctas;
-  return c * q + c * r / ctas;                    // (ctas below 2^12)
+// Share c of `teams` equal ones of `places` (below 2^31): [start(c), start(c + 1)).
+ATTN_DEVINL int share_start(int c, int teams, int places) {
+  const int q = places / teams, r = places - q * teams;
+  return c * q + c * r / teams;                   // (teams below 2^12)
 }
 // The share that holds a place.
-ATTN_DEVINL int share_of(int place, int ctas, int places) {
-  int c = min(ctas - 1, int(float(place) / float(places) * float(ctas)));
-  while (c + 1 < ctas && share_start(c + 1, ctas, places) <= place) ++c;
-  while (c > 0 && share_start(c, ctas, places) > place) --c;
+ATTN_DEVINL int share_of(int place, int teams, int places) {
+  int c = min(teams - 1, int(float(place) / float(places) * float(teams)));
+  while (c + 1 < teams && share_start(c + 1, teams, places) <= place) ++c;
+  while (c > 0 && share_start(c, teams, places) > place) --c;
   return c;
 }
 
@@ -154,17 +160,20 @@ struct Share {
 // The share of this CTA, worked out by its threads: each adds up a run of
 // requests, the block's running sums find the threads whose requests hold the
 // share's ends. Places are counted as units are.
-template <int kTile> ATTN_DEVINL Share find_share(const WindowParams& p, int cta) {
-  __shared__ int sums[2][kWarps];
-  __shared__ Share share;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+template <int kTile, int kTeams>
+ATTN_DEVINL Share find_share(const WindowParams& p, int in_block, int team) {
+  __shared__ int team_sums[kTeams][2][kWarps];
+  __shared__ Share team_share[kTeams];
+  int (&sums)[2][kWarps] = team_sums[in_block];
+  Share& share = team_share[in_block];
+  const int tid = threadIdx.x % kThreads, lane = tid % 32, warp = tid / 32;
   const int per_request = p.Hkv * p.blocks;
   const int per = (p.B + kThreads - 1) / kThreads, r0 = min(p.B, tid * per),
             r1 = min(p.B, r0 + per);
   int places = 0, units = 0;                      // of the thread's requests
   for (int r = r0; r < r1; ++r) {
     const int n = p.lens[r], u = tiles_of<kTile>(p, n).units;
-    if (cta == 0 && unsigned(n) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
+    if (team == 0 && unsigned(n) > unsigned(p.cap)) attn_flag_error(kErrBadIndex);
     places += places_of(u);
     units += u;
   }
@@ -183,7 +192,7 @@ template <int kTile> ATTN_DEVINL Share find_share(const WindowParams& p, int cta
     sums[0][warp] = at;
     sums[1][warp] = at_u;
   }
-  __syncthreads();
+  team_sync(in_block);
   int all = 0, all_u = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -194,11 +203,11 @@ template <int kTile> ATTN_DEVINL Share find_share(const WindowParams& p, int cta
     all += sums[0][w];
     all_u += sums[1][w];
   }
-  const int ctas = min(p.grid, all);
-  if (cta >= ctas) return {0, 0, 0, 0};
+  const int teams = min(p.teams, all);
+  if (team >= teams) return {0, 0, 0, 0};
 #pragma unroll
   for (int end = 0; end < 2; ++end) {
-    const int place = share_start(cta + end, ctas, all);
+    const int place = share_start(team + end, teams, all);
     if (end == 1 && place == all && tid == 0) share.end = all_u;
     if (place < at - places || place >= at) continue;
     int from = at - places, from_u = at_u - units, r = r0, u;
@@ -220,7 +229,7 @@ template <int kTile> ATTN_DEVINL Share find_share(const WindowParams& p, int cta
       share.before = from_u;
     }
   }
-  __syncthreads();
+  team_sync(in_block);
   return share;
 }
 
@@ -346,7 +355,7 @@ template <int D, bool k4, int kRun> struct Ring {
 };
 
 // CTAs per SM the registers are cut for.
-template <int NT, bool k4, bool kTwice> constexpr int kResident = k4 ? (NT == 1 ? 4 : 3) : 2;
+template <bool k4, int NT> constexpr int kTeamsOf = k4 ? (NT == 1 ? 4 : 3) : 2;
 
 // Blocks of 16 elements whose sums the warps hand one another at a time, each as
 // [32 lanes] of four floats a warp and block of 8 rows: all of them, or as many as
@@ -360,6 +369,10 @@ constexpr int handed_bytes() {                    // (m, l) too
 }
 template <int D, bool k4, int NT>
 constexpr int ring_bytes() { return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes; }
+template <int D, bool k4, int NT, bool kTwice>
+constexpr int smem_bytes() {
+  return (handed_bytes<D, k4, NT, kTwice>() + ring_bytes<D, k4, NT>() + 127) / 128 * 128;
+}
 // What the other CTAs of a cluster write into the first one's shared memory, in the
 // place of its rings.
 template <int D, int NT, bool kTwice>
@@ -379,7 +392,7 @@ enum : uint32_t { kNone = 0, kFull = 1, kPart = 2, kLacks = 4 };
 // and probabilities (the unscaled halves of columns come out of the products
 // too, and are not read).
 template <int D, bool k4, int NT, bool kRuns, bool kTwice>
-__global__ void __launch_bounds__(kThreads, kResident<NT, k4, kTwice>)
+__global__ void __launch_bounds__(kThreads * kTeamsOf<k4, NT>, 1)
 window_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kRun = kRunsOf<k4, NT>, kTile = kRun * kKeys;
   using RingT = Ring<D, k4, kRun>;
@@ -389,10 +402,14 @@ window_kernel(const __grid_constant__ WindowParams p) {
   // groups that a lane scales
   constexpr int kOwn = kTwice ? kGroups / 2 : kGroups;
   constexpr int kRowMask = kTwice ? 3 : 15;       // of a column's query row
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t block_smem[];
   // (uniform, and known to be)
-  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
+  constexpr int kTeams = kTeamsOf<k4, NT>;
+  const int warp_ = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
+  const int warp = warp_ % kWarps, in_block = warp_ / kWarps;
+  const int team = int(blockIdx.x) * p.block_teams + in_block;
   const int g = lane / 4, t = lane % 4;
+  uint8_t* const smem = block_smem + in_block * smem_bytes<D, k4, NT, kTwice>();
   float4* handed = reinterpret_cast<float4*>(smem);
   uint8_t* const rings = smem + handed_bytes<D, k4, NT, kTwice>();
   const uint32_t ring = smem_u32(rings) + warp * RingT::kBytes;
@@ -412,7 +429,8 @@ window_kernel(const __grid_constant__ WindowParams p) {
     u_begin = first + share_start(rank, p.cluster, units);
     u_end = first + share_start(rank + 1, p.cluster, units);
   } else {
-    const Share share = find_share<kTile>(p, int(blockIdx.x));
+    if (team >= p.teams) return;
+    const Share share = find_share<kTile, kTeams>(p, in_block, team);
     if (share.begin == share.end) return;
     b = share.b;
     before = share.before;
@@ -1110,7 +1128,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int nt = 0; nt < NT; ++nt)
           handed[((mt * NT + nt) * kWarps + warp) * 32 + lane] = make_float4(
               o[m0 + mt][nt][0], o[m0 + mt][nt][1], o[m0 + mt][nt][2], o[m0 + mt][nt][3]);
-      __syncthreads();
+      team_sync(in_block);
       if (m0 == 0)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1129,7 +1147,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
               NT == 1 || nt == 0 ? w[0][1][y] : w[NT - 1][1][y]);
         sum[m0 * NT / kWarps + x] = to;
       }
-      __syncthreads();
+      team_sync(in_block);
     }
     if (p.cluster > 1) {
       // Join the CTAs: the others write into the first one's shared memory.
@@ -1181,7 +1199,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
         sum[x] = to;
       }
     }
-    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    const int slot = 2 * team + (u == u_begin ? 0 : 1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int nt = NT == 1 ? 0 : warp % NT, r = (8 * nt + 2 * t + j) & kRowMask;
@@ -1253,13 +1271,13 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
   float acc[kLane] = {}, sum = 0.f, top = -INFINITY;
   if (tl.units > 0) {
     const int per_request = p.Hkv * p.blocks, places = sums.total * per_request;
-    const int ctas = min(p.grid, places);
+    const int teams = min(p.teams, places);
     const int item = sums.before * per_request +
                      (h * p.blocks + r / kRows) * places_of(tl.units);
     const int u0 = item + kItemCost, u1 = u0 + tl.units - 1;
-    const int c0 = share_of(u0, ctas, places), c1 = share_of(u1, ctas, places);
+    const int c0 = share_of(u0, teams, places), c1 = share_of(u1, teams, places);
     // (a share that begins before the item holds a unit of another one first)
-    const bool at_start = share_start(c0, ctas, places) >= item;
+    const bool at_start = share_start(c0, teams, places) >= item;
     auto slot_of = [&](int c) {
       return (2 * c + (c == c0 && !at_start ? 1 : 0)) * kRows + r % kRows;
     };
@@ -1389,11 +1407,12 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   constexpr int kTile = kKeys * kRunsOf<k4, NT>;
   constexpr int handed = handed_bytes<D, k4, NT, kTwice>(), rings = ring_bytes<D, k4, NT>(),
                 inbox = inbox_bytes<D, NT, kTwice>();
-  constexpr int smem = handed + rings, smem_cluster = handed + std::max(rings, inbox);
+  constexpr int smem = smem_bytes<D, k4, NT, kTwice>(), kTeams = kTeamsOf<k4, NT>,
+                smem_cluster = handed + std::max(rings, inbox);
   const void* kernel =
       reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(kernel, smem_cluster, allowed);
+  cudaError_t e = allow_smem(kernel, std::max(kTeams * smem, smem_cluster), allowed);
   if (e != cudaSuccess) return e;
   p.blocks = (p.R + 8 * NT - 1) / (8 * NT);
   // most units that an item can have, by the table and the window
@@ -1402,19 +1421,23 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
     tiles = std::min(tiles, (1LL * p.left + p.T + kTile - 1) / kTile + 1 +
                                 (1LL * p.n_global + kTile - 1) / kTile);
   const long long units = (tiles + kWarps - 1) / kWarps, items = 1LL * p.B * p.Hkv * p.blocks;
-  const long long slots = 1LL * a.sm_count * kResident<NT, k4, kTwice>;
+  const long long slots = 1LL * a.sm_count * kTeams;
   // Clusters, where all of them run at once and a CTA has two units at most.
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < units) cluster *= 2;
-  constexpr int resident = std::min(kResident<NT, k4, kTwice>, kSmemPerSm / (smem_cluster + 1024));
+  constexpr int resident = std::min(kTeams, kSmemPerSm / (smem_cluster + 1024));
   if (units <= kClusterUnits * cluster && items * cluster <= 1LL * a.sm_count * resident) {
     p.cluster = cluster;
-    p.grid = int(items) * cluster;
-    return launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem_cluster, cluster, p,
+    p.teams = int(items) * cluster;
+    p.block_teams = 1;
+    return launch_dependent(kernel, dim3(unsigned(p.teams)), kThreads, smem_cluster, cluster, p,
                             a.stream);
   }
-  p.grid = int(std::min(items * (units + kItemCost), slots));
-  e = launch_dependent(kernel, dim3(unsigned(p.grid)), kThreads, smem, 1, p, a.stream);
+  // Blocks that fill an SM each, or of one team where those are fewer.
+  p.teams = int(std::min(items * (units + kItemCost), slots));
+  p.block_teams = p.teams == slots ? kTeams : 1;
+  e = launch_dependent(kernel, dim3(unsigned(p.teams / p.block_teams)),
+                       kThreads * p.block_teams, smem * p.block_teams, 1, p, a.stream);
   if (e != cudaSuccess) return e;
   // Few rows have many partial results each, over which a block's warps share.
   const int rows = p.Hkv * p.R;
@@ -1439,9 +1462,10 @@ template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams
 }  // namespace
 
 int window_partial_rows(int R, int sm_count) {
-  // two partial results of 8 or 16 rows per CTA
-  return R <= 8 ? sm_count * kResident<1, true, true> * 2 * 8
-                : sm_count * kResident<2, true, false> * 2 * 16;
+  // two partial results of 8 or 16 rows a team
+  static_assert(kTeamsOf<true, 1> >= kTeamsOf<false, 1> && kTeamsOf<true, 2> >= kTeamsOf<false, 2>,
+                "one size for both kinds of cache");
+  return R <= 8 ? sm_count * kTeamsOf<true, 1> * 2 * 8 : sm_count * kTeamsOf<true, 2> * 2 * 16;
 }
 
 cudaError_t launch_decode_window(const WindowArgs& a) {
