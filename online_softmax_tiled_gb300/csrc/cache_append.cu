@@ -106,52 +106,66 @@ ATTN_DEVINL float2 token_turn(const AppendParams<T>& p, const Token& t, int pair
   return x;
 }
 
-// The larger magnitude, NaN if either is not a number.
-ATTN_DEVINL float larger(float a, float b) {
+// The largest magnitude, NaN if any is not a number.
+ATTN_DEVINL float largest(float a, float b, float c) {
   float x;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(fabsf(a)), "f"(fabsf(b)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
   return x;
 }
 template <int V> ATTN_DEVINL float largest(const float (&y)[V]) {
-  float top = larger(y[0], y[1]);
+  float top = y[V - 1];
 #pragma unroll
-  for (int i = 2; i < V; ++i) top = larger(top, y[i]);
+  for (int i = 0; i + 1 < V; i += 2) top = largest(top, y[i], y[i + 1]);
   return top;
 }
 // The largest of four neighbouring lanes (or of two).
 template <int kLanes> ATTN_DEVINL float largest_of_lanes(float top) {
 #pragma unroll
-  for (int off = 1; off < kLanes; off *= 2)
-    top = larger(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int off = 1; off < kLanes; off *= 2) {
+    const float other = __shfl_xor_sync(0xffffffffu, top, off);
+    top = largest(top, other, other);
+  }
   return top;
 }
+// Quotients below are correctly rounded without a division: with r = 1 / s rounded
+// once and q = y·r, q + (y - q·s)·r rounds to y / s (Markstein 1990: the residual of a q
+// within an ulp is exact in an FMA), as long as reciprocal and residual stay normal
+// numbers. r itself comes from an approximation r0 within an ulp in the same way, r0 +
+// (1 - r0·s)·r0, which fails for no s but significands of all ones, which no bf16
+// value is.
+//
 // A group's scale from its largest magnitude.
 ATTN_DEVINL __nv_bfloat16 scale_of(float top) {
-  return __float2bfloat16_rn(top < INFINITY ? __fdiv_rn(top, 6.f) : __uint_as_float(0x7fffffffu));
+  constexpr float kSixth = 1.f / 6.f;
+  float q = top * kSixth;
+  q = fmaf(fmaf(-q, 6.f, top), kSixth, q);
+  if (top < 0x1p-90f) q = __fdiv_rn(top, 6.f);
+  return __float2bfloat16_rn(top < INFINITY ? q : __uint_as_float(0x7fffffffu));
 }
-// Codes of V elements (8), two a byte; zeros where the scale is 0 or not a number. The
-// quotients are correctly rounded: q = y·r with r = 1 / s rounded once, then
-// q + (y - q·s)·r (Markstein 1990: the residual of a q within an ulp is exact in an
-// FMA, and the corrected sum rounds to the quotient), for scales whose reciprocals
-// and residuals stay normal numbers; others divide.
+// Codes of V = 8 elements, two a byte; zeros where the scale is 0 or not a number.
 template <int V> ATTN_DEVINL uint32_t codes_of(const float (&y)[V], __nv_bfloat16 scale) {
   const float s = __bfloat162float(scale);
-  float q[V];
+  f2 q[V / 2];
   if (s >= 0x1p-90f && s <= 0x1p90f) {
-    const float r = __frcp_rn(s);
+    float r0;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(s));
+    const float r = fmaf(fmaf(-r0, s, 1.f), r0, r0);
+    const f2 rr{r, r}, ss{-s, -s};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float first = y[i] * r;
-      q[i] = fmaf(fmaf(-first, s, y[i]), r, first);
+    for (int i = 0; i < V / 2; ++i) {
+      const f2 x{y[2 * i], y[2 * i + 1]}, first = mul2(x, rr);
+      q[i] = fma2(fma2(first, ss, x), rr, first);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
+    for (int i = 0; i < V / 2; ++i)
+      q[i] = s > 0.f ? f2{__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)}
+                     : f2{0.f, 0.f};
   }
-  uint32_t x = 0;
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) x |= f32_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
-  return x;
+  if constexpr (V == 8)
+    return f32_to_e2m1x8(q);
+  else
+    return 0;
 }
 
 // The codes x0, x1 of a lane's two pieces (8 elements a word, of which the low
@@ -312,21 +326,29 @@ append_kernel(const __grid_constant__ AppendParams<T> p) {
             y1[j] = to_f32(x1[u].x[j]);
           }
           if (turn) {
+            // pair i: elements 2i, 2i + 1 of both pieces, or i of either; two at a time
+            auto first = [&](int i) -> float& {
+              return !kInterleaved ? y0[i] : i < V / 2 ? y0[2 * i % V] : y1[2 * i % V];
+            };
+            auto second = [&](int i) -> float& {
+              return !kInterleaved ? y1[i] : i < V / 2 ? y0[2 * i % V + 1] : y1[2 * i % V + 1];
+            };
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              // pair i: elements 2i, 2i + 1 of both pieces, or i of either
-              float& a = !kInterleaved ? y0[i] : i < V / 2 ? y0[2 * i % V] : y1[2 * i % V];
-              float& b = !kInterleaved ? y1[i] : i < V / 2 ? y0[2 * i % V + 1] : y1[2 * i % V + 1];
-              const float xa = a, xb = b;
-              a = fmaf(xa, cs[i], -xb * sn[i]);
-              b = fmaf(xb, cs[i], xa * sn[i]);
+            for (int i = 0; i < V; i += 2) {
+              const f2 a{first(i), first(i + 1)}, b{second(i), second(i + 1)}, c2{cs[i], cs[i + 1]},
+                  s2{sn[i], sn[i + 1]};
+              const f2 ya = fma2(a, c2, mul2(b, {-s2.x, -s2.y})), yb = fma2(b, c2, mul2(a, s2));
+              first(i) = ya.x;
+              first(i + 1) = ya.y;
+              second(i) = yb.x;
+              second(i + 1) = yb.y;
             }
           }
           if constexpr (kKind == kCoded) {
             const float top0 = largest(y0), top1 = largest(y1);
             __nv_bfloat16 s0, s1;
             if constexpr (kInterleaved) {
-              s0 = s1 = scale_of(largest_of_lanes<2>(larger(top0, top1)));
+              s0 = s1 = scale_of(largest_of_lanes<2>(largest(top0, top1, top1)));
             } else {
               s0 = scale_of(largest_of_lanes<4>(top0));
               s1 = scale_of(largest_of_lanes<4>(top1));
@@ -458,10 +480,9 @@ append_any_kernel(const __grid_constant__ AppendParams<T> p, int interleaved) {
 constexpr int kReadRows = 4;
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-read4_kernel(const uint8_t* __restrict__ k_codes, const __nv_bfloat16* __restrict__ k_scales,
-             const uint8_t* __restrict__ v_codes, const __nv_bfloat16* __restrict__ v_scales,
-             const int* __restrict__ table, const int* __restrict__ lens,
-             __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out, int Hkv,
+read4_kernel(const uint8_t* k_codes, const __nv_bfloat16* k_scales, const uint8_t* v_codes,
+             const __nv_bfloat16* v_scales, const int* table, const int* lens,
+             __nv_bfloat16* k_out, __nv_bfloat16* v_out, int Hkv,
              int num_pages, int page_size, int max_pages, int L) {
   constexpr int kRowsPerStep = kThreads / 4, kGroups = D / 32;
   using Codes = typename std::conditional<D == 128, uint4, uint2>::type;

@@ -25,12 +25,16 @@ template <int i> ATTN_DEVINL uint32_t e2m1x2_to_f16x2(uint32_t w) {
   return r;
 }
 
-// The codes nearest to a (low half) and b, ties to the even code, beyond 6
-// the code of 6.
-ATTN_DEVINL uint32_t f32_to_e2m1x2(float a, float b) {
+// The codes nearest to eight values, two a byte, the first in the low half; ties to
+// the even code, beyond 6 the code of 6.
+ATTN_DEVINL uint32_t f32_to_e2m1x8(const f2 (&x)[4]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\t"
-      "mov.b32 %0, {x, 0, 0, 0};\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\tmov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x),
+        "f"(x[3].y));
   return r;
 }
 
