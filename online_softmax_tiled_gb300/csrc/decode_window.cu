@@ -1045,7 +1045,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
           for (int tok = 0; tok < p.T; ++tok) {
             // keys 2t, 2t + 1, 2t + 8, 2t + 9 as masks of pairs, for this token
             const int top = tl.n - p.T + tok, key0 = kTile * tl.at(i);
-            const uint32_t there = kRuns ? 0xffffu : lds32(at + RingT::kInfo);
+            const uint32_t there = !kRuns ? lds32(at + RingT::kInfo) : what & kLacks ? 0u : 0xffffu;
             uint32_t keep[2] = {0u, 0u};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

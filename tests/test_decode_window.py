@@ -423,6 +423,34 @@ def test_bad_lengths_and_pages_are_flagged_not_read(ost, four):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("d,page,T", [(64, 16, 1), (128, 64, 4), (128, 24, 1)])
+def test_bad_pages_are_not_seen_whatever_page_0_holds(ost, four, d, page, T):
+    lens = [3 * page, 2 * page + 5]
+    c = Cache(four, lens, 2, d, page, T, -1, 0, 61)
+    c.pools = [torch.cat([torch.full_like(x[:1], float("nan") if x.is_floating_point() else 255), x])
+               for x in c.pools]
+    c.table = torch.where(c.table >= 0, c.table + 1, c.table).to(torch.int32)
+    q = random_like_shape((2, 4, T, d), BF, 62)
+    pools, table, n = c.to(DEV)
+    table[:, 1] = -1
+    f = ost.decode_cache4 if four else ost.decode_window
+    o, lse = f(q.to(DEV), *pools, table, n)
+    assert ost.attn_sync_status() == -7
+    for b, length in enumerate(lens):
+        k, v = (c.of_request(i, b, c.values(i)) for i in range(2))
+        keep = np.r_[0:page, 2 * page:length]
+        # (positions stay: every token sees the keys that are left, but those behind it)
+        for i in range(T):
+            seen = keep[keep <= length - T + i]
+            ro, rl, spread = oracle.decode_window(to_f64(q[b, :, i:i + 1]), k[:, seen], v[:, seen],
+                                                  d ** -0.5)
+            assert np.max(np.abs(to_f64(lse[b, :, i]) - rl[:, 0])) <= 2.0 ** -11
+            assert np.all(np.abs(to_f64(o[b, :, i]) - ro[:, 0])
+                          <= 2.0 ** -8 * np.abs(ro[:, 0]) + 2.0 ** -9.4 * spread[:, 0])
+
+
+@pytest.mark.gpu
 def test_agrees_with_paged_decode(ost):
     lens, Hq, Hkv, d, page = [700, 1, 33, 2000], 8, 2, 128, 16
     c = Cache(False, lens, Hkv, d, page, 1, -1, 0, 61)
