@@ -569,9 +569,9 @@ ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float*
  * token falls into are not read. Nothing that is written may overlap what is read
  * or written elsewhere (checked); two new tokens that block_table sends to one row
  * leave either of them there.
- * Rows at multiples of 16 bytes with rot_dim a multiple of 16 (interleaved: 8)
- * move in 16-byte pieces; everything else element by element. q, q_out, k, v need
- * their element's alignment only. B * N at most 2^31 - 256, page_size *
+ * Rows at multiples of 16 bytes with rot_dim a multiple of 16 move in 16-byte
+ * pieces; everything else element by element. q, q_out, k, v need their element's
+ * alignment only. B * N at most 2^31 - 256, Hq + 2 Hkv at most 262140, page_size *
  * max_pages_per_seq at most 2^30, fewer than 2^32 rows in a pool.
  * Device-side checks: a request with seq_lens outside [0, capacity] or new_lens
  * outside [0, min(N, n)] has no tokens; a token behind a page index outside [0,
@@ -685,10 +685,11 @@ ATTN_API attn_status attn_decode_window(const void* q, const void* k_pages, cons
  * attn_decode_window over a cache held in 4 bits (attn_cache_append4), with the
  * same workspace. Attention over the values code * scale: the products with
  * codes are exact, a group's scale multiplies their sum in float32 (K) or the
- * probability (V), which then enters the product in float16 (2^-12 of it is
- * lost; scales of V from 2^-60 to 2^90 of any size keep this). A group whose scale
- * is not finite spoils its own elements of V, and the key that it belongs to in K,
- * for the tokens that see it.
+ * probability (V), which then enters the product in float16: off by 2^-12 of it,
+ * and by 2^-31 of the largest scale of V that the row's keys have (scales from
+ * 2^-60 to 2^90; scales of K below 2^110). A group whose scale is not finite
+ * spoils its own elements of V, and the key that it belongs to in K, for the tokens
+ * that see it.
  */
 ATTN_API attn_status attn_decode_cache4(const void* q, const void* k_codes, const void* k_scales,
                                         const void* v_codes, const void* v_scales,

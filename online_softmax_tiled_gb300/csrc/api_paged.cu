@@ -60,7 +60,7 @@ attn_status append_common(AppendArgs a, const attn_strides* q_strides,
   if (a.interleaved != 0 && a.interleaved != 1) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(a.magnitude) || a.pos_stride < 0) return ATTN_ERR_INVALID_ARG;
   if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
-  // tokens and heads are numbered in 32 bits; grid y carries at least 4 heads a block
+  // tokens and heads are numbered in 32 bits
   if (1LL * a.B * a.N > (1LL << 31) - 256 || 1LL * a.Hq + 2LL * a.Hkv > 4 * 65535LL ||
       !pages_supported(a.Hkv, a.num_pages, a.page_size, a.max_pages))
     return ATTN_ERR_UNSUPPORTED;

@@ -357,6 +357,45 @@ def test_every_border_between_codes(ost, d):
 
 
 @pytest.mark.gpu
+def test_quotients_are_those_of_ieee_divisions(ost):
+    """Every significand of a scale, at several exponents, with elements within two
+    float32 steps of every border times the scale: the codes of the float32 quotients,
+    correctly rounded (numpy's)."""
+    marks = np.float32([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    levels = np.array(oracle.LEVELS)
+    rows, scales = [], []
+    for e in (-89, -30, 0, 3, 88):
+        for m in range(128):
+            s = np.float32((1 + m / 128) * 2.0 ** e)
+            y = marks * s
+            near = np.concatenate([y] + [y := np.nextafter(y, np.float32(np.inf) * d)
+                                         for d in (1, 1, -1, -1, -1, -1)])[7:]
+            near = np.concatenate([near, y]).astype(np.float32)          # 42 and 7
+            for at in (near[:31], np.concatenate([near[31:], -near[:13]])):
+                rows.append(np.concatenate([at[:31], [6 * s]]).astype(np.float32))
+                scales.append(s)
+    x, s = np.stack(rows), np.float32(scales)
+    x = x[:x.shape[0] // 4 * 4].reshape(1, 1, -1, 128)
+    s = s[:x.shape[2] * 4].reshape(-1, 4)
+    v = torch.from_numpy(x).to(DEV)
+    n = x.shape[2]
+    pools = [t for i in range(2) for t in (_pool((1, 1, n, 64), torch.uint8, i),
+                                           _pool((1, 1, n, 4), BF, 9 + i))]
+    ost.cache_append4(None, v, v, *pools, _ints([[0]]), _ints([n]))
+    q = x[0, 0] / np.repeat(s, 32, -1)
+    assert q.dtype == np.float32
+    mids = (levels[1:] + levels[:-1]) / 2
+    a = np.abs(q).astype(np.float64)
+    at = np.searchsorted(mids, a, side="left")                    # ties to the lower code,
+    at += (at < 7) & (a == mids[np.minimum(at, 6)]) & (at % 2 == 1)   # or the even one above
+    want = np.sign(q) * levels[at] * np.repeat(s.astype(np.float64), 32, -1)
+    for c, sc in (pools[:2], pools[2:]):
+        assert np.array_equal(to_f64(sc)[0, 0], s)
+        got = oracle.values4(oracle.unpack4(c.cpu().numpy()[0, 0]), to_f64(sc)[0, 0])
+        assert np.array_equal(got, want)
+
+
+@pytest.mark.gpu
 def test_values_that_are_not_finite_spoil_their_group_alone(ost):
     v = random_like_shape((1, 1, 4, 128), BF, 3).to(DEV)
     v[0, 0, 0, 5], v[0, 0, 1, 40], v[0, 0, 2, 127] = float("nan"), float("inf"), -float("inf")
