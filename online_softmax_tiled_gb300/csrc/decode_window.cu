@@ -19,23 +19,32 @@
 // bf16. P enters P·V as two bf16 parts (2^-17 of a probability is lost at most).
 //
 // Work. Memory bound: 4·D bytes of K and V per key and KV head (4 bits: 9/8·D),
-// 4·D flops per (query row, key). A warp takes 16 keys a step. Sᵀ = K Qᵀ has the
-// keys as rows of the fragments, so that 8 query rows (the heads of a group times
-// the tokens) fill an instruction; P moves into the fragments of Oᵀ = Vᵀ Pᵀ by
-// transposes of 8 x 8 within the warp. K and V fragments of a 4-bit row are built
-// in registers straight from its bytes (fp4.cuh), at one conversion for two
+// 4·D flops per (query row, key). A warp takes 16 keys a step (4 bits, up to 8 rows:
+// 32). Sᵀ = K Qᵀ has the keys as rows of the fragments, so that 8 query rows (the heads
+// of a group times the tokens) fill an instruction; P moves into the fragments of Oᵀ =
+// Vᵀ Pᵀ by transposes of 8 x 8 within the warp. K and V fragments of a 4-bit row are
+// built in registers straight from its bytes (fp4.cuh), at one conversion for two
 // values; the tensor instructions are those that take both operands from
 // registers, since values unpacked for the ones that read shared memory would be
 // written there at four times their size.
 //
-// Order. All visible keys of all requests and KV heads, in tiles of 16 of which
-// four make a unit, are laid end to end and cut into equal shares, one per CTA
-// (lengths are read on the device). A CTA whose share begins or ends inside a
-// (request, head) leaves a partial result there, two at most; a dependent launch
+// Order. All visible keys of all requests and KV heads, in tiles of 16 or 32 of which
+// four make a unit, are laid end to end and cut into equal shares, one per team of
+// four warps (lengths are read on the device). A team whose share begins or ends inside
+// a (request, head) leaves a partial result there, two at most; a dependent launch
 // joins them. Calls of so few and short items that the CTAs of one cluster cover
 // each one run as clusters instead, which join through distributed shared memory:
-// one launch, and no sums over the lengths before it starts. Each warp copies its own tiles into a ring of its own, kStages - 1
-// ahead, with no barrier of the CTA until the end of a run.
+// one launch, and no sums over the lengths before it starts. Each warp copies its own
+// tiles into a ring of its own, kStages - 1 ahead and across requests, with no barrier
+// until the end of a run.
+//
+// Measured (GB300; Hq 32, Hkv 8, D 128, 16-key pages; of a plain copy's 6.7 TB/s):
+// bf16, 64 requests behind a window of 1024, 53 us (0.76), 32 requests of 4 tokens behind
+// 4096, 98 us (0.82); 4 bits, 64 requests of mean 4096 keys, 57-60 us (0.75), two of
+// 131072, 46 us (0.72). About 6 us of each are a chain of latencies: the call before,
+// lengths, shares, tables, first copies, the join. Copies alone, nothing computed, take 3
+// us less. bf16 shares end 71 to 97 us after the start by the part of the chip that an SM
+// is in, the same SMs in every run.
 
 #include <cooperative_groups.h>
 
@@ -56,7 +65,8 @@ ATTN_DEFINE_ERROR_WORD(take_error_decode_window)
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kMaxCluster = 8, kSmemPerSm = 228 * 1024;
-// Keys of a fragment, and runs of them in a step of a warp.
+// Keys of a fragment, and runs of them in a step of a warp. (One run a step in 4 bits: 71
+// us where two take 63, with blocks of one team.)
 constexpr int kKeys = 16;
 template <bool k4, int NT> constexpr int kRunsOf = k4 && NT == 1 ? 2 : 1;
 
@@ -104,7 +114,8 @@ template <int kTile> ATTN_DEVINL Tiles tiles_of(const WindowParams& p, int n) {
 }
 
 // Work is divided by cost: every run of units of one (request, KV head, block of
-// rows) counts as kItemCost units more, for its queries, its start and its end.
+// rows) counts as kItemCost units more, for its queries, its start and its end. (4 bits,
+// 64 requests of mean 4096 keys: 67.4 us at 0, 60.5 at 1, 57.4 at 2, 58.0 at 4.)
 // The places of an item are its kItemCost first ones, then one per unit.
 constexpr int kItemCost = 2;
 ATTN_DEVINL int places_of(int units) { return units > 0 ? units + kItemCost : 0; }
@@ -354,7 +365,9 @@ template <int D, bool k4, int kRun> struct Ring {
   static ATTN_DEVINL int v_scale_at(int r) { return k_scale_at(r) + kKeys * kScales; }
 };
 
-// CTAs per SM the registers are cut for.
+// Teams of a block, which has an SM to itself: as many as registers (4 bits) or rings
+// (bf16) leave room for. Blocks of one team start one after the other: 62.3 us for the 64
+// requests in 4 bits where blocks of four take 57.9; bf16 alike.
 template <bool k4, int NT> constexpr int kTeamsOf = k4 ? (NT == 1 ? 4 : 3) : 2;
 
 // Blocks of 16 elements whose sums the warps hand one another at a time, each as
@@ -384,13 +397,15 @@ constexpr int inbox_bytes() {
 // kLacks << r: run r of its keys is not there.
 enum : uint32_t { kNone = 0, kFull = 1, kPart = 2, kLacks = 4 };
 
-// NT blocks of 8 query rows at a time. kRuns: pages hold whole tiles (page_size
-// a multiple of 16), so a tile's rows are adjacent: one table entry and one
-// address instead of one per row. kTwice (4 bits, up to 4 query rows): the
-// fragments' columns 4 .. 7 hold the rows a second time and take the odd groups of
-// 32 elements, columns 0 .. 3 the even ones, so that a lane scales half as many sums
-// and probabilities (the unscaled halves of columns come out of the products
-// too, and are not read).
+// NT blocks of 8 query rows at a time (two beyond 8 rows: one would read the keys twice as
+// often). kRuns: pages hold whole runs (page_size a multiple of 16), so a run's rows
+// are adjacent: one table entry and one address instead of one per row (as per row: 78 us
+// where 64 requests behind 1024 keys take 53, 68 where 64 of mean 4096 in 4 bits take
+// 57). kTwice (4 bits, up to 4 query rows): the fragments' columns 4 .. 7 hold the rows
+// a second time and take the odd groups of 32 elements, columns 0 .. 3 the even
+// ones, so that a lane scales half as many sums and probabilities; the unscaled
+// halves of columns come out of the products too, and are not read (without it 59.8 us
+// instead of 57.4, for two requests of 131072 keys 48.1 instead of 45.8).
 template <int D, bool k4, int NT, bool kRuns, bool kTwice>
 __global__ void __launch_bounds__(kThreads * kTeamsOf<k4, NT>, 1)
 window_kernel(const __grid_constant__ WindowParams p) {
@@ -1255,6 +1270,9 @@ window_kernel(const __grid_constant__ WindowParams p) {
 // writes those of requests without keys. kPer warps a row; grid: x over groups of
 // kJoinWarps / kPer of the Hkv·R rows of request y. Partial results are fetched
 // eight at a time.
+// Up to kFewRows rows have many partial results each, over which a block's warps share
+// (two requests of 131072 keys, 64 rows: 60 us with a warp a row, 46 with eight); more rows
+// fill the SMs a warp each (2048 rows: 59 us with eight warps a row, 53 with one).
 constexpr int kJoinWarps = 8, kFewRows = 1024, kClusterUnits = 2;
 template <int D, int kRows, int kPer, int kTile>
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -1422,7 +1440,9 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
                                 (1LL * p.n_global + kTile - 1) / kTile);
   const long long units = (tiles + kWarps - 1) / kWarps, items = 1LL * p.B * p.Hkv * p.blocks;
   const long long slots = 1LL * a.sm_count * kTeams;
-  // Clusters, where all of them run at once and a CTA has two units at most.
+  // Clusters, where all of them run at once and a CTA has kClusterUnits at most. (Against
+  // shares with a join, 8 items: one unit a CTA 6.0 and 6.9 us in 4 bits, 6.1 and 7.0 in
+  // bf16; two 6.9 and 7.6, 6.5 and 7.4; four 8.5 and 8.2, 7.7 and 8.3.)
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < units) cluster *= 2;
   constexpr int resident = std::min(kTeams, kSmemPerSm / (smem_cluster + 1024));
@@ -1439,7 +1459,6 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   e = launch_dependent(kernel, dim3(unsigned(p.teams / p.block_teams)),
                        kThreads * p.block_teams, smem * p.block_teams, 1, p, a.stream);
   if (e != cudaSuccess) return e;
-  // Few rows have many partial results each, over which a block's warps share.
   const int rows = p.Hkv * p.R;
   if (1LL * p.B * rows <= kFewRows)
     return launch_dependent(
