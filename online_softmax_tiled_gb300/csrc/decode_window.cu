@@ -19,8 +19,7 @@
 // bf16. P enters P·V as two bf16 parts (2^-17 of a probability is lost at most).
 //
 // Work. Memory bound: 4·D bytes of K and V per key and KV head (4 bits: 9/8·D),
-// 4·D flops per (query row, key). A warp takes 16 keys a step (4 bits, up to 8 rows:
-// 32). Sᵀ = K Qᵀ has the keys as rows of the fragments, so that 8 query rows (the heads
+// 4·D flops per (query row, key). A warp takes 16 keys a step (4 bits: 32). Sᵀ = K Qᵀ has the keys as rows of the fragments, so that 8 query rows (the heads
 // of a group times the tokens) fill an instruction; P moves into the fragments of Oᵀ =
 // Vᵀ Pᵀ by transposes of 8 x 8 within the warp. K and V fragments of a 4-bit row are
 // built in registers straight from its bytes (fp4.cuh), at one conversion for two
@@ -64,11 +63,11 @@ ATTN_DEFINE_ERROR_WORD(take_error_decode_window)
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kMaxCluster = 8, kSmemPerSm = 228 * 1024;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kMaxCluster = 8, kMaxTeams = 4, kSmemPerSm = 228 * 1024;
 // Keys of a fragment, and runs of them in a step of a warp. (One run a step in 4 bits: 71
-// us where two take 63, with blocks of one team.)
+// us where two take 63, with blocks of one team; at 16 rows 116 and 98.)
 constexpr int kKeys = 16;
-template <bool k4, int NT> constexpr int kRunsOf = k4 && NT == 1 ? 2 : 1;
+template <bool k4> constexpr int kRunsOf = k4 ? 2 : 1;
 
 struct WindowParams {
   const __nv_bfloat16* q;
@@ -367,8 +366,10 @@ template <int D, bool k4, int kRun> struct Ring {
 
 // Teams of a block, which has an SM to itself: as many as registers (4 bits) or rings
 // (bf16) leave room for. Blocks of one team start one after the other: 62.3 us for the 64
-// requests in 4 bits where blocks of four take 57.9; bf16 alike.
-template <bool k4, int NT> constexpr int kTeamsOf = k4 ? (NT == 1 ? 4 : 3) : 2;
+// requests in 4 bits where blocks of four take 57.9; bf16 alike. In 4 bits at 16 rows two
+// teams of D = 128 spill nothing (98 us; three 111); of D = 64, four take 57 us, three 61.
+template <int D, bool k4, int NT>
+constexpr int kTeamsOf = k4 && (D == 64 || NT == 1) ? 4 : 2;
 
 // Blocks of 16 elements whose sums the warps hand one another at a time, each as
 // [32 lanes] of four floats a warp and block of 8 rows: all of them, or as many as
@@ -381,7 +382,7 @@ constexpr int handed_bytes() {                    // (m, l) too
   return kAtOnce<D, k4, NT, kTwice> * NT * kWarps * 512 + kWarps * 8 * NT * 8;
 }
 template <int D, bool k4, int NT>
-constexpr int ring_bytes() { return kWarps * Ring<D, k4, kRunsOf<k4, NT>>::kBytes; }
+constexpr int ring_bytes() { return kWarps * Ring<D, k4, kRunsOf<k4>>::kBytes; }
 template <int D, bool k4, int NT, bool kTwice>
 constexpr int smem_bytes() {
   return (handed_bytes<D, k4, NT, kTwice>() + ring_bytes<D, k4, NT>() + 127) / 128 * 128;
@@ -407,9 +408,9 @@ enum : uint32_t { kNone = 0, kFull = 1, kPart = 2, kLacks = 4 };
 // halves of columns come out of the products too, and are not read (without it 59.8 us
 // instead of 57.4, for two requests of 131072 keys 48.1 instead of 45.8).
 template <int D, bool k4, int NT, bool kRuns, bool kTwice>
-__global__ void __launch_bounds__(kThreads * kTeamsOf<k4, NT>, 1)
+__global__ void __launch_bounds__(kThreads * kTeamsOf<D, k4, NT>, 1)
 window_kernel(const __grid_constant__ WindowParams p) {
-  constexpr int kRun = kRunsOf<k4, NT>, kTile = kRun * kKeys;
+  constexpr int kRun = kRunsOf<k4>, kTile = kRun * kKeys;
   using RingT = Ring<D, k4, kRun>;
   constexpr int kStages = RingT::kStages, kRows = 8 * NT, kGroups = D / 32;
   // blocks of 16 elements of a row's sums (kTwice: even and odd groups share theirs)
@@ -419,7 +420,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kRowMask = kTwice ? 3 : 15;       // of a column's query row
   extern __shared__ __align__(128) uint8_t block_smem[];
   // (uniform, and known to be)
-  constexpr int kTeams = kTeamsOf<k4, NT>;
+  constexpr int kTeams = kTeamsOf<D, k4, NT>;
   const int warp_ = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
   const int warp = warp_ % kWarps, in_block = warp_ / kWarps;
   const int team = int(blockIdx.x) * p.block_teams + in_block;
@@ -1422,11 +1423,12 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 
 template <int D, bool k4, int NT, bool kRuns, bool kTwice = false>
 cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
-  constexpr int kTile = kKeys * kRunsOf<k4, NT>;
+  constexpr int kTile = kKeys * kRunsOf<k4>;
   constexpr int handed = handed_bytes<D, k4, NT, kTwice>(), rings = ring_bytes<D, k4, NT>(),
                 inbox = inbox_bytes<D, NT, kTwice>();
-  constexpr int smem = smem_bytes<D, k4, NT, kTwice>(), kTeams = kTeamsOf<k4, NT>,
+  constexpr int smem = smem_bytes<D, k4, NT, kTwice>(), kTeams = kTeamsOf<D, k4, NT>,
                 smem_cluster = handed + std::max(rings, inbox);
+  static_assert(kTeams <= kMaxTeams, "partial results of all teams have room");
   const void* kernel =
       reinterpret_cast<const void*>(window_kernel<D, k4, NT, kRuns, kTwice>);
   static std::atomic<uint64_t> allowed{0};
@@ -1482,9 +1484,7 @@ template <int D, bool k4> cudaError_t launch_d(const WindowArgs& a, WindowParams
 
 int window_partial_rows(int R, int sm_count) {
   // two partial results of 8 or 16 rows a team
-  static_assert(kTeamsOf<true, 1> >= kTeamsOf<false, 1> && kTeamsOf<true, 2> >= kTeamsOf<false, 2>,
-                "one size for both kinds of cache");
-  return R <= 8 ? sm_count * kTeamsOf<true, 1> * 2 * 8 : sm_count * kTeamsOf<true, 2> * 2 * 16;
+  return sm_count * kMaxTeams * 2 * (R <= 8 ? 8 : 16);
 }
 
 cudaError_t launch_decode_window(const WindowArgs& a) {
