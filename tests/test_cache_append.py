@@ -216,6 +216,15 @@ CASES = [
     (1, 33, 7, 300, 64, 64, False, BF, 48, [11], None, True, 0),
     (5, 0, 4, 3, 128, 128, False, BF, 16, [0, 1, 2, 3, 4], [3, 0, 1, 2, 3], False, 0),
 ]
+# as many tokens as fill the SMs without warps that share theirs, in 4 bits 8 and 16
+# heads a thread
+LARGE = [
+    (2, 44, 2, 3400, 128, 128, False, BF, 16, [5, 0], [3400, 3111], True, 0),
+    (1, 44, 2, 3300, 128, 64, True, BF, 48, [700], None, True, 0),
+    (4, 44, 2, 3300, 64, 64, False, BF, 16, [0, 1, 2, 3], [3300, 0, 17, 3300], True, 0),
+    (2, 45, 3, 3300, 64, 32, True, F32, 24, [9, 100], None, False, 0),
+    (2, 43, 2, 1700, 128, 128, False, F32, 16, [0, 30], None, True, 0),
+]
 
 
 def _setup(case, seed):
@@ -238,7 +247,7 @@ def _turn(ost, x, pos, w, inter, mag):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("given", [False, True])
-@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("case", CASES + LARGE)
 def test_rows_are_those_of_rope(ost, case, given):
     """Keys bit for bit attn_rope's, values as they are, everything else untouched."""
     B, Hq, Hkv, N, d, rot, inter, dt, page, old, new, fused, shift = case
@@ -268,7 +277,7 @@ def test_rows_are_those_of_rope(ost, case, given):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("case", CASES + LARGE)
 def test_rows_in_four_bits(ost, case):
     """Scales and codes equal those worked out from attn_rope's float32 keys in
     float32 divisions; what they stand for is as near as 4 bits allow, and is read
