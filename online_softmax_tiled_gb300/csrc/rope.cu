@@ -120,8 +120,9 @@ rope_kernel(RopeTensor<T> tq, RopeTensor<T> tk, const int* __restrict__ position
     const long long p = positions[b * pos_stride + n];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      turn_cos_sin(p, inv_freq[chunk * V + i], magnitude, cs[i], sn[i]);
-      if (inverse) sn[i] = -sn[i];
+      float s;
+      turn_cos_sin(p, inv_freq[chunk * V + i], magnitude, cs[i], s);
+      sn[i] = inverse ? -s : s;
     }
   }
   for (int h = h0; h < h1; h += U) {

@@ -41,13 +41,14 @@ ATTN_DEVINL void turn_cos_sin(long long p, double w, float magnitude, float& c, 
   // the angle as a fraction of a turn: its top 32 bits, rounded, are off
   // by 2^-33 turns at most, and rounded to float32 once more
   const uint64_t t = uint64_t(p) * turns_of(w) + 0x80000000ull;
-  sincospif(float(int(uint32_t(t >> 32))) * 0x1p-31f, &s, &c);
+  float sine, cosine;
+  sincospif(float(int(uint32_t(t >> 32))) * 0x1p-31f, &sine, &cosine);
   // a frequency that is not finite, or of 2^64 and more, gives NaN, not a
   // wrong angle (its exponent tells; comparing float64 values is slow here)
   const bool good = ((uint64_t(__double_as_longlong(w)) >> 52) & 0x7ff) < 1023 + 64;
   const float m = good ? magnitude : __int_as_float(0x7fffffff);
-  c *= m;
-  s *= m;
+  c = cosine * m;
+  s = sine * m;
 }
 
 }  // namespace attn
