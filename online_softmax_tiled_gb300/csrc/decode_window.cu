@@ -14,7 +14,7 @@
 // added in float32. For V the scale differs per key, the index summed over:
 // P·scale_c is what enters the product, in float16 (2^-12 of a probability; bf16
 // would lose 2^-9) times a power of two f that follows the largest scale seen,
-// so that it stays between 2^-24 and 2^15.
+// so that it stays between 2^-24 and 2^15: the largest that the row itself has seen.
 //
 // bf16. P enters P·V as two bf16 parts (2^-17 of a probability is lost at most).
 //
@@ -712,10 +712,15 @@ window_kernel(const __grid_constant__ WindowParams p) {
       for (int j = 0; j < 2; ++j) last[nt][j] = tl.n - p.T + (r0 + ((8 * nt + 2 * t + j) & kRowMask)) % p.T;
 
     // m: row maxima, in log2 units, as of the last time that one was passed by 8;
-    // limit: 8 above them, as raw sums. Sums are of 2^(s - m + e_f).
+    // limit: 8 above them, as raw sums. Sums are of 2^(s - m + e), e of a column's own:
+    // what one token sees and another does not (a key after it, or one that has left
+    // its window) may be 2^150 times as large. e is in [-84, 66], the columns' e four
+    // bytes of a register; v_limit: the scale of V that the largest of them allows. (With
+    // one e for all columns 64.0 us instead of 64.5 at 8 rows, 108.8 instead of 110 at 16,
+    // 41.9 instead of 43.5 at 16 behind a window of 1024.)
     float o[kM][NT][4], m[NT][2], limit[NT][2], minus_ref[NT][2], l[NT][2], v_limit = 128.f;
-    int e_f = 0;
-    bool fresh = true;                            // e_f is of no tile yet
+    uint32_t e_packed = 0;
+    auto e_of = [&](int nt, int j) { return int(int8_t(e_packed >> (8 * (2 * nt + j)))); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -860,25 +865,15 @@ window_kernel(const __grid_constant__ WindowParams p) {
               if ((hidden[nt][j] >> (16 * r + g + 8)) & 1u) s[r][nt][j + 2] = -INFINITY;
             }
           }
-        if constexpr (k4) {                       // what no token sees has no say in e_f
-          const uint32_t any = there & (~below(tl.lo - key0) | first);
-#pragma unroll
-          for (int r = 0; r < kRun; ++r)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (!((any >> (16 * r + g + 8 * j)) & 1u))
-#pragma unroll
-                for (int c = 0; c < kOwn; ++c) vs[r][j][c] = 0.f;
-        }
       }
       // whether a score passes its row's maximum so far by 8 binary orders, or a
-      // scale of V the power of two that P is taken with by 2^7
+      // scale of V, seen or not, the power of two that P is taken with by 2^7
       auto top_score = [&](int nt, int j) {
         float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
         if constexpr (kRun == 2) x = max3(x, s[kRun - 1][nt][j], s[kRun - 1][nt][j + 2]);
         return x;
       };
-      bool above = false;
+      bool above = false, scales = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -889,40 +884,71 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int r = 0; r < kRun; ++r)
 #pragma unroll
           for (int c = 0; c < kOwn; ++c) vmax = max3(vmax, vs[r][0][c], vs[r][1][c]);
-        above |= vmax > v_limit;
+        scales = vmax > v_limit;
       }
-      if (__any_sync(0xffffffffu, above)) {
+      if (__any_sync(0xffffffffu, above || scales)) {
         // the references move: everything so far is rescaled
-        int e_new = e_f;
         if constexpr (k4) {
-          // (a scale that is not finite counts for nothing: its group alone is lost)
-          uint32_t top = 0;
+          // (a row that has seen nothing has no sums yet, and takes any e)
 #pragma unroll
-          for (int r = 0; r < kRun; ++r)
+          for (int nt = 0; nt < NT; ++nt) scales |= m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
+          if (__any_sync(0xffffffffu, scales)) {
+            // Of a key of the lane its largest scale, as bits. (One that is not finite
+            // counts for nothing: its group alone is lost.)
+            uint32_t top[kRun][2];
 #pragma unroll
-            for (int c = 0; c < kOwn; ++c)
+            for (int r = 0; r < kRun; ++r)
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (vs[r][j][c] < INFINITY)
-                  top = max(top, __float_as_uint(fmaxf(vs[r][j][c], 0.f)));
-          top = __reduce_max_sync(0xffffffffu, top);
-          const int want = 6 - min(max(int(top >> 23) - 127, -60), 90);
-          if (fresh || want < e_f) e_new = want;
-          fresh = false;
-          v_limit = pow2i(7 - e_new);
+              for (int y = 0; y < 2; ++y) {
+                top[r][y] = 0;
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c)
+                  if (vs[r][y][c] < INFINITY)
+                    top[r][y] = max(top[r][y], __float_as_uint(fmaxf(vs[r][y][c], 0.f)));
+              }
+            uint32_t all = 0;                     // full: of all keys
+            if (full) {
+#pragma unroll
+              for (int r = 0; r < kRun; ++r) all = max(all, max(top[r][0], top[r][1]));
+              all = __reduce_max_sync(0xffffffffu, all);
+            }
+            int e_top = -128;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t x = all;
+                if (!full) {                      // of those that the column's row sees
+#pragma unroll
+                  for (int r = 0; r < kRun; ++r)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                      if (!((hidden[nt][j] >> (16 * r + g + 8 * y)) & 1u)) x = max(x, top[r][y]);
+                  // (the lanes of one t; kTwice: and the lane with the row's other groups)
+#pragma unroll
+                  for (int off = kTwice ? 2 : 4; off < 32; off *= 2)
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
+                }
+                const int want = 6 - min(max(int(x >> 23) - 127, -60), 90), e = e_of(nt, j);
+                const int e_new = m[nt][j] == -INFINITY || want < e ? want : e;
+                const int at_bit = 8 * (2 * nt + j);
+                e_packed = (e_packed & ~(0xffu << at_bit)) | uint32_t(e_new & 0xff) << at_bit;
+                e_top = max(e_top, e_new);
+              }
+            v_limit = pow2i(7 - e_top);
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float to = fmaxf(m[nt][j], max_over_keys(top_score(nt, j)) * to_log2[nt][j]);
+            const float ref = to == -INFINITY ? 0.f : float(e_of(nt, j)) - to;
             // (nothing seen yet: sums of zeros, whatever they are scaled by)
-            const float by = to == -INFINITY ? 1.f
-                             : to == m[nt][j] && e_new == e_f
-                                 ? 1.f : fast_exp2(m[nt][j] - to + float(e_new - e_f));
+            const float by = m[nt][j] == -INFINITY ? 1.f : fast_exp2(ref - minus_ref[nt][j]);
             m[nt][j] = to;
             limit[nt][j] = to == -INFINITY ? -INFINITY : (to + 8.f) / to_log2[nt][j];
-            minus_ref[nt][j] = to == -INFINITY ? 0.f : float(e_new) - to;
+            minus_ref[nt][j] = ref;
             l[nt][j] *= by;
 #pragma unroll
             for (int mt = 0; mt < kM; ++mt) {
@@ -930,7 +956,6 @@ window_kernel(const __grid_constant__ WindowParams p) {
               o[mt][nt][j + 2] *= by;
             }
           }
-        e_f = e_new;
       }
 #pragma unroll
       for (int r = 0; r < kRun; ++r)
@@ -1106,7 +1131,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         l[nt][j] = sum_over_keys(l[nt][j]);
-        m[nt][j] -= float(e_f);                   // (-inf stays)
+        m[nt][j] -= float(e_of(nt, j));           // (-inf stays)
         if (g == 0)
           handed_ml[warp * kRows + 8 * nt + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
       }
