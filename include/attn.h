@@ -660,9 +660,11 @@ ATTN_API attn_status attn_cache_read4(const void* k_codes, const void* k_scales,
  * window may have been given back). Any page_size >= 1, any Hq that is a multiple
  * of Hkv, d 64 or 128, scale positive and finite, n_global >= 0. Keys are read
  * once for every 8 query rows per KV head while Hq / Hkv * T <= 8, for every 16
- * beyond. The probabilities enter the P·V product as two bf16 parts (2^-17 of one
- * is lost at most); all softmax state is float32, and results do not depend on
- * the order in which anything runs.
+ * beyond. The probabilities enter the P·V product as two bf16 parts (off by 2^-16
+ * of one at most); all softmax state is float32, and results do not depend on
+ * the order in which anything runs. An infinite value that a token sees makes its
+ * element of O infinite (NaN where the token sees both infinities, or the key's
+ * probability is below 2^-100 of the row's largest).
  * Device-side checks: a length outside [0, capacity] counts as 0; keys behind a
  * page index outside [0, num_pages) are not seen; attn_sync_status() reports
  * ATTN_ERR_DEVICE_INDEX for both.

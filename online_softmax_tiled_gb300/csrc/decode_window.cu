@@ -16,7 +16,7 @@
 // would lose 2^-9) times a power of two f that follows the largest scale seen,
 // so that it stays between 2^-24 and 2^15: the largest that the row itself has seen.
 //
-// bf16. P enters P·V as two bf16 parts (2^-17 of a probability is lost at most).
+// bf16. P enters P·V as two bf16 parts (off by 2^-16 of a probability at most).
 //
 // Work. Memory bound: 4·D bytes of K and V per key and KV head (4 bits: 9/8·D),
 // 4·D flops per (query row, key). A warp takes 16 keys a step (4 bits: 32). Sᵀ = K Qᵀ has the keys as rows of the fragments, so that 8 query rows (the heads
@@ -281,6 +281,12 @@ ATTN_DEVINL void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
 ATTN_DEVINL uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two floats as bf16, rounded towards zero; `lo` goes to the low half.
+ATTN_DEVINL uint32_t cut_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 template <int kBytes> ATTN_DEVINL void copy_async(uint32_t dst, const void* src) {
@@ -1049,10 +1055,12 @@ window_kernel(const __grid_constant__ WindowParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float a = s[0][nt][2 * j], z = s[0][nt][2 * j + 1];
-            const uint32_t x = pack_bf16x2(a, z);
+            // The first part is cut off, and the rest gets 2^-23 of P besides, so that both
+            // are above 0 wherever P is: an infinite value keeps its sign in their sum.
+            const float a = s[0][nt][2 * j], z = s[0][nt][2 * j + 1], up = 1.f + 0x1p-23f;
+            const uint32_t x = cut_bf16x2(a, z);
             hi[nt][j] = transpose8x8(x);
-            lo[nt][j] = transpose8x8(pack_bf16x2(a - bf16lo(x), z - bf16hi(x)));
+            lo[nt][j] = transpose8x8(pack_bf16x2(fmaf(a, up, -bf16lo(x)), fmaf(z, up, -bf16hi(x))));
           }
         // Keys that a token does not see may hold values that are not finite, which
         // would reach its rows through the product (0 · inf): then the tokens'
