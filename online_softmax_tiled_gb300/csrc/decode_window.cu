@@ -841,13 +841,12 @@ window_kernel(const __grid_constant__ WindowParams p) {
         }
       }
 
-      uint32_t hidden[NT][2];                     // !full: a bit a key that a row does not see
-      if (!full) {
-        const int key0 = kTile * tl.at(i);
-        // the tile's keys below key0 + x
-        auto below = [](int x) {
-          return x <= 0 ? 0u : x >= kTile ? 0xffffffffu : (1u << x) - 1u;
-        };
+      // the tile's keys below key0 + x, those that are there, and those of them that a
+      // token at position `top` sees, a bit each
+      auto below = [](int x) {
+        return x <= 0 ? 0u : x >= kTile ? 0xffffffffu : (1u << x) - 1u;
+      };
+      auto present = [&](int key0) {
         uint32_t there = below(tl.n - key0);
         if constexpr (!kRuns) {
           there &= lds32(at + RingT::kInfo);
@@ -856,15 +855,22 @@ window_kernel(const __grid_constant__ WindowParams p) {
           for (int r = 0; r < kRun; ++r)
             if (what & (kLacks << r)) there &= ~(0xffffu << (16 * r));
         }
-        const uint32_t first = below(p.n_global - key0);
+        return there;
+      };
+      auto seen_at = [&](int top, int key0, uint32_t there, uint32_t first) {
+        const uint32_t near =
+            below(top + 1 - key0) & ~(p.left < 0 ? 0u : below(top - p.left - key0));
+        return there & (near | first);
+      };
+      uint32_t hidden[NT][2];                     // !full: a bit a key that a row does not see
+      if (!full) {
+        const int key0 = kTile * tl.at(i);
+        const uint32_t there = present(key0), first = below(p.n_global - key0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int top = last[nt][j];
-            const uint32_t near = below(top + 1 - key0) &
-                                  ~(p.left < 0 ? 0u : below(top - p.left - key0));
-            hidden[nt][j] = ~(there & (near | first));
+            hidden[nt][j] = ~seen_at(last[nt][j], key0, there, first);
 #pragma unroll
             for (int r = 0; r < kRun; ++r) {
               if ((hidden[nt][j] >> (16 * r + g)) & 1u) s[r][nt][j] = -INFINITY;
@@ -1062,13 +1068,29 @@ window_kernel(const __grid_constant__ WindowParams p) {
             hi[nt][j] = transpose8x8(x);
             lo[nt][j] = transpose8x8(pack_bf16x2(fmaf(a, up, -bf16lo(x)), fmaf(z, up, -bf16hi(x))));
           }
-        // Keys that a token does not see may hold values that are not finite, which
-        // would reach its rows through the product (0 · inf): then the tokens'
-        // rows go one token after the other, each over the keys that it sees,
+        // Keys that a row does not see may hold values that are not finite, which would
+        // reach it through the product (0 · inf). Those that no row of the block sees
+        // enter as zeros; where those that some rows see and others do not are not finite,
+        // the tokens' rows go one token after the other, each over the keys that it sees,
         // the others' V as zeros.
-        bool spoilt = false;
+        uint32_t some = 0, mixed = 0;             // keys, a bit each
         if (!full) {
+          uint32_t all = 0xffffu;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (8 * nt + 2 * t + j < rows) {
+                some |= ~hidden[nt][j];
+                all &= ~hidden[nt][j];
+              }
+          some = __reduce_or_sync(0xffffffffu, some);
+          mixed = some & 0xffffu & ~__reduce_and_sync(0xffffffffu, all);
+        }
+        bool spoilt = false;
+        if (mixed != 0) {
           for (int c = lane; c < kTile * RingT::kPieces; c += 32) {
+            if (!((mixed >> (c / RingT::kPieces)) & 1u)) continue;
             const uint4 x = lds128(at + kTile * RingT::kRow + 16 * c);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -1077,13 +1099,35 @@ window_kernel(const __grid_constant__ WindowParams p) {
           }
           spoilt = __any_sync(0xffffffffu, spoilt);
         }
-        if (!spoilt) {
+        // V of blocks 2 mt and 2 mt + 1 of 8 elements, and of the keys of a mask alone
+        auto load_v = [&](uint32_t (&a)[4], int mt) {
+          // matrices: elements 0-7 and 8-15 of keys 0-7, then of keys 8-15
+          ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8, 2 * mt + lane / 8 % 2));
+        };
+        auto load_v_of = [&](uint32_t (&a)[4], int mt, uint32_t keys) {
+          load_v(a, mt);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {           // (a lane holds keys 2t, 2t + 1, and + 8)
+            const uint32_t x = keys >> (2 * t + 8 * (j / 2));
+            a[j] &= (x & 1u ? 0xffffu : 0u) | (x & 2u ? 0xffff0000u : 0u);
+          }
+        };
+        if (full) {
 #pragma unroll
           for (int mt = 0; mt < kM; ++mt) {
             uint32_t a[4];
-            // matrices: elements 0-7 and 8-15 of keys 0-7, then of keys 8-15
-            ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
-                                                2 * mt + lane / 8 % 2));
+            load_v(a, mt);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<false>(o[mt][nt], a, lo[nt][0], lo[nt][1]);
+              mma16816<false>(o[mt][nt], a, hi[nt][0], hi[nt][1]);
+            }
+          }
+        } else if (!spoilt) {
+#pragma unroll
+          for (int mt = 0; mt < kM; ++mt) {
+            uint32_t a[4];
+            load_v_of(a, mt, some);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16816<false>(o[mt][nt], a, lo[nt][0], lo[nt][1]);
@@ -1091,27 +1135,16 @@ window_kernel(const __grid_constant__ WindowParams p) {
             }
           }
         } else {
-          for (int tok = 0; tok < p.T; ++tok) {
-            // keys 2t, 2t + 1, 2t + 8, 2t + 9 as masks of pairs, for this token
-            const int top = tl.n - p.T + tok, key0 = kTile * tl.at(i);
-            const uint32_t there = !kRuns ? lds32(at + RingT::kInfo) : what & kLacks ? 0u : 0xffffu;
-            uint32_t keep[2] = {0u, 0u};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = 2 * t + (j & 1) + 8 * (j / 2), key = key0 + r;
-              if (((there >> r) & 1u) && key < tl.n &&
-                  ((key <= top && (p.left < 0 || key >= top - p.left)) || key < p.n_global))
-                keep[j / 2] |= j & 1 ? 0xffff0000u : 0xffffu;
-            }
+          // (the block's rows, one after the other by token, have as many tokens)
+          const int key0 = kTile * tl.at(i), tokens = min(rows, p.T);
+          const uint32_t there = present(key0), first = below(p.n_global - key0);
+          for (int x0 = 0; x0 < tokens; ++x0) {
+            const int tok = (r0 + x0) % p.T;
+            const uint32_t keys = seen_at(tl.n - p.T + tok, key0, there, first);
 #pragma unroll
             for (int mt = 0; mt < kM; ++mt) {
               uint32_t a[4];
-              ldmatrix4_trans(a, at + RingT::v_at(lane % 8 + lane / 16 * 8,
-                                                  2 * mt + lane / 8 % 2));
-              a[0] &= keep[0];
-              a[1] &= keep[0];
-              a[2] &= keep[1];
-              a[3] &= keep[1];
+              load_v_of(a, mt, keys);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 // P of this token's rows; others take no part (their sums would

@@ -85,7 +85,7 @@ def test_infinite_values_that_a_token_sees(ost, d, page, Hq, T, lens):
             assert np.array_equal(np.isnan(got), np.isnan(ro)), b
             assert np.array_equal(got[~finite & ~np.isnan(ro)], ro[~finite & ~np.isnan(ro)]), b
             tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + n * 2.0 ** -23) * spread
-            assert np.all(np.abs(got - ro)[finite] <= tol[finite]), b
+            assert np.all(np.abs(got[finite] - ro[finite]) <= tol[finite]), b
 
 
 @pytest.mark.gpu
@@ -113,4 +113,66 @@ def test_infinite_scales_of_v_that_a_token_sees(ost, d, T):
             assert np.array_equal(np.isnan(got), np.isnan(ro)), b
             assert np.array_equal(got[~finite & ~np.isnan(ro)], ro[~finite & ~np.isnan(ro)]), b
             tol = 2.0 ** -8 * np.abs(ro) + 2.0 ** -9.4 * spread
-            assert np.all(np.abs(got - ro)[finite] <= tol[finite]), b
+            assert np.all(np.abs(got[finite] - ro[finite]) <= tol[finite]), b
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,T,d,page,left,first", [(1, 40, 128, 16, -1, 0), (3, 20, 64, 16, 25, 2),
+                                                   (3, 20, 128, 24, -1, 0), (5, 7, 64, 48, 9, 0),
+                                                   (2, 33, 64, 24, 40, 20)])
+def test_values_that_are_not_finite_among_many_tokens(ost, Hq, T, d, page, left, first):
+    """bf16: blocks of 16 query rows that hold some of the tokens, or tokens of two
+    heads; NaN in V at keys that some of the tokens see."""
+    lens = [max(T, 30) + 45, T]
+    c = Cache(False, lens, 1, d, page, T, left, first, 161)
+    q = random_like_shape((2, Hq, T, d), BF, 162)
+    for b, n in enumerate(lens):
+        for e, j in ((1, n - 1), (9, n - T // 2), (33, n - T + 1), (60, max(0, n - T - left + 3))):
+            pg, slot = _pool_row(c, b, j)
+            c.pools[1][pg, :, slot, e] = float("nan") if e != 9 else float("-inf")
+    pools, table, n = c.to(DEV)
+    o, lse = ost.decode_window(q.to(DEV), *pools, table, n, window_left=left, n_global=first)
+    assert ost.attn_sync_status() == 0
+    kv = [c.values(i) for i in range(2)]
+    for b, n in enumerate(lens):
+        k, v = (c.of_request(i, b, kv[i]) for i in range(2))
+        with np.errstate(invalid="ignore"):
+            ro, rl, spread = oracle.decode_window(to_f64(q[b]), k, v, d ** -0.5, left, first)
+        got, finite = to_f64(o[b]), np.isfinite(ro)
+        assert (~finite).any() and np.array_equal(np.isnan(got), np.isnan(ro)), b
+        assert np.array_equal(got[np.isinf(ro)], ro[np.isinf(ro)]), b
+        tol = 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * spread
+        assert np.all(np.abs(got[finite] - ro[finite]) <= tol[finite]), b
+        assert np.max(np.abs(to_f64(lse[b]) - rl)) <= 2.0 ** -11
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["behind the last key", "at the last key"])
+def test_what_rows_hold_does_not_change_the_time(ost, what):
+    """A chunk of 2040 tokens: NaN behind the last key of its last page, or in the
+    last token's own value, against a page without (one pass per token of the
+    request over the tile took 30 times as long)."""
+    T, d, page = 2040, 128, 16
+    c = Cache(False, [T], 1, d, page, T, -1, 0, 171)
+    q = random_like_shape((1, 1, T, d), BF, 172).to(DEV)
+    pools, table, n = c.to(DEV)
+    last = pools[1][int(c.table[0, -1])]
+    clean, spoilt = pools[1].clone(), pools[1].clone()
+    clean[int(c.table[0, -1]), :, T % page:] = 0
+    if what == "at the last key":
+        spoilt.copy_(clean)
+        spoilt[int(c.table[0, -1]), :, T % page - 1] = float("nan")
+    assert not torch.isfinite(last[:, T % page:]).any()
+    times = []
+    for v in (clean, spoilt, clean, spoilt):
+        ost.decode_window(q, pools[0], v, table, n)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(10):
+            o, _ = ost.decode_window(q, pools[0], v, table, n)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+        assert torch.isfinite(o[:, :, :-1]).all()
+    # (the passes over the last tile of a block are 17 instead of one, of its 128 tiles)
+    assert min(times[1::2]) < 2 * min(times[::2]), times
