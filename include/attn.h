@@ -572,7 +572,9 @@ ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float*
  * Rows at multiples of 16 bytes with rot_dim a multiple of 16 move in 16-byte
  * pieces; everything else element by element. q, q_out, k, v need their element's
  * alignment only. B * N at most 2^31 - 256, Hq + 2 Hkv at most 262140, page_size *
- * max_pages_per_seq at most 2^30, fewer than 2^32 rows in a pool.
+ * max_pages_per_seq at most 2^30, fewer than 2^32 rows in a pool; B * N *
+ * ceil((Hq + 2 Hkv) / 16) above 2^31 may be more blocks than a grid has
+ * (ATTN_ERR_UNSUPPORTED).
  * Device-side checks: a request with seq_lens outside [0, capacity] or new_lens
  * outside [0, min(N, n)] has no tokens; a token behind a page index outside [0,
  * num_pages) is not stored (its q_out is written); attn_sync_status() reports

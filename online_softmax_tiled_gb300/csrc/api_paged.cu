@@ -114,7 +114,9 @@ attn_status append_common(AppendArgs a, const attn_strides* q_strides,
     for (int i = 0; i < n_pools; ++i)
       if (RowsMeet::test(plain_bytes(pools[i]), out)) return ATTN_ERR_INVALID_ARG;
   }
-  return from_cuda(launch_cache_append(a));
+  const cudaError_t launched = launch_cache_append(a);
+  // (more blocks than a grid has: nothing was launched)
+  return launched == cudaErrorInvalidConfiguration ? ATTN_ERR_UNSUPPORTED : from_cuda(launched);
 }
 
 struct WindowLayout {
