@@ -150,8 +150,9 @@ ATTN_DEVINL __nv_bfloat16 scale_of(float top) {
   if (top < 0x1p-90f) q = __fdiv_rn(top, 6.f);
   return __float2bfloat16_rn(top < INFINITY ? q : __uint_as_float(0x7fffffffu));
 }
-// Codes of V = 8 elements, two a byte; zeros where the scale is 0 or not a number.
+// Codes of 8 elements, two a byte; zeros where the scale is 0 or not a number.
 template <int V> ATTN_DEVINL uint32_t codes_of(const float (&y)[V], __nv_bfloat16 scale) {
+  static_assert(V == 8, "a piece of 4-bit rows is a quarter of a group");
   const float s = __bfloat162float(scale);
   f2 q[V / 2];
   if (s >= 0x1p-90f && s <= 0x1p90f) {
@@ -170,10 +171,7 @@ template <int V> ATTN_DEVINL uint32_t codes_of(const float (&y)[V], __nv_bfloat1
       q[i] = s > 0.f ? f2{__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)}
                      : f2{0.f, 0.f};
   }
-  if constexpr (V == 8)
-    return f32_to_e2m1x8(q);
-  else
-    return 0;
+  return f32_to_e2m1x8(q);
 }
 
 // The codes x0, x1 of a lane's two pieces (8 elements a word, of which the low

@@ -5,7 +5,7 @@
 // Mathematics. Softmax attention with the online recurrence: per query row a
 // reference m, Σ p and Σ p v of p = 2^(s - m); the reference moves only when a
 // score passes it by 8, so p <= 2^8. Partial sums of one row, of warps or of
-// CTAs, are joined exactly on the larger reference.
+// teams of warps, are joined exactly on the larger reference.
 //
 // 4 bits. With K codes k̂ and one scale per group of 32 elements,
 // s = Σ_c scale_c (Σ_{i in c} q_i k̂_i): the sums of a group are one pair of
@@ -76,7 +76,7 @@ struct WindowParams {
   const int *table, *lens;
   __nv_bfloat16* o;
   float* lse;
-  float *o_part, *m_part, *l_part;          // [2 · CTAs][rows of a block][D], [...]
+  float *o_part, *m_part, *l_part;          // [2 · teams][rows of a block][D], [...]
   int B, Hkv, T, R, blocks;                 // R = query rows per KV head, in `blocks` blocks
   int num_pages, page_size, max_pages, cap, left, n_global;
   uint32_t page_mul;                        // key / page_size = umulhi(2 key, mul) >> shift
@@ -121,15 +121,15 @@ ATTN_DEVINL int places_of(int units) { return units > 0 ? units + kItemCost : 0;
 
 // Sums over the requests of an item's places: of all, and of those before request
 // `upto` (all threads of the block get both).
-// kEarly: lengths may only come from L2.
-template <int kN, int kTile, bool kEarly> struct PlaceSums {
+// Lengths come from L2: the join reads them before it waits. (Every block of the join
+// reads all B of them: 4 B^2 bytes a run of rows, 16 KB a block at 4096 requests.)
+template <int kN, int kTile> struct PlaceSums {
   int total, before;
   ATTN_DEVINL PlaceSums(const WindowParams& p, int upto) {
     __shared__ int part[2][kN / 32];
     int a = 0, b = 0;
     for (int r = threadIdx.x; r < p.B; r += kN) {
-      const int n = kEarly ? __ldcg(p.lens + r) : p.lens[r];
-      const int u = places_of(tiles_of<kTile>(p, n).units);
+      const int u = places_of(tiles_of<kTile>(p, __ldcg(p.lens + r)).units);
       a += u;
       if (r < upto) b += u;
     }
@@ -167,7 +167,7 @@ ATTN_DEVINL int share_of(int place, int teams, int places) {
 struct Share {
   int begin, end, b, before;
 };
-// The share of this CTA, worked out by its threads: each adds up a run of
+// The share of a team, worked out by its threads: each adds up a run of
 // requests, the block's running sums find the threads whose requests hold the
 // share's ends. Places are counted as units are.
 template <int kTile, int kTeams>
@@ -349,7 +349,7 @@ template <int D, bool k4, int kRun> struct Ring {
   static constexpr int kPart = 2 * kKeys * (kRow + kScales);  // bytes of a run
   static constexpr int kInfo = kRun * kPart;
   static constexpr int kStage = kInfo + 16;
-  static constexpr int kStages = kRun == 2 ? 2 : k4 ? 4 : 3;
+  static constexpr int kStages = kRun == 2 ? 2 : 3;
   static constexpr int kBytes = kStages * kStage;
   static constexpr int kPieces = kRow / 16;                 // 16-byte pieces of a row
 
@@ -378,8 +378,8 @@ template <int D, bool k4, int NT>
 constexpr int kTeamsOf = k4 && (D == 64 || NT == 1) ? 4 : 2;
 
 // Blocks of 16 elements whose sums the warps hand one another at a time, each as
-// [32 lanes] of four floats a warp and block of 8 rows: all of them, or as many as
-// leave shared memory for two CTAs an SM.
+// [32 lanes] of four floats a warp and block of 8 rows: all of them, or (bf16) four at a
+// time: at 16 rows those of two teams do not fit beside their rings.
 template <int D, bool k4, int NT, bool kTwice>
 constexpr int kAtOnce = k4 ? (kTwice ? D / 32 : D / 16) : 4 / NT;
 
@@ -1333,7 +1333,7 @@ window_kernel(const __grid_constant__ WindowParams p) {
   }
 }
 
-// Joins the partial results of rows that more than one CTA worked on, and
+// Joins the partial results of rows that more than one team worked on, and
 // writes those of requests without keys. kPer warps a row; grid: x over groups of
 // kJoinWarps / kPer of the Hkv·R rows of request y. Partial results are fetched
 // eight at a time.
@@ -1348,7 +1348,7 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
   // The lengths are read before the wait: this grid starts when every CTA of the
   // one before it has waited for what precedes the call.
   const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const PlaceSums<32 * kJoinWarps, kTile, true> sums(p, b);
+  const PlaceSums<32 * kJoinWarps, kTile> sums(p, b);
   const int row = blockIdx.x * (kJoinWarps / kPer) + warp / kPer;
   const int h = row / p.R, r = row % p.R;
   const Tiles tl = tiles_of<kTile>(p, __ldcg(p.lens + b));
@@ -1368,7 +1368,7 @@ window_join_kernel(const __grid_constant__ WindowParams p) {
     };
     pdl_wait_primary();
     pdl_launch_dependents();
-    if (row >= p.Hkv * p.R || c0 == c1) return;   // (one CTA alone has written its rows)
+    if (row >= p.Hkv * p.R || c0 == c1) return;   // (one team alone has written its rows)
     for (int first = c0 + warp % kPer; first <= c1; first += kPer * kBatch) {
       // (one round trip to memory: nothing of a batch depends on the rest of it)
       float x[kBatch][kLane], m[kBatch], l[kBatch];
