@@ -570,8 +570,9 @@ ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float*
  * or written elsewhere (checked); two new tokens that block_table sends to one row
  * leave either of them there.
  * Rows at multiples of 16 bytes with rot_dim a multiple of 16 move in 16-byte
- * pieces; everything else element by element. q, q_out, k, v need their element's
- * alignment only. B * N at most 2^31 - 256, Hq + 2 Hkv at most 262140, page_size *
+ * pieces; everything else element by element (2.5 to 3.4 times the time). Of the
+ * calls here attn_cache_evict takes float32 pages, no decode does. q, q_out, k, v need
+ * their element's alignment only. B * N at most 2^31 - 256, Hq + 2 Hkv at most 262140, page_size *
  * max_pages_per_seq at most 2^30, fewer than 2^32 rows in a pool; B * N *
  * ceil((Hq + 2 Hkv) / 16) above 2^31 may be more blocks than a grid has
  * (ATTN_ERR_UNSUPPORTED).
@@ -607,7 +608,11 @@ ATTN_API attn_status attn_cache_append(const void* q, const attn_strides* q_stri
  * [num_pages,Hkv,page_size,d/32] bf16; byte (d/16) g + 2c + b of a row's codes
  * holds elements 32c + 4g + 2b (low half) and 32c + 4g + 2b + 1 (g < 8, b < 2):
  * the order in which the decode's matrix products take them. 9/16 of a byte an
- * element. `dt` is the type of q, k, v and q_out. Otherwise as attn_cache_append.
+ * element. `dt` is the type of q, k, v and q_out. With the two halves of rot_dim as pairs
+ * (interleaved = 0) rows move in 16-byte pieces where rot_dim is a multiple of 64, so that
+ * a pair's pieces belong to whole quarters of groups; other values of it go element by
+ * element (rot_dim 32: 2.4 to 2.6 times the time of a prompt, 1.3 of one token's). Otherwise
+ * as attn_cache_append.
  */
 ATTN_API attn_status attn_cache_append4(const void* q, const attn_strides* q_strides, void* q_out,
                                         const attn_strides* q_out_strides, const void* k,
@@ -673,9 +678,17 @@ ATTN_API attn_status attn_cache_read4(const void* k_codes, const void* k_scales,
  * B at most 65535, Hq / Hkv * T at most 65536, page_size * max_pages_per_seq at
  * most 2^30, fewer than 2^32 rows in a pool, B * Hkv * ceil(Hq / Hkv * T / 8) *
  * ceil(capacity / 64) below 2^30.
+ * How a call runs is chosen by its sizes, the capacity among them, since lengths stay on
+ * the device: few items over a narrow table (or behind a narrow window) run as one
+ * launch, the same short requests behind a table of 8192 keys and more as two (500 keys:
+ * 5.7 and 9.1 us over 4 bits, 5.9 and 8.1 in bf16). Every block of the second reads all B lengths.
+ * With T = 1 and window_left < 0 this is attn_decode_paged without a choice of splits:
+ * as fast or faster where KV heads are shared (0.5 to 0.8 of its time at 2 to 64 requests
+ * of 4096 keys and more, 8 KV heads of 128), up to a tenth slower where Hq = Hkv.
  * workspace: at least attn_decode_window_workspace_size() bytes for the same
- * sizes on the current device, 256-byte aligned; it depends on the device and on
- * Hq / Hkv * T, not on the lengths.
+ * sizes on the current device, 256-byte aligned; it depends on the device, d and
+ * Hq / Hkv * T, not on the lengths, and holds what the larger of the two caches' forms
+ * leaves (bf16 uses half of it).
  */
 ATTN_API size_t attn_decode_window_workspace_size(int B, int Hq, int Hkv, int T, int d);
 ATTN_API attn_status attn_decode_window(const void* q, const void* k_pages, const void* v_pages,

@@ -23,10 +23,11 @@
 // Measured (GB300, of a plain copy's 6.7 TB/s): two prompts of 8192 tokens, 32 + 8 heads of
 // 128, bf16, 62 us (0.97: memory); one token of 64 requests 3.5 us (3.1 in a CUDA graph: a
 // launch and its chain length, table entry, angles, store). 2048 tokens of four requests
-// into 4 bits 36 us (0.74): keys and values, 19 us by themselves, are bound by
-// instructions, queries by memory, and the first blocks take the
-// former; blocks that mix both took 44. 8192 keys of four requests back from 4 bits 23.2 us
-// (0.92: memory).
+// into 4 bits 36 us (0.74): queries are bound by memory; keys and values, 19 us by
+// themselves, by neither (issue slots and ALU at 45 %: each thread loads, then
+// computes), and the first blocks take them; blocks that mix both took 44. The same
+// element by element: rot_dim 32 of 128 88 us, of 64 50 (in pieces 19), bf16 pages 83 to 112
+// (33). 8192 keys of four requests back from 4 bits 23.2 us (0.92: memory).
 
 #include <algorithm>
 #include <type_traits>

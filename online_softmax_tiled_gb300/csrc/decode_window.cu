@@ -38,9 +38,9 @@
 // until the end of a run.
 //
 // Measured (GB300; Hq 32, Hkv 8, D 128, 16-key pages; of a plain copy's 6.7 TB/s):
-// bf16, 64 requests behind a window of 1024, 53 us (0.76), 32 requests of 4 tokens behind
-// 4096, 98 us (0.82); 4 bits, 64 requests of mean 4096 keys, 57-60 us (0.75), two of
-// 131072, 46 us (0.72). About 6 us of each are a chain of latencies: the call before,
+// bf16, 64 requests behind a window of 1024, 53-54 us (0.75), 32 requests of 4 tokens behind
+// 4096, 98-100 us (0.81); 4 bits, 64 requests of mean 4096 keys, 57-61 us (0.75-0.8), two of
+// 131072, 46-50 us (0.67-0.73). About 6 us of each are a chain of latencies: the call before,
 // lengths, shares, tables, first copies, the join. Copies alone, nothing computed, take 3
 // us less. bf16 shares end 71 to 97 us after the start by the part of the chip that an SM
 // is in, the same SMs in every run.
@@ -373,7 +373,7 @@ template <int D, bool k4, int kRun> struct Ring {
 // Teams of a block, which has an SM to itself: as many as registers (4 bits) or rings
 // (bf16) leave room for. Blocks of one team start one after the other: 62.3 us for the 64
 // requests in 4 bits where blocks of four take 57.9; bf16 alike. In 4 bits at 16 rows two
-// teams of D = 128 spill nothing (98 us; three 111); of D = 64, four take 57 us, three 61.
+// teams of D = 128 spill 8 bytes (99 us; three 111); of D = 64, four take 57 us, three 61.
 template <int D, bool k4, int NT>
 constexpr int kTeamsOf = k4 && (D == 64 || NT == 1) ? 4 : 2;
 
@@ -1510,7 +1510,8 @@ cudaError_t launch_t(const WindowArgs& a, WindowParams& p) {
   const long long slots = 1LL * a.sm_count * kTeams;
   // Clusters, where all of them run at once and a CTA has kClusterUnits at most. (Against
   // shares with a join, 8 items: one unit a CTA 6.0 and 6.9 us in 4 bits, 6.1 and 7.0 in
-  // bf16; two 6.9 and 7.6, 6.5 and 7.4; four 8.5 and 8.2, 7.7 and 8.3.)
+  // bf16; two 6.9 and 7.6, 6.5 and 7.4; four 8.5 and 8.2, 7.7 and 8.3. 32 items of bf16 in
+  // clusters of eight, which then do not all run at once: 10.4 and 8.8.)
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < units) cluster *= 2;
   constexpr int resident = std::min(kTeams, kSmemPerSm / (smem_cluster + 1024));
