@@ -568,7 +568,7 @@ ATTN_API attn_status attn_cache_evict(const void* k, const void* v, const float*
  * magnitude as for attn_rope. d 64 or 128. Entries of block_table that no new
  * token falls into are not read. Nothing that is written may overlap what is read
  * or written elsewhere (checked); two new tokens that block_table sends to one row
- * leave either of them there.
+ * leave parts of either there.
  * Rows at multiples of 16 bytes with rot_dim a multiple of 16 move in 16-byte
  * pieces; everything else element by element (2.5 to 3.4 times the time). Of the
  * calls here attn_cache_evict takes float32 pages, no decode does. q, q_out, k, v need
