@@ -704,7 +704,7 @@ ATTN_API attn_status attn_decode_window(const void* q, const void* k_pages, cons
  * codes are exact, a group's scale multiplies their sum in float32 (K) or the
  * probability (V), which then enters the product in float16: off by 2^-12 of it,
  * and by 2^-31 of the largest scale of V that the row's keys have (scales from
- * 2^-60 to 2^90; scales of K below 2^110). A group whose scale is not finite
+ * 2^-60 to 2^90; scales of K below 2^109). A group whose scale is not finite
  * spoils its own elements of V, and the key that it belongs to in K, for the tokens
  * that see it.
  */

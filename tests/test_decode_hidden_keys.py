@@ -176,3 +176,30 @@ def test_what_rows_hold_does_not_change_the_time(ost, what):
         assert torch.isfinite(o[:, :, :-1]).all()
     # (the passes over the last tile of a block are 17 instead of one, of its 128 tiles)
     assert min(times[1::2]) < 2 * min(times[::2]), times
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,T", [(128, 4, 1), (128, 16, 1), (64, 4, 4), (64, 16, 1)])
+def test_largest_scales_of_k(ost, d, Hq, T):
+    """4 bits: sums of a row are of queries below 2^9 times codes up to 6, scaled: 128 · 6 ·
+    2^9 · 2^109 < 2^128 where all elements are as large as can be. One key has
+    them, the others are smaller by 2^8: it takes all of the probability."""
+    lens, page = [97, 300], 16
+    c = Cache(True, lens, 1, d, page, T, -1, 0, 181)
+    q = torch.full((2, Hq, T, d), 2.0 ** -100 * (2 - 2.0 ** -7), dtype=BF)
+    for b in range(2):
+        for j in range(lens[b]):
+            pg, slot = _pool_row(c, b, j)
+            c.pools[0][pg, :, slot] = 0x77 if j == 20 else 0x55
+            c.pools[1][pg, :, slot] = 2.0 ** 109 * (1 - 2.0 ** -8) if j == 20 else 2.0 ** 101
+    pools, table, n = c.to(DEV)
+    o, lse = ost.decode_cache4(q.to(DEV), *pools, table, n)
+    assert torch.isfinite(lse).all()
+    kv = [c.values(i) for i in range(2)]
+    for b in range(2):
+        k, v = (c.of_request(i, b, kv[i]) for i in range(2))
+        ro, rl, spread = oracle.decode_window(to_f64(q[b]), k, v, d ** -0.5)
+        assert np.all(rl > 2.0 ** 14)
+        assert np.all(np.abs(to_f64(lse[b]) - rl) <= (d + 8) * 2.0 ** -24 * rl)
+        # (a probability of 1 in float16 times its scale: exact; one rounding of the result)
+        assert np.all(np.abs(to_f64(o[b]) - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -9.4 * spread)
